@@ -17,8 +17,9 @@
  * Conventions for every entry point:
  *   - Tensor arguments are DEVICE memory owned by the caller, dense and row-major:
  *     views (gmmfr_tensor, checked against the problem) for the operator and the
- *     weight preparation, plain pointers for the routing step and the FFN, whose
- *     problem structs give every size; the library keeps no pointer after a call returns.
+ *     weight preparation, plain pointers for the other entry points, whose
+ *     problem structs give every size (and row stride, where rows may be strided); the
+ *     library keeps no pointer after a call returns.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Work is enqueued on it; no entry point synchronises unless it says so.
  *   - A call that returns an error status enqueues no work.  The message of the
@@ -368,6 +369,126 @@ GMMFR_API gmmfr_status gmmfr_llada2_moe_grouped_gemm(const gmmfr_ffn_problem* pr
                                                      const void* prepared, const int32_t* expert_cumsum,
                                                      void* result, void* workspace, size_t workspace_bytes,
                                                      void* stream);
+
+/*
+ * The router (gate) that produces topk_ids and topk_weights for gmmfr_moe_route: for every token t
+ *   l[t,e] = sum_h x[t,h] * weight[e,h]                                (FP32 sums of BF16 products)
+ *   p[t,:] = softmax over e (GMMFR_GATE_SOFTMAX), or 1 / (1 + exp(-l)) (GMMFR_GATE_SIGMOID)
+ *   s[t,e] = p[t,e] + select_bias[e]                                   (the bias selects, it does not weigh)
+ * With n_group > 1 the experts form n_group runs of E / n_group consecutive experts; a group's score is
+ * the sum of its group_top (1 or 2) highest s, and only the topk_group best groups stay eligible.
+ *   topk_ids[t,:]     the topk eligible experts by descending s
+ *   topk_weights[t,k] = scale * p[t,ids[k]] (/ (sum_k p[t,ids[k]] + 1e-20) when renormalise)
+ * Equal scores go to the lowest index, of groups too; NaN scores rank below every number (then by
+ * index); a token whose logits are all -inf has p = 0.  A NaN logit makes its token's softmax NaN.
+ *   T       tokens, 0 <= T < 2^31;  H  row length, a multiple of 8;  E  experts (1..1024)
+ *   topk    1 .. 32, at most the eligible experts (topk_group * E / n_group)
+ *   n_group 1 .. 64, divides E (1: no groups);  topk_group  1 .. n_group;  group_top  1 or 2, at most
+ *           E / n_group.  topk_group and group_top are read only when n_group > 1
+ *   ids_type  gmmfr_index_type of topk_ids
+ *   ldx     elements from one row of x to the next: a multiple of 8, >= H; 0 stands for H
+ */
+typedef enum { GMMFR_GATE_SOFTMAX = 0, GMMFR_GATE_SIGMOID = 1 } gmmfr_gate_scoring;
+typedef struct {
+  int64_t T, H, E, topk, ldx;
+  int32_t scoring;
+  int32_t n_group, topk_group, group_top;
+  int32_t renormalise;
+  int32_t ids_type;
+  float scale;
+} gmmfr_gate_problem;
+
+/* Workspace bytes of gmmfr_moe_gate (256-byte aligned).  Host only. */
+GMMFR_API gmmfr_status gmmfr_moe_gate_workspace_size(const gmmfr_gate_problem* problem, size_t* bytes);
+
+/* x [T, H] BF16 and weight [E, H] BF16 (dense), both 16-byte aligned; select_bias [E] float32 or NULL;
+ * topk_ids [T, topk] int64 or int32; topk_weights [T, topk] float32; logits [T, E] float32 or NULL
+ * (written when given).  Deterministic; never syncs, never allocates. */
+GMMFR_API gmmfr_status gmmfr_moe_gate(const gmmfr_gate_problem* problem, const void* x, const void* weight,
+                                      const float* select_bias, void* topk_ids, float* topk_weights, float* logits,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Weights of the grouped FFN in MXFP8, for gmmfr_moe_layer: E4M3 codes with one E8M0 scale per 32 K
+ * elements.  w13 [E, H, 2I] (K = H) with w13_scale [E, ceil(H/64), 2I, 2]; w2 [E, I, H] (K = I) with
+ * w2_scale [E, ceil(I/64), H, 2] (the operator's per-expert scale layout).  The prepared buffer holds
+ * E*ceil(I/64)*ceil(H/128) + E*ceil(H/128)*ceil(I/128) tiles of 16896 bytes: 128 rows (a w13 tile: 64
+ * gate columns, then the 64 up columns of the same indices) of 128 K codes, then their scales.
+ * `problem` as for the FFN (N is not read); all buffers 16-byte aligned; one launch on `stream`.
+ */
+GMMFR_API gmmfr_status gmmfr_ffn_prepared_weights_size_mx(const gmmfr_ffn_problem* problem, size_t* bytes);
+GMMFR_API gmmfr_status gmmfr_ffn_prepare_weights_mx(const gmmfr_ffn_problem* problem, const void* w13,
+                                                    const void* w13_scale, const void* w2, const void* w2_scale,
+                                                    void* prepared, size_t prepared_bytes, void* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (decoding), gate included:
+ *   ids, w  = the gate above on x (gate.ids_type is not read)
+ *   out[t]  = residual[t] + sum_k w[t,k] * FFN_ids[t,k](x[t]) + FFN_shared(x[t])
+ *   FFN_e(x) = (SiLU(x Wg_e) * (x Wu_e)) W2_e,   SiLU(g) = g / (1 + exp(-g)),   FP32 sums
+ * Every chosen expert's weights are read once per call, whatever the number of its tokens.
+ *   gate          the gate's sizes and rule; 0 <= T <= 64
+ *   I             the routed experts' intermediate size, a multiple of 8
+ *   shared_I      the shared expert's, a multiple of 8; 0: no shared expert
+ *   weight_type   GMMFR_DT_BF16: `prepared` from gmmfr_ffn_prepare_weights (the buffer the grouped FFN
+ *                 uses serves both); GMMFR_DT_E4M3: from gmmfr_ffn_prepare_weights_mx
+ *   ld_residual, ld_out  elements from one row to the next; 0 stands for H
+ */
+typedef struct {
+  gmmfr_gate_problem gate;
+  int64_t I, shared_I;
+  int64_t ld_residual, ld_out;
+  int32_t weight_type;
+} gmmfr_layer_problem;
+
+/* Workspace bytes of gmmfr_moe_layer (256-byte aligned; contents on entry do not matter).  Host only. */
+GMMFR_API gmmfr_status gmmfr_moe_layer_workspace_size(const gmmfr_layer_problem* problem, size_t* bytes);
+
+/* x [T, H] BF16 and gate_weight [E, H] BF16, 16-byte aligned; select_bias [E] float32 or NULL; residual [T, H]
+ * BF16 or NULL; out [T, H] BF16 (may be the residual's memory, not x's); prepared: the routed experts' weights, E experts of
+ * sizes H, I; shared_prepared: the shared expert's (E = 1, I = shared_I), required when shared_I > 0;
+ * topk_ids [T, topk] int32 and topk_weights [T, topk] float32: the gate's choice, written when given.
+ * Never syncs, never allocates; deterministic. */
+GMMFR_API gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, const void* gate_weight,
+                                       const float* select_bias, const void* residual, void* out,
+                                       const void* prepared, size_t prepared_bytes, const void* shared_prepared,
+                                       size_t shared_prepared_bytes, int32_t* topk_ids, float* topk_weights,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The dense product beside the experts (shared expert, dense layers, projections), with its epilogue:
+ *   y = act(x @ weight^T + bias) + residual                            (FP32 sums, one rounding at the end)
+ * act: none, ReLU, GELU (erf form), GELU (tanh form), SiLU, or SwiGLU: weight and bias then hold 2N rows,
+ * the N gate rows followed by the N up rows, and act is SiLU(gate) * up.
+ *   M, N, K   x [M, K], weight [N or 2N, K], y [M, N]; M, N >= 0, K >= 1, each < 2^31
+ *   ldx, ldw, ld_residual, ld_out   elements from one row to the next; 0 stands for the row's length
+ *   out_type  GMMFR_DT_BF16 or GMMFR_DT_F32
+ */
+typedef enum {
+  GMMFR_ACT_NONE = 0,
+  GMMFR_ACT_RELU = 1,
+  GMMFR_ACT_GELU = 2,
+  GMMFR_ACT_GELU_TANH = 3,
+  GMMFR_ACT_SILU = 4,
+  GMMFR_ACT_SWIGLU = 5
+} gmmfr_activation;
+typedef struct {
+  int64_t M, N, K;
+  int64_t ldx, ldw, ld_residual, ld_out;
+  int32_t activation;
+  int32_t out_type;
+} gmmfr_linear_problem;
+
+/* Workspace bytes of gmmfr_linear (256-byte aligned; contents on entry do not matter).  Host only. */
+GMMFR_API gmmfr_status gmmfr_linear_workspace_size(const gmmfr_linear_problem* problem, size_t* bytes);
+
+/* x, weight, bias ([N or 2N] or NULL), residual ([M, N] or NULL) BF16; out of out_type (may be the residual's
+ * memory when both are BF16 with the same row stride).  Any alignment and K are taken; rows of x and weight that
+ * start on 16-byte boundaries (ldx, ldw and K multiples of 8) take the tensor-core path.  Never syncs,
+ * never allocates; deterministic. */
+GMMFR_API gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight,
+                                    const void* bias, const void* residual, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* Message of the last error returned on the calling thread ("" if none). */
 GMMFR_API const char* gmmfr_last_error(void);

@@ -33,7 +33,14 @@ ENTRY_POINTS = (
     "gmmfr_moe_route_workspace_size", "gmmfr_moe_route",
     "gmmfr_ffn_prepared_weights_size", "gmmfr_ffn_prepare_weights", "gmmfr_ffn_workspace_size",
     "gmmfr_llada2_moe_grouped_gemm",
+    "gmmfr_moe_gate_workspace_size", "gmmfr_moe_gate",
+    "gmmfr_ffn_prepared_weights_size_mx", "gmmfr_ffn_prepare_weights_mx",
+    "gmmfr_moe_layer_workspace_size", "gmmfr_moe_layer",
+    "gmmfr_linear_workspace_size", "gmmfr_linear",
 )
+GATE_SCORING = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
+LAYER_MAX_TOKENS = 64
 
 
 DT_U8, DT_E4M3, DT_E5M2, DT_E2M1X2, DT_E8M0, DT_I64, DT_I32, DT_F32, DT_BF16 = range(9)
@@ -92,6 +99,29 @@ class FfnProblem(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64), ("E", ctypes.c_int64)]
 
 
+class GateProblem(ctypes.Structure):
+    """Mirror of gmmfr_gate_problem."""
+    _fields_ = [
+        ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("E", ctypes.c_int64), ("topk", ctypes.c_int64),
+        ("ldx", ctypes.c_int64), ("scoring", ctypes.c_int32), ("n_group", ctypes.c_int32),
+        ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+        ("ids_type", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class LayerProblem(ctypes.Structure):
+    """Mirror of gmmfr_layer_problem."""
+    _fields_ = [("gate", GateProblem), ("I", ctypes.c_int64), ("shared_I", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("weight_type", ctypes.c_int32)]
+
+
+class LinearProblem(ctypes.Structure):
+    """Mirror of gmmfr_linear_problem."""
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ldw", ctypes.c_int64), ("ld_residual", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
 class GmmfrError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"gmmfr status {status}: {message}")
@@ -127,6 +157,15 @@ def load(path: str = LIB_PATH):
             lib.gmmfr_ffn_prepare_weights.argtypes = [FP, vp, vp, vp, sz, vp]
             lib.gmmfr_ffn_workspace_size.argtypes = [FP, ctypes.POINTER(sz)]
             lib.gmmfr_llada2_moe_grouped_gemm.argtypes = [FP, vp, vp, vp, vp, vp, sz, vp]
+            GP, LP, DP = ctypes.POINTER(GateProblem), ctypes.POINTER(LayerProblem), ctypes.POINTER(LinearProblem)
+            lib.gmmfr_moe_gate_workspace_size.argtypes = [GP, ctypes.POINTER(sz)]
+            lib.gmmfr_moe_gate.argtypes = [GP] + [vp] * 7 + [sz, vp]
+            lib.gmmfr_ffn_prepared_weights_size_mx.argtypes = [FP, ctypes.POINTER(sz)]
+            lib.gmmfr_ffn_prepare_weights_mx.argtypes = [FP] + [vp] * 5 + [sz, vp]
+            lib.gmmfr_moe_layer_workspace_size.argtypes = [LP, ctypes.POINTER(sz)]
+            lib.gmmfr_moe_layer.argtypes = [LP] + [vp] * 6 + [sz, vp, sz] + [vp] * 3 + [sz, vp]
+            lib.gmmfr_linear_workspace_size.argtypes = [DP, ctypes.POINTER(sz)]
+            lib.gmmfr_linear.argtypes = [DP] + [vp] * 6 + [sz, vp]
             lib.gmmfr_check_device_errors.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
             lib.gmmfr_last_error.restype = ctypes.c_char_p
             lib.gmmfr_profile_begin.argtypes = [ctypes.c_int]
@@ -254,6 +293,56 @@ def gmmfr_llada2_moe_grouped_gemm(problem: FfnProblem, sorted_tokens, prepared, 
                                   workspace_bytes, stream=None) -> None:
     _check(load().gmmfr_llada2_moe_grouped_gemm(ctypes.byref(problem), sorted_tokens, prepared, expert_cumsum,
                                                 result, workspace, workspace_bytes, stream))
+
+
+def gmmfr_moe_gate_workspace_size(problem: GateProblem) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gmmfr_moe_gate_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def gmmfr_moe_gate(problem: GateProblem, x, weight, select_bias, topk_ids, topk_weights, logits, workspace,
+                   workspace_bytes, stream=None) -> None:
+    _check(load().gmmfr_moe_gate(ctypes.byref(problem), x, weight, select_bias, topk_ids, topk_weights, logits,
+                                 workspace, workspace_bytes, stream))
+
+
+def gmmfr_ffn_prepared_weights_size_mx(problem: FfnProblem) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gmmfr_ffn_prepared_weights_size_mx(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def gmmfr_ffn_prepare_weights_mx(problem: FfnProblem, w13, w13_scale, w2, w2_scale, prepared, prepared_bytes,
+                                 stream=None) -> None:
+    _check(load().gmmfr_ffn_prepare_weights_mx(ctypes.byref(problem), w13, w13_scale, w2, w2_scale, prepared,
+                                               prepared_bytes, stream))
+
+
+def gmmfr_moe_layer_workspace_size(problem: LayerProblem) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gmmfr_moe_layer_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def gmmfr_moe_layer(problem: LayerProblem, x, gate_weight, select_bias, residual, out, prepared, prepared_bytes,
+                    shared_prepared, shared_prepared_bytes, topk_ids, topk_weights, workspace, workspace_bytes,
+                    stream=None) -> None:
+    _check(load().gmmfr_moe_layer(ctypes.byref(problem), x, gate_weight, select_bias, residual, out, prepared,
+                                  prepared_bytes, shared_prepared, shared_prepared_bytes, topk_ids, topk_weights,
+                                  workspace, workspace_bytes, stream))
+
+
+def gmmfr_linear_workspace_size(problem: LinearProblem) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gmmfr_linear_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def gmmfr_linear(problem: LinearProblem, x, weight, bias, residual, out, workspace, workspace_bytes,
+                 stream=None) -> None:
+    _check(load().gmmfr_linear(ctypes.byref(problem), x, weight, bias, residual, out, workspace, workspace_bytes,
+                               stream))
 
 
 def gmmfr_check_device_errors(workspace: int, stream: Optional[int] = None) -> int:
@@ -400,3 +489,233 @@ def ffn(sorted_tokens, prepared, expert_cumsum, H: int, I: int, E: int, result=N
     gmmfr_llada2_moe_grouped_gemm(fp, _ptr(sorted_tokens), _ptr(prepared), _ptr(expert_cumsum), _ptr(result),
                                   _ptr(ws), ws.numel(), _stream(stream))
     return result, ws
+
+
+def ffn_prepare_mx(H: int, I: int, E: int, w13, w13_scale, w2, w2_scale, stream=None):
+    """Prepared-weight buffer (torch uint8) of MXFP8 FFN weights: w13 [E, H, 2I], w2 [E, I, H] E4M3
+    (or their bytes) with E8M0 scales [E, ceil(K/64), columns, 2]."""
+    import torch
+    for name, t, shape in (("w13", w13, (E, H, 2 * I)), ("w13_scale", w13_scale, (E, -(-H // 64), 2 * I, 2)),
+                           ("w2", w2, (E, I, H)), ("w2_scale", w2_scale, (E, -(-I // 64), H, 2))):
+        if t.numel() != _numel(shape) or t.element_size() != 1:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} in single bytes")
+    fp = FfnProblem(N=0, H=H, I=I, E=E)
+    n = gmmfr_ffn_prepared_weights_size_mx(fp)
+    buf = torch.empty(n, dtype=torch.uint8, device=w13.device)
+    gmmfr_ffn_prepare_weights_mx(fp, _ptr(w13), _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(buf), n,
+                                 _stream(stream))
+    return buf
+
+
+# ------------------------------------------------------------- handles of the router, the layer, the product
+def _numel(shape) -> int:
+    n = 1
+    for d in shape:
+        n *= d
+    return n
+
+
+def _rows(t, name: str, cols: int, dtype):
+    """(address, row stride) of a 2-D device tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("gmmfr takes device tensors")
+    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected [rows, {cols}] {dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row must be contiguous, got strides {t.stride()}")
+    # one row has no stride to speak of, and an expanded row (stride 0) is not a row of its own
+    if t.shape[0] > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _row_shape(t, name: str, rows: int, cols: int, dtype):
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name}: {tuple(t.shape)}, expected ({rows}, {cols})")
+    return _rows(t, name, cols, dtype)
+
+
+class _Handle:
+    """Workspaces of a handle, one per stream it has been called on (a workspace serves one call in
+    flight at a time); they grow with the largest call."""
+
+    def __init__(self, device):
+        load()
+        self._device = device
+        self._spaces = {}
+
+    def _workspace(self, stream: int, bytes_needed: int):
+        ws = self._spaces.get(stream)
+        if ws is None or ws.numel() < bytes_needed:
+            import torch
+            ws = torch.empty(max(bytes_needed, 256), dtype=torch.uint8, device=self._device)
+            if stream != torch.cuda.current_stream(self._device).cuda_stream:
+                ws.record_stream(torch.cuda.ExternalStream(stream, device=self._device))
+            self._spaces[stream] = ws
+        return ws.data_ptr(), ws.numel()
+
+    def _on(self, stream):
+        """The stream's address; None is the current one."""
+        import torch
+        return (torch.cuda.current_stream(self._device) if stream is None else stream).cuda_stream
+
+    def _new(self, shape, dtype, stream):
+        import torch
+        t = torch.empty(shape, dtype=dtype, device=self._device)
+        if stream is not None:
+            t.record_stream(stream)
+        return t
+
+
+def _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale) -> GateProblem:
+    import torch
+    E, H = weight.shape
+    _rows(weight, "weight", H, torch.bfloat16)
+    _ptr(weight)
+    if scoring not in GATE_SCORING:
+        raise ValueError(f"scoring {scoring!r} is not one of {sorted(GATE_SCORING)}")
+    if select_bias is not None and (select_bias.dtype != torch.float32 or tuple(select_bias.shape) != (E,)):
+        raise ValueError(f"select_bias: {tuple(select_bias.shape)} {select_bias.dtype}, expected ({E},) float32")
+    return GateProblem(T=0, H=H, E=E, topk=topk, ldx=0, scoring=GATE_SCORING[scoring], n_group=n_group,
+                       topk_group=topk_group, group_top=group_top, renormalise=int(bool(renormalise)),
+                       ids_type=INDEX_I32, scale=scale)
+
+
+class MoeGate(_Handle):
+    """The router: ``gate(x)`` -> (topk_ids [T, topk], topk_weights [T, topk] float32), the inputs of
+    :func:`route`.  ``weight`` [E, H] bfloat16; the rule is gmmfr_gate_problem's."""
+
+    def __init__(self, weight, topk: int, scoring: str = "softmax", select_bias=None, n_group: int = 1,
+                 topk_group: int = 1, group_top: int = 2, renormalise: bool = True, scale: float = 1.0,
+                 ids_dtype=None):
+        import torch
+        super().__init__(weight.device)
+        self._p = _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
+        self._ids_dtype = torch.int32 if ids_dtype is None else ids_dtype
+        if self._ids_dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"ids_dtype {ids_dtype} is not int32 or int64")
+        self._p.ids_type = INDEX_I32 if self._ids_dtype == torch.int32 else INDEX_I64
+        self._weight, self._bias = weight, select_bias
+        self._bf16, self._f32 = torch.bfloat16, torch.float32
+        gmmfr_moe_gate_workspace_size(self._p)  # refuses a rule that is out of range
+
+    def __call__(self, x, ids=None, weights=None, logits=None, stream=None):
+        p = self._p
+        ptr, p.ldx = _rows(x, "x", p.H, self._bf16)
+        p.T = T = x.shape[0]
+        for name, t, shape, dt in (("ids", ids, (T, p.topk), self._ids_dtype), ("weights", weights, (T, p.topk), self._f32),
+                                   ("logits", logits, (T, p.E), self._f32)):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
+                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} {dt}")
+        s = self._on(stream)
+        if ids is None:
+            ids = self._new((T, p.topk), self._ids_dtype, stream)
+        if weights is None:
+            weights = self._new((T, p.topk), self._f32, stream)
+        ws, n = self._workspace(s, gmmfr_moe_gate_workspace_size(p))
+        gmmfr_moe_gate(p, ptr, _ptr(self._weight), _ptr(self._bias), _ptr(ids), _ptr(weights), _ptr(logits), ws, n, s)
+        return ids, weights
+
+
+class MoeLayer(_Handle):
+    """A whole MoE layer for up to 64 tokens, gate included: ``layer(x, residual=None)`` -> out [T, H].
+
+    ``gate_weight`` [E, H]; ``w13`` [E, H, 2I] and ``w2`` [E, I, H] bfloat16, or E4M3 with
+    ``w13_scale`` / ``w2_scale`` (E8M0, [E, ceil(K/64), columns, 2]); the shared expert's weights as
+    [H, 2 shared_I] and [shared_I, H] of the same kind.  The weights are laid out once, here; the
+    keyword arguments after them are the gate's."""
+
+    def __init__(self, gate_weight, w13, w2, w13_scale=None, w2_scale=None, shared_w13=None, shared_w2=None,
+                 shared_w13_scale=None, shared_w2_scale=None, *, topk: int, scoring: str = "softmax",
+                 select_bias=None, n_group: int = 1, topk_group: int = 1, group_top: int = 2,
+                 renormalise: bool = True, scale: float = 1.0):
+        import torch
+        super().__init__(gate_weight.device)
+        gp = _gate_problem(gate_weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
+        E, H, I = gp.E, gp.H, w2.shape[1]
+        mx = w13_scale is not None
+        self._prepared = self._prepare(E, H, I, w13, w13_scale, w2, w2_scale, mx)
+        shared_I, self._shared = 0, None
+        if shared_w13 is not None:
+            shared_I = shared_w2.shape[0]
+            self._shared = self._prepare(1, H, shared_I, shared_w13, shared_w13_scale, shared_w2, shared_w2_scale, mx)
+        self._p = LayerProblem(gate=gp, I=I, shared_I=shared_I, ld_residual=0, ld_out=0,
+                               weight_type=DT_E4M3 if mx else DT_BF16)
+        self._weight, self._bias = gate_weight, select_bias
+        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
+        gmmfr_moe_layer_workspace_size(self._p)
+
+    @staticmethod
+    def _prepare(E, H, I, w13, s13, w2, s2, mx):
+        import torch
+        if mx:
+            return ffn_prepare_mx(H, I, E, w13, s13, w2, s2)
+        for name, t, shape in (("w13", w13, (E, H, 2 * I)), ("w2", w2, (E, I, H))):
+            if t.dtype != torch.bfloat16 or t.numel() != _numel(shape):
+                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} bfloat16")
+        return ffn_prepare(H, I, E, w13, w2)
+
+    def __call__(self, x, residual=None, out=None, topk_ids=None, topk_weights=None, stream=None):
+        p = self._p
+        g = p.gate
+        ptr, g.ldx = _rows(x, "x", g.H, self._bf16)
+        g.T = T = x.shape[0]
+        rptr = None
+        if residual is not None:
+            rptr, p.ld_residual = _row_shape(residual, "residual", T, g.H, self._bf16)
+        s = self._on(stream)
+        if out is None:
+            out = self._new((T, g.H), self._bf16, stream)
+        optr, p.ld_out = _row_shape(out, "out", T, g.H, self._bf16)
+        for name, t, dt in (("topk_ids", topk_ids, self._i32), ("topk_weights", topk_weights, self._f32)):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != (T, g.topk)):
+                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {(T, g.topk)} {dt}")
+        ws, n = self._workspace(s, gmmfr_moe_layer_workspace_size(p))
+        gmmfr_moe_layer(p, ptr, _ptr(self._weight), _ptr(self._bias), rptr, optr, _ptr(self._prepared),
+                        self._prepared.numel(), _ptr(self._shared), 0 if self._shared is None else self._shared.numel(),
+                        _ptr(topk_ids), _ptr(topk_weights), ws, n, s)
+        return out
+
+
+class Linear(_Handle):
+    """The dense product: ``linear(x, residual=None)`` -> act(x @ weight.T + bias) + residual.
+
+    ``weight`` [N, K] bfloat16 (rows may be strided); with ``activation="swiglu"`` [2N, K], the gate
+    rows then the up rows, and ``bias`` [2N]."""
+
+    def __init__(self, weight, bias=None, activation: str = "none", out_dtype=None):
+        import torch
+        super().__init__(weight.device)
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
+        self._out = torch.bfloat16 if out_dtype is None else out_dtype
+        if self._out not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
+        rows, K = weight.shape
+        self._wptr, ldw = _rows(weight, "weight", K, torch.bfloat16)
+        if activation == "swiglu" and rows % 2:
+            raise ValueError(f"weight: {rows} rows; swiglu takes gate and up rows, an even number")
+        if bias is not None and (bias.dtype != torch.bfloat16 or tuple(bias.shape) != (rows,)):
+            raise ValueError(f"bias: {tuple(bias.shape)} {bias.dtype}, expected ({rows},) bfloat16")
+        self._weight, self._bias = weight, bias
+        self._p = LinearProblem(M=0, N=rows // 2 if activation == "swiglu" else rows, K=K, ldx=0, ldw=ldw, ld_residual=0,
+                                ld_out=0, activation=ACTIVATIONS[activation],
+                                out_type=DT_F32 if self._out == torch.float32 else DT_BF16)
+        self._bf16 = torch.bfloat16
+        gmmfr_linear_workspace_size(self._p)
+
+    def __call__(self, x, residual=None, out=None, stream=None):
+        p = self._p
+        ptr, p.ldx = _rows(x, "x", p.K, self._bf16)
+        p.M = M = x.shape[0]
+        rptr = None
+        if residual is not None:
+            rptr, p.ld_residual = _row_shape(residual, "residual", M, p.N, self._bf16)
+        s = self._on(stream)
+        if out is None:
+            out = self._new((M, p.N), self._out, stream)
+        optr, p.ld_out = _row_shape(out, "out", M, p.N, self._out)
+        need = gmmfr_linear_workspace_size(p)
+        ws, n = self._workspace(s, need) if need else (None, 0)
+        gmmfr_linear(p, ptr, self._wptr, _ptr(self._bias), rptr, optr, ws, n, s)
+        return out

@@ -1,0 +1,20 @@
+// Activations of the dense product's epilogue (FP32).
+#pragma once
+#include "gmmfr.h"
+
+namespace gmmfr {
+
+__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+
+__device__ __forceinline__ float activate(int act, float v) {
+  switch (act) {
+    case GMMFR_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
+    case GMMFR_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case GMMFR_ACT_GELU_TANH:
+      return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+    case GMMFR_ACT_SILU: return silu(v);
+    default: return v;
+  }
+}
+
+}  // namespace gmmfr
