@@ -463,6 +463,9 @@ GMMFR_API gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const
  *   M, N, K   x [M, K], weight [N or 2N, K], y [M, N]; M, N >= 0, K >= 1, each < 2^31
  *   ldx, ldw, ld_residual, ld_out   elements from one row to the next; 0 stands for the row's length
  *   out_type  GMMFR_DT_BF16 or GMMFR_DT_F32
+ *   unaligned 1: x or weight may start off a 16-byte boundary.  Rows that do, or whose stride is not a
+ *             multiple of 8, are copied into the workspace first (the tensor copies that feed the products need
+ *             16-byte rows), which then has room for both matrices; 0 otherwise
  */
 typedef enum {
   GMMFR_ACT_NONE = 0,
@@ -477,15 +480,16 @@ typedef struct {
   int64_t ldx, ldw, ld_residual, ld_out;
   int32_t activation;
   int32_t out_type;
+  int32_t unaligned;
 } gmmfr_linear_problem;
 
 /* Workspace bytes of gmmfr_linear (256-byte aligned; contents on entry do not matter).  Host only. */
 GMMFR_API gmmfr_status gmmfr_linear_workspace_size(const gmmfr_linear_problem* problem, size_t* bytes);
 
 /* x, weight, bias ([N or 2N] or NULL), residual ([M, N] or NULL) BF16; out of out_type (may be the residual's
- * memory when both are BF16 with the same row stride).  Any alignment and K are taken; rows of x and weight that
- * start on 16-byte boundaries (ldx, ldw and K multiples of 8) take the tensor-core path.  Never syncs,
- * never allocates; deterministic. */
+ * memory when both are BF16 with the same row stride).  Any K, stride and element alignment is taken.  One launch,
+ * plus one for each matrix that is copied first.  Never syncs, never allocates; deterministic; a wait that gave up
+ * sets GMMFR_DEV_TIMEOUT in the workspace's device error word (gmmfr_check_device_errors). */
 GMMFR_API gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight,
                                     const void* bias, const void* residual, void* out, void* workspace,
                                     size_t workspace_bytes, void* stream);

@@ -119,7 +119,7 @@ class LinearProblem(ctypes.Structure):
     """Mirror of gmmfr_linear_problem."""
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64),
                 ("ldw", ctypes.c_int64), ("ld_residual", ctypes.c_int64), ("ld_out", ctypes.c_int64),
-                ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+                ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32), ("unaligned", ctypes.c_int32)]
 
 
 class GmmfrError(RuntimeError):
@@ -715,7 +715,7 @@ class Linear(_Handle):
         if out is None:
             out = self._new((M, p.N), self._out, stream)
         optr, p.ld_out = _row_shape(out, "out", M, p.N, self._out)
-        need = gmmfr_linear_workspace_size(p)
-        ws, n = self._workspace(s, need) if need else (None, 0)
+        p.unaligned = int((ptr | self._wptr) & 15 != 0)
+        ws, n = self._workspace(s, gmmfr_linear_workspace_size(p))
         gmmfr_linear(p, ptr, self._wptr, _ptr(self._bias), rptr, optr, ws, n, s)
         return out

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "ops.cuh"
 
 namespace {
 
@@ -261,6 +262,8 @@ void* view_data(const gmmfr_tensor* t) { return t ? t->data : nullptr; }
 namespace gmmfr {
 // Records `message` as the calling thread's last error (for other files of the library).
 gmmfr_status record_error(gmmfr_status st, const char* message) { return fail(st, "%s", message); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encode_fn(); }
+int sm_count() { return device_sms(); }
 }  // namespace gmmfr
 
 extern "C" {

@@ -143,12 +143,44 @@ gmmfr_status validate_linear(const gmmfr_linear_problem* p) {
                 (long long)p->ldx, (long long)p->ldw, (long long)p->ld_residual, (long long)p->ld_out);
   if (p->activation < GMMFR_ACT_NONE || p->activation > GMMFR_ACT_SWIGLU)
     return fail(GMMFR_ERR_INVALID_ARG, "activation=%d is not a gmmfr_activation", p->activation);
+  if (p->unaligned != 0 && p->unaligned != 1) return fail(GMMFR_ERR_INVALID_ARG, "unaligned must be 0 or 1");
   if (p->out_type != GMMFR_DT_BF16 && p->out_type != GMMFR_DT_F32)
     return fail(GMMFR_ERR_INVALID_ARG, "out_type=%d is not BF16 (%d) or F32 (%d)", p->out_type, GMMFR_DT_BF16, GMMFR_DT_F32);
   return GMMFR_OK;
 }
 
-size_t linear_ws_bytes(const gmmfr_linear_problem*) { return 0; }
+// Rows that TMA cannot read in place are copied to a pitch of K rounded up to 8.
+bool repitch_x(const gmmfr_linear_problem* p) { return p->unaligned || (p->M > 1 && stride_or(p->ldx, p->K) % 8); }
+bool repitch_w(const gmmfr_linear_problem* p) {
+  return p->unaligned || (p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1) > 1 && stride_or(p->ldw, p->K) % 8);
+}
+
+struct LinearLayout {
+  size_t x, w, total;
+};
+LinearLayout linear_layout(const gmmfr_linear_problem* p) {
+  LinearLayout L{};
+  const size_t Kp = (size_t)cdiv(p->K, 8) * 8;
+  size_t off = gmmfr::kHdrBytes;
+  L.x = off;
+  if (repitch_x(p)) off = align256(off + 2 * Kp * p->M);
+  L.w = off;
+  if (repitch_w(p)) off = align256(off + 2 * Kp * p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1));
+  L.total = off;
+  return L;
+}
+
+// [rows, K] BF16 with boxes of `box_rows` rows of 64 elements (128 bytes, 128-byte swizzle)
+bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const void* base, int64_t rows, int64_t K,
+                 int64_t ld, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : cdiv(K, 8) * 8) * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace
 
@@ -276,7 +308,7 @@ gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, 
 gmmfr_status gmmfr_linear_workspace_size(const gmmfr_linear_problem* problem, size_t* bytes) {
   if (gmmfr_status st = validate_linear(problem)) return st;
   if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = linear_ws_bytes(problem);
+  *bytes = linear_layout(problem).total;
   return GMMFR_OK;
 }
 
@@ -289,15 +321,24 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   if (!aligned(x, 2) || !aligned(weight, 2) || !aligned(bias, 2) || !aligned(residual, 2) ||
       !aligned(out, p.out_type == GMMFR_DT_F32 ? 4 : 2))
     return fail(GMMFR_ERR_INVALID_ARG, "an input or output is not aligned to its element size");
-  const size_t need = linear_ws_bytes(problem);
-  if (need)
-    if (gmmfr_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  const bool gated = p.activation == GMMFR_ACT_SWIGLU;
+  const int64_t rows_w = gated ? 2 * p.N : p.N;
+  const LinearLayout L = linear_layout(problem);
+  if ((!aligned(x, 16) && !repitch_x(problem)) || (!aligned(weight, 16) && !repitch_w(problem)))
+    return fail(GMMFR_ERR_INVALID_ARG, "x or weight is off a 16-byte boundary: set problem.unaligned (and size the workspace with it)");
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, L.total)) return st;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+  if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = gmmfr::sm_count();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   gmmfr::LinearParams lp{};
   lp.x = static_cast<const __nv_bfloat16*>(x);
   lp.w = static_cast<const __nv_bfloat16*>(weight);
   lp.bias = static_cast<const __nv_bfloat16*>(bias);
   lp.residual = static_cast<const __nv_bfloat16*>(residual);
   lp.out = out;
+  lp.hdr = reinterpret_cast<uint32_t*>(ws);
   lp.M = p.M;
   lp.N = p.N;
   lp.K = p.K;
@@ -305,9 +346,31 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   lp.ldw = stride_or(p.ldw, p.K);
   lp.ldr = stride_or(p.ld_residual, p.N);
   lp.ldo = stride_or(p.ld_out, p.N);
+  lp.timeout_ns = 4000000000ll;
   lp.act = p.activation;
   lp.out_f32 = p.out_type == GMMFR_DT_F32;
-  cudaError_t e = gmmfr::launch_linear(lp, static_cast<cudaStream_t>(stream));
+  lp.vec_out = aligned(out, 16) && lp.ldo % (lp.out_f32 ? 4 : 8) == 0 && aligned(residual, 16) && lp.ldr % 8 == 0;
+  const int64_t Kp = cdiv(p.K, 8) * 8;
+  if (repitch_x(problem)) {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
+    cudaError_t e = gmmfr::launch_linear_repitch(lp.x, dst, p.M, p.K, Kp, lp.ldx, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "x copy launch");
+    lp.x = dst;
+    lp.ldx = Kp;
+  }
+  if (repitch_w(problem)) {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(ws + L.w);
+    cudaError_t e = gmmfr::launch_linear_repitch(lp.w, dst, rows_w, p.K, Kp, lp.ldw, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
+    lp.w = dst;
+    lp.ldw = Kp;
+  }
+  gmmfr::plan_linear(lp, sms);
+  gmmfr::LinearMaps maps;
+  if (!encode_rows(encode, &maps.x, lp.x, p.M, p.K, lp.ldx, lp.stream ? lp.bn : 128) ||
+      !encode_rows(encode, &maps.w, lp.w, rows_w, p.K, lp.ldw, lp.stream ? (gated ? 64 : 128) : lp.bn / 2))
+    return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  cudaError_t e = gmmfr::launch_linear(maps, lp, s);
   if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   return GMMFR_OK;
 }

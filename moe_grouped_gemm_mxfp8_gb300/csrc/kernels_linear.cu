@@ -1,88 +1,623 @@
 // The dense product with its epilogue: y = act(x W^T + bias) + residual.
+//
+// Two tensor-core forms (tcgen05 kind::f16, FP32 accumulators in TMEM, operands by TMA):
+//   stream  few rows of x.  The weights are the 128-row operand, the rows of x the N-wide one, so every
+//           weight byte crosses HBM once; the K range of a tile is split over the CTAs of a cluster, whose
+//           partial sums meet in shared memory (in rank order: deterministic).
+//   pair    many rows.  A pair of CTAs holds a 256 x BN tile of y (cta_group::2: each CTA loads 128 rows of x
+//           and half of the BN rows of W), accumulators double-buffered in TMEM, so that a tile's epilogue
+//           runs beside the next tile's products.
+// Rows of x or W that do not start on 16-byte boundaries (a TMA rule) are first copied to a pitch that does.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "epilogue.cuh"
 #include "ops.cuh"
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace gmmfr {
+namespace lin {
 
-// Plain form for rows of any alignment: 64 x 64 outputs per CTA, 16 K at a time through shared
-// memory, 4 x 4 FP32 sums per thread (twice that with the gated activation).
-template <bool kGated>
-__global__ void __launch_bounds__(256) linear_plain_kernel(LinearParams p) {
-  __shared__ float sx[16][64 + 4];
-  __shared__ float sw[kGated ? 2 : 1][16][64 + 4];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  float acc[kGated ? 2 : 1][4][4] = {};
-  const int lk = tid & 15, lr = tid >> 4;
-  for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
+constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr int kBK = 64;        // K per stage: 128-byte rows
+constexpr int kTileBytes = 128 * 128;
+
+// ---- pair form
+constexpr int kPairArena = 6 * 32768;
+constexpr int kPairMaxStages = 10;
+constexpr int kPairBars = 2 * kPairMaxStages + 5;
+constexpr int kPairSmem = kPairArena + kPairBars * 8 + 32 + 1024;
+static_assert(kPairSmem <= 232448, "shared memory budget");
+
+// ---- stream form
+constexpr int kStreamMaxStages = 8;
+constexpr int kStreamBars = 2 * kStreamMaxStages + 6;
+// ring and partial sums: up to 32 rows two CTAs share an SM, beyond one has it
+__host__ __device__ constexpr int stream_arena(int rows) { return rows <= 32 ? 104 * 1024 : 220 * 1024; }
+__host__ __device__ constexpr int stream_smem(int rows) { return stream_arena(rows) + kStreamBars * 8 + 32 + 1024; }
+static_assert(2 * (stream_smem(32) + 1024) <= 228 * 1024 && stream_smem(64) <= 232448, "shared memory budget");
+
+}  // namespace lin
+
+namespace {
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void store_out(const LinearParams& p, int64_t m, int64_t n, float v) {
+  if (p.residual) v += __bfloat162float(p.residual[m * p.ldr + n]);
+  if (p.out_f32) static_cast<float*>(p.out)[m * p.ldo + n] = v;
+  else static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
+}
+
+// 32 consecutive columns n.. of row m, activated values in v (bias included).
+__device__ __forceinline__ void store_row32(const LinearParams& p, int64_t m, int64_t n, float (&v)[32]) {
+  if (p.vec_out && n + 32 <= p.N) {
+    if (p.residual) {
+      const uint4* r = reinterpret_cast<const uint4*>(p.residual + m * p.ldr + n);
+      uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = lr + 16 * i;
-      const bool k_ok = k0 + lk < p.K;
-      sx[lk][r] = k_ok && m0 + r < p.M ? __bfloat162float(p.x[(m0 + r) * p.ldx + k0 + lk]) : 0.f;
+      for (int i = 0; i < 4; ++i) w[i] = r[i];
 #pragma unroll
-      for (int g = 0; g < (kGated ? 2 : 1); ++g)
-        sw[g][lk][r] = k_ok && n0 + r < p.N ? __bfloat162float(p.w[(g * p.N + n0 + r) * p.ldw + k0 + lk]) : 0.f;
-    }
-    __syncthreads();
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(&sx[k][ty * 4]);
-      const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int g = 0; g < (kGated ? 2 : 1); ++g) {
-        const float4 b = *reinterpret_cast<const float4*>(&sw[g][k][tx * 4]);
-        const float bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[g][i][j] = fmaf(av[i], bv[j], acc[g][i][j]);
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] += bf16_lo(u[j]);
+          v[8 * i + 2 * j + 1] += bf16_hi(u[j]);
+        }
       }
     }
-    __syncthreads();
-  }
+    if (p.out_f32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + m * p.ldo + n);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
-    if (m >= p.M) break;
+      for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + m * p.ldo + n);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + tx * 4 + j;
-      if (n >= p.N) break;
-      float v = acc[0][i][j];
-      if (p.bias) v += __bfloat162float(p.bias[n]);
-      if constexpr (kGated) {
-        float u = acc[1][i][j];
-        if (p.bias) u += __bfloat162float(p.bias[p.N + n]);
-        v = silu(v) * u;
-      } else {
-        v = activate(p.act, v);
-      }
-      if (p.residual) v += __bfloat162float(p.residual[m * p.ldr + n]);
-      if (p.out_f32) static_cast<float*>(p.out)[m * p.ldo + n] = v;
-      else static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
+      for (int i = 0; i < 4; ++i)
+        o[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                          pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n + j < p.N) store_out(p, m, n + j, v[j]);
   }
 }
 
-cudaError_t launch_linear(const LinearParams& p, cudaStream_t s) {
-  if (p.M == 0 || p.N == 0) return cudaSuccess;
-  const int64_t per_launch = (int64_t)65535 * 64;  // grid.y limit
-  for (int64_t m = 0; m < p.M; m += per_launch) {
-    LinearParams q = p;
-    q.x += m * p.ldx;
-    if (q.residual) q.residual += m * p.ldr;
-    q.out = static_cast<uint8_t*>(p.out) + m * p.ldo * (p.out_f32 ? 4 : 2);
-    q.M = p.M - m < per_launch ? p.M - m : per_launch;
-    const dim3 grid((unsigned)((q.N + 63) / 64), (unsigned)((q.M + 63) / 64));
-    if (p.act == GMMFR_ACT_SWIGLU) linear_plain_kernel<true><<<grid, 256, 0, s>>>(q);
-    else linear_plain_kernel<false><<<grid, 256, 0, s>>>(q);
-    if (cudaError_t e = cudaGetLastError()) return e;
+__device__ __forceinline__ void add_bias32(const __nv_bfloat16* bias, int64_t n, int64_t n_end, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (n + j < n_end) v[j] += __bfloat162float(bias[n + j]);
+}
+
+}  // namespace
+
+// ============================================================================ pair form
+// Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
+// tiles in flight share rows of x and of W in L2.
+template <int kAct>
+__global__ void __launch_bounds__(lin::kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
+  constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::kPairArena);  // used in rank 0: both CTAs' loads
+  uint64_t* empty = full + lin::kPairMaxStages;
+  uint64_t* accf = empty + lin::kPairMaxStages;
+  uint64_t* acce = accf + 2;  // used in rank 0: both CTAs' epilogue warps
+  uint64_t* drain = acce + 2;
+  int32_t* misc = reinterpret_cast<int32_t*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
+  int* abort_flag = &misc[1];
+  uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_rank();
+  const int BN = p.bn;
+  const int stage_bytes = lin::kTileBytes + BN * 64, n_stages = p.n_stages;
+  const int KB = p.KB;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < n_stages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&acce[b]), 8);
+    }
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    *abort_flag = 0;
+    *s_err = 0;
+    ptx::fence_mbar_init();
   }
-  return cudaSuccess;
+  if (warp == 0 && lane < 2) ptx::prefetch_tensormap(lane ? &maps.w : &maps.x);
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Ctl ctl{abort_flag, s_err, p.timeout_ns};
+  const uint32_t smem_base = ptx::smem_u32(smem);
+  const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+  const int tiles = p.tiles_m * p.tiles_n;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  auto tile_at = [&](int t, int& mt, int& nt) {
+    const int per = p.group_m * p.tiles_n, g = t / per, r = t - g * per;
+    const int rows = min(p.group_m, p.tiles_m - g * p.group_m);
+    nt = r / rows;
+    mt = g * p.group_m + (r - nt * rows);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = ptx::l2_evict_last_policy();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs) {
+        int mt, nt;
+        tile_at(t, mt, nt);
+        const int ym = mt * 256 + (int)rank * 128;
+        const int yn = kGated ? nt * (BN / 2) + (rank ? (int)p.N : 0) : nt * BN + (int)rank * (BN / 2);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = smem_base + stage * stage_bytes;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), 2 * stage_bytes);
+          const uint32_t fb = ptx::map_to_rank(ptx::smem_u32(&full[stage]), 0);
+          ptx::tma_load_2d_pair(sb, &maps.x, kb * lin::kBK, ym, fb, pol);
+          ptx::tma_load_2d_pair(sb + lin::kTileBytes, &maps.w, kb * lin::kBK, yn, fb, pol);
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // the last stages: released once their products are done, so that no load is in flight at exit
+      for (int s = 0; ok && s < n_stages; ++s) {
+        ok = wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok && rank == 0)  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
+        for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // kind::f16: FP32 accumulator, A and B BF16, M = 256
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc_i = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs) {
+        const int buf = acc_i & 1;
+        if (!wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + buf * 256;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sb = smem_base + stage * stage_bytes;
+          const uint64_t da = ptx::smem_desc(sb, 16, 1024, ptx::kSwizzle128B);
+          const uint64_t db = ptx::smem_desc(sb + lin::kTileBytes, 16, 1024, ptx::kSwizzle128B);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ptx::tc_mma_f16_pair(d, da + 2 * q, db + 2 * q, idesc, (kb > 0 || q > 0) ? 1u : 0u);
+          ptx::tc_commit_pair(ptx::smem_u32(&empty[stage]));
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+        ++acc_i;
+      }
+      ptx::tc_commit_pair(ptx::smem_u32(drain));
+      wait_bar_drain(ptx::smem_u32(drain), 0);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    int acc_i = 0;
+    for (int t = first; t < tiles; t += pairs) {
+      int mt, nt;
+      tile_at(t, mt, nt);
+      const int buf = acc_i & 1;
+      if (!warp_wait_bar(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
+      const int64_t m = (int64_t)mt * 256 + rank * 128 + q * 32 + lane;
+      const int cols = kGated ? BN / 2 : BN;
+      const int64_t n0 = (int64_t)nt * cols;
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        uint32_t r[32];
+        float v[32];
+        ptx::tmem_ld_32x32b_x32(taddr + c0, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        if (p.bias) add_bias32(p.bias, n0 + c0, p.N, v);
+        if constexpr (kGated) {
+          ptx::tmem_ld_32x32b_x32(taddr + BN / 2 + c0, r);
+          ptx::tmem_wait_ld();
+          float u[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
+          if (p.bias) add_bias32(p.bias + p.N, n0 + c0, p.N, u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = silu(v[j]) * u[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = activate(kAct, v[j]);
+        }
+        if (m < p.M) store_row32(p, m, n0 + c0, v);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[buf]), 0));
+      ++acc_i;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (rank == 1 && threadIdx.x == 0) wait_bar_drain(ptx::smem_u32(drain), 0);  // rank 0's last arrival here
+  __syncthreads();
+  ptx::cluster_sync();  // the other CTA's products read this one's shared memory, its epilogue arrives here
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, 512);
+  }
+  if (threadIdx.x == 0) {
+    p.hdr[1 + blockIdx.x] = *s_err;
+    if (blockIdx.x == 0) p.hdr[0] = gridDim.x;
+  }
+}
+
+// ============================================================================ stream form
+// Cluster c takes the tiles c, c + clusters, ...; its CTA of rank r the K blocks [KB r / S, KB (r + 1) / S).
+// A tile is 128 rows of W; with the gated activation 64 gate rows and the 64 up rows of the same columns.
+template <int kAct>
+__global__ void __launch_bounds__(lin::kThreads, 2)
+    linear_stream_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
+  constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
+  constexpr int kCols = kGated ? 64 : 128;  // columns of y per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::stream_arena((int)p.M));
+  uint64_t* empty = full + lin::kStreamMaxStages;
+  uint64_t* accf = empty + lin::kStreamMaxStages;
+  uint64_t* acce = accf + 1;
+  uint64_t* drain = acce + 1;
+  uint64_t* pready = drain + 1;  // every CTA's partial sums are in its shared memory
+  uint64_t* pfree = pready + 1;  // every CTA has read this one's
+  int32_t* misc = reinterpret_cast<int32_t*>(pfree + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
+  int* abort_flag = &misc[1];
+  uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.split;
+  const uint32_t rank = S > 1 ? ptx::cluster_rank() : 0u;
+  const int T = (int)p.M, npad = p.bn;
+  const int stage_bytes = lin::kTileBytes + npad * 128, n_stages = p.n_stages;
+  float* part = reinterpret_cast<float*>(smem + n_stages * stage_bytes);  // [T][128]
+  const uint32_t tmem_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < n_stages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(accf), 1);
+    ptx::mbar_init(ptx::smem_u32(acce), 4);
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    ptx::mbar_init(ptx::smem_u32(pready), S);
+    ptx::mbar_init(ptx::smem_u32(pfree), S);
+    *abort_flag = 0;
+    *s_err = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane < 2) ptx::prefetch_tensormap(lane ? &maps.w : &maps.x);
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), tmem_cols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (S > 1) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Ctl ctl{abort_flag, s_err, p.timeout_ns};
+  const uint32_t smem_base = ptx::smem_u32(smem);
+  const int clusters = gridDim.x / S, first = blockIdx.x / S;
+  const int tiles = p.tiles_n;
+  const int kb0 = (int)((int64_t)p.KB * rank / S), kb1 = (int)((int64_t)p.KB * (rank + 1) / S);
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_w = ptx::l2_evict_first_policy(), pol_x = ptx::l2_evict_last_policy();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += clusters) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = smem_base + stage * stage_bytes, fb = ptx::smem_u32(&full[stage]);
+          ptx::mbar_arrive_expect_tx(fb, stage_bytes);
+          if constexpr (kGated) {
+            ptx::tma_load_2d(sb, &maps.w, kb * lin::kBK, t * 64, fb, pol_w);
+            ptx::tma_load_2d(sb + 64 * 128, &maps.w, kb * lin::kBK, (int)p.N + t * 64, fb, pol_w);
+          } else {
+            ptx::tma_load_2d(sb, &maps.w, kb * lin::kBK, t * 128, fb, pol_w);
+          }
+          ptx::tma_load_2d(sb + lin::kTileBytes, &maps.x, kb * lin::kBK, 0, fb, pol_x);
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      for (int s = 0; ok && s < n_stages; ++s) {  // no load is in flight at exit
+        ok = wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok)  // aborted: let what is in flight land
+        for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(npad >> 3) << 17) | ((128u >> 4) << 24);
+      int stage = 0;
+      uint32_t phase = 0, aph = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += clusters) {
+        if (!wait_bar(ptx::smem_u32(acce), aph ^ 1, ctl)) break;
+        ptx::tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sb = smem_base + stage * stage_bytes;
+          const uint64_t da = ptx::smem_desc(sb, 16, 1024, ptx::kSwizzle128B);
+          const uint64_t db = ptx::smem_desc(sb + lin::kTileBytes, 16, 1024, ptx::kSwizzle128B);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            ptx::tc_mma_f16(tmem_base, da + 2 * q, db + 2 * q, idesc, (kb > kb0 || q > 0) ? 1u : 0u);
+          ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        ptx::tc_commit(ptx::smem_u32(accf));
+        aph ^= 1;
+      }
+      ptx::tc_commit(ptx::smem_u32(drain));
+      wait_bar_drain(ptx::smem_u32(drain), 0);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, ep = threadIdx.x - 64;
+    uint32_t ph = 0;
+    for (int t = first; t < tiles; t += clusters, ph ^= 1) {
+      bool ok = warp_wait_bar(ptx::smem_u32(accf), ph, ctl);
+      // the partial sums of the tile before have been read by every CTA of the cluster
+      if (ok && S > 1) ok = wait_bar_cluster(ptx::smem_u32(pfree), ph ^ 1, ctl);
+      if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
+      for (int c0 = 0; c0 < T; c0 += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld_32x32b_x16(taddr + c0, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c0 + j < T) part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(acce));
+      ptx::bar_sync(1, 128);
+      if (S > 1) {
+        if (ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pready), ep));
+        if (!ptx::bar_all(1, 128, wait_bar_cluster(ptx::smem_u32(pready), ph, ctl))) break;
+      }
+      // this CTA's share of the tile's T x kCols outputs, columns fastest
+      const int total = T * kCols, lo = (int)((int64_t)total * rank / S), hi = (int)((int64_t)total * (rank + 1) / S);
+      for (int i = lo + ep; i < hi; i += 128) {
+        const int tok = i / kCols, c = i - tok * kCols;
+        const int64_t n = (int64_t)t * kCols + c;
+        if (n >= p.N) continue;
+        float v = 0.f, u = 0.f;
+        if (S > 1) {
+          const uint32_t a = ptx::smem_u32(part + tok * 128 + c);
+          for (int s = 0; s < S; ++s) {
+            const uint32_t b = ptx::map_to_rank(a, s);
+            v += ptx::ld_cluster_f32(b);
+            if constexpr (kGated) u += ptx::ld_cluster_f32(b + 64 * 4);
+          }
+        } else {
+          v = part[tok * 128 + c];
+          if constexpr (kGated) u = part[tok * 128 + 64 + c];
+        }
+        if (p.bias) v += __bfloat162float(p.bias[n]);
+        if constexpr (kGated) {
+          if (p.bias) u += __bfloat162float(p.bias[p.N + n]);
+          v = silu(v) * u;
+        } else {
+          v = activate(kAct, v);
+        }
+        store_out(p, tok, n, v);
+      }
+      ptx::bar_sync(1, 128);
+      if (S > 1 && ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pfree), ep));
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (S > 1) ptx::cluster_sync();  // other CTAs read this one's partial sums and arrive on its barriers
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, tmem_cols);
+  }
+  if (threadIdx.x == 0) {
+    p.hdr[1 + blockIdx.x] = *s_err;
+    if (blockIdx.x == 0) p.hdr[0] = gridDim.x;
+  }
+}
+
+// ============================================================================ rows off 16-byte boundaries
+// dst [rows, Kp] = src [rows, K] (row stride ld), zero past K; Kp = K rounded up to 8.
+__global__ void __launch_bounds__(256) linear_repitch_kernel(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t K,
+                                                             int64_t Kp, int64_t ld) {
+  ptx::griddep_wait();
+  const int64_t per = Kp / 8, n = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per, k = (i - r * per) * 8;
+    const uint16_t* s = src + r * ld + k;
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k + j < K ? s[j] : (uint16_t)0;
+    *reinterpret_cast<uint4*>(dst + r * Kp + k) = *reinterpret_cast<const uint4*>(v);
+  }
+}
+
+cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t rows, int64_t K, int64_t Kp,
+                                  int64_t ld, int sms, cudaStream_t s) {
+  const int64_t n = rows * (Kp / 8), blocks = (n + 255) / 256;
+  linear_repitch_kernel<<<(unsigned)std::min<int64_t>(blocks, (int64_t)sms * 16), 256, 0, s>>>(
+      reinterpret_cast<const uint16_t*>(src), reinterpret_cast<uint16_t*>(dst), rows, K, Kp, ld);
+  return cudaGetLastError();
+}
+
+// ============================================================================ plan and launch
+void plan_linear(LinearParams& p, int sms) {
+  const int64_t rows_w = p.act == GMMFR_ACT_SWIGLU ? 2 * p.N : p.N;
+  p.KB = (int32_t)((p.K + lin::kBK - 1) / lin::kBK);
+  if (p.M <= kLinearStreamRows) {
+    p.stream = 1;
+    p.bn = (int32_t)((p.M + 15) / 16 * 16);
+    p.tiles_m = 1;
+    p.tiles_n = (int32_t)(p.act == GMMFR_ACT_SWIGLU ? (p.N + 63) / 64 : (p.N + 127) / 128);
+    const int stage = lin::kTileBytes + p.bn * 128;
+    p.n_stages = std::min<int>(lin::kStreamMaxStages, (lin::stream_arena((int)p.M) - (int)p.M * 512) / stage);
+    // the cluster size that ends soonest: tiles in waves over the CTAs that fit, each a share of the K blocks
+    // and a fixed cost of about six of them
+    const int per_sm = p.M <= 32 ? 2 : 1;
+    double best = 1e30;
+    for (int S = 1; S <= 8 && S <= p.KB; S *= 2) {
+      const int64_t slots = std::max<int64_t>(1, per_sm * sms / S);
+      const double waves = (double)((p.tiles_n + slots - 1) / slots);
+      const double t = waves * ((double)((p.KB + S - 1) / S) + 6.0);
+      if (t < best) {
+        best = t;
+        p.split = S;
+        p.grid = (int32_t)(std::min<int64_t>(p.tiles_n, slots) * S);
+      }
+    }
+    return;
+  }
+  p.stream = 0;
+  const int pairs = sms / 2;
+  p.tiles_m = (int32_t)((p.M + 255) / 256);
+  // tile width that ends soonest: the products take 2.1 BN cycles per K block, the loads of a CTA's operands
+  // (128 + BN / 2 rows of 128 bytes) about a byte per 1/50 cycle; waves of tiles over the pairs
+  double best = 1e30;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    if (p.act == GMMFR_ACT_SWIGLU && bn % 64) continue;
+    const int64_t tn = (rows_w + bn - 1) / bn, tiles = tn * p.tiles_m;
+    const double waves = (double)((tiles + pairs - 1) / pairs);
+    const double t = waves * (p.KB * std::max(2.1 * bn, (16384.0 + 64.0 * bn) / 50.0) + 300.0) + 12.0 * bn;
+    if (t < best) {
+      best = t;
+      p.bn = bn;
+      p.tiles_n = (int32_t)tn;
+    }
+  }
+  if (p.act == GMMFR_ACT_SWIGLU) p.tiles_n = (int32_t)((p.N + p.bn / 2 - 1) / (p.bn / 2));
+  p.n_stages = std::min<int>(lin::kPairMaxStages, lin::kPairArena / (lin::kTileBytes + p.bn * 64));
+  p.group_m = 8;
+  p.grid = (int32_t)(2 * std::min<int64_t>(pairs, (int64_t)p.tiles_m * p.tiles_n));
+  p.split = 2;
+}
+
+template <int kAct>
+static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
+  auto kernel = p.stream ? linear_stream_kernel<kAct> : linear_pair_kernel<kAct>;
+  const int smem = p.stream ? lin::stream_smem((int)p.M) : lin::kPairSmem;
+  static int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         lin::stream_smem(kLinearStreamRows));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)p.grid);
+  lc.blockDim = dim3(lin::kThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&lc, kernel, maps, p);
+}
+
+cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
+  switch (p.act) {
+    case GMMFR_ACT_RELU: return launch_one<GMMFR_ACT_RELU>(maps, p, s);
+    case GMMFR_ACT_GELU: return launch_one<GMMFR_ACT_GELU>(maps, p, s);
+    case GMMFR_ACT_GELU_TANH: return launch_one<GMMFR_ACT_GELU_TANH>(maps, p, s);
+    case GMMFR_ACT_SILU: return launch_one<GMMFR_ACT_SILU>(maps, p, s);
+    case GMMFR_ACT_SWIGLU: return launch_one<GMMFR_ACT_SWIGLU>(maps, p, s);
+    default: return launch_one<GMMFR_ACT_NONE>(maps, p, s);
+  }
 }
 
 }  // namespace gmmfr

@@ -1,8 +1,14 @@
 // Parameters and launchers of the router, the few-token MoE layer and the dense product.
 #pragma once
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 
 namespace gmmfr {
+
+// defined in api.cu
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // null when the driver has none
+int sm_count();
 
 constexpr int kMaxTopk = 32;
 constexpr int kMaxGroups = 64;
@@ -51,12 +57,28 @@ struct LayerParams {
 };
 cudaError_t launch_layer(const LayerParams& p, cudaStream_t s);
 
+// Up to this many rows the dense product streams the weights past all of them.
+constexpr int kLinearStreamRows = 128;
+
 struct LinearParams {
-  const __nv_bfloat16 *x, *w, *bias, *residual;
+  const __nv_bfloat16 *x, *w, *bias, *residual;  // x and w at 16-byte row pitches
   void* out;
+  uint32_t* hdr;  // error words
   int64_t M, N, K, ldx, ldw, ldr, ldo;
+  int64_t timeout_ns;
   int32_t act, out_f32;
+  int32_t vec_out;  // rows of out and residual on 16-byte boundaries
+  // plan_linear's choice
+  int32_t stream;            // few rows: weights streamed past them
+  int32_t bn;                // N of the products: rows of x (stream), columns of a tile before gating (pair)
+  int32_t KB, tiles_m, tiles_n, n_stages, split, group_m, grid;
 };
-cudaError_t launch_linear(const LinearParams& p, cudaStream_t s);
+struct LinearMaps {
+  CUtensorMap x, w;
+};
+void plan_linear(LinearParams& p, int sms);
+cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
+cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t rows, int64_t K, int64_t Kp,
+                                  int64_t ld, int sms, cudaStream_t s);
 
 }  // namespace gmmfr

@@ -54,6 +54,20 @@ __device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, con
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// Bounded wait on a barrier that other CTAs of the cluster arrive on, ordering what they wrote.
+__device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, const Ctl& c) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait_cluster(bar, parity)) {
+    if (*c.abort) return false;
+    if (ptx::globaltimer() - t0 > (uint64_t)c.timeout_ns) {
+      *c.abort = 1;
+      atomicOr(c.err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 // Wait used while draining after an abort: ignores the abort flag, fixed 1 s limit.
 __device__ __forceinline__ bool wait_bar_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer();

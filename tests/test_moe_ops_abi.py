@@ -19,7 +19,7 @@ def _lib():
 def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(B.GateProblem) == 5 * 8 + 6 * 4 + 4 + 4  # padded to 8
     assert ctypes.sizeof(B.LayerProblem) == ctypes.sizeof(B.GateProblem) + 4 * 8 + 4 + 4
-    assert ctypes.sizeof(B.LinearProblem) == 7 * 8 + 2 * 4
+    assert ctypes.sizeof(B.LinearProblem) == 7 * 8 + 3 * 4 + 4
 
 
 def _gate(**kw):
@@ -130,7 +130,7 @@ def _linear(**kw):
 @pytest.mark.parametrize("kw,msg", [
     (dict(M=-1), "M=-1"), (dict(N=-1), "N=-1"), (dict(K=0), "K=0"), (dict(M=1 << 31), "M="), (dict(N=1 << 30), "N="),
     (dict(ldx=31), "ldx=31"), (dict(ldw=8), "ldw=8"), (dict(ld_residual=15), "ld_residual=15"), (dict(ld_out=1), "ld_out=1"),
-    (dict(activation=6), "activation=6"), (dict(activation=-1), "activation"), (dict(out_type=B.DT_U8), "out_type")],
+    (dict(activation=6), "activation=6"), (dict(activation=-1), "activation"), (dict(unaligned=2), "unaligned"), (dict(out_type=B.DT_U8), "out_type")],
     ids=lambda v: str(v)[:24])
 def test_linear_refusals(kw, msg):
     for call in (lambda p: B.gmmfr_linear_workspace_size(p), lambda p: B.gmmfr_linear(p, A, A, None, None, A, A, 1 << 40)):
@@ -147,5 +147,15 @@ def test_linear_pointer_refusals():
         assert ei.value.status == B.ERR_INVALID_ARG
     with pytest.raises(B.GmmfrError):  # a float32 out on a 2-byte boundary
         B.gmmfr_linear(_linear(out_type=B.DT_F32), A, A, None, None, A + 2, A, 1 << 40)
+    for args, msg in (((A + 2, A, None, None, A), "unaligned"), ((A, A + 8, None, None, A), "unaligned")):
+        with pytest.raises(B.GmmfrError, match=msg):
+            B.gmmfr_linear(_linear(), *args, A, 1 << 40)
+    big = B.gmmfr_linear_workspace_size(_linear(unaligned=1))
+    assert big > B.gmmfr_linear_workspace_size(_linear()) == 4096
+    for p, ws, n in ((_linear(), None, 1 << 20), (_linear(), A + 8, 1 << 20), (_linear(), A, 4095), (_linear(unaligned=1), A, big - 1),
+                     (_linear(K=33), A, 4096)):
+        with pytest.raises(B.GmmfrError) as ei:
+            B.gmmfr_linear(p, A, A, None, None, A, ws, n)
+        assert ei.value.status == B.ERR_WORKSPACE
     B.gmmfr_linear(_linear(M=0), None, None, None, None, None, None, 0)
     B.gmmfr_linear(_linear(N=0), None, None, None, None, None, None, 0)
