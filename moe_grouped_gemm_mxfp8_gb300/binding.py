@@ -508,6 +508,8 @@ def ffn_prepare_mx(H: int, I: int, E: int, w13, w13_scale, w2, w2_scale, stream=
 
 
 # ------------------------------------------------------------- handles of the router, the layer, the product
+# A call of a handle costs the host as little as Python allows (its GPU work may be a few microseconds):
+# what does not change between calls is marshalled once, in the constructor.
 def _numel(shape) -> int:
     n = 1
     for d in shape:
@@ -515,53 +517,63 @@ def _numel(shape) -> int:
     return n
 
 
-def _rows(t, name: str, cols: int, dtype):
-    """(address, row stride) of a 2-D device tensor whose rows are contiguous."""
-    if not t.is_cuda:
+def _refuse(name, t, want):
+    if t is not None and not t.is_cuda:
         raise ValueError("gmmfr takes device tensors")
-    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected [rows, {cols}] {dtype}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: elements of a row must be contiguous, got strides {t.stride()}")
-    # one row has no stride to speak of, and an expanded row (stride 0) is not a row of its own
-    if t.shape[0] > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+    raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} strides {t.stride()}, expected {want}")
 
 
-def _row_shape(t, name: str, rows: int, cols: int, dtype):
-    if t.dim() != 2 or t.shape[0] != rows:
-        raise ValueError(f"{name}: {tuple(t.shape)}, expected ({rows}, {cols})")
-    return _rows(t, name, cols, dtype)
+def _rows(t, name: str, rows, cols: int, dtype):
+    """The row stride of a 2-D device tensor [rows, cols] (rows None: any) whose rows are contiguous; 0
+    (dense) when it has one row, which has no stride to speak of."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or shape[1] != cols or not t.is_cuda or (rows is not None and shape[0] != rows):
+        _refuse(name, t, f"[{'rows' if rows is None else rows}, {cols}] {dtype}")
+    ld, inner = t.stride()
+    if shape[0] > 1:
+        # an expanded row (stride 0) is not a row of its own
+        if ld < cols or (inner != 1 and cols > 1):
+            _refuse(name, t, "rows that are contiguous and do not overlap")
+        return ld
+    if inner != 1 and cols > 1:
+        _refuse(name, t, "contiguous rows")
+    return 0
+
+
+def _dense(t, name: str, shape, dtype):
+    """The address of a dense device tensor of this shape, or None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(name, t, f"dense {shape} {dtype}")
+    return t.data_ptr()
 
 
 class _Handle:
     """Workspaces of a handle, one per stream it has been called on (a workspace serves one call in
-    flight at a time); they grow with the largest call."""
+    flight at a time); they grow with the largest call.  A handle serves one host thread at a time."""
 
     def __init__(self, device):
-        load()
+        import torch
+        if device.type != "cuda":
+            raise ValueError("gmmfr takes device tensors")
+        self._lib = load()
         self._device = device
+        self._index = torch.cuda.current_device() if device.index is None else device.index
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._empty = torch.empty
         self._spaces = {}
 
-    def _workspace(self, stream: int, bytes_needed: int):
-        ws = self._spaces.get(stream)
-        if ws is None or ws.numel() < bytes_needed:
-            import torch
-            ws = torch.empty(max(bytes_needed, 256), dtype=torch.uint8, device=self._device)
-            if stream != torch.cuda.current_stream(self._device).cuda_stream:
-                ws.record_stream(torch.cuda.ExternalStream(stream, device=self._device))
-            self._spaces[stream] = ws
-        return ws.data_ptr(), ws.numel()
-
-    def _on(self, stream):
-        """The stream's address; None is the current one."""
+    def _grow(self, stream: int, need: int):
         import torch
-        return (torch.cuda.current_stream(self._device) if stream is None else stream).cuda_stream
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self._device)
+        if stream != self._raw_stream(self._index):
+            ws.record_stream(torch.cuda.ExternalStream(stream, device=self._device))
+        self._spaces[stream] = entry = (ws.data_ptr(), ws.numel(), ws)
+        return entry
 
     def _new(self, shape, dtype, stream):
-        import torch
-        t = torch.empty(shape, dtype=dtype, device=self._device)
+        t = self._empty(shape, dtype=dtype, device=self._device)
         if stream is not None:
             t.record_stream(stream)
         return t
@@ -569,13 +581,13 @@ class _Handle:
 
 def _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale) -> GateProblem:
     import torch
+    if weight.dim() != 2:
+        _refuse("weight", weight, "[E, H]")
     E, H = weight.shape
-    _rows(weight, "weight", H, torch.bfloat16)
-    _ptr(weight)
+    _dense(weight, "weight", (E, H), torch.bfloat16)
+    _dense(select_bias, "select_bias", (E,), torch.float32)
     if scoring not in GATE_SCORING:
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(GATE_SCORING)}")
-    if select_bias is not None and (select_bias.dtype != torch.float32 or tuple(select_bias.shape) != (E,)):
-        raise ValueError(f"select_bias: {tuple(select_bias.shape)} {select_bias.dtype}, expected ({E},) float32")
     return GateProblem(T=0, H=H, E=E, topk=topk, ldx=0, scoring=GATE_SCORING[scoring], n_group=n_group,
                        topk_group=topk_group, group_top=group_top, renormalise=int(bool(renormalise)),
                        ids_type=INDEX_I32, scale=scale)
@@ -590,30 +602,46 @@ class MoeGate(_Handle):
                  ids_dtype=None):
         import torch
         super().__init__(weight.device)
-        self._p = _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
+        self._p = p = _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
         self._ids_dtype = torch.int32 if ids_dtype is None else ids_dtype
         if self._ids_dtype not in (torch.int32, torch.int64):
             raise ValueError(f"ids_dtype {ids_dtype} is not int32 or int64")
-        self._p.ids_type = INDEX_I32 if self._ids_dtype == torch.int32 else INDEX_I64
-        self._weight, self._bias = weight, select_bias
+        p.ids_type = INDEX_I32 if self._ids_dtype == torch.int32 else INDEX_I64
+        self._keep = (weight, select_bias)
+        self._wptr, self._bptr = weight.data_ptr(), _ptr(select_bias)
         self._bf16, self._f32 = torch.bfloat16, torch.float32
-        gmmfr_moe_gate_workspace_size(self._p)  # refuses a rule that is out of range
+        self._H, self._E, self._topk = p.H, p.E, p.topk
+        self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_moe_gate
+        gmmfr_moe_gate_workspace_size(p)  # refuses a rule that is out of range
+        self._T, self._need = 0, 0
 
     def __call__(self, x, ids=None, weights=None, logits=None, stream=None):
         p = self._p
-        ptr, p.ldx = _rows(x, "x", p.H, self._bf16)
-        p.T = T = x.shape[0]
-        for name, t, shape, dt in (("ids", ids, (T, p.topk), self._ids_dtype), ("weights", weights, (T, p.topk), self._f32),
-                                   ("logits", logits, (T, p.E), self._f32)):
-            if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
-                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} {dt}")
-        s = self._on(stream)
+        p.ldx = _rows(x, "x", None, self._H, self._bf16)
+        T = x.shape[0]
+        if T != self._T:
+            p.T = T
+            self._need = gmmfr_moe_gate_workspace_size(p)
+            self._T = T
+        shape = (T, self._topk)
         if ids is None:
-            ids = self._new((T, p.topk), self._ids_dtype, stream)
+            ids = self._new(shape, self._ids_dtype, stream)
+            iptr = ids.data_ptr()
+        else:
+            iptr = _dense(ids, "ids", shape, self._ids_dtype)
         if weights is None:
-            weights = self._new((T, p.topk), self._f32, stream)
-        ws, n = self._workspace(s, gmmfr_moe_gate_workspace_size(p))
-        gmmfr_moe_gate(p, ptr, _ptr(self._weight), _ptr(self._bias), _ptr(ids), _ptr(weights), _ptr(logits), ws, n, s)
+            weights = self._new(shape, self._f32, stream)
+            wptr = weights.data_ptr()
+        else:
+            wptr = _dense(weights, "weights", shape, self._f32)
+        lptr = None if logits is None else _dense(logits, "logits", (T, self._E), self._f32)
+        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
+        ws = self._spaces.get(s)
+        if ws is None or ws[1] < self._need:
+            ws = self._grow(s, self._need)
+        st = self._fn(self._ref, x.data_ptr(), self._wptr, self._bptr, iptr, wptr, lptr, ws[0], ws[1], s)
+        if st:
+            _check(st)
         return ids, weights
 
 
@@ -639,11 +667,18 @@ class MoeLayer(_Handle):
         if shared_w13 is not None:
             shared_I = shared_w2.shape[0]
             self._shared = self._prepare(1, H, shared_I, shared_w13, shared_w13_scale, shared_w2, shared_w2_scale, mx)
-        self._p = LayerProblem(gate=gp, I=I, shared_I=shared_I, ld_residual=0, ld_out=0,
-                               weight_type=DT_E4M3 if mx else DT_BF16)
-        self._weight, self._bias = gate_weight, select_bias
+        self._p = p = LayerProblem(gate=gp, I=I, shared_I=shared_I, ld_residual=0, ld_out=0,
+                                   weight_type=DT_E4M3 if mx else DT_BF16)
+        self._g = p.gate
+        self._keep = (gate_weight, select_bias)
+        self._wptr, self._bptr = gate_weight.data_ptr(), _ptr(select_bias)
+        self._weights = (self._prepared.data_ptr(), self._prepared.numel(), _ptr(self._shared),
+                         0 if self._shared is None else self._shared.numel())
         self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
-        gmmfr_moe_layer_workspace_size(self._p)
+        self._H, self._topk = H, gp.topk
+        self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_moe_layer
+        gmmfr_moe_layer_workspace_size(p)
+        self._T, self._need = 0, 0
 
     @staticmethod
     def _prepare(E, H, I, w13, s13, w2, s2, mx):
@@ -656,24 +691,32 @@ class MoeLayer(_Handle):
         return ffn_prepare(H, I, E, w13, w2)
 
     def __call__(self, x, residual=None, out=None, topk_ids=None, topk_weights=None, stream=None):
-        p = self._p
-        g = p.gate
-        ptr, g.ldx = _rows(x, "x", g.H, self._bf16)
-        g.T = T = x.shape[0]
+        p, g, H = self._p, self._g, self._H
+        g.ldx = _rows(x, "x", None, H, self._bf16)
+        T = x.shape[0]
+        if T != self._T:
+            g.T = T
+            self._need = gmmfr_moe_layer_workspace_size(p)
+            self._T = T
         rptr = None
         if residual is not None:
-            rptr, p.ld_residual = _row_shape(residual, "residual", T, g.H, self._bf16)
-        s = self._on(stream)
+            p.ld_residual = _rows(residual, "residual", T, H, self._bf16)
+            rptr = residual.data_ptr()
         if out is None:
-            out = self._new((T, g.H), self._bf16, stream)
-        optr, p.ld_out = _row_shape(out, "out", T, g.H, self._bf16)
-        for name, t, dt in (("topk_ids", topk_ids, self._i32), ("topk_weights", topk_weights, self._f32)):
-            if t is not None and (t.dtype != dt or tuple(t.shape) != (T, g.topk)):
-                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {(T, g.topk)} {dt}")
-        ws, n = self._workspace(s, gmmfr_moe_layer_workspace_size(p))
-        gmmfr_moe_layer(p, ptr, _ptr(self._weight), _ptr(self._bias), rptr, optr, _ptr(self._prepared),
-                        self._prepared.numel(), _ptr(self._shared), 0 if self._shared is None else self._shared.numel(),
-                        _ptr(topk_ids), _ptr(topk_weights), ws, n, s)
+            out = self._new((T, H), self._bf16, stream)
+            p.ld_out = 0
+        else:
+            p.ld_out = _rows(out, "out", T, H, self._bf16)
+        iptr = None if topk_ids is None else _dense(topk_ids, "topk_ids", (T, self._topk), self._i32)
+        kptr = None if topk_weights is None else _dense(topk_weights, "topk_weights", (T, self._topk), self._f32)
+        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
+        ws = self._spaces.get(s)
+        if ws is None or ws[1] < self._need:
+            ws = self._grow(s, self._need)
+        st = self._fn(self._ref, x.data_ptr(), self._wptr, self._bptr, rptr, out.data_ptr(), *self._weights, iptr, kptr,
+                      ws[0], ws[1], s)
+        if st:
+            _check(st)
         return out
 
 
@@ -691,31 +734,47 @@ class Linear(_Handle):
         self._out = torch.bfloat16 if out_dtype is None else out_dtype
         if self._out not in (torch.bfloat16, torch.float32):
             raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
+        if weight.dim() != 2:
+            _refuse("weight", weight, "[N, K]")
         rows, K = weight.shape
-        self._wptr, ldw = _rows(weight, "weight", K, torch.bfloat16)
+        ldw = _rows(weight, "weight", None, K, torch.bfloat16)
         if activation == "swiglu" and rows % 2:
             raise ValueError(f"weight: {rows} rows; swiglu takes gate and up rows, an even number")
-        if bias is not None and (bias.dtype != torch.bfloat16 or tuple(bias.shape) != (rows,)):
-            raise ValueError(f"bias: {tuple(bias.shape)} {bias.dtype}, expected ({rows},) bfloat16")
-        self._weight, self._bias = weight, bias
-        self._p = LinearProblem(M=0, N=rows // 2 if activation == "swiglu" else rows, K=K, ldx=0, ldw=ldw, ld_residual=0,
-                                ld_out=0, activation=ACTIVATIONS[activation],
-                                out_type=DT_F32 if self._out == torch.float32 else DT_BF16)
+        self._bptr = _dense(bias, "bias", (rows,), torch.bfloat16)
+        self._keep = (weight, bias)
+        self._wptr = weight.data_ptr()
+        self._K, self._N = K, rows // 2 if activation == "swiglu" else rows
+        self._p = p = LinearProblem(M=0, N=self._N, K=K, ldx=0, ldw=ldw, ld_residual=0, ld_out=0,
+                                    activation=ACTIVATIONS[activation],
+                                    out_type=DT_F32 if self._out == torch.float32 else DT_BF16)
         self._bf16 = torch.bfloat16
-        gmmfr_linear_workspace_size(self._p)
+        self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_linear
+        gmmfr_linear_workspace_size(p)
+        self._seen, self._need = None, 0
 
     def __call__(self, x, residual=None, out=None, stream=None):
-        p = self._p
-        ptr, p.ldx = _rows(x, "x", p.K, self._bf16)
-        p.M = M = x.shape[0]
+        p, N = self._p, self._N
+        ldx = _rows(x, "x", None, self._K, self._bf16)
+        M, xptr = x.shape[0], x.data_ptr()
+        seen = (M, ldx, (xptr | self._wptr) & 15)
+        if seen != self._seen:
+            p.M, p.ldx, p.unaligned = M, ldx, int(seen[2] != 0)
+            self._need = gmmfr_linear_workspace_size(p)
+            self._seen = seen
         rptr = None
         if residual is not None:
-            rptr, p.ld_residual = _row_shape(residual, "residual", M, p.N, self._bf16)
-        s = self._on(stream)
+            p.ld_residual = _rows(residual, "residual", M, N, self._bf16)
+            rptr = residual.data_ptr()
         if out is None:
-            out = self._new((M, p.N), self._out, stream)
-        optr, p.ld_out = _row_shape(out, "out", M, p.N, self._out)
-        p.unaligned = int((ptr | self._wptr) & 15 != 0)
-        ws, n = self._workspace(s, gmmfr_linear_workspace_size(p))
-        gmmfr_linear(p, ptr, self._wptr, _ptr(self._bias), rptr, optr, ws, n, s)
+            out = self._new((M, N), self._out, stream)
+            p.ld_out = 0
+        else:
+            p.ld_out = _rows(out, "out", M, N, self._out)
+        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
+        ws = self._spaces.get(s)
+        if ws is None or ws[1] < self._need:
+            ws = self._grow(s, self._need)
+        st = self._fn(self._ref, xptr, self._wptr, self._bptr, rptr, out.data_ptr(), ws[0], ws[1], s)
+        if st:
+            _check(st)
         return out

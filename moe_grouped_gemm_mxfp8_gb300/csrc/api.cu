@@ -5,6 +5,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -263,7 +264,15 @@ namespace gmmfr {
 // Records `message` as the calling thread's last error (for other files of the library).
 gmmfr_status record_error(gmmfr_status st, const char* message) { return fail(st, "%s", message); }
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encode_fn(); }
-int sm_count() { return device_sms(); }
+int sm_count() {  // asked once per device: small calls notice each runtime call
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return device_sms();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) known[dev].store(n = device_sms(), std::memory_order_relaxed);
+  return n;
+}
 }  // namespace gmmfr
 
 extern "C" {

@@ -1,5 +1,6 @@
 // C ABI of the router, the few-token MoE layer and the dense product (declared in include/gmmfr.h):
 // argument checks, workspace layout, launches.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 
@@ -113,20 +114,38 @@ gmmfr_status validate_layer(const gmmfr_layer_problem* p) {
 }
 
 struct LayerLayout {
-  size_t logits, ids, weights, sw, total;
+  int64_t npad, NT1, KB1, NT2, KB2, NT1s, KB2s, n_counters;
+  size_t logits, ids, weights, counters, ximg, swimg, swimg_s, slots_up, slots_down, total;
 };
 LayerLayout layer_layout(const gmmfr_layer_problem* p) {
   LayerLayout L{};
-  const int64_t T = p->gate.T, k = p->gate.topk;
-  size_t off = 0;
-  L.logits = off;
-  off = align256(off + sizeof(float) * (size_t)T * p->gate.E);
-  L.ids = off;
-  off = align256(off + sizeof(int32_t) * (size_t)T * k);
-  L.weights = off;
-  off = align256(off + sizeof(float) * (size_t)T * k);
-  L.sw = off;
-  off = align256(off + sizeof(float) * (size_t)T * (k * p->I + p->shared_I));
+  const bool mx = p->weight_type == GMMFR_DT_E4M3;
+  const int64_t T = p->gate.T, k = p->gate.topk, H = p->gate.H, kt = mx ? 128 : 64;
+  L.npad = std::max<int64_t>(16, cdiv(T, 16) * 16);
+  L.NT1 = cdiv(p->I, 64);
+  L.KB1 = cdiv(H, kt);
+  L.NT2 = cdiv(H, 128);
+  L.KB2 = cdiv(p->I, kt);
+  L.NT1s = cdiv(p->shared_I, 64);
+  L.KB2s = cdiv(p->shared_I, kt);
+  const int64_t experts = std::min<int64_t>(p->gate.E, T * k);  // at most so many are chosen
+  L.n_counters = 2 + L.NT1s + experts * L.NT1 + L.NT2;
+  const size_t img = (size_t)gmmfr::layer_image_bytes(mx, L.npad);
+  size_t off = gmmfr::kHdrBytes;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.logits = take(sizeof(float) * (size_t)T * p->gate.E);
+  L.ids = take(sizeof(int32_t) * (size_t)T * k);
+  L.weights = take(sizeof(float) * (size_t)T * k);
+  L.counters = take(sizeof(uint32_t) * (size_t)L.n_counters);
+  L.ximg = take(img * L.KB1);
+  L.swimg = take(img * experts * L.KB2);
+  L.swimg_s = take(img * L.KB2s);
+  L.slots_up = take(sizeof(float) * 128 * T * 4 * gmmfr::kLayerMaxCtas);
+  L.slots_down = take(sizeof(float) * 128 * T * 2 * gmmfr::kLayerMaxCtas);
   L.total = off;
   return L;
 }
@@ -294,13 +313,33 @@ gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, 
   lp.out = static_cast<__nv_bfloat16*>(out);
   lp.prepared = static_cast<const uint8_t*>(prepared);
   lp.shared = static_cast<const uint8_t*>(shared_prepared);
-  lp.sw = reinterpret_cast<float*>(ws + L.sw);
-  lp.I = p.I;
-  lp.shared_I = p.shared_I;
   lp.ld_residual = stride_or(p.ld_residual, p.gate.H);
   lp.ld_out = stride_or(p.ld_out, p.gate.H);
   lp.mx = mx;
-  cudaError_t e = gmmfr::launch_layer(lp, static_cast<cudaStream_t>(stream));
+  const int64_t tile = mx ? gmmfr::kPrepTileBytes : gmmfr::kWTileBytes;
+  lp.prepared2 = lp.prepared + p.gate.E * L.NT1 * L.KB1 * tile;
+  lp.shared2 = lp.shared + L.NT1s * L.KB1 * tile;
+  lp.hdr = reinterpret_cast<uint32_t*>(ws);
+  lp.ximg = ws + L.ximg;
+  lp.swimg = ws + L.swimg;
+  lp.swimg_s = ws + L.swimg_s;
+  lp.slots_up = reinterpret_cast<float*>(ws + L.slots_up);
+  lp.slots_down = reinterpret_cast<float*>(ws + L.slots_down);
+  lp.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
+  lp.select_done = lp.counters;
+  lp.up_done = lp.counters + 1;
+  lp.down_cnt = lp.counters + 2;
+  lp.up_cnt = lp.down_cnt + L.NT2;
+  lp.n_counters = (int32_t)L.n_counters;
+  lp.npad = (int32_t)L.npad;
+  lp.NT1 = (int32_t)L.NT1;
+  lp.KB1 = (int32_t)L.KB1;
+  lp.NT2 = (int32_t)L.NT2;
+  lp.KB2 = (int32_t)L.KB2;
+  lp.NT1s = (int32_t)L.NT1s;
+  lp.KB2s = (int32_t)L.KB2s;
+  lp.timeout_ns = 4000000000ll;
+  cudaError_t e = gmmfr::launch_layer(lp, gmmfr::sm_count(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "MoE layer launch");
   return GMMFR_OK;
 }

@@ -16,7 +16,7 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 
 // One warp selects token `logits[0..E)`'s experts; lane k < topk returns the k-th expert and its
 // weight.  Expert e sits in lane e % 32, register e / 32 (kPer registers: E <= 32 * kPer).
-// `scratch`: kPer * 32 floats of shared memory of this warp, used when there are groups.
+// `scratch`: E floats of shared memory of this warp, used when there are groups.
 // All sums are FP32; the exponential's argument is at most 0 and its sum at least 1.
 template <int kPer>
 __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float* logits, const float* select_bias,
@@ -57,7 +57,7 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
     float s = p[i];
     if (select_bias != nullptr && e < r.E) s += select_bias[e];
     key[i] = e < r.E ? order_key(s) : 0u;
-    if (r.n_group > 1) scratch[e] = s;
+    if (r.n_group > 1 && e < r.E) scratch[e] = s;
   }
   if (r.n_group > 1) {
     __syncwarp();

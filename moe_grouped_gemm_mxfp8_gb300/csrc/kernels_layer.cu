@@ -1,12 +1,37 @@
-// A whole mixture-of-experts layer for a few tokens: the gate, then for every token and chosen
-// expert (and the shared expert) the gate/up product with SwiGLU, then the down product summed over
-// the token's experts.  Weights are the prepared tiles of the grouped FFN (BF16: 64 K per 128-byte row)
-// or their MXFP8 form (128 K codes per row and 512 scale bytes per tile).
+// A whole mixture-of-experts layer for a few tokens (at most 64), in two kernels.
+//
+//   front   the gate's logits; the tokens as images of the products' B operand; counters to zero
+//   layer   one persistent CTA per SM: top-k of every token, then three runs of weight tiles
+//             shared up   x times the shared expert's gate/up tiles
+//             up          x times the chosen experts' gate/up tiles  (experts in index order)
+//             down        column tile by column tile: sw times the down tiles of every chosen expert and of
+//                         the shared one, one long sum over (expert, intermediate index)
+//           each run cut into equal contiguous ranges over the CTAs.
+//
+// The weights are the 128-row operand of tcgen05.mma (prepared tiles, one bulk copy each), the tokens the N-wide
+// one: all T of them for every expert (T padded to 16), since the time goes to the weights' bytes and a token
+// that did not choose the expert costs only tensor-core slots that would idle.  Its row of sw is zero, which lets
+// the down run add all experts of a column tile into the same accumulator, the router's weight being folded into
+// sw (in FP32, before its rounding).
+// The weights' producer never waits for a token: the first tiles (shared expert) are requested before the gate is
+// known, the down tiles while other CTAs still finish the up run.
+//
+// A column tile cut between CTAs is joined through the workspace: each piece stores its FP32 sums, and
+//   up     the CTA that arrives last adds the pieces in CTA order, applies SwiGLU and stores sw;
+//   down   every CTA with a piece waits for the others at its end and adds its share of the tile.
+// Both orders are fixed, so results are the same bits every time.
+//
+// sw is rounded to what the tensor cores take: BF16, or with MXFP8 weights a sum of two E4M3 numbers with
+// their block scales (hi + lo, about as exact as BF16), and the tokens likewise: BF16's eight bits split exactly
+// into hi and lo, so that MXFP8 weights meet unrounded activations.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "epilogue.cuh"
+#include "gate_select.cuh"
 #include "ops.cuh"
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace gmmfr {
@@ -63,90 +88,776 @@ cudaError_t launch_ffn_prep_mx(const FfnPrepMxParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-namespace {
-// Sum over k of tile row r of the K blocks [0, KB) with v[k]; one lane's share (the warp adds up).
-__device__ __forceinline__ float row_dot(const uint8_t* tiles, int mx, int64_t KB, int64_t K, int r, int lane,
-                                         const __nv_bfloat16* xb, const float* xf) {
-  const int kt = mx ? 128 : 64;
-  const int64_t tb = mx ? kPrepTileBytes : kWTileBytes;
-  float acc = 0.f;
-  for (int64_t k = lane; k < KB * kt; k += 32) {
-    if (k >= K) break;
-    const uint8_t* tile = tiles + (k / kt) * tb;
-    const int c = (int)(k % kt);
-    float w;
-    if (mx) {
-      __nv_fp8_e4m3 code;
-      code.__x = tile[r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15)];
-      w = (float)code * exp2f((float)tile[kWTileBytes + 16 * (r & 31) + 4 * (r >> 5) + (c >> 5)] - 127.f);
-    } else {
-      w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(tile + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2));
-    }
-    acc = fmaf(w, xb ? __bfloat162float(xb[k]) : xf[k], acc);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  return acc;
+namespace layer {
+
+constexpr int kThreads = 256;  // warp 0 weights, 1 MMA, 2..5 epilogue, 6 tokens' producer, 7 none; 1..7 also top-k
+constexpr int kSelectWarps = 7;
+constexpr int kMaxStages = 11;
+// A stage: weight tile (with MXFP8 its 512 scale bytes), then the tokens' image: BF16 npad rows of 128 bytes;
+// MXFP8 scale chunks of hi and lo (512 bytes each), 512 unused, npad rows of hi, npad of lo.
+__host__ __device__ constexpr int tile_bytes(bool mx) { return mx ? kPrepTileBytes : kWTileBytes; }
+__host__ __device__ constexpr int rows_off(bool mx) { return mx ? 18432 : kWTileBytes; }
+__host__ __device__ constexpr int image_bytes(bool mx, int npad) { return mx ? 1536 + 256 * npad : 128 * npad; }
+__host__ __device__ constexpr int stage_bytes(bool mx, int npad) { return tile_bytes(mx) + image_bytes(mx, npad); }
+constexpr int kArena = 11 * 18432;
+__host__ __device__ constexpr int n_stages(bool mx, int npad) {
+  return kArena / stage_bytes(mx, npad) < kMaxStages ? kArena / stage_bytes(mx, npad) : kMaxStages;
 }
+static_assert(stage_bytes(true, 16) % 1024 == 0 && stage_bytes(false, 16) % 1024 == 0 && rows_off(true) % 1024 == 0,
+              "swizzled operands need 1024-byte alignment");
+static_assert(kSelectWarps * kMaxExperts * 4 <= 2 * 18432, "the selection's scratch fits the last two stages");
+constexpr int kBarOff = kArena;
+constexpr int kNumBars = 2 * kMaxStages + 5;
+constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;             // int32 misc[16]
+constexpr int kMaskOff = kMiscOff + 64;                          // uint64 mask[1024]: tokens of each expert
+constexpr int kActOff = kMaskOff + 8 * kMaxExperts;              // uint16 act[1024]: the chosen experts
+constexpr int kIdsOff = kActOff + 2 * kMaxExperts;               // uint16 ids[64 * 32]
+constexpr int kWtOff = kIdsOff + 2 * kLayerMaxTokens * kMaxTopk; // float weights[64 * 32]
+constexpr int kXchgOff = kWtOff + 4 * kLayerMaxTokens * kMaxTopk;  // float [2][16][32]: up values for SwiGLU
+constexpr int kTokWOff = kXchgOff + 2 * 16 * 32 * 4;             // float [64]: the unit's router weights
+constexpr int kSmemBytes = kTokWOff + 4 * kLayerMaxTokens + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+__host__ __device__ constexpr int sf_cols(bool mx) { return mx ? 12 : 0; }  // TMEM scale columns per stage
+constexpr int kTmemCols = 256;
+static_assert(2 * 64 + sf_cols(true) * n_stages(true, 64) <= kTmemCols && 2 * 16 + sf_cols(true) * n_stages(true, 16) <= kTmemCols &&
+                  2 * 32 + sf_cols(true) * n_stages(true, 32) <= kTmemCols && 2 * 48 + sf_cols(true) * n_stages(true, 48) <= kTmemCols,
+              "TMEM");
+
+}  // namespace layer
+
+namespace {
+
+// 16-byte chunk c of row t of a 128-byte-row image with the 128-byte swizzle.
+__device__ __forceinline__ int image_chunk(int t, int c) { return t * 128 + ((c ^ (t & 7)) << 4); }
+// Scale byte of row t, 32-block q of a tile (the layout tcgen05.cp 32x128b.warpx4 spreads over TMEM).
+__device__ __forceinline__ int scale_at(int t, int q) { return 16 * (t & 31) + 4 * (t >> 5) + q; }
+
+// The power of two that puts a block with largest magnitude bits `amax` into E4M3's upper range: hi codes stand
+// for x / 2^(e-7) (below 256 of E4M3's 448), lo codes for the rest in units of 2^(e-12).  Blocks below 2^-100
+// keep that unit.  A block with an infinity or NaN gets the NaN scale: its products are NaN.
+struct BlockScale {
+  float inv_hi, unit_hi, inv_lo;
+  uint32_t byte_hi, byte_lo;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax) {
+  BlockScale b;
+  int e = (int)(amax >> 23) - 127;
+  const bool finite = e < 128;
+  e = e < -100 ? -100 : (finite ? e : 0);
+  b.inv_hi = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+  b.unit_hi = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+  b.inv_lo = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
+  b.byte_hi = finite ? (uint32_t)(127 + e - 7) : 255u;
+  b.byte_lo = finite ? (uint32_t)(127 + e - 12) : 255u;
+  return b;
+}
+__device__ __forceinline__ void split_e4m3(float x, const BlockScale& b, uint32_t& hi, uint32_t& lo) {
+  hi = __nv_cvt_float_to_fp8(x * b.inv_hi, __NV_SATFINITE, __NV_E4M3);
+  const float h = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)hi, __NV_E4M3)));
+  lo = __nv_cvt_float_to_fp8((x - h * b.unit_hi) * b.inv_lo, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void red_release_add(uint32_t* p, uint32_t v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+// Bounded wait until *p reaches n.
+__device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n, const Ctl& c) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (ld_acquire(p) < n) {
+    if (*c.abort) return false;
+    if (ptx::globaltimer() - t0 > (uint64_t)c.timeout_ns) {
+      *c.abort = 1;
+      atomicOr(c.err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+// One run of U tiles in units of K tiles, cut evenly over G CTAs: CTA b has [U b / G, U (b + 1) / G).
+struct Run {
+  int64_t U;
+  int K, G;
+  __device__ int64_t lo(int b) const { return U * b / G; }
+  __device__ int owner(int64_t x) const { return (int)(((x + 1) * G - 1) / U); }
+  // pieces of unit u, and the CTA of piece i (with fewer tiles than CTAs every tile is a piece)
+  __device__ int pieces(int64_t u) const { return U < G ? K : owner((u + 1) * K - 1) - owner(u * K) + 1; }
+  __device__ int cta(int64_t u, int i) const { return U < G ? owner(u * K + i) : owner(u * K) + i; }
+  // a CTA's pieces of cut units lie in two slots: 0 where its range begins in the unit, 1 where it ends there
+  __device__ int slot(int64_t u, int b) const { return lo(b) >= u * K ? 0 : 1; }
+};
+
+enum { kSharedUp = 0, kUp = 1, kDown = 2 };
+
+// The pieces of one CTA: units (or parts of units) of the three runs in order; every role walks them.
+struct Walk {
+  Run run[3];
+  int seg;
+  int64_t pos, end;
+  int unit, k0, k1;
+  __device__ void begin(int first_seg, int last_seg) {
+    seg = first_seg;
+    set(last_seg);
+  }
+  __device__ void set(int last_seg) {
+    for (; seg <= last_seg; ++seg) {
+      pos = run[seg].U ? run[seg].lo(blockIdx.x) : 0;
+      end = run[seg].U ? run[seg].lo(blockIdx.x + 1) : 0;
+      if (pos < end) return;
+    }
+  }
+  // the next piece of segments up to last_seg: tiles [k0, k1) of `unit` of `seg`
+  __device__ bool next(int last_seg) {
+    if (seg > last_seg) return false;
+    const Run& r = run[seg];
+    unit = (int)(pos / r.K);
+    k0 = (int)(pos - (int64_t)unit * r.K);
+    const int64_t left = end - pos;
+    k1 = (int64_t)(r.K - k0) < left ? r.K : k0 + (int)left;
+    cur = seg;
+    pos += k1 - k0;
+    if (pos == end) {
+      ++seg;
+      set(last_seg);
+    }
+    return true;
+  }
+  int cur;  // segment of the current piece
+};
+
 }  // namespace
 
-// One warp per (token, choice, intermediate index); choice topk is the shared expert.
-__global__ void __launch_bounds__(256) layer_up_kernel(LayerParams p) {
-  const int lane = threadIdx.x & 31;
+// ============================================================================ front
+// One warp per (expert, up to 8 tokens) for the logits; then the token images and the counters.
+template <bool kMx>
+__global__ void __launch_bounds__(256) layer_front_kernel(const __grid_constant__ LayerParams p) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const GateParams& g = p.gate;
-  const int64_t topk = g.rule.topk;
-  const int64_t n_routed = g.T * topk * p.I;
-  const int64_t o = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (o >= n_routed + g.T * p.shared_I) return;
-  const bool routed = o < n_routed;
-  const int64_t I = routed ? p.I : p.shared_I;
-  const int64_t pair = (routed ? o : o - n_routed) / I, i = (routed ? o : o - n_routed) % I;
-  const int64_t t = routed ? pair / topk : pair;
-  const int64_t e = routed ? static_cast<const int32_t*>(g.ids)[pair] : 0;
-  const int64_t kt = p.mx ? 128 : 64, tb = p.mx ? kPrepTileBytes : kWTileBytes;
-  const int64_t NT = (I + 63) / 64, KB = (g.H + kt - 1) / kt;
-  const uint8_t* tiles = (routed ? p.prepared : p.shared) + (e * NT + i / 64) * KB * tb;
-  const float gate = row_dot(tiles, p.mx, KB, g.H, (int)(i & 63), lane, g.x + t * g.ldx, nullptr);
-  const float up = row_dot(tiles, p.mx, KB, g.H, (int)(i & 63) + 64, lane, g.x + t * g.ldx, nullptr);
-  if (lane == 0) p.sw[o] = silu(gate) * up * (routed ? g.weights[pair] : 1.f);
+  const int T = (int)g.T, E = g.rule.E;
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * 8, w0 = threadIdx.x / 32 * gridDim.x + blockIdx.x;
+  const int groups = (T + 7) / 8;
+  for (int task = w0; task < E * groups; task += warps) {
+    const int e = task % E, t0 = task / E * 8;
+    const __nv_bfloat16* wrow = g.weight + (int64_t)e * g.H;
+    float acc[8] = {};
+    for (int64_t h = lane * 8; h < g.H; h += 256) {
+      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(wrow + h));
+      const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (t0 + i < T) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(g.x + (int64_t)(t0 + i) * g.ldx + h);
+          const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[i] = fmaf(__uint_as_float(wu[q] << 16), __uint_as_float(xu[q] << 16), acc[i]);
+            acc[i] = fmaf(__uint_as_float(wu[q] & 0xffff0000u), __uint_as_float(xu[q] & 0xffff0000u), acc[i]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (t0 + i < T) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        if (lane == 0) g.logits[(int64_t)(t0 + i) * E + e] = acc[i];
+      }
+    }
+  }
+  const int tid = threadIdx.x * gridDim.x + blockIdx.x, threads = gridDim.x * 256;
+  for (int i = tid; i < p.n_counters; i += threads) p.counters[i] = 0;
+  // images: 8 elements of a row per thread, zero past H (their weights are zero, but 0 x NaN is not)
+  const int img = layer::image_bytes(kMx, p.npad);
+  const int per_row = p.KB1 * (kMx ? 16 : 8);
+  // a warp's 32 items are consecutive 8-element chunks of a row (per_row is a multiple of 8: quads never straddle)
+  const int items = T * per_row, w_items = (items + 31) / 32;
+  for (int wi = blockIdx.x + threadIdx.x / 32 * gridDim.x; wi < w_items; wi += warps) {
+    const int it = wi * 32 + lane;
+    const bool in = it < items;
+    const int t = in ? it / per_row : 0, c = in ? it - t * per_row : 0;
+    const int64_t h = (int64_t)c * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (in && h < g.H) v = *reinterpret_cast<const uint4*>(g.x + (int64_t)t * g.ldx + h);
+    if constexpr (!kMx) {
+      if (in) *reinterpret_cast<uint4*>(p.ximg + (int64_t)(c >> 3) * img + image_chunk(t, c & 7)) = v;
+    } else {
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      uint32_t amax = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        amax = max(amax, (u[q] << 16) & 0x7fffffffu);
+        amax = max(amax, u[q] & 0x7fff0000u);
+      }
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // four lanes hold a block of 32
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const BlockScale b = block_scale(amax);
+      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint32_t a, r;
+        split_e4m3(__uint_as_float((q & 1) ? u[q >> 1] & 0xffff0000u : u[q >> 1] << 16), b, a, r);
+        hi[q >> 2] |= a << (8 * (q & 3));
+        lo[q >> 2] |= r << (8 * (q & 3));
+      }
+      if (in) {
+        uint8_t* dst = p.ximg + (int64_t)(c >> 4) * img;
+        const int at = image_chunk(t, (c & 15) >> 1) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(dst + 1536 + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + 1536 + p.npad * 128 + at) = make_uint2(lo[0], lo[1]);
+        if ((c & 3) == 0) {
+          dst[scale_at(t, (c & 15) >> 2)] = (uint8_t)b.byte_hi;
+          dst[512 + scale_at(t, (c & 15) >> 2)] = (uint8_t)b.byte_lo;
+        }
+      }
+    }
+  }
 }
 
-// One warp per (token, output column).
-__global__ void __launch_bounds__(256) layer_down_kernel(LayerParams p) {
-  const int lane = threadIdx.x & 31;
+// ============================================================================ layer
+template <bool kMx>
+__global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_constant__ LayerParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + layer::kBarOff);  // both producers' copies landed
+  uint64_t* empty = full + layer::kMaxStages;
+  uint64_t* accf = empty + layer::kMaxStages;
+  uint64_t* acce = accf + 2;
+  uint64_t* drain = acce + 2;
+  int32_t* misc = reinterpret_cast<int32_t*>(smem + layer::kMiscOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
+  int* abort_flag = &misc[1];
+  uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
+  int* s_warp_sum = &misc[4];  // [8]
+  int* s_last = &misc[12];
+  unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(smem + layer::kMaskOff);
+  uint16_t* s_act = reinterpret_cast<uint16_t*>(smem + layer::kActOff);
+  uint16_t* s_ids = reinterpret_cast<uint16_t*>(smem + layer::kIdsOff);
+  float* s_wt = reinterpret_cast<float*>(smem + layer::kWtOff);
+  float* xchg = reinterpret_cast<float*>(smem + layer::kXchgOff);
+  float* s_tokw = reinterpret_cast<float*>(smem + layer::kTokWOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const GateParams& g = p.gate;
-  const int64_t topk = g.rule.topk;
-  const int64_t o = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (o >= g.T * g.H) return;
-  const int64_t t = o / g.H, n = o % g.H;
-  const int64_t kt = p.mx ? 128 : 64, tb = p.mx ? kPrepTileBytes : kWTileBytes;
-  const int64_t NT2 = (g.H + 127) / 128, KBh = (g.H + kt - 1) / kt;
-  float acc = 0.f;
-  for (int64_t k = 0; k <= topk; ++k) {
-    const bool routed = k < topk;
-    const int64_t I = routed ? p.I : p.shared_I;
-    if (I == 0) continue;
-    const int64_t e = routed ? static_cast<const int32_t*>(g.ids)[t * topk + k] : 0;
-    const int64_t E = routed ? g.rule.E : 1, KB = (I + kt - 1) / kt;
-    const uint8_t* base = (routed ? p.prepared : p.shared) + E * ((I + 63) / 64) * KBh * tb;
-    const float* sw = routed ? p.sw + (t * topk + k) * I : p.sw + g.T * topk * p.I + t * I;
-    acc += row_dot(base + (e * NT2 + n / 128) * KB * tb, p.mx, KB, I, (int)(n & 127), lane, nullptr, sw);
+  const int T = (int)g.T, E = g.rule.E, topk = g.rule.topk, G = gridDim.x;
+  const int npad = p.npad, img = layer::image_bytes(kMx, npad);
+  const int tile = layer::tile_bytes(kMx), stage_bytes = layer::stage_bytes(kMx, npad), n_stages = layer::n_stages(kMx, npad);
+  const uint32_t smem_base = ptx::smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < n_stages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 2);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&acce[b]), 4);
+    }
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    *abort_flag = 0;
+    *s_err = 0;
+    ptx::fence_mbar_init();
   }
-  if (lane == 0) {
-    if (p.residual) acc += __bfloat162float(p.residual[t * p.ld_residual + n]);
-    p.out[t * p.ld_out + n] = __float2bfloat16_rn(acc);
+  for (int e = threadIdx.x; e < E; e += layer::kThreads) s_mask[e] = 0;
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), layer::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Ctl ctl{abort_flag, s_err, p.timeout_ns};
+
+  Walk walk;
+  walk.run[kSharedUp] = {(int64_t)p.NT1s * p.KB1, p.KB1, G};
+  // the shared expert's first tiles: requested before the gate is known.  The kernel before (front) started after
+  // everything that wrote the weights had completed, so they may be read before it has.
+  int pre = 0;
+  if (warp == 0) {
+    if (lane == 0 && p.NT1s) {
+      const uint64_t pol = ptx::l2_evict_first_policy();
+      const int64_t lo = walk.run[kSharedUp].lo(blockIdx.x), hi = walk.run[kSharedUp].lo(blockIdx.x + 1);
+      for (int64_t x = lo; x < hi && pre < n_stages - 2; ++x, ++pre) {
+        const uint32_t fb = ptx::smem_u32(&full[pre]);
+        ptx::mbar_arrive_expect_tx(fb, tile);
+        ptx::bulk_g2s(smem_base + pre * stage_bytes, p.shared + x * tile, tile, fb, pol);
+      }
+    }
+    __syncwarp();
+  }
+  ptx::griddep_wait();
+
+  // ---------------------------------------------------------------- top-k
+  // up to one token per selecting warp: every CTA selects all of them; more: CTA t selects token t
+  bool ok0 = true;
+  float* scratch = reinterpret_cast<float*>(smem + (n_stages - 2) * stage_bytes) + (warp - 1) * E;
+  const bool everywhere = T <= layer::kSelectWarps;
+  if (warp > 0) {
+    for (int t = everywhere ? warp - 1 : (int)blockIdx.x + (warp - 1) * G; t < T; t += everywhere ? layer::kSelectWarps : layer::kSelectWarps * G) {
+      int id;
+      float w;
+      const float* l = g.logits + (int64_t)t * E;
+      if (E <= 64) gate_select_warp<2>(g.rule, l, g.select_bias, scratch, lane, id, w);
+      else if (E <= 256) gate_select_warp<8>(g.rule, l, g.select_bias, scratch, lane, id, w);
+      else gate_select_warp<32>(g.rule, l, g.select_bias, scratch, lane, id, w);
+      if (lane < topk) {
+        if (everywhere) {
+          s_ids[t * topk + lane] = (uint16_t)id;
+          s_wt[t * topk + lane] = w;
+        }
+        if (!everywhere || blockIdx.x == 0) {
+          static_cast<int32_t*>(g.ids)[t * topk + lane] = id;
+          g.weights[t * topk + lane] = w;
+        }
+      }
+      if (!everywhere) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) red_release_add(p.select_done, 1);
+      }
+    }
+    ptx::fence_proxy_async_smem();  // the scratch becomes a target of bulk copies
+  }
+  if (!everywhere) {
+    if (threadIdx.x == 32) ok0 = wait_count(p.select_done, T, ctl);
+    __syncthreads();
+    for (int i = threadIdx.x; i < T * topk; i += layer::kThreads) {
+      s_ids[i] = (uint16_t)(__ldcg(static_cast<const int32_t*>(g.ids) + i) & (kMaxExperts - 1));
+      s_wt[i] = __ldcg(g.weights + i);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < T * topk; i += layer::kThreads) {
+    const int e = s_ids[i] < E ? s_ids[i] : 0;
+    atomicOr(&s_mask[e], 1ull << (i / topk));
+  }
+  __syncthreads();
+  // the chosen experts in index order: four experts per thread
+  int A;
+  {
+    const int e0 = threadIdx.x * 4;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += e0 + i < E && s_mask[e0 + i] != 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) s_warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - n, all = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      before += w < warp ? s_warp_sum[w] : 0;
+      all += s_warp_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e0 + i < E && s_mask[e0 + i] != 0) s_act[before++] = (uint16_t)(e0 + i);
+    A = all;
+  }
+  __syncthreads();
+  const int D = A * p.KB2 + p.KB2s;  // tiles of one column tile of the down run
+  walk.run[kUp] = {(int64_t)A * p.NT1 * p.KB1, p.KB1, G};
+  walk.run[kDown] = {(int64_t)p.NT2 * D, D, G};
+  const int n_units = A * p.NT1 + p.NT1s;
+  if (*abort_flag) {
+    // the selection never arrived: the copies requested so far land before shared memory is given back
+    if (warp == 0 && lane == 0)
+      for (int s = 0; s < pre; ++s) {
+        ptx::mbar_arrive(ptx::smem_u32(&full[s]));
+        wait_bar_drain(ptx::smem_u32(&full[s]), 0);
+      }
+    __syncwarp();
+  } else if (warp == 0) {
+    // -------------------------------------------------------------- weights
+    if (lane == 0) {
+      const uint64_t pol = ptx::l2_evict_first_policy();
+      int stage = 0, seen = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      walk.begin(kSharedUp, kDown);
+      while (ok && walk.next(kDown)) {
+        for (int k = walk.k0; k < walk.k1; ++k) {
+          if (seen++ >= pre) {
+            if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+              ok = false;
+              break;
+            }
+            const uint8_t* src;
+            if (walk.cur == kSharedUp) {
+              src = p.shared + ((int64_t)walk.unit * p.KB1 + k) * tile;
+            } else if (walk.cur == kUp) {
+              const int a = walk.unit / p.NT1, j = walk.unit - a * p.NT1;
+              src = p.prepared + (((int64_t)s_act[a] * p.NT1 + j) * p.KB1 + k) * tile;
+            } else if (k < A * p.KB2) {
+              const int a = k / p.KB2, kb = k - a * p.KB2;
+              src = p.prepared2 + (((int64_t)s_act[a] * p.NT2 + walk.unit) * p.KB2 + kb) * tile;
+            } else {
+              src = p.shared2 + ((int64_t)walk.unit * p.KB2s + (k - A * p.KB2)) * tile;
+            }
+            const uint32_t fb = ptx::smem_u32(&full[stage]);
+            ptx::mbar_arrive_expect_tx(fb, tile);
+            ptx::bulk_g2s(smem_base + stage * stage_bytes, src, tile, fb, pol);
+          }
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      for (int s = 0; ok && s < n_stages; ++s) {  // no copy is in flight at exit
+        ok = wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok)  // aborted: let what is in flight land
+        for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // -------------------------------------------------------------- the tokens' images
+    if (lane == 0) {
+      const uint64_t pol = ptx::l2_evict_last_policy();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, sw_ready = false;
+      walk.begin(kSharedUp, kDown);
+      while (ok && walk.next(kDown)) {
+        if (walk.cur == kDown && !sw_ready) {  // every unit of the up runs has stored its sw
+          ok = wait_count(p.up_done, n_units, ctl);
+          asm volatile("fence.proxy.async;" ::: "memory");
+          sw_ready = true;
+          if (!ok) break;
+        }
+        for (int k = walk.k0; k < walk.k1; ++k) {
+          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint8_t* src = walk.cur != kDown ? p.ximg + (int64_t)k * img
+                               : k < A * p.KB2   ? p.swimg + (int64_t)k * img
+                                                 : p.swimg_s + (int64_t)(k - A * p.KB2) * img;
+          const uint32_t fb = ptx::smem_u32(&full[stage]);
+          ptx::mbar_arrive_expect_tx(fb, img);
+          ptx::bulk_g2s(smem_base + stage * stage_bytes + tile, src, img, fb, pol);
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      // kind::f16: FP32 accumulator, BF16 operands; kind::mxf8f6f4: E4M3 operands with E8M0 scales
+      const uint32_t idesc = (kMx ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) | ((128u >> 4) << 24) | ((uint32_t)(npad >> 3) << 17);
+      const uint32_t sf0 = tmem_base + 2 * npad;
+      int stage = 0, acc_i = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      walk.begin(kSharedUp, kDown);
+      while (ok && walk.next(kDown)) {
+        const int buf = acc_i & 1;
+        if (!wait_bar(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + buf * npad;
+        for (int k = walk.k0; k < walk.k1; ++k) {
+          if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sb = smem_base + stage * stage_bytes;
+          const uint64_t da = ptx::smem_desc(sb, 16, 1024, ptx::kSwizzle128B);
+          const uint64_t db = ptx::smem_desc(sb + layer::rows_off(kMx), 16, 1024, ptx::kSwizzle128B);
+          if constexpr (!kMx) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > walk.k0 || q > 0) ? 1u : 0u);
+          } else {
+            const uint64_t ds = ptx::smem_desc(sb + kWTileBytes, 0, 128, ptx::kSwizzleNone);
+            const uint32_t sfa = sf0 + 12 * stage;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) ptx::tc_cp_sf(sfa + 4 * q, ds + q * (kSfChunk >> 4));  // weights, hi, lo
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t id = idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29);
+              ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, id, sfa, sfa + 4, (k > walk.k0 || q > 0) ? 1u : 0u);
+              ptx::tc_mma_mxf8(d, da + 2 * q, db + (uint32_t)(npad * 128 >> 4) + 2 * q, id, sfa, sfa + 8, 1u);
+            }
+          }
+          ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        ptx::tc_commit(ptx::smem_u32(&accf[buf]));
+        ++acc_i;
+      }
+      ptx::tc_commit(ptx::smem_u32(drain));
+      wait_bar_drain(ptx::smem_u32(drain), 0);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3, ep = threadIdx.x - 64;
+    const int row = q * 32 + lane;  // this thread's TMEM lane: row of the weight tile
+    const int64_t slot_floats = (int64_t)T * 128;
+    int acc_i = 0;
+    int cut_j[2], n_cut = 0;  // column tiles of the down run that this CTA has a piece of
+    bool ok = true;
+    walk.begin(kSharedUp, kDown);
+    while (walk.next(kDown)) {
+      const int seg = walk.cur, buf = acc_i & 1;
+      const bool down = seg == kDown;
+      const Run& run = walk.run[seg];
+      const int a = seg == kUp ? walk.unit / p.NT1 : 0, j = seg == kUp ? walk.unit - a * p.NT1 : walk.unit;
+      const int e = seg == kUp ? s_act[a] : 0;
+      const unsigned long long every = T == 64 ? ~0ull : (1ull << T) - 1;
+      const unsigned long long mask = seg == kUp ? s_mask[e] : every;
+      const bool whole = walk.k1 - walk.k0 == run.K;
+      if (!down && ep < T) {  // the router's weight of each token for this expert
+        float w = seg == kSharedUp ? 1.f : 0.f;
+        if (seg == kUp)
+          for (int k = 0; k < topk; ++k) w = s_ids[ep * topk + k] == e ? s_wt[ep * topk + k] : w;
+        s_tokw[ep] = w;
+      }
+      ok = warp_wait_bar(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
+      if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * npad;
+      bool finish = whole;
+      if (!whole) {
+        float* slot = down ? p.slots_down + ((int64_t)blockIdx.x * 2 + run.slot(walk.unit, blockIdx.x)) * slot_floats
+                           : p.slots_up + ((int64_t)blockIdx.x * 4 + seg * 2 + run.slot(walk.unit, blockIdx.x)) * slot_floats;
+        for (int c0 = 0; c0 < T; c0 += 16) {
+          if (((mask >> c0) & 0xffff) == 0) continue;
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c0, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int jj = 0; jj < 16; ++jj)
+            if ((mask >> (c0 + jj)) & 1) __stcg(slot + (c0 + jj) * 128 + row, __uint_as_float(v[jj]));
+        }
+        __threadfence();
+        ptx::bar_sync(1, 128);
+        if (down) {
+          if (ep == 0) red_release_add(p.down_cnt + walk.unit, 1);
+          cut_j[n_cut++ & 1] = walk.unit;
+        } else {
+          const int n = run.pieces(walk.unit);
+          if (ep == 0) {
+            const uint32_t before = atomicAdd(p.up_cnt + (seg == kUp ? p.NT1s : 0) + walk.unit, 1u);
+            *s_last = before == (uint32_t)(n - 1);
+            __threadfence();
+          }
+          ptx::bar_sync(1, 128);
+          finish = *s_last != 0;
+        }
+      }
+      if (finish && down) {  // a column tile of this CTA alone
+        for (int c0 = 0; c0 < T; c0 += 16) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c0, v);
+          ptx::tmem_wait_ld();
+          const int64_t n = (int64_t)j * 128 + row;
+#pragma unroll
+          for (int jj = 0; jj < 16; ++jj) {
+            const int t = c0 + jj;
+            if (t < T && n < g.H) {
+              float o = __uint_as_float(v[jj]);
+              if (p.residual) o += __bfloat162float(p.residual[t * p.ld_residual + n]);
+              p.out[t * p.ld_out + n] = __float2bfloat16_rn(o);
+            }
+          }
+        }
+      } else if (finish) {
+        // SwiGLU: rows 0..63 of the tile hold gate columns, 64..127 the up columns of the same indices
+        uint8_t* dst = seg == kUp ? p.swimg + (int64_t)a * p.KB2 * img : p.swimg_s;
+        dst += (int64_t)(kMx ? j >> 1 : j) * img;
+        const bool pad_half = kMx && (j & 1) == 0 && j + 1 == (seg == kUp ? p.NT1 : p.NT1s);
+        const int n = whole ? 0 : run.pieces(walk.unit);
+        for (int c0 = 0; c0 < T; c0 += 16) {
+          const uint32_t m16 = (uint32_t)(mask >> c0) & 0xffffu;
+          float v[16];
+          if (m16) {  // uniform over the four warps
+            if (whole) {
+              uint32_t r[16];
+              ptx::tmem_ld_32x32b_x16(taddr + c0, r);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int jj = 0; jj < 16; ++jj) v[jj] = __uint_as_float(r[jj]);
+            } else {
+#pragma unroll
+              for (int jj = 0; jj < 16; ++jj) v[jj] = 0.f;
+              for (int i = 0; i < n; ++i) {
+                const int b = run.cta(walk.unit, i);
+                const float* slot = p.slots_up + ((int64_t)b * 4 + seg * 2 + run.slot(walk.unit, b)) * slot_floats + row;
+#pragma unroll
+                for (int jj = 0; jj < 16; ++jj)
+                  if ((m16 >> jj) & 1) v[jj] += __ldcg(slot + (c0 + jj) * 128);
+              }
+            }
+            if (q >= 2) {
+#pragma unroll
+              for (int jj = 0; jj < 16; ++jj) xchg[((q - 2) * 16 + jj) * 32 + lane] = v[jj];
+            }
+            ptx::bar_sync(1, 128);
+          }
+          if (q < 2) {
+#pragma unroll
+            for (int jj = 0; jj < 16; ++jj) {
+              const int t = c0 + jj;
+              if (t < T) {
+                float sw = 0.f;
+                if ((m16 >> jj) & 1) sw = silu(v[jj]) * xchg[(q * 16 + jj) * 32 + lane] * s_tokw[t];
+                if constexpr (!kMx) {
+                  *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, row >> 3) + (row & 7) * 2) = __float2bfloat16_rn(sw);
+                } else {
+                  const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
+                  uint32_t hi, lo;
+                  split_e4m3(sw, b, hi, lo);
+                  const int col = (j & 1) * 64 + row;
+                  uint8_t* at = dst + 1536 + image_chunk(t, col >> 4) + (col & 15);
+                  at[0] = (uint8_t)hi;
+                  at[npad * 128] = (uint8_t)lo;
+                  if (lane == 0) {
+                    dst[scale_at(t, col >> 5)] = (uint8_t)b.byte_hi;
+                    dst[512 + scale_at(t, col >> 5)] = (uint8_t)b.byte_lo;
+                  }
+                  if (pad_half) {  // the tile's second half lies past the intermediate size
+                    uint8_t* z = dst + 1536 + image_chunk(t, (col + 64) >> 4) + (col & 15);
+                    z[0] = 0;
+                    z[npad * 128] = 0;
+                    if (lane == 0) dst[scale_at(t, (col + 64) >> 5)] = dst[512 + scale_at(t, (col + 64) >> 5)] = 127;
+                  }
+                }
+              }
+            }
+          }
+          if (m16) ptx::bar_sync(1, 128);  // xchg is written again
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");  // sw is read by bulk copies
+        __threadfence();
+        ptx::bar_sync(1, 128);
+        if (ep == 0) red_release_add(p.up_done, 1);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
+      ++acc_i;
+      ok = true;
+    }
+    // the cut column tiles: this CTA's share of each, once all its pieces are there
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 7) == 0 &&
+                     ((p.ld_out | p.ld_residual) & 3) == 0;
+    if (ok && !*abort_flag) {
+      const Run& run = walk.run[kDown];
+      for (int c = 0; c < n_cut; ++c) {
+        const int j = cut_j[c & 1], n = run.pieces(j);
+        if (ep == 0) ok = wait_count(p.down_cnt + j, n, ctl);
+        if (!ptx::bar_all(1, 128, ok)) break;
+        int mine = 0;
+        while (run.cta(j, mine) != (int)blockIdx.x) ++mine;
+        const int total = T * 32, lo = total * mine / n, hi = total * (mine + 1) / n;
+        for (int i = lo + ep; i < hi; i += 128) {
+          const int t = i >> 5, r4 = (i & 31) * 4;
+          const int64_t col = (int64_t)j * 128 + r4;
+          if (col >= g.H) continue;
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) {
+            const int b = run.cta(j, k);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                p.slots_down + ((int64_t)b * 2 + run.slot(j, b)) * slot_floats + t * 128 + r4));
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+          }
+          __nv_bfloat16* o = p.out + t * p.ld_out + col;
+          const __nv_bfloat16* res = p.residual ? p.residual + t * p.ld_residual + col : nullptr;
+          if (vec) {
+            if (res) {
+              const uint2 r = *reinterpret_cast<const uint2*>(res);
+              s.x += __uint_as_float(r.x << 16);
+              s.y += __uint_as_float(r.x & 0xffff0000u);
+              s.z += __uint_as_float(r.y << 16);
+              s.w += __uint_as_float(r.y & 0xffff0000u);
+            }
+            const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+            *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          } else {
+            const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = __float2bfloat16_rn(res ? f[k] + __bfloat162float(res[k]) : f[k]);
+          }
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, layer::kTmemCols);
+  }
+  if (threadIdx.x == 0) {
+    p.hdr[1 + blockIdx.x] = *s_err;
+    if (blockIdx.x == 0) p.hdr[0] = gridDim.x;
   }
 }
 
-cudaError_t launch_layer(const LayerParams& p, cudaStream_t s) {
-  const GateParams& g = p.gate;
-  if (g.T == 0) return cudaSuccess;
-  if (cudaError_t e = launch_gate(g, s)) return e;
-  const int64_t up = g.T * (g.rule.topk * p.I + p.shared_I);
-  layer_up_kernel<<<(unsigned)((up + 7) / 8), 256, 0, s>>>(p);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  layer_down_kernel<<<(unsigned)((g.T * g.H + 7) / 8), 256, 0, s>>>(p);
-  return cudaGetLastError();
+template <bool kMx>
+static cudaError_t launch_layer_of(const LayerParams& p, int sms, cudaStream_t s) {
+  static int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(layer_kernel<kMx>, cudaFuncAttributeMaxDynamicSharedMemorySize, layer::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;  // CTAs wait for one another: all must be resident
+  attr[1].val.cooperative = 1;
+  lc.attrs = attr;
+  lc.stream = s;
+  lc.gridDim = dim3((unsigned)sms);
+  lc.blockDim = dim3(256);
+  lc.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&lc, layer_front_kernel<kMx>, p);
+  if (e != cudaSuccess) return e;
+  lc.gridDim = dim3((unsigned)(sms < kLayerMaxCtas ? sms : kLayerMaxCtas));
+  lc.blockDim = dim3(layer::kThreads);
+  lc.dynamicSmemBytes = layer::kSmemBytes;
+  lc.numAttrs = 2;
+  return cudaLaunchKernelEx(&lc, layer_kernel<kMx>, p);
 }
+
+cudaError_t launch_layer(const LayerParams& p, int sms, cudaStream_t s) {
+  return p.mx ? launch_layer_of<true>(p, sms, s) : launch_layer_of<false>(p, sms, s);
+}
+
+int64_t layer_image_bytes(bool mx, int64_t npad) { return layer::image_bytes(mx, (int)npad); }
 
 }  // namespace gmmfr

@@ -45,17 +45,26 @@ struct FfnPrepMxParams {
 };
 cudaError_t launch_ffn_prep_mx(const FfnPrepMxParams& p, cudaStream_t s);
 
+constexpr int kLayerMaxCtas = 160;  // the workspace has slots for so many
 struct LayerParams {
   GateParams gate;  // its ids are int32; ids, weights and logits may lie in the workspace
   const __nv_bfloat16* residual;
   __nv_bfloat16* out;
-  const uint8_t* prepared;
-  const uint8_t* shared;
-  float* sw;  // workspace [T][topk][I], then [T][shared_I]
-  int64_t I, shared_I, ld_residual, ld_out;
+  const uint8_t *prepared, *prepared2;  // routed experts: gate/up tiles, down tiles
+  const uint8_t *shared, *shared2;      // the shared expert's
+  uint32_t* hdr;                        // error words
+  uint8_t *ximg, *swimg, *swimg_s;      // B operand images: tokens, SwiGLU values (routed, shared)
+  float *slots_up, *slots_down;         // pieces of cut tiles: [CTA][4][T][128], [CTA][2][T][128]
+  // counters, zeroed by the front kernel
+  uint32_t *counters, *select_done, *up_done, *up_cnt, *down_cnt;
+  int64_t ld_residual, ld_out, timeout_ns;
+  int32_t n_counters, npad;
+  int32_t NT1, KB1, NT2, KB2;  // tiles of a routed expert
+  int32_t NT1s, KB2s;          // of the shared expert (0 without one)
   int32_t mx;
 };
-cudaError_t launch_layer(const LayerParams& p, cudaStream_t s);
+cudaError_t launch_layer(const LayerParams& p, int sms, cudaStream_t s);
+int64_t layer_image_bytes(bool mx, int64_t npad);
 
 // Up to this many rows the dense product streams the weights past all of them.
 constexpr int kLinearStreamRows = 128;
