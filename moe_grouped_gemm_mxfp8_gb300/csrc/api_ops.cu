@@ -110,6 +110,13 @@ gmmfr_status validate_layer(const gmmfr_layer_problem* p) {
   if (p->ld_out != 0 && p->ld_out < p->gate.H) return fail(GMMFR_ERR_INVALID_ARG, "ld_out=%lld is below H", (long long)p->ld_out);
   if (p->weight_type != GMMFR_DT_BF16 && p->weight_type != GMMFR_DT_E4M3)
     return fail(GMMFR_ERR_INVALID_ARG, "weight_type=%d is not BF16 (%d) or E4M3 (%d)", p->weight_type, GMMFR_DT_BF16, GMMFR_DT_E4M3);
+  // the kernel counts the tiles of a run, times its CTAs, in 32 bits
+  const int64_t kt = p->weight_type == GMMFR_DT_BF16 ? 64 : 128, H = p->gate.H, E = p->gate.E;
+  const int64_t up = (E * cdiv(p->I, 64) + cdiv(p->shared_I, 64)) * cdiv(H, kt);
+  const int64_t down = (E * cdiv(p->I, kt) + cdiv(p->shared_I, kt)) * cdiv(H, 128);
+  if (std::max(up, down) >= (int64_t(1) << 32) / gmmfr::kLayerMaxCtas)
+    return fail(GMMFR_ERR_UNSUPPORTED, "the layer's weights have %lld tiles, above 2^32 / %d", (long long)std::max(up, down),
+                gmmfr::kLayerMaxCtas);
   return GMMFR_OK;
 }
 
@@ -144,7 +151,7 @@ LayerLayout layer_layout(const gmmfr_layer_problem* p) {
   L.ximg = take(img * L.KB1);
   L.swimg = take(img * experts * L.KB2);
   L.swimg_s = take(img * L.KB2s);
-  L.slots_up = take(sizeof(float) * 128 * T * 4 * gmmfr::kLayerMaxCtas);
+  L.slots_up = take(sizeof(float) * 128 * T * 2 * gmmfr::kLayerMaxCtas);
   L.slots_down = take(sizeof(float) * 128 * T * 2 * gmmfr::kLayerMaxCtas);
   L.total = off;
   return L;

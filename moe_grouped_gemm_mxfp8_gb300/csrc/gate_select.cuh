@@ -14,20 +14,25 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_value(uint32_t k) {  // of a key above 1
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
 // One warp selects token `logits[0..E)`'s experts; lane k < topk returns the k-th expert and its
 // weight.  Expert e sits in lane e % 32, register e / 32 (kPer registers: E <= 32 * kPer).
-// `scratch`: E floats of shared memory of this warp, used when there are groups.
-// All sums are FP32; the exponential's argument is at most 0 and its sum at least 1.
+// All sums are FP32; the exponential's argument is at most 0 and its sum at least 1.  Maxima and minima over the
+// warp are single redux instructions on order-preserving integers.
 template <int kPer>
 __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float* logits, const float* select_bias,
-                                                 float* scratch, int lane, int& id_out, float& w_out) {
+                                                 int lane, int& id_out, float& w_out) {
   constexpr uint32_t kAll = 0xffffffffu;
   const float kNegInf = __int_as_float(0xff800000);
-  float p[kPer];
+  float p[kPer], bias[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
     p[i] = e < r.E ? logits[e] : kNegInf;
+    bias[i] = select_bias != nullptr && e < r.E ? __ldg(select_bias + e) : 0.f;
   }
   if (r.sigmoid) {
 #pragma unroll
@@ -52,52 +57,41 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
   }
   uint32_t key[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    float s = p[i];
-    if (select_bias != nullptr && e < r.E) s += select_bias[e];
-    key[i] = e < r.E ? order_key(s) : 0u;
-    if (r.n_group > 1 && e < r.E) scratch[e] = s;
-  }
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < r.E ? order_key(p[i] + bias[i]) : 0u;
   if (r.n_group > 1) {
-    __syncwarp();
     const int per = r.E / r.n_group;
-    uint32_t gkey[2] = {0u, 0u};  // groups lane and lane + 32
+    uint32_t gkey[2] = {0u, 0u};  // of groups lane and lane + 32
+    for (int g = 0; g < r.n_group; ++g) {
+      const int first = g * per;
+      uint32_t a = 0, b = 0;  // the lane's two highest keys of the group
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int g = lane + 32 * h;
-      if (g < r.n_group) {
-        float a = kNegInf, b = kNegInf;  // the two highest scores of the group
-        for (int i = 0; i < per; ++i) {
-          // each lane starts at another place of its group: consecutive lanes read other banks
-          const int k = (i + lane) % per;
-          const float v = scratch[g * per + k];
-          if (v > a) {
-            b = a;
-            a = v;
-          } else if (v > b) {
-            b = v;
-          }
-        }
-        gkey[h] = order_key(r.group_top == 2 ? a + b : a);
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t k = (unsigned)(lane + 32 * i - first) < (unsigned)per ? key[i] : 0u;
+        b = max(b, min(a, k));
+        a = max(a, k);
       }
-    }
-    uint64_t ok = 0;  // eligible groups: fewer than topk_group groups are better, or equal and earlier
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      int rank = 0;
-      for (int g = 0; g < r.n_group; ++g) {
-        const uint32_t lo = __shfl_sync(kAll, gkey[0], g & 31), hi = __shfl_sync(kAll, gkey[1], g & 31);
-        const uint32_t o = g < 32 ? lo : hi;
-        rank += (o > gkey[h] || (o == gkey[h] && g < lane + 32 * h)) ? 1 : 0;
+      const uint32_t top = __reduce_max_sync(kAll, a);
+      float s = top > 1u ? key_value(top) : kNegInf;
+      if (r.group_top == 2) {  // one lane that has the highest gives it up
+        const bool holder = lane == __ffs(__ballot_sync(kAll, a == top)) - 1;
+        const uint32_t second = __reduce_max_sync(kAll, holder ? b : a);
+        s += second > 1u ? key_value(second) : kNegInf;
       }
-      const uint32_t m = __ballot_sync(kAll, lane + 32 * h < r.n_group && rank < r.topk_group);
-      ok |= (uint64_t)m << (32 * h);
+      if (lane == (g & 31)) gkey[g >> 5] = order_key(s);
     }
+    // eligible groups: fewer than topk_group groups are better, or equal and earlier
+    int rank[2] = {0, 0};
+    for (int g = 0; g < r.n_group; ++g) {
+      const uint32_t o = __shfl_sync(kAll, g < 32 ? gkey[0] : gkey[1], g & 31);
+      rank[0] += (o > gkey[0] || (o == gkey[0] && g < lane)) ? 1 : 0;
+      rank[1] += (o > gkey[1] || (o == gkey[1] && g < lane + 32)) ? 1 : 0;
+    }
+    const uint32_t ok0 = __ballot_sync(kAll, lane < r.n_group && rank[0] < r.topk_group);
+    const uint32_t ok1 = __ballot_sync(kAll, lane + 32 < r.n_group && rank[1] < r.topk_group);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      if (e < r.E && !((ok >> (e / per)) & 1)) key[i] = 0u;
+      const int g = (lane + 32 * i) / per;
+      if (!(((g < 32 ? ok0 : ok1) >> (g & 31)) & 1u)) key[i] = 0u;
     }
   }
   id_out = 0;

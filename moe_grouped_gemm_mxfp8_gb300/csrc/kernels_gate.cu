@@ -49,13 +49,12 @@ __global__ void __launch_bounds__(256) gate_logits_kernel(GateParams p) {
 
 template <int kPer>
 __global__ void __launch_bounds__(128) gate_select_kernel(GateParams p) {
-  __shared__ float scratch[4][kPer * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * 4 + warp;
   if (t >= p.T) return;
   int id;
   float w;
-  gate_select_warp<kPer>(p.rule, p.logits + t * p.rule.E, p.select_bias, scratch[warp], lane, id, w);
+  gate_select_warp<kPer>(p.rule, p.logits + t * p.rule.E, p.select_bias, lane, id, w);
   if (lane < p.rule.topk) {
     const int64_t o = t * p.rule.topk + lane;
     if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = id;

@@ -1,9 +1,8 @@
 // A whole mixture-of-experts layer for a few tokens (at most 64), in two kernels.
 //
 //   front   the gate's logits; the tokens as images of the products' B operand; counters to zero
-//   layer   one persistent CTA per SM: top-k of every token, then three runs of weight tiles
-//             shared up   x times the shared expert's gate/up tiles
-//             up          x times the chosen experts' gate/up tiles  (experts in index order)
+//   layer   one persistent CTA per SM: top-k of every token, then two runs of weight tiles
+//             up          x times the gate/up tiles of the shared expert and of the chosen ones
 //             down        column tile by column tile: sw times the down tiles of every chosen expert and of
 //                         the shared one, one long sum over (expert, intermediate index)
 //           each run cut into equal contiguous ranges over the CTAs.
@@ -13,8 +12,8 @@
 // that did not choose the expert costs only tensor-core slots that would idle.  Its row of sw is zero, which lets
 // the down run add all experts of a column tile into the same accumulator, the router's weight being folded into
 // sw (in FP32, before its rounding).
-// The weights' producer never waits for a token: the first tiles (shared expert) are requested before the gate is
-// known, the down tiles while other CTAs still finish the up run.
+// The weights' producer never waits for a token: the first down tiles are requested while other CTAs still finish
+// the up run.
 //
 // A column tile cut between CTAs is joined through the workspace: each piece stores its FP32 sums, and
 //   up     the CTA that arrives last adds the pieces in CTA order, applies SwiGLU and stores sw;
@@ -105,7 +104,6 @@ __host__ __device__ constexpr int n_stages(bool mx, int npad) {
 }
 static_assert(stage_bytes(true, 16) % 1024 == 0 && stage_bytes(false, 16) % 1024 == 0 && rows_off(true) % 1024 == 0,
               "swizzled operands need 1024-byte alignment");
-static_assert(kSelectWarps * kMaxExperts * 4 <= 2 * 18432, "the selection's scratch fits the last two stages");
 constexpr int kBarOff = kArena;
 constexpr int kNumBars = 2 * kMaxStages + 5;
 constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;             // int32 misc[16]
@@ -180,54 +178,54 @@ __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n, const 
 }
 
 // One run of U tiles in units of K tiles, cut evenly over G CTAs: CTA b has [U b / G, U (b + 1) / G).
+// (The host refuses sizes whose U * G passes 32 bits.)
 struct Run {
-  int64_t U;
-  int K, G;
-  __device__ int64_t lo(int b) const { return U * b / G; }
-  __device__ int owner(int64_t x) const { return (int)(((x + 1) * G - 1) / U); }
-  // pieces of unit u, and the CTA of piece i (with fewer tiles than CTAs every tile is a piece)
-  __device__ int pieces(int64_t u) const { return U < G ? K : owner((u + 1) * K - 1) - owner(u * K) + 1; }
-  __device__ int cta(int64_t u, int i) const { return U < G ? owner(u * K + i) : owner(u * K) + i; }
-  // a CTA's pieces of cut units lie in two slots: 0 where its range begins in the unit, 1 where it ends there
-  __device__ int slot(int64_t u, int b) const { return lo(b) >= u * K ? 0 : 1; }
+  uint32_t U, K, G;
+  __device__ uint32_t lo(uint32_t b) const { return U * b / G; }
+  __device__ uint32_t owner(uint32_t x) const { return ((x + 1) * G - 1) / U; }
+};
+// The pieces of unit u: with at least as many tiles as CTAs those of n consecutive CTAs from b0, otherwise its
+// tiles, each some CTA's.  A CTA's pieces of cut units lie in its slots: 0 where its range begins in the unit, 1
+// where it ends there; so only the first piece of a unit can lie in slot 1.
+struct Pieces {
+  uint32_t b0, n, first_slot;
+  const Run* run;
+  uint32_t x0;
+  __device__ Pieces(const Run& r, uint32_t u) : run(&r), x0(u * r.K) {
+    b0 = r.owner(x0);
+    n = r.U < r.G ? r.K : r.owner(x0 + r.K - 1) - b0 + 1;
+    first_slot = r.lo(b0) >= x0 ? 0 : 1;
+  }
+  __device__ uint32_t cta(uint32_t i) const { return run->U < run->G ? run->owner(x0 + i) : b0 + i; }
+  // piece i's slot among the CTAs' pairs of slots
+  __device__ uint32_t slot(uint32_t i) const { return cta(i) * 2 + (i == 0 ? first_slot : 0); }
 };
 
-enum { kSharedUp = 0, kUp = 1, kDown = 2 };
-
-// The pieces of one CTA: units (or parts of units) of the three runs in order; every role walks them.
+// The pieces of one CTA: units (or parts of units) of the two runs in order; every role walks them.
 struct Walk {
-  Run run[3];
-  int seg;
-  int64_t pos, end;
-  int unit, k0, k1;
-  __device__ void begin(int first_seg, int last_seg) {
-    seg = first_seg;
-    set(last_seg);
+  const Run *up, *down;
+  uint32_t pos, end, end2;
+  uint32_t unit, k0, k1;
+  bool is_down;  // of the current piece
+  __device__ Walk(const Run& up_, const Run& down_) : up(&up_), down(&down_), is_down(false) {
+    pos = up->lo(blockIdx.x);
+    end = up->lo(blockIdx.x + 1);
   }
-  __device__ void set(int last_seg) {
-    for (; seg <= last_seg; ++seg) {
-      pos = run[seg].U ? run[seg].lo(blockIdx.x) : 0;
-      end = run[seg].U ? run[seg].lo(blockIdx.x + 1) : 0;
-      if (pos < end) return;
-    }
-  }
-  // the next piece of segments up to last_seg: tiles [k0, k1) of `unit` of `seg`
-  __device__ bool next(int last_seg) {
-    if (seg > last_seg) return false;
-    const Run& r = run[seg];
-    unit = (int)(pos / r.K);
-    k0 = (int)(pos - (int64_t)unit * r.K);
-    const int64_t left = end - pos;
-    k1 = (int64_t)(r.K - k0) < left ? r.K : k0 + (int)left;
-    cur = seg;
-    pos += k1 - k0;
+  __device__ bool next() {
     if (pos == end) {
-      ++seg;
-      set(last_seg);
+      if (is_down) return false;
+      is_down = true;
+      pos = down->lo(blockIdx.x);
+      end = down->lo(blockIdx.x + 1);
+      if (pos == end) return false;
     }
+    const uint32_t K = is_down ? down->K : up->K;
+    unit = pos / K;
+    k0 = pos - unit * K;
+    k1 = min(K, k0 + (end - pos));
+    pos += k1 - k0;
     return true;
   }
-  int cur;  // segment of the current piece
 };
 
 }  // namespace
@@ -375,38 +373,20 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   const uint32_t tmem_base = *tmem_slot;
   const Ctl ctl{abort_flag, s_err, p.timeout_ns};
 
-  Walk walk;
-  walk.run[kSharedUp] = {(int64_t)p.NT1s * p.KB1, p.KB1, G};
-  // the shared expert's first tiles: requested before the gate is known.  The kernel before (front) started after
-  // everything that wrote the weights had completed, so they may be read before it has.
-  int pre = 0;
-  if (warp == 0) {
-    if (lane == 0 && p.NT1s) {
-      const uint64_t pol = ptx::l2_evict_first_policy();
-      const int64_t lo = walk.run[kSharedUp].lo(blockIdx.x), hi = walk.run[kSharedUp].lo(blockIdx.x + 1);
-      for (int64_t x = lo; x < hi && pre < n_stages - 2; ++x, ++pre) {
-        const uint32_t fb = ptx::smem_u32(&full[pre]);
-        ptx::mbar_arrive_expect_tx(fb, tile);
-        ptx::bulk_g2s(smem_base + pre * stage_bytes, p.shared + x * tile, tile, fb, pol);
-      }
-    }
-    __syncwarp();
-  }
   ptx::griddep_wait();
 
   // ---------------------------------------------------------------- top-k
   // up to one token per selecting warp: every CTA selects all of them; more: CTA t selects token t
   bool ok0 = true;
-  float* scratch = reinterpret_cast<float*>(smem + (n_stages - 2) * stage_bytes) + (warp - 1) * E;
   const bool everywhere = T <= layer::kSelectWarps;
   if (warp > 0) {
     for (int t = everywhere ? warp - 1 : (int)blockIdx.x + (warp - 1) * G; t < T; t += everywhere ? layer::kSelectWarps : layer::kSelectWarps * G) {
       int id;
       float w;
       const float* l = g.logits + (int64_t)t * E;
-      if (E <= 64) gate_select_warp<2>(g.rule, l, g.select_bias, scratch, lane, id, w);
-      else if (E <= 256) gate_select_warp<8>(g.rule, l, g.select_bias, scratch, lane, id, w);
-      else gate_select_warp<32>(g.rule, l, g.select_bias, scratch, lane, id, w);
+      if (E <= 64) gate_select_warp<2>(g.rule, l, g.select_bias, lane, id, w);
+      else if (E <= 256) gate_select_warp<8>(g.rule, l, g.select_bias, lane, id, w);
+      else gate_select_warp<32>(g.rule, l, g.select_bias, lane, id, w);
       if (lane < topk) {
         if (everywhere) {
           s_ids[t * topk + lane] = (uint16_t)id;
@@ -423,7 +403,6 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         if (lane == 0) red_release_add(p.select_done, 1);
       }
     }
-    ptx::fence_proxy_async_smem();  // the scratch becomes a target of bulk copies
   }
   if (!everywhere) {
     if (threadIdx.x == 32) ok0 = wait_count(p.select_done, T, ctl);
@@ -467,48 +446,51 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   }
   __syncthreads();
   const int D = A * p.KB2 + p.KB2s;  // tiles of one column tile of the down run
-  walk.run[kUp] = {(int64_t)A * p.NT1 * p.KB1, p.KB1, G};
-  walk.run[kDown] = {(int64_t)p.NT2 * D, D, G};
-  const int n_units = A * p.NT1 + p.NT1s;
+  const int n_units = A * p.NT1 + p.NT1s;  // the shared expert's first
+  const Run up{(uint32_t)n_units * p.KB1, (uint32_t)p.KB1, (uint32_t)G}, down{(uint32_t)p.NT2 * D, (uint32_t)D, (uint32_t)G};
+  Walk walk(up, down);
   if (*abort_flag) {
-    // the selection never arrived: the copies requested so far land before shared memory is given back
-    if (warp == 0 && lane == 0)
-      for (int s = 0; s < pre; ++s) {
-        ptx::mbar_arrive(ptx::smem_u32(&full[s]));
-        wait_bar_drain(ptx::smem_u32(&full[s]), 0);
-      }
-    __syncwarp();
+    // the selection never arrived: nothing has been requested
   } else if (warp == 0) {
     // -------------------------------------------------------------- weights
     if (lane == 0) {
       const uint64_t pol = ptx::l2_evict_first_policy();
-      int stage = 0, seen = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      walk.begin(kSharedUp, kDown);
-      while (ok && walk.next(kDown)) {
-        for (int k = walk.k0; k < walk.k1; ++k) {
-          if (seen++ >= pre) {
-            if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
-              ok = false;
-              break;
-            }
-            const uint8_t* src;
-            if (walk.cur == kSharedUp) {
-              src = p.shared + ((int64_t)walk.unit * p.KB1 + k) * tile;
-            } else if (walk.cur == kUp) {
-              const int a = walk.unit / p.NT1, j = walk.unit - a * p.NT1;
-              src = p.prepared + (((int64_t)s_act[a] * p.NT1 + j) * p.KB1 + k) * tile;
+      while (ok && walk.next()) {
+        // the piece's tiles lie in runs of consecutive ones: `src` walks a run of `left` tiles
+        const uint8_t* src = nullptr;
+        int left = 0;
+        for (int k = walk.k0; k < (int)walk.k1; ++k) {
+          if (left == 0) {
+            if (!walk.is_down) {
+              const int u = (int)walk.unit - p.NT1s;
+              if (u < 0) {
+                src = p.shared + ((int64_t)walk.unit * p.KB1 + k) * tile;
+              } else {
+                const int a = u / p.NT1;
+                src = p.prepared + (((int64_t)s_act[a] * p.NT1 + (u - a * p.NT1)) * p.KB1 + k) * tile;
+              }
+              left = p.KB1 - k;
             } else if (k < A * p.KB2) {
               const int a = k / p.KB2, kb = k - a * p.KB2;
               src = p.prepared2 + (((int64_t)s_act[a] * p.NT2 + walk.unit) * p.KB2 + kb) * tile;
+              left = p.KB2 - kb;
             } else {
               src = p.shared2 + ((int64_t)walk.unit * p.KB2s + (k - A * p.KB2)) * tile;
+              left = D - k;
             }
-            const uint32_t fb = ptx::smem_u32(&full[stage]);
-            ptx::mbar_arrive_expect_tx(fb, tile);
-            ptx::bulk_g2s(smem_base + stage * stage_bytes, src, tile, fb, pol);
           }
+          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = ptx::smem_u32(&full[stage]);
+          ptx::mbar_arrive_expect_tx(fb, tile);
+          ptx::bulk_g2s(smem_base + stage * stage_bytes, src, tile, fb, pol);
+          src += tile;
+          --left;
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
@@ -533,22 +515,21 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, sw_ready = false;
-      walk.begin(kSharedUp, kDown);
-      while (ok && walk.next(kDown)) {
-        if (walk.cur == kDown && !sw_ready) {  // every unit of the up runs has stored its sw
+      while (ok && walk.next()) {
+        if (walk.is_down && !sw_ready) {  // every unit of the up runs has stored its sw
           ok = wait_count(p.up_done, n_units, ctl);
           asm volatile("fence.proxy.async;" ::: "memory");
           sw_ready = true;
           if (!ok) break;
         }
-        for (int k = walk.k0; k < walk.k1; ++k) {
+        for (int k = walk.k0; k < (int)walk.k1; ++k) {
           if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
             ok = false;
             break;
           }
-          const uint8_t* src = walk.cur != kDown ? p.ximg + (int64_t)k * img
-                               : k < A * p.KB2   ? p.swimg + (int64_t)k * img
-                                                 : p.swimg_s + (int64_t)(k - A * p.KB2) * img;
+          const uint8_t* src = !walk.is_down   ? p.ximg + (int64_t)k * img
+                               : k < A * p.KB2 ? p.swimg + (int64_t)k * img
+                                               : p.swimg_s + (int64_t)(k - A * p.KB2) * img;
           const uint32_t fb = ptx::smem_u32(&full[stage]);
           ptx::mbar_arrive_expect_tx(fb, img);
           ptx::bulk_g2s(smem_base + stage * stage_bytes + tile, src, img, fb, pol);
@@ -569,13 +550,12 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
       int stage = 0, acc_i = 0;
       uint32_t phase = 0;
       bool ok = true;
-      walk.begin(kSharedUp, kDown);
-      while (ok && walk.next(kDown)) {
+      while (ok && walk.next()) {
         const int buf = acc_i & 1;
         if (!wait_bar(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * npad;
-        for (int k = walk.k0; k < walk.k1; ++k) {
+        for (int k = walk.k0; k < (int)walk.k1; ++k) {
           if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
             ok = false;
             break;
@@ -586,7 +566,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           const uint64_t db = ptx::smem_desc(sb + layer::rows_off(kMx), 16, 1024, ptx::kSwizzle128B);
           if constexpr (!kMx) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > walk.k0 || q > 0) ? 1u : 0u);
+            for (int q = 0; q < 4; ++q) ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
           } else {
             const uint64_t ds = ptx::smem_desc(sb + kWTileBytes, 0, 128, ptx::kSwizzleNone);
             const uint32_t sfa = sf0 + 12 * stage;
@@ -595,7 +575,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t id = idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29);
-              ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, id, sfa, sfa + 4, (k > walk.k0 || q > 0) ? 1u : 0u);
+              ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, id, sfa, sfa + 4, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
               ptx::tc_mma_mxf8(d, da + 2 * q, db + (uint32_t)(npad * 128 >> 4) + 2 * q, id, sfa, sfa + 8, 1u);
             }
           }
@@ -621,19 +601,19 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     int acc_i = 0;
     int cut_j[2], n_cut = 0;  // column tiles of the down run that this CTA has a piece of
     bool ok = true;
-    walk.begin(kSharedUp, kDown);
-    while (walk.next(kDown)) {
-      const int seg = walk.cur, buf = acc_i & 1;
-      const bool down = seg == kDown;
-      const Run& run = walk.run[seg];
-      const int a = seg == kUp ? walk.unit / p.NT1 : 0, j = seg == kUp ? walk.unit - a * p.NT1 : walk.unit;
-      const int e = seg == kUp ? s_act[a] : 0;
-      const unsigned long long every = T == 64 ? ~0ull : (1ull << T) - 1;
-      const unsigned long long mask = seg == kUp ? s_mask[e] : every;
+    while (walk.next()) {
+      const int buf = acc_i & 1;
+      const bool is_down = walk.is_down;
+      const Run& run = is_down ? down : up;
+      const bool routed = !is_down && (int)walk.unit >= p.NT1s;
+      const int a = routed ? ((int)walk.unit - p.NT1s) / p.NT1 : 0;
+      const int j = routed ? (int)walk.unit - p.NT1s - a * p.NT1 : (int)walk.unit;  // column tile
+      const int e = routed ? s_act[a] : 0;
+      const unsigned long long mask = routed ? s_mask[e] : (T == 64 ? ~0ull : (1ull << T) - 1);
       const bool whole = walk.k1 - walk.k0 == run.K;
-      if (!down && ep < T) {  // the router's weight of each token for this expert
-        float w = seg == kSharedUp ? 1.f : 0.f;
-        if (seg == kUp)
+      if (!is_down && ep < T) {  // the router's weight of each token for this expert
+        float w = routed ? 0.f : 1.f;
+        if (routed)
           for (int k = 0; k < topk; ++k) w = s_ids[ep * topk + k] == e ? s_wt[ep * topk + k] : w;
         s_tokw[ep] = w;
       }
@@ -642,9 +622,11 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * npad;
       bool finish = whole;
+      const Pieces pieces(run, walk.unit);
       if (!whole) {
-        float* slot = down ? p.slots_down + ((int64_t)blockIdx.x * 2 + run.slot(walk.unit, blockIdx.x)) * slot_floats
-                           : p.slots_up + ((int64_t)blockIdx.x * 4 + seg * 2 + run.slot(walk.unit, blockIdx.x)) * slot_floats;
+        // this CTA's range begins in the unit (slot 0) or ends there (slot 1)
+        const uint32_t at = blockIdx.x * 2 + (run.lo(blockIdx.x) >= pieces.x0 ? 0 : 1);
+        float* slot = (is_down ? p.slots_down : p.slots_up) + (int64_t)at * slot_floats;
         for (int c0 = 0; c0 < T; c0 += 16) {
           if (((mask >> c0) & 0xffff) == 0) continue;
           uint32_t v[16];
@@ -656,21 +638,20 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         }
         __threadfence();
         ptx::bar_sync(1, 128);
-        if (down) {
+        if (is_down) {
           if (ep == 0) red_release_add(p.down_cnt + walk.unit, 1);
           cut_j[n_cut++ & 1] = walk.unit;
         } else {
-          const int n = run.pieces(walk.unit);
           if (ep == 0) {
-            const uint32_t before = atomicAdd(p.up_cnt + (seg == kUp ? p.NT1s : 0) + walk.unit, 1u);
-            *s_last = before == (uint32_t)(n - 1);
+            const uint32_t before = atomicAdd(p.up_cnt + walk.unit, 1u);
+            *s_last = before == pieces.n - 1;
             __threadfence();
           }
           ptx::bar_sync(1, 128);
           finish = *s_last != 0;
         }
       }
-      if (finish && down) {  // a column tile of this CTA alone
+      if (finish && is_down) {  // a column tile of this CTA alone
         for (int c0 = 0; c0 < T; c0 += 16) {
           uint32_t v[16];
           ptx::tmem_ld_32x32b_x16(taddr + c0, v);
@@ -688,10 +669,9 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         }
       } else if (finish) {
         // SwiGLU: rows 0..63 of the tile hold gate columns, 64..127 the up columns of the same indices
-        uint8_t* dst = seg == kUp ? p.swimg + (int64_t)a * p.KB2 * img : p.swimg_s;
+        uint8_t* dst = routed ? p.swimg + (int64_t)a * p.KB2 * img : p.swimg_s;
         dst += (int64_t)(kMx ? j >> 1 : j) * img;
-        const bool pad_half = kMx && (j & 1) == 0 && j + 1 == (seg == kUp ? p.NT1 : p.NT1s);
-        const int n = whole ? 0 : run.pieces(walk.unit);
+        const bool pad_half = kMx && (j & 1) == 0 && j + 1 == (routed ? p.NT1 : p.NT1s);
         for (int c0 = 0; c0 < T; c0 += 16) {
           const uint32_t m16 = (uint32_t)(mask >> c0) & 0xffffu;
           float v[16];
@@ -705,9 +685,9 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             } else {
 #pragma unroll
               for (int jj = 0; jj < 16; ++jj) v[jj] = 0.f;
-              for (int i = 0; i < n; ++i) {
-                const int b = run.cta(walk.unit, i);
-                const float* slot = p.slots_up + ((int64_t)b * 4 + seg * 2 + run.slot(walk.unit, b)) * slot_floats + row;
+#pragma unroll 2
+              for (uint32_t i = 0; i < pieces.n; ++i) {
+                const float* slot = p.slots_up + (int64_t)pieces.slot(i) * slot_floats + row;
 #pragma unroll
                 for (int jj = 0; jj < 16; ++jj)
                   if ((m16 >> jj) & 1) v[jj] += __ldcg(slot + (c0 + jj) * 128);
@@ -767,13 +747,13 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 7) == 0 &&
                      ((p.ld_out | p.ld_residual) & 3) == 0;
     if (ok && !*abort_flag) {
-      const Run& run = walk.run[kDown];
       for (int c = 0; c < n_cut; ++c) {
-        const int j = cut_j[c & 1], n = run.pieces(j);
+        const int j = cut_j[c & 1];
+        const Pieces pieces(down, j);
+        const int n = pieces.n;
         if (ep == 0) ok = wait_count(p.down_cnt + j, n, ctl);
         if (!ptx::bar_all(1, 128, ok)) break;
-        int mine = 0;
-        while (run.cta(j, mine) != (int)blockIdx.x) ++mine;
+        const int mine = down.U < down.G ? down.lo(blockIdx.x) - pieces.x0 : blockIdx.x - pieces.b0;
         const int total = T * 32, lo = total * mine / n, hi = total * (mine + 1) / n;
         for (int i = lo + ep; i < hi; i += 128) {
           const int t = i >> 5, r4 = (i & 31) * 4;
@@ -782,9 +762,8 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int k = 0; k < n; ++k) {
-            const int b = run.cta(j, k);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                p.slots_down + ((int64_t)b * 2 + run.slot(j, b)) * slot_floats + t * 128 + r4));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.slots_down + (int64_t)pieces.slot(k) * slot_floats +
+                                                                    t * 128 + r4));
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;

@@ -54,7 +54,7 @@ struct LayerParams {
   const uint8_t *shared, *shared2;      // the shared expert's
   uint32_t* hdr;                        // error words
   uint8_t *ximg, *swimg, *swimg_s;      // B operand images: tokens, SwiGLU values (routed, shared)
-  float *slots_up, *slots_down;         // pieces of cut tiles: [CTA][4][T][128], [CTA][2][T][128]
+  float *slots_up, *slots_down;         // pieces of cut tiles: [CTA][2][T][128] each
   // counters, zeroed by the front kernel
   uint32_t *counters, *select_done, *up_done, *up_cnt, *down_cnt;
   int64_t ld_residual, ld_out, timeout_ns;
