@@ -66,7 +66,9 @@ gmmfr_status validate_gate(const gmmfr_gate_problem* p) {
   return GMMFR_OK;
 }
 
-size_t gate_ws_bytes(const gmmfr_gate_problem* p) { return align256(sizeof(float) * (size_t)p->T * p->E); }
+size_t gate_ws_bytes(const gmmfr_gate_problem* p) {
+  return p->T <= gmmfr::kGateClusterTokens ? 256 : align256(sizeof(float) * (size_t)p->T * p->E);
+}
 
 gmmfr::GateParams gate_params(const gmmfr_gate_problem& p, const void* x, const void* weight, const float* select_bias) {
   gmmfr::GateParams g{};
@@ -122,7 +124,7 @@ gmmfr_status validate_layer(const gmmfr_layer_problem* p) {
 
 struct LayerLayout {
   int64_t npad, NT1, KB1, NT2, KB2, NT1s, KB2s, n_counters;
-  size_t logits, ids, weights, counters, ximg, swimg, swimg_s, slots_up, slots_down, total;
+  size_t ids, weights, counters, ximg, swimg, swimg_s, slots_up, slots_down, total;
 };
 LayerLayout layer_layout(const gmmfr_layer_problem* p) {
   LayerLayout L{};
@@ -136,7 +138,7 @@ LayerLayout layer_layout(const gmmfr_layer_problem* p) {
   L.NT1s = cdiv(p->shared_I, 64);
   L.KB2s = cdiv(p->shared_I, kt);
   const int64_t experts = std::min<int64_t>(p->gate.E, T * k);  // at most so many are chosen
-  L.n_counters = 2 + L.NT1s + experts * L.NT1 + L.NT2;
+  L.n_counters = 1 + L.NT1s + experts * L.NT1 + L.NT2;
   const size_t img = (size_t)gmmfr::layer_image_bytes(mx, L.npad);
   size_t off = gmmfr::kHdrBytes;
   auto take = [&](size_t bytes) {
@@ -144,7 +146,6 @@ LayerLayout layer_layout(const gmmfr_layer_problem* p) {
     off = align256(off + bytes);
     return at;
   };
-  L.logits = take(sizeof(float) * (size_t)T * p->gate.E);
   L.ids = take(sizeof(int32_t) * (size_t)T * k);
   L.weights = take(sizeof(float) * (size_t)T * k);
   L.counters = take(sizeof(uint32_t) * (size_t)L.n_counters);
@@ -233,7 +234,7 @@ gmmfr_status gmmfr_moe_gate(const gmmfr_gate_problem* problem, const void* x, co
     return fail(GMMFR_ERR_INVALID_ARG, "an input or output is not aligned to its element size");
   if (gmmfr_status st = check_workspace(workspace, workspace_bytes, gate_ws_bytes(problem))) return st;
   gmmfr::GateParams g = gate_params(p, x, weight, select_bias);
-  g.logits = logits ? logits : static_cast<float*>(workspace);
+  g.logits = logits || p.T <= gmmfr::kGateClusterTokens ? logits : static_cast<float*>(workspace);
   g.ids = topk_ids;
   g.weights = topk_weights;
   g.ids_i64 = p.ids_type == GMMFR_INDEX_I64;
@@ -313,7 +314,6 @@ gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   gmmfr::LayerParams lp{};
   lp.gate = gate_params(p.gate, x, gate_weight, select_bias);
-  lp.gate.logits = reinterpret_cast<float*>(ws + L.logits);
   lp.gate.ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(ws + L.ids);
   lp.gate.weights = topk_weights ? topk_weights : reinterpret_cast<float*>(ws + L.weights);
   lp.residual = static_cast<const __nv_bfloat16*>(residual);
@@ -333,9 +333,8 @@ gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, 
   lp.slots_up = reinterpret_cast<float*>(ws + L.slots_up);
   lp.slots_down = reinterpret_cast<float*>(ws + L.slots_down);
   lp.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
-  lp.select_done = lp.counters;
-  lp.up_done = lp.counters + 1;
-  lp.down_cnt = lp.counters + 2;
+  lp.up_done = lp.counters;
+  lp.down_cnt = lp.counters + 1;
   lp.up_cnt = lp.down_cnt + L.NT2;
   lp.n_counters = (int32_t)L.n_counters;
   lp.npad = (int32_t)L.npad;

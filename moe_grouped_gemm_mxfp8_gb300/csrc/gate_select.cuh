@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "ops.cuh"
+#include "ptx.cuh"
 
 namespace gmmfr {
 
@@ -27,12 +28,14 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
                                                  int lane, int& id_out, float& w_out) {
   constexpr uint32_t kAll = 0xffffffffu;
   const float kNegInf = __int_as_float(0xff800000);
-  float p[kPer], bias[kPer];
+  // the bias is asked for beside the logits (with many experts per lane it would cost too many registers)
+  constexpr bool kBiasFirst = kPer <= 8;
+  float p[kPer], bias[kBiasFirst ? kPer : 1];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
     p[i] = e < r.E ? logits[e] : kNegInf;
-    bias[i] = select_bias != nullptr && e < r.E ? __ldg(select_bias + e) : 0.f;
+    if constexpr (kBiasFirst) bias[i] = select_bias != nullptr && e < r.E ? __ldg(select_bias + e) : 0.f;
   }
   if (r.sigmoid) {
 #pragma unroll
@@ -57,7 +60,13 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
   }
   uint32_t key[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < r.E ? order_key(p[i] + bias[i]) : 0u;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 32 * i;
+    float b = 0.f;
+    if constexpr (kBiasFirst) b = bias[i];
+    else if (select_bias != nullptr && e < r.E) b = __ldg(select_bias + e);
+    key[i] = e < r.E ? order_key(p[i] + b) : 0u;
+  }
   if (r.n_group > 1) {
     const int per = r.E / r.n_group;
     uint32_t gkey[2] = {0u, 0u};  // of groups lane and lane + 32
@@ -95,36 +104,122 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
     }
   }
   id_out = 0;
-  w_out = 0.f;
-  float total = 0.f;
   for (int k = 0; k < r.topk; ++k) {
-    uint32_t best = 0;
-    int at = 0;
-    float pw = 0.f;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (key[i] > best) {  // strictly: the lane's lowest index among equals
-        best = key[i];
-        at = i;
-        pw = p[i];
+    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    uint32_t mine = kAll;  // the lane's lowest index with that key
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i) mine = key[i] == top ? (uint32_t)(lane + 32 * i) : mine;
+    const uint32_t id = __reduce_min_sync(kAll, mine);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i == (int)id ? 0u : key[i];
+    if (lane == k) id_out = (int)id;
+  }
+  w_out = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float v = __shfl_sync(kAll, p[i], id_out & 31);
+    w_out = (id_out >> 5) == i ? v : w_out;
+  }
+  if (r.renormalise) {
+    float total = lane < r.topk ? w_out : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    w_out = w_out / (total + 1e-20f);
+  }
+  w_out *= r.scale;
+}
+
+// ---------------------------------------------------------------- the router for up to 8 tokens by one cluster
+// A cluster of 8 CTAs takes 8 tokens: CTA c computes the logits of expert groups c, c + 8, ... (16 experts each, the
+// 16 warps splitting groups and the K range), sends token i's to CTA i, which selects for it.  The weight rows are
+// read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows l / 4 and
+// l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike, which
+// leaves the sums alone), so each row is read in 16-byte pieces with no staging.
+namespace gate {
+constexpr int kCluster = 8;
+constexpr int kTok = 8;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+struct Smem {
+  float part[kWarps][16][8];    // a warp's sums
+  float logits[kMaxExperts];    // of the token this CTA selects for
+};
+}  // namespace gate
+
+__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem& sm, uint32_t rank) {
+  ptx::cluster_arrive_relaxed();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = p.rule.E, groups = (E + 15) / 16;
+  const int per_cta = (groups + gate::kCluster - 1) / gate::kCluster;  // 1..8
+  const int splits = gate::kWarps / per_cta;
+  const int gi = warp % per_cta, split = warp / per_cta;
+  const int grp = (int)rank + gate::kCluster * gi;
+  if (split < splits && grp < groups) {
+    // rows past the end repeat the last one; what they give is not read
+    const int ea = min(grp * 16 + (lane >> 2), E - 1), eb = min(grp * 16 + 8 + (lane >> 2), E - 1);
+    const int64_t t = t0 + (lane >> 2) < p.T ? t0 + (lane >> 2) : p.T - 1;
+    const __nv_bfloat16* wa = p.weight + (int64_t)ea * p.H;
+    const __nv_bfloat16* wb = p.weight + (int64_t)eb * p.H;
+    const __nv_bfloat16* xr = p.x + t * p.ldx;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int blocks = (int)((p.H + 31) / 32);
+    constexpr int kU = 4;  // blocks of 32 K in flight
+    for (int b0 = split; b0 < blocks; b0 += splits * kU) {
+      uint4 a[kU], b[kU], x[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t k = (int64_t)(b0 + u * splits) * 32 + (lane & 3) * 8;
+        a[u] = b[u] = x[u] = make_uint4(0, 0, 0, 0);
+        if (k < p.H) {
+          a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
+          b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
+          x[u] = *reinterpret_cast<const uint4*>(xr + k);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        ptx::mma_16816(acc, a[u].x, b[u].x, a[u].y, b[u].y, x[u].x, x[u].y);
+        ptx::mma_16816(acc, a[u].z, b[u].z, a[u].w, b[u].w, x[u].z, x[u].w);
       }
     }
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    const uint32_t id = __reduce_min_sync(kAll, best == top ? (uint32_t)(lane + 32 * at) : kAll);
-    const float w = __shfl_sync(kAll, pw, id & 31);
-    total += w;
-    if (lane == k) {
-      id_out = (int)id;
-      w_out = w;
-    }
-    if (lane == (int)(id & 31)) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == at) key[i] = 0u;
+    float* d = &sm.part[warp][lane >> 2][(lane & 3) * 2];
+    d[0] = acc[0];
+    d[1] = acc[1];
+    d[64] = acc[2];
+    d[65] = acc[3];
+  }
+  ptx::cluster_wait();  // the other CTAs have started: their shared memory may be written
+  __syncthreads();
+  for (int i = tid; i < per_cta * 128; i += gate::kThreads) {
+    const int g = i >> 7, r = (i >> 3) & 15, tok = i & 7;
+    const int e = ((int)rank + gate::kCluster * g) * 16 + r;
+    if (e < E && t0 + tok < p.T) {
+      float s = 0.f;
+      for (int k = 0; k < splits; ++k) s += sm.part[k * per_cta + g][r][tok];
+      ptx::st_cluster_f32(ptx::map_to_rank(ptx::smem_u32(&sm.logits[e]), (uint32_t)tok), s);
     }
   }
-  if (r.renormalise) w_out = w_out / (total + 1e-20f);
-  w_out *= r.scale;
+  ptx::cluster_sync();
+  const int64_t t = t0 + rank;
+  if (t >= p.T) return;
+  if (p.logits)
+    for (int e = tid; e < E; e += gate::kThreads) p.logits[t * E + e] = sm.logits[e];
+  if (warp == 0) {
+    int id;
+    float w;
+    if (E <= 64) gate_select_warp<2>(p.rule, sm.logits, p.select_bias, lane, id, w);
+    else if (E <= 256) gate_select_warp<8>(p.rule, sm.logits, p.select_bias, lane, id, w);
+    else gate_select_warp<32>(p.rule, sm.logits, p.select_bias, lane, id, w);
+    if (lane < p.rule.topk) {
+      const int64_t o = t * p.rule.topk + lane;
+      if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = id;
+      else static_cast<int32_t*>(p.ids)[o] = id;
+      p.weights[o] = w;
+    }
+  }
 }
 
 }  // namespace gmmfr

@@ -63,8 +63,30 @@ __global__ void __launch_bounds__(128) gate_select_kernel(GateParams p) {
   }
 }
 
+__global__ void __launch_bounds__(gate::kThreads) gate_cluster_kernel(const __grid_constant__ GateParams p) {
+  __shared__ gate::Smem sm;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  gate_cluster(p, (int64_t)(blockIdx.x / gate::kCluster) * gate::kTok, sm, ptx::cluster_rank());
+}
+
 cudaError_t launch_gate(const GateParams& p, cudaStream_t s) {
   if (p.T == 0) return cudaSuccess;
+  if (p.T <= kGateClusterTokens) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = gate::kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    lc.stream = s;
+    lc.gridDim = dim3((unsigned)((p.T + gate::kTok - 1) / gate::kTok * gate::kCluster));
+    lc.blockDim = dim3(gate::kThreads);
+    return cudaLaunchKernelEx(&lc, gate_cluster_kernel, p);
+  }
   const int64_t per_launch = (int64_t)65535 * kGateTok;  // grid.y limit
   for (int64_t t = 0; t < p.T; t += per_launch) {
     GateParams q = p;

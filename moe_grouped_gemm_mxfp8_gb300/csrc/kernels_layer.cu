@@ -1,7 +1,7 @@
 // A whole mixture-of-experts layer for a few tokens (at most 64), in two kernels.
 //
-//   front   the gate's logits; the tokens as images of the products' B operand; counters to zero
-//   layer   one persistent CTA per SM: top-k of every token, then two runs of weight tiles
+//   front   the gate; the tokens as images of the products' B operand; counters to zero
+//   layer   one persistent CTA per SM; two runs of weight tiles
 //             up          x times the gate/up tiles of the shared expert and of the chosen ones
 //             down        column tile by column tile: sw times the down tiles of every chosen expert and of
 //                         the shared one, one long sum over (expert, intermediate index)
@@ -89,8 +89,7 @@ cudaError_t launch_ffn_prep_mx(const FfnPrepMxParams& p, cudaStream_t s) {
 
 namespace layer {
 
-constexpr int kThreads = 256;  // warp 0 weights, 1 MMA, 2..5 epilogue, 6 tokens' producer, 7 none; 1..7 also top-k
-constexpr int kSelectWarps = 7;
+constexpr int kThreads = 256;  // warp 0 weights, 1 MMA, 2..5 epilogue, 6 tokens' producer
 constexpr int kMaxStages = 11;
 // A stage: weight tile (with MXFP8 its 512 scale bytes), then the tokens' image: BF16 npad rows of 128 bytes;
 // MXFP8 scale chunks of hi and lo (512 bytes each), 512 unused, npad rows of hi, npad of lo.
@@ -163,6 +162,11 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
 __device__ __forceinline__ void red_release_add(uint32_t* p, uint32_t v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
 // Bounded wait until *p reaches n.
 __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n, const Ctl& c) {
   const uint64_t t0 = ptx::globaltimer();
@@ -231,53 +235,29 @@ struct Walk {
 }  // namespace
 
 // ============================================================================ front
-// One warp per (expert, up to 8 tokens) for the logits; then the token images and the counters.
+// The first T / 8 clusters are the router (gate_select.cuh); the others make the token images and zero the counters.
 template <bool kMx>
-__global__ void __launch_bounds__(256) layer_front_kernel(const __grid_constant__ LayerParams p) {
+__global__ void __launch_bounds__(gate::kThreads) layer_front_kernel(const __grid_constant__ LayerParams p) {
+  __shared__ gate::Smem sm;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const GateParams& g = p.gate;
-  const int T = (int)g.T, E = g.rule.E;
+  const int T = (int)g.T;
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * 8, w0 = threadIdx.x / 32 * gridDim.x + blockIdx.x;
-  const int groups = (T + 7) / 8;
-  for (int task = w0; task < E * groups; task += warps) {
-    const int e = task % E, t0 = task / E * 8;
-    const __nv_bfloat16* wrow = g.weight + (int64_t)e * g.H;
-    float acc[8] = {};
-    for (int64_t h = lane * 8; h < g.H; h += 256) {
-      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(wrow + h));
-      const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (t0 + i < T) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(g.x + (int64_t)(t0 + i) * g.ldx + h);
-          const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[i] = fmaf(__uint_as_float(wu[q] << 16), __uint_as_float(xu[q] << 16), acc[i]);
-            acc[i] = fmaf(__uint_as_float(wu[q] & 0xffff0000u), __uint_as_float(xu[q] & 0xffff0000u), acc[i]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (t0 + i < T) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-        if (lane == 0) g.logits[(int64_t)(t0 + i) * E + e] = acc[i];
-      }
-    }
+  const int routers = (T + gate::kTok - 1) / gate::kTok * gate::kCluster;
+  if ((int)blockIdx.x < routers) {
+    gate_cluster(g, (int64_t)(blockIdx.x / gate::kCluster) * gate::kTok, sm, ptx::cluster_rank());
+    return;
   }
-  const int tid = threadIdx.x * gridDim.x + blockIdx.x, threads = gridDim.x * 256;
+  const int block = blockIdx.x - routers, blocks = gridDim.x - routers, warps = blocks * gate::kWarps;
+  const int tid = threadIdx.x * blocks + block, threads = blocks * gate::kThreads;
   for (int i = tid; i < p.n_counters; i += threads) p.counters[i] = 0;
   // images: 8 elements of a row per thread, zero past H (their weights are zero, but 0 x NaN is not)
   const int img = layer::image_bytes(kMx, p.npad);
   const int per_row = p.KB1 * (kMx ? 16 : 8);
   // a warp's 32 items are consecutive 8-element chunks of a row (per_row is a multiple of 8: quads never straddle)
   const int items = T * per_row, w_items = (items + 31) / 32;
-  for (int wi = blockIdx.x + threadIdx.x / 32 * gridDim.x; wi < w_items; wi += warps) {
+  for (int wi = block + threadIdx.x / 32 * blocks; wi < w_items; wi += warps) {
     const int it = wi * 32 + lane;
     const bool in = it < items;
     const int t = in ? it / per_row : 0, c = in ? it - t * per_row : 0;
@@ -375,46 +355,11 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
 
   ptx::griddep_wait();
 
-  // ---------------------------------------------------------------- top-k
-  // up to one token per selecting warp: every CTA selects all of them; more: CTA t selects token t
-  bool ok0 = true;
-  const bool everywhere = T <= layer::kSelectWarps;
-  if (warp > 0) {
-    for (int t = everywhere ? warp - 1 : (int)blockIdx.x + (warp - 1) * G; t < T; t += everywhere ? layer::kSelectWarps : layer::kSelectWarps * G) {
-      int id;
-      float w;
-      const float* l = g.logits + (int64_t)t * E;
-      if (E <= 64) gate_select_warp<2>(g.rule, l, g.select_bias, lane, id, w);
-      else if (E <= 256) gate_select_warp<8>(g.rule, l, g.select_bias, lane, id, w);
-      else gate_select_warp<32>(g.rule, l, g.select_bias, lane, id, w);
-      if (lane < topk) {
-        if (everywhere) {
-          s_ids[t * topk + lane] = (uint16_t)id;
-          s_wt[t * topk + lane] = w;
-        }
-        if (!everywhere || blockIdx.x == 0) {
-          static_cast<int32_t*>(g.ids)[t * topk + lane] = id;
-          g.weights[t * topk + lane] = w;
-        }
-      }
-      if (!everywhere) {
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) red_release_add(p.select_done, 1);
-      }
-    }
-  }
-  if (!everywhere) {
-    if (threadIdx.x == 32) ok0 = wait_count(p.select_done, T, ctl);
-    __syncthreads();
-    for (int i = threadIdx.x; i < T * topk; i += layer::kThreads) {
-      s_ids[i] = (uint16_t)(__ldcg(static_cast<const int32_t*>(g.ids) + i) & (kMaxExperts - 1));
-      s_wt[i] = __ldcg(g.weights + i);
-    }
-  }
-  __syncthreads();
+  // ---------------------------------------------------------------- the chosen experts
   for (int i = threadIdx.x; i < T * topk; i += layer::kThreads) {
-    const int e = s_ids[i] < E ? s_ids[i] : 0;
+    const int e = static_cast<const int32_t*>(g.ids)[i];  // in [0, E): the front kernel's
+    s_ids[i] = (uint16_t)e;
+    s_wt[i] = g.weights[i];
     atomicOr(&s_mask[e], 1ull << (i / topk));
   }
   __syncthreads();
@@ -449,9 +394,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   const int n_units = A * p.NT1 + p.NT1s;  // the shared expert's first
   const Run up{(uint32_t)n_units * p.KB1, (uint32_t)p.KB1, (uint32_t)G}, down{(uint32_t)p.NT2 * D, (uint32_t)D, (uint32_t)G};
   Walk walk(up, down);
-  if (*abort_flag) {
-    // the selection never arrived: nothing has been requested
-  } else if (warp == 0) {
+  if (warp == 0) {
     // -------------------------------------------------------------- weights
     if (lane == 0) {
       const uint64_t pol = ptx::l2_evict_first_policy();
@@ -599,7 +542,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     const int row = q * 32 + lane;  // this thread's TMEM lane: row of the weight tile
     const int64_t slot_floats = (int64_t)T * 128;
     int acc_i = 0;
-    int cut_j[2], n_cut = 0;  // column tiles of the down run that this CTA has a piece of
+    int cut0 = 0, cut1 = 0, n_cut = 0;  // column tiles of the down run that this CTA has a piece of
     bool ok = true;
     while (walk.next()) {
       const int buf = acc_i & 1;
@@ -636,16 +579,14 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           for (int jj = 0; jj < 16; ++jj)
             if ((mask >> (c0 + jj)) & 1) __stcg(slot + (c0 + jj) * 128 + row, __uint_as_float(v[jj]));
         }
-        __threadfence();
-        ptx::bar_sync(1, 128);
+        ptx::bar_sync(1, 128);  // the pieces' stores, then one thread's release
         if (is_down) {
           if (ep == 0) red_release_add(p.down_cnt + walk.unit, 1);
-          cut_j[n_cut++ & 1] = walk.unit;
+          if (n_cut++ == 0) cut0 = walk.unit;
+          else cut1 = walk.unit;
         } else {
           if (ep == 0) {
-            const uint32_t before = atomicAdd(p.up_cnt + walk.unit, 1u);
-            *s_last = before == pieces.n - 1;
-            __threadfence();
+            *s_last = atom_add_acq_rel(p.up_cnt + walk.unit, 1u) == pieces.n - 1;
           }
           ptx::bar_sync(1, 128);
           finish = *s_last != 0;
@@ -685,7 +626,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             } else {
 #pragma unroll
               for (int jj = 0; jj < 16; ++jj) v[jj] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
               for (uint32_t i = 0; i < pieces.n; ++i) {
                 const float* slot = p.slots_up + (int64_t)pieces.slot(i) * slot_floats + row;
 #pragma unroll
@@ -693,39 +634,48 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
                   if ((m16 >> jj) & 1) v[jj] += __ldcg(slot + (c0 + jj) * 128);
               }
             }
-            if (q >= 2) {
+            // warps 2, 3 (gate rows) take the even tokens, warps 4, 5 (up rows) the odd ones: each hands
+            // the other what it needs
 #pragma unroll
-              for (int jj = 0; jj < 16; ++jj) xchg[((q - 2) * 16 + jj) * 32 + lane] = v[jj];
-            }
+            for (int jj = 0; jj < 16; ++jj)
+              if ((jj & 1) == (q >= 2 ? 0 : 1)) xchg[((q & 1) * 16 + jj) * 32 + lane] = v[jj];
             ptx::bar_sync(1, 128);
           }
-          if (q < 2) {
+          const int half = q >= 2, col = (q & 1) * 32 + lane;  // intermediate index within the unit
 #pragma unroll
-            for (int jj = 0; jj < 16; ++jj) {
-              const int t = c0 + jj;
-              if (t < T) {
-                float sw = 0.f;
-                if ((m16 >> jj) & 1) sw = silu(v[jj]) * xchg[(q * 16 + jj) * 32 + lane] * s_tokw[t];
-                if constexpr (!kMx) {
-                  *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, row >> 3) + (row & 7) * 2) = __float2bfloat16_rn(sw);
-                } else {
+          for (int i = 0; i < 8; ++i) {
+            const int jj = 2 * i + half, t = c0 + jj;
+            if (t < T) {
+              const bool on = (m16 >> jj) & 1;  // the token chose this expert
+              float sw = 0.f;
+              if (on) {
+                const float o = xchg[((q & 1) * 16 + jj) * 32 + lane];
+                const float mine = half ? v[2 * i + 1] : v[2 * i];
+                sw = silu(half ? o : mine) * (half ? mine : o) * s_tokw[t];
+              }
+              if constexpr (!kMx) {
+                *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(sw);
+              } else {
+                uint32_t hi = 0, lo = 0, byte_hi = 127, byte_lo = 127;
+                if (on) {
                   const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
-                  uint32_t hi, lo;
                   split_e4m3(sw, b, hi, lo);
-                  const int col = (j & 1) * 64 + row;
-                  uint8_t* at = dst + 1536 + image_chunk(t, col >> 4) + (col & 15);
-                  at[0] = (uint8_t)hi;
-                  at[npad * 128] = (uint8_t)lo;
-                  if (lane == 0) {
-                    dst[scale_at(t, col >> 5)] = (uint8_t)b.byte_hi;
-                    dst[512 + scale_at(t, col >> 5)] = (uint8_t)b.byte_lo;
-                  }
-                  if (pad_half) {  // the tile's second half lies past the intermediate size
-                    uint8_t* z = dst + 1536 + image_chunk(t, (col + 64) >> 4) + (col & 15);
-                    z[0] = 0;
-                    z[npad * 128] = 0;
-                    if (lane == 0) dst[scale_at(t, (col + 64) >> 5)] = dst[512 + scale_at(t, (col + 64) >> 5)] = 127;
-                  }
+                  byte_hi = b.byte_hi;
+                  byte_lo = b.byte_lo;
+                }
+                const int c = (j & 1) * 64 + col;
+                uint8_t* at = dst + 1536 + image_chunk(t, c >> 4) + (c & 15);
+                at[0] = (uint8_t)hi;
+                at[npad * 128] = (uint8_t)lo;
+                if (lane == 0) {
+                  dst[scale_at(t, c >> 5)] = (uint8_t)byte_hi;
+                  dst[512 + scale_at(t, c >> 5)] = (uint8_t)byte_lo;
+                }
+                if (pad_half) {  // the tile's second half lies past the intermediate size
+                  uint8_t* z = dst + 1536 + image_chunk(t, (c + 64) >> 4) + (c & 15);
+                  z[0] = 0;
+                  z[npad * 128] = 0;
+                  if (lane == 0) dst[scale_at(t, (c + 64) >> 5)] = dst[512 + scale_at(t, (c + 64) >> 5)] = 127;
                 }
               }
             }
@@ -733,7 +683,6 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           if (m16) ptx::bar_sync(1, 128);  // xchg is written again
         }
         asm volatile("fence.proxy.async;" ::: "memory");  // sw is read by bulk copies
-        __threadfence();
         ptx::bar_sync(1, 128);
         if (ep == 0) red_release_add(p.up_done, 1);
       }
@@ -748,7 +697,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
                      ((p.ld_out | p.ld_residual) & 3) == 0;
     if (ok && !*abort_flag) {
       for (int c = 0; c < n_cut; ++c) {
-        const int j = cut_j[c & 1];
+        const int j = c == 0 ? cut0 : cut1;
         const Pieces pieces(down, j);
         const int n = pieces.n;
         if (ep == 0) ok = wait_count(p.down_cnt + j, n, ctl);
@@ -819,17 +768,23 @@ static cudaError_t launch_layer_of(const LayerParams& p, int sms, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeCooperative;  // CTAs wait for one another: all must be resident
   attr[1].val.cooperative = 1;
-  lc.attrs = attr;
   lc.stream = s;
-  lc.gridDim = dim3((unsigned)sms);
-  lc.blockDim = dim3(256);
-  lc.numAttrs = 1;
+  // the router's clusters (one per 8 tokens, at most 8), and at least 10 for the images
+  lc.gridDim = dim3((unsigned)((p.gate.T + gate::kTok - 1) / gate::kTok + 10) * gate::kCluster);
+  lc.blockDim = dim3(gate::kThreads);
+  cudaLaunchAttribute fattr[2];
+  fattr[0] = attr[0];
+  fattr[1].id = cudaLaunchAttributeClusterDimension;
+  fattr[1].val.clusterDim.x = gate::kCluster;
+  fattr[1].val.clusterDim.y = fattr[1].val.clusterDim.z = 1;
+  lc.attrs = fattr;
+  lc.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&lc, layer_front_kernel<kMx>, p);
   if (e != cudaSuccess) return e;
   lc.gridDim = dim3((unsigned)(sms < kLayerMaxCtas ? sms : kLayerMaxCtas));
   lc.blockDim = dim3(layer::kThreads);
   lc.dynamicSmemBytes = layer::kSmemBytes;
-  lc.numAttrs = 2;
+  lc.attrs = attr;
   return cudaLaunchKernelEx(&lc, layer_kernel<kMx>, p);
 }
 

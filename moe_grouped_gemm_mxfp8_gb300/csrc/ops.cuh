@@ -13,6 +13,7 @@ int sm_count();
 constexpr int kMaxTopk = 32;
 constexpr int kMaxGroups = 64;
 constexpr int kLayerMaxTokens = 64;
+constexpr int kGateClusterTokens = 512;  // the router up to here: clusters of 8 CTAs, 8 tokens each
 
 // The router's rule (gmmfr_gate_problem).
 struct GateRule {
@@ -27,7 +28,7 @@ struct GateParams {
   const __nv_bfloat16* x;       // [T, H], row stride ldx
   const __nv_bfloat16* weight;  // [E, H]
   const float* select_bias;     // [E] or null
-  float* logits;                // [T, E]: the caller's or the workspace's
+  float* logits;                // [T, E] or null (up to kGateClusterTokens tokens)
   void* ids;                    // [T, topk] int32 or int64
   float* weights;               // [T, topk]
   int64_t T, H, ldx;
@@ -47,7 +48,7 @@ cudaError_t launch_ffn_prep_mx(const FfnPrepMxParams& p, cudaStream_t s);
 
 constexpr int kLayerMaxCtas = 160;  // the workspace has slots for so many
 struct LayerParams {
-  GateParams gate;  // its ids are int32; ids, weights and logits may lie in the workspace
+  GateParams gate;  // its ids are int32; ids and weights may lie in the workspace, logits is null
   const __nv_bfloat16* residual;
   __nv_bfloat16* out;
   const uint8_t *prepared, *prepared2;  // routed experts: gate/up tiles, down tiles
@@ -56,7 +57,7 @@ struct LayerParams {
   uint8_t *ximg, *swimg, *swimg_s;      // B operand images: tokens, SwiGLU values (routed, shared)
   float *slots_up, *slots_down;         // pieces of cut tiles: [CTA][2][T][128] each
   // counters, zeroed by the front kernel
-  uint32_t *counters, *select_done, *up_done, *up_cnt, *down_cnt;
+  uint32_t *counters, *up_done, *up_cnt, *down_cnt;
   int64_t ld_residual, ld_out, timeout_ns;
   int32_t n_counters, npad;
   int32_t NT1, KB1, NT2, KB2;  // tiles of a routed expert
