@@ -92,10 +92,10 @@ namespace layer {
 constexpr int kThreads = 256;  // warp 0 weights, 1 MMA, 2..5 epilogue, 6 tokens' producer
 constexpr int kMaxStages = 11;
 // A stage: weight tile (with MXFP8 its 512 scale bytes), then the tokens' image: BF16 npad rows of 128 bytes;
-// MXFP8 scale chunks of hi and lo (512 bytes each), 512 unused, npad rows of hi, npad of lo.
+// MXFP8 the scale chunk of hi and lo (512 bytes), npad rows of hi codes, npad of lo.
 __host__ __device__ constexpr int tile_bytes(bool mx) { return mx ? kPrepTileBytes : kWTileBytes; }
-__host__ __device__ constexpr int rows_off(bool mx) { return mx ? 18432 : kWTileBytes; }
-__host__ __device__ constexpr int image_bytes(bool mx, int npad) { return mx ? 1536 + 256 * npad : 128 * npad; }
+__host__ __device__ constexpr int rows_off(bool mx) { return mx ? kPrepTileBytes + kSfChunk : kWTileBytes; }
+__host__ __device__ constexpr int image_bytes(bool mx, int npad) { return mx ? kSfChunk + 256 * npad : 128 * npad; }
 __host__ __device__ constexpr int stage_bytes(bool mx, int npad) { return tile_bytes(mx) + image_bytes(mx, npad); }
 constexpr int kArena = 11 * 18432;
 __host__ __device__ constexpr int n_stages(bool mx, int npad) {
@@ -114,10 +114,12 @@ constexpr int kXchgOff = kWtOff + 4 * kLayerMaxTokens * kMaxTopk;  // float [2][
 constexpr int kTokWOff = kXchgOff + 2 * 16 * 32 * 4;             // float [64]: the unit's router weights
 constexpr int kSmemBytes = kTokWOff + 4 * kLayerMaxTokens + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-__host__ __device__ constexpr int sf_cols(bool mx) { return mx ? 12 : 0; }  // TMEM scale columns per stage
-constexpr int kTmemCols = 256;
-static_assert(2 * 64 + sf_cols(true) * n_stages(true, 64) <= kTmemCols && 2 * 16 + sf_cols(true) * n_stages(true, 16) <= kTmemCols &&
-                  2 * 32 + sf_cols(true) * n_stages(true, 32) <= kTmemCols && 2 * 48 + sf_cols(true) * n_stages(true, 48) <= kTmemCols,
+// TMEM: two accumulators of acc_cols columns (MXFP8: the products with hi, then those with lo), then with MXFP8 the
+// scale columns of every stage
+__host__ __device__ constexpr int acc_cols(bool mx, int npad) { return mx ? 2 * npad : npad; }
+__host__ __device__ constexpr int tmem_cols(bool mx) { return mx ? 512 : 128; }
+static_assert(2 * acc_cols(true, 64) + 8 * n_stages(true, 64) <= tmem_cols(true) &&
+                  2 * acc_cols(true, 16) + 8 * n_stages(true, 16) <= tmem_cols(true) && 2 * acc_cols(false, 64) <= tmem_cols(false),
               "TMEM");
 
 }  // namespace layer
@@ -179,6 +181,24 @@ __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n, const 
     }
   }
   return true;
+}
+
+// Tokens c0 .. c0 + 15 of this thread's accumulator row (MXFP8: the sums with hi and with lo).
+template <bool kMx>
+__device__ __forceinline__ void load_acc16(uint32_t taddr, int npad, float (&v)[16]) {
+  uint32_t r[16];
+  ptx::tmem_ld_32x32b_x16(taddr, r);
+  if constexpr (kMx) {
+    uint32_t l[16];
+    ptx::tmem_ld_32x32b_x16(taddr + npad, l);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]) + __uint_as_float(l[i]);
+  } else {
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  }
 }
 
 // One run of U tiles in units of K tiles, cut evenly over G CTAs: CTA b has [U b / G, U (b + 1) / G).
@@ -288,11 +308,11 @@ __global__ void __launch_bounds__(gate::kThreads) layer_front_kernel(const __gri
       if (in) {
         uint8_t* dst = p.ximg + (int64_t)(c >> 4) * img;
         const int at = image_chunk(t, (c & 15) >> 1) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(dst + 1536 + at) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + 1536 + p.npad * 128 + at) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(dst + kSfChunk + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + kSfChunk + p.npad * 128 + at) = make_uint2(lo[0], lo[1]);
         if ((c & 3) == 0) {
           dst[scale_at(t, (c & 15) >> 2)] = (uint8_t)b.byte_hi;
-          dst[512 + scale_at(t, (c & 15) >> 2)] = (uint8_t)b.byte_lo;
+          dst[scale_at(p.npad + t, (c & 15) >> 2)] = (uint8_t)b.byte_lo;
         }
       }
     }
@@ -324,7 +344,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const GateParams& g = p.gate;
   const int T = (int)g.T, E = g.rule.E, topk = g.rule.topk, G = gridDim.x;
-  const int npad = p.npad, img = layer::image_bytes(kMx, npad);
+  const int npad = p.npad, acc = layer::acc_cols(kMx, npad), img = layer::image_bytes(kMx, npad);
   const int tile = layer::tile_bytes(kMx), stage_bytes = layer::stage_bytes(kMx, npad), n_stages = layer::n_stages(kMx, npad);
   const uint32_t smem_base = ptx::smem_u32(smem);
 
@@ -344,7 +364,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   }
   for (int e = threadIdx.x; e < E; e += layer::kThreads) s_mask[e] = 0;
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), layer::kTmemCols);
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), layer::tmem_cols(kMx));
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -488,8 +508,8 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     // -------------------------------------------------------------- products
     if (lane == 0) {
       // kind::f16: FP32 accumulator, BF16 operands; kind::mxf8f6f4: E4M3 operands with E8M0 scales
-      const uint32_t idesc = (kMx ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) | ((128u >> 4) << 24) | ((uint32_t)(npad >> 3) << 17);
-      const uint32_t sf0 = tmem_base + 2 * npad;
+      const uint32_t idesc = (kMx ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) | ((128u >> 4) << 24) | ((uint32_t)(acc >> 3) << 17);
+      const uint32_t sf0 = tmem_base + 2 * acc;
       int stage = 0, acc_i = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -497,7 +517,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         const int buf = acc_i & 1;
         if (!wait_bar(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem_base + buf * npad;
+        const uint32_t d = tmem_base + buf * acc;
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
           if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
             ok = false;
@@ -512,15 +532,13 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             for (int q = 0; q < 4; ++q) ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
           } else {
             const uint64_t ds = ptx::smem_desc(sb + kWTileBytes, 0, 128, ptx::kSwizzleNone);
-            const uint32_t sfa = sf0 + 12 * stage;
+            const uint32_t sfa = sf0 + 8 * stage;
+            ptx::tc_cp_sf(sfa, ds);                         // the weights' scales
+            ptx::tc_cp_sf(sfa + 4, ds + (kSfChunk >> 4));  // the tokens'
 #pragma unroll
-            for (int q = 0; q < 3; ++q) ptx::tc_cp_sf(sfa + 4 * q, ds + q * (kSfChunk >> 4));  // weights, hi, lo
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t id = idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29);
-              ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, id, sfa, sfa + 4, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
-              ptx::tc_mma_mxf8(d, da + 2 * q, db + (uint32_t)(npad * 128 >> 4) + 2 * q, id, sfa, sfa + 8, 1u);
-            }
+            for (int q = 0; q < 4; ++q)
+              ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29), sfa, sfa + 4,
+                               (k > (int)walk.k0 || q > 0) ? 1u : 0u);
           }
           ptx::tc_commit(ptx::smem_u32(&empty[stage]));
           if (++stage == n_stages) {
@@ -563,7 +581,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
       ok = warp_wait_bar(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
       if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
       ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * npad;
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * acc;
       bool finish = whole;
       const Pieces pieces(run, walk.unit);
       if (!whole) {
@@ -572,12 +590,11 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         float* slot = (is_down ? p.slots_down : p.slots_up) + (int64_t)at * slot_floats;
         for (int c0 = 0; c0 < T; c0 += 16) {
           if (((mask >> c0) & 0xffff) == 0) continue;
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + c0, v);
-          ptx::tmem_wait_ld();
+          float v[16];
+          load_acc16<kMx>(taddr + c0, npad, v);
 #pragma unroll
           for (int jj = 0; jj < 16; ++jj)
-            if ((mask >> (c0 + jj)) & 1) __stcg(slot + (c0 + jj) * 128 + row, __uint_as_float(v[jj]));
+            if ((mask >> (c0 + jj)) & 1) __stcg(slot + (c0 + jj) * 128 + row, v[jj]);
         }
         ptx::bar_sync(1, 128);  // the pieces' stores, then one thread's release
         if (is_down) {
@@ -594,15 +611,14 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
       }
       if (finish && is_down) {  // a column tile of this CTA alone
         for (int c0 = 0; c0 < T; c0 += 16) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + c0, v);
-          ptx::tmem_wait_ld();
+          float v[16];
+          load_acc16<kMx>(taddr + c0, npad, v);
           const int64_t n = (int64_t)j * 128 + row;
 #pragma unroll
           for (int jj = 0; jj < 16; ++jj) {
             const int t = c0 + jj;
             if (t < T && n < g.H) {
-              float o = __uint_as_float(v[jj]);
+              float o = v[jj];
               if (p.residual) o += __bfloat162float(p.residual[t * p.ld_residual + n]);
               p.out[t * p.ld_out + n] = __float2bfloat16_rn(o);
             }
@@ -618,11 +634,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           float v[16];
           if (m16) {  // uniform over the four warps
             if (whole) {
-              uint32_t r[16];
-              ptx::tmem_ld_32x32b_x16(taddr + c0, r);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int jj = 0; jj < 16; ++jj) v[jj] = __uint_as_float(r[jj]);
+              load_acc16<kMx>(taddr + c0, npad, v);
             } else {
 #pragma unroll
               for (int jj = 0; jj < 16; ++jj) v[jj] = 0.f;
@@ -664,18 +676,18 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
                   byte_lo = b.byte_lo;
                 }
                 const int c = (j & 1) * 64 + col;
-                uint8_t* at = dst + 1536 + image_chunk(t, c >> 4) + (c & 15);
+                uint8_t* at = dst + kSfChunk + image_chunk(t, c >> 4) + (c & 15);
                 at[0] = (uint8_t)hi;
                 at[npad * 128] = (uint8_t)lo;
                 if (lane == 0) {
                   dst[scale_at(t, c >> 5)] = (uint8_t)byte_hi;
-                  dst[512 + scale_at(t, c >> 5)] = (uint8_t)byte_lo;
+                  dst[scale_at(npad + t, c >> 5)] = (uint8_t)byte_lo;
                 }
                 if (pad_half) {  // the tile's second half lies past the intermediate size
-                  uint8_t* z = dst + 1536 + image_chunk(t, (c + 64) >> 4) + (c & 15);
+                  uint8_t* z = dst + kSfChunk + image_chunk(t, (c + 64) >> 4) + (c & 15);
                   z[0] = 0;
                   z[npad * 128] = 0;
-                  if (lane == 0) dst[scale_at(t, (c + 64) >> 5)] = dst[512 + scale_at(t, (c + 64) >> 5)] = 127;
+                  if (lane == 0) dst[scale_at(t, (c + 64) >> 5)] = dst[scale_at(npad + t, (c + 64) >> 5)] = 127;
                 }
               }
             }
@@ -744,7 +756,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, layer::kTmemCols);
+    ptx::tmem_dealloc(tmem_base, layer::tmem_cols(kMx));
   }
   if (threadIdx.x == 0) {
     p.hdr[1 + blockIdx.x] = *s_err;

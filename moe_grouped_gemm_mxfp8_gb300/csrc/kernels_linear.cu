@@ -28,7 +28,8 @@ constexpr int kTileBytes = 128 * 128;
 constexpr int kPairArena = 6 * 32768;
 constexpr int kPairMaxStages = 10;
 constexpr int kPairBars = 2 * kPairMaxStages + 5;
-constexpr int kPairSmem = kPairArena + kPairBars * 8 + 32 + 1024;
+constexpr int kPairTurnOff = kPairArena + kPairBars * 8 + 32;  // float [4][32][33]: an epilogue warp's 32 x 32 outputs
+constexpr int kPairSmem = kPairTurnOff + 4 * 32 * 33 * 4 + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget");
 
 // ---- stream form
@@ -56,9 +57,12 @@ __device__ __forceinline__ void store_out(const LinearParams& p, int64_t m, int6
   else static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
 }
 
-// 32 consecutive columns n.. of row m, activated values in v (bias included).
-__device__ __forceinline__ void store_row32(const LinearParams& p, int64_t m, int64_t n, float (&v)[32]) {
+// A warp's 32 rows m0.. by 32 columns n.., activated values in v (bias included), lane l holding row m0 + l.
+__device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, int64_t n, float (&v)[32], float* turn) {
+  const int lane = threadIdx.x & 31;
+  const int64_t m = m0 + lane;
   if (p.vec_out && n + 32 <= p.N) {
+    if (m >= p.M) return;
     if (p.residual) {
       const uint4* r = reinterpret_cast<const uint4*>(p.residual + m * p.ldr + n);
       uint4 w[4];
@@ -86,9 +90,17 @@ __device__ __forceinline__ void store_row32(const LinearParams& p, int64_t m, in
                           pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
     }
   } else {
+    // rows off 16-byte boundaries, or the ragged last columns: turned around in shared memory, so that the warp
+    // writes one row after the other in consecutive elements
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (n + j < p.N) store_out(p, m, n + j, v[j]);
+    for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = v[j];
+    __syncwarp();
+    const int rows = p.M - m0 < 32 ? (int)(p.M - m0) : 32;
+    if (n + lane < p.N) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) store_out(p, m0 + r, n + lane, turn[r * 33 + lane]);
+    }
+    __syncwarp();
   }
 }
 
@@ -241,6 +253,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3;
+    float* turn = reinterpret_cast<float*>(smem + lin::kPairTurnOff) + q * 32 * 33;
     int acc_i = 0;
     for (int t = first; t < tiles; t += pairs) {
       int mt, nt;
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
       if (!warp_wait_bar(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
-      const int64_t m = (int64_t)mt * 256 + rank * 128 + q * 32 + lane;
+      const int64_t m0 = (int64_t)mt * 256 + rank * 128 + q * 32;  // this warp's rows
       const int cols = kGated ? BN / 2 : BN;
       const int64_t n0 = (int64_t)nt * cols;
       for (int c0 = 0; c0 < cols; c0 += 32) {
@@ -273,7 +286,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = activate(kAct, v[j]);
         }
-        if (m < p.M) store_row32(p, m, n0 + c0, v);
+        store_tile32(p, m0, n0 + c0, v, turn);
       }
       ptx::tc_fence_before();
       __syncwarp();
