@@ -372,8 +372,6 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   if ((!aligned(x, 16) && !repitch_x(problem)) || (!aligned(weight, 16) && !repitch_w(problem)))
     return fail(GMMFR_ERR_INVALID_ARG, "x or weight is off a 16-byte boundary: set problem.unaligned (and size the workspace with it)");
   if (gmmfr_status st = check_workspace(workspace, workspace_bytes, L.total)) return st;
-  PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
-  if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = gmmfr::sm_count();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -412,9 +410,14 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   }
   gmmfr::plan_linear(lp, sms);
   gmmfr::LinearMaps maps;
-  if (!encode_rows(encode, &maps.x, lp.x, p.M, p.K, lp.ldx, lp.stream ? lp.bn : 128) ||
-      !encode_rows(encode, &maps.w, lp.w, rows_w, p.K, lp.ldw, lp.stream ? (gated ? 64 : 128) : lp.bn / 2))
-    return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  if (lp.form != gmmfr::kLinearDirect) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const bool stream_form = lp.form == gmmfr::kLinearStream;
+    if (!encode_rows(encode, &maps.x, lp.x, p.M, p.K, lp.ldx, stream_form ? lp.bn : 128) ||
+        !encode_rows(encode, &maps.w, lp.w, rows_w, p.K, lp.ldw, stream_form ? (gated ? 64 : 128) : lp.bn / 2))
+      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  }
   cudaError_t e = gmmfr::launch_linear(maps, lp, s);
   if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   return GMMFR_OK;

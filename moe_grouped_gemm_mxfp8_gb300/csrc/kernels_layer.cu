@@ -171,15 +171,9 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
 }
 // Bounded wait until *p reaches n.
 __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n, const Ctl& c) {
-  const uint64_t t0 = ptx::globaltimer();
-  while (ld_acquire(p) < n) {
-    if (*c.abort) return false;
-    if (ptx::globaltimer() - t0 > (uint64_t)c.timeout_ns) {
-      *c.abort = 1;
-      atomicOr(c.err, kErrTimeout);
-      return false;
-    }
-  }
+  Deadline d;
+  while (ld_acquire(p) < n)
+    if (!d.go_on(c)) return false;
   return true;
 }
 
@@ -341,7 +335,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   float* s_wt = reinterpret_cast<float*>(smem + layer::kWtOff);
   float* xchg = reinterpret_cast<float*>(smem + layer::kXchgOff);
   float* s_tokw = reinterpret_cast<float*>(smem + layer::kTokWOff);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const GateParams& g = p.gate;
   const int T = (int)g.T, E = g.rule.E, topk = g.rule.topk, G = gridDim.x;
   const int npad = p.npad, acc = layer::acc_cols(kMx, npad), img = layer::image_bytes(kMx, npad);
@@ -407,7 +401,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (e0 + i < E && s_mask[e0 + i] != 0) s_act[before++] = (uint16_t)(e0 + i);
-    A = all;
+    A = __shfl_sync(0xffffffffu, all, 0);  // uniform, so that what the roles derive from it is
   }
   __syncthreads();
   const int D = A * p.KB2 + p.KB2s;  // tiles of one column tile of the down run
@@ -416,7 +410,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   Walk walk(up, down);
   if (warp == 0) {
     // -------------------------------------------------------------- weights
-    if (lane == 0) {
+    {
       const uint64_t pol = ptx::l2_evict_first_policy();
       int stage = 0;
       uint32_t phase = 0;
@@ -445,13 +439,15 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
               left = D - k;
             }
           }
-          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
             ok = false;
             break;
           }
-          const uint32_t fb = ptx::smem_u32(&full[stage]);
-          ptx::mbar_arrive_expect_tx(fb, tile);
-          ptx::bulk_g2s(smem_base + stage * stage_bytes, src, tile, fb, pol);
+          if (ptx::elect_one()) {
+            const uint32_t fb = ptx::smem_u32(&full[stage]);
+            ptx::mbar_arrive_expect_tx(fb, tile);
+            ptx::bulk_g2s(smem_base + stage * stage_bytes, src, tile, fb, pol);
+          }
           src += tile;
           --left;
           if (++stage == n_stages) {
@@ -461,7 +457,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         }
       }
       for (int s = 0; ok && s < n_stages; ++s) {  // no copy is in flight at exit
-        ok = wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+        ok = warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1;
@@ -473,29 +469,31 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     __syncwarp();
   } else if (warp == 6) {
     // -------------------------------------------------------------- the tokens' images
-    if (lane == 0) {
+    {
       const uint64_t pol = ptx::l2_evict_last_policy();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, sw_ready = false;
       while (ok && walk.next()) {
         if (walk.is_down && !sw_ready) {  // every unit of the up runs has stored its sw
-          ok = wait_count(p.up_done, n_units, ctl);
+          ok = __all_sync(0xffffffffu, lane != 0 || wait_count(p.up_done, n_units, ctl)) != 0;
           asm volatile("fence.proxy.async;" ::: "memory");
           sw_ready = true;
           if (!ok) break;
         }
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
-          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
             ok = false;
             break;
           }
           const uint8_t* src = !walk.is_down   ? p.ximg + (int64_t)k * img
                                : k < A * p.KB2 ? p.swimg + (int64_t)k * img
                                                : p.swimg_s + (int64_t)(k - A * p.KB2) * img;
-          const uint32_t fb = ptx::smem_u32(&full[stage]);
-          ptx::mbar_arrive_expect_tx(fb, img);
-          ptx::bulk_g2s(smem_base + stage * stage_bytes + tile, src, img, fb, pol);
+          if (ptx::elect_one()) {
+            const uint32_t fb = ptx::smem_u32(&full[stage]);
+            ptx::mbar_arrive_expect_tx(fb, img);
+            ptx::bulk_g2s(smem_base + stage * stage_bytes + tile, src, img, fb, pol);
+          }
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
@@ -506,51 +504,54 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- products
-    if (lane == 0) {
+    {
       // kind::f16: FP32 accumulator, BF16 operands; kind::mxf8f6f4: E4M3 operands with E8M0 scales
       const uint32_t idesc = (kMx ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) | ((128u >> 4) << 24) | ((uint32_t)(acc >> 3) << 17);
       const uint32_t sf0 = tmem_base + 2 * acc;
+      const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
+      const uint64_t ds0 = ptx::smem_desc(smem_base + kWTileBytes, 0, 128, ptx::kSwizzleNone);
       int stage = 0, acc_i = 0;
       uint32_t phase = 0;
       bool ok = true;
       while (ok && walk.next()) {
         const int buf = acc_i & 1;
-        if (!wait_bar(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
+        if (!warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * acc;
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
-          if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
+          if (!warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sb = smem_base + stage * stage_bytes;
-          const uint64_t da = ptx::smem_desc(sb, 16, 1024, ptx::kSwizzle128B);
-          const uint64_t db = ptx::smem_desc(sb + layer::rows_off(kMx), 16, 1024, ptx::kSwizzle128B);
-          if constexpr (!kMx) {
+          if (ptx::elect_one()) {
+            // the start address is a field of 16-byte units: stages stay below 2^18 bytes
+            const uint32_t off = (uint32_t)(stage * stage_bytes) >> 4;
+            const uint64_t da = da0 + off, db = da0 + off + (layer::rows_off(kMx) >> 4);
+            if constexpr (!kMx) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
-          } else {
-            const uint64_t ds = ptx::smem_desc(sb + kWTileBytes, 0, 128, ptx::kSwizzleNone);
-            const uint32_t sfa = sf0 + 8 * stage;
-            ptx::tc_cp_sf(sfa, ds);                         // the weights' scales
-            ptx::tc_cp_sf(sfa + 4, ds + (kSfChunk >> 4));  // the tokens'
+              for (int q = 0; q < 4; ++q)
+                ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
+            } else {
+              const uint32_t sfa = sf0 + 8 * stage;
+              ptx::tc_cp_sf(sfa, ds0 + off);                         // the weights' scales
+              ptx::tc_cp_sf(sfa + 4, ds0 + off + (kSfChunk >> 4));  // the tokens'
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29), sfa, sfa + 4,
-                               (k > (int)walk.k0 || q > 0) ? 1u : 0u);
+              for (int q = 0; q < 4; ++q)
+                ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29), sfa, sfa + 4,
+                                 (k > (int)walk.k0 || q > 0) ? 1u : 0u);
+            }
+            ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+            if (k == (int)walk.k1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[buf]));
           }
-          ptx::tc_commit(ptx::smem_u32(&empty[stage]));
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        ptx::tc_commit(ptx::smem_u32(&accf[buf]));
         ++acc_i;
       }
-      ptx::tc_commit(ptx::smem_u32(drain));
+      if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(drain));
       wait_bar_drain(ptx::smem_u32(drain), 0);
     }
     __syncwarp();
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           for (int k = 0; k < topk; ++k) w = s_ids[ep * topk + k] == e ? s_wt[ep * topk + k] : w;
         s_tokw[ep] = w;
       }
-      ok = warp_wait_bar(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
+      ok = warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
       if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * acc;

@@ -1,7 +1,9 @@
 // The dense product with its epilogue: y = act(x W^T + bias) + residual.
 //
-// Two tensor-core forms (tcgen05 kind::f16, FP32 accumulators in TMEM, operands by TMA):
-//   stream  few rows of x.  The weights are the 128-row operand, the rows of x the N-wide one, so every
+// Three forms, all on the tensor cores with FP32 sums:
+//   direct  up to 32 rows of x.  Weights from global memory straight into the operand registers of mma.sync: no
+//           staging, no accumulator to set up; what counts here is the time to the first byte and the last.
+//   stream  (tcgen05 kind::f16, accumulators in TMEM, operands by TMA) up to 128 rows.  The weights are the 128-row operand, the rows of x the N-wide one, so every
 //           weight byte crosses HBM once; the K range of a tile is split over the CTAs of a cluster, whose
 //           partial sums meet in shared memory (in rank order: deterministic).
 //   pair    many rows.  A pair of CTAs holds a 256 x BN tile of y (cta_group::2: each CTA loads 128 rows of x
@@ -33,12 +35,12 @@ constexpr int kPairSmem = kPairTurnOff + 4 * 32 * 33 * 4 + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget");
 
 // ---- stream form
-constexpr int kStreamMaxStages = 8;
+constexpr int kStreamMaxStages = 11;
 constexpr int kStreamBars = 2 * kStreamMaxStages + 6;
-// ring and partial sums: up to 32 rows two CTAs share an SM, beyond one has it
-__host__ __device__ constexpr int stream_arena(int rows) { return rows <= 32 ? 104 * 1024 : 220 * 1024; }
-__host__ __device__ constexpr int stream_smem(int rows) { return stream_arena(rows) + kStreamBars * 8 + 32 + 1024; }
-static_assert(2 * (stream_smem(32) + 1024) <= 228 * 1024 && stream_smem(64) <= 232448, "shared memory budget");
+// ring and partial sums: two CTAs share an SM, or one has it
+__host__ __device__ constexpr int stream_arena(int per_sm) { return per_sm == 2 ? 104 * 1024 : 220 * 1024; }
+__host__ __device__ constexpr int stream_smem(int per_sm) { return stream_arena(per_sm) + kStreamBars * 8 + 32 + 1024; }
+static_assert(2 * (stream_smem(2) + 1024) <= 228 * 1024 && stream_smem(1) <= 232448, "shared memory budget");
 
 }  // namespace lin
 
@@ -112,6 +114,88 @@ __device__ __forceinline__ void add_bias32(const __nv_bfloat16* bias, int64_t n,
 
 }  // namespace
 
+// ============================================================================ direct form
+// A warp multiplies 16 rows of W (with the gated activation 8 gate rows and the 8 up rows of the same columns) by the
+// rows of x over its share of the K range, both read straight into the operand registers of mma.sync: lane l holds
+// 8 consecutive elements of rows l / 4 and l / 4 + 8, its K slots of two products (A and B permute K alike).  The 16
+// warps of a CTA are `groups` row groups times 16 / groups shares of K, interleaved in blocks of 32, so that the CTA
+// reads each row in long pieces; their sums meet in shared memory in the order of the shares.
+template <bool kGated, int kTiles>
+__global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_constant__ LinearParams p) {
+  constexpr int kTok = 8 * kTiles;
+  constexpr int kU = kTiles <= 2 ? 4 : 2;  // blocks of 32 K in flight
+  __shared__ float part[16][16][kTok + 1];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int groups = p.group_m, splits = 16 / groups, grp = warp % groups, split = warp / groups;
+  constexpr int kCols = kGated ? 8 : 16;  // columns of y per group
+  const int64_t n0 = ((int64_t)blockIdx.x * groups + grp) * kCols;
+  const int M = (int)p.M;
+  if (split < splits && n0 < p.N) {
+    // rows past the end repeat the last one; what they give is not stored
+    const int64_t ra = min(n0 + (lane >> 2), p.N - 1);
+    const int64_t rb = kGated ? p.N + ra : min(n0 + 8 + (lane >> 2), p.N - 1);
+    const __nv_bfloat16* wa = p.w + ra * p.ldw;
+    const __nv_bfloat16* wb = p.w + rb * p.ldw;
+    const __nv_bfloat16* xr[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) xr[i] = p.x + (int64_t)min(8 * i + (lane >> 2), M - 1) * p.ldx;
+    float acc[kTiles][4] = {};
+    const int64_t blocks = (p.K + 31) / 32;
+    for (int64_t b0 = split; b0 < blocks; b0 += splits * kU) {
+      uint4 a[kU], b[kU], x[kU][kTiles];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t k = (b0 + u * splits) * 32 + (lane & 3) * 8;
+        a[u] = b[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
+        if (k < p.K) {
+          a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
+          b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(xr[i] + k));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          ptx::mma_16816(acc[i], a[u].x, b[u].x, a[u].y, b[u].y, x[u][i].x, x[u][i].y);
+          ptx::mma_16816(acc[i], a[u].z, b[u].z, a[u].w, b[u].w, x[u][i].z, x[u][i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      float* d = &part[warp][lane >> 2][8 * i + (lane & 3) * 2];
+      d[0] = acc[i][0];
+      d[1] = acc[i][1];
+      d[8 * (kTok + 1)] = acc[i][2];
+      d[8 * (kTok + 1) + 1] = acc[i][3];
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < groups * kCols * M; i += 512) {  // columns fastest
+    const int c = i % (groups * kCols), t = i / (groups * kCols), g = c / kCols, r = c - g * kCols;
+    const int64_t n = ((int64_t)blockIdx.x * groups + g) * kCols + r;
+    if (n >= p.N) continue;
+    float v = 0.f, u = 0.f;
+    for (int k = 0; k < splits; ++k) {
+      v += part[k * groups + g][r][t];
+      if constexpr (kGated) u += part[k * groups + g][8 + r][t];
+    }
+    if (p.bias) v += __bfloat162float(p.bias[n]);
+    if constexpr (kGated) {
+      if (p.bias) u += __bfloat162float(p.bias[p.N + n]);
+      v = silu(v) * u;
+    } else {
+      v = activate(p.act, v);
+    }
+    store_out(p, t, n, v);
+  }
+}
+
 // ============================================================================ pair form
 // Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
 // tiles in flight share rows of x and of W in L2.
@@ -130,7 +214,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
   int* abort_flag = &misc[1];
   uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const uint32_t rank = ptx::cluster_rank();
   const int BN = p.bn;
   const int stage_bytes = lin::kTileBytes + BN * 64, n_stages = p.n_stages;
@@ -175,79 +259,80 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = ptx::l2_evict_last_policy();
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += pairs) {
-        int mt, nt;
-        tile_at(t, mt, nt);
-        const int ym = mt * 256 + (int)rank * 128;
-        const int yn = kGated ? nt * (BN / 2) + (rank ? (int)p.N : 0) : nt * BN + (int)rank * (BN / 2);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol = ptx::l2_evict_last_policy();
+    const uint32_t full0 = ptx::map_to_rank(ptx::smem_u32(full), 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += pairs) {
+      int mt, nt;
+      tile_at(t, mt, nt);
+      const int ym = mt * 256 + (int)rank * 128;
+      const int yn = kGated ? nt * (BN / 2) + (rank ? (int)p.N : 0) : nt * BN + (int)rank * (BN / 2);
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          ok = false;
+          break;
+        }
+        if (ptx::elect_one()) {
           const uint32_t sb = smem_base + stage * stage_bytes;
           if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), 2 * stage_bytes);
-          const uint32_t fb = ptx::map_to_rank(ptx::smem_u32(&full[stage]), 0);
-          ptx::tma_load_2d_pair(sb, &maps.x, kb * lin::kBK, ym, fb, pol);
-          ptx::tma_load_2d_pair(sb + lin::kTileBytes, &maps.w, kb * lin::kBK, yn, fb, pol);
-          if (++stage == n_stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          ptx::tma_load_2d_pair(sb, &maps.x, kb * lin::kBK, ym, full0 + 8 * stage, pol);
+          ptx::tma_load_2d_pair(sb + lin::kTileBytes, &maps.w, kb * lin::kBK, yn, full0 + 8 * stage, pol);
         }
-      }
-      // the last stages: released once their products are done, so that no load is in flight at exit
-      for (int s = 0; ok && s < n_stages; ++s) {
-        ok = wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1;
         }
       }
-      if (!ok && rank == 0)  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
-        for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
     }
+    // the last stages: released once their products are done, so that no load is in flight at exit
+    for (int s = 0; ok && s < n_stages; ++s) {
+      ok = warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+      if (++stage == n_stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok && rank == 0)  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
+      for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       // kind::f16: FP32 accumulator, A and B BF16, M = 256
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+      const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
       int stage = 0;
       uint32_t phase = 0;
       int acc_i = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs) {
         const int buf = acc_i & 1;
-        if (!wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
+        if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
+          if (!warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sb = smem_base + stage * stage_bytes;
-          const uint64_t da = ptx::smem_desc(sb, 16, 1024, ptx::kSwizzle128B);
-          const uint64_t db = ptx::smem_desc(sb + lin::kTileBytes, 16, 1024, ptx::kSwizzle128B);
+          if (ptx::elect_one()) {
+            // the start address is a field of 16-byte units: stages stay below 2^18 bytes
+            const uint64_t da = da0 + (uint32_t)(stage * stage_bytes >> 4), db = da + (lin::kTileBytes >> 4);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) ptx::tc_mma_f16_pair(d, da + 2 * q, db + 2 * q, idesc, (kb > 0 || q > 0) ? 1u : 0u);
-          ptx::tc_commit_pair(ptx::smem_u32(&empty[stage]));
+            for (int q = 0; q < 4; ++q) ptx::tc_mma_f16_pair(d, da + 2 * q, db + 2 * q, idesc, (kb > 0 || q > 0) ? 1u : 0u);
+            ptx::tc_commit_pair(ptx::smem_u32(&empty[stage]));
+            if (kb == KB - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+          }
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
         ++acc_i;
       }
-      ptx::tc_commit_pair(ptx::smem_u32(drain));
+      if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(drain));
       wait_bar_drain(ptx::smem_u32(drain), 0);
     }
     __syncwarp();
@@ -259,7 +344,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
       int mt, nt;
       tile_at(t, mt, nt);
       const int buf = acc_i & 1;
-      if (!warp_wait_bar(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
+      if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
       const int64_t m0 = (int64_t)mt * 256 + rank * 128 + q * 32;  // this warp's rows
@@ -320,7 +405,7 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   constexpr int kCols = kGated ? 64 : 128;  // columns of y per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::stream_arena((int)p.M));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::stream_arena(p.per_sm));
   uint64_t* empty = full + lin::kStreamMaxStages;
   uint64_t* accf = empty + lin::kStreamMaxStages;
   uint64_t* acce = accf + 1;
@@ -331,7 +416,7 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
   int* abort_flag = &misc[1];
   uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const int S = p.split;
   const uint32_t rank = S > 1 ? ptx::cluster_rank() : 0u;
   const int T = (int)p.M, npad = p.bn;
@@ -372,17 +457,17 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   ptx::griddep_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_w = ptx::l2_evict_first_policy(), pol_x = ptx::l2_evict_last_policy();
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += clusters) {
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol_w = ptx::l2_evict_first_policy(), pol_x = ptx::l2_evict_last_policy();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += clusters) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          ok = false;
+          break;
+        }
+        if (ptx::elect_one()) {
           const uint32_t sb = smem_base + stage * stage_bytes, fb = ptx::smem_u32(&full[stage]);
           ptx::mbar_arrive_expect_tx(fb, stage_bytes);
           if constexpr (kGated) {
@@ -392,63 +477,61 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
             ptx::tma_load_2d(sb, &maps.w, kb * lin::kBK, t * 128, fb, pol_w);
           }
           ptx::tma_load_2d(sb + lin::kTileBytes, &maps.x, kb * lin::kBK, 0, fb, pol_x);
-          if (++stage == n_stages) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-      }
-      for (int s = 0; ok && s < n_stages; ++s) {  // no load is in flight at exit
-        ok = wait_bar(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1;
         }
       }
-      if (!ok)  // aborted: let what is in flight land
-        for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
     }
+    for (int s = 0; ok && s < n_stages; ++s) {  // no load is in flight at exit
+      ok = warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+      if (++stage == n_stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok)  // aborted: let what is in flight land
+      for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(npad >> 3) << 17) | ((128u >> 4) << 24);
-      int stage = 0;
-      uint32_t phase = 0, aph = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += clusters) {
-        if (!wait_bar(ptx::smem_u32(acce), aph ^ 1, ctl)) break;
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(npad >> 3) << 17) | ((128u >> 4) << 24);
+    const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
+    int stage = 0;
+    uint32_t phase = 0, aph = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += clusters) {
+      if (!warp_wait_quick(ptx::smem_u32(acce), aph ^ 1, ctl)) break;
+      ptx::tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl)) {
+          ok = false;
+          break;
+        }
         ptx::tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_bar(ptx::smem_u32(&full[stage]), phase, ctl)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t sb = smem_base + stage * stage_bytes;
-          const uint64_t da = ptx::smem_desc(sb, 16, 1024, ptx::kSwizzle128B);
-          const uint64_t db = ptx::smem_desc(sb + lin::kTileBytes, 16, 1024, ptx::kSwizzle128B);
+        if (ptx::elect_one()) {
+          const uint64_t da = da0 + (uint32_t)(stage * stage_bytes >> 4), db = da + (lin::kTileBytes >> 4);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             ptx::tc_mma_f16(tmem_base, da + 2 * q, db + 2 * q, idesc, (kb > kb0 || q > 0) ? 1u : 0u);
           ptx::tc_commit(ptx::smem_u32(&empty[stage]));
-          if (++stage == n_stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          if (kb == kb1 - 1) ptx::tc_commit(ptx::smem_u32(accf));
         }
-        if (!ok) break;
-        ptx::tc_commit(ptx::smem_u32(accf));
-        aph ^= 1;
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      ptx::tc_commit(ptx::smem_u32(drain));
-      wait_bar_drain(ptx::smem_u32(drain), 0);
+      aph ^= 1;
     }
+    if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(drain));
+    wait_bar_drain(ptx::smem_u32(drain), 0);
     __syncwarp();
   } else {
     const int q = warp & 3, ep = threadIdx.x - 64;
     uint32_t ph = 0;
     for (int t = first; t < tiles; t += clusters, ph ^= 1) {
-      bool ok = warp_wait_bar(ptx::smem_u32(accf), ph, ctl);
+      bool ok = warp_wait_quick(ptx::smem_u32(accf), ph, ctl);
       // the partial sums of the tile before have been read by every CTA of the cluster
       if (ok && S > 1) ok = wait_bar_cluster(ptx::smem_u32(pfree), ph ^ 1, ctl);
       if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
@@ -541,32 +624,48 @@ cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, 
 
 // ============================================================================ plan and launch
 void plan_linear(LinearParams& p, int sms) {
+  p.form = kLinearDirect;
+  if (p.M <= kLinearDirectRows) {
+    // one CTA per SM: as many row groups each as that takes (up to 8; then in waves)
+    const int cols = p.act == GMMFR_ACT_SWIGLU ? 8 : 16;
+    const int64_t row_groups = (p.N + cols - 1) / cols;
+    p.group_m = 1;
+    while (p.group_m < 8 && (row_groups + p.group_m - 1) / p.group_m > sms) ++p.group_m;
+    p.grid = (int32_t)((row_groups + p.group_m - 1) / p.group_m);
+    return;
+  }
   const int64_t rows_w = p.act == GMMFR_ACT_SWIGLU ? 2 * p.N : p.N;
   p.KB = (int32_t)((p.K + lin::kBK - 1) / lin::kBK);
   if (p.M <= kLinearStreamRows) {
-    p.stream = 1;
+    p.form = kLinearStream;
     p.bn = (int32_t)((p.M + 15) / 16 * 16);
     p.tiles_m = 1;
     p.tiles_n = (int32_t)(p.act == GMMFR_ACT_SWIGLU ? (p.N + 63) / 64 : (p.N + 127) / 128);
+    // The cluster size and the CTAs per SM that end soonest.  A CTA's rate is its bytes in flight over a round trip
+    // of about 1.4 us (load, product, release), or its share of what HBM or L2 give; about 2 us per wave pass before
+    // the first product and in joining the partial sums.
     const int stage = lin::kTileBytes + p.bn * 128;
-    p.n_stages = std::min<int>(lin::kStreamMaxStages, (lin::stream_arena((int)p.M) - (int)p.M * 512) / stage);
-    // the cluster size that ends soonest: tiles in waves over the CTAs that fit, each a share of the K blocks
-    // and a fixed cost of about six of them
-    const int per_sm = p.M <= 32 ? 2 : 1;
     double best = 1e30;
-    for (int S = 1; S <= 8 && S <= p.KB; S *= 2) {
-      const int64_t slots = std::max<int64_t>(1, per_sm * sms / S);
-      const double waves = (double)((p.tiles_n + slots - 1) / slots);
-      const double t = waves * ((double)((p.KB + S - 1) / S) + 6.0);
-      if (t < best) {
-        best = t;
-        p.split = S;
-        p.grid = (int32_t)(std::min<int64_t>(p.tiles_n, slots) * S);
+    for (int per_sm = 1; per_sm <= 2; ++per_sm) {
+      const int stages = std::min<int>(lin::kStreamMaxStages, (lin::stream_arena(per_sm) - (int)p.M * 512) / stage);
+      if (stages < 2) continue;
+      for (int S = 1; S <= 8 && S <= p.KB; S *= 2) {
+        const int64_t slots = std::max<int64_t>(1, per_sm * sms / S);
+        const int64_t waves = (p.tiles_n + slots - 1) / slots, ctas = std::min<int64_t>(p.tiles_n, slots) * S;
+        const double t_stage = std::max(1.4 / stages, lin::kTileBytes * (double)ctas / 6.7e6);
+        const double t = waves * ((double)((p.KB + S - 1) / S) * t_stage + 2.0);
+        if (t < best) {
+          best = t;
+          p.split = S;
+          p.per_sm = per_sm;
+          p.n_stages = stages;
+          p.grid = (int32_t)ctas;
+        }
       }
     }
     return;
   }
-  p.stream = 0;
+  p.form = kLinearPair;
   const int pairs = sms / 2;
   p.tiles_m = (int32_t)((p.M + 255) / 256);
   // tile width that ends soonest: the products take 2.1 BN cycles per K block, the loads of a CTA's operands
@@ -592,14 +691,14 @@ void plan_linear(LinearParams& p, int sms) {
 
 template <int kAct>
 static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  auto kernel = p.stream ? linear_stream_kernel<kAct> : linear_pair_kernel<kAct>;
-  const int smem = p.stream ? lin::stream_smem((int)p.M) : lin::kPairSmem;
+  auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct> : linear_pair_kernel<kAct>;
+  const int smem = p.form == kLinearStream ? lin::stream_smem(p.per_sm) : lin::kPairSmem;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
     cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         lin::stream_smem(kLinearStreamRows));
+                                         lin::stream_smem(1));
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(linear_pair_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
     if (e != cudaSuccess) return e;
@@ -622,7 +721,25 @@ static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cud
   return cudaLaunchKernelEx(&lc, kernel, maps, p);
 }
 
+static cudaError_t launch_direct(const LinearParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)p.grid);
+  lc.blockDim = dim3(512);
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  const int tiles = p.M <= 8 ? 1 : (p.M <= 16 ? 2 : 4);
+  auto kernel = p.act == GMMFR_ACT_SWIGLU
+                    ? (tiles == 1 ? linear_direct_kernel<true, 1> : (tiles == 2 ? linear_direct_kernel<true, 2> : linear_direct_kernel<true, 4>))
+                    : (tiles == 1 ? linear_direct_kernel<false, 1> : (tiles == 2 ? linear_direct_kernel<false, 2> : linear_direct_kernel<false, 4>));
+  return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
 cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
+  if (p.form == kLinearDirect) return launch_direct(p, s);
   switch (p.act) {
     case GMMFR_ACT_RELU: return launch_one<GMMFR_ACT_RELU>(maps, p, s);
     case GMMFR_ACT_GELU: return launch_one<GMMFR_ACT_GELU>(maps, p, s);

@@ -67,7 +67,9 @@ struct LayerParams {
 cudaError_t launch_layer(const LayerParams& p, int sms, cudaStream_t s);
 int64_t layer_image_bytes(bool mx, int64_t npad);
 
-// Up to this many rows the dense product streams the weights past all of them.
+// The dense product's forms (kernels_linear.cu), and the most rows of x for the first two.
+enum { kLinearDirect = 0, kLinearStream = 1, kLinearPair = 2 };
+constexpr int kLinearDirectRows = 32;
 constexpr int kLinearStreamRows = 128;
 
 struct LinearParams {
@@ -79,9 +81,9 @@ struct LinearParams {
   int32_t act, out_f32;
   int32_t vec_out;  // rows of out and residual on 16-byte boundaries
   // plan_linear's choice
-  int32_t stream;            // few rows: weights streamed past them
+  int32_t form;              // kLinearDirect, ...
   int32_t bn;                // N of the products: rows of x (stream), columns of a tile before gating (pair)
-  int32_t KB, tiles_m, tiles_n, n_stages, split, group_m, grid;
+  int32_t KB, tiles_m, tiles_n, n_stages, split, per_sm, group_m, grid;
 };
 struct LinearMaps {
   CUtensorMap x, w;

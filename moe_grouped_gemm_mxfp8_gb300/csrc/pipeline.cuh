@@ -54,17 +54,41 @@ __device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, con
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// The wait of the kernels with short stages: the timer is read only every 16th failed try, since reading it takes
+// hundreds of cycles, which a wait that is about to end would pay in full.
+struct Deadline {
+  uint64_t t0 = 0;
+  int tries = 0;
+  // false once the limit has passed (or another role aborted)
+  __device__ __forceinline__ bool go_on(const Ctl& c) {
+    if (*c.abort) return false;
+    if ((++tries & 15) == 0) {
+      const uint64_t t = ptx::globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > (uint64_t)c.timeout_ns) {
+        *c.abort = 1;
+        atomicOr(c.err, kErrTimeout);
+        return false;
+      }
+    }
+    return true;
+  }
+};
+__device__ __forceinline__ bool wait_quick(uint32_t bar, uint32_t parity, const Ctl& c) {
+  Deadline d;
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (!d.go_on(c)) return false;
+  return true;
+}
+__device__ __forceinline__ bool warp_wait_quick(uint32_t bar, uint32_t parity, const Ctl& c) {
+  return __all_sync(0xffffffffu, wait_quick(bar, parity, c)) != 0;
+}
+
 // Bounded wait on a barrier that other CTAs of the cluster arrive on, ordering what they wrote.
 __device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, const Ctl& c) {
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait_cluster(bar, parity)) {
-    if (*c.abort) return false;
-    if (ptx::globaltimer() - t0 > (uint64_t)c.timeout_ns) {
-      *c.abort = 1;
-      atomicOr(c.err, kErrTimeout);
-      return false;
-    }
-  }
+  Deadline d;
+  while (!ptx::mbar_try_wait_cluster(bar, parity))
+    if (!d.go_on(c)) return false;
   return true;
 }
 

@@ -68,6 +68,19 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// One thread of a converged warp, always the same one.  The compiler knows the guarded code to be one thread's and
+// keeps the operands of tcgen05 / bulk-copy instructions in uniform registers: in a loop that one lane runs alone,
+// issuing a tcgen05.mma takes about 160 cycles; guarded like this, within a loop of the whole warp, 39 (N = 16).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Barrier `id` over `n` threads (a multiple of 32) of the CTA.
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
