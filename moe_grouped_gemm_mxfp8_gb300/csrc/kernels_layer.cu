@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     // -------------------------------------------------------------- weights
     {
       const uint64_t pol = ptx::l2_evict_first_policy();
+      const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, sb = smem_base;
       bool ok = true;
       while (ok && walk.next()) {
         // the piece's tiles lie in runs of consecutive ones: `src` walks a run of `left` tiles
@@ -439,20 +440,21 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
               left = D - k;
             }
           }
-          if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
             ok = false;
             break;
           }
           if (ptx::elect_one()) {
-            const uint32_t fb = ptx::smem_u32(&full[stage]);
-            ptx::mbar_arrive_expect_tx(fb, tile);
-            ptx::bulk_g2s(smem_base + stage * stage_bytes, src, tile, fb, pol);
+            ptx::mbar_arrive_expect_tx(full0 + 8 * stage, tile);
+            ptx::bulk_g2s(sb, src, tile, full0 + 8 * stage, pol);
           }
           src += tile;
           --left;
+          sb += stage_bytes;
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
+            sb = smem_base;
           }
         }
       }
@@ -471,32 +473,37 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     // -------------------------------------------------------------- the tokens' images
     {
       const uint64_t pol = ptx::l2_evict_last_policy();
+      const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, sb = smem_base + tile;
       bool ok = true, sw_ready = false;
       while (ok && walk.next()) {
-        if (walk.is_down && !sw_ready) {  // every unit of the up runs has stored its sw
+        if (walk.is_down && !sw_ready) {  // every unit of the up run has stored its sw
           ok = __all_sync(0xffffffffu, lane != 0 || wait_count(p.up_done, n_units, ctl)) != 0;
           asm volatile("fence.proxy.async;" ::: "memory");
           sw_ready = true;
           if (!ok) break;
         }
+        // the shared expert's images follow the chosen ones' in the down run, in a buffer of their own
+        const int past = walk.is_down ? (int)walk.k0 - A * p.KB2 : -1;
+        const uint8_t* src = past >= 0 ? p.swimg_s + (int64_t)past * img
+                                       : (walk.is_down ? p.swimg : p.ximg) + (int64_t)walk.k0 * img;
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
-          if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          if (walk.is_down && past < 0 && k == A * p.KB2) src = p.swimg_s;
+          if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
             ok = false;
             break;
           }
-          const uint8_t* src = !walk.is_down   ? p.ximg + (int64_t)k * img
-                               : k < A * p.KB2 ? p.swimg + (int64_t)k * img
-                                               : p.swimg_s + (int64_t)(k - A * p.KB2) * img;
           if (ptx::elect_one()) {
-            const uint32_t fb = ptx::smem_u32(&full[stage]);
-            ptx::mbar_arrive_expect_tx(fb, img);
-            ptx::bulk_g2s(smem_base + stage * stage_bytes + tile, src, img, fb, pol);
+            ptx::mbar_arrive_expect_tx(full0 + 8 * stage, img);
+            ptx::bulk_g2s(sb, src, img, full0 + 8 * stage, pol);
           }
+          src += img;
+          sb += stage_bytes;
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
+            sb = smem_base + tile;
           }
         }
       }
@@ -508,45 +515,51 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
       // kind::f16: FP32 accumulator, BF16 operands; kind::mxf8f6f4: E4M3 operands with E8M0 scales
       const uint32_t idesc = (kMx ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) | ((128u >> 4) << 24) | ((uint32_t)(acc >> 3) << 17);
       const uint32_t sf0 = tmem_base + 2 * acc;
+      // the start address is a field of 16-byte units in the low word: stages stay below 2^18 bytes
       const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
       const uint64_t ds0 = ptx::smem_desc(smem_base + kWTileBytes, 0, 128, ptx::kSwizzleNone);
+      const uint32_t hi = (uint32_t)(da0 >> 32), s_hi = (uint32_t)(ds0 >> 32), s_lo0 = (uint32_t)ds0 - (uint32_t)da0;
+      const uint32_t lo0 = (uint32_t)da0, lo_step = (uint32_t)stage_bytes >> 4;
+      const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
+      constexpr uint32_t kB = layer::rows_off(kMx) >> 4;
       int stage = 0, acc_i = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, lo = lo0;
       bool ok = true;
       while (ok && walk.next()) {
         const int buf = acc_i & 1;
         if (!warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * acc;
+        uint32_t accumulate = 0;
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
-          if (!warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl)) {
+          if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
-            // the start address is a field of 16-byte units: stages stay below 2^18 bytes
-            const uint32_t off = (uint32_t)(stage * stage_bytes) >> 4;
-            const uint64_t da = da0 + off, db = da0 + off + (layer::rows_off(kMx) >> 4);
             if constexpr (!kMx) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                ptx::tc_mma_f16(d, da + 2 * q, db + 2 * q, idesc, (k > (int)walk.k0 || q > 0) ? 1u : 0u);
+                ptx::tc_mma_f16_lo(d, lo + 2 * q, lo + kB + 2 * q, hi, idesc, q > 0 ? 1u : accumulate);
             } else {
               const uint32_t sfa = sf0 + 8 * stage;
-              ptx::tc_cp_sf(sfa, ds0 + off);                         // the weights' scales
-              ptx::tc_cp_sf(sfa + 4, ds0 + off + (kSfChunk >> 4));  // the tokens'
+              ptx::tc_cp_sf_lo(sfa, lo + s_lo0, s_hi);                         // the weights' scales
+              ptx::tc_cp_sf_lo(sfa + 4, lo + s_lo0 + (kSfChunk >> 4), s_hi);  // the tokens'
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                ptx::tc_mma_mxf8(d, da + 2 * q, db + 2 * q, idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29), sfa, sfa + 4,
-                                 (k > (int)walk.k0 || q > 0) ? 1u : 0u);
+                ptx::tc_mma_mxf8_lo(d, lo + 2 * q, lo + kB + 2 * q, hi, idesc | ((uint32_t)q << 4) | ((uint32_t)q << 29), sfa,
+                                    sfa + 4, q > 0 ? 1u : accumulate);
             }
-            ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+            ptx::tc_commit(empty0 + 8 * stage);
             if (k == (int)walk.k1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[buf]));
           }
+          accumulate = 1;
+          lo += lo_step;
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
+            lo = lo0;
           }
         }
         ++acc_i;

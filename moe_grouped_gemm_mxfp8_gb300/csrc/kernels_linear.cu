@@ -123,7 +123,7 @@ __device__ __forceinline__ void add_bias32(const __nv_bfloat16* bias, int64_t n,
 template <bool kGated, int kTiles>
 __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kTok = 8 * kTiles;
-  constexpr int kU = kTiles <= 2 ? 4 : 2;  // blocks of 32 K in flight
+  constexpr int kU = kTiles == 1 ? 4 : (kTiles == 2 ? 2 : 1);  // blocks of 32 K of an operand set
   __shared__ float part[16][16][kTok + 1];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -143,28 +143,44 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
     for (int i = 0; i < kTiles; ++i) xr[i] = p.x + (int64_t)min(8 * i + (lane >> 2), M - 1) * p.ldx;
     float acc[kTiles][4] = {};
     const int64_t blocks = (p.K + 31) / 32;
-    for (int64_t b0 = split; b0 < blocks; b0 += splits * kU) {
+    struct Operands {
       uint4 a[kU], b[kU], x[kU][kTiles];
+    };
+    auto load = [&](Operands& o, int64_t b0) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t k = (b0 + u * splits) * 32 + (lane & 3) * 8;
-        a[u] = b[u] = make_uint4(0, 0, 0, 0);
+        o.a[u] = o.b[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kTiles; ++i) o.x[u][i] = make_uint4(0, 0, 0, 0);
         if (k < p.K) {
-          a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
-          b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
+          o.a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
+          o.b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(xr[i] + k));
+          for (int i = 0; i < kTiles; ++i) o.x[u][i] = __ldg(reinterpret_cast<const uint4*>(xr[i] + k));
         }
       }
+    };
+    auto multiply = [&](const Operands& o) {
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          ptx::mma_16816(acc[i], a[u].x, b[u].x, a[u].y, b[u].y, x[u][i].x, x[u][i].y);
-          ptx::mma_16816(acc[i], a[u].z, b[u].z, a[u].w, b[u].w, x[u][i].z, x[u][i].w);
+          ptx::mma_16816(acc[i], o.a[u].x, o.b[u].x, o.a[u].y, o.b[u].y, o.x[u][i].x, o.x[u][i].y);
+          ptx::mma_16816(acc[i], o.a[u].z, o.b[u].z, o.a[u].w, o.b[u].w, o.x[u][i].z, o.x[u][i].w);
         }
+    };
+    // two sets of operands: one is on its way while the other is multiplied
+    Operands even, odd;
+    const int64_t step = (int64_t)splits * kU;
+    load(even, split);
+    for (int64_t b0 = split; b0 < blocks; b0 += 2 * step) {
+      const bool more = b0 + step < blocks;
+      if (more) load(odd, b0 + step);
+      multiply(even);
+      if (!more) break;
+      if (b0 + 2 * step < blocks) load(even, b0 + 2 * step);
+      multiply(odd);
     }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -199,7 +215,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
 // ============================================================================ pair form
 // Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
 // tiles in flight share rows of x and of W in L2.
-template <int kAct>
+template <int kAct, int kKps>
 __global__ void __launch_bounds__(lin::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
@@ -217,8 +233,9 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const uint32_t rank = ptx::cluster_rank();
   const int BN = p.bn;
-  const int stage_bytes = lin::kTileBytes + BN * 64, n_stages = p.n_stages;
-  const int KB = p.KB;
+  // a stage: kKps K blocks of 64, each 128 rows of x and then BN / 2 rows of W
+  const int block_bytes = lin::kTileBytes + BN * 64, stage_bytes = kKps * block_bytes, n_stages = p.n_stages;
+  const int KB = (p.KB + kKps - 1) / kKps;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
@@ -260,29 +277,33 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
 
   if (warp == 0) {
     const uint64_t pol = ptx::l2_evict_last_policy();
-    const uint32_t full0 = ptx::map_to_rank(ptx::smem_u32(full), 0);
+    const uint32_t full_own = ptx::smem_u32(full), full0 = ptx::map_to_rank(full_own, 0), empty0 = ptx::smem_u32(empty);
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, sb = smem_base;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += pairs) {
       int mt, nt;
       tile_at(t, mt, nt);
       const int ym = mt * 256 + (int)rank * 128;
       const int yn = kGated ? nt * (BN / 2) + (rank ? (int)p.N : 0) : nt * BN + (int)rank * (BN / 2);
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+      for (int kb = 0, x = 0; kb < KB; ++kb, x += kKps * lin::kBK) {
+        if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
           ok = false;
           break;
         }
         if (ptx::elect_one()) {
-          const uint32_t sb = smem_base + stage * stage_bytes;
-          if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), 2 * stage_bytes);
-          ptx::tma_load_2d_pair(sb, &maps.x, kb * lin::kBK, ym, full0 + 8 * stage, pol);
-          ptx::tma_load_2d_pair(sb + lin::kTileBytes, &maps.w, kb * lin::kBK, yn, full0 + 8 * stage, pol);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full_own + 8 * stage, 2 * stage_bytes);
+#pragma unroll
+          for (int i = 0; i < kKps; ++i) {  // past K the loads fill zeros
+            ptx::tma_load_2d_pair(sb + i * block_bytes, &maps.x, x + i * lin::kBK, ym, full0 + 8 * stage, pol);
+            ptx::tma_load_2d_pair(sb + i * block_bytes + lin::kTileBytes, &maps.w, x + i * lin::kBK, yn, full0 + 8 * stage, pol);
+          }
         }
+        sb += stage_bytes;
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1;
+          sb = smem_base;
         }
       }
     }
@@ -301,9 +322,13 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
     if (rank == 0) {
       // kind::f16: FP32 accumulator, A and B BF16, M = 256
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+      // the start address is a field of 16-byte units in the low word: stages stay below 2^18 bytes
       const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
+      const uint32_t lo0 = (uint32_t)da0, desc_hi = (uint32_t)(da0 >> 32);
+      const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
+      const uint32_t lo_step = (uint32_t)stage_bytes >> 4, lo_block = (uint32_t)block_bytes >> 4;
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, lo = lo0;
       int acc_i = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs) {
@@ -311,23 +336,29 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
         if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
+        uint32_t accumulate = 0;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl)) {
+          if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
-            // the start address is a field of 16-byte units: stages stay below 2^18 bytes
-            const uint64_t da = da0 + (uint32_t)(stage * stage_bytes >> 4), db = da + (lin::kTileBytes >> 4);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ptx::tc_mma_f16_pair(d, da + 2 * q, db + 2 * q, idesc, (kb > 0 || q > 0) ? 1u : 0u);
-            ptx::tc_commit_pair(ptx::smem_u32(&empty[stage]));
+            for (int i = 0; i < kKps; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                ptx::tc_mma_f16_pair_lo(d, lo + i * lo_block + 2 * q, lo + i * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi,
+                                        idesc, i + q > 0 ? 1u : accumulate);
+            ptx::tc_commit_pair(empty0 + 8 * stage);
             if (kb == KB - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
           }
+          accumulate = 1;
+          lo += lo_step;
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
+            lo = lo0;
           }
         }
         ++acc_i;
@@ -461,26 +492,27 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
+    uint32_t sb = smem_base;
     for (int t = first; ok && t < tiles; t += clusters) {
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+      const int y = t * (kGated ? 64 : 128), y_up = (int)p.N + t * 64;
+      for (int kb = kb0, x = kb0 * lin::kBK; kb < kb1; ++kb, x += lin::kBK) {
+        if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
           ok = false;
           break;
         }
         if (ptx::elect_one()) {
-          const uint32_t sb = smem_base + stage * stage_bytes, fb = ptx::smem_u32(&full[stage]);
+          const uint32_t fb = full0 + 8 * stage;
           ptx::mbar_arrive_expect_tx(fb, stage_bytes);
-          if constexpr (kGated) {
-            ptx::tma_load_2d(sb, &maps.w, kb * lin::kBK, t * 64, fb, pol_w);
-            ptx::tma_load_2d(sb + 64 * 128, &maps.w, kb * lin::kBK, (int)p.N + t * 64, fb, pol_w);
-          } else {
-            ptx::tma_load_2d(sb, &maps.w, kb * lin::kBK, t * 128, fb, pol_w);
-          }
-          ptx::tma_load_2d(sb + lin::kTileBytes, &maps.x, kb * lin::kBK, 0, fb, pol_x);
+          ptx::tma_load_2d(sb, &maps.w, x, y, fb, pol_w);
+          if constexpr (kGated) ptx::tma_load_2d(sb + 64 * 128, &maps.w, x, y_up, fb, pol_w);
+          ptx::tma_load_2d(sb + lin::kTileBytes, &maps.x, x, 0, fb, pol_x);
         }
+        sb += stage_bytes;
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1;
+          sb = smem_base;
         }
       }
     }
@@ -497,29 +529,34 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   } else if (warp == 1) {
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(npad >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
+    const uint32_t lo0 = (uint32_t)da0, desc_hi = (uint32_t)(da0 >> 32), lo_step = (uint32_t)stage_bytes >> 4;
+    const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
     int stage = 0;
-    uint32_t phase = 0, aph = 0;
+    uint32_t phase = 0, aph = 0, lo = lo0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += clusters) {
       if (!warp_wait_quick(ptx::smem_u32(acce), aph ^ 1, ctl)) break;
       ptx::tc_fence_after();
+      uint32_t accumulate = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl)) {
+        if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint64_t da = da0 + (uint32_t)(stage * stage_bytes >> 4), db = da + (lin::kTileBytes >> 4);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            ptx::tc_mma_f16(tmem_base, da + 2 * q, db + 2 * q, idesc, (kb > kb0 || q > 0) ? 1u : 0u);
-          ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+            ptx::tc_mma_f16_lo(tmem_base, lo + 2 * q, lo + (lin::kTileBytes >> 4) + 2 * q, desc_hi, idesc, q > 0 ? 1u : accumulate);
+          ptx::tc_commit(empty0 + 8 * stage);
           if (kb == kb1 - 1) ptx::tc_commit(ptx::smem_u32(accf));
         }
+        accumulate = 1;
+        lo += lo_step;
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1;
+          lo = lo0;
         }
       }
       aph ^= 1;
@@ -553,32 +590,50 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
         if (ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pready), ep));
         if (!ptx::bar_all(1, 128, wait_bar_cluster(ptx::smem_u32(pready), ph, ctl))) break;
       }
-      // this CTA's share of the tile's T x kCols outputs, columns fastest
-      const int total = T * kCols, lo = (int)((int64_t)total * rank / S), hi = (int)((int64_t)total * (rank + 1) / S);
+      // this CTA's share of the tile's T x kCols outputs, four columns at a time, columns fastest
+      const int total = T * (kCols / 4), lo = (int)((int64_t)total * rank / S), hi = (int)((int64_t)total * (rank + 1) / S);
       for (int i = lo + ep; i < hi; i += 128) {
-        const int tok = i / kCols, c = i - tok * kCols;
+        const int tok = i / (kCols / 4), c = (i - tok * (kCols / 4)) * 4;
         const int64_t n = (int64_t)t * kCols + c;
         if (n >= p.N) continue;
-        float v = 0.f, u = 0.f;
-        if (S > 1) {
-          const uint32_t a = ptx::smem_u32(part + tok * 128 + c);
-          for (int s = 0; s < S; ++s) {
-            const uint32_t b = ptx::map_to_rank(a, s);
-            v += ptx::ld_cluster_f32(b);
-            if constexpr (kGated) u += ptx::ld_cluster_f32(b + 64 * 4);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
+        const uint32_t a = ptx::smem_u32(part + tok * 128 + c);
+#pragma unroll 4
+        for (int s = 0; s < S; ++s) {
+          const uint32_t b = S > 1 ? ptx::map_to_rank(a, s) : a;
+          const float4 w = ptx::ld_cluster_v4(b);
+          v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+          if constexpr (kGated) {
+            const float4 z = ptx::ld_cluster_v4(b + 64 * 4);
+            u = make_float4(u.x + z.x, u.y + z.y, u.z + z.z, u.w + z.w);
           }
-        } else {
-          v = part[tok * 128 + c];
-          if constexpr (kGated) u = part[tok * 128 + 64 + c];
         }
-        if (p.bias) v += __bfloat162float(p.bias[n]);
-        if constexpr (kGated) {
-          if (p.bias) u += __bfloat162float(p.bias[p.N + n]);
-          v = silu(v) * u;
-        } else {
-          v = activate(kAct, v);
+        float f[4] = {v.x, v.y, v.z, v.w};
+        const float g[4] = {u.x, u.y, u.z, u.w};
+        const int cols = p.N - n < 4 ? (int)(p.N - n) : 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < cols) {
+            if (p.bias) f[k] += __bfloat162float(p.bias[n + k]);
+            if constexpr (kGated) f[k] = silu(f[k]) * (p.bias ? g[k] + __bfloat162float(p.bias[p.N + n + k]) : g[k]);
+            else f[k] = activate(kAct, f[k]);
+          }
         }
-        store_out(p, tok, n, v);
+        if (p.vec_out && cols == 4) {
+          if (p.residual) {
+            const uint2 r = *reinterpret_cast<const uint2*>(p.residual + tok * p.ldr + n);
+            f[0] += bf16_lo(r.x);
+            f[1] += bf16_hi(r.x);
+            f[2] += bf16_lo(r.y);
+            f[3] += bf16_hi(r.y);
+          }
+          if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tok * p.ldo + n) = make_float4(f[0], f[1], f[2], f[3]);
+          else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + tok * p.ldo + n) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < cols) store_out(p, tok, n + k, f[k]);
+        }
       }
       ptx::bar_sync(1, 128);
       if (S > 1 && ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pfree), ep));
@@ -683,7 +738,8 @@ void plan_linear(LinearParams& p, int sms) {
     }
   }
   if (p.act == GMMFR_ACT_SWIGLU) p.tiles_n = (int32_t)((p.N + p.bn / 2 - 1) / (p.bn / 2));
-  p.n_stages = std::min<int>(lin::kPairMaxStages, lin::kPairArena / (lin::kTileBytes + p.bn * 64));
+  p.kps = p.bn <= 128 && p.KB > 1 ? 2 : 1;
+  p.n_stages = std::min<int>(lin::kPairMaxStages, lin::kPairArena / (p.kps * (lin::kTileBytes + p.bn * 64)));
   p.group_m = 8;
   p.grid = (int32_t)(2 * std::min<int64_t>(pairs, (int64_t)p.tiles_m * p.tiles_n));
   p.split = 2;
@@ -691,7 +747,8 @@ void plan_linear(LinearParams& p, int sms) {
 
 template <int kAct>
 static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct> : linear_pair_kernel<kAct>;
+  auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct>
+                                        : (p.kps == 1 ? linear_pair_kernel<kAct, 1> : linear_pair_kernel<kAct, 2>);
   const int smem = p.form == kLinearStream ? lin::stream_smem(p.per_sm) : lin::kPairSmem;
   static int configured_device = -1;
   int dev = 0;
@@ -700,7 +757,9 @@ static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cud
     cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          lin::stream_smem(1));
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
