@@ -36,6 +36,18 @@ gmmfr_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   return GMMFR_OK;
 }
 
+// [rows, K] BF16 with boxes of `box_rows` rows of 64 elements (128 bytes, 128-byte swizzle)
+bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const void* base, int64_t rows, int64_t K,
+                 int64_t ld, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : cdiv(K, 8) * 8) * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- gate
 gmmfr_status validate_gate(const gmmfr_gate_problem* p) {
   if (!p) return fail(GMMFR_ERR_INVALID_ARG, "problem is NULL");
@@ -66,9 +78,7 @@ gmmfr_status validate_gate(const gmmfr_gate_problem* p) {
   return GMMFR_OK;
 }
 
-size_t gate_ws_bytes(const gmmfr_gate_problem* p) {
-  return p->T <= gmmfr::kGateClusterTokens ? 256 : align256(sizeof(float) * (size_t)p->T * p->E);
-}
+size_t gate_ws_bytes(const gmmfr_gate_problem*) { return gmmfr::kHdrBytes; }
 
 gmmfr::GateParams gate_params(const gmmfr_gate_problem& p, const void* x, const void* weight, const float* select_bias) {
   gmmfr::GateParams g{};
@@ -197,18 +207,6 @@ LinearLayout linear_layout(const gmmfr_linear_problem* p) {
   return L;
 }
 
-// [rows, K] BF16 with boxes of `box_rows` rows of 64 elements (128 bytes, 128-byte swizzle)
-bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const void* base, int64_t rows, int64_t K,
-                 int64_t ld, int box_rows) {
-  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : cdiv(K, 8) * 8) * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 extern "C" {
@@ -234,11 +232,20 @@ gmmfr_status gmmfr_moe_gate(const gmmfr_gate_problem* problem, const void* x, co
     return fail(GMMFR_ERR_INVALID_ARG, "an input or output is not aligned to its element size");
   if (gmmfr_status st = check_workspace(workspace, workspace_bytes, gate_ws_bytes(problem))) return st;
   gmmfr::GateParams g = gate_params(p, x, weight, select_bias);
-  g.logits = logits || p.T <= gmmfr::kGateClusterTokens ? logits : static_cast<float*>(workspace);
+  g.logits = logits;
   g.ids = topk_ids;
   g.weights = topk_weights;
   g.ids_i64 = p.ids_type == GMMFR_INDEX_I64;
-  cudaError_t e = gmmfr::launch_gate(g, static_cast<cudaStream_t>(stream));
+  g.hdr = static_cast<uint32_t*>(workspace);
+  g.timeout_ns = 4000000000ll;
+  gmmfr::GateMaps maps;
+  if (gmmfr::plan_gate(g, gmmfr::sm_count())) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    if (!encode_rows(encode, &maps.x, x, p.T, p.H, g.ldx, 128) || !encode_rows(encode, &maps.w, weight, p.E, p.H, p.H, g.bn / 2))
+      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  }
+  cudaError_t e = gmmfr::launch_gate(maps, g, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gate launch");
   return GMMFR_OK;
 }

@@ -1,109 +1,440 @@
 // The router: logits = x W^T (FP32 sums of BF16 products), then the selection of each token.
-//   gate_logits  one warp per (expert, up to 8 tokens): the weight row is read once for them
-//   gate_select  one warp per token (gate_select.cuh)
+//   cluster  few tokens: clusters of 8 CTAs for 8 tokens each (gate_select.cuh)
+//   pair     many tokens: CTA pairs take 256 tokens against all experts (tcgen05, cta_group::2), and the selection
+//            reads the logits where they are, in TMEM: a token is a TMEM lane, so a thread walks its token's
+//            columns and keeps the best in registers.  Four threads share a token, a quarter of the columns each.
 #include "gate_select.cuh"
 #include "ops.cuh"
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace gmmfr {
 
-namespace {
-constexpr int kGateTok = 8;  // tokens a warp carries through one weight row
+namespace gate {
+constexpr int kPairThreads = 64 + 512;  // warp 0 TMA, warp 1 MMA, 16 epilogue warps
+constexpr int kArena = 160 * 1024;
+constexpr int kMaxStages = 8;
+constexpr int kTop = 8;  // the pair form's longest choice
+constexpr int kBars = 2 * kMaxStages + 5;
+constexpr int kMiscOff = kArena + kBars * 8 + 8;
+constexpr int kBiasOff = kMiscOff + 32;                  // float bias[512]
+constexpr int kStatOff = kBiasOff + 512 * 4;             // float [2][4][128]: maxima, sums
+constexpr int kExchOff = kStatOff + 2 * 4 * 128 * 4;     // group keys [64][128], then lists [3][8][3][128] (uint32)
+constexpr int kPairSmem = kExchOff + 3 * kTop * 3 * 128 * 4 + 1024;
+static_assert(64 <= 3 * kTop * 3 && kPairSmem <= 232448, "shared memory");
+}  // namespace gate
 
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-}  // namespace
-
-__global__ void __launch_bounds__(256) gate_logits_kernel(GateParams p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t e = (int64_t)blockIdx.x * 8 + warp;
-  const int64_t t0 = (int64_t)blockIdx.y * kGateTok;
-  if (e >= p.rule.E) return;
-  float acc[kGateTok] = {};
-  for (int64_t h = lane * 8; h < p.H; h += 256) {
-    float w[8];
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.weight + e * p.H + h), w);
-#pragma unroll
-    for (int i = 0; i < kGateTok; ++i) {
-      if (t0 + i < p.T) {
-        float x[8];
-        bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.x + (t0 + i) * p.ldx + h), x);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) acc[i] = fmaf(w[q], x[q], acc[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kGateTok; ++i) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    if (lane == 0 && t0 + i < p.T) p.logits[(t0 + i) * p.rule.E + e] = acc[i];
-  }
-}
-
-template <int kPer>
-__global__ void __launch_bounds__(128) gate_select_kernel(GateParams p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * 4 + warp;
-  if (t >= p.T) return;
-  int id;
-  float w;
-  gate_select_warp<kPer>(p.rule, p.logits + t * p.rule.E, p.select_bias, lane, id, w);
-  if (lane < p.rule.topk) {
-    const int64_t o = t * p.rule.topk + lane;
-    if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = id;
-    else static_cast<int32_t*>(p.ids)[o] = id;
-    p.weights[o] = w;
-  }
-}
-
+// ============================================================================ cluster form
 __global__ void __launch_bounds__(gate::kThreads) gate_cluster_kernel(const __grid_constant__ GateParams p) {
   __shared__ gate::Smem sm;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {  // no wait here can give up
+    p.hdr[0] = 1;
+    p.hdr[1] = 0;
+  }
   gate_cluster(p, (int64_t)(blockIdx.x / gate::kCluster) * gate::kTok, sm, ptx::cluster_rank());
 }
 
-cudaError_t launch_gate(const GateParams& p, cudaStream_t s) {
-  if (p.T == 0) return cudaSuccess;
-  if (p.T <= kGateClusterTokens) {
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = gate::kCluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 2;
-    lc.stream = s;
+// ============================================================================ pair form
+// kBlocks: experts in blocks of 256 (1 or 2).  Accumulators: kBlocks x 256 TMEM columns, double-buffered when one block.
+template <int kBlocks>
+__global__ void __launch_bounds__(gate::kPairThreads, 1)
+    gate_pair_kernel(const __grid_constant__ GateMaps maps, const __grid_constant__ GateParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + gate::kArena);  // used in rank 0: both CTAs' loads
+  uint64_t* empty = full + gate::kMaxStages;
+  uint64_t* accf = empty + gate::kMaxStages;
+  uint64_t* acce = accf + 2;  // used in rank 0: both CTAs' epilogue warps
+  uint64_t* drain = acce + 2;
+  int32_t* misc = reinterpret_cast<int32_t*>(smem + gate::kMiscOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
+  int* abort_flag = &misc[1];
+  uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
+  float* s_bias = reinterpret_cast<float*>(smem + gate::kBiasOff);
+  float* s_stat = reinterpret_cast<float*>(smem + gate::kStatOff);
+  uint32_t* s_exch = reinterpret_cast<uint32_t*>(smem + gate::kExchOff);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
+  const uint32_t rank = ptx::cluster_rank();
+  const GateRule& r = p.rule;
+  const int E = r.E, BN = p.bn;
+  constexpr int kXBytes = 128 * 128;
+  const int block_bytes = BN * 64, stage_bytes = kXBytes + kBlocks * block_bytes, n_stages = p.n_stages, KB = p.KB;
+  constexpr int kBufs = kBlocks == 1 ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < n_stages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&acce[b]), 32);
+    }
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    *abort_flag = 0;
+    *s_err = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane < 2) ptx::prefetch_tensormap(lane ? &maps.w : &maps.x);
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::griddep_wait();
+  for (int e = threadIdx.x; e < 512; e += gate::kPairThreads) s_bias[e] = p.select_bias && e < E ? p.select_bias[e] : 0.f;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  ptx::griddep_launch_dependents();
+  const uint32_t tmem_base = *tmem_slot;
+  const Ctl ctl{abort_flag, s_err, p.timeout_ns};
+  const uint32_t smem_base = ptx::smem_u32(smem);
+  const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+  const int tiles = (int)((p.T + 255) / 256);
+
+  if (warp == 0) {
+    const uint64_t pol_x = ptx::l2_evict_first_policy(), pol_w = ptx::l2_evict_last_policy();
+    const uint32_t full_own = ptx::smem_u32(full), full0 = ptx::map_to_rank(full_own, 0), empty0 = ptx::smem_u32(empty);
+    int stage = 0;
+    uint32_t phase = 0, sb = smem_base;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += pairs) {
+      const int ym = t * 256 + (int)rank * 128, yn = (int)rank * (BN / 2);
+      for (int kb = 0, x = 0; kb < KB; ++kb, x += 64) {
+        if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
+          ok = false;
+          break;
+        }
+        if (ptx::elect_one()) {
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full_own + 8 * stage, 2 * stage_bytes);
+          ptx::tma_load_2d_pair(sb, &maps.x, x, ym, full0 + 8 * stage, pol_x);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            ptx::tma_load_2d_pair(sb + kXBytes + b * block_bytes, &maps.w, x, yn + b * 256, full0 + 8 * stage, pol_w);
+        }
+        sb += stage_bytes;
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+          sb = smem_base;
+        }
+      }
+    }
+    for (int s = 0; ok && s < n_stages; ++s) {  // no load is in flight at exit
+      ok = warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl);
+      if (++stage == n_stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok && rank == 0)  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
+      for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+      const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
+      const uint32_t lo0 = (uint32_t)da0, desc_hi = (uint32_t)(da0 >> 32);
+      const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
+      const uint32_t lo_step = (uint32_t)stage_bytes >> 4, lo_block = (uint32_t)block_bytes >> 4;
+      int stage = 0, acc_i = 0;
+      uint32_t phase = 0, lo = lo0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs) {
+        const int buf = acc_i % kBufs;
+        if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i / kBufs) & 1) ^ 1, ctl))) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + buf * 256;
+        uint32_t accumulate = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                ptx::tc_mma_f16_pair_lo(d + b * 256, lo + 2 * q, lo + (kXBytes >> 4) + b * lo_block + 2 * q, desc_hi, idesc,
+                                        q > 0 ? 1u : accumulate);
+            ptx::tc_commit_pair(empty0 + 8 * stage);
+            if (kb == KB - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+          }
+          accumulate = 1;
+          lo += lo_step;
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+            lo = lo0;
+          }
+        }
+        ++acc_i;
+      }
+      if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(drain));
+      wait_bar_drain(ptx::smem_u32(drain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ selection
+    const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant; quarter of the columns
+    const int tok = q * 32 + lane;                   // token of this CTA's half of the tile, and exchange column
+    const int chunks = (E + 15) / 16, c_lo = chunks * part / 4, c_hi = chunks * (part + 1) / 4;
+    const float kNegInf = __int_as_float(0xff800000);
+    const bool softmax = !r.sigmoid, grouped = r.n_group > 1;
+    const int per = E / r.n_group;
+    auto quadrant_sync = [&]() { ptx::bar_sync(1 + q, 128); };  // the four warps that share this quadrant's tokens
+    int acc_i = 0;
+    for (int t = first; t < tiles; t += pairs) {
+      const int buf = acc_i % kBufs;
+      const bool ok = wait_quick(ptx::smem_u32(&accf[buf]), (acc_i / kBufs) & 1, ctl);
+      if (!ptx::bar_all(1 + q, 128, ok)) break;  // the four leave together
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
+      const int64_t token = (int64_t)t * 256 + rank * 128 + tok;
+      // columns past E are experts that do not exist (zero rows of W): skipped everywhere below
+      float mx = kNegInf;
+      if (softmax || p.logits) {
+        for (int c = c_lo; c < c_hi; ++c) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (c * 16 + j < E) {
+              mx = fmaxf(mx, __uint_as_float(v[j]));
+              if (p.logits && token < p.T) p.logits[token * E + c * 16 + j] = __uint_as_float(v[j]);
+            }
+          }
+        }
+      }
+      float sum = 1.f;
+      bool none = false;  // logits that are all -inf leave nothing to weigh
+      if (softmax) {
+        s_stat[part * 128 + tok] = mx;
+        quadrant_sync();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, s_stat[k * 128 + tok]);
+        sum = 0.f;
+        for (int c = c_lo; c < c_hi; ++c) {  // exponentials, kept in place of the logits
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float l = __uint_as_float(v[j]);
+            const float e = mx == kNegInf ? (l != l ? l : 0.f) : expf(l - mx);
+            if (c * 16 + j < E) sum += e;
+            v[j] = __float_as_uint(e);
+          }
+          ptx::tmem_st_32x32b_x16(taddr + c * 16, v);
+        }
+        s_stat[(4 + part) * 128 + tok] = sum;
+      } else {
+        for (int c = c_lo; c < c_hi; ++c) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(1.0f / (1.0f + expf(-__uint_as_float(v[j]))));
+          ptx::tmem_st_32x32b_x16(taddr + c * 16, v);
+        }
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      quadrant_sync();
+      ptx::tc_fence_after();
+      if (softmax) {
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += s_stat[(4 + k) * 128 + tok];
+        none = mx == kNegInf && sum == 0.f;
+      }
+      auto probability = [&](uint32_t v) {
+        const float f = __uint_as_float(v);
+        return softmax ? (none ? 0.f : f / sum) : f;
+      };
+      uint64_t eligible = ~0ull;
+      if (grouped) {
+        for (int g = part; g < r.n_group; g += 4) {  // this quarter's share of the groups
+          uint32_t a = 0, b = 0;                     // the two highest keys
+          const int lo = g * per, hi = lo + per;
+          for (int c = lo >> 4; c * 16 < hi; ++c) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int e = c * 16 + j;
+              if (e >= lo && e < hi) {
+                const uint32_t k = order_key(probability(v[j]) + s_bias[e]);
+                b = max(b, min(a, k));
+                a = max(a, k);
+              }
+            }
+          }
+          float s = a > 1u ? key_value(a) : kNegInf;
+          if (r.group_top == 2) s += b > 1u ? key_value(b) : kNegInf;
+          s_exch[g * 128 + tok] = order_key(s);
+        }
+        quadrant_sync();
+        eligible = 0;
+        for (int g = 0; g < r.n_group; ++g) {  // fewer than topk_group groups better, or equal and earlier
+          const uint32_t mine = s_exch[g * 128 + tok];
+          int better = 0;
+          for (int h = 0; h < r.n_group; ++h) {
+            const uint32_t o = s_exch[h * 128 + tok];
+            better += (o > mine || (o == mine && h < g)) ? 1 : 0;
+          }
+          if (better < r.topk_group) eligible |= 1ull << g;
+        }
+        quadrant_sync();  // the lists take the keys' place
+      }
+      // the best kTop of this quarter's columns, in descending order: a column enters in front of what it exceeds,
+      // so equal scores keep the order of their indices
+      uint32_t key[gate::kTop], idx[gate::kTop];
+      float pr[gate::kTop];
+#pragma unroll
+      for (int k = 0; k < gate::kTop; ++k) {
+        key[k] = 0;
+        idx[k] = 0;
+        pr[k] = 0.f;
+      }
+      auto enter = [&](uint32_t nk, uint32_t ni, float np) {
+        bool above[gate::kTop];
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) above[k] = nk > key[k];
+#pragma unroll
+        for (int k = gate::kTop - 1; k > 0; --k) {
+          key[k] = above[k] ? (above[k - 1] ? key[k - 1] : nk) : key[k];
+          idx[k] = above[k] ? (above[k - 1] ? idx[k - 1] : ni) : idx[k];
+          pr[k] = above[k] ? (above[k - 1] ? pr[k - 1] : np) : pr[k];
+        }
+        key[0] = above[0] ? nk : key[0];
+        idx[0] = above[0] ? ni : idx[0];
+        pr[0] = above[0] ? np : pr[0];
+      };
+      int g = grouped ? c_lo * 16 / per : 0, g_end = grouped ? (g + 1) * per : E;  // the column's group
+      for (int c = c_lo; c < c_hi; ++c) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int e = c * 16 + j;
+          if (e >= E) break;
+          if (e >= g_end) {
+            ++g;
+            g_end += per;
+          }
+          const float pv = probability(v[j]);
+          const uint32_t k = (eligible >> g) & 1 ? order_key(pv + s_bias[e]) : 0u;
+          if (k > key[gate::kTop - 1]) enter(k, (uint32_t)e, pv);
+        }
+      }
+      // TMEM is read: the next tile's products may overwrite it
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[buf]), 0));
+      if (part > 0) {
+        uint32_t* o = s_exch + (part - 1) * gate::kTop * 3 * 128 + tok;
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) {
+          o[(3 * k) * 128] = key[k];
+          o[(3 * k + 1) * 128] = idx[k];
+          o[(3 * k + 2) * 128] = __float_as_uint(pr[k]);
+        }
+      }
+      quadrant_sync();
+      if (part == 0) {
+        for (int h = 0; h < 3; ++h) {
+          const uint32_t* o = s_exch + h * gate::kTop * 3 * 128 + tok;
+          for (int k = 0; k < gate::kTop; ++k) {
+            const uint32_t nk = o[(3 * k) * 128];
+            if (nk <= key[gate::kTop - 1]) break;  // the rest of that list is no better
+            enter(nk, o[(3 * k + 1) * 128], __uint_as_float(o[(3 * k + 2) * 128]));
+          }
+        }
+        if (token < p.T) {
+          float total = 0.f;
+#pragma unroll
+          for (int k = 0; k < gate::kTop; ++k) total += k < r.topk ? pr[k] : 0.f;
+#pragma unroll
+          for (int k = 0; k < gate::kTop; ++k) {
+            if (k < r.topk) {
+              const int64_t o = token * r.topk + k;
+              if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = idx[k];
+              else static_cast<int32_t*>(p.ids)[o] = (int32_t)idx[k];
+              p.weights[o] = (r.renormalise ? pr[k] / (total + 1e-20f) : pr[k]) * r.scale;
+            }
+          }
+        }
+      }
+      quadrant_sync();  // the exchange is written again
+      ++acc_i;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (rank == 1 && threadIdx.x == 0) wait_bar_drain(ptx::smem_u32(drain), 0);  // rank 0's last arrival here
+  __syncthreads();
+  ptx::cluster_sync();  // the other CTA's products read this one's shared memory, its epilogue arrives here
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, 512);
+  }
+  if (threadIdx.x == 0) {
+    p.hdr[1 + blockIdx.x] = *s_err;
+    if (blockIdx.x == 0) p.hdr[0] = gridDim.x;
+  }
+}
+
+// ============================================================================ plan and launch
+bool plan_gate(GateParams& p, int sms) {
+  p.pair = p.T > kGateClusterTokens && p.rule.E <= 512 && p.rule.topk <= gate::kTop;
+  if (!p.pair) return false;
+  p.bn = p.rule.E <= 256 ? (p.rule.E + 31) / 32 * 32 : 256;
+  p.KB = (int32_t)((p.H + 63) / 64);
+  const int stage = 128 * 128 + (p.rule.E <= 256 ? 1 : 2) * p.bn * 64;
+  p.n_stages = gate::kArena / stage < gate::kMaxStages ? gate::kArena / stage : gate::kMaxStages;
+  const int64_t tiles = (p.T + 255) / 256;
+  p.grid = (int32_t)(2 * (tiles < sms / 2 ? tiles : sms / 2));
+  return true;
+}
+
+cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.pair ? 2 : gate::kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  lc.stream = s;
+  if (!p.pair) {
     lc.gridDim = dim3((unsigned)((p.T + gate::kTok - 1) / gate::kTok * gate::kCluster));
     lc.blockDim = dim3(gate::kThreads);
     return cudaLaunchKernelEx(&lc, gate_cluster_kernel, p);
   }
-  const int64_t per_launch = (int64_t)65535 * kGateTok;  // grid.y limit
-  for (int64_t t = 0; t < p.T; t += per_launch) {
-    GateParams q = p;
-    q.x += t * p.ldx;
-    q.logits += t * p.rule.E;
-    q.T = p.T - t < per_launch ? p.T - t : per_launch;
-    gate_logits_kernel<<<dim3((unsigned)((p.rule.E + 7) / 8), (unsigned)((q.T + kGateTok - 1) / kGateTok)), 256, 0, s>>>(q);
-    if (cudaError_t e = cudaGetLastError()) return e;
+  static int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    for (auto k : {gate_pair_kernel<1>, gate_pair_kernel<2>})
+      if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, gate::kPairSmem)) return e;
+    configured_device = dev;
   }
-  const unsigned grid = (unsigned)((p.T + 3) / 4);
-  if (p.rule.E <= 32) gate_select_kernel<1><<<grid, 128, 0, s>>>(p);
-  else if (p.rule.E <= 64) gate_select_kernel<2><<<grid, 128, 0, s>>>(p);
-  else if (p.rule.E <= 128) gate_select_kernel<4><<<grid, 128, 0, s>>>(p);
-  else if (p.rule.E <= 256) gate_select_kernel<8><<<grid, 128, 0, s>>>(p);
-  else if (p.rule.E <= 512) gate_select_kernel<16><<<grid, 128, 0, s>>>(p);
-  else gate_select_kernel<32><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  lc.gridDim = dim3((unsigned)p.grid);
+  lc.blockDim = dim3(gate::kPairThreads);
+  lc.dynamicSmemBytes = gate::kPairSmem;
+  return cudaLaunchKernelEx(&lc, p.rule.E <= 256 ? gate_pair_kernel<1> : gate_pair_kernel<2>, maps, p);
 }
 
 }  // namespace gmmfr

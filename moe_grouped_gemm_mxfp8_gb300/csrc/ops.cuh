@@ -13,7 +13,7 @@ int sm_count();
 constexpr int kMaxTopk = 32;
 constexpr int kMaxGroups = 64;
 constexpr int kLayerMaxTokens = 64;
-constexpr int kGateClusterTokens = 512;  // the router up to here: clusters of 8 CTAs, 8 tokens each
+constexpr int kGateClusterTokens = 512;  // the router up to here: clusters of 8 CTAs for 8 tokens each
 
 // The router's rule (gmmfr_gate_problem).
 struct GateRule {
@@ -28,14 +28,22 @@ struct GateParams {
   const __nv_bfloat16* x;       // [T, H], row stride ldx
   const __nv_bfloat16* weight;  // [E, H]
   const float* select_bias;     // [E] or null
-  float* logits;                // [T, E] or null (up to kGateClusterTokens tokens)
+  float* logits;                // [T, E] or null
   void* ids;                    // [T, topk] int32 or int64
   float* weights;               // [T, topk]
   int64_t T, H, ldx;
   int32_t ids_i64;
   GateRule rule;
+  uint32_t* hdr;       // error words (pair form)
+  int64_t timeout_ns;
+  // plan_gate's choice
+  int32_t pair, bn, KB, n_stages, grid;
 };
-cudaError_t launch_gate(const GateParams& p, cudaStream_t s);
+struct GateMaps {
+  CUtensorMap x, w;
+};
+bool plan_gate(GateParams& p, int sms);  // whether the pair form is taken (it needs the maps)
+cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t s);
 
 // Grouped FFN weights in MXFP8 tiles (kernels_layer.cu)
 struct FfnPrepMxParams {
