@@ -55,8 +55,9 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    const float inv = mx == kNegInf && sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) p[i] = mx == kNegInf && sum == 0.f ? 0.f : p[i] / sum;
+    for (int i = 0; i < kPer; ++i) p[i] *= inv;
   }
   uint32_t key[kPer];
 #pragma unroll
@@ -132,24 +133,26 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
   w_out *= r.scale;
 }
 
-// ---------------------------------------------------------------- the router for up to 8 tokens by one cluster
-// A cluster of 8 CTAs takes 8 tokens: CTA c computes the logits of expert groups c, c + 8, ... (16 experts each, the
-// 16 warps splitting groups and the K range), sends token i's to CTA i, which selects for it.  The weight rows are
-// read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows l / 4 and
-// l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike, which
-// leaves the sums alone), so each row is read in 16-byte pieces with no staging.
+// ---------------------------------------------------------------- the router for a few tokens by one cluster
+// A cluster of 8 CTAs takes 8 kTiles tokens: CTA c computes the logits of expert groups c, c + 8, ... (16 experts each,
+// the 16 warps splitting groups and the K range), sends tokens c * kTiles ... to CTA c, which selects for them.  The
+// weight rows are read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows
+// l / 4 and l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike,
+// which leaves the sums alone), so each row is read in 16-byte pieces with no staging.
 namespace gate {
 constexpr int kCluster = 8;
-constexpr int kTok = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+template <int kTiles>
 struct Smem {
-  float part[kWarps][16][8];    // a warp's sums
-  float logits[kMaxExperts];    // of the token this CTA selects for
+  float part[kWarps][16][8 * kTiles + 1];   // a warp's sums
+  float logits[kTiles][kMaxExperts];        // of the tokens this CTA selects for
 };
 }  // namespace gate
 
-__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem& sm, uint32_t rank) {
+template <int kTiles>
+__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem<kTiles>& sm, uint32_t rank) {
+  constexpr int kTok = 8 * kTiles;
   ptx::cluster_arrive_relaxed();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.rule.E, groups = (E + 15) / 16;
@@ -160,61 +163,77 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
   if (split < splits && grp < groups) {
     // rows past the end repeat the last one; what they give is not read
     const int ea = min(grp * 16 + (lane >> 2), E - 1), eb = min(grp * 16 + 8 + (lane >> 2), E - 1);
-    const int64_t t = t0 + (lane >> 2) < p.T ? t0 + (lane >> 2) : p.T - 1;
     const __nv_bfloat16* wa = p.weight + (int64_t)ea * p.H;
     const __nv_bfloat16* wb = p.weight + (int64_t)eb * p.H;
-    const __nv_bfloat16* xr = p.x + t * p.ldx;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const __nv_bfloat16* xr[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int64_t t = t0 + 8 * i + (lane >> 2);
+      xr[i] = p.x + (t < p.T ? t : p.T - 1) * p.ldx;
+    }
+    float acc[kTiles][4] = {};
     const int blocks = (int)((p.H + 31) / 32);
-    constexpr int kU = 4;  // blocks of 32 K in flight
+    constexpr int kU = kTiles == 1 ? 4 : 2;  // blocks of 32 K in flight
     for (int b0 = split; b0 < blocks; b0 += splits * kU) {
-      uint4 a[kU], b[kU], x[kU];
+      uint4 a[kU], b[kU], x[kU][kTiles];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t k = (int64_t)(b0 + u * splits) * 32 + (lane & 3) * 8;
-        a[u] = b[u] = x[u] = make_uint4(0, 0, 0, 0);
+        a[u] = b[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
         if (k < p.H) {
           a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
           b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
-          x[u] = *reinterpret_cast<const uint4*>(xr + k);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(xr[i] + k));
         }
       }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        ptx::mma_16816(acc, a[u].x, b[u].x, a[u].y, b[u].y, x[u].x, x[u].y);
-        ptx::mma_16816(acc, a[u].z, b[u].z, a[u].w, b[u].w, x[u].z, x[u].w);
-      }
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          ptx::mma_16816(acc[i], a[u].x, b[u].x, a[u].y, b[u].y, x[u][i].x, x[u][i].y);
+          ptx::mma_16816(acc[i], a[u].z, b[u].z, a[u].w, b[u].w, x[u][i].z, x[u][i].w);
+        }
     }
-    float* d = &sm.part[warp][lane >> 2][(lane & 3) * 2];
-    d[0] = acc[0];
-    d[1] = acc[1];
-    d[64] = acc[2];
-    d[65] = acc[3];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      float* d = &sm.part[warp][lane >> 2][8 * i + (lane & 3) * 2];
+      d[0] = acc[i][0];
+      d[1] = acc[i][1];
+      d[8 * (kTok + 1)] = acc[i][2];
+      d[8 * (kTok + 1) + 1] = acc[i][3];
+    }
   }
   ptx::cluster_wait();  // the other CTAs have started: their shared memory may be written
   __syncthreads();
-  for (int i = tid; i < per_cta * 128; i += gate::kThreads) {
-    const int g = i >> 7, r = (i >> 3) & 15, tok = i & 7;
+  for (int i = tid; i < per_cta * 16 * kTok; i += gate::kThreads) {
+    const int g = i / (16 * kTok), tok = i / 16 % kTok, r = i & 15;
     const int e = ((int)rank + gate::kCluster * g) * 16 + r;
     if (e < E && t0 + tok < p.T) {
       float s = 0.f;
+#pragma unroll 4
       for (int k = 0; k < splits; ++k) s += sm.part[k * per_cta + g][r][tok];
-      ptx::st_cluster_f32(ptx::map_to_rank(ptx::smem_u32(&sm.logits[e]), (uint32_t)tok), s);
+      ptx::st_cluster_f32(ptx::map_to_rank(ptx::smem_u32(&sm.logits[tok % kTiles][e]), (uint32_t)(tok / kTiles)), s);
     }
   }
   ptx::cluster_sync();
-  const int64_t t = t0 + rank;
-  if (t >= p.T) return;
-  if (p.logits)
-    for (int e = tid; e < E; e += gate::kThreads) p.logits[t * E + e] = sm.logits[e];
-  if (warp == 0) {
+  const int64_t t = t0 + rank * kTiles;
+  if (p.logits) {
+    for (int i = 0; i < kTiles; ++i)
+      if (t + i < p.T)
+        for (int e = tid; e < E; e += gate::kThreads) p.logits[(t + i) * E + e] = sm.logits[i][e];
+  }
+  if (warp < kTiles && t + warp < p.T) {
+    const float* l = sm.logits[warp];
     int id;
     float w;
-    if (E <= 64) gate_select_warp<2>(p.rule, sm.logits, p.select_bias, lane, id, w);
-    else if (E <= 256) gate_select_warp<8>(p.rule, sm.logits, p.select_bias, lane, id, w);
-    else gate_select_warp<32>(p.rule, sm.logits, p.select_bias, lane, id, w);
+    if (E <= 64) gate_select_warp<2>(p.rule, l, p.select_bias, lane, id, w);
+    else if (E <= 256) gate_select_warp<8>(p.rule, l, p.select_bias, lane, id, w);
+    else gate_select_warp<32>(p.rule, l, p.select_bias, lane, id, w);
     if (lane < p.rule.topk) {
-      const int64_t o = t * p.rule.topk + lane;
+      const int64_t o = (t + warp) * p.rule.topk + lane;
       if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = id;
       else static_cast<int32_t*>(p.ids)[o] = id;
       p.weights[o] = w;

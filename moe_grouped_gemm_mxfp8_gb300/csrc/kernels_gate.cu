@@ -1,8 +1,8 @@
 // The router: logits = x W^T (FP32 sums of BF16 products), then the selection of each token.
-//   cluster  few tokens: clusters of 8 CTAs for 8 tokens each (gate_select.cuh)
+//   cluster  few tokens: clusters of 8 CTAs for 8, 16 or 32 tokens each (gate_select.cuh)
 //   pair     many tokens: CTA pairs take 256 tokens against all experts (tcgen05, cta_group::2), and the selection
 //            reads the logits where they are, in TMEM: a token is a TMEM lane, so a thread walks its token's
-//            columns and keeps the best in registers.  Four threads share a token, a quarter of the columns each.
+//            columns and keeps the best keys in registers.  Four threads share a token, a quarter of the columns each.
 #include "gate_select.cuh"
 #include "ops.cuh"
 #include "pipeline.cuh"
@@ -18,22 +18,25 @@ constexpr int kTop = 8;  // the pair form's longest choice
 constexpr int kBars = 2 * kMaxStages + 5;
 constexpr int kMiscOff = kArena + kBars * 8 + 8;
 constexpr int kBiasOff = kMiscOff + 32;                  // float bias[512]
-constexpr int kStatOff = kBiasOff + 512 * 4;             // float [2][4][128]: maxima, sums
-constexpr int kExchOff = kStatOff + 2 * 4 * 128 * 4;     // group keys [64][128], then lists [3][8][3][128] (uint32)
-constexpr int kPairSmem = kExchOff + 3 * kTop * 3 * 128 * 4 + 1024;
-static_assert(64 <= 3 * kTop * 3 && kPairSmem <= 232448, "shared memory");
+constexpr int kStatOff = kBiasOff + 512 * 4;             // float [2][4][128]: maxima and sums; eligible groups
+constexpr int kListOff = kStatOff + 2 * 4 * 128 * 4;     // uint32 [4][8][128]: each quarter's best keys
+constexpr int kCandOff = kListOff + 4 * kTop * 128 * 4;  // group keys [64][128], then candidates [4][8][2][128]
+constexpr int kSelOff = kCandOff + 64 * 128 * 4;         // the choice [8][2][128]
+constexpr int kPairSmem = kSelOff + kTop * 2 * 128 * 4 + 1024;
+static_assert(4 * kTop * 2 <= 64 && kPairSmem <= 232448, "shared memory");
 }  // namespace gate
 
 // ============================================================================ cluster form
+template <int kTiles>
 __global__ void __launch_bounds__(gate::kThreads) gate_cluster_kernel(const __grid_constant__ GateParams p) {
-  __shared__ gate::Smem sm;
+  __shared__ gate::Smem<kTiles> sm;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) {  // no wait here can give up
     p.hdr[0] = 1;
     p.hdr[1] = 0;
   }
-  gate_cluster(p, (int64_t)(blockIdx.x / gate::kCluster) * gate::kTok, sm, ptx::cluster_rank());
+  gate_cluster<kTiles>(p, (int64_t)(blockIdx.x / gate::kCluster) * 8 * kTiles, sm, ptx::cluster_rank());
 }
 
 // ============================================================================ pair form
@@ -54,7 +57,9 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
   uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
   float* s_bias = reinterpret_cast<float*>(smem + gate::kBiasOff);
   float* s_stat = reinterpret_cast<float*>(smem + gate::kStatOff);
-  uint32_t* s_exch = reinterpret_cast<uint32_t*>(smem + gate::kExchOff);
+  uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + gate::kListOff);
+  uint32_t* s_cand = reinterpret_cast<uint32_t*>(smem + gate::kCandOff);
+  uint32_t* s_sel = reinterpret_cast<uint32_t*>(smem + gate::kSelOff);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const uint32_t rank = ptx::cluster_rank();
   const GateRule& r = p.rule;
@@ -213,7 +218,6 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
         }
       }
       float sum = 1.f;
-      bool none = false;  // logits that are all -inf leave nothing to weigh
       if (softmax) {
         s_stat[part * 128 + tok] = mx;
         quadrant_sync();
@@ -252,12 +256,10 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
         sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum += s_stat[(4 + k) * 128 + tok];
-        none = mx == kNegInf && sum == 0.f;
       }
-      auto probability = [&](uint32_t v) {
-        const float f = __uint_as_float(v);
-        return softmax ? (none ? 0.f : f / sum) : f;
-      };
+      // logits that are all -inf leave nothing to weigh
+      const float inv = !softmax ? 1.0f : (mx == kNegInf && sum == 0.f ? 0.f : 1.0f / sum);
+      auto probability = [&](uint32_t v) { return __uint_as_float(v) * inv; };
       uint64_t eligible = ~0ull;
       if (grouped) {
         for (int g = part; g < r.n_group; g += 4) {  // this quarter's share of the groups
@@ -279,102 +281,140 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
           }
           float s = a > 1u ? key_value(a) : kNegInf;
           if (r.group_top == 2) s += b > 1u ? key_value(b) : kNegInf;
-          s_exch[g * 128 + tok] = order_key(s);
+          s_cand[g * 128 + tok] = order_key(s);
         }
         quadrant_sync();
-        eligible = 0;
-        for (int g = 0; g < r.n_group; ++g) {  // fewer than topk_group groups better, or equal and earlier
-          const uint32_t mine = s_exch[g * 128 + tok];
+        uint64_t mine = 0;
+        for (int g = part; g < r.n_group; g += 4) {  // fewer than topk_group groups better, or equal and earlier
+          const uint32_t k = s_cand[g * 128 + tok];
           int better = 0;
           for (int h = 0; h < r.n_group; ++h) {
-            const uint32_t o = s_exch[h * 128 + tok];
-            better += (o > mine || (o == mine && h < g)) ? 1 : 0;
+            const uint32_t o = s_cand[h * 128 + tok];
+            better += (o > k || (o == k && h < g)) ? 1 : 0;
           }
-          if (better < r.topk_group) eligible |= 1ull << g;
+          if (better < r.topk_group) mine |= 1ull << g;
         }
-        quadrant_sync();  // the lists take the keys' place
+        uint32_t* m = reinterpret_cast<uint32_t*>(s_stat);  // [2][4][128]: low and high words
+        m[part * 128 + tok] = (uint32_t)mine;
+        m[(4 + part) * 128 + tok] = (uint32_t)(mine >> 32);
+        quadrant_sync();
+        eligible = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) eligible |= (uint64_t)m[(4 + k) * 128 + tok] << 32 | m[k * 128 + tok];
       }
-      // the best kTop of this quarter's columns, in descending order: a column enters in front of what it exceeds,
-      // so equal scores keep the order of their indices
-      uint32_t key[gate::kTop], idx[gate::kTop];
-      float pr[gate::kTop];
+      // Walks this quarter's columns with their selection keys (0 outside the eligible groups).
+      auto columns = [&](auto&& visit) {
+        int g = grouped ? c_lo * 16 / per : 0, g_end = grouped ? (g + 1) * per : E;  // the column's group
+        bool in = (eligible >> g) & 1;
+        for (int c = c_lo; c < c_hi; ++c) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          ptx::tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < gate::kTop; ++k) {
-        key[k] = 0;
-        idx[k] = 0;
-        pr[k] = 0.f;
-      }
-      auto enter = [&](uint32_t nk, uint32_t ni, float np) {
-        bool above[gate::kTop];
-#pragma unroll
-        for (int k = 0; k < gate::kTop; ++k) above[k] = nk > key[k];
-#pragma unroll
-        for (int k = gate::kTop - 1; k > 0; --k) {
-          key[k] = above[k] ? (above[k - 1] ? key[k - 1] : nk) : key[k];
-          idx[k] = above[k] ? (above[k - 1] ? idx[k - 1] : ni) : idx[k];
-          pr[k] = above[k] ? (above[k - 1] ? pr[k - 1] : np) : pr[k];
+          for (int j = 0; j < 16; ++j) {
+            const int e = c * 16 + j;
+            if (e >= g_end && e < E) {
+              g_end += per;
+              in = (eligible >> ++g) & 1;
+            }
+            const float pv = probability(v[j]);
+            visit(in && e < E ? order_key(pv + s_bias[e & 511]) : 0u, e, pv);
+          }
         }
-        key[0] = above[0] ? nk : key[0];
-        idx[0] = above[0] ? ni : idx[0];
-        pr[0] = above[0] ? np : pr[0];
       };
-      int g = grouped ? c_lo * 16 / per : 0, g_end = grouped ? (g + 1) * per : E;  // the column's group
-      for (int c = c_lo; c < c_hi; ++c) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
-        ptx::tmem_wait_ld();
+      // 1. the quarter's highest keys, in descending order: two instructions per place
+      uint32_t key[gate::kTop];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int e = c * 16 + j;
-          if (e >= E) break;
-          if (e >= g_end) {
-            ++g;
-            g_end += per;
-          }
-          const float pv = probability(v[j]);
-          const uint32_t k = (eligible >> g) & 1 ? order_key(pv + s_bias[e]) : 0u;
-          if (k > key[gate::kTop - 1]) enter(k, (uint32_t)e, pv);
+      for (int k = 0; k < gate::kTop; ++k) key[k] = 0;
+      columns([&](uint32_t x, int, float) {
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) {
+          const uint32_t hi = max(key[k], x);
+          x = min(key[k], x);
+          key[k] = hi;
         }
+      });
+#pragma unroll
+      for (int k = 0; k < gate::kTop; ++k) s_list[(part * gate::kTop + k) * 128 + tok] = key[k];
+      quadrant_sync();
+      // 2. the token's highest keys: the best 8 of two descending lists are max(a[i], b[7 - i]), put in order by the
+      // halving steps of a bitonic sort
+#pragma unroll
+      for (int h = 1; h < 4; ++h) {
+        const uint32_t* o = s_list + ((part + h) & 3) * gate::kTop * 128 + tok;
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) key[k] = max(key[k], o[(gate::kTop - 1 - k) * 128]);
+#pragma unroll
+        for (int d = gate::kTop / 2; d > 0; d >>= 1)
+#pragma unroll
+          for (int k = 0; k < gate::kTop; ++k)
+            if (!(k & d)) {
+              const uint32_t a = max(key[k], key[k + d]), b = min(key[k], key[k + d]);
+              key[k] = a;
+              key[k + d] = b;
+            }
       }
+      uint32_t last = key[0];  // the topk-th
+#pragma unroll
+      for (int k = 1; k < gate::kTop; ++k) last = k < r.topk ? key[k] : last;
+      // 3. the columns above it, and of its equals the first that fill the choice: at most topk per quarter
+      int need = r.topk;
+#pragma unroll
+      for (int k = 0; k < gate::kTop; ++k) need -= key[k] > last ? 1 : 0;
+      int n = 0;
+      uint32_t* cand = s_cand + part * gate::kTop * 2 * 128 + tok;
+      columns([&](uint32_t x, int e, float pv) {
+        if (x > last || (x == last && x > 0 && need > 0)) {
+          need -= x == last ? 1 : 0;
+          cand[2 * n * 128] = (uint32_t)e;
+          cand[(2 * n + 1) * 128] = __float_as_uint(pv);
+          ++n;
+        }
+      });
       // TMEM is read: the next tile's products may overwrite it
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[buf]), 0));
-      if (part > 0) {
-        uint32_t* o = s_exch + (part - 1) * gate::kTop * 3 * 128 + tok;
+      // 4. each candidate's place: the keys above it, and its equals in earlier columns
+      for (int i = 0; i < n; ++i) {
+        const uint32_t e = cand[2 * i * 128], pv = cand[(2 * i + 1) * 128];
+        const uint32_t x = order_key(__uint_as_float(pv) + s_bias[e & 511]);
+        int place = 0, equal = 0;
 #pragma unroll
         for (int k = 0; k < gate::kTop; ++k) {
-          o[(3 * k) * 128] = key[k];
-          o[(3 * k + 1) * 128] = idx[k];
-          o[(3 * k + 2) * 128] = __float_as_uint(pr[k]);
+          place += key[k] > x ? 1 : 0;
+          equal += key[k] == x ? 1 : 0;
+        }
+        if (equal > 1 || x == last) {  // equals of the last may lie beyond the list
+          for (int k = 0; k < i; ++k)
+            place += order_key(__uint_as_float(cand[(2 * k + 1) * 128]) + s_bias[cand[2 * k * 128] & 511]) == x ? 1 : 0;
+          for (int k = 0; k < part * gate::kTop; ++k) place += s_list[k * 128 + tok] == x ? 1 : 0;
+        }
+        if (place < r.topk) {
+          s_sel[2 * place * 128 + tok] = e;
+          s_sel[(2 * place + 1) * 128 + tok] = pv;
         }
       }
       quadrant_sync();
-      if (part == 0) {
-        for (int h = 0; h < 3; ++h) {
-          const uint32_t* o = s_exch + h * gate::kTop * 3 * 128 + tok;
-          for (int k = 0; k < gate::kTop; ++k) {
-            const uint32_t nk = o[(3 * k) * 128];
-            if (nk <= key[gate::kTop - 1]) break;  // the rest of that list is no better
-            enter(nk, o[(3 * k + 1) * 128], __uint_as_float(o[(3 * k + 2) * 128]));
-          }
+      if (part == 0 && token < p.T) {
+        float w[gate::kTop], total = 0.f;
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) {
+          w[k] = k < r.topk ? __uint_as_float(s_sel[(2 * k + 1) * 128 + tok]) : 0.f;
+          total += w[k];
         }
-        if (token < p.T) {
-          float total = 0.f;
 #pragma unroll
-          for (int k = 0; k < gate::kTop; ++k) total += k < r.topk ? pr[k] : 0.f;
-#pragma unroll
-          for (int k = 0; k < gate::kTop; ++k) {
-            if (k < r.topk) {
-              const int64_t o = token * r.topk + k;
-              if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = idx[k];
-              else static_cast<int32_t*>(p.ids)[o] = (int32_t)idx[k];
-              p.weights[o] = (r.renormalise ? pr[k] / (total + 1e-20f) : pr[k]) * r.scale;
-            }
+        for (int k = 0; k < gate::kTop; ++k) {
+          if (k < r.topk) {
+            const int64_t o = token * r.topk + k;
+            const uint32_t e = s_sel[2 * k * 128 + tok];
+            if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = e;
+            else static_cast<int32_t*>(p.ids)[o] = (int32_t)e;
+            p.weights[o] = (r.renormalise ? w[k] / (total + 1e-20f) : w[k]) * r.scale;
           }
         }
       }
-      quadrant_sync();  // the exchange is written again
+      quadrant_sync();  // the exchange areas are written again
       ++acc_i;
     }
   }
@@ -419,9 +459,11 @@ cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t 
   lc.numAttrs = 2;
   lc.stream = s;
   if (!p.pair) {
-    lc.gridDim = dim3((unsigned)((p.T + gate::kTok - 1) / gate::kTok * gate::kCluster));
+    // tokens per cluster: the fewest whose clusters all run at once (about 18 of 8 CTAs)
+    const int tiles = p.T <= 18 * 8 ? 1 : (p.T <= 18 * 16 ? 2 : 4);
+    lc.gridDim = dim3((unsigned)((p.T + 8 * tiles - 1) / (8 * tiles) * gate::kCluster));
     lc.blockDim = dim3(gate::kThreads);
-    return cudaLaunchKernelEx(&lc, gate_cluster_kernel, p);
+    return cudaLaunchKernelEx(&lc, tiles == 1 ? gate_cluster_kernel<1> : (tiles == 2 ? gate_cluster_kernel<2> : gate_cluster_kernel<4>), p);
   }
   static int configured_device = -1;
   int dev = 0;

@@ -252,15 +252,15 @@ struct Walk {
 // The first T / 8 clusters are the router (gate_select.cuh); the others make the token images and zero the counters.
 template <bool kMx>
 __global__ void __launch_bounds__(gate::kThreads) layer_front_kernel(const __grid_constant__ LayerParams p) {
-  __shared__ gate::Smem sm;
+  __shared__ gate::Smem<1> sm;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const GateParams& g = p.gate;
   const int T = (int)g.T;
   const int lane = threadIdx.x & 31;
-  const int routers = (T + gate::kTok - 1) / gate::kTok * gate::kCluster;
+  const int routers = (T + 7) / 8 * gate::kCluster;
   if ((int)blockIdx.x < routers) {
-    gate_cluster(g, (int64_t)(blockIdx.x / gate::kCluster) * gate::kTok, sm, ptx::cluster_rank());
+    gate_cluster<1>(g, (int64_t)(blockIdx.x / gate::kCluster) * 8, sm, ptx::cluster_rank());
     return;
   }
   const int block = blockIdx.x - routers, blocks = gridDim.x - routers, warps = blocks * gate::kWarps;
@@ -796,7 +796,7 @@ static cudaError_t launch_layer_of(const LayerParams& p, int sms, cudaStream_t s
   attr[1].val.cooperative = 1;
   lc.stream = s;
   // the router's clusters (one per 8 tokens, at most 8), and at least 10 for the images
-  lc.gridDim = dim3((unsigned)((p.gate.T + gate::kTok - 1) / gate::kTok + 10) * gate::kCluster);
+  lc.gridDim = dim3((unsigned)((p.gate.T + 7) / 8 + 10) * gate::kCluster);
   lc.blockDim = dim3(gate::kThreads);
   cudaLaunchAttribute fattr[2];
   fattr[0] = attr[0];
