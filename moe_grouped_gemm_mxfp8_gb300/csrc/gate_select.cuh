@@ -15,6 +15,8 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// 1 / (1 + exp(-l)) with the approximate reciprocal (one more ulp; 0 for l = -inf)
+__device__ __forceinline__ float gate_sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 __device__ __forceinline__ float key_value(uint32_t k) {  // of a key above 1
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
@@ -39,7 +41,7 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
   }
   if (r.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) p[i] = 1.0f / (1.0f + expf(-p[i]));
+    for (int i = 0; i < kPer; ++i) p[i] = gate_sigmoid(p[i]);
   } else {
     float mx = kNegInf;
 #pragma unroll

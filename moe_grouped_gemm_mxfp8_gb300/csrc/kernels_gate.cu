@@ -2,7 +2,7 @@
 //   cluster  few tokens: clusters of 8 CTAs for 8, 16 or 32 tokens each (gate_select.cuh)
 //   pair     many tokens: CTA pairs take 256 tokens against all experts (tcgen05, cta_group::2), and the selection
 //            reads the logits where they are, in TMEM: a token is a TMEM lane, so a thread walks its token's
-//            columns and keeps the best keys in registers.  Four threads share a token, a quarter of the columns each.
+//            columns.  Four threads share a token, a quarter of the columns each.
 #include "gate_select.cuh"
 #include "ops.cuh"
 #include "pipeline.cuh"
@@ -12,18 +12,20 @@ namespace gmmfr {
 
 namespace gate {
 constexpr int kPairThreads = 64 + 512;  // warp 0 TMA, warp 1 MMA, 16 epilogue warps
-constexpr int kArena = 160 * 1024;
+constexpr int kArena = 128 * 1024;
 constexpr int kMaxStages = 8;
 constexpr int kTop = 8;  // the pair form's longest choice
-constexpr int kBars = 2 * kMaxStages + 5;
+constexpr int kBars = 2 * kMaxStages + 3;
 constexpr int kMiscOff = kArena + kBars * 8 + 8;
 constexpr int kBiasOff = kMiscOff + 32;                  // float bias[512]
 constexpr int kStatOff = kBiasOff + 512 * 4;             // float [2][4][128]: maxima and sums; eligible groups
 constexpr int kListOff = kStatOff + 2 * 4 * 128 * 4;     // uint32 [4][8][128]: each quarter's best keys
-constexpr int kCandOff = kListOff + 4 * kTop * 128 * 4;  // group keys [64][128], then candidates [4][8][2][128]
-constexpr int kSelOff = kCandOff + 64 * 128 * 4;         // the choice [8][2][128]
+constexpr int kCap = 16;                                 // candidates a quarter has room for
+constexpr int kCandOff = kListOff + 4 * kTop * 128 * 4;  // group keys [64][128], then candidates [4][kCap][2][128]
+constexpr int kSelOff = kCandOff + 4 * kCap * 2 * 128 * 4;  // the choice [8][2][128]
 constexpr int kPairSmem = kSelOff + kTop * 2 * 128 * 4 + 1024;
-static_assert(4 * kTop * 2 <= 64 && kPairSmem <= 232448, "shared memory");
+static_assert(kMaxGroups <= 4 * kCap * 2 && kPairSmem <= 232448, "shared memory");
+constexpr int kPairExperts = 512;  // the pair form's most: their logits fill TMEM
 }  // namespace gate
 
 // ============================================================================ cluster form
@@ -40,7 +42,8 @@ __global__ void __launch_bounds__(gate::kThreads) gate_cluster_kernel(const __gr
 }
 
 // ============================================================================ pair form
-// kBlocks: experts in blocks of 256 (1 or 2).  Accumulators: kBlocks x 256 TMEM columns, double-buffered when one block.
+// kBlocks: experts in blocks of 256 (1 or 2).  TMEM: the logits, which the probabilities replace; with one block the
+// selection keys in columns 256 .. 511 (with two they are made anew whenever the columns are walked).
 template <int kBlocks>
 __global__ void __launch_bounds__(gate::kPairThreads, 1)
     gate_pair_kernel(const __grid_constant__ GateMaps maps, const __grid_constant__ GateParams p) {
@@ -49,8 +52,8 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + gate::kArena);  // used in rank 0: both CTAs' loads
   uint64_t* empty = full + gate::kMaxStages;
   uint64_t* accf = empty + gate::kMaxStages;
-  uint64_t* acce = accf + 2;  // used in rank 0: both CTAs' epilogue warps
-  uint64_t* drain = acce + 2;
+  uint64_t* acce = accf + 1;  // used in rank 0: both CTAs' epilogue warps
+  uint64_t* drain = acce + 1;
   int32_t* misc = reinterpret_cast<int32_t*>(smem + gate::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
   int* abort_flag = &misc[1];
@@ -65,18 +68,16 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
   const GateRule& r = p.rule;
   const int E = r.E, BN = p.bn;
   constexpr int kXBytes = 128 * 128;
+  constexpr bool kKeys = kBlocks == 1;
   const int block_bytes = BN * 64, stage_bytes = kXBytes + kBlocks * block_bytes, n_stages = p.n_stages, KB = p.KB;
-  constexpr int kBufs = kBlocks == 1 ? 2 : 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&acce[b]), 32);
-    }
+    ptx::mbar_init(ptx::smem_u32(accf), 1);
+    ptx::mbar_init(ptx::smem_u32(acce), 32);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0;
     *s_err = 0;
@@ -145,14 +146,12 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
       const uint32_t lo0 = (uint32_t)da0, desc_hi = (uint32_t)(da0 >> 32);
       const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
       const uint32_t lo_step = (uint32_t)stage_bytes >> 4, lo_block = (uint32_t)block_bytes >> 4;
-      int stage = 0, acc_i = 0;
-      uint32_t phase = 0, lo = lo0;
+      int stage = 0;
+      uint32_t phase = 0, aph = 0, lo = lo0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs) {
-        const int buf = acc_i % kBufs;
-        if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i / kBufs) & 1) ^ 1, ctl))) break;
+        if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(acce), aph ^ 1, ctl))) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem_base + buf * 256;
         uint32_t accumulate = 0;
         for (int kb = 0; kb < KB; ++kb) {
           if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
@@ -165,10 +164,10 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                ptx::tc_mma_f16_pair_lo(d + b * 256, lo + 2 * q, lo + (kXBytes >> 4) + b * lo_block + 2 * q, desc_hi, idesc,
+                ptx::tc_mma_f16_pair_lo(tmem_base + b * 256, lo + 2 * q, lo + (kXBytes >> 4) + b * lo_block + 2 * q, desc_hi, idesc,
                                         q > 0 ? 1u : accumulate);
             ptx::tc_commit_pair(empty0 + 8 * stage);
-            if (kb == KB - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+            if (kb == KB - 1) ptx::tc_commit_pair(ptx::smem_u32(accf));
           }
           accumulate = 1;
           lo += lo_step;
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
             lo = lo0;
           }
         }
-        ++acc_i;
+        aph ^= 1;
       }
       if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(drain));
       wait_bar_drain(ptx::smem_u32(drain), 0);
@@ -193,89 +192,133 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
     const bool softmax = !r.sigmoid, grouped = r.n_group > 1;
     const int per = E / r.n_group;
     auto quadrant_sync = [&]() { ptx::bar_sync(1 + q, 128); };  // the four warps that share this quadrant's tokens
-    int acc_i = 0;
-    for (int t = first; t < tiles; t += pairs) {
-      const int buf = acc_i % kBufs;
-      const bool ok = wait_quick(ptx::smem_u32(&accf[buf]), (acc_i / kBufs) & 1, ctl);
+    uint32_t ph = 0;
+    for (int t = first; t < tiles; t += pairs, ph ^= 1) {
+      const bool ok = wait_quick(ptx::smem_u32(accf), ph, ctl);
       if (!ptx::bar_all(1 + q, 128, ok)) break;  // the four leave together
       ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
       const int64_t token = (int64_t)t * 256 + rank * 128 + tok;
-      // columns past E are experts that do not exist (zero rows of W): skipped everywhere below
-      float mx = kNegInf;
+      // chunk c's columns that are experts (past E the rows of W are zeros that do not exist)
+      auto valid = [&](int c) { return c * 16 + 16 <= E ? 0xffffu : (1u << (E - c * 16)) - 1; };
+      float mx = kNegInf, inv = 1.f;
       if (softmax || p.logits) {
         for (int c = c_lo; c < c_hi; ++c) {
           uint32_t v[16];
           ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          const uint32_t in = valid(c);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c * 16 + j < E) {
-              mx = fmaxf(mx, __uint_as_float(v[j]));
-              if (p.logits && token < p.T) p.logits[token * E + c * 16 + j] = __uint_as_float(v[j]);
-            }
+          for (int j = 0; j < 16; ++j)
+            if ((in >> j) & 1) mx = fmaxf(mx, __uint_as_float(v[j]));
+          if (p.logits && token < p.T) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if ((in >> j) & 1) p.logits[token * E + c * 16 + j] = __uint_as_float(v[j]);
           }
         }
       }
-      float sum = 1.f;
       if (softmax) {
         s_stat[part * 128 + tok] = mx;
         quadrant_sync();
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx = fmaxf(mx, s_stat[k * 128 + tok]);
-        sum = 0.f;
-        for (int c = c_lo; c < c_hi; ++c) {  // exponentials, kept in place of the logits
+        float sum = 0.f;
+        for (int c = c_lo; c < c_hi; ++c) {
           uint32_t v[16];
           ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          const uint32_t in = valid(c);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float l = __uint_as_float(v[j]);
             const float e = mx == kNegInf ? (l != l ? l : 0.f) : expf(l - mx);
-            if (c * 16 + j < E) sum += e;
+            if ((in >> j) & 1) sum += e;
             v[j] = __float_as_uint(e);
           }
           ptx::tmem_st_32x32b_x16(taddr + c * 16, v);
         }
         s_stat[(4 + part) * 128 + tok] = sum;
-      } else {
-        for (int c = c_lo; c < c_hi; ++c) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+        ptx::tmem_wait_st();
+        quadrant_sync();
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += s_stat[(4 + k) * 128 + tok];
+        // logits that are all -inf leave nothing to weigh
+        inv = mx == kNegInf && sum == 0.f ? 0.f : 1.0f / sum;
+      }
+      auto probability = [&](uint32_t v) { return __uint_as_float(v) * inv; };
+      // chunk c's keys, from TMEM
+      auto load_keys = [&](int c, uint32_t (&k)[16]) {
+        if constexpr (kKeys) {
+          ptx::tmem_ld_32x32b_x16(taddr + 256 + c * 16, k);
+          ptx::tmem_wait_ld();
+        } else {
+          ptx::tmem_ld_32x32b_x16(taddr + c * 16, k);
+          const uint32_t in = valid(c);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(1.0f / (1.0f + expf(-__uint_as_float(v[j]))));
-          ptx::tmem_st_32x32b_x16(taddr + c * 16, v);
+          for (int j = 0; j < 16; ++j) k[j] = (in >> j) & 1 ? order_key(__uint_as_float(k[j]) + s_bias[c * 16 + j]) : 0u;
+        }
+      };
+      // probabilities and selection keys, and the highest key of each run of 8 columns (16 when there are more than
+      // four chunks: at most 8 runs)
+      uint32_t* runs = s_list + part * gate::kTop * 128 + tok;
+      const bool halves = c_hi - c_lo <= 4;
+      for (int c = c_lo; c < c_hi; ++c) {
+        uint32_t v[16], k[16];
+        ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+        float b[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(b + 4 * j) = *reinterpret_cast<const float4*>(s_bias + c * 16 + 4 * j);
+        const uint32_t in = valid(c);
+        ptx::tmem_wait_ld();
+        uint32_t lo = 0, hi = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float pv = softmax ? probability(v[j]) : gate_sigmoid(__uint_as_float(v[j]));
+          v[j] = __float_as_uint(pv);
+          k[j] = (in >> j) & 1 ? order_key(pv + b[j]) : 0u;
+          if (j < 8) lo = max(lo, k[j]);
+          else hi = max(hi, k[j]);
+        }
+        ptx::tmem_st_32x32b_x16(taddr + c * 16, v);
+        if constexpr (kKeys) ptx::tmem_st_32x32b_x16(taddr + 256 + c * 16, k);
+        if (halves) {
+          runs[2 * (c - c_lo) * 128] = lo;
+          runs[(2 * (c - c_lo) + 1) * 128] = hi;
+        } else {
+          runs[(c - c_lo) * 128] = max(lo, hi);
         }
       }
+      for (int k = halves ? 2 * (c_hi - c_lo) : c_hi - c_lo; k < gate::kTop; ++k) runs[k * 128] = 0;
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       quadrant_sync();
       ptx::tc_fence_after();
-      if (softmax) {
-        sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum += s_stat[(4 + k) * 128 + tok];
-      }
-      // logits that are all -inf leave nothing to weigh
-      const float inv = !softmax ? 1.0f : (mx == kNegInf && sum == 0.f ? 0.f : 1.0f / sum);
-      auto probability = [&](uint32_t v) { return __uint_as_float(v) * inv; };
       uint64_t eligible = ~0ull;
       if (grouped) {
         for (int g = part; g < r.n_group; g += 4) {  // this quarter's share of the groups
           uint32_t a = 0, b = 0;                     // the two highest keys
           const int lo = g * per, hi = lo + per;
           for (int c = lo >> 4; c * 16 < hi; ++c) {
-            uint32_t v[16];
-            ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
-            ptx::tmem_wait_ld();
+            uint32_t k[16];
+            load_keys(c, k);
+            uint32_t in = 0xffffu;  // the chunk's columns of this group
+            if (c * 16 < lo) in &= 0xffffu << (lo - c * 16);
+            if (c * 16 + 16 > hi) in &= (1u << (hi - c * 16)) - 1;
+            if (in == 0xffffu) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int e = c * 16 + j;
-              if (e >= lo && e < hi) {
-                const uint32_t k = order_key(probability(v[j]) + s_bias[e]);
-                b = max(b, min(a, k));
-                a = max(a, k);
+              for (int j = 0; j < 16; ++j) {
+                b = max(b, min(a, k[j]));
+                a = max(a, k[j]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const uint32_t x = (in >> j) & 1 ? k[j] : 0u;
+                b = max(b, min(a, x));
+                a = max(a, x);
               }
             }
           }
@@ -302,83 +345,150 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) eligible |= (uint64_t)m[(4 + k) * 128 + tok] << 32 | m[k * 128 + tok];
       }
-      // Walks this quarter's columns with their selection keys (0 outside the eligible groups).
+      // chunk c's columns in eligible groups
+      auto in_groups = [&](int c) {
+        if (!grouped) return 0xffffu;
+        if (per % 16 == 0) return (eligible >> (c * 16 / per)) & 1 ? 0xffffu : 0u;
+        uint32_t in = 0;
+        for (int j = 0; j < 16 && c * 16 + j < E; ++j) in |= (uint32_t)((eligible >> ((c * 16 + j) / per)) & 1) << j;
+        return in;
+      };
+      // Walks this quarter's columns, 16 at a time, with their keys (0 outside the eligible groups).
       auto columns = [&](auto&& visit) {
-        int g = grouped ? c_lo * 16 / per : 0, g_end = grouped ? (g + 1) * per : E;  // the column's group
-        bool in = (eligible >> g) & 1;
         for (int c = c_lo; c < c_hi; ++c) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
-          ptx::tmem_wait_ld();
+          uint32_t k[16];
+          load_keys(c, k);
+          if (grouped) {
+            const uint32_t in = in_groups(c);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int e = c * 16 + j;
-            if (e >= g_end && e < E) {
-              g_end += per;
-              in = (eligible >> ++g) & 1;
-            }
-            const float pv = probability(v[j]);
-            visit(in && e < E ? order_key(pv + s_bias[e & 511]) : 0u, e, pv);
+            for (int j = 0; j < 16; ++j) k[j] = (in >> j) & 1 ? k[j] : 0u;
           }
+          visit(c, k);
         }
       };
-      // 1. the quarter's highest keys, in descending order: two instructions per place
-      uint32_t key[gate::kTop];
-#pragma unroll
-      for (int k = 0; k < gate::kTop; ++k) key[k] = 0;
-      columns([&](uint32_t x, int, float) {
+      uint32_t key[gate::kTop];  // in descending order
+      auto put = [&](uint32_t x) {
 #pragma unroll
         for (int k = 0; k < gate::kTop; ++k) {
           const uint32_t hi = max(key[k], x);
           x = min(key[k], x);
           key[k] = hi;
         }
-      });
+      };
+      // Takes the best of the four quarters' lists (in shared memory) into this thread's: the best 8 of two descending
+      // lists are max(a[i], b[7 - i]), put in order by the halving steps of a bitonic sort.
+      auto merge = [&]() {
 #pragma unroll
-      for (int k = 0; k < gate::kTop; ++k) s_list[(part * gate::kTop + k) * 128 + tok] = key[k];
-      quadrant_sync();
-      // 2. the token's highest keys: the best 8 of two descending lists are max(a[i], b[7 - i]), put in order by the
-      // halving steps of a bitonic sort
+        for (int k = 0; k < gate::kTop; ++k) s_list[(part * gate::kTop + k) * 128 + tok] = key[k];
+        quadrant_sync();
 #pragma unroll
-      for (int h = 1; h < 4; ++h) {
-        const uint32_t* o = s_list + ((part + h) & 3) * gate::kTop * 128 + tok;
+        for (int h = 1; h < 4; ++h) {
+          const uint32_t* o = s_list + ((part + h) & 3) * gate::kTop * 128 + tok;
 #pragma unroll
-        for (int k = 0; k < gate::kTop; ++k) key[k] = max(key[k], o[(gate::kTop - 1 - k) * 128]);
+          for (int k = 0; k < gate::kTop; ++k) key[k] = max(key[k], o[(gate::kTop - 1 - k) * 128]);
 #pragma unroll
-        for (int d = gate::kTop / 2; d > 0; d >>= 1)
+          for (int d = gate::kTop / 2; d > 0; d >>= 1)
 #pragma unroll
-          for (int k = 0; k < gate::kTop; ++k)
-            if (!(k & d)) {
-              const uint32_t a = max(key[k], key[k + d]), b = min(key[k], key[k + d]);
-              key[k] = a;
-              key[k + d] = b;
-            }
+            for (int k = 0; k < gate::kTop; ++k)
+              if (!(k & d)) {
+                const uint32_t a = max(key[k], key[k + d]), b = min(key[k], key[k + d]);
+                key[k] = a;
+                key[k + d] = b;
+              }
+        }
+      };
+      auto topk_th = [&]() {
+        uint32_t last = key[0];
+#pragma unroll
+        for (int k = 1; k < gate::kTop; ++k) last = k < r.topk ? key[k] : last;
+        return last;
+      };
+      // Keeping the best 8 of all columns in order (8 maxima and 8 minima per column) is what a token would mostly spend
+      // its time on.  Instead:
+      // 1. a bound from below on the topk-th key: the topk-th of the runs' maxima
+#pragma unroll
+      for (int k = 0; k < gate::kTop; ++k) key[k] = 0;
+      if (grouped) {
+        columns([&](int c, const uint32_t (&k)[16]) {
+          uint32_t a = 0, b = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            a = max(a, k[j]);
+            b = max(b, k[8 + j]);
+          }
+          if (halves) {
+            put(a);
+            put(b);
+          } else {
+            put(max(a, b));
+          }
+        });
+      } else {
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) put(runs[k * 128]);
       }
-      uint32_t last = key[0];  // the topk-th
-#pragma unroll
-      for (int k = 1; k < gate::kTop; ++k) last = k < r.topk ? key[k] : last;
-      // 3. the columns above it, and of its equals the first that fill the choice: at most topk per quarter
-      int need = r.topk;
-#pragma unroll
-      for (int k = 0; k < gate::kTop; ++k) need -= key[k] > last ? 1 : 0;
+      merge();
+      uint32_t last = topk_th();
+      last = last > 0 ? last : 1u;
+      // 2. the columns that reach it: few, unless many scores are equal (or one run holds them all)
       int n = 0;
-      uint32_t* cand = s_cand + part * gate::kTop * 2 * 128 + tok;
-      columns([&](uint32_t x, int e, float pv) {
-        if (x > last || (x == last && x > 0 && need > 0)) {
-          need -= x == last ? 1 : 0;
-          cand[2 * n * 128] = (uint32_t)e;
-          cand[(2 * n + 1) * 128] = __float_as_uint(pv);
-          ++n;
+      uint32_t* cand = s_cand + part * gate::kCap * 2 * 128 + tok;  // column and probability
+      auto cand_key = [&](int i) { return order_key(__uint_as_float(cand[(2 * i + 1) * 128]) + s_bias[cand[2 * i * 128]]); };
+      columns([&](int c, const uint32_t (&k)[16]) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (k[j] >= last) {
+            uint32_t* o = cand + (n & (gate::kCap - 1)) * 2 * 128;
+            o[0] = (uint32_t)(c * 16 + j);
+            o[128] = v[j];
+            ++n;
+          }
         }
       });
+      // 3. the topk-th key: from the candidates, or, when they did not fit, from all columns
+      const bool fits = ptx::bar_all(1 + q, 128, n <= gate::kCap);
+#pragma unroll
+      for (int k = 0; k < gate::kTop; ++k) key[k] = 0;
+      if (fits) {
+        for (int i = 0; i < n; ++i) put(cand_key(i));
+      } else {
+        columns([&](int, const uint32_t (&k)[16]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) put(k[j]);
+        });
+      }
+      merge();
+      last = topk_th();
+      if (!fits) {  // the columns above it, and of its equals the first that fill the choice: at most topk per quarter
+        int need = r.topk;
+#pragma unroll
+        for (int k = 0; k < gate::kTop; ++k) need -= key[k] > last ? 1 : 0;
+        n = 0;
+        columns([&](int c, const uint32_t (&k)[16]) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c * 16, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (k[j] > last || (k[j] == last && need > 0)) {
+              need -= k[j] == last ? 1 : 0;
+              cand[2 * n * 128] = (uint32_t)(c * 16 + j);
+              cand[(2 * n + 1) * 128] = v[j];
+              ++n;
+            }
+          }
+        });
+      }
       // TMEM is read: the next tile's products may overwrite it
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[buf]), 0));
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(acce), 0));
       // 4. each candidate's place: the keys above it, and its equals in earlier columns
       for (int i = 0; i < n; ++i) {
-        const uint32_t e = cand[2 * i * 128], pv = cand[(2 * i + 1) * 128];
-        const uint32_t x = order_key(__uint_as_float(pv) + s_bias[e & 511]);
+        const uint32_t x = cand_key(i);
         int place = 0, equal = 0;
 #pragma unroll
         for (int k = 0; k < gate::kTop; ++k) {
@@ -386,13 +496,12 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
           equal += key[k] == x ? 1 : 0;
         }
         if (equal > 1 || x == last) {  // equals of the last may lie beyond the list
-          for (int k = 0; k < i; ++k)
-            place += order_key(__uint_as_float(cand[(2 * k + 1) * 128]) + s_bias[cand[2 * k * 128] & 511]) == x ? 1 : 0;
+          for (int k = 0; k < i; ++k) place += cand_key(k) == x ? 1 : 0;
           for (int k = 0; k < part * gate::kTop; ++k) place += s_list[k * 128 + tok] == x ? 1 : 0;
         }
         if (place < r.topk) {
-          s_sel[2 * place * 128 + tok] = e;
-          s_sel[(2 * place + 1) * 128 + tok] = pv;
+          s_sel[2 * place * 128 + tok] = cand[2 * i * 128];
+          s_sel[(2 * place + 1) * 128 + tok] = cand[(2 * i + 1) * 128];
         }
       }
       quadrant_sync();
@@ -415,7 +524,6 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
         }
       }
       quadrant_sync();  // the exchange areas are written again
-      ++acc_i;
     }
   }
 
@@ -436,7 +544,7 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
 
 // ============================================================================ plan and launch
 bool plan_gate(GateParams& p, int sms) {
-  p.pair = p.T > kGateClusterTokens && p.rule.E <= 512 && p.rule.topk <= gate::kTop;
+  p.pair = p.T > kGateClusterTokens && p.rule.E <= gate::kPairExperts && p.rule.topk <= gate::kTop;
   if (!p.pair) return false;
   p.bn = p.rule.E <= 256 ? (p.rule.E + 31) / 32 * 32 : 256;
   p.KB = (int32_t)((p.H + 63) / 64);
@@ -459,8 +567,9 @@ cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t 
   lc.numAttrs = 2;
   lc.stream = s;
   if (!p.pair) {
-    // tokens per cluster: the fewest whose clusters all run at once (about 18 of 8 CTAs)
-    const int tiles = p.T <= 18 * 8 ? 1 : (p.T <= 18 * 16 ? 2 : 4);
+    // tokens per cluster: the fewest whose clusters all run at once (15 of 8 CTAs: 256 tokens of 256 experts took
+    // 16.5 us in 16 clusters of 16, 10 in 8 of 32)
+    const int tiles = p.T <= 15 * 8 ? 1 : (p.T <= 15 * 16 ? 2 : 4);
     lc.gridDim = dim3((unsigned)((p.T + 8 * tiles - 1) / (8 * tiles) * gate::kCluster));
     lc.blockDim = dim3(gate::kThreads);
     return cudaLaunchKernelEx(&lc, tiles == 1 ? gate_cluster_kernel<1> : (tiles == 2 ? gate_cluster_kernel<2> : gate_cluster_kernel<4>), p);

@@ -27,6 +27,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "epilogue.cuh"
 #include "gate_select.cuh"
 #include "ops.cuh"
@@ -795,8 +797,8 @@ static cudaError_t launch_layer_of(const LayerParams& p, int sms, cudaStream_t s
   attr[1].id = cudaLaunchAttributeCooperative;  // CTAs wait for one another: all must be resident
   attr[1].val.cooperative = 1;
   lc.stream = s;
-  // the router's clusters (one per 8 tokens, at most 8), and at least 10 for the images
-  lc.gridDim = dim3((unsigned)((p.gate.T + 7) / 8 + 10) * gate::kCluster);
+  // the router's clusters (one per 8 tokens, at most 8) and the images': about as many as run at once
+  lc.gridDim = dim3((unsigned)std::max<int64_t>(15, (p.gate.T + 7) / 8 + 7) * gate::kCluster);
   lc.blockDim = dim3(gate::kThreads);
   cudaLaunchAttribute fattr[2];
   fattr[0] = attr[0];

@@ -13,7 +13,7 @@ int sm_count();
 constexpr int kMaxTopk = 32;
 constexpr int kMaxGroups = 64;
 constexpr int kLayerMaxTokens = 64;
-constexpr int kGateClusterTokens = 512;  // the router up to here: clusters of 8 CTAs for 8 tokens each
+constexpr int kGateClusterTokens = 960;  // the router up to here: two waves of clusters (19 us; the pair form 32)
 
 // The router's rule (gmmfr_gate_problem).
 struct GateRule {

@@ -90,10 +90,10 @@ GATES = [
     dict(T=1000, H=2048, E=256, topk=8, scoring="sigmoid", bias=True, n_group=8, topk_group=4, scale=2.5),
     dict(T=2500, H=1288, E=200, topk=3, scoring="softmax"),
     dict(T=4100, H=256, E=48, topk=2, scoring="softmax"),
-    dict(T=700, H=264, E=512, topk=8, scoring="softmax", n_group=4, topk_group=1),
-    dict(T=900, H=200, E=300, topk=8, scoring="sigmoid", bias=True, n_group=50, topk_group=9),
-    dict(T=513, H=72, E=7, topk=7, scoring="softmax", renormalise=False),
-    dict(T=600, H=128, E=64, topk=32, scoring="sigmoid", n_group=64, topk_group=33, group_top=1),
+    dict(T=1700, H=264, E=512, topk=8, scoring="softmax", n_group=4, topk_group=1),
+    dict(T=1900, H=200, E=300, topk=8, scoring="sigmoid", bias=True, n_group=50, topk_group=9),
+    dict(T=961, H=72, E=7, topk=7, scoring="softmax", renormalise=False),
+    dict(T=961, H=128, E=64, topk=32, scoring="sigmoid", n_group=64, topk_group=33, group_top=1),
     dict(T=40000, H=64, E=36, topk=5, scoring="sigmoid", n_group=12, topk_group=5),
     dict(T=530, H=64, E=600, topk=8, scoring="softmax"),
 ]
@@ -126,7 +126,7 @@ def test_gate_ties_go_to_the_lowest_index(T):
         assert np.array_equal(ids, want)
 
 
-@pytest.mark.parametrize("T", [2, 200, 777])
+@pytest.mark.parametrize("T", [2, 200, 1777])
 def test_gate_masked_and_infinite_scores(T):
     g = _gen(7)
     E, H = 64, 64
@@ -163,7 +163,7 @@ def test_gate_masked_and_infinite_scores(T):
     assert torch.equal(ids[keep], ref_ids[keep]) and torch.equal(wt[keep], ref_wt[keep])
 
 
-@pytest.mark.parametrize("T", [3, 333, 777])
+@pytest.mark.parametrize("T", [3, 333, 1777])
 def test_gate_strided_rows_int64_ids_and_another_stream(T):
     g = _gen(11)
     wide = _randn(g, T, 200).cuda()
