@@ -4,7 +4,8 @@
 
 namespace gmmfr {
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// v / (1 + exp(-v)) with the approximate division (two ulp; where exp(-v) overflows the quotient is 0)
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + expf(-v)); }
 
 __device__ __forceinline__ float activate(int act, float v) {
   switch (act) {

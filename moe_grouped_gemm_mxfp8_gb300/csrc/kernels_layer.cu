@@ -16,7 +16,7 @@
 // the up run.
 //
 // A column tile cut between CTAs is joined through the workspace: each piece stores its FP32 sums, and
-//   up     the CTA that arrives last adds the pieces in CTA order, applies SwiGLU and stores sw;
+//   up     one of its CTAs adds the pieces in CTA order, applies SwiGLU and stores sw;
 //   down   every CTA with a piece waits for the others at its end and adds its share of the tile.
 // Both orders are fixed, so results are the same bits every time.
 //
@@ -112,8 +112,8 @@ constexpr int kMaskOff = kMiscOff + 64;                          // uint64 mask[
 constexpr int kActOff = kMaskOff + 8 * kMaxExperts;              // uint16 act[1024]: the chosen experts
 constexpr int kIdsOff = kActOff + 2 * kMaxExperts;               // uint16 ids[64 * 32]
 constexpr int kWtOff = kIdsOff + 2 * kLayerMaxTokens * kMaxTopk; // float weights[64 * 32]
-constexpr int kXchgOff = kWtOff + 4 * kLayerMaxTokens * kMaxTopk;  // float [2][16][32]: up values for SwiGLU
-constexpr int kTokWOff = kXchgOff + 2 * 16 * 32 * 4;             // float [64]: the unit's router weights
+constexpr int kXchgOff = kWtOff + 4 * kLayerMaxTokens * kMaxTopk;  // float [8][2][32]: values handed over for SwiGLU
+constexpr int kTokWOff = kXchgOff + 8 * 2 * 32 * 4;             // float [64]: the unit's router weights
 constexpr int kSmemBytes = kTokWOff + 4 * kLayerMaxTokens + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 // TMEM: two accumulators of acc_cols columns (MXFP8: the products with hi, then those with lo), then with MXFP8 the
@@ -166,11 +166,6 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
 __device__ __forceinline__ void red_release_add(uint32_t* p, uint32_t v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
 // Bounded wait until *p reaches n.
 __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n, const Ctl& c) {
   Deadline d;
@@ -208,17 +203,19 @@ struct Run {
 // tiles, each some CTA's.  A CTA's pieces of cut units lie in its slots: 0 where its range begins in the unit, 1
 // where it ends there; so only the first piece of a unit can lie in slot 1.
 struct Pieces {
-  uint32_t b0, n, first_slot;
-  const Run* run;
-  uint32_t x0;
-  __device__ Pieces(const Run& r, uint32_t u) : run(&r), x0(u * r.K) {
+  uint32_t b0, n, first_slot, x0;
+  bool scattered;  // fewer tiles than CTAs
+  __device__ Pieces(const Run& r, uint32_t u) : x0(u * r.K), scattered(r.U < r.G) {
     b0 = r.owner(x0);
-    n = r.U < r.G ? r.K : r.owner(x0 + r.K - 1) - b0 + 1;
+    n = scattered ? r.K : r.owner(x0 + r.K - 1) - b0 + 1;
     first_slot = r.lo(b0) >= x0 ? 0 : 1;
   }
-  __device__ uint32_t cta(uint32_t i) const { return run->U < run->G ? run->owner(x0 + i) : b0 + i; }
   // piece i's slot among the CTAs' pairs of slots
-  __device__ uint32_t slot(uint32_t i) const { return cta(i) * 2 + (i == 0 ? first_slot : 0); }
+  __device__ uint32_t slot(const Run& r, uint32_t i) const {
+    uint32_t b = b0 + i;
+    if (scattered) b = r.owner(x0 + i);
+    return b * 2 + (i == 0 ? first_slot : 0);
+  }
 };
 
 // The pieces of one CTA: units (or parts of units) of the two runs in order; every role walks them.
@@ -330,7 +327,6 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   int* abort_flag = &misc[1];
   uint32_t* s_err = reinterpret_cast<uint32_t*>(&misc[2]);
   int* s_warp_sum = &misc[4];  // [8]
-  int* s_last = &misc[12];
   unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(smem + layer::kMaskOff);
   uint16_t* s_act = reinterpret_cast<uint16_t*>(smem + layer::kActOff);
   uint16_t* s_ids = reinterpret_cast<uint16_t*>(smem + layer::kIdsOff);
@@ -578,29 +574,43 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     int acc_i = 0;
     int cut0 = 0, cut1 = 0, n_cut = 0;  // column tiles of the down run that this CTA has a piece of
     bool ok = true;
-    while (walk.next()) {
+    // A cut unit of the up run is finished by the CTA of its second piece, whose range begins inside the unit: a CTA
+    // owes at most one, after its own pieces (its others are waited for by others).  That code runs once before, on no
+    // pieces at all (it leaves zeros, which the real pass overwrites): its instructions come from memory the first
+    // time, which here costs nothing (nothing has arrived yet) and later 1.5 us on the way of every CTA.
+    const uint32_t begin = up.lo(blockIdx.x);
+    int owed_unit = -1;
+    if (begin < up.lo(blockIdx.x + 1)) {
+      const Pieces first(up, begin / up.K);
+      if ((first.scattered ? begin - first.x0 : blockIdx.x - first.b0) == 1) owed_unit = (int)(begin / up.K);
+    }
+    bool rehearse = owed_unit >= 0;
+    bool more = walk.next();
+    while (more || owed_unit >= 0) {
+      const bool owed = owed_unit >= 0 && (rehearse || !more || walk.is_down);
       const int buf = acc_i & 1;
-      const bool is_down = walk.is_down;
+      const bool is_down = !owed && walk.is_down;
+      const uint32_t unit = owed ? (uint32_t)owed_unit : walk.unit;
       const Run& run = is_down ? down : up;
-      const bool routed = !is_down && (int)walk.unit >= p.NT1s;
-      const int a = routed ? ((int)walk.unit - p.NT1s) / p.NT1 : 0;
-      const int j = routed ? (int)walk.unit - p.NT1s - a * p.NT1 : (int)walk.unit;  // column tile
+      const bool routed = !is_down && (int)unit >= p.NT1s;
+      const int a = routed ? ((int)unit - p.NT1s) / p.NT1 : 0;
+      const int j = routed ? (int)unit - p.NT1s - a * p.NT1 : (int)unit;  // column tile
       const int e = routed ? s_act[a] : 0;
       const unsigned long long mask = routed ? s_mask[e] : (T == 64 ? ~0ull : (1ull << T) - 1);
-      const bool whole = walk.k1 - walk.k0 == run.K;
+      const bool whole = !owed && walk.k1 - walk.k0 == run.K;
+      const Pieces pieces(run, unit);
       if (!is_down && ep < T) {  // the router's weight of each token for this expert
         float w = routed ? 0.f : 1.f;
         if (routed)
           for (int k = 0; k < topk; ++k) w = s_ids[ep * topk + k] == e ? s_wt[ep * topk + k] : w;
         s_tokw[ep] = w;
       }
-      ok = warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
+      if (!owed) ok = warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
+      else if (!rehearse && ep == 0) ok = wait_count(p.up_cnt + unit, pieces.n, ctl);
       if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * acc;
-      bool finish = whole;
-      const Pieces pieces(run, walk.unit);
-      if (!whole) {
+      if (!whole && !owed) {
         // this CTA's range begins in the unit (slot 0) or ends there (slot 1)
         const uint32_t at = blockIdx.x * 2 + (run.lo(blockIdx.x) >= pieces.x0 ? 0 : 1);
         float* slot = (is_down ? p.slots_down : p.slots_up) + (int64_t)at * slot_floats;
@@ -613,19 +623,12 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             if ((mask >> (c0 + jj)) & 1) __stcg(slot + (c0 + jj) * 128 + row, v[jj]);
         }
         ptx::bar_sync(1, 128);  // the pieces' stores, then one thread's release
+        if (ep == 0) red_release_add((is_down ? p.down_cnt : p.up_cnt) + unit, 1);
         if (is_down) {
-          if (ep == 0) red_release_add(p.down_cnt + walk.unit, 1);
-          if (n_cut++ == 0) cut0 = walk.unit;
-          else cut1 = walk.unit;
-        } else {
-          if (ep == 0) {
-            *s_last = atom_add_acq_rel(p.up_cnt + walk.unit, 1u) == pieces.n - 1;
-          }
-          ptx::bar_sync(1, 128);
-          finish = *s_last != 0;
+          if (n_cut++ == 0) cut0 = unit;
+          else cut1 = unit;
         }
-      }
-      if (finish && is_down) {  // a column tile of this CTA alone
+      } else if (is_down) {  // a column tile of this CTA alone
         for (int c0 = 0; c0 < T; c0 += 16) {
           float v[16];
           load_acc16<kMx>(taddr + c0, npad, v);
@@ -640,85 +643,109 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             }
           }
         }
-      } else if (finish) {
+      } else {
+        const uint32_t n_pieces = rehearse ? 0 : pieces.n;
         // SwiGLU: rows 0..63 of the tile hold gate columns, 64..127 the up columns of the same indices
         uint8_t* dst = routed ? p.swimg + (int64_t)a * p.KB2 * img : p.swimg_s;
         dst += (int64_t)(kMx ? j >> 1 : j) * img;
-        const bool pad_half = kMx && (j & 1) == 0 && j + 1 == (routed ? p.NT1 : p.NT1s);
-        for (int c0 = 0; c0 < T; c0 += 16) {
-          const uint32_t m16 = (uint32_t)(mask >> c0) & 0xffffu;
-          float v[16];
-          if (m16) {  // uniform over the four warps
-            if (whole) {
-              load_acc16<kMx>(taddr + c0, npad, v);
-            } else {
-#pragma unroll
-              for (int jj = 0; jj < 16; ++jj) v[jj] = 0.f;
-#pragma unroll 4
-              for (uint32_t i = 0; i < pieces.n; ++i) {
-                const float* slot = p.slots_up + (int64_t)pieces.slot(i) * slot_floats + row;
-#pragma unroll
-                for (int jj = 0; jj < 16; ++jj)
-                  if ((m16 >> jj) & 1) v[jj] += __ldcg(slot + (c0 + jj) * 128);
-              }
-            }
-            // warps 2, 3 (gate rows) take the even tokens, warps 4, 5 (up rows) the odd ones: each hands
-            // the other what it needs
-#pragma unroll
-            for (int jj = 0; jj < 16; ++jj)
-              if ((jj & 1) == (q >= 2 ? 0 : 1)) xchg[((q & 1) * 16 + jj) * 32 + lane] = v[jj];
-            ptx::bar_sync(1, 128);
+        const bool pad_half = kMx && (j & 1) == 0 && j + 1 == (routed ? p.NT1 : p.NT1s);  // no unit fills the tile's other half
+        // rows of tokens that did not choose the expert: zeros, in 16-byte chunks (MXFP8: of hi and of lo)
+        for (int i = ep; i < T * 8; i += 128) {
+          const int t = i >> 3, c = i & 7;
+          if ((mask >> t) & 1) continue;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          if constexpr (!kMx) {
+            *reinterpret_cast<uint4*>(dst + image_chunk(t, c)) = zero;
+          } else {
+            uint8_t* at = dst + kSfChunk + (c >> 2) * npad * 128;
+            *reinterpret_cast<uint4*>(at + image_chunk(t, (j & 1) * 4 + (c & 3))) = zero;
+            if ((c & 3) < 2) dst[scale_at((c >> 2) * npad + t, (j & 1) * 2 + (c & 3))] = 127;
           }
-          const int half = q >= 2, col = (q & 1) * 32 + lane;  // intermediate index within the unit
+        }
+        if (pad_half) {
+          for (int i = ep; i < T * 8; i += 128) {
+            const int t = i >> 3, c = i & 7;
+            uint8_t* at = dst + kSfChunk + (c >> 2) * npad * 128;
+            *reinterpret_cast<uint4*>(at + image_chunk(t, 4 + (c & 3))) = make_uint4(0, 0, 0, 0);
+            if ((c & 3) < 2) dst[scale_at((c >> 2) * npad + t, 2 + (c & 3))] = 127;
+          }
+        }
+        // the others, eight at a time: warps 2, 3 (gate rows) take the even ones, warps 4, 5 (up rows) the odd, each
+        // handing the other what it needs
+        const int half = q >= 2, col = (q & 1) * 32 + lane;  // intermediate index within the unit
+        for (unsigned long long m = mask; m;) {
+          int tok[8];
+          float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int jj = 2 * i + half, t = c0 + jj;
-            if (t < T) {
-              const bool on = (m16 >> jj) & 1;  // the token chose this expert
-              float sw = 0.f;
-              if (on) {
-                const float o = xchg[((q & 1) * 16 + jj) * 32 + lane];
-                const float mine = half ? v[2 * i + 1] : v[2 * i];
-                sw = silu(half ? o : mine) * (half ? mine : o) * s_tokw[t];
+            tok[i] = m ? __ffsll((long long)m) - 1 : -1;
+            m &= m - 1;
+          }
+          if (whole) {
+            uint32_t r[8], l[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (tok[i] >= 0) {
+                r[i] = ptx::tmem_ld_32x32b_x1(taddr + tok[i]);
+                if constexpr (kMx) l[i] = ptx::tmem_ld_32x32b_x1(taddr + npad + tok[i]);
               }
-              if constexpr (!kMx) {
-                *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(sw);
-              } else {
-                uint32_t hi = 0, lo = 0, byte_hi = 127, byte_lo = 127;
-                if (on) {
-                  const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
-                  split_e4m3(sw, b, hi, lo);
-                  byte_hi = b.byte_hi;
-                  byte_lo = b.byte_lo;
-                }
-                const int c = (j & 1) * 64 + col;
-                uint8_t* at = dst + kSfChunk + image_chunk(t, c >> 4) + (c & 15);
-                at[0] = (uint8_t)hi;
-                at[npad * 128] = (uint8_t)lo;
-                if (lane == 0) {
-                  dst[scale_at(t, c >> 5)] = (uint8_t)byte_hi;
-                  dst[scale_at(npad + t, c >> 5)] = (uint8_t)byte_lo;
-                }
-                if (pad_half) {  // the tile's second half lies past the intermediate size
-                  uint8_t* z = dst + kSfChunk + image_chunk(t, (c + 64) >> 4) + (c & 15);
-                  z[0] = 0;
-                  z[npad * 128] = 0;
-                  if (lane == 0) dst[scale_at(t, (c + 64) >> 5)] = dst[scale_at(npad + t, (c + 64) >> 5)] = 127;
-                }
+            }
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = kMx ? __uint_as_float(r[i]) + __uint_as_float(l[i]) : __uint_as_float(r[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll 4
+            for (uint32_t k = 0; k < n_pieces; ++k) {
+              const float* slot = p.slots_up + (int64_t)pieces.slot(up, k) * slot_floats + row;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (tok[i] >= 0) v[i] += __ldcg(slot + tok[i] * 128);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((i & 1) != half) xchg[(i * 2 + (q & 1)) * 32 + lane] = v[i];
+          ptx::bar_sync(1, 128);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = half ? tok[2 * i + 1] : tok[2 * i];
+            if (t < 0) break;
+            const float mine = half ? v[2 * i + 1] : v[2 * i], other = xchg[((2 * i + half) * 2 + (q & 1)) * 32 + lane];
+            const float sw = silu(half ? other : mine) * (half ? mine : other) * s_tokw[t];
+            if constexpr (!kMx) {
+              *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(sw);
+            } else {
+              const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
+              uint32_t hi, lo;
+              split_e4m3(sw, b, hi, lo);
+              const int c = (j & 1) * 64 + col;
+              uint8_t* at = dst + kSfChunk + image_chunk(t, c >> 4) + (c & 15);
+              at[0] = (uint8_t)hi;
+              at[npad * 128] = (uint8_t)lo;
+              if (lane == 0) {
+                dst[scale_at(t, c >> 5)] = (uint8_t)b.byte_hi;
+                dst[scale_at(npad + t, c >> 5)] = (uint8_t)b.byte_lo;
               }
             }
           }
-          if (m16) ptx::bar_sync(1, 128);  // xchg is written again
+          if (m) ptx::bar_sync(1, 128);  // xchg is written again
         }
         asm volatile("fence.proxy.async;" ::: "memory");  // sw is read by bulk copies
         ptx::bar_sync(1, 128);
-        if (ep == 0) red_release_add(p.up_done, 1);
+        if (ep == 0 && !rehearse) red_release_add(p.up_done, 1);
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
-      ++acc_i;
-      ok = true;
+      if (owed) {
+        if (!rehearse) owed_unit = -1;
+        rehearse = false;
+      } else {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
+        ++acc_i;
+        more = walk.next();
+      }
     }
     // the cut column tiles: this CTA's share of each, once all its pieces are there
     const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 7) == 0 &&
@@ -739,7 +766,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int k = 0; k < n; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.slots_down + (int64_t)pieces.slot(k) * slot_floats +
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.slots_down + (int64_t)pieces.slot(down, k) * slot_floats +
                                                                     t * 128 + r4));
             s.x += v.x;
             s.y += v.y;
