@@ -12,7 +12,8 @@ __device__ __forceinline__ float activate(int act, float v) {
     case GMMFR_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
     case GMMFR_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     case GMMFR_ACT_GELU_TANH:
-      return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+      // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
+      return __fdividef(v, 1.0f + expf(-1.59576912160573071f * (v + 0.044715f * v * v * v)));
     case GMMFR_ACT_SILU: return silu(v);
     default: return v;
   }

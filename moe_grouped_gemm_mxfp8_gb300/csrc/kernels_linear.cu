@@ -22,7 +22,8 @@
 namespace gmmfr {
 namespace lin {
 
-constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr int kThreads = 192;      // stream: warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr int kPairThreads = 320;  // pair: warps 2..9 epilogue
 constexpr int kBK = 64;        // K per stage: 128-byte rows
 constexpr int kTileBytes = 128 * 128;
 
@@ -30,8 +31,8 @@ constexpr int kTileBytes = 128 * 128;
 constexpr int kPairArena = 6 * 32768;
 constexpr int kPairMaxStages = 10;
 constexpr int kPairBars = 2 * kPairMaxStages + 5;
-constexpr int kPairTurnOff = kPairArena + kPairBars * 8 + 32;  // float [4][32][33]: an epilogue warp's 32 x 32 outputs
-constexpr int kPairSmem = kPairTurnOff + 4 * 32 * 33 * 4 + 1024;
+constexpr int kPairTurnOff = kPairArena + kPairBars * 8 + 32;  // float [8][32][33]: an epilogue warp's 32 x 32 outputs
+constexpr int kPairSmem = kPairTurnOff + 8 * 32 * 33 * 4 + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget");
 
 // ---- stream form
@@ -93,14 +94,39 @@ __device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, 
     }
   } else {
     // rows off 16-byte boundaries, or the ragged last columns: turned around in shared memory, so that the warp
-    // writes one row after the other in consecutive elements
+    // writes one row after the other in consecutive elements, eight rows in flight
 #pragma unroll
     for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = v[j];
     __syncwarp();
     const int rows = p.M - m0 < 32 ? (int)(p.M - m0) : 32;
     if (n + lane < p.N) {
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) store_out(p, m0 + r, n + lane, turn[r * 33 + lane]);
+      const __nv_bfloat16* res = p.residual ? p.residual + m0 * p.ldr + n + lane : nullptr;
+      __nv_bfloat16* o16 = static_cast<__nv_bfloat16*>(p.out) + m0 * p.ldo + n + lane;
+      float* o32 = static_cast<float*>(p.out) + m0 * p.ldo + n + lane;
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+        float f[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) f[r] = turn[(r0 + r) * 33 + lane];
+        if (res) {
+          __nv_bfloat16 w[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) w[r] = r0 + r < rows ? res[r * p.ldr] : __nv_bfloat16(0.f);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) f[r] += __bfloat162float(w[r]);
+          res += 8 * p.ldr;
+        }
+        if (p.out_f32) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r0 + r < rows) o32[r * p.ldo] = f[r];
+          o32 += 8 * p.ldo;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r0 + r < rows) o16[r * p.ldo] = __float2bfloat16_rn(f[r]);
+          o16 += 8 * p.ldo;
+        }
+      }
     }
     __syncwarp();
   }
@@ -216,7 +242,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
 // Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
 // tiles in flight share rows of x and of W in L2.
 template <int kAct, int kKps>
-__global__ void __launch_bounds__(lin::kThreads, 1)
+__global__ void __launch_bounds__(lin::kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   extern __shared__ uint8_t smem_raw[];
@@ -244,7 +270,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&acce[b]), 8);
+      ptx::mbar_init(ptx::smem_u32(&acce[b]), 16);
     }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0;
@@ -368,8 +394,9 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
-    float* turn = reinterpret_cast<float*>(smem + lin::kPairTurnOff) + q * 32 * 33;
+    // two warps per TMEM lane quadrant, taking its 32-column chunks in turn
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    float* turn = reinterpret_cast<float*>(smem + lin::kPairTurnOff) + (warp - 2) * 32 * 33;
     int acc_i = 0;
     for (int t = first; t < tiles; t += pairs) {
       int mt, nt;
@@ -381,7 +408,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
       const int64_t m0 = (int64_t)mt * 256 + rank * 128 + q * 32;  // this warp's rows
       const int cols = kGated ? BN / 2 : BN;
       const int64_t n0 = (int64_t)nt * cols;
-      for (int c0 = 0; c0 < cols; c0 += 32) {
+      for (int c0 = 32 * half; c0 < cols; c0 += 64) {
         uint32_t r[32];
         float v[32];
         ptx::tmem_ld_32x32b_x32(taddr + c0, r);
@@ -765,7 +792,7 @@ static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cud
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)p.grid);
-  lc.blockDim = dim3(lin::kThreads);
+  lc.blockDim = dim3(p.form == kLinearStream ? lin::kThreads : lin::kPairThreads);
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute attr[2];
