@@ -137,13 +137,13 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
 
 // ---------------------------------------------------------------- the router for a few tokens by one cluster
 // A cluster of 8 CTAs takes 8 kTiles tokens: CTA c computes the logits of expert groups c, c + 8, ... (16 experts each,
-// the 16 warps splitting groups and the K range), sends tokens c * kTiles ... to CTA c, which selects for them.  The
+// the 8 warps splitting groups and the K range), sends tokens c * kTiles ... to CTA c, which selects for them.  The
 // weight rows are read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows
 // l / 4 and l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike,
 // which leaves the sums alone), so each row is read in 16-byte pieces with no staging.
 namespace gate {
 constexpr int kCluster = 8;
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;  // 128 registers each: half an SM, so that the kernel that follows fits beside it
 constexpr int kWarps = kThreads / 32;
 template <int kTiles>
 struct Smem {
@@ -175,7 +175,7 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
     }
     float acc[kTiles][4] = {};
     const int blocks = (int)((p.H + 31) / 32);
-    constexpr int kU = kTiles == 1 ? 4 : 2;  // blocks of 32 K in flight
+    constexpr int kU = kTiles == 1 ? 6 : (kTiles == 2 ? 4 : 2);  // blocks of 32 K in flight
     for (int b0 = split; b0 < blocks; b0 += splits * kU) {
       uint4 a[kU], b[kU], x[kU][kTiles];
 #pragma unroll

@@ -92,14 +92,15 @@ cudaError_t launch_ffn_prep_mx(const FfnPrepMxParams& p, cudaStream_t s) {
 namespace layer {
 
 constexpr int kThreads = 256;  // warp 0 weights, 1 MMA, 2..5 epilogue, 6 tokens' producer
-constexpr int kMaxStages = 11;
+constexpr int kMaxStages = 10;
+constexpr int kRound = 8;  // tokens whose SwiGLU values are made at a time
 // A stage: weight tile (with MXFP8 its 512 scale bytes), then the tokens' image: BF16 npad rows of 128 bytes;
 // MXFP8 the scale chunk of hi and lo (512 bytes), npad rows of hi codes, npad of lo.
 __host__ __device__ constexpr int tile_bytes(bool mx) { return mx ? kPrepTileBytes : kWTileBytes; }
 __host__ __device__ constexpr int rows_off(bool mx) { return mx ? kPrepTileBytes + kSfChunk : kWTileBytes; }
 __host__ __device__ constexpr int image_bytes(bool mx, int npad) { return mx ? kSfChunk + 256 * npad : 128 * npad; }
 __host__ __device__ constexpr int stage_bytes(bool mx, int npad) { return tile_bytes(mx) + image_bytes(mx, npad); }
-constexpr int kArena = 11 * 18432;
+constexpr int kArena = 10 * 18432;  // leaves room for a CTA of the front kernel on the same SM
 __host__ __device__ constexpr int n_stages(bool mx, int npad) {
   return kArena / stage_bytes(mx, npad) < kMaxStages ? kArena / stage_bytes(mx, npad) : kMaxStages;
 }
@@ -112,8 +113,8 @@ constexpr int kMaskOff = kMiscOff + 64;                          // uint64 mask[
 constexpr int kActOff = kMaskOff + 8 * kMaxExperts;              // uint16 act[1024]: the chosen experts
 constexpr int kIdsOff = kActOff + 2 * kMaxExperts;               // uint16 ids[64 * 32]
 constexpr int kWtOff = kIdsOff + 2 * kLayerMaxTokens * kMaxTopk; // float weights[64 * 32]
-constexpr int kXchgOff = kWtOff + 4 * kLayerMaxTokens * kMaxTopk;  // float [8][2][32]: values handed over for SwiGLU
-constexpr int kTokWOff = kXchgOff + 8 * 2 * 32 * 4;             // float [64]: the unit's router weights
+constexpr int kXchgOff = kWtOff + 4 * kLayerMaxTokens * kMaxTopk;  // float [kRound][2][32]: values handed over for SwiGLU
+constexpr int kTokWOff = kXchgOff + kRound * 2 * 32 * 4;             // float [64]: the unit's router weights
 constexpr int kSmemBytes = kTokWOff + 4 * kLayerMaxTokens + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 // TMEM: two accumulators of acc_cols columns (MXFP8: the products with hi, then those with lo), then with MXFP8 the
@@ -192,30 +193,26 @@ __device__ __forceinline__ void load_acc16(uint32_t taddr, int npad, float (&v)[
   }
 }
 
-// One run of U tiles in units of K tiles, cut evenly over G CTAs: CTA b has [U b / G, U (b + 1) / G).
+// One run of U tiles in units of K tiles, cut evenly over the first G CTAs: CTA b has [U b / G, U (b + 1) / G).  A
+// small run leaves some CTAs out: fewer than four tiles each save less in streaming than their joins cost.
 // (The host refuses sizes whose U * G passes 32 bits.)
 struct Run {
   uint32_t U, K, G;
-  __device__ uint32_t lo(uint32_t b) const { return U * b / G; }
+  __device__ Run(uint32_t U_, uint32_t K_, uint32_t ctas) : U(U_), K(K_), G(min(ctas, max(1u, U_ / 4))) {}
+  __device__ uint32_t lo(uint32_t b) const { return b < G ? U * b / G : U; }
   __device__ uint32_t owner(uint32_t x) const { return ((x + 1) * G - 1) / U; }
 };
-// The pieces of unit u: with at least as many tiles as CTAs those of n consecutive CTAs from b0, otherwise its
-// tiles, each some CTA's.  A CTA's pieces of cut units lie in its slots: 0 where its range begins in the unit, 1
-// where it ends there; so only the first piece of a unit can lie in slot 1.
+// The pieces of unit u: those of n consecutive CTAs from b0 (every CTA of the run has a tile at least).  A CTA's pieces
+// of cut units lie in its two slots: 0 where its range begins in the unit, 1 where it ends there; so only the first
+// piece of a unit can lie in slot 1.
 struct Pieces {
   uint32_t b0, n, first_slot, x0;
-  bool scattered;  // fewer tiles than CTAs
-  __device__ Pieces(const Run& r, uint32_t u) : x0(u * r.K), scattered(r.U < r.G) {
+  __device__ Pieces(const Run& r, uint32_t u) : x0(u * r.K) {
     b0 = r.owner(x0);
-    n = scattered ? r.K : r.owner(x0 + r.K - 1) - b0 + 1;
+    n = r.owner(x0 + r.K - 1) - b0 + 1;
     first_slot = r.lo(b0) >= x0 ? 0 : 1;
   }
-  // piece i's slot among the CTAs' pairs of slots
-  __device__ uint32_t slot(const Run& r, uint32_t i) const {
-    uint32_t b = b0 + i;
-    if (scattered) b = r.owner(x0 + i);
-    return b * 2 + (i == 0 ? first_slot : 0);
-  }
+  __device__ uint32_t slot(uint32_t i) const { return (b0 + i) * 2 + (i == 0 ? first_slot : 0); }
 };
 
 // The pieces of one CTA: units (or parts of units) of the two runs in order; every role walks them.
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(gate::kThreads) layer_front_kernel(const __gri
 
 // ============================================================================ layer
 template <bool kMx>
-__global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_constant__ LayerParams p) {
+__global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_constant__ LayerParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + layer::kBarOff);  // both producers' copies landed
@@ -404,7 +401,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
   __syncthreads();
   const int D = A * p.KB2 + p.KB2s;  // tiles of one column tile of the down run
   const int n_units = A * p.NT1 + p.NT1s;  // the shared expert's first
-  const Run up{(uint32_t)n_units * p.KB1, (uint32_t)p.KB1, (uint32_t)G}, down{(uint32_t)p.NT2 * D, (uint32_t)D, (uint32_t)G};
+  const Run up((uint32_t)n_units * p.KB1, (uint32_t)p.KB1, (uint32_t)G), down((uint32_t)p.NT2 * D, (uint32_t)D, (uint32_t)G);
   Walk walk(up, down);
   if (warp == 0) {
     // -------------------------------------------------------------- weights
@@ -582,7 +579,7 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
     int owed_unit = -1;
     if (begin < up.lo(blockIdx.x + 1)) {
       const Pieces first(up, begin / up.K);
-      if ((first.scattered ? begin - first.x0 : blockIdx.x - first.b0) == 1) owed_unit = (int)(begin / up.K);
+      if (blockIdx.x - first.b0 == 1) owed_unit = (int)(begin / up.K);
     }
     bool rehearse = owed_unit >= 0;
     bool more = walk.next();
@@ -670,21 +667,67 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             if ((c & 3) < 2) dst[scale_at((c >> 2) * npad + t, 2 + (c & 3))] = 127;
           }
         }
-        // the others, eight at a time: warps 2, 3 (gate rows) take the even ones, warps 4, 5 (up rows) the odd, each
-        // handing the other what it needs
-        const int half = q >= 2, col = (q & 1) * 32 + lane;  // intermediate index within the unit
-        for (unsigned long long m = mask; m;) {
-          int tok[8];
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            tok[i] = m ? __ffsll((long long)m) - 1 : -1;
-            m &= m - 1;
+        // the others
+        auto store_sw = [&](int t, int col, float sw) {  // col: intermediate index within the unit, a lane each
+          if constexpr (!kMx) {
+            *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(sw);
+          } else {
+            const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
+            uint32_t hi, lo;
+            split_e4m3(sw, b, hi, lo);
+            const int c = (j & 1) * 64 + col;
+            uint8_t* at = dst + kSfChunk + image_chunk(t, c >> 4) + (c & 15);
+            at[0] = (uint8_t)hi;
+            at[npad * 128] = (uint8_t)lo;
+            if (lane == 0) {
+              dst[scale_at(t, c >> 5)] = (uint8_t)b.byte_hi;
+              dst[scale_at(npad + t, c >> 5)] = (uint8_t)b.byte_lo;
+            }
           }
-          if (whole) {
-            uint32_t r[8], l[8];
+        };
+        if (owed) {
+          // from the slots: a thread takes both rows of an index, for every other token
+          const int col = ep & 63;
+          unsigned long long m = mask;
+          if (ep >= 64) m &= m - 1;  // the second, fourth, ...
+          while (m) {
+            constexpr int kTok = 4;
+            int tok[kTok];
+            float gate_v[kTok] = {}, up_v[kTok] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kTok; ++i) {
+              tok[i] = m ? __ffsll((long long)m) - 1 : -1;
+              m &= m - 1;
+              m &= m - 1;
+            }
+#pragma unroll 4
+            for (uint32_t k = 0; k < n_pieces; ++k) {
+              const float* slot = p.slots_up + (int64_t)pieces.slot(k) * slot_floats + col;
+#pragma unroll
+              for (int i = 0; i < kTok; ++i) {
+                if (tok[i] >= 0) {
+                  gate_v[i] += __ldcg(slot + tok[i] * 128);
+                  up_v[i] += __ldcg(slot + tok[i] * 128 + 64);
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)
+              if (tok[i] >= 0) store_sw(tok[i], col, silu(gate_v[i]) * up_v[i] * s_tokw[tok[i]]);
+          }
+        } else {
+          // from TMEM, kRound tokens at a time: warps 2, 3 (gate rows) take the even ones, warps 4, 5 (up rows) the odd,
+          // each handing the other what it needs
+          constexpr int kRound = layer::kRound;
+          const int half = q >= 2, col = (q & 1) * 32 + lane;
+          for (unsigned long long m = mask; m;) {
+            int tok[kRound];
+            uint32_t r[kRound], l[kRound];
+            float v[kRound];
+#pragma unroll
+            for (int i = 0; i < kRound; ++i) {
+              tok[i] = m ? __ffsll((long long)m) - 1 : -1;
+              m &= m - 1;
               if (tok[i] >= 0) {
                 r[i] = ptx::tmem_ld_32x32b_x1(taddr + tok[i]);
                 if constexpr (kMx) l[i] = ptx::tmem_ld_32x32b_x1(taddr + npad + tok[i]);
@@ -692,45 +735,19 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
             }
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = kMx ? __uint_as_float(r[i]) + __uint_as_float(l[i]) : __uint_as_float(r[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll 4
-            for (uint32_t k = 0; k < n_pieces; ++k) {
-              const float* slot = p.slots_up + (int64_t)pieces.slot(up, k) * slot_floats + row;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (tok[i] >= 0) v[i] += __ldcg(slot + tok[i] * 128);
+            for (int i = 0; i < kRound; ++i) {
+              v[i] = kMx ? __uint_as_float(r[i]) + __uint_as_float(l[i]) : __uint_as_float(r[i]);
+              if ((i & 1) != half) xchg[(i * 2 + (q & 1)) * 32 + lane] = v[i];
             }
-          }
+            ptx::bar_sync(1, 128);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((i & 1) != half) xchg[(i * 2 + (q & 1)) * 32 + lane] = v[i];
-          ptx::bar_sync(1, 128);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = half ? tok[2 * i + 1] : tok[2 * i];
-            if (t < 0) break;
-            const float mine = half ? v[2 * i + 1] : v[2 * i], other = xchg[((2 * i + half) * 2 + (q & 1)) * 32 + lane];
-            const float sw = silu(half ? other : mine) * (half ? mine : other) * s_tokw[t];
-            if constexpr (!kMx) {
-              *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(sw);
-            } else {
-              const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
-              uint32_t hi, lo;
-              split_e4m3(sw, b, hi, lo);
-              const int c = (j & 1) * 64 + col;
-              uint8_t* at = dst + kSfChunk + image_chunk(t, c >> 4) + (c & 15);
-              at[0] = (uint8_t)hi;
-              at[npad * 128] = (uint8_t)lo;
-              if (lane == 0) {
-                dst[scale_at(t, c >> 5)] = (uint8_t)b.byte_hi;
-                dst[scale_at(npad + t, c >> 5)] = (uint8_t)b.byte_lo;
-              }
+            for (int i = 0; i < kRound / 2; ++i) {
+              const int t = half ? tok[2 * i + 1] : tok[2 * i];
+              const float mine = half ? v[2 * i + 1] : v[2 * i], other = xchg[((2 * i + half) * 2 + (q & 1)) * 32 + lane];
+              if (t >= 0) store_sw(t, col, silu(half ? other : mine) * (half ? mine : other) * s_tokw[t]);
             }
+            if (m) ptx::bar_sync(1, 128);  // xchg is written again
           }
-          if (m) ptx::bar_sync(1, 128);  // xchg is written again
         }
         asm volatile("fence.proxy.async;" ::: "memory");  // sw is read by bulk copies
         ptx::bar_sync(1, 128);
@@ -747,27 +764,30 @@ __global__ void __launch_bounds__(layer::kThreads, 1) layer_kernel(const __grid_
         more = walk.next();
       }
     }
-    // the cut column tiles: this CTA's share of each, once all its pieces are there
+    // the cut column tiles (at most two): this CTA's share of each, once all its pieces are there
     const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 7) == 0 &&
                      ((p.ld_out | p.ld_residual) & 3) == 0;
-    if (ok && !*abort_flag) {
-      for (int c = 0; c < n_cut; ++c) {
-        const int j = c == 0 ? cut0 : cut1;
-        const Pieces pieces(down, j);
-        const int n = pieces.n;
-        if (ep == 0) ok = wait_count(p.down_cnt + j, n, ctl);
-        if (!ptx::bar_all(1, 128, ok)) break;
-        const int mine = down.U < down.G ? down.lo(blockIdx.x) - pieces.x0 : blockIdx.x - pieces.b0;
-        const int total = T * 32, lo = total * mine / n, hi = total * (mine + 1) / n;
-        for (int i = lo + ep; i < hi; i += 128) {
+    if (ok && !*abort_flag && n_cut > 0) {
+      const Pieces pa(down, cut0), pb(down, n_cut > 1 ? cut1 : cut0);
+      if (ep == 0) ok = wait_count(p.down_cnt + cut0, pa.n, ctl);
+      if (ep == 32 && n_cut > 1) ok = wait_count(p.down_cnt + cut1, pb.n, ctl);
+      if (ptx::bar_all(1, 128, ok)) {
+        const int total = T * 32, a_lo = total * (int)(blockIdx.x - pa.b0) / (int)pa.n,
+                  a_n = total * (int)(blockIdx.x - pa.b0 + 1) / (int)pa.n - a_lo,
+                  b_lo = total * (int)(blockIdx.x - pb.b0) / (int)pb.n,
+                  b_n = n_cut > 1 ? total * (int)(blockIdx.x - pb.b0 + 1) / (int)pb.n - b_lo : 0;
+        for (int x = ep; x < a_n + b_n; x += 128) {
+          const bool in_a = x < a_n;
+          const int i = in_a ? a_lo + x : b_lo + x - a_n, j = in_a ? cut0 : cut1, n = in_a ? pa.n : pb.n;
+          const uint32_t b0 = in_a ? pa.b0 : pb.b0, first_slot = in_a ? pa.first_slot : pb.first_slot;
           const int t = i >> 5, r4 = (i & 31) * 4;
           const int64_t col = (int64_t)j * 128 + r4;
           if (col >= g.H) continue;
+          const float* slot = p.slots_down + (int64_t)(b0 * 2) * slot_floats + t * 128 + r4;
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
           for (int k = 0; k < n; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.slots_down + (int64_t)pieces.slot(down, k) * slot_floats +
-                                                                    t * 128 + r4));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(slot + (int64_t)(2 * k + (k == 0 ? first_slot : 0)) * slot_floats));
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
