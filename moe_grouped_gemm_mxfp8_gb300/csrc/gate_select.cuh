@@ -21,7 +21,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {  // of a key above 1
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// One warp selects token `logits[0..E)`'s experts; lane k < topk returns the k-th expert and its
+// One warp selects token `logits[0..E)`'s experts (long choices of many experts); lane k < topk returns the k-th expert and its
 // weight.  Expert e sits in lane e % 32, register e / 32 (kPer registers: E <= 32 * kPer).
 // All sums are FP32; the exponential's argument is at most 0 and its sum at least 1.  Maxima and minima over the
 // warp are single redux instructions on order-preserving integers.
@@ -136,33 +136,192 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
 }
 
 // ---------------------------------------------------------------- the router for a few tokens by one cluster
-// A cluster of 8 CTAs takes 8 kTiles tokens: CTA c computes the logits of expert groups c, c + 8, ... (16 experts each,
-// the 8 warps splitting groups and the K range), sends tokens c * kTiles ... to CTA c, which selects for them.  The
-// weight rows are read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows
-// l / 4 and l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike,
-// which leaves the sums alone), so each row is read in 16-byte pieces with no staging.
+// A cluster of 8 CTAs takes 8 kTiles tokens.  Its 64 warps share the products: a warp takes one group of 16 experts and
+// one of 64 / groups splits of K (blocks of 32, taken in turn) against all the tokens, and sends its sums straight to
+// the CTAs that select for those tokens (CTA c: tokens c * kTiles ...), which add the splits in order.  The weight rows
+// are read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows l / 4 and
+// l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike, which leaves
+// the sums alone), so each row is read in 16-byte pieces with no staging.
+// One token of H = 2048 and 256 experts takes 6.6 us: about 3 until the weights are there (they come through 8 SMs in
+// three rounds of loads), 0.6 for the sums, 2.9 for the selection, all of it latency.
 namespace gate {
 constexpr int kCluster = 8;
 constexpr int kThreads = 256;  // 128 registers each: half an SM, so that the kernel that follows fits beside it
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCand = 256;
+// What a team of threads needs to select for one token.
+struct TeamScratch {
+  uint32_t cand_key[kMaxCand];
+  uint16_t cand_e[kMaxCand];
+  uint32_t group_key[kMaxGroups];
+  uint32_t eligible[2];
+  float stat[16];
+  uint32_t out_e[kMaxTopk];
+  float out_p[kMaxTopk];
+};
 template <int kTiles>
 struct Smem {
-  float part[kWarps][16][8 * kTiles + 1];   // a warp's sums
-  float logits[kTiles][kMaxExperts];        // of the tokens this CTA selects for
+  float logits[kTiles][kMaxExperts];  // of the tokens this CTA selects for: the splits' sums, the logits, the probabilities
+  uint32_t key[kTiles][kMaxExperts];
+  TeamScratch team[kTiles];
+  float bias[kMaxExperts];
 };
 }  // namespace gate
 
+// Selects for one token with kTeam threads (`tid` 0 .. kTeam - 1, named barrier `bar`), in steps that are short even
+// when no instruction of them is in the cache yet (3.8 us by one warp, 2.9 by eight: 256 experts, sigmoid, groups):
+//   scores and keys, a thread per expert;  groups, a warp per group
+//   per 32 consecutive experts their topk best, by counting for each lane the keys that precede it (equal keys: the lower
+//   index precedes)
+//   of those candidates the topk best, again by counting
+// p holds the logits and then the probabilities.  At most kMaxCand candidates (topk per 32 experts).
+template <int kTeam>
+__device__ __forceinline__ void gate_select_team(const GateRule& r, const float* select_bias, float* p, uint32_t* key,
+                                                 gate::TeamScratch& sc, int tid, int bar, void* ids, int ids_i64,
+                                                 float* weights, int64_t out_at) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kTeamWarps = kTeam / 32;
+  const float kNegInf = __int_as_float(0xff800000);
+  const int lane = tid & 31, warp = tid >> 5, E = r.E, topk = r.topk;
+  auto sync = [&]() { ptx::bar_sync(bar, kTeam); };
+  float inv = 1.f, mx = kNegInf;
+  if (!r.sigmoid) {
+    for (int e = tid; e < E; e += kTeam) mx = fmaxf(mx, p[e]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    if (lane == 0) sc.stat[warp] = mx;
+    sync();
+#pragma unroll
+    for (int w = 0; w < kTeamWarps; ++w) mx = fmaxf(mx, sc.stat[w]);
+    float sum = 0.f;
+    for (int e = tid; e < E; e += kTeam) {
+      // logits that are all -inf leave nothing to weigh: p = 0 (a NaN among them stays one)
+      const float l = p[e], v = mx == kNegInf ? (l != l ? l : 0.f) : expf(l - mx);
+      p[e] = v;
+      sum += v;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (lane == 0) sc.stat[8 + warp] = sum;
+    sync();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTeamWarps; ++w) sum += sc.stat[8 + w];
+    inv = mx == kNegInf && sum == 0.f ? 0.f : 1.0f / sum;
+  }
+  for (int e = tid; e < E; e += kTeam) {
+    const float v = r.sigmoid ? gate_sigmoid(p[e]) : p[e] * inv;
+    p[e] = v;
+    key[e] = order_key(select_bias ? v + select_bias[e] : v);
+  }
+  sync();
+  const int per = E / r.n_group;
+  if (r.n_group > 1) {
+    for (int g = warp; g < r.n_group; g += kTeamWarps) {
+      uint32_t a = 0, b = 0;  // the lane's two highest keys of the group
+      for (int i = lane; i < per; i += 32) {
+        const uint32_t k = key[g * per + i];
+        b = max(b, min(a, k));
+        a = max(a, k);
+      }
+      const uint32_t top = __reduce_max_sync(kAll, a);
+      float s = top > 1u ? key_value(top) : kNegInf;
+      if (r.group_top == 2) {  // one lane that has the highest gives it up
+        const bool holder = lane == __ffs(__ballot_sync(kAll, a == top)) - 1;
+        const uint32_t second = __reduce_max_sync(kAll, holder ? b : a);
+        s += second > 1u ? key_value(second) : kNegInf;
+      }
+      if (lane == 0) sc.group_key[g] = order_key(s);
+    }
+    sync();
+    if (tid < 64) {  // fewer than topk_group groups are better, or equal and earlier
+      bool in = false;
+      if (tid < r.n_group) {
+        const uint32_t mine = sc.group_key[tid];
+        int better = 0;
+        for (int h = 0; h < r.n_group; ++h) {
+          const uint32_t o = sc.group_key[h];
+          better += (o > mine || (o == mine && h < tid)) ? 1 : 0;
+        }
+        in = better < r.topk_group;
+      }
+      const uint32_t m = __ballot_sync(kAll, in);
+      if (lane == 0) sc.eligible[warp] = m;
+    }
+    sync();
+  }
+  const int segs = (E + 31) / 32;
+  const float per_inv = 1.0f / (float)per;
+  for (int s = warp; s < segs; s += kTeamWarps) {
+    const int e = s * 32 + lane;
+    uint32_t k = e < E ? key[e] : 0u;
+    if (r.n_group > 1 && e < E) {
+      const int g = (int)(((float)e + 0.5f) * per_inv);  // e / per: the half keeps it clear of rounding (e < 1024)
+      if (!((sc.eligible[g >> 5] >> (g & 31)) & 1)) k = 0u;
+    }
+    const uint32_t k_1 = k - 1;  // o >= k of an earlier lane: o > k - 1
+    if (lane < topk) sc.cand_key[s * topk + lane] = 0u;  // places that stay free
+    __syncwarp();
+    int place = 0;
+#pragma unroll 4
+    for (int l = 0; l < 32; ++l) {
+      const uint32_t o = __shfl_sync(kAll, k, l);
+      place += o > (l < lane ? k_1 : k) ? 1 : 0;
+    }
+    if (k != 0 && place < topk) {
+      sc.cand_key[s * topk + place] = k;
+      sc.cand_e[s * topk + place] = (uint16_t)e;
+    }
+  }
+  sync();
+  // several lanes share a candidate when there are threads enough
+  const int n = segs * topk;
+  int sh = 0;
+  while (sh < 4 && (2 << sh) * n <= kTeam) ++sh;
+  const int share = 1 << sh, part = tid & (share - 1);
+  for (int c0 = 0; c0 < n; c0 += kTeam >> sh) {
+    const int c = c0 + (tid >> sh);
+    const uint32_t k = c < n ? sc.cand_key[c] : 0u;
+    int place = 0;  // equal candidates stand in the order of their indices
+#pragma unroll 4
+    for (int o = part; o < n; o += share) {
+      const uint32_t v = sc.cand_key[o];
+      place += (v > k || (v == k && o < c)) ? 1 : 0;
+    }
+    for (int o = share / 2; o > 0; o >>= 1) place += __shfl_xor_sync(kAll, place, o);
+    if (k != 0 && place < topk && part == 0) {
+      sc.out_e[place] = sc.cand_e[c];
+      sc.out_p[place] = p[sc.cand_e[c]];
+    }
+  }
+  sync();
+  if (warp == 0) {
+    float w = lane < topk ? sc.out_p[lane] : 0.f;
+    if (r.renormalise) {
+      float total = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+      w = w / (total + 1e-20f);
+    }
+    if (lane < topk) {
+      if (ids_i64) static_cast<int64_t*>(ids)[out_at + lane] = sc.out_e[lane];
+      else static_cast<int32_t*>(ids)[out_at + lane] = (int32_t)sc.out_e[lane];
+      weights[out_at + lane] = w * r.scale;
+    }
+  }
+}
+
 template <int kTiles>
-__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem<kTiles>& sm, uint32_t rank) {
-  constexpr int kTok = 8 * kTiles;
-  ptx::cluster_arrive_relaxed();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int E = p.rule.E, groups = (E + 15) / 16;
-  const int per_cta = (groups + gate::kCluster - 1) / gate::kCluster;  // 1..8
-  const int splits = gate::kWarps / per_cta;
-  const int gi = warp % per_cta, split = warp / per_cta;
-  const int grp = (int)rank + gate::kCluster * gi;
-  if (split < splits && grp < groups) {
+__device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t t0, gate::Smem<kTiles>& sm, uint32_t rank,
+                                                    int warp, int lane) {
+  const int tid = threadIdx.x, E = p.rule.E, groups = (E + 15) / 16;
+  const int blocks = (int)((p.H + 31) / 32);
+  constexpr int kU = kTiles == 1 ? 6 : (kTiles == 2 ? 4 : 2);  // blocks of 32 K in flight
+  const int w = (int)rank * gate::kWarps + warp;
+  const int splits = min(gate::kCluster * gate::kWarps / groups, (blocks + kU - 1) / kU);
+  const int split = w / groups, grp = w - split * groups;
+  ptx::cluster_wait();  // the other CTAs have started: their shared memory may be written
+  if (split < splits) {
     // rows past the end repeat the last one; what they give is not read
     const int ea = min(grp * 16 + (lane >> 2), E - 1), eb = min(grp * 16 + 8 + (lane >> 2), E - 1);
     const __nv_bfloat16* wa = p.weight + (int64_t)ea * p.H;
@@ -174,8 +333,6 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
       xr[i] = p.x + (t < p.T ? t : p.T - 1) * p.ldx;
     }
     float acc[kTiles][4] = {};
-    const int blocks = (int)((p.H + 31) / 32);
-    constexpr int kU = kTiles == 1 ? 6 : (kTiles == 2 ? 4 : 2);  // blocks of 32 K in flight
     for (int b0 = split; b0 < blocks; b0 += splits * kU) {
       uint4 a[kU], b[kU], x[kU][kTiles];
 #pragma unroll
@@ -199,41 +356,59 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
           ptx::mma_16816(acc[i], a[u].z, b[u].z, a[u].w, b[u].w, x[u][i].z, x[u][i].w);
         }
     }
+    const int at = split * groups * 16 + grp * 16 + (lane >> 2);  // below 64 x 16
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      float* d = &sm.part[warp][lane >> 2][8 * i + (lane & 3) * 2];
-      d[0] = acc[i][0];
-      d[1] = acc[i][1];
-      d[8 * (kTok + 1)] = acc[i][2];
-      d[8 * (kTok + 1) + 1] = acc[i][3];
-    }
-  }
-  ptx::cluster_wait();  // the other CTAs have started: their shared memory may be written
-  __syncthreads();
-  for (int i = tid; i < per_cta * 16 * kTok; i += gate::kThreads) {
-    const int g = i / (16 * kTok), tok = i / 16 % kTok, r = i & 15;
-    const int e = ((int)rank + gate::kCluster * g) * 16 + r;
-    if (e < E && t0 + tok < p.T) {
-      float s = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < splits; ++k) s += sm.part[k * per_cta + g][r][tok];
-      ptx::st_cluster_f32(ptx::map_to_rank(ptx::smem_u32(&sm.logits[tok % kTiles][e]), (uint32_t)(tok / kTiles)), s);
-    }
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int tok = 8 * i + (lane & 3) * 2 + c;
+        const uint32_t dst = ptx::map_to_rank(ptx::smem_u32(&sm.logits[tok % kTiles][at]), (uint32_t)(tok / kTiles));
+        ptx::st_cluster_f32(dst, acc[i][c]);
+        ptx::st_cluster_f32(dst + 32, acc[i][2 + c]);
+      }
   }
   ptx::cluster_sync();
+  if (splits > 1) {  // the splits' sums, in order
+    constexpr int kTeam = gate::kThreads / kTiles;
+    float* l = sm.logits[tid / kTeam];
+    for (int e = tid % kTeam; e < E; e += kTeam) {
+      float s = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < splits; ++k) s += l[k * groups * 16 + e];
+      l[e] = s;
+    }
+    __syncthreads();
+  }
+}
+
+template <int kTiles>
+__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem<kTiles>& sm, uint32_t rank) {
+  constexpr int kTeam = gate::kThreads / kTiles;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int E = p.rule.E;
   const int64_t t = t0 + rank * kTiles;
+  const bool by_team = (E + 31) / 32 * p.rule.topk <= gate::kMaxCand;
+  ptx::cluster_arrive_relaxed();
+  if (p.select_bias)
+    for (int e = tid; e < E; e += gate::kThreads) sm.bias[e] = p.select_bias[e];
+  gate_cluster_logits<kTiles>(p, t0, sm, rank, warp, lane);
   if (p.logits) {
     for (int i = 0; i < kTiles; ++i)
       if (t + i < p.T)
         for (int e = tid; e < E; e += gate::kThreads) p.logits[(t + i) * E + e] = sm.logits[i][e];
+    __syncthreads();  // the probabilities take the logits' place
   }
-  if (warp < kTiles && t + warp < p.T) {
+  const float* bias = p.select_bias ? sm.bias : nullptr;
+  if (by_team) {
+    const int i = tid / kTeam;  // the team's token
+    if (t + i < p.T)
+      gate_select_team<kTeam>(p.rule, bias, sm.logits[i], sm.key[i], sm.team[i], tid % kTeam, 1 + i, p.ids, p.ids_i64,
+                              p.weights, (t + i) * p.rule.topk);
+  } else if (warp < kTiles && t + warp < p.T) {
     const float* l = sm.logits[warp];
     int id;
     float w;
-    if (E <= 64) gate_select_warp<2>(p.rule, l, p.select_bias, lane, id, w);
-    else if (E <= 256) gate_select_warp<8>(p.rule, l, p.select_bias, lane, id, w);
-    else gate_select_warp<32>(p.rule, l, p.select_bias, lane, id, w);
+    gate_select_warp<32>(p.rule, l, bias, lane, id, w);
     if (lane < p.rule.topk) {
       const int64_t o = (t + warp) * p.rule.topk + lane;
       if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = id;

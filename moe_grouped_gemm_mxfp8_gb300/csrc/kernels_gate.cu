@@ -567,9 +567,9 @@ cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t 
   lc.numAttrs = 2;
   lc.stream = s;
   if (!p.pair) {
-    // tokens per cluster: the fewest whose clusters all run at once (15 of 8 CTAs: 256 tokens of 256 experts took
-    // 16.5 us in 16 clusters of 16, 10 in 8 of 32)
-    const int tiles = p.T <= 15 * 8 ? 1 : (p.T <= 15 * 16 ? 2 : 4);
+    // tokens per cluster: the fewest whose clusters all run at once (32 of 8 CTAs, two CTAs per SM).  H = 2048, 256
+    // experts: 256 tokens 9.5 us in clusters of 8, 11.8 of 16; 512 tokens 12.4 of 16, 18.0 of 32 and of 8
+    const int tiles = p.T <= 32 * 8 ? 1 : (p.T <= 32 * 16 ? 2 : 4);
     lc.gridDim = dim3((unsigned)((p.T + 8 * tiles - 1) / (8 * tiles) * gate::kCluster));
     lc.blockDim = dim3(gate::kThreads);
     return cudaLaunchKernelEx(&lc, tiles == 1 ? gate_cluster_kernel<1> : (tiles == 2 ? gate_cluster_kernel<2> : gate_cluster_kernel<4>), p);

@@ -96,6 +96,11 @@ GATES = [
     dict(T=961, H=128, E=64, topk=32, scoring="sigmoid", n_group=64, topk_group=33, group_top=1),
     dict(T=40000, H=64, E=36, topk=5, scoring="sigmoid", n_group=12, topk_group=5),
     dict(T=530, H=64, E=600, topk=8, scoring="softmax"),
+    dict(T=1025, H=72, E=7, topk=7, scoring="softmax", renormalise=False),
+    dict(T=1025, H=128, E=64, topk=32, scoring="sigmoid", n_group=64, topk_group=33, group_top=1),
+    dict(T=300, H=200, E=500, topk=32, scoring="sigmoid", n_group=5, topk_group=2),
+    dict(T=530, H=136, E=129, topk=20, scoring="softmax"),
+    dict(T=9, H=2048, E=16, topk=4, scoring="softmax"),
 ]
 
 
