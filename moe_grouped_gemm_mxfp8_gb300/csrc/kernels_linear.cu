@@ -1,11 +1,13 @@
 // The dense product with its epilogue: y = act(x W^T + bias) + residual.
 //
 // Three forms, all on the tensor cores with FP32 sums:
-//   direct  up to 32 rows of x.  Weights from global memory straight into the operand registers of mma.sync: no
+//   direct  up to 32 rows of x and small weights.  Weights from global memory straight into the operand registers of mma.sync: no
 //           staging, no accumulator to set up; what counts here is the time to the first byte and the last.
-//   stream  (tcgen05 kind::f16, accumulators in TMEM, operands by TMA) up to 128 rows.  The weights are the 128-row operand, the rows of x the N-wide one, so every
-//           weight byte crosses HBM once; the K range of a tile is split over the CTAs of a cluster, whose
-//           partial sums meet in shared memory (in rank order: deterministic).
+//   stream  up to 128 rows (tcgen05 kind::f16, accumulators in TMEM, operands by TMA).  The weights are the 128-row
+//           operand, the rows of x the N-wide one, so every weight byte crosses HBM once; the K range of a tile is
+//           split over the CTAs of a cluster, whose partial sums meet in shared memory (in rank order: deterministic).
+//           W of 4096 x 14336 takes 22.9 us with 64 rows (5.2 TB/s; 6.8 in the loop, about 5 us are launch, ramp and
+//           join), the gated 2 x 2048 x 7168 with 48 rows 14.6 us.
 //   pair    many rows.  A pair of CTAs holds a 256 x BN tile of y (cta_group::2: each CTA loads 128 rows of x
 //           and half of the BN rows of W), accumulators double-buffered in TMEM, so that a tile's epilogue
 //           runs beside the next tile's products.
@@ -22,7 +24,7 @@
 namespace gmmfr {
 namespace lin {
 
-constexpr int kThreads = 192;      // stream: warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr int kThreads = 320;      // stream: warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
 constexpr int kPairThreads = 320;  // pair: warps 2..9 epilogue
 constexpr int kBK = 64;        // K per stage: 128-byte rows
 constexpr int kTileBytes = 128 * 128;
@@ -38,10 +40,10 @@ static_assert(kPairSmem <= 232448, "shared memory budget");
 // ---- stream form
 constexpr int kStreamMaxStages = 11;
 constexpr int kStreamBars = 2 * kStreamMaxStages + 6;
-// ring and partial sums: two CTAs share an SM, or one has it
-__host__ __device__ constexpr int stream_arena(int per_sm) { return per_sm == 2 ? 104 * 1024 : 220 * 1024; }
-__host__ __device__ constexpr int stream_smem(int per_sm) { return stream_arena(per_sm) + kStreamBars * 8 + 32 + 1024; }
-static_assert(2 * (stream_smem(2) + 1024) <= 228 * 1024 && stream_smem(1) <= 232448, "shared memory budget");
+constexpr int kStreamKps = 2;  // K blocks per stage: 0.33 us per stage where a CTA has the memory to itself, 0.25 with one
+constexpr int kStreamArena = 220 * 1024;  // the ring, and the partial sums unless they take its place
+constexpr int kStreamSmem = kStreamArena + kStreamBars * 8 + 32 + 1024;
+static_assert(kStreamSmem <= 232448, "shared memory budget");
 
 }  // namespace lin
 
@@ -457,13 +459,14 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
 // Cluster c takes the tiles c, c + clusters, ...; its CTA of rank r the K blocks [KB r / S, KB (r + 1) / S).
 // A tile is 128 rows of W; with the gated activation 64 gate rows and the 64 up rows of the same columns.
 template <int kAct>
-__global__ void __launch_bounds__(lin::kThreads, 2)
+__global__ void __launch_bounds__(lin::kThreads, 1)
     linear_stream_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   constexpr int kCols = kGated ? 64 : 128;  // columns of y per tile
+  constexpr int kEpi = lin::kThreads - 64, kKps = lin::kStreamKps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::stream_arena(p.per_sm));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::kStreamArena);
   uint64_t* empty = full + lin::kStreamMaxStages;
   uint64_t* accf = empty + lin::kStreamMaxStages;
   uint64_t* acce = accf + 1;
@@ -478,8 +481,10 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   const int S = p.split;
   const uint32_t rank = S > 1 ? ptx::cluster_rank() : 0u;
   const int T = (int)p.M, npad = p.bn;
-  const int stage_bytes = lin::kTileBytes + npad * 128, n_stages = p.n_stages;
-  float* part = reinterpret_cast<float*>(smem + n_stages * stage_bytes);  // [T][128]
+  const int block_bytes = lin::kTileBytes + npad * 128, stage_bytes = kKps * block_bytes, n_stages = p.n_stages;
+  const int clusters = gridDim.x / S, first = blockIdx.x / S, tiles = p.tiles_n;
+  // [T][128]: in the ring's place when no tile follows, whose loads would write there
+  float* part = reinterpret_cast<float*>(smem + (tiles <= clusters ? 0 : n_stages * stage_bytes));
   const uint32_t tmem_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128);
 
   if (threadIdx.x == 0) {
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
     ptx::mbar_init(ptx::smem_u32(accf), 1);
-    ptx::mbar_init(ptx::smem_u32(acce), 4);
+    ptx::mbar_init(ptx::smem_u32(acce), 8);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     ptx::mbar_init(ptx::smem_u32(pready), S);
     ptx::mbar_init(ptx::smem_u32(pfree), S);
@@ -508,9 +513,8 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   const uint32_t tmem_base = *tmem_slot;
   const Ctl ctl{abort_flag, s_err, p.timeout_ns};
   const uint32_t smem_base = ptx::smem_u32(smem);
-  const int clusters = gridDim.x / S, first = blockIdx.x / S;
-  const int tiles = p.tiles_n;
-  const int kb0 = (int)((int64_t)p.KB * rank / S), kb1 = (int)((int64_t)p.KB * (rank + 1) / S);
+  const int units = (p.KB + kKps - 1) / kKps;  // what lies past K is loaded as zeros
+  const int kb0 = (int)((int64_t)units * rank / S), kb1 = (int)((int64_t)units * (rank + 1) / S);
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
@@ -523,7 +527,7 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
     uint32_t sb = smem_base;
     for (int t = first; ok && t < tiles; t += clusters) {
       const int y = t * (kGated ? 64 : 128), y_up = (int)p.N + t * 64;
-      for (int kb = kb0, x = kb0 * lin::kBK; kb < kb1; ++kb, x += lin::kBK) {
+      for (int kb = kb0, x = kb0 * kKps * lin::kBK; kb < kb1; ++kb, x += kKps * lin::kBK) {
         if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
           ok = false;
           break;
@@ -531,9 +535,13 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
         if (ptx::elect_one()) {
           const uint32_t fb = full0 + 8 * stage;
           ptx::mbar_arrive_expect_tx(fb, stage_bytes);
-          ptx::tma_load_2d(sb, &maps.w, x, y, fb, pol_w);
-          if constexpr (kGated) ptx::tma_load_2d(sb + 64 * 128, &maps.w, x, y_up, fb, pol_w);
-          ptx::tma_load_2d(sb + lin::kTileBytes, &maps.x, x, 0, fb, pol_x);
+#pragma unroll
+          for (int h = 0; h < kKps; ++h) {
+            const uint32_t d = sb + h * block_bytes;
+            ptx::tma_load_2d(d, &maps.w, x + h * lin::kBK, y, fb, pol_w);
+            if constexpr (kGated) ptx::tma_load_2d(d + 64 * 128, &maps.w, x + h * lin::kBK, y_up, fb, pol_w);
+            ptx::tma_load_2d(d + lin::kTileBytes, &maps.x, x + h * lin::kBK, 0, fb, pol_x);
+          }
         }
         sb += stage_bytes;
         if (++stage == n_stages) {
@@ -556,7 +564,8 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
   } else if (warp == 1) {
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(npad >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
-    const uint32_t lo0 = (uint32_t)da0, desc_hi = (uint32_t)(da0 >> 32), lo_step = (uint32_t)stage_bytes >> 4;
+    const uint32_t lo0 = (uint32_t)da0, desc_hi = (uint32_t)(da0 >> 32), lo_step = (uint32_t)stage_bytes >> 4,
+                   lo_block = (uint32_t)block_bytes >> 4;
     const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
     int stage = 0;
     uint32_t phase = 0, aph = 0, lo = lo0;
@@ -573,8 +582,11 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            ptx::tc_mma_f16_lo(tmem_base, lo + 2 * q, lo + (lin::kTileBytes >> 4) + 2 * q, desc_hi, idesc, q > 0 ? 1u : accumulate);
+          for (int h = 0; h < kKps; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              ptx::tc_mma_f16_lo(tmem_base, lo + h * lo_block + 2 * q, lo + h * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi,
+                                 idesc, h + q > 0 ? 1u : accumulate);
           ptx::tc_commit(empty0 + 8 * stage);
           if (kb == kb1 - 1) ptx::tc_commit(ptx::smem_u32(accf));
         }
@@ -598,10 +610,10 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
       bool ok = warp_wait_quick(ptx::smem_u32(accf), ph, ctl);
       // the partial sums of the tile before have been read by every CTA of the cluster
       if (ok && S > 1) ok = wait_bar_cluster(ptx::smem_u32(pfree), ph ^ 1, ctl);
-      if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
+      if (!ptx::bar_all(1, kEpi, ok)) break;  // the warps leave together: they share named barriers
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
-      for (int c0 = 0; c0 < T; c0 += 16) {
+      for (int c0 = (warp - 2) / 4 * 16; c0 < T; c0 += 32) {
         uint32_t r[16];
         ptx::tmem_ld_32x32b_x16(taddr + c0, r);
         ptx::tmem_wait_ld();
@@ -612,57 +624,78 @@ __global__ void __launch_bounds__(lin::kThreads, 2)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(acce));
-      ptx::bar_sync(1, 128);
+      ptx::bar_sync(1, kEpi);
       if (S > 1) {
         if (ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pready), ep));
-        if (!ptx::bar_all(1, 128, wait_bar_cluster(ptx::smem_u32(pready), ph, ctl))) break;
+        if (!ptx::bar_all(1, kEpi, wait_bar_cluster(ptx::smem_u32(pready), ph, ctl))) break;
       }
-      // this CTA's share of the tile's T x kCols outputs, four columns at a time, columns fastest
+      // this CTA's share of the tile's T x kCols outputs, four columns at a time, columns fastest; a thread has kTwo in
+      // flight.  kEpi is a multiple of the column groups: a thread's columns, and with them its bias, stay the same.
       const int total = T * (kCols / 4), lo = (int)((int64_t)total * rank / S), hi = (int)((int64_t)total * (rank + 1) / S);
-      for (int i = lo + ep; i < hi; i += 128) {
-        const int tok = i / (kCols / 4), c = (i - tok * (kCols / 4)) * 4;
-        const int64_t n = (int64_t)t * kCols + c;
-        if (n >= p.N) continue;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
-        const uint32_t a = ptx::smem_u32(part + tok * 128 + c);
+      const int c = (lo + ep) % (kCols / 4) * 4;
+      const int64_t n = (int64_t)t * kCols + c;
+      const int cols = p.N - n < 4 ? (int)(p.N - n) : 4;
+      float bias[4] = {}, bias_up[4] = {};
+      if (p.bias) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < cols) {
+            bias[k] = __bfloat162float(p.bias[n + k]);
+            if constexpr (kGated) bias_up[k] = __bfloat162float(p.bias[p.N + n + k]);
+          }
+      }
+      constexpr int kTwo = 2;
+      for (int i0 = lo + ep; i0 < hi && cols > 0; i0 += kTwo * kEpi) {
+        float4 v[kTwo], u[kTwo];
+        uint2 res[kTwo];
+        uint32_t at[kTwo];
+#pragma unroll
+        for (int w = 0; w < kTwo; ++w) {
+          const int tok = min(i0 + w * kEpi, hi - 1) / (kCols / 4);  // past the end: not stored
+          v[w] = u[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+          at[w] = ptx::smem_u32(part + tok * 128 + c);
+          res[w] = make_uint2(0, 0);
+          if (p.residual && p.vec_out && cols == 4) res[w] = *reinterpret_cast<const uint2*>(p.residual + tok * p.ldr + n);
+        }
 #pragma unroll 4
         for (int s = 0; s < S; ++s) {
-          const uint32_t b = S > 1 ? ptx::map_to_rank(a, s) : a;
-          const float4 w = ptx::ld_cluster_v4(b);
-          v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-          if constexpr (kGated) {
-            const float4 z = ptx::ld_cluster_v4(b + 64 * 4);
-            u = make_float4(u.x + z.x, u.y + z.y, u.z + z.z, u.w + z.w);
+#pragma unroll
+          for (int w = 0; w < kTwo; ++w) {
+            const uint32_t b = S > 1 ? ptx::map_to_rank(at[w], s) : at[w];
+            const float4 x = ptx::ld_cluster_v4(b);
+            v[w] = make_float4(v[w].x + x.x, v[w].y + x.y, v[w].z + x.z, v[w].w + x.w);
+            if constexpr (kGated) {
+              const float4 z = ptx::ld_cluster_v4(b + 64 * 4);
+              u[w] = make_float4(u[w].x + z.x, u[w].y + z.y, u[w].z + z.z, u[w].w + z.w);
+            }
           }
         }
-        float f[4] = {v.x, v.y, v.z, v.w};
-        const float g[4] = {u.x, u.y, u.z, u.w};
-        const int cols = p.N - n < 4 ? (int)(p.N - n) : 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < cols) {
-            if (p.bias) f[k] += __bfloat162float(p.bias[n + k]);
-            if constexpr (kGated) f[k] = silu(f[k]) * (p.bias ? g[k] + __bfloat162float(p.bias[p.N + n + k]) : g[k]);
+        for (int w = 0; w < kTwo; ++w) {
+          if (i0 + w * kEpi >= hi) continue;
+          const int tok = (i0 + w * kEpi) / (kCols / 4);
+          float f[4] = {v[w].x + bias[0], v[w].y + bias[1], v[w].z + bias[2], v[w].w + bias[3]};
+          const float g[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kGated) f[k] = silu(f[k]) * (g[k] + bias_up[k]);
             else f[k] = activate(kAct, f[k]);
           }
-        }
-        if (p.vec_out && cols == 4) {
-          if (p.residual) {
-            const uint2 r = *reinterpret_cast<const uint2*>(p.residual + tok * p.ldr + n);
-            f[0] += bf16_lo(r.x);
-            f[1] += bf16_hi(r.x);
-            f[2] += bf16_lo(r.y);
-            f[3] += bf16_hi(r.y);
-          }
-          if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tok * p.ldo + n) = make_float4(f[0], f[1], f[2], f[3]);
-          else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + tok * p.ldo + n) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-        } else {
+          if (p.vec_out && cols == 4) {
+            f[0] += bf16_lo(res[w].x);
+            f[1] += bf16_hi(res[w].x);
+            f[2] += bf16_lo(res[w].y);
+            f[3] += bf16_hi(res[w].y);
+            if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tok * p.ldo + n) = make_float4(f[0], f[1], f[2], f[3]);
+            else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + tok * p.ldo + n) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < cols) store_out(p, tok, n + k, f[k]);
+            for (int k = 0; k < 4; ++k)
+              if (k < cols) store_out(p, tok, n + k, f[k]);
+          }
         }
       }
-      ptx::bar_sync(1, 128);
+      ptx::bar_sync(1, kEpi);
       if (S > 1 && ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pfree), ep));
     }
   }
@@ -705,16 +738,53 @@ cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, 
 }
 
 // ============================================================================ plan and launch
+// Clusters of S CTAs of the stream form that run at once: what the driver says of this device, whose SMs are not all in
+// groups of 8 (152 SMs: 15 clusters of 8); without an answer, as many as the SMs hold.
+static int64_t stream_slots(int S, int sms) {
+  static int64_t known[4] = {};  // S = 1, 2, 4, 8
+  int at = 0;
+  while ((1 << at) < S) ++at;
+  if (known[at] == 0) {
+    int64_t n = std::max(1, sms / S);
+    if (S > 1) {
+      auto kernel = linear_stream_kernel<GMMFR_ACT_NONE>;
+      cudaLaunchConfig_t lc = {};
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = (unsigned)S;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      lc.gridDim = dim3((unsigned)S);
+      lc.blockDim = dim3(lin::kThreads);
+      lc.dynamicSmemBytes = lin::kStreamSmem;
+      lc.attrs = &attr;
+      lc.numAttrs = 1;
+      int clusters = 0;
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kStreamSmem) == cudaSuccess &&
+          cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc) == cudaSuccess && clusters > 0)
+        n = clusters;
+      else
+        cudaGetLastError();
+    }
+    known[at] = n;
+  }
+  return known[at];
+}
+
 void plan_linear(LinearParams& p, int sms) {
-  p.form = kLinearDirect;
   if (p.M <= kLinearDirectRows) {
     // one CTA per SM: as many row groups each as that takes (up to 8; then in waves)
     const int cols = p.act == GMMFR_ACT_SWIGLU ? 8 : 16;
     const int64_t row_groups = (p.N + cols - 1) / cols;
     p.group_m = 1;
     while (p.group_m < 8 && (row_groups + p.group_m - 1) / p.group_m > sms) ++p.group_m;
-    p.grid = (int32_t)((row_groups + p.group_m - 1) / p.group_m);
-    return;
+    // Its products come out of the registers that the loads need, so it falls behind with rows x weights per CTA: W of
+    // 2048 x 2048 and 32 rows (1.0 M) 6.0 us, the stream form 6.7; 5125 x 1288 and 32 (2.0 M) 8.7 and 7.9;
+    // 7168 x 4096: 8 rows (1.6 M) 12.5 and 13.8, 16 (3.1 M) 13.6 and 13.9, 32 (6.3 M) 17.7 and 14.0.
+    if (p.M == 1 || p.M * p.group_m * 16 * p.K <= 1900000) {
+      p.form = kLinearDirect;
+      p.grid = (int32_t)((row_groups + p.group_m - 1) / p.group_m);
+      return;
+    }
   }
   const int64_t rows_w = p.act == GMMFR_ACT_SWIGLU ? 2 * p.N : p.N;
   p.KB = (int32_t)((p.K + lin::kBK - 1) / lin::kBK);
@@ -723,26 +793,22 @@ void plan_linear(LinearParams& p, int sms) {
     p.bn = (int32_t)((p.M + 15) / 16 * 16);
     p.tiles_m = 1;
     p.tiles_n = (int32_t)(p.act == GMMFR_ACT_SWIGLU ? (p.N + 63) / 64 : (p.N + 127) / 128);
-    // The cluster size and the CTAs per SM that end soonest.  A CTA's rate is its bytes in flight over a round trip
-    // of about 1.4 us (load, product, release), or its share of what HBM or L2 give; about 2 us per wave pass before
-    // the first product and in joining the partial sums.
-    const int stage = lin::kTileBytes + p.bn * 128;
+    // The cluster size that ends soonest, with what was measured: a stage takes a CTA 0.33 us and more with more rows,
+    // or its share of HBM; a wave ends with the epilogue, and with the join in a cluster.  W of 7168 x 4096, 32 rows:
+    // clusters of 1, 2, 4, 8 take 14.9, 14.0, 15.1, 20.8 us; of 512 x 8192: 24.9, 15.3, 10.5, 8.3.
+    const int stage = lin::kStreamKps * (lin::kTileBytes + p.bn * 128), units = (p.KB + lin::kStreamKps - 1) / lin::kStreamKps;
     double best = 1e30;
-    for (int per_sm = 1; per_sm <= 2; ++per_sm) {
-      const int stages = std::min<int>(lin::kStreamMaxStages, (lin::stream_arena(per_sm) - (int)p.M * 512) / stage);
-      if (stages < 2) continue;
-      for (int S = 1; S <= 8 && S <= p.KB; S *= 2) {
-        const int64_t slots = std::max<int64_t>(1, per_sm * sms / S);
-        const int64_t waves = (p.tiles_n + slots - 1) / slots, ctas = std::min<int64_t>(p.tiles_n, slots) * S;
-        const double t_stage = std::max(1.4 / stages, lin::kTileBytes * (double)ctas / 6.7e6);
-        const double t = waves * ((double)((p.KB + S - 1) / S) * t_stage + 2.0);
-        if (t < best) {
-          best = t;
-          p.split = S;
-          p.per_sm = per_sm;
-          p.n_stages = stages;
-          p.grid = (int32_t)ctas;
-        }
+    for (int S = 1; S <= 8 && S <= units; S *= 2) {
+      const int64_t slots = stream_slots(S, sms);
+      const int64_t waves = (p.tiles_n + slots - 1) / slots, ctas = std::min<int64_t>(p.tiles_n, slots) * S;
+      const double t_stage = std::max(0.33 + 0.0009 * p.bn, lin::kStreamKps * lin::kTileBytes * (double)ctas / 6.7e6);
+      const double join = S > 1 ? 1.2 + 0.15 * S : 0.0;
+      const double t = waves * ((double)((units + S - 1) / S) * t_stage + 1.0 + 0.02 * p.bn / S + join);
+      if (t < best) {
+        best = t;
+        p.split = S;
+        p.n_stages = std::min<int>(lin::kStreamMaxStages, (lin::kStreamArena - (waves > 1 ? (int)p.M * 512 : 0)) / stage);
+        p.grid = (int32_t)ctas;
       }
     }
     return;
@@ -776,13 +842,13 @@ template <int kAct>
 static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
   auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct>
                                         : (p.kps == 1 ? linear_pair_kernel<kAct, 1> : linear_pair_kernel<kAct, 2>);
-  const int smem = p.form == kLinearStream ? lin::stream_smem(p.per_sm) : lin::kPairSmem;
+  const int smem = p.form == kLinearStream ? lin::kStreamSmem : lin::kPairSmem;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
     cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         lin::stream_smem(1));
+                                         lin::kStreamSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
     if (e == cudaSuccess)

@@ -93,7 +93,7 @@ struct LinearParams {
   // plan_linear's choice
   int32_t form;              // kLinearDirect, ...
   int32_t bn;                // N of the products: rows of x (stream), columns of a tile before gating (pair)
-  int32_t KB, tiles_m, tiles_n, n_stages, kps, split, per_sm, group_m, grid;
+  int32_t KB, tiles_m, tiles_n, n_stages, kps, split, group_m, grid;
 };
 struct LinearMaps {
   CUtensorMap x, w;
