@@ -415,18 +415,22 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
     lp.w = dst;
     lp.ldw = Kp;
   }
-  gmmfr::plan_linear(lp, sms);
-  gmmfr::LinearMaps maps;
-  if (lp.form != gmmfr::kLinearDirect) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
-    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const bool stream_form = lp.form == gmmfr::kLinearStream;
-    if (!encode_rows(encode, &maps.x, lp.x, p.M, p.K, lp.ldx, stream_form ? lp.bn : 128) ||
-        !encode_rows(encode, &maps.w, lp.w, rows_w, p.K, lp.ldw, stream_form ? (gated ? 64 : 128) : lp.bn / 2))
-      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  gmmfr::LinearParams parts[2] = {lp, lp};
+  gmmfr::plan_linear(parts[0], parts[1], sms);
+  for (const gmmfr::LinearParams& q : parts) {
+    if (q.M == 0) continue;
+    gmmfr::LinearMaps maps;
+    if (q.form != gmmfr::kLinearDirect) {
+      PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+      if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+      const bool stream_form = q.form == gmmfr::kLinearStream;
+      if (!encode_rows(encode, &maps.x, q.x, q.M, q.K, q.ldx, stream_form ? q.bn : 128) ||
+          !encode_rows(encode, &maps.w, q.w, rows_w, q.K, q.ldw, stream_form ? (gated ? 64 : 128) : q.bn / 2))
+        return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    }
+    cudaError_t e = gmmfr::launch_linear(maps, q, s);
+    if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   }
-  cudaError_t e = gmmfr::launch_linear(maps, lp, s);
-  if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   return GMMFR_OK;
 }
 

@@ -155,6 +155,10 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
   __shared__ float part[16][16][kTok + 1];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {  // no wait here can give up
+    p.hdr[0] = 1;
+    p.hdr[1] = 0;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = p.group_m, splits = 16 / groups, grp = warp % groups, split = warp / groups;
   constexpr int kCols = kGated ? 8 : 16;  // columns of y per group
@@ -450,8 +454,8 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
     ptx::tmem_dealloc_pair(tmem_base, 512);
   }
   if (threadIdx.x == 0) {
-    p.hdr[1 + blockIdx.x] = *s_err;
-    if (blockIdx.x == 0) p.hdr[0] = gridDim.x;
+    p.hdr[1 + p.slot_base + blockIdx.x] = *s_err;
+    if (p.slot_base + blockIdx.x == 0) p.hdr[0] = p.slots;
   }
 }
 
@@ -515,7 +519,9 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   const uint32_t smem_base = ptx::smem_u32(smem);
   const int units = (p.KB + kKps - 1) / kKps;  // what lies past K is loaded as zeros
   const int kb0 = (int)((int64_t)units * rank / S), kb1 = (int)((int64_t)units * (rank + 1) / S);
-  ptx::griddep_wait();
+  // Beside the pair form: this kernel starts when every CTA of that one has seen its predecessors end, and may not end
+  // before it does.
+  if (!p.beside) ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
   if (warp == 0) {
@@ -703,13 +709,14 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (S > 1) ptx::cluster_sync();  // other CTAs read this one's partial sums and arrive on its barriers
+  if (p.beside) ptx::griddep_wait();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, tmem_cols);
   }
   if (threadIdx.x == 0) {
-    p.hdr[1 + blockIdx.x] = *s_err;
-    if (blockIdx.x == 0) p.hdr[0] = gridDim.x;
+    p.hdr[1 + p.slot_base + blockIdx.x] = *s_err;
+    if (p.slot_base + blockIdx.x == 0) p.hdr[0] = p.slots;
   }
 }
 
@@ -739,38 +746,72 @@ cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, 
 
 // ============================================================================ plan and launch
 // Clusters of S CTAs of the stream form that run at once: what the driver says of this device, whose SMs are not all in
-// groups of 8 (152 SMs: 15 clusters of 8); without an answer, as many as the SMs hold.
+// groups of 8 (152 SMs: 15 clusters of 8); without an answer, as many as the SMs hold.  One CTA each: `sms`.
 static int64_t stream_slots(int S, int sms) {
-  static int64_t known[4] = {};  // S = 1, 2, 4, 8
-  int at = 0;
-  while ((1 << at) < S) ++at;
-  if (known[at] == 0) {
-    int64_t n = std::max(1, sms / S);
-    if (S > 1) {
-      auto kernel = linear_stream_kernel<GMMFR_ACT_NONE>;
-      cudaLaunchConfig_t lc = {};
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = (unsigned)S;
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      lc.gridDim = dim3((unsigned)S);
-      lc.blockDim = dim3(lin::kThreads);
-      lc.dynamicSmemBytes = lin::kStreamSmem;
-      lc.attrs = &attr;
-      lc.numAttrs = 1;
-      int clusters = 0;
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kStreamSmem) == cudaSuccess &&
-          cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc) == cudaSuccess && clusters > 0)
-        n = clusters;
-      else
-        cudaGetLastError();
+  if (S == 1) return std::max(1, sms);
+  static int64_t known[3] = {};  // S = 2, 4, 8
+  int64_t& n = known[S == 2 ? 0 : (S == 4 ? 1 : 2)];
+  if (n == 0) {
+    auto kernel = linear_stream_kernel<GMMFR_ACT_NONE>;
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    lc.gridDim = dim3((unsigned)S);
+    lc.blockDim = dim3(lin::kThreads);
+    lc.dynamicSmemBytes = lin::kStreamSmem;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kStreamSmem) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc) == cudaSuccess && clusters > 0) {
+      n = clusters;
+    } else {
+      cudaGetLastError();
+      n = std::max(1, sms / S);
     }
-    known[at] = n;
   }
-  return known[at];
+  return n;
 }
 
-void plan_linear(LinearParams& p, int sms) {
+// The stream form's plan on `sms` SMs; microseconds that it takes.  Beside another kernel a tile is one CTA's.
+static double plan_stream(LinearParams& p, int sms, bool beside) {
+  p.form = kLinearStream;
+  p.bn = (int32_t)((p.M + 15) / 16 * 16);
+  p.tiles_m = 1;
+  p.tiles_n = (int32_t)(p.act == GMMFR_ACT_SWIGLU ? (p.N + 63) / 64 : (p.N + 127) / 128);
+  // The cluster size that ends soonest, with what was measured: a stage takes a CTA 0.33 us and more with more rows,
+  // or its share of HBM; a wave ends with the epilogue, and with the join in a cluster.  W of 7168 x 4096, 32 rows:
+  // clusters of 1, 2, 4, 8 take 14.9, 14.0, 15.1, 20.8 us; of 512 x 8192: 24.9, 15.3, 10.5, 8.3.
+  const int stage = lin::kStreamKps * (lin::kTileBytes + p.bn * 128), units = (p.KB + lin::kStreamKps - 1) / lin::kStreamKps;
+  double best = 1e30;
+  for (int S = 1; S <= (beside ? 1 : 8) && S <= units; S *= 2) {
+    const int64_t slots = stream_slots(S, sms);
+    const int64_t waves = (p.tiles_n + slots - 1) / slots, ctas = std::min<int64_t>(p.tiles_n, slots) * S;
+    const double t_stage = std::max(0.33 + 0.0009 * p.bn, lin::kStreamKps * lin::kTileBytes * (double)ctas / 6.7e6);
+    const double join = S > 1 ? 1.2 + 0.15 * S : 0.0;
+    const double t = waves * ((double)((units + S - 1) / S) * t_stage + 1.0 + 0.02 * p.bn / S + join) + 3.0;
+    if (t < best) {
+      best = t;
+      p.split = S;
+      p.n_stages = std::min<int>(lin::kStreamMaxStages, (lin::kStreamArena - (waves > 1 ? (int)p.M * 512 : 0)) / stage);
+      p.grid = (int32_t)ctas;
+    }
+  }
+  return best;
+}
+
+// The pair form's time in microseconds with tiles of bn columns: the products take 2.1 BN cycles per K block, the loads
+// of a CTA's operands (128 + BN / 2 rows of 128 bytes) about a byte per 1/50 cycle; waves of tiles over the pairs.
+static double pair_time(const LinearParams& p, int64_t M, int64_t rows_w, int bn, int pairs, int64_t* tiles) {
+  *tiles = (rows_w + bn - 1) / bn * ((M + 255) / 256);
+  const double waves = (double)((*tiles + pairs - 1) / pairs);
+  return (waves * (p.KB * std::max(2.1 * bn, (16384.0 + 64.0 * bn) / 50.0) + 300.0) + 12.0 * bn) / 1900.0 + 4.0;
+}
+
+void plan_linear(LinearParams& p, LinearParams& tail, int sms) {
+  tail.M = 0;
   if (p.M <= kLinearDirectRows) {
     // one CTA per SM: as many row groups each as that takes (up to 8; then in waves)
     const int cols = p.act == GMMFR_ACT_SWIGLU ? 8 : 16;
@@ -789,53 +830,60 @@ void plan_linear(LinearParams& p, int sms) {
   const int64_t rows_w = p.act == GMMFR_ACT_SWIGLU ? 2 * p.N : p.N;
   p.KB = (int32_t)((p.K + lin::kBK - 1) / lin::kBK);
   if (p.M <= kLinearStreamRows) {
-    p.form = kLinearStream;
-    p.bn = (int32_t)((p.M + 15) / 16 * 16);
-    p.tiles_m = 1;
-    p.tiles_n = (int32_t)(p.act == GMMFR_ACT_SWIGLU ? (p.N + 63) / 64 : (p.N + 127) / 128);
-    // The cluster size that ends soonest, with what was measured: a stage takes a CTA 0.33 us and more with more rows,
-    // or its share of HBM; a wave ends with the epilogue, and with the join in a cluster.  W of 7168 x 4096, 32 rows:
-    // clusters of 1, 2, 4, 8 take 14.9, 14.0, 15.1, 20.8 us; of 512 x 8192: 24.9, 15.3, 10.5, 8.3.
-    const int stage = lin::kStreamKps * (lin::kTileBytes + p.bn * 128), units = (p.KB + lin::kStreamKps - 1) / lin::kStreamKps;
-    double best = 1e30;
-    for (int S = 1; S <= 8 && S <= units; S *= 2) {
-      const int64_t slots = stream_slots(S, sms);
-      const int64_t waves = (p.tiles_n + slots - 1) / slots, ctas = std::min<int64_t>(p.tiles_n, slots) * S;
-      const double t_stage = std::max(0.33 + 0.0009 * p.bn, lin::kStreamKps * lin::kTileBytes * (double)ctas / 6.7e6);
-      const double join = S > 1 ? 1.2 + 0.15 * S : 0.0;
-      const double t = waves * ((double)((units + S - 1) / S) * t_stage + 1.0 + 0.02 * p.bn / S + join);
-      if (t < best) {
-        best = t;
-        p.split = S;
-        p.n_stages = std::min<int>(lin::kStreamMaxStages, (lin::kStreamArena - (waves > 1 ? (int)p.M * 512 : 0)) / stage);
-        p.grid = (int32_t)ctas;
-      }
-    }
+    plan_stream(p, sms, false);
+    p.slots = p.grid;
     return;
   }
   p.form = kLinearPair;
   const int pairs = sms / 2;
-  p.tiles_m = (int32_t)((p.M + 255) / 256);
-  // tile width that ends soonest: the products take 2.1 BN cycles per K block, the loads of a CTA's operands
-  // (128 + BN / 2 rows of 128 bytes) about a byte per 1/50 cycle; waves of tiles over the pairs
+  int64_t tiles;
   double best = 1e30;
   for (int bn = 256; bn >= 64; bn -= 32) {
     if (p.act == GMMFR_ACT_SWIGLU && bn % 64) continue;
-    const int64_t tn = (rows_w + bn - 1) / bn, tiles = tn * p.tiles_m;
-    const double waves = (double)((tiles + pairs - 1) / pairs);
-    const double t = waves * (p.KB * std::max(2.1 * bn, (16384.0 + 64.0 * bn) / 50.0) + 300.0) + 12.0 * bn;
+    const double t = pair_time(p, p.M, rows_w, bn, pairs, &tiles);
     if (t < best) {
       best = t;
       p.bn = bn;
-      p.tiles_n = (int32_t)tn;
     }
   }
-  if (p.act == GMMFR_ACT_SWIGLU) p.tiles_n = (int32_t)((p.N + p.bn / 2 - 1) / (p.bn / 2));
+  // The rows past the last full 256 cost as much as 256.  When the tiles of the others leave SMs idle, the stream form
+  // takes those rows there at the same time.  W of 5120 x 1288: 777 rows 17.8 us, in the pair form alone 20.8; of
+  // 4096 x 4096: 1030 rows 27.4 and 32.8.
+  const int64_t rest = p.M % 256;
+  if (p.M > 256 && rest > 0 && rest <= kLinearStreamRows) {
+    double least = 0.9 * best;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+      if (p.act == GMMFR_ACT_SWIGLU && bn % 64) continue;
+      const double t = pair_time(p, p.M - rest, rows_w, bn, pairs, &tiles);
+      const int left = sms - 2 * (int)std::min<int64_t>(tiles, pairs);
+      if (left < 8 || t >= least) continue;
+      LinearParams q = p;
+      q.M = rest;
+      const double both = std::max(t, plan_stream(q, left, true) + 2.0);
+      if (both < least) {
+        least = both;
+        p.bn = bn;
+        tail = q;
+      }
+    }
+  }
+  if (tail.M) {
+    p.M -= rest;
+    const int64_t at = p.M;
+    tail.x += at * p.ldx;
+    if (tail.residual) tail.residual += at * p.ldr;
+    tail.out = static_cast<char*>(p.out) + at * p.ldo * (p.out_f32 ? 4 : 2);
+    tail.beside = 1;
+  }
+  p.tiles_m = (int32_t)((p.M + 255) / 256);
+  p.tiles_n = (int32_t)(p.act == GMMFR_ACT_SWIGLU ? (p.N + p.bn / 2 - 1) / (p.bn / 2) : (rows_w + p.bn - 1) / p.bn);
   p.kps = p.bn <= 128 && p.KB > 1 ? 2 : 1;
   p.n_stages = std::min<int>(lin::kPairMaxStages, lin::kPairArena / (p.kps * (lin::kTileBytes + p.bn * 64)));
   p.group_m = 8;
   p.grid = (int32_t)(2 * std::min<int64_t>(pairs, (int64_t)p.tiles_m * p.tiles_n));
   p.split = 2;
+  p.slots = p.grid + (tail.M ? tail.grid : 0);
+  tail.slot_base = p.grid;
 }
 
 template <int kAct>

@@ -94,11 +94,14 @@ struct LinearParams {
   int32_t form;              // kLinearDirect, ...
   int32_t bn;                // N of the products: rows of x (stream), columns of a tile before gating (pair)
   int32_t KB, tiles_m, tiles_n, n_stages, kps, split, group_m, grid;
+  int32_t beside;             // 1: started while the launch before it runs, which it has to outlast
+  int32_t slot_base, slots;   // its error words, and how many the call has
 };
 struct LinearMaps {
   CUtensorMap x, w;
 };
-void plan_linear(LinearParams& p, int sms);
+// Chooses p's form.  tail.M > 0: the last rows, taken out of p, are a second launch that runs beside p's.
+void plan_linear(LinearParams& p, LinearParams& tail, int sms);
 cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
 cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t rows, int64_t K, int64_t Kp,
                                   int64_t ld, int sms, cudaStream_t s);

@@ -369,7 +369,8 @@ def _check_linear(x, w, act="none", bias=None, residual=None, out_dtype=torch.bf
 
 LINEARS = [(1, 1, 1), (1, 2048, 2048), (3, 5, 7), (2, 130, 264), (7, 1000, 520), (16, 256, 512), (17, 77, 1032), (33, 4096, 136),
            (48, 300, 1024), (64, 64, 64), (65, 129, 72), (100, 640, 1000), (128, 256, 128), (200, 257, 2051), (300, 1000, 520),
-           (777, 517, 1288), (1025, 384, 4096), (1, 333, 7168), (5, 2000, 1023)]
+           (777, 517, 1288), (1025, 384, 4096), (1, 333, 7168), (5, 2000, 1023), (20, 2000, 4096), (100, 20000, 200),
+           (128, 2048, 2048)]
 
 
 @pytest.mark.parametrize("act", list(B.ACTIVATIONS))
@@ -382,6 +383,56 @@ def test_linear_parity(M, N, K, act):
     bias = _randn(g, rows, scale=0.5) if pick & 1 else None
     residual = _randn(g, M, N) if pick & 2 else None
     _check_linear(x, w, act, bias, residual, torch.float32 if (N + len(act)) % 2 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,N,K,act,unaligned", [(777, 5120, 1288, "gelu_tanh", False), (1030, 4096, 2048, "none", False),
+                                                 (777, 2560, 1288, "swiglu", False), (777, 5125, 1289, "silu", True)])
+def test_linear_rows_past_the_last_full_tile(M, N, K, act, unaligned):
+    """Sizes whose last rows are a launch of their own beside the others'."""
+    g = _gen(M + N + K)
+    rows = 2 * N if act == "swiglu" else N
+    x, w = _randn(g, M, K).cuda(), _randn(g, rows, K, scale=K ** -0.5).cuda()
+    bias, residual = _randn(g, rows, scale=0.5).cuda(), _randn(g, M, N + 3).cuda()[:, 1:1 + N]
+    _check_linear(x, w, act, bias, residual, torch.float32 if unaligned else torch.bfloat16)
+    # what follows on the stream sees all rows, and what came before is seen by all
+    lin, back = B.Linear(w, bias=bias, activation=act), B.Linear(_randn(g, 64, N, scale=N ** -0.5).cuda())
+    outs = []
+    for wait in (True, False):
+        y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+        xs = torch.zeros_like(x)
+        torch.cuda.synchronize()
+        for i in range(4):
+            xs.copy_(x).mul_(1 + i)
+            if wait:
+                torch.cuda.synchronize()
+            lin(xs, out=y)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(back(y))
+    for a, b in zip(outs[:4], outs[4:]):
+        assert torch.equal(a, b)
+
+
+def test_error_words_are_clean():
+    g = _gen(3)
+    s = torch.cuda.current_stream().cuda_stream
+
+    def clean(handle):
+        ws = handle._spaces[s][0]
+        assert B.gmmfr_check_device_errors(ws, s) == 0
+
+    for M, N, K in ((1, 64, 64), (16, 256, 512), (100, 640, 1000), (300, 1000, 520), (1030, 4096, 2048)):
+        lin = B.Linear(_randn(g, N, K).cuda())
+        lin(_randn(g, M, K).cuda())
+        clean(lin)
+    for T in (5, 1500):
+        gate = B.MoeGate(_randn(g, 64, 128).cuda(), topk=4)
+        gate(_randn(g, T, 128).cuda())
+        clean(gate)
+    d = _layer_inputs(g, 6, 256, 16, 64, 64, False)
+    layer = _make_layer(d, topk=4)
+    layer(d["x"].cuda())
+    clean(layer)
 
 
 @pytest.mark.parametrize("M", [1, 20, 150])
