@@ -615,6 +615,10 @@ class MoeGate(_Handle):
         gmmfr_moe_gate_workspace_size(p)  # refuses a rule that is out of range
         self._T, self._need = 0, 0
 
+    @property
+    def topk(self) -> int:
+        return self._topk
+
     def __call__(self, x, ids=None, weights=None, logits=None, stream=None):
         p = self._p
         p.ldx = _rows(x, "x", None, self._H, self._bf16)
@@ -679,6 +683,11 @@ class MoeLayer(_Handle):
         self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_moe_layer
         gmmfr_moe_layer_workspace_size(p)
         self._T, self._need = 0, 0
+
+    @property
+    def prepared(self):
+        """The routed experts' prepared weights (BF16 ones are what :func:`ffn` takes)."""
+        return self._prepared
 
     @staticmethod
     def _prepare(E, H, I, w13, s13, w2, s2, mx):
