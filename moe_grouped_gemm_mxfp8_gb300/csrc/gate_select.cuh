@@ -136,18 +136,23 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
 }
 
 // ---------------------------------------------------------------- the router for a few tokens by one cluster
-// A cluster of 8 CTAs takes 8 kTiles tokens.  Its 64 warps share the products: a warp takes one group of 16 experts and
-// one of 64 / groups splits of K (blocks of 32, taken in turn) against all the tokens, and sends its sums straight to
+// A cluster of 8 CTAs takes 8 kTiles tokens.  Its warps (64 or 128) share the products: a warp takes one group of 16 experts
+// and one of warps / groups splits of K (blocks of 32, taken in turn) against all the tokens, and sends its sums straight to
 // the CTAs that select for those tokens (CTA c: tokens c * kTiles ...), which add the splits in order.  The weight rows
 // are read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows l / 4 and
 // l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike, which leaves
 // the sums alone), so each row is read in 16-byte pieces with no staging.
-// One token of H = 2048 and 256 experts takes 6.6 us: about 3 until the weights are there (they come through 8 SMs in
-// three rounds of loads), 0.6 for the sums, 2.9 for the selection, all of it latency.
+// One token of H = 2048 and 256 experts takes 5.9 us: about 2 until the weights are there (they come through 8 SMs),
+// 0.6 for the sums, 2.9 for the selection, all of it latency.
 namespace gate {
 constexpr int kCluster = 8;
-constexpr int kThreads = 256;  // 128 registers each: half an SM, so that the kernel that follows fits beside it
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: of 256 two CTAs share an SM; 512 ask for the weights in fewer rounds, when there are more than the
+// six blocks that a warp of the 64 asks for at once, and the clusters are few (15 with a CTA per SM).  One token,
+// H = 2048, 256 experts: 5.9 us with 512, 6.6 with 256; H = 7168, 16 experts: 5.8 and 5.0.
+constexpr int kSmall = 512, kLarge = 256;
+inline int cluster_threads(int64_t T, int64_t H, int E) {
+  return T <= 15 * 8 && (int64_t)((E + 15) / 16) * ((H + 31) / 32) > 64 * 6 ? kSmall : kLarge;
+}
 constexpr int kMaxCand = 256;
 // What a team of threads needs to select for one token.
 struct TeamScratch {
@@ -159,9 +164,10 @@ struct TeamScratch {
   uint32_t out_e[kMaxTopk];
   float out_p[kMaxTopk];
 };
-template <int kTiles>
+template <int kTiles, int kThr>
 struct Smem {
-  float logits[kTiles][kMaxExperts];  // of the tokens this CTA selects for: the splits' sums, the logits, the probabilities
+  // of the tokens this CTA selects for: the splits' sums (a warp's 16 each), the logits, the probabilities
+  float logits[kTiles][kThr / 32 * kCluster * 16 > kMaxExperts ? kThr / 32 * kCluster * 16 : kMaxExperts];
   uint32_t key[kTiles][kMaxExperts];
   TeamScratch team[kTiles];
   float bias[kMaxExperts];
@@ -311,14 +317,14 @@ __device__ __forceinline__ void gate_select_team(const GateRule& r, const float*
   }
 }
 
-template <int kTiles>
-__device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t t0, gate::Smem<kTiles>& sm, uint32_t rank,
+template <int kTiles, int kThr>
+__device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t t0, gate::Smem<kTiles, kThr>& sm, uint32_t rank,
                                                     int warp, int lane) {
   const int tid = threadIdx.x, E = p.rule.E, groups = (E + 15) / 16;
   const int blocks = (int)((p.H + 31) / 32);
-  constexpr int kU = kTiles == 1 ? 6 : (kTiles == 2 ? 4 : 2);  // blocks of 32 K in flight
-  const int w = (int)rank * gate::kWarps + warp;
-  const int splits = min(gate::kCluster * gate::kWarps / groups, (blocks + kU - 1) / kU);
+  constexpr int kU = kThr == gate::kSmall ? 8 : kTiles == 1 ? 6 : (kTiles == 2 ? 4 : 2);  // blocks of 32 K in flight
+  const int w = (int)rank * (kThr / 32) + warp;
+  const int splits = min(gate::kCluster * (kThr / 32) / groups, (blocks + kU - 1) / kU);
   const int split = w / groups, grp = w - split * groups;
   ptx::cluster_wait();  // the other CTAs have started: their shared memory may be written
   if (split < splits) {
@@ -356,7 +362,7 @@ __device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t
           ptx::mma_16816(acc[i], a[u].z, b[u].z, a[u].w, b[u].w, x[u][i].z, x[u][i].w);
         }
     }
-    const int at = split * groups * 16 + grp * 16 + (lane >> 2);  // below 64 x 16
+    const int at = split * groups * 16 + grp * 16 + (lane >> 2);  // the warp's place in the cluster x 16 at most
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -369,7 +375,7 @@ __device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t
   }
   ptx::cluster_sync();
   if (splits > 1) {  // the splits' sums, in order
-    constexpr int kTeam = gate::kThreads / kTiles;
+    constexpr int kTeam = kThr / kTiles;
     float* l = sm.logits[tid / kTeam];
     for (int e = tid % kTeam; e < E; e += kTeam) {
       float s = 0.f;
@@ -381,27 +387,27 @@ __device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t
   }
 }
 
-template <int kTiles>
-__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem<kTiles>& sm, uint32_t rank) {
-  constexpr int kTeam = gate::kThreads / kTiles;
+template <int kTiles, int kThr>
+__device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem<kTiles, kThr>& sm, uint32_t rank) {
+  constexpr int kTeam = (kThr < 256 ? kThr : 256) / kTiles;  // more threads than that would wait on one another for longer
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int E = p.rule.E;
   const int64_t t = t0 + rank * kTiles;
   const bool by_team = (E + 31) / 32 * p.rule.topk <= gate::kMaxCand;
   ptx::cluster_arrive_relaxed();
   if (p.select_bias)
-    for (int e = tid; e < E; e += gate::kThreads) sm.bias[e] = p.select_bias[e];
-  gate_cluster_logits<kTiles>(p, t0, sm, rank, warp, lane);
+    for (int e = tid; e < E; e += kThr) sm.bias[e] = p.select_bias[e];
+  gate_cluster_logits<kTiles, kThr>(p, t0, sm, rank, warp, lane);
   if (p.logits) {
     for (int i = 0; i < kTiles; ++i)
       if (t + i < p.T)
-        for (int e = tid; e < E; e += gate::kThreads) p.logits[(t + i) * E + e] = sm.logits[i][e];
+        for (int e = tid; e < E; e += kThr) p.logits[(t + i) * E + e] = sm.logits[i][e];
     __syncthreads();  // the probabilities take the logits' place
   }
   const float* bias = p.select_bias ? sm.bias : nullptr;
   if (by_team) {
     const int i = tid / kTeam;  // the team's token
-    if (t + i < p.T)
+    if (i < kTiles && t + i < p.T)
       gate_select_team<kTeam>(p.rule, bias, sm.logits[i], sm.key[i], sm.team[i], tid % kTeam, 1 + i, p.ids, p.ids_i64,
                               p.weights, (t + i) * p.rule.topk);
   } else if (warp < kTiles && t + warp < p.T) {

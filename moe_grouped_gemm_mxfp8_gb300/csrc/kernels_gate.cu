@@ -29,16 +29,16 @@ constexpr int kPairExperts = 512;  // the pair form's most: their logits fill TM
 }  // namespace gate
 
 // ============================================================================ cluster form
-template <int kTiles>
-__global__ void __launch_bounds__(gate::kThreads) gate_cluster_kernel(const __grid_constant__ GateParams p) {
-  __shared__ gate::Smem<kTiles> sm;
+template <int kTiles, int kThr>
+__global__ void __launch_bounds__(kThr) gate_cluster_kernel(const __grid_constant__ GateParams p) {
+  __shared__ gate::Smem<kTiles, kThr> sm;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) {  // no wait here can give up
     p.hdr[0] = 1;
     p.hdr[1] = 0;
   }
-  gate_cluster<kTiles>(p, (int64_t)(blockIdx.x / gate::kCluster) * 8 * kTiles, sm, ptx::cluster_rank());
+  gate_cluster<kTiles, kThr>(p, (int64_t)(blockIdx.x / gate::kCluster) * 8 * kTiles, sm, ptx::cluster_rank());
 }
 
 // ============================================================================ pair form
@@ -571,8 +571,12 @@ cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t 
     // experts: 256 tokens 9.5 us in clusters of 8, 11.8 of 16; 512 tokens 12.4 of 16, 18.0 of 32 and of 8
     const int tiles = p.T <= 32 * 8 ? 1 : (p.T <= 32 * 16 ? 2 : 4);
     lc.gridDim = dim3((unsigned)((p.T + 8 * tiles - 1) / (8 * tiles) * gate::kCluster));
-    lc.blockDim = dim3(gate::kThreads);
-    return cudaLaunchKernelEx(&lc, tiles == 1 ? gate_cluster_kernel<1> : (tiles == 2 ? gate_cluster_kernel<2> : gate_cluster_kernel<4>), p);
+    const int threads = gate::cluster_threads(p.T, p.H, p.rule.E);
+    lc.blockDim = dim3((unsigned)threads);
+    auto kernel = threads == gate::kSmall ? gate_cluster_kernel<1, gate::kSmall>
+                        : (tiles == 1 ? gate_cluster_kernel<1, gate::kLarge>
+                                      : (tiles == 2 ? gate_cluster_kernel<2, gate::kLarge> : gate_cluster_kernel<4, gate::kLarge>));
+    return cudaLaunchKernelEx(&lc, kernel, p);
   }
   static int configured_device = -1;
   int dev = 0;

@@ -246,9 +246,9 @@ struct Walk {
 
 // ============================================================================ front
 // The first T / 8 clusters are the router (gate_select.cuh); the others make the token images and zero the counters.
-template <bool kMx>
-__global__ void __launch_bounds__(gate::kThreads) layer_front_kernel(const __grid_constant__ LayerParams p) {
-  __shared__ gate::Smem<1> sm;
+template <bool kMx, int kThr>
+__global__ void __launch_bounds__(kThr) layer_front_kernel(const __grid_constant__ LayerParams p) {
+  __shared__ gate::Smem<1, kThr> sm;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const GateParams& g = p.gate;
@@ -256,11 +256,11 @@ __global__ void __launch_bounds__(gate::kThreads) layer_front_kernel(const __gri
   const int lane = threadIdx.x & 31;
   const int routers = (T + 7) / 8 * gate::kCluster;
   if ((int)blockIdx.x < routers) {
-    gate_cluster<1>(g, (int64_t)(blockIdx.x / gate::kCluster) * 8, sm, ptx::cluster_rank());
+    gate_cluster<1, kThr>(g, (int64_t)(blockIdx.x / gate::kCluster) * 8, sm, ptx::cluster_rank());
     return;
   }
-  const int block = blockIdx.x - routers, blocks = gridDim.x - routers, warps = blocks * gate::kWarps;
-  const int tid = threadIdx.x * blocks + block, threads = blocks * gate::kThreads;
+  const int block = blockIdx.x - routers, blocks = gridDim.x - routers, warps = blocks * (kThr / 32);
+  const int tid = threadIdx.x * blocks + block, threads = blocks * kThr;
   for (int i = tid; i < p.n_counters; i += threads) p.counters[i] = 0;
   // images: 8 elements of a row per thread, zero past H (their weights are zero, but 0 x NaN is not)
   const int img = layer::image_bytes(kMx, p.npad);
@@ -846,7 +846,8 @@ static cudaError_t launch_layer_of(const LayerParams& p, int sms, cudaStream_t s
   lc.stream = s;
   // the router's clusters (one per 8 tokens, at most 8) and the images': about as many as run at once
   lc.gridDim = dim3((unsigned)std::max<int64_t>(15, (p.gate.T + 7) / 8 + 7) * gate::kCluster);
-  lc.blockDim = dim3(gate::kThreads);
+  const int threads = gate::cluster_threads(p.gate.T, p.gate.H, p.gate.rule.E);
+  lc.blockDim = dim3((unsigned)threads);
   cudaLaunchAttribute fattr[2];
   fattr[0] = attr[0];
   fattr[1].id = cudaLaunchAttributeClusterDimension;
@@ -854,7 +855,7 @@ static cudaError_t launch_layer_of(const LayerParams& p, int sms, cudaStream_t s
   fattr[1].val.clusterDim.y = fattr[1].val.clusterDim.z = 1;
   lc.attrs = fattr;
   lc.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&lc, layer_front_kernel<kMx>, p);
+  cudaError_t e = cudaLaunchKernelEx(&lc, threads == gate::kSmall ? layer_front_kernel<kMx, gate::kSmall> : layer_front_kernel<kMx, gate::kLarge>, p);
   if (e != cudaSuccess) return e;
   lc.gridDim = dim3((unsigned)(sms < kLayerMaxCtas ? sms : kLayerMaxCtas));
   lc.blockDim = dim3(layer::kThreads);
