@@ -93,7 +93,7 @@ namespace layer {
 
 constexpr int kThreads = 256;  // warp 0 weights, 1 MMA, 2..5 epilogue, 6 tokens' producer
 constexpr int kMaxStages = 10;
-constexpr int kRound = 8;  // tokens whose SwiGLU values are made at a time
+constexpr int kRound = 4;  // tokens whose SwiGLU values are made at a time
 // A stage: weight tile (with MXFP8 its 512 scale bytes), then the tokens' image: BF16 npad rows of 128 bytes;
 // MXFP8 the scale chunk of hi and lo (512 bytes), npad rows of hi codes, npad of lo.
 __host__ __device__ constexpr int tile_bytes(bool mx) { return mx ? kPrepTileBytes : kWTileBytes; }
@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(kThr) layer_front_kernel(const __grid_constant
 }
 
 // ============================================================================ layer
+// Loops of unknown length are kept rolled: in a small call every instruction comes from memory the first time, and the
+// shorter code is up to 5% faster there (39 tokens, 20 experts of 728: 32.2 -> 30.5 us) and nowhere slower.
 template <bool kMx>
 __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_constant__ LayerParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
   const uint32_t smem_base = ptx::smem_u32(smem);
 
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int s = 0; s < n_stages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full[s]), 2);
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
@@ -351,6 +354,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
     *s_err = 0;
     ptx::fence_mbar_init();
   }
+#pragma unroll 1
   for (int e = threadIdx.x; e < E; e += layer::kThreads) s_mask[e] = 0;
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), layer::tmem_cols(kMx));
@@ -365,6 +369,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
   ptx::griddep_wait();
 
   // ---------------------------------------------------------------- the chosen experts
+#pragma unroll 1
   for (int i = threadIdx.x; i < T * topk; i += layer::kThreads) {
     const int e = static_cast<const int32_t*>(g.ids)[i];  // in [0, E): the front kernel's
     s_ids[i] = (uint16_t)e;
@@ -415,6 +420,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         // the piece's tiles lie in runs of consecutive ones: `src` walks a run of `left` tiles
         const uint8_t* src = nullptr;
         int left = 0;
+#pragma unroll 1
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
           if (left == 0) {
             if (!walk.is_down) {
@@ -453,6 +459,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           }
         }
       }
+#pragma unroll 1
       for (int s = 0; ok && s < n_stages; ++s) {  // no copy is in flight at exit
         ok = warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
         if (++stage == n_stages) {
@@ -461,6 +468,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         }
       }
       if (!ok)  // aborted: let what is in flight land
+#pragma unroll 1
         for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
     }
     __syncwarp();
@@ -483,6 +491,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         const int past = walk.is_down ? (int)walk.k0 - A * p.KB2 : -1;
         const uint8_t* src = past >= 0 ? p.swimg_s + (int64_t)past * img
                                        : (walk.is_down ? p.swimg : p.ximg) + (int64_t)walk.k0 * img;
+#pragma unroll 1
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
           if (walk.is_down && past < 0 && k == A * p.KB2) src = p.swimg_s;
           if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
@@ -526,6 +535,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * acc;
         uint32_t accumulate = 0;
+#pragma unroll 1
         for (int k = walk.k0; k < (int)walk.k1; ++k) {
           if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
             ok = false;
@@ -599,6 +609,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
       if (!is_down && ep < T) {  // the router's weight of each token for this expert
         float w = routed ? 0.f : 1.f;
         if (routed)
+#pragma unroll 1
           for (int k = 0; k < topk; ++k) w = s_ids[ep * topk + k] == e ? s_wt[ep * topk + k] : w;
         s_tokw[ep] = w;
       }
@@ -611,6 +622,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         // this CTA's range begins in the unit (slot 0) or ends there (slot 1)
         const uint32_t at = blockIdx.x * 2 + (run.lo(blockIdx.x) >= pieces.x0 ? 0 : 1);
         float* slot = (is_down ? p.slots_down : p.slots_up) + (int64_t)at * slot_floats;
+#pragma unroll 1
         for (int c0 = 0; c0 < T; c0 += 16) {
           if (((mask >> c0) & 0xffff) == 0) continue;
           float v[16];
@@ -626,6 +638,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           else cut1 = unit;
         }
       } else if (is_down) {  // a column tile of this CTA alone
+#pragma unroll 1
         for (int c0 = 0; c0 < T; c0 += 16) {
           float v[16];
           load_acc16<kMx>(taddr + c0, npad, v);
@@ -647,6 +660,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         dst += (int64_t)(kMx ? j >> 1 : j) * img;
         const bool pad_half = kMx && (j & 1) == 0 && j + 1 == (routed ? p.NT1 : p.NT1s);  // no unit fills the tile's other half
         // rows of tokens that did not choose the expert: zeros, in 16-byte chunks (MXFP8: of hi and of lo)
+#pragma unroll 1
         for (int i = ep; i < T * 8; i += 128) {
           const int t = i >> 3, c = i & 7;
           if ((mask >> t) & 1) continue;
@@ -660,6 +674,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           }
         }
         if (pad_half) {
+#pragma unroll 1
           for (int i = ep; i < T * 8; i += 128) {
             const int t = i >> 3, c = i & 7;
             uint8_t* at = dst + kSfChunk + (c >> 2) * npad * 128;
@@ -776,6 +791,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
                   a_n = total * (int)(blockIdx.x - pa.b0 + 1) / (int)pa.n - a_lo,
                   b_lo = total * (int)(blockIdx.x - pb.b0) / (int)pb.n,
                   b_n = n_cut > 1 ? total * (int)(blockIdx.x - pb.b0 + 1) / (int)pb.n - b_lo : 0;
+#pragma unroll 1
         for (int x = ep; x < a_n + b_n; x += 128) {
           const bool in_a = x < a_n;
           const int i = in_a ? a_lo + x : b_lo + x - a_n, j = in_a ? cut0 : cut1, n = in_a ? pa.n : pb.n;
