@@ -33,9 +33,9 @@ constexpr int kTileBytes = 128 * 128;
 constexpr int kPairArena = 6 * 32768;
 constexpr int kPairMaxStages = 10;
 constexpr int kPairBars = 2 * kPairMaxStages + 5;
-constexpr int kPairTurnOff = kPairArena + kPairBars * 8 + 32;  // float [8][32][33]: an epilogue warp's 32 x 32 outputs
+constexpr int kPairTurnOff = (kPairArena + kPairBars * 8 + 32 + 15) / 16 * 16;  // float [8][32][33]: an epilogue warp's 32 x 32 outputs
 constexpr int kPairSmem = kPairTurnOff + 8 * 32 * 33 * 4 + 1024;
-static_assert(kPairSmem <= 232448, "shared memory budget");
+static_assert(kPairSmem <= 232448 && 32 * 33 * 4 % 16 == 0, "shared memory budget; 16-byte reads of the turn buffers");
 
 // ---- stream form
 constexpr int kStreamMaxStages = 11;
@@ -134,10 +134,19 @@ __device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, 
   }
 }
 
-__device__ __forceinline__ void add_bias32(const __nv_bfloat16* bias, int64_t n, int64_t n_end, float (&v)[32]) {
+// Lane j's bias, of column j of 32, onto a thread's 32 columns, by way of 128 bytes of the warp's.
+__device__ __forceinline__ void add_bias32(float bias, float (&v)[32], float* room) {
+  room[threadIdx.x & 31] = bias;
+  __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (n + j < n_end) v[j] += __bfloat162float(bias[n + j]);
+  for (int j = 0; j < 32; j += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(room + j);
+    v[j] += b.x;
+    v[j + 1] += b.y;
+    v[j + 2] += b.z;
+    v[j + 3] += b.w;
+  }
+  __syncwarp();
 }
 
 }  // namespace
@@ -408,32 +417,51 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       int mt, nt;
       tile_at(t, mt, nt);
       const int buf = acc_i & 1;
+      const int cols = kGated ? BN / 2 : BN;
+      const int64_t n0 = (int64_t)nt * cols;
+      // the tile's biases, a column per lane, before the wait for its products
+      constexpr int kChunks = kGated ? 2 : 4;
+      float bias[kChunks] = {}, bias_up[kChunks] = {};
+      if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int64_t n = n0 + 32 * half + 64 * i + lane;
+          if (n < p.N) {
+            bias[i] = __bfloat162float(p.bias[n]);
+            if constexpr (kGated) bias_up[i] = __bfloat162float(p.bias[p.N + n]);
+          }
+        }
+      }
       if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
       const int64_t m0 = (int64_t)mt * 256 + rank * 128 + q * 32;  // this warp's rows
-      const int cols = kGated ? BN / 2 : BN;
-      const int64_t n0 = (int64_t)nt * cols;
-      for (int c0 = 32 * half; c0 < cols; c0 += 64) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c0 = 32 * half + 64 * i;
+        if (c0 >= cols) break;
         uint32_t r[32];
         float v[32];
         ptx::tmem_ld_32x32b_x32(taddr + c0, r);
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (p.bias) add_bias32(p.bias, n0 + c0, p.N, v);
+        if (p.bias) add_bias32(bias[i], v, turn);
         if constexpr (kGated) {
           ptx::tmem_ld_32x32b_x32(taddr + BN / 2 + c0, r);
           ptx::tmem_wait_ld();
           float u[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
-          if (p.bias) add_bias32(p.bias + p.N, n0 + c0, p.N, u);
+          if (p.bias) add_bias32(bias_up[i], u, turn);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = silu(v[j]) * u[j];
-        } else {
+          for (int j = 0; j < 32; ++j) v[j] = (p.out_f32 ? silu(v[j]) : silu<true>(v[j])) * u[j];
+        } else if (p.out_f32) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = activate(kAct, v[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = activate<true>(kAct, v[j]);
         }
         store_tile32(p, m0, n0 + c0, v, turn);
       }
