@@ -10,7 +10,10 @@
 //           join), the gated 2 x 2048 x 7168 with 48 rows 14.6 us.
 //   pair    many rows.  A pair of CTAs holds a 256 x BN tile of y (cta_group::2: each CTA loads 128 rows of x
 //           and half of the BN rows of W), accumulators double-buffered in TMEM, so that a tile's epilogue
-//           runs beside the next tile's products.
+//           runs beside the next tile's products.  8192 rows of 7168 x 4096: 261 us, 1.84 PFLOP/s (97% of the
+//           library's burst rate; the tensor pipe is active 88% of the time), bound by the products and, called for
+//           long, by the power limit.  Products of some hundred rows are bound by what reaches an SM from L2, about
+//           64 bytes a cycle: 300 rows of 4096 x 4096 take 16.7 us.
 // Rows of x or W that do not start on 16-byte boundaries (a TMA rule) are first copied to a pitch that does.
 #include <cuda_bf16.h>
 
@@ -38,7 +41,7 @@ constexpr int kPairSmem = kPairTurnOff + 8 * 32 * 33 * 4 + 1024;
 static_assert(kPairSmem <= 232448 && 32 * 33 * 4 % 16 == 0, "shared memory budget; 16-byte reads of the turn buffers");
 
 // ---- stream form
-constexpr int kStreamMaxStages = 11;
+constexpr int kStreamMaxStages = 6;
 constexpr int kStreamBars = 2 * kStreamMaxStages + 6;
 constexpr int kStreamKps = 2;  // K blocks per stage: 0.33 us per stage where a CTA has the memory to itself, 0.25 with one
 constexpr int kStreamArena = 220 * 1024;  // the ring, and the partial sums unless they take its place
