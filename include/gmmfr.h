@@ -403,7 +403,8 @@ GMMFR_API gmmfr_status gmmfr_moe_gate_workspace_size(const gmmfr_gate_problem* p
 
 /* x [T, H] BF16 and weight [E, H] BF16 (dense), both 16-byte aligned; select_bias [E] float32 or NULL;
  * topk_ids [T, topk] int64 or int32; topk_weights [T, topk] float32; logits [T, E] float32 or NULL
- * (written when given).  Deterministic; never syncs, never allocates. */
+ * (written when given).  One launch.  Deterministic; never syncs, never allocates; a wait that gave up sets
+ * GMMFR_DEV_TIMEOUT in the workspace's device error word (gmmfr_check_device_errors). */
 GMMFR_API gmmfr_status gmmfr_moe_gate(const gmmfr_gate_problem* problem, const void* x, const void* weight,
                                       const float* select_bias, void* topk_ids, float* topk_weights, float* logits,
                                       void* workspace, size_t workspace_bytes, void* stream);
@@ -448,7 +449,10 @@ GMMFR_API gmmfr_status gmmfr_moe_layer_workspace_size(const gmmfr_layer_problem*
  * BF16 or NULL; out [T, H] BF16 (may be the residual's memory, not x's); prepared: the routed experts' weights, E experts of
  * sizes H, I; shared_prepared: the shared expert's (E = 1, I = shared_I), required when shared_I > 0;
  * topk_ids [T, topk] int32 and topk_weights [T, topk] float32: the gate's choice, written when given.
- * Never syncs, never allocates; deterministic. */
+ * Two launches, the second cooperative (its CTAs, one per SM, wait for one another, so all must be resident: it
+ * starts when the device has room for all of them).  A token with an infinity or NaN spoils its own row only; with E4M3
+ * weights the blocks of 32 that hold it count as NaN.  Never syncs, never allocates; deterministic; a wait that gave up
+ * sets GMMFR_DEV_TIMEOUT in the workspace's device error word (gmmfr_check_device_errors). */
 GMMFR_API gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, const void* gate_weight,
                                        const float* select_bias, const void* residual, void* out,
                                        const void* prepared, size_t prepared_bytes, const void* shared_prepared,
@@ -488,8 +492,9 @@ GMMFR_API gmmfr_status gmmfr_linear_workspace_size(const gmmfr_linear_problem* p
 
 /* x, weight, bias ([N or 2N] or NULL), residual ([M, N] or NULL) BF16; out of out_type (may be the residual's
  * memory when both are BF16 with the same row stride).  Any K, stride and element alignment is taken.  One launch,
- * plus one for each matrix that is copied first.  Never syncs, never allocates; deterministic; a wait that gave up
- * sets GMMFR_DEV_TIMEOUT in the workspace's device error word (gmmfr_check_device_errors). */
+ * plus one for each matrix that is copied first and one where the last M % 256 rows run beside the others.  Never
+ * syncs, never allocates; deterministic; a wait that gave up sets GMMFR_DEV_TIMEOUT in the workspace's device error
+ * word (gmmfr_check_device_errors). */
 GMMFR_API gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight,
                                     const void* bias, const void* residual, void* out, void* workspace,
                                     size_t workspace_bytes, void* stream);
