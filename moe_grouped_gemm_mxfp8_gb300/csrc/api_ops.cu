@@ -140,7 +140,8 @@ LayerLayout layer_layout(const gmmfr_layer_problem* p) {
   LayerLayout L{};
   const bool mx = p->weight_type == GMMFR_DT_E4M3;
   const int64_t T = p->gate.T, k = p->gate.topk, H = p->gate.H, kt = mx ? 128 : 64;
-  L.npad = std::max<int64_t>(16, cdiv(T, 16) * 16);
+  // columns of the products, a multiple of 16: BF16 npad, MXFP8 2 npad (hi and lo)
+  L.npad = mx ? std::max<int64_t>(8, cdiv(T, 8) * 8) : std::max<int64_t>(16, cdiv(T, 16) * 16);
   L.NT1 = cdiv(p->I, 64);
   L.KB1 = cdiv(H, kt);
   L.NT2 = cdiv(H, 128);

@@ -112,7 +112,7 @@ constexpr int kArena = 180 * 1024;
 __host__ __device__ constexpr int n_stages(bool mx, int npad) {
   return kArena / stage_bytes(mx, npad) < kMaxStages ? kArena / stage_bytes(mx, npad) : kMaxStages;
 }
-static_assert(stage_bytes(true, 16) % 1024 == 0 && stage_bytes(false, 16) % 1024 == 0 && rows_off(true) % 1024 == 0,
+static_assert(stage_bytes(true, 8) % 1024 == 0 && stage_bytes(false, 16) % 1024 == 0 && rows_off(true) % 1024 == 0,
               "swizzled operands need 1024-byte alignment");
 constexpr int kBarOff = kArena;
 constexpr int kNumBars = 2 * kMaxStages + 5;
@@ -130,7 +130,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 __host__ __device__ constexpr int acc_cols(bool mx, int npad) { return mx ? 2 * npad : npad; }
 __host__ __device__ constexpr int tmem_cols(bool mx) { return mx ? 512 : 128; }
 static_assert(2 * acc_cols(true, 64) + 8 * n_stages(true, 64) <= tmem_cols(true) &&
-                  2 * acc_cols(true, 16) + 8 * n_stages(true, 16) <= tmem_cols(true) && 2 * acc_cols(false, 64) <= tmem_cols(false),
+                  2 * acc_cols(true, 8) + 8 * n_stages(true, 8) <= tmem_cols(true) && 2 * acc_cols(false, 64) <= tmem_cols(false),
               "TMEM");
 
 }  // namespace layer
@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
       const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
       int stage = 0;
       uint32_t phase = 0, sb = smem_base + tile;
+      const uint32_t bytes = img - (npad - T) * 128;  // without the rows past the tokens (their columns are not read)
       bool ok = true, sw_ready = false;
       while (ok && walk.next()) {
         if (walk.is_down && !sw_ready) {  // every unit of the up run has stored its sw
@@ -507,8 +508,8 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
             break;
           }
           if (ptx::elect_one()) {
-            ptx::mbar_arrive_expect_tx(full0 + 8 * stage, img);
-            ptx::bulk_g2s(sb, src, img, full0 + 8 * stage, pol);
+            ptx::mbar_arrive_expect_tx(full0 + 8 * stage, bytes);
+            ptx::bulk_g2s(sb, src, bytes, full0 + 8 * stage, pol);
           }
           src += img;
           sb += stage_bytes;
