@@ -120,6 +120,10 @@ __device__ __forceinline__ void prefetch_tensormap(const void* tmap) {
 
 // ---------------------------------------------------------------- bulk / tensor copies
 // Contiguous global -> shared copy completing on `bar` (16-byte aligned, size % 16 == 0).
+// Asks for `bytes` (a multiple of 16, 16-byte aligned) in L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
                                          uint64_t policy) {
   asm volatile(
