@@ -817,7 +817,8 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           if (col >= g.H) continue;
           const float* slot = p.slots_down + (int64_t)(b0 * 2) * slot_floats + t * 128 + r4;
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+          constexpr int kJoin = kMx ? 4 : 8;
+#pragma unroll kJoin
           for (int k = 0; k < n; ++k) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(slot + (int64_t)(2 * k + (k == 0 ? first_slot : 0)) * slot_floats));
             s.x += v.x;
