@@ -3,9 +3,9 @@
 //   pair     many tokens: CTA pairs take 256 tokens against all experts (tcgen05, cta_group::2), and the selection
 //            reads the logits where they are, in TMEM: a token is a TMEM lane, so a thread walks its token's
 //            columns.  Four threads share a token, a quarter of the columns each.  16384 tokens of 2048, 256 experts,
-//            sigmoid and groups: 36.8 us (69 MB, 1.9 TB/s), one tile per pair.  24 of them remain with H = 64: the
-//            selection is what bounds it, by its instructions (64 columns a thread, each an exponential, a key and
-//            its compares), and a CTA with one tile has nothing to run beside it.
+//            sigmoid and groups: 35.5 us (69 MB, 1.9 TB/s), one tile per pair.  24 of them remain with H = 64: the
+//            selection is what bounds it, a thread's chain of exponentials, keys and compares over 64 columns (tiles
+//            of fewer tokens, on fewer warps, take as long), and a CTA with one tile has nothing to run beside it.
 #include "gate_select.cuh"
 #include "ops.cuh"
 #include "pipeline.cuh"
@@ -15,18 +15,20 @@ namespace gmmfr {
 
 namespace gate {
 constexpr int kPairThreads = 64 + 512;  // warp 0 TMA, warp 1 MMA, 16 epilogue warps
+// The ring; the selection's exchange areas, which the ring has too when no tile follows; barriers, biases
 constexpr int kArena = 128 * 1024;
 constexpr int kMaxStages = 8;
 constexpr int kTop = 8;  // the pair form's longest choice
-constexpr int kBars = 2 * kMaxStages + 3;
-constexpr int kMiscOff = kArena + kBars * 8 + 8;
-constexpr int kBiasOff = kMiscOff + 32;                  // float bias[512]
-constexpr int kStatOff = kBiasOff + 512 * 4;             // float [2][4][128]: maxima and sums; eligible groups
+constexpr int kStatOff = kArena;                         // float [2][4][128]: maxima and sums; eligible groups
 constexpr int kListOff = kStatOff + 2 * 4 * 128 * 4;     // uint32 [4][8][128]: each quarter's best keys
 constexpr int kCap = 16;                                 // candidates a quarter has room for
 constexpr int kCandOff = kListOff + 4 * kTop * 128 * 4;  // group keys [64][128], then candidates [4][kCap][2][128]
 constexpr int kSelOff = kCandOff + 4 * kCap * 2 * 128 * 4;  // the choice [8][2][128]
-constexpr int kPairSmem = kSelOff + kTop * 2 * 128 * 4 + 1024;
+constexpr int kBars = 2 * kMaxStages + 3;
+constexpr int kBarOff = kSelOff + kTop * 2 * 128 * 4;
+constexpr int kMiscOff = kBarOff + kBars * 8 + 8;
+constexpr int kBiasOff = kMiscOff + 32;                  // float bias[512]
+constexpr int kPairSmem = kBiasOff + 512 * 4 + 1024;
 static_assert(kMaxGroups <= 4 * kCap * 2 && kPairSmem <= 232448, "shared memory");
 constexpr int kPairExperts = 512;  // the pair form's most: their logits fill TMEM
 }  // namespace gate
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
     gate_pair_kernel(const __grid_constant__ GateMaps maps, const __grid_constant__ GateParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + gate::kArena);  // used in rank 0: both CTAs' loads
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + gate::kBarOff);  // used in rank 0: both CTAs' loads
   uint64_t* empty = full + gate::kMaxStages;
   uint64_t* accf = empty + gate::kMaxStages;
   uint64_t* acce = accf + 1;  // used in rank 0: both CTAs' epilogue warps
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
       }
       merge();
       uint32_t last = topk_th();
-      last = last > 0 ? last : 1u;
+      last = token < p.T ? (last > 0 ? last : 1u) : 0xffffffffu;  // past the tokens all scores are equal: none is taken
       // 2. the columns that reach it: few, unless many scores are equal (or one run holds them all)
       int n = 0;
       uint32_t* cand = s_cand + part * gate::kCap * 2 * 128 + tok;  // column and probability
@@ -552,8 +554,11 @@ bool plan_gate(GateParams& p, int sms) {
   p.bn = p.rule.E <= 256 ? (p.rule.E + 31) / 32 * 32 : 256;
   p.KB = (int32_t)((p.H + 63) / 64);
   const int stage = 128 * 128 + (p.rule.E <= 256 ? 1 : 2) * p.bn * 64;
-  p.n_stages = gate::kArena / stage < gate::kMaxStages ? gate::kArena / stage : gate::kMaxStages;
   const int64_t tiles = (p.T + 255) / 256;
+  // more stages where the selection's areas are free until the only tile's products are done (2048 tokens of 7168, 512
+  // experts: two stages 117 us, four 95.6; 16384 of 2048, 256 experts: four 36.7, six 35.5)
+  const int room = tiles <= sms / 2 ? gate::kBarOff : gate::kArena;
+  p.n_stages = room / stage < gate::kMaxStages ? room / stage : gate::kMaxStages;
   p.grid = (int32_t)(2 * (tiles < sms / 2 ? tiles : sms / 2));
   return true;
 }

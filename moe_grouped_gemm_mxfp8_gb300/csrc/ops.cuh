@@ -14,7 +14,7 @@ constexpr int kMaxTopk = 32;
 constexpr int kMaxGroups = 64;
 constexpr int kLayerMaxTokens = 64;
 // The router's cluster form up to here, one wave of its largest clusters (1024 tokens of 2048, 256 experts: 18.7 us,
-// the pair form 32; 1440 tokens: 34.9, the pair form 32)
+// the pair form 32; 1440 tokens: 34.9 and 32)
 constexpr int kGateClusterTokens = 1024;
 
 // The router's rule (gmmfr_gate_problem).
