@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "epilogue.cuh"
 #include "ops.cuh"
@@ -780,8 +781,9 @@ cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, 
 // groups of 8 (152 SMs: 15 clusters of 8); without an answer, as many as the SMs hold.  One CTA each: `sms`.
 static int64_t stream_slots(int S, int sms) {
   if (S == 1) return std::max(1, sms);
-  static int64_t known[3] = {};  // S = 2, 4, 8
-  int64_t& n = known[S == 2 ? 0 : (S == 4 ? 1 : 2)];
+  static std::atomic<int> known[3];  // S = 2, 4, 8
+  std::atomic<int>& kept = known[S == 2 ? 0 : (S == 4 ? 1 : 2)];
+  int n = kept.load(std::memory_order_relaxed);
   if (n == 0) {
     auto kernel = linear_stream_kernel<GMMFR_ACT_NONE>;
     cudaLaunchConfig_t lc = {};
@@ -802,6 +804,7 @@ static int64_t stream_slots(int S, int sms) {
       cudaGetLastError();
       n = std::max(1, sms / S);
     }
+    kept.store(n, std::memory_order_relaxed);
   }
   return n;
 }

@@ -413,6 +413,31 @@ def test_linear_rows_past_the_last_full_tile(M, N, K, act, unaligned):
         assert torch.equal(a, b)
 
 
+def test_calls_in_a_cuda_graph():
+    g = _gen(4)
+    d = _layer_inputs(g, 24, 256, 16, 64, 64, False)
+    layer = _make_layer(d, topk=4)
+    gate = B.MoeGate(d["wg"].cuda(), topk=4)
+    x = d["x"].cuda()
+    calls = [lambda: layer(x, residual=x), lambda: gate(x)[1]]
+    for M, N, K in ((1, 64, 72), (100, 640, 1000), (1030, 4096, 2048)):
+        lin, y = B.Linear(_randn(g, N, K, scale=K ** -0.5).cuda()), _randn(g, M, K).cuda()
+        calls.append(lambda lin=lin, y=y: lin(y))
+    eager = [c().clone() for c in calls]  # sizes the workspaces
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for c in calls:
+            c()
+        with torch.cuda.graph(graph, stream=stream):
+            captured = [c() for c in calls]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(eager, captured):
+        assert torch.equal(a, b)
+
+
 def test_error_words_are_clean():
     g = _gen(3)
     s = torch.cuda.current_stream().cuda_stream
