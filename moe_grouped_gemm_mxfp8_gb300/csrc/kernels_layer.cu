@@ -20,11 +20,12 @@
 //   down   every CTA with a piece waits for the others at its end and adds its share of the tile.
 // Both orders are fixed, so results are the same bits every time.
 //
-// H = 2048, 256 experts of 512 with a shared one, 8 per token, BF16: 64 tokens (1408 MB) 230 us, 6.1 TB/s, 91% of a copy's
-// rate; 13 tokens that share experts (491 MB) 88.6 us, 5.5 TB/s.  One token (58 MB) 28.5 us, 2.0 TB/s: latencies, one
-// after the other: the gate 6, launch, set-up and first copy 4, the stream 11, the two joins and the up run's
+// H = 2048, 256 experts of 512 with a shared one, 8 per token, BF16: 64 tokens (1408 MB) 229 us, 6.1 TB/s, 92% of a copy's
+// rate; 13 tokens that share experts (491 MB) 87.8 us, 5.6 TB/s.  One token (58 MB) 28 us, 2.1 TB/s: latencies, one
+// after the other: the gate 6, launch, set-up and first copy 4, the stream 10, the two joins and the up run's
 // hand-over 8; the same 18 us or so stand in the larger calls.
-// MXFP8, 16 experts of 7168 x 2048 with a shared one of 4096, 40 tokens (819 MB): 153 us, 5.4 TB/s.
+// MXFP8, 16 experts of 7168 x 2048 with a shared one of 4096, 40 tokens (819 MB): 151 us, 5.4 TB/s; 16 of it between
+// the runs, while the units with all 40 tokens are finished.
 //
 // sw is rounded to what the tensor cores take: BF16, or with MXFP8 weights a sum of two E4M3 numbers with
 // their block scales (hi + lo, about as exact as BF16), and the tokens likewise: BF16's eight bits split exactly
