@@ -136,8 +136,8 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
 }
 
 // ---------------------------------------------------------------- the router for a few tokens by one cluster
-// A cluster of 8 CTAs takes 8 kTiles tokens.  Its warps (64 or 128) share the products: a warp takes one group of 16 experts
-// and one of warps / groups splits of K (blocks of 32, taken in turn) against all the tokens, and sends its sums straight to
+// A cluster of 8 CTAs takes 8 kTiles tokens.  Its warps (64 or 128) share the products: a warp takes one or two groups of 16
+// experts and one of the splits of K (blocks of 32, taken in turn) against all the tokens, and sends its sums straight to
 // the CTAs that select for those tokens (CTA c: tokens c * kTiles ...), which add the splits in order.  The weight rows
 // are read straight into the operand registers of mma.sync: lane l holds 8 consecutive elements of rows l / 4 and
 // l / 4 + 8, which serve as the lane's K slots of two products (the K slots of A and B are permuted alike, which leaves
@@ -150,6 +150,10 @@ constexpr int kCluster = 8;
 // six blocks that a warp of the 64 asks for at once, and the clusters are few (15 with a CTA per SM).  One token,
 // H = 2048, 256 experts: 5.9 us with 512, 6.6 with 256; H = 7168, 16 experts: 5.8 and 5.0.
 constexpr int kSmall = 512, kLarge = 256;
+// Groups of 16 experts that a warp takes: with 16 or 32 tokens two share its tokens' loads, since what reaches an SM is what
+// bounds it then, unless that leaves too few pairs of groups for the warps.  1024 tokens of 7168, 512 experts: 71.5 us
+// with one, 52.5 with two; 333 of 5120, 160 experts: 14.0 and 13.2; 300 of 4096, 64 experts: 7.8 and 8.7.
+inline int cluster_groups(int64_t T, int E) { return T > 32 * 8 && E > 64 ? 2 : 1; }
 inline int cluster_threads(int64_t T, int64_t H, int E) {
   return T <= 15 * 8 && (int64_t)((E + 15) / 16) * ((H + 31) / 32) > 64 * 6 ? kSmall : kLarge;
 }
@@ -166,9 +170,9 @@ struct TeamScratch {
 };
 template <int kTiles, int kThr>
 struct Smem {
-  // of the tokens this CTA selects for: the splits' sums (a warp's 16 each), the logits, the probabilities
-  float logits[kTiles][kThr / 32 * kCluster * 16 > kMaxExperts ? kThr / 32 * kCluster * 16 : kMaxExperts];
-  uint32_t key[kTiles][kMaxExperts];
+  // of the tokens this CTA selects for: the splits' sums; then the logits, the probabilities, and the selection's keys
+  // behind them
+  float logits[kTiles][2 * kMaxExperts];
   TeamScratch team[kTiles];
   float bias[kMaxExperts];
 };
@@ -317,39 +321,41 @@ __device__ __forceinline__ void gate_select_team(const GateRule& r, const float*
   }
 }
 
-template <int kTiles, int kThr>
+template <int kTiles, int kThr, int kG>
 __device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t t0, gate::Smem<kTiles, kThr>& sm, uint32_t rank,
                                                     int warp, int lane) {
-  const int tid = threadIdx.x, E = p.rule.E, groups = (E + 15) / 16;
+  // blocks of 32 K in flight
+  constexpr int kU = kThr == gate::kSmall ? 8 : (kTiles == 1 ? 6 : (kTiles == 2 ? (kG == 1 ? 4 : 3) : (kG == 1 ? 3 : 2)));
+  const int tid = threadIdx.x, E = p.rule.E, groups = ((E + 15) / 16 + kG - 1) / kG;  // of kG x 16 experts
   const int blocks = (int)((p.H + 31) / 32);
-  constexpr int kU = kThr == gate::kSmall ? 8 : kTiles == 1 ? 6 : (kTiles == 2 ? 4 : 2);  // blocks of 32 K in flight
   const int w = (int)rank * (kThr / 32) + warp;
   const int splits = min(gate::kCluster * (kThr / 32) / groups, (blocks + kU - 1) / kU);
-  const int split = w / groups, grp = w - split * groups;
+  const int split = w / groups, grp = w - split * groups, row = groups * kG * 16;
   ptx::cluster_wait();  // the other CTAs have started: their shared memory may be written
   if (split < splits) {
     // rows past the end repeat the last one; what they give is not read
-    const int ea = min(grp * 16 + (lane >> 2), E - 1), eb = min(grp * 16 + 8 + (lane >> 2), E - 1);
-    const __nv_bfloat16* wa = p.weight + (int64_t)ea * p.H;
-    const __nv_bfloat16* wb = p.weight + (int64_t)eb * p.H;
+    const __nv_bfloat16* wr[2 * kG];
+#pragma unroll
+    for (int i = 0; i < 2 * kG; ++i) wr[i] = p.weight + (int64_t)min((grp * 2 * kG + i) * 8 + (lane >> 2), E - 1) * p.H;
     const __nv_bfloat16* xr[kTiles];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       const int64_t t = t0 + 8 * i + (lane >> 2);
       xr[i] = p.x + (t < p.T ? t : p.T - 1) * p.ldx;
     }
-    float acc[kTiles][4] = {};
+    float acc[kG][kTiles][4] = {};
     for (int b0 = split; b0 < blocks; b0 += splits * kU) {
-      uint4 a[kU], b[kU], x[kU][kTiles];
+      uint4 a[kU][2 * kG], x[kU][kTiles];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t k = (int64_t)(b0 + u * splits) * 32 + (lane & 3) * 8;
-        a[u] = b[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * kG; ++i) a[u][i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
         if (k < p.H) {
-          a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
-          b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
+#pragma unroll
+          for (int i = 0; i < 2 * kG; ++i) a[u][i] = __ldg(reinterpret_cast<const uint4*>(wr[i] + k));
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(xr[i] + k));
         }
@@ -357,21 +363,27 @@ __device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          ptx::mma_16816(acc[i], a[u].x, b[u].x, a[u].y, b[u].y, x[u][i].x, x[u][i].y);
-          ptx::mma_16816(acc[i], a[u].z, b[u].z, a[u].w, b[u].w, x[u][i].z, x[u][i].w);
+        for (int g = 0; g < kG; ++g)
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            const uint4 &lo = a[u][2 * g], &hi = a[u][2 * g + 1];
+            ptx::mma_16816(acc[g][i], lo.x, hi.x, lo.y, hi.y, x[u][i].x, x[u][i].y);
+            ptx::mma_16816(acc[g][i], lo.z, hi.z, lo.w, hi.w, x[u][i].z, x[u][i].w);
+          }
+    }
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const int at = split * row + (grp * kG + g) * 16 + (lane >> 2);  // at most the cluster's warps x kG x 16: 2 kMaxExperts
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int tok = 8 * i + (lane & 3) * 2 + c;
+          const uint32_t dst = ptx::map_to_rank(ptx::smem_u32(&sm.logits[tok % kTiles][at]), (uint32_t)(tok / kTiles));
+          ptx::st_cluster_f32(dst, acc[g][i][c]);
+          ptx::st_cluster_f32(dst + 32, acc[g][i][2 + c]);
         }
     }
-    const int at = split * groups * 16 + grp * 16 + (lane >> 2);  // the warp's place in the cluster x 16 at most
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int tok = 8 * i + (lane & 3) * 2 + c;
-        const uint32_t dst = ptx::map_to_rank(ptx::smem_u32(&sm.logits[tok % kTiles][at]), (uint32_t)(tok / kTiles));
-        ptx::st_cluster_f32(dst, acc[i][c]);
-        ptx::st_cluster_f32(dst + 32, acc[i][2 + c]);
-      }
   }
   ptx::cluster_sync();
   if (splits > 1) {  // the splits' sums, in order
@@ -380,14 +392,14 @@ __device__ __forceinline__ void gate_cluster_logits(const GateParams& p, int64_t
     for (int e = tid % kTeam; e < E; e += kTeam) {
       float s = 0.f;
 #pragma unroll 4
-      for (int k = 0; k < splits; ++k) s += l[k * groups * 16 + e];
+      for (int k = 0; k < splits; ++k) s += l[k * row + e];
       l[e] = s;
     }
     __syncthreads();
   }
 }
 
-template <int kTiles, int kThr>
+template <int kTiles, int kThr, int kG>
 __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, gate::Smem<kTiles, kThr>& sm, uint32_t rank) {
   constexpr int kTeam = (kThr < 256 ? kThr : 256) / kTiles;  // more threads than that would wait on one another for longer
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -397,7 +409,7 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
   ptx::cluster_arrive_relaxed();
   if (p.select_bias)
     for (int e = tid; e < E; e += kThr) sm.bias[e] = p.select_bias[e];
-  gate_cluster_logits<kTiles, kThr>(p, t0, sm, rank, warp, lane);
+  gate_cluster_logits<kTiles, kThr, kG>(p, t0, sm, rank, warp, lane);
   if (p.logits) {
     for (int i = 0; i < kTiles; ++i)
       if (t + i < p.T)
@@ -408,7 +420,8 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
   if (by_team) {
     const int i = tid / kTeam;  // the team's token
     if (i < kTiles && t + i < p.T)
-      gate_select_team<kTeam>(p.rule, bias, sm.logits[i], sm.key[i], sm.team[i], tid % kTeam, 1 + i, p.ids, p.ids_i64,
+      gate_select_team<kTeam>(p.rule, bias, sm.logits[i], reinterpret_cast<uint32_t*>(sm.logits[i] + kMaxExperts),
+                              sm.team[i], tid % kTeam, 1 + i, p.ids, p.ids_i64,
                               p.weights, (t + i) * p.rule.topk);
   } else if (warp < kTiles && t + warp < p.T) {
     const float* l = sm.logits[warp];

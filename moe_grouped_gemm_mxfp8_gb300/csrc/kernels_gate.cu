@@ -34,7 +34,7 @@ constexpr int kPairExperts = 512;  // the pair form's most: their logits fill TM
 }  // namespace gate
 
 // ============================================================================ cluster form
-template <int kTiles, int kThr>
+template <int kTiles, int kThr, int kG = 1>
 __global__ void __launch_bounds__(kThr) gate_cluster_kernel(const __grid_constant__ GateParams p) {
   __shared__ gate::Smem<kTiles, kThr> sm;
   ptx::griddep_wait();
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThr) gate_cluster_kernel(const __grid_constan
     p.hdr[0] = 1;
     p.hdr[1] = 0;
   }
-  gate_cluster<kTiles, kThr>(p, (int64_t)(blockIdx.x / gate::kCluster) * 8 * kTiles, sm, ptx::cluster_rank());
+  gate_cluster<kTiles, kThr, kG>(p, (int64_t)(blockIdx.x / gate::kCluster) * 8 * kTiles, sm, ptx::cluster_rank());
 }
 
 // ============================================================================ pair form
@@ -581,9 +581,10 @@ cudaError_t launch_gate(const GateMaps& maps, const GateParams& p, cudaStream_t 
     lc.gridDim = dim3((unsigned)((p.T + 8 * tiles - 1) / (8 * tiles) * gate::kCluster));
     const int threads = gate::cluster_threads(p.T, p.H, p.rule.E);
     lc.blockDim = dim3((unsigned)threads);
-    auto kernel = threads == gate::kSmall ? gate_cluster_kernel<1, gate::kSmall>
-                        : (tiles == 1 ? gate_cluster_kernel<1, gate::kLarge>
-                                      : (tiles == 2 ? gate_cluster_kernel<2, gate::kLarge> : gate_cluster_kernel<4, gate::kLarge>));
+    auto kernel = threads == gate::kSmall ? gate_cluster_kernel<1, gate::kSmall> : gate_cluster_kernel<1, gate::kLarge>;
+    const bool two = gate::cluster_groups(p.T, p.rule.E) == 2;
+    if (tiles == 2) kernel = two ? gate_cluster_kernel<2, gate::kLarge, 2> : gate_cluster_kernel<2, gate::kLarge>;
+    if (tiles == 4) kernel = two ? gate_cluster_kernel<4, gate::kLarge, 2> : gate_cluster_kernel<4, gate::kLarge>;
     return cudaLaunchKernelEx(&lc, kernel, p);
   }
   static int configured_device = -1;

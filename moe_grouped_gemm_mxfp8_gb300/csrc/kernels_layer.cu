@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThr) layer_front_kernel(const __grid_constant
   const int lane = threadIdx.x & 31;
   const int routers = (T + 7) / 8 * gate::kCluster;
   if ((int)blockIdx.x < routers) {
-    gate_cluster<1, kThr>(g, (int64_t)(blockIdx.x / gate::kCluster) * 8, sm, ptx::cluster_rank());
+    gate_cluster<1, kThr, 1>(g, (int64_t)(blockIdx.x / gate::kCluster) * 8, sm, ptx::cluster_rank());
     return;
   }
   const int block = blockIdx.x - routers, blocks = gridDim.x - routers, warps = blocks * (kThr / 32);
