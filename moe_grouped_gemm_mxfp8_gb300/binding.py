@@ -562,6 +562,11 @@ class _Handle:
         self._index = torch.cuda.current_device() if device.index is None else device.index
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._empty = torch.empty
+        # what torch.empty ends in for a CUDA tensor, without its argument parsing and dispatch (half its time); on the
+        # current device only
+        guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+        self._empty_here = getattr(guards, "_empty_strided_cuda", None)
+        self._current = torch._C._cuda_getDevice
         self._spaces = {}
 
     def _grow(self, stream: int, need: int):
@@ -573,7 +578,10 @@ class _Handle:
         return entry
 
     def _new(self, shape, dtype, stream):
-        t = self._empty(shape, dtype=dtype, device=self._device)
+        if self._empty_here is not None and self._current() == self._index:
+            t = self._empty_here(shape, (shape[1], 1), dtype)
+        else:
+            t = self._empty(shape, dtype=dtype, device=self._device)
         if stream is not None:
             t.record_stream(stream)
         return t
