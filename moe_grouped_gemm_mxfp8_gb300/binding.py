@@ -524,11 +524,13 @@ def _refuse(name, t, want):
 
 
 def _rows(t, name: str, rows, cols: int, dtype):
-    """The row stride of a 2-D device tensor [rows, cols] (rows None: any) whose rows are contiguous; 0
-    (dense) when it has one row, which has no stride to speak of."""
+    """The row stride of a 2-D device tensor [rows, cols] (rows None: any) whose rows are contiguous; 0 when
+    they are dense, or there is one, which has no stride to speak of."""
     shape = t.shape
     if t.dtype is not dtype or len(shape) != 2 or shape[1] != cols or not t.is_cuda or (rows is not None and shape[0] != rows):
         _refuse(name, t, f"[{'rows' if rows is None else rows}, {cols}] {dtype}")
+    if t.is_contiguous():
+        return 0
     ld, inner = t.stride()
     if shape[0] > 1:
         # an expanded row (stride 0) is not a row of its own
@@ -574,8 +576,14 @@ class _Handle:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self._device)
         if stream != self._raw_stream(self._index):
             ws.record_stream(torch.cuda.ExternalStream(stream, device=self._device))
-        self._spaces[stream] = entry = (ws.data_ptr(), ws.numel(), ws)
+        # the C call's arguments are kept as ctypes objects: converting Python integers costs more than setting them
+        entry = (ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream), ws.numel(), ws)
+        self._spaces[stream] = entry
         return entry
+
+    def _entry(self, name):
+        """The C entry, called with ctypes objects of its argument types alone."""
+        return self._lib[name]
 
     def _new(self, shape, dtype, stream):
         if self._empty_here is not None and self._current() == self._index:
@@ -619,7 +627,9 @@ class MoeGate(_Handle):
         self._wptr, self._bptr = weight.data_ptr(), _ptr(select_bias)
         self._bf16, self._f32 = torch.bfloat16, torch.float32
         self._H, self._E, self._topk = p.H, p.E, p.topk
-        self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_moe_gate
+        self._ref, self._fn = ctypes.byref(p), self._entry("gmmfr_moe_gate")
+        self._cx, self._ci, self._ck, self._cl = (ctypes.c_void_p() for _ in range(4))
+        self._cw, self._cb = ctypes.c_void_p(self._wptr), ctypes.c_void_p(self._bptr)
         gmmfr_moe_gate_workspace_size(p)  # refuses a rule that is out of range
         self._T, self._need = 0, 0
 
@@ -649,9 +659,11 @@ class MoeGate(_Handle):
         lptr = None if logits is None else _dense(logits, "logits", (T, self._E), self._f32)
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
-        if ws is None or ws[1] < self._need:
+        if ws is None or ws[3] < self._need:
             ws = self._grow(s, self._need)
-        st = self._fn(self._ref, x.data_ptr(), self._wptr, self._bptr, iptr, wptr, lptr, ws[0], ws[1], s)
+        cx, ci, ck, cl = self._cx, self._ci, self._ck, self._cl
+        cx.value, ci.value, ck.value, cl.value = x.data_ptr(), iptr, wptr, lptr
+        st = self._fn(self._ref, cx, self._cw, self._cb, ci, ck, cl, ws[0], ws[1], ws[2])
         if st:
             _check(st)
         return ids, weights
@@ -684,11 +696,14 @@ class MoeLayer(_Handle):
         self._g = p.gate
         self._keep = (gate_weight, select_bias)
         self._wptr, self._bptr = gate_weight.data_ptr(), _ptr(select_bias)
-        self._weights = (self._prepared.data_ptr(), self._prepared.numel(), _ptr(self._shared),
-                         0 if self._shared is None else self._shared.numel())
+        self._weights = (ctypes.c_void_p(self._prepared.data_ptr()), ctypes.c_size_t(self._prepared.numel()),
+                         ctypes.c_void_p(_ptr(self._shared)),
+                         ctypes.c_size_t(0 if self._shared is None else self._shared.numel()))
         self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
         self._H, self._topk = H, gp.topk
-        self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_moe_layer
+        self._ref, self._fn = ctypes.byref(p), self._entry("gmmfr_moe_layer")
+        self._cx, self._cr, self._co, self._ci, self._ck = (ctypes.c_void_p() for _ in range(5))
+        self._cw, self._cb = ctypes.c_void_p(self._wptr), ctypes.c_void_p(self._bptr)
         gmmfr_moe_layer_workspace_size(p)
         self._T, self._need = 0, 0
 
@@ -728,10 +743,11 @@ class MoeLayer(_Handle):
         kptr = None if topk_weights is None else _dense(topk_weights, "topk_weights", (T, self._topk), self._f32)
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
-        if ws is None or ws[1] < self._need:
+        if ws is None or ws[3] < self._need:
             ws = self._grow(s, self._need)
-        st = self._fn(self._ref, x.data_ptr(), self._wptr, self._bptr, rptr, out.data_ptr(), *self._weights, iptr, kptr,
-                      ws[0], ws[1], s)
+        cx, cr, co, ci, ck = self._cx, self._cr, self._co, self._ci, self._ck
+        cx.value, cr.value, co.value, ci.value, ck.value = x.data_ptr(), rptr, out.data_ptr(), iptr, kptr
+        st = self._fn(self._ref, cx, self._cw, self._cb, cr, co, *self._weights, ci, ck, ws[0], ws[1], ws[2])
         if st:
             _check(st)
         return out
@@ -765,7 +781,9 @@ class Linear(_Handle):
                                     activation=ACTIVATIONS[activation],
                                     out_type=DT_F32 if self._out == torch.float32 else DT_BF16)
         self._bf16 = torch.bfloat16
-        self._ref, self._fn = ctypes.byref(p), self._lib.gmmfr_linear
+        self._ref, self._fn = ctypes.byref(p), self._entry("gmmfr_linear")
+        self._cx, self._cr, self._co = (ctypes.c_void_p() for _ in range(3))
+        self._cw, self._cb = ctypes.c_void_p(self._wptr), ctypes.c_void_p(self._bptr)
         gmmfr_linear_workspace_size(p)
         self._seen, self._need = None, 0
 
@@ -789,9 +807,11 @@ class Linear(_Handle):
             p.ld_out = _rows(out, "out", M, N, self._out)
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
-        if ws is None or ws[1] < self._need:
+        if ws is None or ws[3] < self._need:
             ws = self._grow(s, self._need)
-        st = self._fn(self._ref, xptr, self._wptr, self._bptr, rptr, out.data_ptr(), ws[0], ws[1], s)
+        cx, cr, co = self._cx, self._cr, self._co
+        cx.value, cr.value, co.value = xptr, rptr, out.data_ptr()
+        st = self._fn(self._ref, cx, self._cw, self._cb, cr, co, ws[0], ws[1], ws[2])
         if st:
             _check(st)
         return out
