@@ -21,23 +21,20 @@ __device__ __forceinline__ float key_value(uint32_t k) {  // of a key above 1
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// One warp selects token `logits[0..E)`'s experts (long choices of many experts); lane k < topk returns the k-th expert and its
-// weight.  Expert e sits in lane e % 32, register e / 32 (kPer registers: E <= 32 * kPer).
+// One warp selects token `logits[0..E)`'s experts (long choices of many experts); lane k < topk returns the k-th expert and
+// its weight.  Expert e sits in lane e % 32, register e / 32; select_bias may be in shared memory.
 // All sums are FP32; the exponential's argument is at most 0 and its sum at least 1.  Maxima and minima over the
 // warp are single redux instructions on order-preserving integers.
-template <int kPer>
 __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float* logits, const float* select_bias,
                                                  int lane, int& id_out, float& w_out) {
   constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kPer = kMaxExperts / 32;
   const float kNegInf = __int_as_float(0xff800000);
-  // the bias is asked for beside the logits (with many experts per lane it would cost too many registers)
-  constexpr bool kBiasFirst = kPer <= 8;
-  float p[kPer], bias[kBiasFirst ? kPer : 1];
+  float p[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
     p[i] = e < r.E ? logits[e] : kNegInf;
-    if constexpr (kBiasFirst) bias[i] = select_bias != nullptr && e < r.E ? __ldg(select_bias + e) : 0.f;
   }
   if (r.sigmoid) {
 #pragma unroll
@@ -65,10 +62,7 @@ __device__ __forceinline__ void gate_select_warp(const GateRule& r, const float*
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
-    float b = 0.f;
-    if constexpr (kBiasFirst) b = bias[i];
-    else if (select_bias != nullptr && e < r.E) b = __ldg(select_bias + e);
-    key[i] = e < r.E ? order_key(p[i] + b) : 0u;
+    key[i] = e < r.E ? order_key(select_bias ? p[i] + select_bias[e] : p[i]) : 0u;
   }
   if (r.n_group > 1) {
     const int per = r.E / r.n_group;
@@ -427,7 +421,7 @@ __device__ __forceinline__ void gate_cluster(const GateParams& p, int64_t t0, ga
     const float* l = sm.logits[warp];
     int id;
     float w;
-    gate_select_warp<32>(p.rule, l, bias, lane, id, w);
+    gate_select_warp(p.rule, l, bias, lane, id, w);
     if (lane < p.rule.topk) {
       const int64_t o = (t + warp) * p.rule.topk + lane;
       if (p.ids_i64) static_cast<int64_t*>(p.ids)[o] = id;

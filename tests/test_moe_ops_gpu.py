@@ -101,6 +101,9 @@ GATES = [
     dict(T=300, H=200, E=500, topk=32, scoring="sigmoid", n_group=5, topk_group=2),
     dict(T=530, H=136, E=129, topk=20, scoring="softmax"),
     dict(T=9, H=2048, E=16, topk=4, scoring="softmax"),
+    dict(T=5, H=72, E=600, topk=20, scoring="sigmoid", bias=True),
+    dict(T=270, H=64, E=600, topk=32, scoring="sigmoid", bias=True, n_group=30, topk_group=7),
+    dict(T=600, H=64, E=1000, topk=17, scoring="softmax", bias=True),
 ]
 
 
