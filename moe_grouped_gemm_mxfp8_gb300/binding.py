@@ -642,6 +642,7 @@ class MoeGate(_Handle):
         p.ldx = _rows(x, "x", None, self._H, self._bf16)
         T = x.shape[0]
         if T != self._T:
+            self._T = -1  # until the size is known to be taken: the problem holds what a refused call left in it
             p.T = T
             self._need = gmmfr_moe_gate_workspace_size(p)
             self._T = T
@@ -727,10 +728,11 @@ class MoeLayer(_Handle):
         g.ldx = _rows(x, "x", None, H, self._bf16)
         T = x.shape[0]
         if T != self._T:
+            self._T = -1  # until the size is known to be taken: the problem holds what a refused call left in it
             g.T = T
             self._need = gmmfr_moe_layer_workspace_size(p)
             self._T = T
-        rptr = None
+        rptr, p.ld_residual = None, 0
         if residual is not None:
             p.ld_residual = _rows(residual, "residual", T, H, self._bf16)
             rptr = residual.data_ptr()
@@ -793,10 +795,11 @@ class Linear(_Handle):
         M, xptr = x.shape[0], x.data_ptr()
         seen = (M, ldx, (xptr | self._wptr) & 15)
         if seen != self._seen:
+            self._seen = None  # until the size is known to be taken: the problem holds what a refused call left in it
             p.M, p.ldx, p.unaligned = M, ldx, int(seen[2] != 0)
             self._need = gmmfr_linear_workspace_size(p)
             self._seen = seen
-        rptr = None
+        rptr, p.ld_residual = None, 0
         if residual is not None:
             p.ld_residual = _rows(residual, "residual", M, N, self._bf16)
             rptr = residual.data_ptr()
