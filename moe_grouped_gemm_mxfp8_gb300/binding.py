@@ -553,7 +553,9 @@ def _dense(t, name: str, shape, dtype):
 
 class _Handle:
     """Workspaces of a handle, one per stream it has been called on (a workspace serves one call in
-    flight at a time); they grow with the largest call.  A handle serves one host thread at a time."""
+    flight at a time).  One that a larger call outgrows stays with the handle, since a CUDA graph captured on that
+    stream writes to it: a handle is kept as long as the graphs it was captured in, and graphs captured on the same
+    stream are replayed one after the other.  A handle serves one host thread at a time."""
 
     def __init__(self, device):
         import torch
@@ -570,9 +572,14 @@ class _Handle:
         self._empty_here = getattr(guards, "_empty_strided_cuda", None)
         self._current = torch._C._cuda_getDevice
         self._spaces = {}
+        self._outgrown = []
 
     def _grow(self, stream: int, need: int):
         import torch
+        old = self._spaces.get(stream)
+        if old is not None:
+            self._outgrown.append(old[4])
+            need = max(need, 2 * old[3])  # so that all that are kept come to less than the newest
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self._device)
         if stream != self._raw_stream(self._index):
             ws.record_stream(torch.cuda.ExternalStream(stream, device=self._device))
@@ -705,8 +712,9 @@ class MoeLayer(_Handle):
         self._ref, self._fn = ctypes.byref(p), self._entry("gmmfr_moe_layer")
         self._cx, self._cr, self._co, self._ci, self._ck = (ctypes.c_void_p() for _ in range(5))
         self._cw, self._cb = ctypes.c_void_p(self._wptr), ctypes.c_void_p(self._bptr)
-        gmmfr_moe_layer_workspace_size(p)
-        self._T, self._need = 0, 0
+        # one workspace for every number of tokens: sizes called, or captured in graphs, in any order share it
+        self._g.T = LAYER_MAX_TOKENS
+        self._need = gmmfr_moe_layer_workspace_size(p)
 
     @property
     def prepared(self):
@@ -726,12 +734,7 @@ class MoeLayer(_Handle):
     def __call__(self, x, residual=None, out=None, topk_ids=None, topk_weights=None, stream=None):
         p, g, H = self._p, self._g, self._H
         g.ldx = _rows(x, "x", None, H, self._bf16)
-        T = x.shape[0]
-        if T != self._T:
-            self._T = -1  # until the size is known to be taken: the problem holds what a refused call left in it
-            g.T = T
-            self._need = gmmfr_moe_layer_workspace_size(p)
-            self._T = T
+        g.T = T = x.shape[0]
         rptr, p.ld_residual = None, 0
         if residual is not None:
             p.ld_residual = _rows(residual, "residual", T, H, self._bf16)

@@ -1,6 +1,7 @@
 """The handles' own bookkeeping, on the host: real library checks, tensors that are addresses only, and a recording
 function in place of the C entry.  (No GPU: nothing is launched and no address is read.)"""
-import ctypes
+import gc
+import weakref
 
 import pytest
 import torch
@@ -78,7 +79,7 @@ def fakes(monkeypatch):
         self._lib, self._device, self._index = B.load(), torch.device("cuda", 0), 0
         self._raw_stream = lambda index: 7
         self._current = lambda: 0
-        self._spaces, self._old = {}, []
+        self._spaces, self._outgrown = {}, []
 
     monkeypatch.setattr(B._Handle, "__init__", init)
     monkeypatch.setattr(B._Handle, "_new", lambda self, shape, dtype, stream: FakeTensor(*shape, dtype=dtype))
@@ -154,3 +155,32 @@ def test_a_stride_of_one_call_is_not_the_next_ones(fakes):
     lin(FakeTensor(8, 128), residual=FakeTensor(8, 16, ld=19), out=FakeTensor(8, 16, ld=17))
     lin(FakeTensor(8, 128))
     assert [(p.ld_residual, p.ld_out) for p in calls.problems] == [(19, 17), (0, 0)]
+
+
+# ------------------------------------------------------------------------- what a captured graph writes to stays
+def test_every_number_of_tokens_takes_the_same_layer_workspace(fakes):
+    layer, calls = _layer()
+    for T in (1, 16, 64, 3):
+        layer(FakeTensor(T, 128))
+    assert len({w[0] for w in calls.workspaces}) == 1
+    layer._p.gate.T = 64
+    assert calls.workspaces[0][1] >= B.gmmfr_moe_layer_workspace_size(layer._p)
+
+
+def test_an_outgrown_workspace_stays_with_the_handle(fakes):
+    lin = B.Linear(FakeTensor(16, 129))  # rows off 16-byte boundaries: copies, whose size goes with the rows
+    calls = Calls(lin)
+    for M in (64, 128, 4096, 5000, 100000):
+        lin(FakeTensor(M, 129))
+        assert calls.workspaces[-1][1] >= B.gmmfr_linear_workspace_size(lin._p)
+    kept = [weakref.ref(t) for t in fakes]
+    addresses = [t.address for t in fakes]
+    largest = fakes[-1].numel()
+    assert len(fakes) > 2 and sum(t.numel() for t in fakes[:-1]) < largest + 256
+    fakes.clear()
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    assert {w[0] for w in calls.workspaces} <= set(addresses)
+    del lin, calls
+    gc.collect()
+    assert not any(r() is not None for r in kept)

@@ -41,3 +41,34 @@ def test_a_good_call_after_a_refused_one():
         with pytest.raises(B.GmmfrError):
             gate(odd[:rows])
         assert torch.equal(gate(x)[0], want_ids)
+
+
+def test_graphs_of_growing_sizes_captured_on_one_stream():
+    """Each size warmed up and captured in turn; whatever memory the handles gave back is taken and watched while the
+    graphs are replayed."""
+    layer = _layer()
+    lin = B.Linear(_randn(5, 48, 129))
+    x, y = _randn(6, 64, 256), _randn(7, 4096, 129)
+    sizes, rows = (1, 16, 64), (40, 700, 4096)
+    want = [(_layer()(x[:T]), B.Linear(_randn(5, 48, 129))(y[:M])) for T, M in zip(sizes, rows)]
+    stream, graphs = torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for T, M in zip(sizes, rows):
+            layer(x[:T]), lin(y[:M])
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                out = layer(x[:T]), lin(y[:M])
+            graphs.append((graph, out))
+        layer(x), lin(y)
+        taken = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in (1 << 10, 1 << 13, 1 << 16, 1 << 19, 1 << 21, 1 << 22)
+                 for _ in range(20)]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for (graph, out), ref in zip(graphs, want):
+            for o in out:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert all((t == 77).all() for t in taken)
