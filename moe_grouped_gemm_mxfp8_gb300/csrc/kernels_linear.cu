@@ -138,6 +138,16 @@ __device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, 
   }
 }
 
+// The first n (below 8) elements at p, and zeros.
+__device__ __forceinline__ uint4 load_part(const __nv_bfloat16* p, int n) {
+  const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+  uint32_t v[4] = {};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) v[i >> 1] |= (uint32_t)__ldg(e + i) << (16 * (i & 1));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // Lane j's bias, of column j of 32, onto a thread's 32 columns, by way of 128 bytes of the warp's.
 __device__ __forceinline__ void add_bias32(float bias, float (&v)[32], float* room) {
   room[threadIdx.x & 31] = bias;
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) xr[i] = p.x + (int64_t)min(8 * i + (lane >> 2), M - 1) * p.ldx;
     float acc[kTiles][4] = {};
-    const int64_t blocks = (p.K + 31) / 32;
+    const int64_t blocks = (p.K + 31) / 32, whole = p.K & ~int64_t(7);  // K in 16-byte pieces
     struct Operands {
       uint4 a[kU], b[kU], x[kU][kTiles];
     };
@@ -198,7 +208,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
         o.a[u] = o.b[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) o.x[u][i] = make_uint4(0, 0, 0, 0);
-        if (k < p.K) {
+        if (k < whole) {
           o.a[u] = __ldg(reinterpret_cast<const uint4*>(wa + k));
           o.b[u] = __ldg(reinterpret_cast<const uint4*>(wb + k));
 #pragma unroll
@@ -226,6 +236,19 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
       if (!more) break;
       if (b0 + 2 * step < blocks) load(even, b0 + 2 * step);
       multiply(odd);
+    }
+    // The elements past the last whole piece, one by one: what lies behind a row is another's, or nobody's, and a zero on
+    // one side would not do (0 x NaN).
+    if (whole < p.K && split == (int)(whole / 32 % splits)) {
+      const bool mine = (lane & 3) == (int)(whole % 32 / 8);
+      const int n = mine ? (int)(p.K - whole) : 0;
+      const uint4 a = load_part(wa + whole, n), b = load_part(wb + whole, n);
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        const uint4 x = load_part(xr[i] + whole, n);
+        ptx::mma_16816(acc[i], a.x, b.x, a.y, b.y, x.x, x.y);
+        ptx::mma_16816(acc[i], a.z, b.z, a.w, b.w, x.z, x.w);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {

@@ -83,7 +83,7 @@ constexpr int kLinearDirectRows = 32;
 constexpr int kLinearStreamRows = 128;
 
 struct LinearParams {
-  const __nv_bfloat16 *x, *w, *bias, *residual;  // x and w at 16-byte row pitches
+  const __nv_bfloat16 *x, *w, *bias, *residual;  // x and w at 16-byte row pitches; nothing is read past K
   void* out;
   uint32_t* hdr;  // error words
   int64_t M, N, K, ldx, ldw, ldr, ldo;
