@@ -406,11 +406,28 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _in_pool_of(stream):
+    """Allocations within come from the memory pool of the stream that is going to use them (None: the current one).  A
+    block of another stream's pool may be one that this stream's kernels still use."""
+    import torch
+    return torch.cuda.stream(stream)
+
+
+def _handed_over(stream, *tensors) -> None:
+    """Results of a call on `stream` are going to be used on the current stream."""
+    import torch
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def prepare_weights(problem: Problem, x2, scale, stream=None):
     """Allocate (torch) and fill the prepared-weight buffer for x2/scale."""
     import torch
     n = gmmfr_prepared_weights_size(problem)
-    buf = torch.empty(max(n, 16), dtype=torch.uint8, device=x2.device)
+    with _in_pool_of(stream):
+        buf = torch.empty(max(n, 16), dtype=torch.uint8, device=x2.device)
+    _handed_over(stream, buf)
     gmmfr_prepare_weights(problem, view(x2), view(scale), _ptr(buf), n, _stream(stream))
     return buf
 
@@ -425,7 +442,8 @@ def run(problem: Problem, inputs: dict, out, prepared=None, ws=None, stream=None
     """One call of the operator on device tensors (``inputs`` as made by
     workloads.make_inputs); accumulates into ``out`` in place."""
     if ws is None:
-        ws = workspace(problem, prepared is not None, out.device)
+        with _in_pool_of(stream):
+            ws = workspace(problem, prepared is not None, out.device)
     gmmfr_grouped_matmul_finalize_routing(
         problem, view(inputs["x1"]), view(inputs["x2"]) if prepared is None else None,
         view(inputs["scale"]) if prepared is None else None, view(inputs["pertoken_scale"]),
@@ -453,14 +471,16 @@ def route(topk_ids, topk_weights, x, x_scale, E: int, group_list_type: int = 1, 
                       group_list_type=group_list_type)
     M = batch * topk
     dev = x.device
-    o = dict(x1=torch.empty((M, K), dtype=torch.uint8, device=dev),
-             pertoken_scale=torch.empty((M,) + tuple(x_scale.shape[1:]), dtype=torch.uint8, device=dev),
-             group_list=torch.empty(E, dtype=torch.int64, device=dev),
-             row_index=torch.empty(M, dtype=torch.int64, device=dev),
-             logit=torch.empty(M, dtype=torch.float32, device=dev),
-             perm=torch.empty(M, dtype=torch.int32, device=dev))
-    if ws is None:
-        ws = torch.empty(max(gmmfr_moe_route_workspace_size(rp), 256), dtype=torch.uint8, device=dev)
+    with _in_pool_of(stream):
+        o = dict(x1=torch.empty((M, K), dtype=torch.uint8, device=dev),
+                 pertoken_scale=torch.empty((M,) + tuple(x_scale.shape[1:]), dtype=torch.uint8, device=dev),
+                 group_list=torch.empty(E, dtype=torch.int64, device=dev),
+                 row_index=torch.empty(M, dtype=torch.int64, device=dev),
+                 logit=torch.empty(M, dtype=torch.float32, device=dev),
+                 perm=torch.empty(M, dtype=torch.int32, device=dev))
+        if ws is None:
+            ws = torch.empty(max(gmmfr_moe_route_workspace_size(rp), 256), dtype=torch.uint8, device=dev)
+    _handed_over(stream, *o.values())
     gmmfr_moe_route(rp, _ptr(topk_ids), _ptr(topk_weights), _ptr(x), _ptr(x_scale), _ptr(o["x1"]),
                     _ptr(o["pertoken_scale"]), _ptr(o["group_list"]), _ptr(o["row_index"]), _ptr(o["logit"]),
                     _ptr(o["perm"]), _ptr(ws), ws.numel(), _stream(stream))
@@ -472,7 +492,9 @@ def ffn_prepare(H: int, I: int, E: int, w13_flat, w2_flat, stream=None):
     import torch
     fp = FfnProblem(N=0, H=H, I=I, E=E)
     n = gmmfr_ffn_prepared_weights_size(fp)
-    buf = torch.empty(n, dtype=torch.uint8, device=w13_flat.device)
+    with _in_pool_of(stream):
+        buf = torch.empty(n, dtype=torch.uint8, device=w13_flat.device)
+    _handed_over(stream, buf)
     gmmfr_ffn_prepare_weights(fp, _ptr(w13_flat), _ptr(w2_flat), _ptr(buf), n, _stream(stream))
     return buf
 
@@ -482,10 +504,12 @@ def ffn(sorted_tokens, prepared, expert_cumsum, H: int, I: int, E: int, result=N
     import torch
     N = sorted_tokens.shape[0]
     fp = FfnProblem(N=N, H=H, I=I, E=E)
-    if result is None:
-        result = torch.zeros((N, H), dtype=torch.bfloat16, device=sorted_tokens.device)
-    if ws is None:
-        ws = torch.empty(gmmfr_ffn_workspace_size(fp), dtype=torch.uint8, device=sorted_tokens.device)
+    with _in_pool_of(stream):
+        if result is None:
+            result = torch.zeros((N, H), dtype=torch.bfloat16, device=sorted_tokens.device)
+        if ws is None:
+            ws = torch.empty(gmmfr_ffn_workspace_size(fp), dtype=torch.uint8, device=sorted_tokens.device)
+    _handed_over(stream, result)
     gmmfr_llada2_moe_grouped_gemm(fp, _ptr(sorted_tokens), _ptr(prepared), _ptr(expert_cumsum), _ptr(result),
                                   _ptr(ws), ws.numel(), _stream(stream))
     return result, ws
@@ -501,7 +525,9 @@ def ffn_prepare_mx(H: int, I: int, E: int, w13, w13_scale, w2, w2_scale, stream=
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} in single bytes")
     fp = FfnProblem(N=0, H=H, I=I, E=E)
     n = gmmfr_ffn_prepared_weights_size_mx(fp)
-    buf = torch.empty(n, dtype=torch.uint8, device=w13.device)
+    with _in_pool_of(stream):
+        buf = torch.empty(n, dtype=torch.uint8, device=w13.device)
+    _handed_over(stream, buf)
     gmmfr_ffn_prepare_weights_mx(fp, _ptr(w13), _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(buf), n,
                                  _stream(stream))
     return buf
@@ -574,32 +600,38 @@ class _Handle:
         self._spaces = {}
         self._outgrown = []
 
-    def _grow(self, stream: int, need: int):
+    def _grow(self, raw: int, need: int, stream):
         import torch
-        old = self._spaces.get(stream)
+        old = self._spaces.get(raw)
         if old is not None:
             self._outgrown.append(old[4])
             need = max(need, 2 * old[3])  # so that all that are kept come to less than the newest
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self._device)
-        if stream != self._raw_stream(self._index):
-            ws.record_stream(torch.cuda.ExternalStream(stream, device=self._device))
+        with _in_pool_of(stream):
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self._device)
+            if old is None:  # a stream that the weights are new to
+                for t in self._weight_tensors():
+                    t.record_stream(torch.cuda.current_stream(self._device))
         # the C call's arguments are kept as ctypes objects: converting Python integers costs more than setting them
-        entry = (ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream), ws.numel(), ws)
-        self._spaces[stream] = entry
+        entry = (ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()), ctypes.c_void_p(raw), ws.numel(), ws)
+        self._spaces[raw] = entry
         return entry
+
+    def _weight_tensors(self):
+        return [t for t in self._keep if t is not None]
 
     def _entry(self, name):
         """The C entry, called with ctypes objects of its argument types alone."""
         return self._lib[name]
 
     def _new(self, shape, dtype, stream):
-        if self._empty_here is not None and self._current() == self._index:
-            t = self._empty_here(shape, (shape[1], 1), dtype)
-        else:
-            t = self._empty(shape, dtype=dtype, device=self._device)
         if stream is not None:
-            t.record_stream(stream)
-        return t
+            with _in_pool_of(stream):
+                t = self._empty(shape, dtype=dtype, device=self._device)
+            _handed_over(stream, t)
+            return t
+        if self._empty_here is not None and self._current() == self._index:
+            return self._empty_here(shape, (shape[1], 1), dtype)
+        return self._empty(shape, dtype=dtype, device=self._device)
 
 
 def _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale) -> GateProblem:
@@ -668,7 +700,7 @@ class MoeGate(_Handle):
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
         if ws is None or ws[3] < self._need:
-            ws = self._grow(s, self._need)
+            ws = self._grow(s, self._need, stream)
         cx, ci, ck, cl = self._cx, self._ci, self._ck, self._cl
         cx.value, ci.value, ck.value, cl.value = x.data_ptr(), iptr, wptr, lptr
         st = self._fn(self._ref, cx, self._cw, self._cb, ci, ck, cl, ws[0], ws[1], ws[2])
@@ -702,7 +734,7 @@ class MoeLayer(_Handle):
         self._p = p = LayerProblem(gate=gp, I=I, shared_I=shared_I, ld_residual=0, ld_out=0,
                                    weight_type=DT_E4M3 if mx else DT_BF16)
         self._g = p.gate
-        self._keep = (gate_weight, select_bias)
+        self._keep = (gate_weight, select_bias, self._prepared, self._shared)
         self._wptr, self._bptr = gate_weight.data_ptr(), _ptr(select_bias)
         self._weights = (ctypes.c_void_p(self._prepared.data_ptr()), ctypes.c_size_t(self._prepared.numel()),
                          ctypes.c_void_p(_ptr(self._shared)),
@@ -749,7 +781,7 @@ class MoeLayer(_Handle):
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
         if ws is None or ws[3] < self._need:
-            ws = self._grow(s, self._need)
+            ws = self._grow(s, self._need, stream)
         cx, cr, co, ci, ck = self._cx, self._cr, self._co, self._ci, self._ck
         cx.value, cr.value, co.value, ci.value, ck.value = x.data_ptr(), rptr, out.data_ptr(), iptr, kptr
         st = self._fn(self._ref, cx, self._cw, self._cb, cr, co, *self._weights, ci, ck, ws[0], ws[1], ws[2])
@@ -814,7 +846,7 @@ class Linear(_Handle):
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
         if ws is None or ws[3] < self._need:
-            ws = self._grow(s, self._need)
+            ws = self._grow(s, self._need, stream)
         cx, cr, co = self._cx, self._cr, self._co
         cx.value, cr.value, co.value = xptr, rptr, out.data_ptr()
         st = self._fn(self._ref, cx, self._cw, self._cb, cr, co, ws[0], ws[1], ws[2])

@@ -90,6 +90,7 @@ def fakes(monkeypatch):
         return spaces[-1]
 
     monkeypatch.setattr(torch, "empty", space)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
     prepared = FakeTensor(1, 1 << 20, dtype=torch.uint8)
     monkeypatch.setattr(B.MoeLayer, "_prepare", staticmethod(lambda *a: prepared))
     return spaces

@@ -72,3 +72,71 @@ def test_graphs_of_growing_sizes_captured_on_one_stream():
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, ref))
     assert all((t == 77).all() for t in taken)
+
+
+def _busy(*sizes):
+    """Gives back to the current stream's pool blocks of these bytes that the stream still writes to; what is returned
+    lies between them and keeps them from growing together; and the addresses."""
+    torch.cuda.synchronize()
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(128)]
+    torch.cuda._sleep(200_000_000)
+    for b in blocks:
+        b.fill_(255)
+    return blocks[::2], {b.data_ptr() for b in blocks[1::2]}
+
+
+def test_outputs_on_another_stream_take_no_memory_that_this_one_still_writes_to():
+    x, w = _randn(8, 2000, 256), _randn(9, 16, 256, scale=0.1)
+    gate, lin, layer, s = B.MoeGate(w, topk=4), B.Linear(w), _layer(), torch.cuda.Stream()
+    ids, weights = gate(x)
+    y, out = lin(x), layer(x[:9])
+    between, used = _busy(ids.nbytes, y.nbytes, out.nbytes)
+    got = (*gate(x, stream=s), lin(x, stream=s), layer(x[:9], stream=s))
+    assert not used & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    del between
+    for a, b in zip(got, (ids, weights, y, out)):
+        assert torch.equal(a, b)
+
+
+def test_functions_on_another_stream_take_no_memory_that_this_one_still_writes_to():
+    s = torch.cuda.Stream()
+    E, H, I, N = 4, 256, 64, 300
+    w13, w2, x = _randn(2, E, H, 2 * I, scale=0.06), _randn(3, E, I, H, scale=0.1), _randn(4, N, H)
+    ends = torch.tensor([0, 100, 100, 250, 300], dtype=torch.int32, device="cuda")
+    prepared = B.ffn_prepare(H, I, E, w13, w2)
+    want, _ = B.ffn(x, prepared, ends, H, I, E)
+    codes = [torch.randint(0, 120, shape, dtype=torch.uint8, device="cuda") for shape in ((E, H, 2 * I), (E, I, H))]
+    scales = [torch.full((E, k, n, 2), 120, dtype=torch.uint8, device="cuda") for k, n in ((H // 64, 2 * I), (I // 64, H))]
+    mx = B.ffn_prepare_mx(H, I, E, codes[0], scales[0], codes[1], scales[1])
+    ids = torch.randint(0, E, (N, 2), dtype=torch.int32, device="cuda")
+    wt, tok_scale = torch.rand(N, 2, device="cuda"), torch.full((N, H // 64, 2), 127, dtype=torch.uint8, device="cuda")
+    routed, _ = B.route(ids, wt, x.view(torch.uint8)[:, :H].contiguous(), tok_scale, E)
+    few = x.view(torch.uint8)[:, :H].contiguous()
+    between, used = _busy(prepared.nbytes, want.nbytes, mx.nbytes, *(t.nbytes for t in routed.values()))
+    got = B.ffn_prepare(H, I, E, w13, w2, stream=s)
+    got_mx = B.ffn_prepare_mx(H, I, E, codes[0], scales[0], codes[1], scales[1], stream=s)
+    got_routed, ws = B.route(ids, wt, few, tok_scale, E, stream=s)
+    y, ws2 = B.ffn(x, got, ends, H, I, E, stream=s)
+    assert not used & {t.data_ptr() for t in (got, got_mx, y, ws, ws2, *got_routed.values())}
+    torch.cuda.synchronize()
+    del between
+    assert torch.equal(got, prepared) and torch.equal(got_mx, mx) and torch.equal(y, want)
+    for k in routed:
+        assert torch.equal(got_routed[k], routed[k])
+
+
+def test_a_handle_dropped_while_another_stream_uses_its_weights():
+    x, s = _randn(10, 8, 256), torch.cuda.Stream()
+    want = _layer()(x)
+    layer = _layer()
+    layer(x)
+    torch.cuda.synchronize()
+    size = layer.prepared.numel()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    out = layer(x, stream=s)
+    del layer
+    taken = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all((t == 255).all() for t in taken)
