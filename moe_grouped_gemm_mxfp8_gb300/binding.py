@@ -543,37 +543,39 @@ def _numel(shape) -> int:
     return n
 
 
-def _refuse(name, t, want):
-    if t is not None and not t.is_cuda:
+def _refuse(name, t, want, device):
+    if t.get_device() < 0:
         raise ValueError("gmmfr takes device tensors")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, its handle on cuda:{device}")
     raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} strides {t.stride()}, expected {want}")
 
 
-def _rows(t, name: str, rows, cols: int, dtype):
-    """The row stride of a 2-D device tensor [rows, cols] (rows None: any) whose rows are contiguous; 0 when
+def _rows(t, name: str, rows, cols: int, dtype, device: int):
+    """The row stride of a 2-D tensor [rows, cols] (rows None: any) on cuda:`device` whose rows are contiguous; 0 when
     they are dense, or there is one, which has no stride to speak of."""
     shape = t.shape
-    if t.dtype is not dtype or len(shape) != 2 or shape[1] != cols or not t.is_cuda or (rows is not None and shape[0] != rows):
-        _refuse(name, t, f"[{'rows' if rows is None else rows}, {cols}] {dtype}")
+    if t.dtype is not dtype or len(shape) != 2 or shape[1] != cols or t.get_device() != device or (rows is not None and shape[0] != rows):
+        _refuse(name, t, f"[{'rows' if rows is None else rows}, {cols}] {dtype}", device)
     if t.is_contiguous():
         return 0
     ld, inner = t.stride()
     if shape[0] > 1:
         # an expanded row (stride 0) is not a row of its own
         if ld < cols or (inner != 1 and cols > 1):
-            _refuse(name, t, "rows that are contiguous and do not overlap")
+            _refuse(name, t, "rows that are contiguous and do not overlap", device)
         return ld
     if inner != 1 and cols > 1:
-        _refuse(name, t, "contiguous rows")
+        _refuse(name, t, "contiguous rows", device)
     return 0
 
 
-def _dense(t, name: str, shape, dtype):
-    """The address of a dense device tensor of this shape, or None for None."""
+def _dense(t, name: str, shape, dtype, device: int):
+    """The address of a dense tensor of this shape on cuda:`device`, or None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
-        _refuse(name, t, f"dense {shape} {dtype}")
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(name, t, f"dense {shape} {dtype}", device)
     return t.data_ptr()
 
 
@@ -581,7 +583,8 @@ class _Handle:
     """Workspaces of a handle, one per stream it has been called on (a workspace serves one call in
     flight at a time).  One that a larger call outgrows stays with the handle, since a CUDA graph captured on that
     stream writes to it: a handle is kept as long as the graphs it was captured in, and graphs captured on the same
-    stream are replayed one after the other.  A handle serves one host thread at a time."""
+    stream are replayed one after the other.  A handle serves one host thread at a time, and runs on the device
+    of its weights, whichever is current."""
 
     def __init__(self, device):
         import torch
@@ -592,8 +595,7 @@ class _Handle:
         self._index = torch.cuda.current_device() if device.index is None else device.index
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._empty = torch.empty
-        # what torch.empty ends in for a CUDA tensor, without its argument parsing and dispatch (half its time); on the
-        # current device only
+        # what torch.empty ends in for a CUDA tensor, without its argument parsing and dispatch (half its time)
         guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
         self._empty_here = getattr(guards, "_empty_strided_cuda", None)
         self._current = torch._C._cuda_getDevice
@@ -616,6 +618,12 @@ class _Handle:
         self._spaces[raw] = entry
         return entry
 
+    def _there(self, *args):
+        """The same call with the handle's device as the current one: a launch goes to the current device."""
+        import torch
+        with torch.cuda.device(self._index):
+            return self(*args)
+
     def _weight_tensors(self):
         return [t for t in self._keep if t is not None]
 
@@ -629,18 +637,18 @@ class _Handle:
                 t = self._empty(shape, dtype=dtype, device=self._device)
             _handed_over(stream, t)
             return t
-        if self._empty_here is not None and self._current() == self._index:
+        if self._empty_here is not None:
             return self._empty_here(shape, (shape[1], 1), dtype)
         return self._empty(shape, dtype=dtype, device=self._device)
 
 
-def _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale) -> GateProblem:
+def _gate_problem(device, weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale) -> GateProblem:
     import torch
     if weight.dim() != 2:
-        _refuse("weight", weight, "[E, H]")
+        _refuse("weight", weight, "[E, H]", device)
     E, H = weight.shape
-    _dense(weight, "weight", (E, H), torch.bfloat16)
-    _dense(select_bias, "select_bias", (E,), torch.float32)
+    _dense(weight, "weight", (E, H), torch.bfloat16, device)
+    _dense(select_bias, "select_bias", (E,), torch.float32, device)
     if scoring not in GATE_SCORING:
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(GATE_SCORING)}")
     return GateProblem(T=0, H=H, E=E, topk=topk, ldx=0, scoring=GATE_SCORING[scoring], n_group=n_group,
@@ -657,7 +665,7 @@ class MoeGate(_Handle):
                  ids_dtype=None):
         import torch
         super().__init__(weight.device)
-        self._p = p = _gate_problem(weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
+        self._p = p = _gate_problem(self._index, weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
         self._ids_dtype = torch.int32 if ids_dtype is None else ids_dtype
         if self._ids_dtype not in (torch.int32, torch.int64):
             raise ValueError(f"ids_dtype {ids_dtype} is not int32 or int64")
@@ -677,8 +685,10 @@ class MoeGate(_Handle):
         return self._topk
 
     def __call__(self, x, ids=None, weights=None, logits=None, stream=None):
-        p = self._p
-        p.ldx = _rows(x, "x", None, self._H, self._bf16)
+        p, dev = self._p, self._index
+        if self._current() != dev:
+            return self._there(x, ids, weights, logits, stream)
+        p.ldx = _rows(x, "x", None, self._H, self._bf16, dev)
         T = x.shape[0]
         if T != self._T:
             self._T = -1  # until the size is known to be taken: the problem holds what a refused call left in it
@@ -690,13 +700,13 @@ class MoeGate(_Handle):
             ids = self._new(shape, self._ids_dtype, stream)
             iptr = ids.data_ptr()
         else:
-            iptr = _dense(ids, "ids", shape, self._ids_dtype)
+            iptr = _dense(ids, "ids", shape, self._ids_dtype, dev)
         if weights is None:
             weights = self._new(shape, self._f32, stream)
             wptr = weights.data_ptr()
         else:
-            wptr = _dense(weights, "weights", shape, self._f32)
-        lptr = None if logits is None else _dense(logits, "logits", (T, self._E), self._f32)
+            wptr = _dense(weights, "weights", shape, self._f32, dev)
+        lptr = None if logits is None else _dense(logits, "logits", (T, self._E), self._f32, dev)
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
         if ws is None or ws[3] < self._need:
@@ -723,14 +733,19 @@ class MoeLayer(_Handle):
                  renormalise: bool = True, scale: float = 1.0):
         import torch
         super().__init__(gate_weight.device)
-        gp = _gate_problem(gate_weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
+        gp = _gate_problem(self._index, gate_weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
         E, H, I = gp.E, gp.H, w2.shape[1]
         mx = w13_scale is not None
-        self._prepared = self._prepare(E, H, I, w13, w13_scale, w2, w2_scale, mx)
+        for name, t in (("w13", w13), ("w2", w2), ("w13_scale", w13_scale), ("w2_scale", w2_scale), ("shared_w13", shared_w13),
+                        ("shared_w2", shared_w2), ("shared_w13_scale", shared_w13_scale), ("shared_w2_scale", shared_w2_scale)):
+            if t is not None and t.get_device() != self._index:
+                _refuse(name, t, "", self._index)
         shared_I, self._shared = 0, None
-        if shared_w13 is not None:
-            shared_I = shared_w2.shape[0]
-            self._shared = self._prepare(1, H, shared_I, shared_w13, shared_w13_scale, shared_w2, shared_w2_scale, mx)
+        with torch.cuda.device(self._index):
+            self._prepared = self._prepare(E, H, I, w13, w13_scale, w2, w2_scale, mx)
+            if shared_w13 is not None:
+                shared_I = shared_w2.shape[0]
+                self._shared = self._prepare(1, H, shared_I, shared_w13, shared_w13_scale, shared_w2, shared_w2_scale, mx)
         self._p = p = LayerProblem(gate=gp, I=I, shared_I=shared_I, ld_residual=0, ld_out=0,
                                    weight_type=DT_E4M3 if mx else DT_BF16)
         self._g = p.gate
@@ -764,20 +779,22 @@ class MoeLayer(_Handle):
         return ffn_prepare(H, I, E, w13, w2)
 
     def __call__(self, x, residual=None, out=None, topk_ids=None, topk_weights=None, stream=None):
-        p, g, H = self._p, self._g, self._H
-        g.ldx = _rows(x, "x", None, H, self._bf16)
+        p, g, H, dev = self._p, self._g, self._H, self._index
+        if self._current() != dev:
+            return self._there(x, residual, out, topk_ids, topk_weights, stream)
+        g.ldx = _rows(x, "x", None, H, self._bf16, dev)
         g.T = T = x.shape[0]
         rptr, p.ld_residual = None, 0
         if residual is not None:
-            p.ld_residual = _rows(residual, "residual", T, H, self._bf16)
+            p.ld_residual = _rows(residual, "residual", T, H, self._bf16, dev)
             rptr = residual.data_ptr()
         if out is None:
             out = self._new((T, H), self._bf16, stream)
             p.ld_out = 0
         else:
-            p.ld_out = _rows(out, "out", T, H, self._bf16)
-        iptr = None if topk_ids is None else _dense(topk_ids, "topk_ids", (T, self._topk), self._i32)
-        kptr = None if topk_weights is None else _dense(topk_weights, "topk_weights", (T, self._topk), self._f32)
+            p.ld_out = _rows(out, "out", T, H, self._bf16, dev)
+        iptr = None if topk_ids is None else _dense(topk_ids, "topk_ids", (T, self._topk), self._i32, dev)
+        kptr = None if topk_weights is None else _dense(topk_weights, "topk_weights", (T, self._topk), self._f32, dev)
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
         if ws is None or ws[3] < self._need:
@@ -805,12 +822,12 @@ class Linear(_Handle):
         if self._out not in (torch.bfloat16, torch.float32):
             raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
         if weight.dim() != 2:
-            _refuse("weight", weight, "[N, K]")
+            _refuse("weight", weight, "[N, K]", self._index)
         rows, K = weight.shape
-        ldw = _rows(weight, "weight", None, K, torch.bfloat16)
+        ldw = _rows(weight, "weight", None, K, torch.bfloat16, self._index)
         if activation == "swiglu" and rows % 2:
             raise ValueError(f"weight: {rows} rows; swiglu takes gate and up rows, an even number")
-        self._bptr = _dense(bias, "bias", (rows,), torch.bfloat16)
+        self._bptr = _dense(bias, "bias", (rows,), torch.bfloat16, self._index)
         self._keep = (weight, bias)
         self._wptr = weight.data_ptr()
         self._K, self._N = K, rows // 2 if activation == "swiglu" else rows
@@ -825,8 +842,10 @@ class Linear(_Handle):
         self._seen, self._need = None, 0
 
     def __call__(self, x, residual=None, out=None, stream=None):
-        p, N = self._p, self._N
-        ldx = _rows(x, "x", None, self._K, self._bf16)
+        p, N, dev = self._p, self._N, self._index
+        if self._current() != dev:
+            return self._there(x, residual, out, stream)
+        ldx = _rows(x, "x", None, self._K, self._bf16, dev)
         M, xptr = x.shape[0], x.data_ptr()
         seen = (M, ldx, (xptr | self._wptr) & 15)
         if seen != self._seen:
@@ -836,13 +855,13 @@ class Linear(_Handle):
             self._seen = seen
         rptr, p.ld_residual = None, 0
         if residual is not None:
-            p.ld_residual = _rows(residual, "residual", M, N, self._bf16)
+            p.ld_residual = _rows(residual, "residual", M, N, self._bf16, dev)
             rptr = residual.data_ptr()
         if out is None:
             out = self._new((M, N), self._out, stream)
             p.ld_out = 0
         else:
-            p.ld_out = _rows(out, "out", M, N, self._out)
+            p.ld_out = _rows(out, "out", M, N, self._out, dev)
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
         ws = self._spaces.get(s)
         if ws is None or ws[3] < self._need:

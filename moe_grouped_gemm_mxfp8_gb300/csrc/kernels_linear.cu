@@ -804,8 +804,11 @@ cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, 
 // groups of 8 (152 SMs: 15 clusters of 8); without an answer, as many as the SMs hold.  One CTA each: `sms`.
 static int64_t stream_slots(int S, int sms) {
   if (S == 1) return std::max(1, sms);
-  static std::atomic<int> known[3];  // S = 2, 4, 8
-  std::atomic<int>& kept = known[S == 2 ? 0 : (S == 4 ? 1 : 2)];
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][3];  // S = 2, 4, 8
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return std::max(1, sms / S);
+  std::atomic<int>& kept = known[dev][S == 2 ? 0 : (S == 4 ? 1 : 2)];
   int n = kept.load(std::memory_order_relaxed);
   if (n == 0) {
     auto kernel = linear_stream_kernel<GMMFR_ACT_NONE>;

@@ -1,5 +1,6 @@
 """The handles' own bookkeeping, on the host: real library checks, tensors that are addresses only, and a recording
 function in place of the C entry.  (No GPU: nothing is launched and no address is read.)"""
+import contextlib
 import gc
 import weakref
 
@@ -22,7 +23,7 @@ class FakeTensor:
 
     def __init__(self, *shape, dtype=torch.bfloat16, ld=None, device=0, off=0):
         self.shape, self.dtype = torch.Size(shape), dtype
-        self.ld = shape[1] if ld is None else ld
+        self.ld = shape[-1] if ld is None else ld
         self.index = device
         FakeTensor._next += 1 << 20
         self.address = FakeTensor._next + off
@@ -91,6 +92,8 @@ def fakes(monkeypatch):
 
     monkeypatch.setattr(torch, "empty", space)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
     prepared = FakeTensor(1, 1 << 20, dtype=torch.uint8)
     monkeypatch.setattr(B.MoeLayer, "_prepare", staticmethod(lambda *a: prepared))
     return spaces
@@ -102,8 +105,7 @@ def _gate(**kw):
 
 
 def _layer(**kw):
-    w2 = type("W", (), {"shape": (16, 64, 128)})()
-    h = B.MoeLayer(FakeTensor(16, 128), None, w2, topk=4, **kw)
+    h = B.MoeLayer(FakeTensor(16, 128), FakeTensor(16, 128, 128), FakeTensor(16, 64, 128), topk=4, **kw)
     return h, Calls(h)
 
 
@@ -185,3 +187,45 @@ def test_an_outgrown_workspace_stays_with_the_handle(fakes):
     del lin, calls
     gc.collect()
     assert not any(r() is not None for r in kept)
+
+
+# ------------------------------------------------------------------------- devices
+def test_tensors_of_another_device_are_refused(fakes):
+    gate, gate_calls = _gate()
+    layer, layer_calls = _layer()
+    lin = B.Linear(FakeTensor(16, 128))
+    lin_calls = Calls(lin)
+    here, there = FakeTensor(8, 128), FakeTensor(8, 128, device=1)
+    host = FakeTensor(8, 128, device=-1)
+    i32 = dict(dtype=torch.int32, device=1)
+    f32 = dict(dtype=torch.float32, device=1)
+    for call in (lambda: gate(there), lambda: layer(there), lambda: lin(there), lambda: gate(host), lambda: lin(host),
+                 lambda: gate(here, ids=FakeTensor(8, 4, **i32)), lambda: gate(here, weights=FakeTensor(8, 4, **f32)),
+                 lambda: gate(here, logits=FakeTensor(8, 64, **f32)), lambda: layer(here, residual=there),
+                 lambda: layer(here, out=there), lambda: layer(here, topk_ids=FakeTensor(8, 4, **i32)),
+                 lambda: layer(here, topk_weights=FakeTensor(8, 4, **f32)),
+                 lambda: lin(here, residual=FakeTensor(8, 16, device=1)), lambda: lin(here, out=FakeTensor(8, 16, device=1)),
+                 lambda: B.MoeGate(FakeTensor(64, 128, device=1), topk=2),
+                 lambda: B.Linear(FakeTensor(16, 128), bias=FakeTensor(16, device=1)),
+                 lambda: B.MoeLayer(FakeTensor(16, 128), FakeTensor(16, 128, 128, device=1), FakeTensor(16, 64, 128), topk=2)):
+        with pytest.raises(ValueError, match="cuda:1|device tensors"):
+            call()
+    assert not gate_calls.problems and not layer_calls.problems and not lin_calls.problems
+
+
+def test_a_call_runs_on_the_device_of_its_handle(fakes, monkeypatch):
+    current = [1]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    seen = []
+    for handle, x in ((_gate()[0], FakeTensor(8, 128)), (_layer()[0], FakeTensor(8, 128)), (B.Linear(FakeTensor(16, 128)), FakeTensor(8, 128))):
+        handle._current = lambda: current[0]
+        handle._fn = lambda *a: seen.append(current[0]) or 0
+        handle(x)
+    assert seen == [0, 0, 0] and current == [1]
