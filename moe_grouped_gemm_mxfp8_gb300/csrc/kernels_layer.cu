@@ -11,7 +11,8 @@
 // one: all T of them for every expert (T padded to 16), since the time goes to the weights' bytes and a token
 // that did not choose the expert costs only tensor-core slots that would idle.  Its row of sw is zero, which lets
 // the down run add all experts of a column tile into the same accumulator, the router's weight being folded into
-// sw (in FP32, before its rounding).
+// sw (in FP32, before its rounding).  Zero times an infinite or NaN weight is NaN: sums that come out NaN are made
+// again from the experts that the token chose (own_sum).
 // The weights' producer never waits for a token: the first down tiles are requested while other CTAs still finish
 // the up run.
 //
@@ -251,6 +252,78 @@ struct Walk {
     return true;
   }
 };
+
+// One E8M0 scale, and 32 K elements of a row in MXFP8: codes in two 16-byte chunks of an image, for a sum in FP32.
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+}
+__device__ __forceinline__ float scaled(float s, uint32_t a, uint32_t b) {  // s 2^(a - 127) 2^(b - 127)
+  return a == 255u || b == 255u ? __int_as_float(0x7fffffff) : ldexpf(s, (int)(a + b) - 254);
+}
+
+// sum over k of tiles[r, k] sw[t, k] over KB tiles of consecutive K
+template <bool kMx>
+__device__ float row_product(const uint8_t* tiles, int r, const uint8_t* images, int t, int KB, int npad) {
+  float s = 0.f;
+  const int img = layer::image_bytes(kMx, npad), tile = layer::tile_bytes(kMx);
+#pragma unroll 1
+  for (int kb = 0; kb < KB; ++kb, tiles += tile, images += img) {
+    if constexpr (!kMx) {
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        const uint4 w4 = *reinterpret_cast<const uint4*>(tiles + image_chunk(r, c));
+        const uint4 x4 = *reinterpret_cast<const uint4*>(images + image_chunk(t, c));
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w}, x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(x[i] << 16), s);
+          s = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(x[i] & 0xffff0000u), s);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float hi = 0.f, lo = 0.f;
+#pragma unroll 1
+        for (int c = 2 * q; c < 2 * q + 2; ++c) {
+          const uint8_t* w = tiles + image_chunk(r, c);
+          const uint8_t* x = images + kSfChunk + image_chunk(t, c);
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i) {
+            const float v = e4m3_value(w[i]);
+            hi = fmaf(v, e4m3_value(x[i]), hi);
+            lo = fmaf(v, e4m3_value(x[npad * 128 + i]), lo);
+          }
+        }
+        const uint32_t b = tiles[kWTileBytes + scale_at(r, q)];
+        s += scaled(hi, b, images[scale_at(t, q)]) + scaled(lo, b, images[scale_at(npad + t, q)]);
+      }
+    }
+  }
+  return s;
+}
+
+// Column n of token t's result, without the residual, from the experts that t chose and the shared one alone: what a NaN
+// in the accumulated sum is replaced by.  It is NaN for good when one of those is; else it came from an infinite or NaN
+// weight of an expert that only other tokens chose.  A rare call, kept out of line and small rather than fast.
+template <bool kMx>
+__device__ __noinline__ float own_sum(const LayerParams& p, const uint16_t* s_act, const uint16_t* s_ids, int A, int n_units, int t,
+                                      int64_t n) {
+  // every unit's sw is there (the sum was made of them), and with this read they are visible to this thread too
+  if (ld_acquire(p.up_done) < (uint32_t)n_units) return __int_as_float(0x7fffffff);
+  const int topk = p.gate.rule.topk, tile = layer::tile_bytes(kMx), j = (int)(n >> 7), r = (int)(n & 127);
+  const int64_t img = layer::image_bytes(kMx, p.npad);
+  float s = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < topk; ++k) {
+    const int e = s_ids[t * topk + k];
+    int a = 0;  // its place among the chosen experts, which are in order
+    while (a < A - 1 && s_act[a] != e) ++a;
+    s += row_product<kMx>(p.prepared2 + ((int64_t)e * p.NT2 + j) * p.KB2 * tile, r, p.swimg + a * p.KB2 * img, t, p.KB2, p.npad);
+  }
+  if (p.KB2s > 0) s += row_product<kMx>(p.shared2 + (int64_t)j * p.KB2s * tile, r, p.swimg_s, t, p.KB2s, p.npad);
+  return s;
+}
 
 }  // namespace
 
@@ -665,6 +738,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
             const int t = c0 + jj;
             if (t < T && n < g.H) {
               float o = v[jj];
+              if (o != o) o = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, n);
               if (p.residual) o += __bfloat162float(p.residual[t * p.ld_residual + n]);
               p.out[t * p.ld_out + n] = __float2bfloat16_rn(o);
             }
@@ -826,6 +900,13 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
+          }
+          const float all = s.x + s.y + s.z + s.w;
+          if (all != all) {  // (opposite infinities too, which own_sum is not asked about)
+            if (s.x != s.x) s.x = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col);
+            if (s.y != s.y) s.y = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col + 1);
+            if (s.z != s.z) s.z = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col + 2);
+            if (s.w != s.w) s.w = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col + 3);
           }
           __nv_bfloat16* o = p.out + t * p.ld_out + col;
           const __nv_bfloat16* res = p.residual ? p.residual + t * p.ld_residual + col : nullptr;
