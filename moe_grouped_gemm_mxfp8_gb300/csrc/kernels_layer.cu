@@ -12,7 +12,7 @@
 // that did not choose the expert costs only tensor-core slots that would idle.  Its row of sw is zero, which lets
 // the down run add all experts of a column tile into the same accumulator, the router's weight being folded into
 // sw (in FP32, before its rounding).  Zero times an infinite or NaN weight is NaN: sums that come out NaN are made
-// again from the experts that the token chose (own_sum).
+// again from the experts that the token chose (own_sums).
 // The weights' producer never waits for a token: the first down tiles are requested while other CTAs still finish
 // the up run.
 //
@@ -303,26 +303,38 @@ __device__ float row_product(const uint8_t* tiles, int r, const uint8_t* images,
   return s;
 }
 
-// Column n of token t's result, without the residual, from the experts that t chose and the shared one alone: what a NaN
-// in the accumulated sum is replaced by.  It is NaN for good when one of those is; else it came from an infinite or NaN
-// weight of an expert that only other tokens chose.  A rare call, kept out of line and small rather than fast.
+// Columns n .. n + 3 of token t's result, without the residual, of which s holds the accumulated sums: those that are NaN
+// made again from the experts that t chose and the shared one alone.  They stay NaN when one of those made them; else it was
+// an infinite or NaN weight of an expert that only other tokens chose.  A rare call, kept out of line and small rather than
+// fast (one token, MXFP8: 26.7 us without it).
 template <bool kMx>
-__device__ __noinline__ float own_sum(const LayerParams& p, const uint16_t* s_act, const uint16_t* s_ids, int A, int n_units, int t,
-                                      int64_t n) {
-  // every unit's sw is there (the sum was made of them), and with this read they are visible to this thread too
-  if (ld_acquire(p.up_done) < (uint32_t)n_units) return __int_as_float(0x7fffffff);
-  const int topk = p.gate.rule.topk, tile = layer::tile_bytes(kMx), j = (int)(n >> 7), r = (int)(n & 127);
+__device__ __noinline__ float4 own_sums(const LayerParams& p, const uint16_t* s_act, const uint16_t* s_ids, int A, int n_units, int t,
+                                        int64_t n0, float4 s) {
+  // every unit's sw is there (the sums were made of them), and with this read they are visible to this thread too
+  if (ld_acquire(p.up_done) < (uint32_t)n_units) return s;
+  const int topk = p.gate.rule.topk, tile = layer::tile_bytes(kMx);
   const int64_t img = layer::image_bytes(kMx, p.npad);
-  float s = 0.f;
+  float f[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll 1
-  for (int k = 0; k < topk; ++k) {
-    const int e = s_ids[t * topk + k];
-    int a = 0;  // its place among the chosen experts, which are in order
-    while (a < A - 1 && s_act[a] != e) ++a;
-    s += row_product<kMx>(p.prepared2 + ((int64_t)e * p.NT2 + j) * p.KB2 * tile, r, p.swimg + a * p.KB2 * img, t, p.KB2, p.npad);
+  for (int i = 0; i < 4; ++i) {
+    if (f[i] == f[i]) continue;
+    const int j = (int)((n0 + i) >> 7), r = (int)((n0 + i) & 127);
+    float own = 0.f;
+#pragma unroll 1
+    for (int k = 0; k <= topk; ++k) {
+      const uint8_t *tiles = p.shared2 + (int64_t)j * p.KB2s * tile, *images = p.swimg_s;  // last
+      if (k < topk) {
+        const int e = s_ids[t * topk + k];
+        int a = 0;  // its place among the chosen experts, which are in order
+        while (a < A - 1 && s_act[a] != e) ++a;
+        tiles = p.prepared2 + ((int64_t)e * p.NT2 + j) * p.KB2 * tile;
+        images = p.swimg + a * p.KB2 * img;
+      }
+      own += row_product<kMx>(tiles, r, images, t, k < topk ? p.KB2 : p.KB2s, p.npad);
+    }
+    f[i] = own;
   }
-  if (p.KB2s > 0) s += row_product<kMx>(p.shared2 + (int64_t)j * p.KB2s * tile, r, p.swimg_s, t, p.KB2s, p.npad);
-  return s;
+  return make_float4(f[0], f[1], f[2], f[3]);
 }
 
 }  // namespace
@@ -733,16 +745,28 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           float v[16];
           load_acc16<kMx>(taddr + c0, npad, v);
           const int64_t n = (int64_t)j * 128 + row;
+          uint32_t nans = 0;
 #pragma unroll
           for (int jj = 0; jj < 16; ++jj) {
             const int t = c0 + jj;
             if (t < T && n < g.H) {
+              if (v[jj] != v[jj]) {
+                nans |= 1u << jj;
+                continue;
+              }
               float o = v[jj];
-              if (o != o) o = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, n);
               if (p.residual) o += __bfloat162float(p.residual[t * p.ld_residual + n]);
               p.out[t * p.ld_out + n] = __float2bfloat16_rn(o);
             }
           }
+#pragma unroll 1
+          for (; nans; nans &= nans - 1) {
+            const int t = c0 + __ffs((int)nans) - 1;
+            float o = own_sums<kMx>(p, s_act, s_ids, A, n_units, t, n, make_float4(__int_as_float(0x7fffffff), 0.f, 0.f, 0.f)).x;
+            if (p.residual) o += __bfloat162float(p.residual[t * p.ld_residual + n]);
+            p.out[t * p.ld_out + n] = __float2bfloat16_rn(o);
+          }
+          __syncwarp();
         }
       } else {
         const uint32_t n_pieces = rehearse ? 0 : pieces.n;
@@ -902,12 +926,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
             s.w += v.w;
           }
           const float all = s.x + s.y + s.z + s.w;
-          if (all != all) {  // (opposite infinities too, which own_sum is not asked about)
-            if (s.x != s.x) s.x = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col);
-            if (s.y != s.y) s.y = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col + 1);
-            if (s.z != s.z) s.z = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col + 2);
-            if (s.w != s.w) s.w = own_sum<kMx>(p, s_act, s_ids, A, n_units, t, col + 3);
-          }
+          if (all != all) s = own_sums<kMx>(p, s_act, s_ids, A, n_units, t, col, s);
           __nv_bfloat16* o = p.out + t * p.ld_out + col;
           const __nv_bfloat16* res = p.residual ? p.residual + t * p.ld_residual + col : nullptr;
           if (vec) {
