@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 
 #include "gmmfr.h"
 #include "ops.cuh"
@@ -28,6 +29,22 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 int64_t stride_or(int64_t ld, int64_t dense) { return ld ? ld : dense; }
+
+// The limit of every wait in the kernels.  Testing aid: GMMFR_TEST_STALL_NS sets it, and makes a wait run out.  Read once:
+// small calls notice each look at the environment.
+struct Waits {
+  int64_t limit_ns;
+  int32_t stall;
+};
+const Waits& waits() {
+  static const Waits w = [] {
+    const char* t = std::getenv("GMMFR_TEST_STALL_NS");
+    if (!t) return Waits{4000000000ll, 0};
+    const long long ns = std::atoll(t);
+    return Waits{ns > 0 ? ns : 1000000, 1};
+  }();
+  return w;
+}
 
 gmmfr_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (!workspace) return fail(GMMFR_ERR_WORKSPACE, "workspace is NULL (needs %zu bytes)", need);
@@ -238,7 +255,8 @@ gmmfr_status gmmfr_moe_gate(const gmmfr_gate_problem* problem, const void* x, co
   g.weights = topk_weights;
   g.ids_i64 = p.ids_type == GMMFR_INDEX_I64;
   g.hdr = static_cast<uint32_t*>(workspace);
-  g.timeout_ns = 4000000000ll;
+  g.timeout_ns = waits().limit_ns;
+  g.test_stall = waits().stall;
   gmmfr::GateMaps maps;
   if (gmmfr::plan_gate(g, gmmfr::sm_count())) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
@@ -352,7 +370,8 @@ gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, 
   lp.KB2 = (int32_t)L.KB2;
   lp.NT1s = (int32_t)L.NT1s;
   lp.KB2s = (int32_t)L.KB2s;
-  lp.timeout_ns = 4000000000ll;
+  lp.timeout_ns = waits().limit_ns;
+  lp.test_stall = waits().stall;
   cudaError_t e = gmmfr::launch_layer(lp, gmmfr::sm_count(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "MoE layer launch");
   return GMMFR_OK;
@@ -397,7 +416,8 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   lp.ldw = stride_or(p.ldw, p.K);
   lp.ldr = stride_or(p.ld_residual, p.N);
   lp.ldo = stride_or(p.ld_out, p.N);
-  lp.timeout_ns = 4000000000ll;
+  lp.timeout_ns = waits().limit_ns;
+  lp.test_stall = waits().stall;
   lp.act = p.activation;
   lp.out_f32 = p.out_type == GMMFR_DT_F32;
   lp.vec_out = aligned(out, 16) && lp.ldo % (lp.out_f32 ? 4 : 8) == 0 && aligned(residual, 16) && lp.ldr % 8 == 0;

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(accf), 1);
+    ptx::mbar_init(ptx::smem_u32(accf), 1 + p.test_stall);
     ptx::mbar_init(ptx::smem_u32(acce), 32);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0;
@@ -141,8 +141,12 @@ __global__ void __launch_bounds__(gate::kPairThreads, 1)
         phase ^= 1;
       }
     }
-    if (!ok && rank == 0)  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
-      for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    if (!ok && rank == 0) {  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
+      for (int s = 0; s < n_stages; ++s)
+        if (!wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1)) break;  // rank 1 gave up before its load
+    } else if (!ok) {
+      let_loads_land();  // of a stage that rank 0 may not wait for: it may have given up before its own load
+    }
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
       ptx::mbar_init(ptx::smem_u32(&acce[b]), 4);
     }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
@@ -509,6 +509,13 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
   const int n_units = A * p.NT1 + p.NT1s;  // the shared expert's first
   const Run up((uint32_t)n_units * p.KB1, (uint32_t)p.KB1, (uint32_t)G), down((uint32_t)p.NT2 * D, (uint32_t)D, (uint32_t)G);
   Walk walk(up, down);
+  // Aborted: lets a producer's copies in flight land.  The other producer's may never be asked for, which leaves a stage
+  // short of its arrival; what was in flight has landed by the time such a wait gives up, whichever the stage.
+  auto let_land = [&](int stage, uint32_t phase) {
+#pragma unroll 1
+    for (int s = 0; s < n_stages; ++s)
+      if (!wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1)) break;
+  };
   if (warp == 0) {
     // -------------------------------------------------------------- weights
     {
@@ -568,9 +575,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           phase ^= 1;
         }
       }
-      if (!ok)  // aborted: let what is in flight land
-#pragma unroll 1
-        for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+      if (!ok) let_land(stage, phase);
     }
     __syncwarp();
   } else if (warp == 6) {
@@ -613,6 +618,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
           }
         }
       }
+      if (!ok) let_land(stage, phase);  // (else the weights' producer sees every stage released)
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
     const int64_t slot_floats = (int64_t)T * 128;
     int acc_i = 0;
     int cut0 = 0, cut1 = 0, n_cut = 0;  // column tiles of the down run that this CTA has a piece of
-    bool ok = true;
+    bool ok = true, left = false;       // left: gave up, all four warps together
     // A cut unit of the up run is finished by the CTA of its second piece, whose range begins inside the unit: a CTA
     // owes at most one, after its own pieces (its others are waited for by others).  That code runs once before, on no
     // pieces at all (it leaves zeros, which the real pass overwrites): its instructions come from memory the first
@@ -717,7 +723,8 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
       }
       if (!owed) ok = warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl);
       else if (!rehearse && ep == 0) ok = wait_count(p.up_cnt + unit, pieces.n, ctl);
-      if (!ptx::bar_all(1, 128, ok)) break;  // the four warps leave together: they share named barriers
+      left = !ptx::bar_all(1, 128, ok);  // the four warps leave together: they share named barriers
+      if (left) break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * acc;
       if (!whole && !owed) {
@@ -897,7 +904,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
     // the cut column tiles (at most two): this CTA's share of each, once all its pieces are there
     const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.residual)) & 7) == 0 &&
                      ((p.ld_out | p.ld_residual) & 3) == 0;
-    if (ok && !*abort_flag && n_cut > 0) {
+    if (!left && n_cut > 0) {
       const Pieces pa(down, cut0), pb(down, n_cut > 1 ? cut1 : cut0);
       if (ep == 0) ok = wait_count(p.down_cnt + cut0, pa.n, ctl);
       if (ep == 32 && n_cut > 1) ok = wait_count(p.down_cnt + cut1, pb.n, ctl);

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
       ptx::mbar_init(ptx::smem_u32(&acce[b]), 16);
     }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
@@ -383,8 +383,12 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
         phase ^= 1;
       }
     }
-    if (!ok && rank == 0)  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
-      for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    if (!ok && rank == 0) {  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
+      for (int s = 0; s < n_stages; ++s)
+        if (!wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1)) break;  // rank 1 gave up before its load
+    } else if (!ok) {
+      let_loads_land();  // of a stage that rank 0 may not wait for: it may have given up before its own load
+    }
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(accf), 1);
+    ptx::mbar_init(ptx::smem_u32(accf), 1 + p.test_stall);
     ptx::mbar_init(ptx::smem_u32(acce), 8);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     ptx::mbar_init(ptx::smem_u32(pready), S);

@@ -38,6 +38,7 @@ struct GateParams {
   GateRule rule;
   uint32_t* hdr;       // error words (pair form)
   int64_t timeout_ns;
+  int32_t test_stall;  // testing aid (pair form): 1: the accumulators' barriers wait for an arrival that never comes
   // plan_gate's choice
   int32_t pair, bn, KB, n_stages, grid;
 };
@@ -69,6 +70,7 @@ struct LayerParams {
   // counters, zeroed by the front kernel
   uint32_t *counters, *up_done, *up_cnt, *down_cnt;
   int64_t ld_residual, ld_out, timeout_ns;
+  int32_t test_stall;  // as GateParams'
   int32_t n_counters, npad;
   int32_t NT1, KB1, NT2, KB2;  // tiles of a routed expert
   int32_t NT1s, KB2s;          // of the shared expert (0 without one)
@@ -88,6 +90,7 @@ struct LinearParams {
   uint32_t* hdr;  // error words
   int64_t M, N, K, ldx, ldw, ldr, ldo;
   int64_t timeout_ns;
+  int32_t test_stall;  // as GateParams' (stream and pair form)
   int32_t act, out_f32;
   int32_t vec_out;  // rows of out and residual on 16-byte boundaries
   // plan_linear's choice

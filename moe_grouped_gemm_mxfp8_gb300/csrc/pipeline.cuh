@@ -101,6 +101,13 @@ __device__ __forceinline__ bool wait_bar_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// After an abort, where no barrier of this CTA tells when its loads have landed: a thousand times what one takes.
+__device__ __forceinline__ void let_loads_land() {
+  const uint64_t t0 = ptx::globaltimer();
+  while (ptx::globaltimer() - t0 < 2000000ull) {
+  }
+}
+
 // Block-wide inclusive scan (sum or max) over kThreads threads; `total`
 // gets the last value.  Every thread must call it.
 template <bool kMax, int kThreads>
