@@ -422,34 +422,39 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   lp.out_f32 = p.out_type == GMMFR_DT_F32;
   lp.vec_out = aligned(out, 16) && lp.ldo % (lp.out_f32 ? 4 : 8) == 0 && aligned(residual, 16) && lp.ldr % 8 == 0;
   const int64_t Kp = cdiv(p.K, 8) * 8;
+  __nv_bfloat16 *x_copy = nullptr, *w_copy = nullptr;
   if (repitch_x(problem)) {
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
-    cudaError_t e = gmmfr::launch_linear_repitch(lp.x, dst, p.M, p.K, Kp, lp.ldx, sms, s);
-    if (e != cudaSuccess) return cuda_fail(e, "x copy launch");
-    lp.x = dst;
+    lp.x = x_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
     lp.ldx = Kp;
   }
   if (repitch_w(problem)) {
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(ws + L.w);
-    cudaError_t e = gmmfr::launch_linear_repitch(lp.w, dst, rows_w, p.K, Kp, lp.ldw, sms, s);
-    if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
-    lp.w = dst;
+    lp.w = w_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.w);
     lp.ldw = Kp;
   }
   gmmfr::LinearParams parts[2] = {lp, lp};
+  gmmfr::LinearMaps maps[2];
   gmmfr::plan_linear(parts[0], parts[1], sms);
-  for (const gmmfr::LinearParams& q : parts) {
-    if (q.M == 0) continue;
-    gmmfr::LinearMaps maps;
-    if (q.form != gmmfr::kLinearDirect) {
-      PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
-      if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-      const bool stream_form = q.form == gmmfr::kLinearStream;
-      if (!encode_rows(encode, &maps.x, q.x, q.M, q.K, q.ldx, stream_form ? q.bn : 128) ||
-          !encode_rows(encode, &maps.w, q.w, rows_w, q.K, q.ldw, stream_form ? (gated ? 64 : 128) : q.bn / 2))
-        return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    }
-    cudaError_t e = gmmfr::launch_linear(maps, q, s);
+  for (int i = 0; i < 2; ++i) {  // what can be refused, before anything is launched
+    const gmmfr::LinearParams& q = parts[i];
+    if (q.M == 0 || q.form == gmmfr::kLinearDirect) continue;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const bool stream_form = q.form == gmmfr::kLinearStream;
+    if (!encode_rows(encode, &maps[i].x, q.x, q.M, q.K, q.ldx, stream_form ? q.bn : 128) ||
+        !encode_rows(encode, &maps[i].w, q.w, rows_w, q.K, q.ldw, stream_form ? (gated ? 64 : 128) : q.bn / 2))
+      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld ldw=%lld)", (long long)q.ldx, (long long)q.ldw);
+  }
+  if (x_copy) {
+    cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(x), x_copy, p.M, p.K, Kp, stride_or(p.ldx, p.K), sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "x copy launch");
+  }
+  if (w_copy) {
+    cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(weight), w_copy, rows_w, p.K, Kp, stride_or(p.ldw, p.K), sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (parts[i].M == 0) continue;
+    cudaError_t e = gmmfr::launch_linear(maps[i], parts[i], s);
     if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   }
   return GMMFR_OK;

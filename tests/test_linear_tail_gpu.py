@@ -60,3 +60,27 @@ def test_one_weight_row(M):
     g = torch.Generator().manual_seed(M)
     for K in (3, 515, 4097):
         _check(_rows(g, M, K, K), _rows(g, 1, K, K, scale=K ** -0.5), "gelu")
+
+
+def _entry(x, w, workspace, unaligned=0, **kw):
+    """The C entry itself, on a workspace of the caller's."""
+    M, K = x.shape
+    N = w.shape[0]
+    p = B.LinearProblem(**{**dict(M=M, N=N, K=K, ldx=x.stride(0), ldw=w.stride(0), ld_residual=0, ld_out=0, activation=0,
+                                  out_type=B.DT_F32, unaligned=unaligned), **kw})
+    need = B.gmmfr_linear_workspace_size(p)
+    assert workspace.numel() >= need
+    out = torch.empty((M, N), device="cuda")
+    B.gmmfr_linear(p, x.data_ptr(), w.data_ptr(), None, None, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                   torch.cuda.current_stream().cuda_stream)
+    return out
+
+
+def test_a_refused_call_enqueues_nothing():
+    g = torch.Generator().manual_seed(1)
+    x, w = _rows(g, 300, 129, 131), _rows(g, 64, 129, 136)
+    ws = torch.full((1 << 20,), 0xA5, dtype=torch.uint8, device="cuda")
+    with pytest.raises(B.GmmfrError):
+        _entry(x, w, ws, ldw=1 << 40)  # a row stride that no tensor copy takes; x is copied to the workspace first
+    torch.cuda.synchronize()
+    assert (ws == 0xA5).all()
