@@ -204,10 +204,11 @@ gmmfr_status validate_linear(const gmmfr_linear_problem* p) {
   return GMMFR_OK;
 }
 
-// Rows that TMA cannot read in place are copied to a pitch of K rounded up to 8.
-bool repitch_x(const gmmfr_linear_problem* p) { return p->unaligned || (p->M > 1 && stride_or(p->ldx, p->K) % 8); }
-bool repitch_w(const gmmfr_linear_problem* p) {
-  return p->unaligned || (p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1) > 1 && stride_or(p->ldw, p->K) % 8);
+// Rows that TMA cannot read in place are copied to a pitch of K rounded up to 8: by their stride, or by where they start
+// (which the size of the workspace does not depend on).
+bool odd_stride_x(const gmmfr_linear_problem* p) { return p->M > 1 && stride_or(p->ldx, p->K) % 8; }
+bool odd_stride_w(const gmmfr_linear_problem* p) {
+  return p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1) > 1 && stride_or(p->ldw, p->K) % 8;
 }
 
 struct LinearLayout {
@@ -218,9 +219,9 @@ LinearLayout linear_layout(const gmmfr_linear_problem* p) {
   const size_t Kp = (size_t)cdiv(p->K, 8) * 8;
   size_t off = gmmfr::kHdrBytes;
   L.x = off;
-  if (repitch_x(p)) off = align256(off + 2 * Kp * p->M);
+  if (p->unaligned || odd_stride_x(p)) off = align256(off + 2 * Kp * p->M);
   L.w = off;
-  if (repitch_w(p)) off = align256(off + 2 * Kp * p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1));
+  if (p->unaligned || odd_stride_w(p)) off = align256(off + 2 * Kp * p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1));
   L.total = off;
   return L;
 }
@@ -396,7 +397,8 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   const bool gated = p.activation == GMMFR_ACT_SWIGLU;
   const int64_t rows_w = gated ? 2 * p.N : p.N;
   const LinearLayout L = linear_layout(problem);
-  if ((!aligned(x, 16) && !repitch_x(problem)) || (!aligned(weight, 16) && !repitch_w(problem)))
+  const bool copy_x = !aligned(x, 16) || odd_stride_x(problem), copy_w = !aligned(weight, 16) || odd_stride_w(problem);
+  if (!p.unaligned && ((copy_x && !odd_stride_x(problem)) || (copy_w && !odd_stride_w(problem))))
     return fail(GMMFR_ERR_INVALID_ARG, "x or weight is off a 16-byte boundary: set problem.unaligned (and size the workspace with it)");
   if (gmmfr_status st = check_workspace(workspace, workspace_bytes, L.total)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -423,11 +425,11 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
   lp.vec_out = aligned(out, 16) && lp.ldo % (lp.out_f32 ? 4 : 8) == 0 && aligned(residual, 16) && lp.ldr % 8 == 0;
   const int64_t Kp = cdiv(p.K, 8) * 8;
   __nv_bfloat16 *x_copy = nullptr, *w_copy = nullptr;
-  if (repitch_x(problem)) {
+  if (copy_x) {
     lp.x = x_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
     lp.ldx = Kp;
   }
-  if (repitch_w(problem)) {
+  if (copy_w) {
     lp.w = w_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.w);
     lp.ldw = Kp;
   }

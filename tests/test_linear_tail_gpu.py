@@ -84,3 +84,20 @@ def test_a_refused_call_enqueues_nothing():
         _entry(x, w, ws, ldw=1 << 40)  # a row stride that no tensor copy takes; x is copied to the workspace first
     torch.cuda.synchronize()
     assert (ws == 0xA5).all()
+
+
+@pytest.mark.parametrize("M", [1, 20, 60, 300])
+def test_only_what_is_off_a_boundary_is_copied(M):
+    g = torch.Generator().manual_seed(M)
+    K, N = 264, 48
+    x, w = (torch.randn((r, K + 8), generator=g).to(torch.bfloat16).cuda() for r in (M, N))
+    copies = {"x": M * K * 2, "w": N * K * 2}
+    for off_x, off_w in ((0, 0), (1, 0), (0, 3), (5, 1)):
+        xs, wsl = x[:, off_x:off_x + K], w[:, off_w:off_w + K]
+        ws = torch.full((1 << 20,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = _entry(xs, wsl, ws, unaligned=1)
+        ref, absb = O.linear(_f64(xs), _f64(wsl))
+        assert np.all(np.abs(_f64(out) - ref) <= 2.0 ** -20 * np.abs(ref) + K / 8 * 2.0 ** -23 * absb + 1e-30)
+        written = ws[4096:].ne(0xA5).sum().item()  # behind the error words
+        want = (copies["x"] if off_x else 0) + (copies["w"] if off_w else 0)
+        assert 0.98 * want <= written <= want, (off_x, off_w, written, want)
