@@ -517,12 +517,14 @@ def ffn(sorted_tokens, prepared, expert_cumsum, H: int, I: int, E: int, result=N
 
 def ffn_prepare_mx(H: int, I: int, E: int, w13, w13_scale, w2, w2_scale, stream=None):
     """Prepared-weight buffer (torch uint8) of MXFP8 FFN weights: w13 [E, H, 2I], w2 [E, I, H] E4M3
-    (or their bytes) with E8M0 scales [E, ceil(K/64), columns, 2]."""
+    (or their bytes) with E8M0 scales (or their bytes) [E, ceil(K/64), columns, 2]."""
     import torch
-    for name, t, shape in (("w13", w13, (E, H, 2 * I)), ("w13_scale", w13_scale, (E, -(-H // 64), 2 * I, 2)),
-                           ("w2", w2, (E, I, H)), ("w2_scale", w2_scale, (E, -(-I // 64), H, 2))):
-        if t.numel() != _numel(shape) or t.element_size() != 1:
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} in single bytes")
+    codes, exponents = ((torch.uint8, torch.int8, t) for t in (torch.float8_e4m3fn, getattr(torch, "float8_e8m0fnu", torch.uint8)))
+    for name, t, shape, types in (("w13", w13, (E, H, 2 * I), codes), ("w13_scale", w13_scale, (E, -(-H // 64), 2 * I, 2), exponents),
+                                  ("w2", w2, (E, I, H), codes), ("w2_scale", w2_scale, (E, -(-I // 64), H, 2), exponents)):
+        if t is None or t.numel() != _numel(shape) or t.dtype not in types:
+            got = None if t is None else f"{tuple(t.shape)} {t.dtype}"
+            raise ValueError(f"{name}: {got}, expected {shape} of {' or '.join(str(d) for d in dict.fromkeys(types))}")
     fp = FfnProblem(N=0, H=H, I=I, E=E)
     n = gmmfr_ffn_prepared_weights_size_mx(fp)
     with _in_pool_of(stream):
@@ -735,11 +737,13 @@ class MoeLayer(_Handle):
         super().__init__(gate_weight.device)
         gp = _gate_problem(self._index, gate_weight, topk, scoring, select_bias, n_group, topk_group, group_top, renormalise, scale)
         E, H, I = gp.E, gp.H, w2.shape[1]
-        mx = w13_scale is not None
+        mx = w13_scale is not None or w2_scale is not None
         for name, t in (("w13", w13), ("w2", w2), ("w13_scale", w13_scale), ("w2_scale", w2_scale), ("shared_w13", shared_w13),
                         ("shared_w2", shared_w2), ("shared_w13_scale", shared_w13_scale), ("shared_w2_scale", shared_w2_scale)):
             if t is not None and t.get_device() != self._index:
                 _refuse(name, t, "", self._index)
+        if (shared_w13 is None) != (shared_w2 is None):
+            raise ValueError("shared_w13 and shared_w2 come together")
         shared_I, self._shared = 0, None
         with torch.cuda.device(self._index):
             self._prepared = self._prepare(E, H, I, w13, w13_scale, w2, w2_scale, mx)
@@ -774,8 +778,9 @@ class MoeLayer(_Handle):
         if mx:
             return ffn_prepare_mx(H, I, E, w13, s13, w2, s2)
         for name, t, shape in (("w13", w13, (E, H, 2 * I)), ("w2", w2, (E, I, H))):
-            if t.dtype != torch.bfloat16 or t.numel() != _numel(shape):
-                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} bfloat16")
+            if t is None or t.dtype != torch.bfloat16 or t.numel() != _numel(shape):
+                got = None if t is None else f"{tuple(t.shape)} {t.dtype}"
+                raise ValueError(f"{name}: {got}, expected {shape} bfloat16 (or E4M3 with its scales)")
         return ffn_prepare(H, I, E, w13, w2)
 
     def __call__(self, x, residual=None, out=None, topk_ids=None, topk_weights=None, stream=None):

@@ -229,3 +229,41 @@ def test_a_call_runs_on_the_device_of_its_handle(fakes, monkeypatch):
         handle._fn = lambda *a: seen.append(current[0]) or 0
         handle(x)
     assert seen == [0, 0, 0] and current == [1]
+
+
+# ------------------------------------------------------------------------- weights of the wrong kind
+def _mx_weights(**kw):
+    E, H, I = 4, 128, 64
+    u8 = dict(dtype=torch.uint8)
+    w = dict(w13=FakeTensor(E, H, 2 * I, dtype=torch.float8_e4m3fn), w13_scale=FakeTensor(E, H // 64, 2 * I, 2, **u8),
+             w2=FakeTensor(E, I, H, **u8), w2_scale=FakeTensor(E, I // 64, H, 2, **u8))
+    w.update(kw)
+    return (H, I, E), w
+
+
+@pytest.mark.parametrize("bad", [
+    dict(w13=FakeTensor(4, 128, 128, dtype=torch.float8_e5m2)), dict(w2=FakeTensor(4, 64, 128, dtype=torch.bool)),
+    dict(w2=FakeTensor(4, 64, 128, dtype=torch.float8_e5m2)), dict(w2_scale=FakeTensor(4, 1, 128, 2, dtype=torch.float8_e4m3fn)),
+    dict(w13_scale=FakeTensor(4, 2, 128, 2, dtype=torch.float8_e5m2)), dict(w13_scale=FakeTensor(4, 2, 64, 2, dtype=torch.uint8)),
+    dict(w2_scale=None), dict(w13=FakeTensor(4, 128, 128))], ids=lambda b: next(iter(b)))
+def test_mx_weights_of_another_type_are_refused(bad):
+    (H, I, E), w = _mx_weights(**bad)
+    with pytest.raises(ValueError, match=next(iter(bad))):
+        B.ffn_prepare_mx(H, I, E, w["w13"], w["w13_scale"], w["w2"], w["w2_scale"])
+
+
+def test_layers_with_half_of_their_weights_are_refused(monkeypatch):
+    def init(self, device):
+        self._device, self._index = torch.device("cuda", 0), 0
+
+    monkeypatch.setattr(B._Handle, "__init__", init)
+    monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
+    _, w = _mx_weights()
+    gate = FakeTensor(4, 128)
+    bf16 = dict(w13=FakeTensor(4, 128, 128), w2=FakeTensor(4, 64, 128))
+    monkeypatch.setattr(B, "ffn_prepare", lambda *a: FakeTensor(1, 1 << 20, dtype=torch.uint8))
+    for kw in ({**w, "w2_scale": None}, {**w, "w13_scale": None}, {**bf16, "w2_scale": w["w2_scale"]},
+               {**bf16, "shared_w13": FakeTensor(128, 128)}, {**bf16, "shared_w2": FakeTensor(64, 128)},
+               {**bf16, "w13": w["w13"]}):
+        with pytest.raises(ValueError):
+            B.MoeLayer(gate, topk=2, **kw)
