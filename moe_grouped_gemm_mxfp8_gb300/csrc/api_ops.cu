@@ -166,7 +166,7 @@ LayerLayout layer_layout(const gmmfr_layer_problem* p) {
   L.NT1s = cdiv(p->shared_I, 64);
   L.KB2s = cdiv(p->shared_I, kt);
   const int64_t experts = std::min<int64_t>(p->gate.E, T * k);  // at most so many are chosen
-  L.n_counters = 1 + L.NT1s + experts * L.NT1 + L.NT2;
+  L.n_counters = 1 + L.NT1s + experts * L.NT1 + L.NT2 + T;
   const size_t img = (size_t)gmmfr::layer_image_bytes(mx, L.npad);
   size_t off = gmmfr::kHdrBytes;
   auto take = [&](size_t bytes) {
@@ -362,7 +362,8 @@ gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, 
   lp.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
   lp.up_done = lp.counters;
   lp.down_cnt = lp.counters + 1;
-  lp.up_cnt = lp.down_cnt + L.NT2;
+  lp.nan_rows = lp.down_cnt + L.NT2;
+  lp.up_cnt = lp.nan_rows + p.gate.T;
   lp.n_counters = (int32_t)L.n_counters;
   lp.npad = (int32_t)L.npad;
   lp.NT1 = (int32_t)L.NT1;

@@ -304,14 +304,15 @@ __device__ float row_product(const uint8_t* tiles, int r, const uint8_t* images,
 }
 
 // Columns n .. n + 3 of token t's result, without the residual, of which s holds the accumulated sums: those that are NaN
-// made again from the experts that t chose and the shared one alone.  They stay NaN when one of those made them; else it was
-// an infinite or NaN weight of an expert that only other tokens chose.  A rare call, kept out of line and small rather than
-// fast (one token, MXFP8: 26.7 us without it).
+// made again from the experts that t chose and the shared one alone.  A token with a NaN among its own SwiGLU values keeps
+// them; another's stay NaN when a down weight of its own experts made them, and else it was an infinite or NaN weight of an
+// expert that only other tokens chose.  A rare call, kept out of line and small rather than fast: all of 64 x 7168 results
+// of 16 experts of 2048 take 20 ms (BF16) or 53 (MXFP8).
 template <bool kMx>
 __device__ __noinline__ float4 own_sums(const LayerParams& p, const uint16_t* s_act, const uint16_t* s_ids, int A, int n_units, int t,
                                         int64_t n0, float4 s) {
   // every unit's sw is there (the sums were made of them), and with this read they are visible to this thread too
-  if (ld_acquire(p.up_done) < (uint32_t)n_units) return s;
+  if (ld_acquire(p.up_done) < (uint32_t)n_units || __ldcg(p.nan_rows + t) != 0) return s;
   const int topk = p.gate.rule.topk, tile = layer::tile_bytes(kMx);
   const int64_t img = layer::image_bytes(kMx, p.npad);
   float f[4] = {s.x, s.y, s.z, s.w};
@@ -807,6 +808,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
         // the others
         auto store_sw = [&](int t, int col, float sw) {  // col: intermediate index within the unit, a lane each
           if constexpr (!kMx) {
+            if (sw != sw && !rehearse) p.nan_rows[t] = 1;
             *reinterpret_cast<__nv_bfloat16*>(dst + image_chunk(t, col >> 3) + (col & 7) * 2) = __float2bfloat16_rn(sw);
           } else {
             const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(sw) & 0x7fffffffu));
@@ -819,6 +821,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
             if (lane == 0) {
               dst[scale_at(t, c >> 5)] = (uint8_t)b.byte_hi;
               dst[scale_at(npad + t, c >> 5)] = (uint8_t)b.byte_lo;
+              if (b.byte_hi == 255u) p.nan_rows[t] = 1;
             }
           }
         };

@@ -69,6 +69,7 @@ struct LayerParams {
   float *slots_up, *slots_down;         // pieces of cut tiles: [CTA][2][T][128] each
   // counters, zeroed by the front kernel
   uint32_t *counters, *up_done, *up_cnt, *down_cnt;
+  uint32_t* nan_rows;  // [T], among the counters: 1 where a token's SwiGLU values have a NaN
   int64_t ld_residual, ld_out, timeout_ns;
   int32_t test_stall;  // as GateParams'
   int32_t n_counters, npad;

@@ -99,3 +99,34 @@ def test_weights_that_a_token_did_not_choose(c, where, mx):
         assert np.array_equal(got[~fine & ~np.isnan(ref)], ref[~fine & ~np.isnan(ref)])
         assert np.all((np.abs(got - ref) <= 2.0 ** -8 * (np.abs(ref) + absb) + 1e-30)[fine])
     assert torch.equal(out.view(torch.int16), layer(x.cuda(), residual=residual.cuda()).view(torch.int16))
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,H,E,I,topk", [(3, 1024, 4, 64, 1), (40, 520, 16, 136, 4)])
+def test_tokens_and_weights_at_once(T, H, E, I, topk, value, mx):
+    """A token that is not finite itself, beside an expert of NaN weights that some of the others chose."""
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16)
+    wg = (torch.randn((E, H), generator=g) * H ** -0.5).to(torch.bfloat16)
+    x[1] = value
+    w13, w2 = torch.randn((E, H, 2 * I), generator=g), torch.randn((E, I, H), generator=g)
+    scales = {}
+    if mx:
+        w13, w2 = (w.to(torch.float8_e4m3fn) for w in (w13, w2))
+        scales = {n + "_scale": torch.full((E, -(-k // 64), c, 2), 122, dtype=torch.uint8).cuda() for n, k, c in (("w13", H, 2 * I), ("w2", I, H))}
+    else:
+        w13, w2 = (w * H ** -0.5 for w in (w13, w2))
+    bad = int(B.MoeGate(wg.cuda(), topk=topk)(x.cuda())[0][0, 0])
+    clean = [w.to(w.dtype if mx else torch.bfloat16).cuda() for w in (w13, w2)]
+    spoilt = clean[1].clone()
+    spoilt.view(torch.uint8 if mx else torch.int16)[bad] = 0x7F if mx else 0x7FC0
+    chosen = torch.empty((T, topk), dtype=torch.int32, device="cuda")
+    ref = B.MoeLayer(wg.cuda(), *clean, **scales, topk=topk)(x.cuda())
+    out = B.MoeLayer(wg.cuda(), clean[0], spoilt, **scales, topk=topk)(x.cuda(), topk_ids=chosen, topk_weights=torch.empty((T, topk), device="cuda"))
+    got, want, has = _f64(out), _f64(ref), (chosen == bad).any(1).cpu().numpy()
+    assert np.isnan(got[1]).all() and np.isnan(got[has]).all() and not has.all()
+    for t in range(T):
+        if t != 1 and not has[t]:
+            # the same terms, added in another order
+            assert np.all(np.abs(got[t] - want[t]) <= 2.0 ** -7 * np.abs(want[t]) + 2.0 ** -8 * np.abs(want[t]).max())
