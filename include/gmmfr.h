@@ -244,7 +244,8 @@ GMMFR_API gmmfr_status gmmfr_grouped_matmul_finalize_routing(
 
 /*
  * SYNCHRONISES `stream`, then reads the device error word that the last call
- * using `workspace` left there (GMMFR_DEV_* bits, 0 when clean) into *bits.
+ * using `workspace` left there (GMMFR_DEV_* bits, 0 when clean) into *bits.  A call
+ * with nothing to compute launches nothing and leaves none.
  * Returns GMMFR_ERR_DEVICE when any bit is set, GMMFR_OK otherwise.
  */
 GMMFR_API gmmfr_status gmmfr_check_device_errors(const void* workspace, void* stream, uint32_t* bits);
@@ -381,6 +382,7 @@ GMMFR_API gmmfr_status gmmfr_llada2_moe_grouped_gemm(const gmmfr_ffn_problem* pr
  *   topk_weights[t,k] = scale * p[t,ids[k]] (/ (sum_k p[t,ids[k]] + 1e-20) when renormalise)
  * Equal scores go to the lowest index, of groups too; NaN scores rank below every number (then by
  * index); a token whose logits are all -inf has p = 0.  A NaN logit makes its token's softmax NaN.
+ * Everything is FP32; a weight is within 2^-18 of the formula's value on the logits.
  *   T       tokens, 0 <= T < 2^31;  H  row length, a multiple of 8;  E  experts (1..1024)
  *   topk    1 .. 32, at most the eligible experts (topk_group * E / n_group)
  *   n_group 1 .. 64, divides E (1: no groups);  topk_group  1 .. n_group;  group_top  1 or 2, at most
@@ -424,10 +426,13 @@ GMMFR_API gmmfr_status gmmfr_ffn_prepare_weights_mx(const gmmfr_ffn_problem* pro
 
 /*
  * A whole mixture-of-experts layer for a few tokens (decoding), gate included:
- *   ids, w  = the gate above on x (gate.ids_type is not read)
+ *   ids, w  = the gate above on x (ids are int32 here, whichever of its values gate.ids_type has)
  *   out[t]  = residual[t] + sum_k w[t,k] * FFN_ids[t,k](x[t]) + FFN_shared(x[t])
  *   FFN_e(x) = (SiLU(x Wg_e) * (x Wu_e)) W2_e,   SiLU(g) = g / (1 + exp(-g)),   FP32 sums
- * Every chosen expert's weights are read once per call, whatever the number of its tokens.
+ * Every chosen expert's weights are read once per call, whatever the number of its tokens.  The SwiGLU value,
+ * times the router's weight, is rounded once before the down product, as the grouped FFN's is: to BF16, or with E4M3
+ * weights to the sum of two E4M3 numbers with block scales (about as fine); the sum of all experts, the shared one
+ * and the residual once to BF16.
  *   gate          the gate's sizes and rule; 0 <= T <= 64
  *   I             the routed experts' intermediate size, a multiple of 8
  *   shared_I      the shared expert's, a multiple of 8; 0: no shared expert
@@ -451,7 +456,8 @@ GMMFR_API gmmfr_status gmmfr_moe_layer_workspace_size(const gmmfr_layer_problem*
  * topk_ids [T, topk] int32 and topk_weights [T, topk] float32: the gate's choice, written when given.
  * Two launches, the second cooperative (its CTAs, one per SM, wait for one another, so all must be resident: it
  * starts when the device has room for all of them).  A token with an infinity or NaN spoils its own row only; with E4M3
- * weights the blocks of 32 that hold it count as NaN.  Never syncs, never allocates; deterministic; a wait that gave up
+ * weights the blocks of 32 that hold it count as NaN.  Infinite and NaN weights of an expert reach the tokens that chose
+ * it and no others.  Never syncs, never allocates; deterministic; a wait that gave up
  * sets GMMFR_DEV_TIMEOUT in the workspace's device error word (gmmfr_check_device_errors). */
 GMMFR_API gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const void* x, const void* gate_weight,
                                        const float* select_bias, const void* residual, void* out,
@@ -466,10 +472,12 @@ GMMFR_API gmmfr_status gmmfr_moe_layer(const gmmfr_layer_problem* problem, const
  * the N gate rows followed by the N up rows, and act is SiLU(gate) * up.
  *   M, N, K   x [M, K], weight [N or 2N, K], y [M, N]; M, N >= 0, K >= 1, each < 2^31
  *   ldx, ldw, ld_residual, ld_out   elements from one row to the next; 0 stands for the row's length
- *   out_type  GMMFR_DT_BF16 or GMMFR_DT_F32
+ *   out_type  GMMFR_DT_BF16 or GMMFR_DT_F32 (FP32 results carry the tensor cores' sums, which truncate: relative
+ *             error 1.4e-6 at K = 2328, where FP32 additions leave 2.4e-7)
  *   unaligned 1: x or weight may start off a 16-byte boundary.  Rows that do, or whose stride is not a
  *             multiple of 8, are copied into the workspace first (the tensor copies that feed the products need
- *             16-byte rows), which then has room for both matrices; 0 otherwise
+ *             16-byte rows), which then has room for both matrices; 0 otherwise.  What lies behind a row, or between
+ *             two, is neither read nor counted
  */
 typedef enum {
   GMMFR_ACT_NONE = 0,

@@ -726,8 +726,9 @@ class MoeLayer(_Handle):
 
     ``gate_weight`` [E, H]; ``w13`` [E, H, 2I] and ``w2`` [E, I, H] bfloat16, or E4M3 with
     ``w13_scale`` / ``w2_scale`` (E8M0, [E, ceil(K/64), columns, 2]); the shared expert's weights as
-    [H, 2 shared_I] and [shared_I, H] of the same kind.  The weights are laid out once, here; the
-    keyword arguments after them are the gate's."""
+    [H, 2 shared_I] and [shared_I, H] of the same kind.  The weights are laid out once, here, on the current
+    stream (calls on another are ordered after it by the caller, as after any kernel); the keyword arguments after
+    them are the gate's."""
 
     def __init__(self, gate_weight, w13, w2, w13_scale=None, w2_scale=None, shared_w13=None, shared_w2=None,
                  shared_w13_scale=None, shared_w2_scale=None, *, topk: int, scoring: str = "softmax",

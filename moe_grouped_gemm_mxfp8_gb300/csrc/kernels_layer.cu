@@ -30,7 +30,8 @@
 //
 // sw is rounded to what the tensor cores take: BF16, or with MXFP8 weights a sum of two E4M3 numbers with
 // their block scales (hi + lo, about as exact as BF16), and the tokens likewise: BF16's eight bits split exactly
-// into hi and lo, so that MXFP8 weights meet unrounded activations.
+// into hi and lo, so that MXFP8 weights meet unrounded activations (down to 2^-14 of the block's largest; what is
+// smaller is off by at most 2^-22 of it).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(layer::kThreads, 2) layer_kernel(const __grid_
               if (tok[i] >= 0) store_sw(tok[i], col, silu(gate_v[i]) * up_v[i] * s_tokw[tok[i]]);
           }
         } else {
-          // from TMEM, kRound tokens at a time: warps 2, 3 (gate rows) take the even ones, warps 4, 5 (up rows) the odd,
+          // from TMEM, kRound tokens at a time: warps 4, 5 (gate rows) take the even ones, warps 2, 3 (up rows) the odd,
           // each handing the other what it needs
           constexpr int kRound = layer::kRound;
           const int half = q >= 2, col = (q & 1) * 32 + lane;
