@@ -410,6 +410,8 @@ def _in_pool_of(stream):
     """Allocations within come from the memory pool of the stream that is going to use them (None: the current one).  A
     block of another stream's pool may be one that this stream's kernels still use."""
     import torch
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
     return torch.cuda.stream(stream)
 
 
@@ -505,11 +507,13 @@ def ffn(sorted_tokens, prepared, expert_cumsum, H: int, I: int, E: int, result=N
     N = sorted_tokens.shape[0]
     fp = FfnProblem(N=N, H=H, I=I, E=E)
     with _in_pool_of(stream):
-        if result is None:
+        new = result is None
+        if new:
             result = torch.zeros((N, H), dtype=torch.bfloat16, device=sorted_tokens.device)
         if ws is None:
             ws = torch.empty(gmmfr_ffn_workspace_size(fp), dtype=torch.uint8, device=sorted_tokens.device)
-    _handed_over(stream, result)
+    if new:
+        _handed_over(stream, result)
     gmmfr_llada2_moe_grouped_gemm(fp, _ptr(sorted_tokens), _ptr(prepared), _ptr(expert_cumsum), _ptr(result),
                                   _ptr(ws), ws.numel(), _stream(stream))
     return result, ws

@@ -140,3 +140,34 @@ def test_a_handle_dropped_while_another_stream_uses_its_weights():
     taken = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert torch.equal(out, want) and all((t == 255).all() for t in taken)
+
+
+def test_first_calls_inside_a_capture_and_streams_by_address():
+    """A handle whose first call on a stream is a captured one, dropped before the next capture; and any object that has a
+    stream's address as a stream."""
+    x = _randn(11, 20, 256)
+    layer, gate, lin = _layer(), B.MoeGate(_randn(1, 16, 256, scale=0.1), topk=4), B.Linear(_randn(5, 48, 256))
+    want = layer(x), gate(x)[1], lin(x)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        fresh = _layer(), B.MoeGate(_randn(1, 16, 256, scale=0.1), topk=4), B.Linear(_randn(5, 48, 256))
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            out = fresh[0](x), fresh[1](x)[1], fresh[2](x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        del fresh, graph, out
+
+    class Address:
+        cuda_stream = stream.cuda_stream
+
+    ids = torch.zeros((20, 1), dtype=torch.int32, device="cuda")
+    codes = x.view(torch.uint8)
+    scale = torch.full((20, 8, 2), 127, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    got, _ = B.route(ids, torch.ones((20, 1), device="cuda"), codes, scale, 4, stream=Address)
+    torch.cuda.synchronize()
+    assert torch.equal(got["x1"], codes)
