@@ -32,6 +32,13 @@ constexpr int kThreads = 320;      // stream: warp 0 TMA, warp 1 MMA, warps 2..9
 constexpr int kPairThreads = 320;  // pair: warps 2..9 epilogue
 constexpr int kBK = 64;        // K per stage: 128-byte rows
 constexpr int kTileBytes = 128 * 128;
+// FP32 results: K blocks of 64 that are added up in one accumulator; sums of so many are added in registers, to nearest.  The
+// tensor core's additions truncate, which takes 9.4e-7 off a sum of 1024 products, in proportion to their number, and twice
+// that off a gated value (K = 7168 in one accumulator: 7.9e-6 and 1.6e-5).  To go on in the other accumulator costs the
+// tensor pipe about 0.5 us: 8192 rows of 7168 x 4096 262 us in one, 287 with 16 blocks, 309 with 8, 393 with 4; gated, 2000 rows
+// of 4096 x 7168 138, 143, 149, 198.
+template <bool kGated>
+constexpr int kChunk = kGated ? 8 : 16;
 
 // ---- pair form
 constexpr int kPairArena = 6 * 32768;
@@ -43,7 +50,7 @@ static_assert(kPairSmem <= 232448 && 32 * 33 * 4 % 16 == 0, "shared memory budge
 
 // ---- stream form
 constexpr int kStreamMaxStages = 6;
-constexpr int kStreamBars = 2 * kStreamMaxStages + 6;
+constexpr int kStreamBars = 2 * kStreamMaxStages + 8;
 constexpr int kStreamKps = 2;  // K blocks per stage: 0.33 us per stage where a CTA has the memory to itself, 0.25 with one
 constexpr int kStreamArena = 220 * 1024;  // the ring, and the partial sums unless they take its place
 constexpr int kStreamSmem = kStreamArena + kStreamBars * 8 + 32 + 1024;
@@ -67,6 +74,7 @@ __device__ __forceinline__ void store_out(const LinearParams& p, int64_t m, int6
 }
 
 // A warp's 32 rows m0.. by 32 columns n.., activated values in v (bias included), lane l holding row m0 + l.
+template <bool kF32>
 __device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, int64_t n, float (&v)[32], float* turn) {
   const int lane = threadIdx.x & 31;
   const int64_t m = m0 + lane;
@@ -87,7 +95,7 @@ __device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, 
         }
       }
     }
-    if (p.out_f32) {
+    if constexpr (kF32) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + m * p.ldo + n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -121,7 +129,7 @@ __device__ __forceinline__ void store_tile32(const LinearParams& p, int64_t m0, 
           for (int r = 0; r < 8; ++r) f[r] += __bfloat162float(w[r]);
           res += 8 * p.ldr;
         }
-        if (p.out_f32) {
+        if constexpr (kF32) {
 #pragma unroll
           for (int r = 0; r < 8; ++r)
             if (r0 + r < rows) o32[r * p.ldo] = f[r];
@@ -171,7 +179,7 @@ __device__ __forceinline__ void add_bias32(float bias, float (&v)[32], float* ro
 // 8 consecutive elements of rows l / 4 and l / 4 + 8, its K slots of two products (A and B permute K alike).  The 16
 // warps of a CTA are `groups` row groups times 16 / groups shares of K, interleaved in blocks of 32, so that the CTA
 // reads each row in long pieces; their sums meet in shared memory in the order of the shares.
-template <bool kGated, int kTiles>
+template <bool kGated, int kTiles, bool kF32>
 __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kTok = 8 * kTiles;
   constexpr int kU = kTiles == 1 ? 4 : (kTiles == 2 ? 2 : 1);  // blocks of 32 K of an operand set
@@ -216,14 +224,26 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
         }
       }
     };
-    auto multiply = [&](const Operands& o) {
+    auto add_products = [&](const Operands& o, float (&sums)[kTiles][4]) {
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          ptx::mma_16816(acc[i], o.a[u].x, o.b[u].x, o.a[u].y, o.b[u].y, o.x[u][i].x, o.x[u][i].y);
-          ptx::mma_16816(acc[i], o.a[u].z, o.b[u].z, o.a[u].w, o.b[u].w, o.x[u][i].z, o.x[u][i].w);
+          ptx::mma_16816(sums[i], o.a[u].x, o.b[u].x, o.a[u].y, o.b[u].y, o.x[u][i].x, o.x[u][i].y);
+          ptx::mma_16816(sums[i], o.a[u].z, o.b[u].z, o.a[u].w, o.b[u].w, o.x[u][i].z, o.x[u][i].w);
         }
+    };
+    auto multiply = [&](const Operands& o) {
+      if constexpr (!kF32) {
+        add_products(o, acc);
+      } else {  // the tensor core adds 32 to 128 products, truncating; those sums are added to nearest
+        float some[kTiles][4] = {};
+        add_products(o, some);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][c] += some[i][c];
+      }
     };
     // two sets of operands: one is on its way while the other is multiplied
     Operands even, odd;
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
 // ============================================================================ pair form
 // Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
 // tiles in flight share rows of x and of W in L2.
-template <int kAct, int kKps>
+template <int kAct, int kKps, bool kF32>
 __global__ void __launch_bounds__(lin::kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
@@ -304,6 +324,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
   // a stage: kKps K blocks of 64, each 128 rows of x and then BN / 2 rows of W
   const int block_bytes = lin::kTileBytes + BN * 64, stage_bytes = kKps * block_bytes, n_stages = p.n_stages;
   const int KB = (p.KB + kKps - 1) / kKps;
+  const int per = kF32 ? lin::kChunk<kGated> / kKps : KB;  // stages to an accumulator
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
@@ -403,13 +424,13 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       uint32_t phase = 0, lo = lo0;
       int acc_i = 0;
       bool ok = true;
-      for (int t = first; ok && t < tiles; t += pairs) {
-        const int buf = acc_i & 1;
+      for (int t = first, left = KB; ok && t < tiles; t += left == KB ? pairs : 0) {  // left: stages left of the tile
+        const int buf = acc_i & 1, n = kF32 ? min(per, left) : KB;
         if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
         uint32_t accumulate = 0;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < n; ++kb) {
           if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
             ok = false;
             break;
@@ -423,7 +444,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
                 ptx::tc_mma_f16_pair_lo(d, lo + i * lo_block + 2 * q, lo + i * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi,
                                         idesc, i + q > 0 ? 1u : accumulate);
             ptx::tc_commit_pair(empty0 + 8 * stage);
-            if (kb == KB - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+            if (kb == n - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
           }
           accumulate = 1;
           lo += lo_step;
@@ -434,6 +455,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
           }
         }
         ++acc_i;
+        if (kF32) left = left > n ? left - n : KB;
       }
       if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(drain));
       wait_bar_drain(ptx::smem_u32(drain), 0);
@@ -447,59 +469,101 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
     for (int t = first; t < tiles; t += pairs) {
       int mt, nt;
       tile_at(t, mt, nt);
-      const int buf = acc_i & 1;
       const int cols = kGated ? BN / 2 : BN;
       const int64_t n0 = (int64_t)nt * cols;
       // the tile's biases, a column per lane, before the wait for its products
       constexpr int kChunks = kGated ? 2 : 4;
       float bias[kChunks] = {}, bias_up[kChunks] = {};
-      if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int64_t n = n0 + 32 * half + 64 * i + lane;
-          if (n < p.N) {
-            bias[i] = __bfloat162float(p.bias[n]);
-            if constexpr (kGated) bias_up[i] = __bfloat162float(p.bias[p.N + n]);
-          }
+      auto load_bias = [&](int i) {
+        const int64_t n = n0 + 32 * half + 64 * i + lane;
+        if (p.bias && n < p.N) {
+          bias[i] = __bfloat162float(p.bias[n]);
+          if constexpr (kGated) bias_up[i] = __bfloat162float(p.bias[p.N + n]);
         }
+      };
+      if constexpr (!kF32) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) load_bias(i);
       }
-      if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
-      ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * 256;
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
       const int64_t m0 = (int64_t)mt * 256 + rank * 128 + q * 32;  // this warp's rows
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int c0 = 32 * half + 64 * i;
-        if (c0 >= cols) break;
-        uint32_t r[32];
-        float v[32];
-        ptx::tmem_ld_32x32b_x32(taddr + c0, r);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      auto wait_full = [&]() {
+        const bool ok = warp_wait_quick(ptx::smem_u32(&accf[acc_i & 1]), (acc_i >> 1) & 1, ctl);
+        ptx::tc_fence_after();
+        return ok;
+      };
+      auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[acc_i & 1]), 0));
+        ++acc_i;
+      };
+      // chunk i's values v (gated: and up values u), biased, activated, with the residual, to memory
+      auto finish = [&](int i, float (&v)[32], float (&u)[32]) {
         if (p.bias) add_bias32(bias[i], v, turn);
         if constexpr (kGated) {
-          ptx::tmem_ld_32x32b_x32(taddr + BN / 2 + c0, r);
-          ptx::tmem_wait_ld();
-          float u[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
           if (p.bias) add_bias32(bias_up[i], u, turn);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = (p.out_f32 ? silu(v[j]) : silu<true>(v[j])) * u[j];
-        } else if (p.out_f32) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = activate(kAct, v[j]);
+          for (int j = 0; j < 32; ++j) v[j] = silu<!kF32>(v[j]) * u[j];
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = activate<true>(kAct, v[j]);
+          for (int j = 0; j < 32; ++j) v[j] = activate<!kF32>(kAct, v[j]);
         }
-        store_tile32(p, m0, n0 + c0, v, turn);
+        store_tile32<kF32>(p, m0, n0 + 32 * half + 64 * i, v, turn);
+      };
+      if constexpr (!kF32) {
+        if (!wait_full()) break;
+        const uint32_t at = taddr + (acc_i & 1) * 256;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c0 = 32 * half + 64 * i;
+          if (c0 >= cols) break;
+          uint32_t r[32];
+          float v[32], u[32];
+          ptx::tmem_ld_32x32b_x32(at + c0, r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          if constexpr (kGated) {
+            ptx::tmem_ld_32x32b_x32(at + BN / 2 + c0, r);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
+          }
+          finish(i, v, u);
+        }
+        release();
+      } else {
+        float sum[4][32] = {};  // gated: two chunks of gate values, then their up values
+        bool ok = true;
+        for (int kb = 0; kb < KB; kb += per) {
+          ok = wait_full();
+          if (!ok) break;
+          const uint32_t at = taddr + (acc_i & 1) * 256;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = 32 * half + 64 * (i % kChunks);
+            if (c0 < cols) {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {  // 32 at a time would not fit in registers beside the sums
+                uint32_t r[16];
+                ptx::tmem_ld_32x32b_x16(at + c0 + h + i / kChunks * (BN / 2), r);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[i][h + j] += __uint_as_float(r[j]);
+              }
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          if (32 * half + 64 * i >= cols) break;
+          load_bias(i);  // (not before: the sums have the registers)
+          finish(i, sum[i], sum[i + 4 - kChunks]);
+        }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[buf]), 0));
-      ++acc_i;
     }
   }
 
@@ -521,7 +585,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
 // ============================================================================ stream form
 // Cluster c takes the tiles c, c + clusters, ...; its CTA of rank r the K blocks [KB r / S, KB (r + 1) / S).
 // A tile is 128 rows of W; with the gated activation 64 gate rows and the 64 up rows of the same columns.
-template <int kAct>
+template <int kAct, bool kF32>
 __global__ void __launch_bounds__(lin::kThreads, 1)
     linear_stream_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
@@ -532,8 +596,8 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::kStreamArena);
   uint64_t* empty = full + lin::kStreamMaxStages;
   uint64_t* accf = empty + lin::kStreamMaxStages;
-  uint64_t* acce = accf + 1;
-  uint64_t* drain = acce + 1;
+  uint64_t* acce = accf + 2;
+  uint64_t* drain = acce + 2;
   uint64_t* pready = drain + 1;  // every CTA's partial sums are in its shared memory
   uint64_t* pfree = pready + 1;  // every CTA has read this one's
   int32_t* misc = reinterpret_cast<int32_t*>(pfree + 1);
@@ -548,15 +612,20 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   const int clusters = gridDim.x / S, first = blockIdx.x / S, tiles = p.tiles_n;
   // [T][128]: in the ring's place when no tile follows, whose loads would write there
   float* part = reinterpret_cast<float*>(smem + (tiles <= clusters ? 0 : n_stages * stage_bytes));
-  const uint32_t tmem_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128);
+  // one accumulator, or two in turn for the chunks of FP32 results
+  const uint32_t acc_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128), tmem_cols = kF32 ? 2 * acc_cols : acc_cols;
+  auto acc_of = [&](uint32_t i) { return kF32 ? i & 1 : 0; };
+  auto phase_of = [&](uint32_t i) { return kF32 ? (i >> 1) & 1 : i & 1; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(accf), 1 + p.test_stall);
-    ptx::mbar_init(ptx::smem_u32(acce), 8);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
+      ptx::mbar_init(ptx::smem_u32(&acce[b]), 8);
+    }
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     ptx::mbar_init(ptx::smem_u32(pready), S);
     ptx::mbar_init(ptx::smem_u32(pfree), S);
@@ -578,6 +647,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   const uint32_t smem_base = ptx::smem_u32(smem);
   const int units = (p.KB + kKps - 1) / kKps;  // what lies past K is loaded as zeros
   const int kb0 = (int)((int64_t)units * rank / S), kb1 = (int)((int64_t)units * (rank + 1) / S);
+  const int per = kF32 ? lin::kChunk<kGated> / kKps : kb1 - kb0;  // stages to an accumulator
   // Beside the pair form: this kernel starts when every CTA of that one has seen its predecessors end, and may not end
   // before it does.
   if (!p.beside) ptx::griddep_wait();
@@ -633,13 +703,15 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
                    lo_block = (uint32_t)block_bytes >> 4;
     const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
     int stage = 0;
-    uint32_t phase = 0, aph = 0, lo = lo0;
+    uint32_t phase = 0, acc_i = 0, lo = lo0;
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += clusters) {
-      if (!warp_wait_quick(ptx::smem_u32(acce), aph ^ 1, ctl)) break;
+    for (int t = first, k0 = kb0; ok && t < tiles; t += k0 == kb0 ? clusters : 0) {
+      const int k1 = kF32 ? min(k0 + per, kb1) : kb1;
+      if (!warp_wait_quick(ptx::smem_u32(&acce[acc_of(acc_i)]), phase_of(acc_i) ^ 1, ctl)) break;
       ptx::tc_fence_after();
+      const uint32_t d = tmem_base + acc_of(acc_i) * acc_cols;
       uint32_t accumulate = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = k0; kb < k1; ++kb) {
         if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
           ok = false;
           break;
@@ -650,10 +722,10 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
           for (int h = 0; h < kKps; ++h)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              ptx::tc_mma_f16_lo(tmem_base, lo + h * lo_block + 2 * q, lo + h * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi,
-                                 idesc, h + q > 0 ? 1u : accumulate);
+              ptx::tc_mma_f16_lo(d, lo + h * lo_block + 2 * q, lo + h * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi, idesc,
+                                 h + q > 0 ? 1u : accumulate);
           ptx::tc_commit(empty0 + 8 * stage);
-          if (kb == kb1 - 1) ptx::tc_commit(ptx::smem_u32(accf));
+          if (kb == k1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
         }
         accumulate = 1;
         lo += lo_step;
@@ -663,32 +735,71 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
           lo = lo0;
         }
       }
-      aph ^= 1;
+      ++acc_i;
+      if (kF32) k0 = k1 == kb1 ? kb0 : k1;
     }
     if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(drain));
     wait_bar_drain(ptx::smem_u32(drain), 0);
     __syncwarp();
   } else {
     const int q = warp & 3, ep = threadIdx.x - 64;
-    uint32_t ph = 0;
+    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
+    const int c_first = (warp - 2) / 4 * 16;  // every other 16 rows of x from there
+    uint32_t ph = 0, acc_i = 0;
+    auto wait_full = [&]() {
+      const bool ok = warp_wait_quick(ptx::smem_u32(&accf[acc_of(acc_i)]), phase_of(acc_i), ctl);
+      ptx::tc_fence_after();
+      return ok;
+    };
+    auto release = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[acc_of(acc_i)]));
+      ++acc_i;
+    };
     for (int t = first; t < tiles; t += clusters, ph ^= 1) {
-      bool ok = warp_wait_quick(ptx::smem_u32(accf), ph, ctl);
+      [[maybe_unused]] float sum[4][16] = {};
+      bool ok = true;
+      if constexpr (kF32) {
+        for (int kb = kb0; ok && kb < kb1; kb += per) {
+          ok = wait_full();
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (c_first + 32 * i < T) {
+              uint32_t r[16];
+              ptx::tmem_ld_32x32b_x16(taddr + acc_of(acc_i) * acc_cols + c_first + 32 * i, r);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[i][j] += __uint_as_float(r[j]);
+            }
+          }
+          release();
+        }
+      } else {
+        ok = wait_full();
+      }
       // the partial sums of the tile before have been read by every CTA of the cluster
       if (ok && S > 1) ok = wait_bar_cluster(ptx::smem_u32(pfree), ph ^ 1, ctl);
       if (!ptx::bar_all(1, kEpi, ok)) break;  // the warps leave together: they share named barriers
       ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
-      for (int c0 = (warp - 2) / 4 * 16; c0 < T; c0 += 32) {
-        uint32_t r[16];
-        ptx::tmem_ld_32x32b_x16(taddr + c0, r);
-        ptx::tmem_wait_ld();
+      if constexpr (kF32) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c0 + j < T) part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c_first + 32 * i + j < T) part[(c_first + 32 * i + j) * 128 + q * 32 + lane] = sum[i][j];
+      } else {
+        for (int c0 = c_first; c0 < T; c0 += 32) {
+          uint32_t r[16];
+          ptx::tmem_ld_32x32b_x16(taddr + c0, r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < T) part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+        }
+        release();
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(acce));
       ptx::bar_sync(1, kEpi);
       if (S > 1) {
         if (ep < S) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(pready), ep));
@@ -815,7 +926,7 @@ static int64_t stream_slots(int S, int sms) {
   std::atomic<int>& kept = known[dev][S == 2 ? 0 : (S == 4 ? 1 : 2)];
   int n = kept.load(std::memory_order_relaxed);
   if (n == 0) {
-    auto kernel = linear_stream_kernel<GMMFR_ACT_NONE>;
+    auto kernel = linear_stream_kernel<GMMFR_ACT_NONE, false>;
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -950,21 +1061,21 @@ void plan_linear(LinearParams& p, LinearParams& tail, int sms) {
   tail.slot_base = p.grid;
 }
 
-template <int kAct>
+template <int kAct, bool kF32>
 static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct>
-                                        : (p.kps == 1 ? linear_pair_kernel<kAct, 1> : linear_pair_kernel<kAct, 2>);
+  auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct, kF32>
+                                        : (p.kps == 1 ? linear_pair_kernel<kAct, 1, kF32> : linear_pair_kernel<kAct, 2, kF32>);
   const int smem = p.form == kLinearStream ? lin::kStreamSmem : lin::kPairSmem;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          lin::kStreamSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
@@ -985,33 +1096,36 @@ static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cud
   return cudaLaunchKernelEx(&lc, kernel, maps, p);
 }
 
-static cudaError_t launch_direct(const LinearParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)p.grid);
-  lc.blockDim = dim3(512);
-  lc.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  const int tiles = p.M <= 8 ? 1 : (p.M <= 16 ? 2 : 4);
-  auto kernel = p.act == GMMFR_ACT_SWIGLU
-                    ? (tiles == 1 ? linear_direct_kernel<true, 1> : (tiles == 2 ? linear_direct_kernel<true, 2> : linear_direct_kernel<true, 4>))
-                    : (tiles == 1 ? linear_direct_kernel<false, 1> : (tiles == 2 ? linear_direct_kernel<false, 2> : linear_direct_kernel<false, 4>));
-  return cudaLaunchKernelEx(&lc, kernel, p);
+template <bool kF32>
+static cudaError_t launch_form(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
+  if (p.form == kLinearDirect) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)p.grid);
+    lc.blockDim = dim3(512);
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    const int tiles = p.M <= 8 ? 0 : (p.M <= 16 ? 1 : 2);
+    constexpr decltype(&linear_direct_kernel<true, 1, kF32>) kernels[2][3] = {
+        {linear_direct_kernel<false, 1, kF32>, linear_direct_kernel<false, 2, kF32>, linear_direct_kernel<false, 4, kF32>},
+        {linear_direct_kernel<true, 1, kF32>, linear_direct_kernel<true, 2, kF32>, linear_direct_kernel<true, 4, kF32>}};
+    return cudaLaunchKernelEx(&lc, kernels[p.act == GMMFR_ACT_SWIGLU][tiles], p);
+  }
+  switch (p.act) {
+    case GMMFR_ACT_RELU: return launch_one<GMMFR_ACT_RELU, kF32>(maps, p, s);
+    case GMMFR_ACT_GELU: return launch_one<GMMFR_ACT_GELU, kF32>(maps, p, s);
+    case GMMFR_ACT_GELU_TANH: return launch_one<GMMFR_ACT_GELU_TANH, kF32>(maps, p, s);
+    case GMMFR_ACT_SILU: return launch_one<GMMFR_ACT_SILU, kF32>(maps, p, s);
+    case GMMFR_ACT_SWIGLU: return launch_one<GMMFR_ACT_SWIGLU, kF32>(maps, p, s);
+    default: return launch_one<GMMFR_ACT_NONE, kF32>(maps, p, s);
+  }
 }
 
 cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  if (p.form == kLinearDirect) return launch_direct(p, s);
-  switch (p.act) {
-    case GMMFR_ACT_RELU: return launch_one<GMMFR_ACT_RELU>(maps, p, s);
-    case GMMFR_ACT_GELU: return launch_one<GMMFR_ACT_GELU>(maps, p, s);
-    case GMMFR_ACT_GELU_TANH: return launch_one<GMMFR_ACT_GELU_TANH>(maps, p, s);
-    case GMMFR_ACT_SILU: return launch_one<GMMFR_ACT_SILU>(maps, p, s);
-    case GMMFR_ACT_SWIGLU: return launch_one<GMMFR_ACT_SWIGLU>(maps, p, s);
-    default: return launch_one<GMMFR_ACT_NONE>(maps, p, s);
-  }
+  return p.out_f32 ? launch_form<true>(maps, p, s) : launch_form<false>(maps, p, s);
 }
 
 }  // namespace gmmfr

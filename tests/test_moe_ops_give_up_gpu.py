@@ -46,6 +46,8 @@ call("stream, many tiles", B.Linear(randn(40000, 1024), activation="swiglu"), ra
 call("pair", B.Linear(randn(4096, 2048)), randn(5000, 2048))
 call("pair, short stages", B.Linear(randn(64, 2048)), randn(300, 2048))
 call("pair and rows beside it", B.Linear(randn(4096, 2048)), randn(1030, 2048))
+for M, N, K, act in ((100, 40000, 1024, "swiglu"), (60, 300, 7168, "none"), (5000, 4096, 2048, "none"), (1030, 4096, 2048, "swiglu")):
+    call(f"float32 {M} x {N} x {K}", B.Linear(randn(2 * N if act == "swiglu" else N, K), activation=act, out_dtype=torch.float32), randn(M, K))
 x = torch.randn(1000, 1000, device="cuda")
 print(json.dumps([seen, bool(torch.isfinite(x @ x).all())]))
 """
