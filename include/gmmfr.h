@@ -509,6 +509,55 @@ GMMFR_API gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const v
                                     const void* bias, const void* residual, void* out, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/*
+ * Products grouped by expert and their gradients, on weights as they lie in memory (training, where weights change
+ * from step to step, or any expert that is not the FFN above).  The rows of expert e are [start_e, end_e) of x and y, in
+ * the experts' order, as gmmfr_moe_route leaves them:
+ *   y[t]  = sum_k W_e[n,k] x[t,k]                (FP32 sums, one rounding)
+ *   dx[t] = sum_n W_e[n,k] dy[t,n]               the same call on the weights the other way round: N and K exchanged,
+ *                                                transposed flipped
+ *   dW_e  = sum over t of dy[t,n] x[t,k]         gmmfr_grouped_linear_grad_weight; an expert without rows has zeros
+ * An infinity or NaN in a row reaches that row of y (or dx) alone and the gradient of its own expert; one in a row of no
+ * expert reaches nothing, one in an expert's weights its own rows.
+ *   M             rows of x and y, 0 <= M < 2^31
+ *   N, K, E       sizes of the weights: N and K multiples of 8 in [8, 2^24), N * K < 2^38; 1 <= E <= 1024
+ *   ldx, ldy      elements from one row of x, and of y or dy, to the next; 0 stands for the row's length.  Rows that are
+ *                 read lie at multiples of 8
+ *   transposed    0: weight (and its gradient) [E, N, K];  1: [E, K, N]
+ *   group_list_type  0: prefix sums, expert e owns [g[e-1], g[e]) with g[-1] = 0;  1: counts
+ *   out_type      GMMFR_DT_BF16 or GMMFR_DT_F32: of y, or of the gradient.  FP32 results are sums of at most 1024
+ *                 products by the tensor cores, which truncate (at most 3.9e-6 of a sum of terms of one sign), and of those
+ *                 to nearest; BF16 results sums of all K products (y) or of at most 8192 (the gradient) by the tensor cores
+ *   zero_rest     rows of y that belong to no expert: 1: set to zero, 0: left as they are
+ *   accumulate    the gradient is 0: written, 1: added to what lies there (FP32 only)
+ */
+typedef struct {
+  int64_t M, N, K, E;
+  int64_t ldx, ldy;
+  int32_t transposed;
+  int32_t group_list_type;
+  int32_t out_type;
+  int32_t zero_rest;
+  int32_t accumulate;
+} gmmfr_grouped_problem;
+
+/* Workspace bytes of both calls (256-byte aligned; contents on entry do not matter).  Host only. */
+GMMFR_API gmmfr_status gmmfr_grouped_linear_workspace_size(const gmmfr_grouped_problem* problem, size_t* bytes);
+
+/* x [M, K] BF16 and weight BF16, dense, both 16-byte aligned; group_list [E] int64, checked on the device: sizes that are
+ * negative, decrease or pass M set GMMFR_DEV_BAD_GROUP_LIST and are clamped; y [M, N] of out_type, not x's memory.  One
+ * launch.  Never syncs, never allocates; deterministic; a wait that gave up sets GMMFR_DEV_TIMEOUT in the workspace's
+ * device error word (gmmfr_check_device_errors). */
+GMMFR_API gmmfr_status gmmfr_grouped_linear(const gmmfr_grouped_problem* problem, const void* x, const void* weight,
+                                            const int64_t* group_list, void* y, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/* dy [M, N] BF16, x [M, K] BF16 and dweight (of out_type, the weight's layout, dense), all 16-byte aligned; otherwise as
+ * above. */
+GMMFR_API gmmfr_status gmmfr_grouped_linear_grad_weight(const gmmfr_grouped_problem* problem, const void* dy, const void* x,
+                                                        const int64_t* group_list, void* dweight, void* workspace,
+                                                        size_t workspace_bytes, void* stream);
+
 /* Message of the last error returned on the calling thread ("" if none). */
 GMMFR_API const char* gmmfr_last_error(void);
 

@@ -37,6 +37,7 @@ ENTRY_POINTS = (
     "gmmfr_ffn_prepared_weights_size_mx", "gmmfr_ffn_prepare_weights_mx",
     "gmmfr_moe_layer_workspace_size", "gmmfr_moe_layer",
     "gmmfr_linear_workspace_size", "gmmfr_linear",
+    "gmmfr_grouped_linear_workspace_size", "gmmfr_grouped_linear", "gmmfr_grouped_linear_grad_weight",
 )
 GATE_SCORING = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
@@ -122,6 +123,14 @@ class LinearProblem(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32), ("unaligned", ctypes.c_int32)]
 
 
+class GroupedProblem(ctypes.Structure):
+    """Mirror of gmmfr_grouped_problem."""
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("E", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("transposed", ctypes.c_int32),
+                ("group_list_type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("zero_rest", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
 class GmmfrError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"gmmfr status {status}: {message}")
@@ -166,6 +175,10 @@ def load(path: str = LIB_PATH):
             lib.gmmfr_moe_layer.argtypes = [LP] + [vp] * 6 + [sz, vp, sz] + [vp] * 3 + [sz, vp]
             lib.gmmfr_linear_workspace_size.argtypes = [DP, ctypes.POINTER(sz)]
             lib.gmmfr_linear.argtypes = [DP] + [vp] * 6 + [sz, vp]
+            UP = ctypes.POINTER(GroupedProblem)
+            lib.gmmfr_grouped_linear_workspace_size.argtypes = [UP, ctypes.POINTER(sz)]
+            lib.gmmfr_grouped_linear.argtypes = [UP] + [vp] * 5 + [sz, vp]
+            lib.gmmfr_grouped_linear_grad_weight.argtypes = [UP] + [vp] * 5 + [sz, vp]
             lib.gmmfr_check_device_errors.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
             lib.gmmfr_last_error.restype = ctypes.c_char_p
             lib.gmmfr_profile_begin.argtypes = [ctypes.c_int]
@@ -343,6 +356,22 @@ def gmmfr_linear(problem: LinearProblem, x, weight, bias, residual, out, workspa
                  stream=None) -> None:
     _check(load().gmmfr_linear(ctypes.byref(problem), x, weight, bias, residual, out, workspace, workspace_bytes,
                                stream))
+
+
+def gmmfr_grouped_linear_workspace_size(problem: GroupedProblem) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gmmfr_grouped_linear_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def gmmfr_grouped_linear(problem: GroupedProblem, x, weight, group_list, y, workspace, workspace_bytes, stream=None) -> None:
+    _check(load().gmmfr_grouped_linear(ctypes.byref(problem), x, weight, group_list, y, workspace, workspace_bytes, stream))
+
+
+def gmmfr_grouped_linear_grad_weight(problem: GroupedProblem, dy, x, group_list, dweight, workspace, workspace_bytes,
+                                     stream=None) -> None:
+    _check(load().gmmfr_grouped_linear_grad_weight(ctypes.byref(problem), dy, x, group_list, dweight, workspace,
+                                                   workspace_bytes, stream))
 
 
 def gmmfr_check_device_errors(workspace: int, stream: Optional[int] = None) -> int:
@@ -644,7 +673,7 @@ class _Handle:
             _handed_over(stream, t)
             return t
         if self._empty_here is not None:
-            return self._empty_here(shape, (shape[1], 1), dtype)
+            return self._empty_here(shape, (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1), dtype)
         return self._empty(shape, dtype=dtype, device=self._device)
 
 
@@ -879,6 +908,110 @@ class Linear(_Handle):
         cx, cr, co = self._cx, self._cr, self._co
         cx.value, cr.value, co.value = xptr, rptr, out.data_ptr()
         st = self._fn(self._ref, cx, self._cw, self._cb, cr, co, ws[0], ws[1], ws[2])
+        if st:
+            _check(st)
+        return out
+
+
+class GroupedLinear(_Handle):
+    """Products grouped by expert on weights as they lie: ``grouped(x, group_list)`` -> y [M, N], the rows of expert e
+    multiplied by ``weight[e]``.T; and the gradients ``grad_input(dy, group_list)`` -> dx [M, K] bfloat16 and
+    ``grad_weight(dy, x, group_list)`` -> dw, of the weight's layout.
+
+    ``weight`` [E, N, K] bfloat16, or with ``transposed`` [E, K, N]; it is read where it is at each call.  ``group_list``
+    [E] int64 as :func:`route` makes it: counts (``group_list_type`` 1) or prefix sums (0).  Rows of no expert come out as
+    zeros, or stay as they are in a given ``out``.  ``out_dtype`` is y's, ``grad_dtype`` dw's; ``accumulate`` adds to
+    ``out`` (float32)."""
+
+    def __init__(self, weight, transposed: bool = False, group_list_type: int = 1, out_dtype=None, grad_dtype=None):
+        import torch
+        super().__init__(weight.device)
+        types = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+        self._out = torch.bfloat16 if out_dtype is None else out_dtype
+        self._grad = torch.bfloat16 if grad_dtype is None else grad_dtype
+        for name, t in (("out_dtype", self._out), ("grad_dtype", self._grad)):
+            if t not in types:
+                raise ValueError(f"{name} {t} is not bfloat16 or float32")
+        if weight.dim() != 3:
+            _refuse("weight", weight, "[E, N, K] or [E, K, N]", self._index)
+        self._wptr = _dense(weight, "weight", tuple(weight.shape), torch.bfloat16, self._index)
+        self._keep = (weight,)
+        self._shape = tuple(weight.shape)
+        E, N, K = self._shape
+        if transposed:
+            N, K = K, N
+        self._E, self._N, self._K = E, N, K
+        rule = dict(E=E, group_list_type=group_list_type)
+        self._forward = GroupedProblem(N=N, K=K, transposed=int(bool(transposed)), out_type=types[self._out], **rule)
+        # dx = dy W: the same weights the other way round
+        self._input = GroupedProblem(N=K, K=N, transposed=int(not transposed), out_type=DT_BF16, **rule)
+        self._weight = GroupedProblem(N=N, K=K, transposed=int(bool(transposed)), out_type=types[self._grad], **rule)
+        self._bf16, self._i64 = torch.bfloat16, torch.int64
+        self._fn, self._fn_grad = self._entry("gmmfr_grouped_linear"), self._entry("gmmfr_grouped_linear_grad_weight")
+        self._cx, self._cy, self._cg, self._co = (ctypes.c_void_p() for _ in range(4))
+        self._cw = ctypes.c_void_p(self._wptr)
+        for p in (self._forward, self._input, self._weight):
+            self._need = gmmfr_grouped_linear_workspace_size(p)
+
+    def _space(self, stream):
+        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
+        ws = self._spaces.get(s)
+        return self._grow(s, self._need, stream) if ws is None or ws[3] < self._need else ws
+
+    def _product(self, p, x, group_list, out, dtype, stream):
+        dev, N = self._index, p.N
+        p.ldx = _rows(x, "x" if p is self._forward else "dy", None, p.K, self._bf16, dev)
+        p.M = M = x.shape[0]
+        gptr = _dense(group_list, "group_list", (self._E,), self._i64, dev)
+        p.zero_rest = int(out is None)
+        if out is None:
+            out = self._new((M, N), dtype, stream)
+            p.ldy = 0
+        else:
+            p.ldy = _rows(out, "out", M, N, dtype, dev)
+        ws = self._space(stream)
+        cx, cg, co = self._cx, self._cg, self._co
+        cx.value, cg.value, co.value = x.data_ptr(), gptr, out.data_ptr()
+        st = self._fn(ctypes.byref(p), cx, self._cw, cg, co, ws[0], ws[1], ws[2])
+        if st:
+            _check(st)
+        return out
+
+    def __call__(self, x, group_list, out=None, stream=None):
+        if self._current() != self._index:
+            return self._there(x, group_list, out, stream)
+        return self._product(self._forward, x, group_list, out, self._out, stream)
+
+    def grad_input(self, dy, group_list, out=None, stream=None):
+        """dx [M, K]: the rows' gradient, from y's."""
+        import torch
+        if self._current() != self._index:
+            with torch.cuda.device(self._index):
+                return self.grad_input(dy, group_list, out, stream)
+        return self._product(self._input, dy, group_list, out, self._bf16, stream)
+
+    def grad_weight(self, dy, x, group_list, out=None, accumulate: bool = False, stream=None):
+        """dw, of the weight's layout: for each expert the sum over its rows; zeros for one without rows."""
+        import torch
+        if self._current() != self._index:
+            with torch.cuda.device(self._index):
+                return self.grad_weight(dy, x, group_list, out, accumulate, stream)
+        p, dev = self._weight, self._index
+        p.ldy = _rows(dy, "dy", None, self._N, self._bf16, dev)
+        p.M = M = dy.shape[0]
+        p.ldx = _rows(x, "x", M, self._K, self._bf16, dev)
+        gptr = _dense(group_list, "group_list", (self._E,), self._i64, dev)
+        p.accumulate = int(bool(accumulate))
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate adds to a given out")
+            out = self._new(self._shape, self._grad, stream)
+        else:
+            _dense(out, "out", self._shape, self._grad, dev)
+        ws = self._space(stream)
+        cx, cy, cg, co = self._cx, self._cy, self._cg, self._co
+        cx.value, cy.value, cg.value, co.value = x.data_ptr(), dy.data_ptr(), gptr, out.data_ptr()
+        st = self._fn_grad(ctypes.byref(p), cy, cx, cg, co, ws[0], ws[1], ws[2])
         if st:
             _check(st)
         return out

@@ -1,4 +1,4 @@
-// C ABI of the router, the few-token MoE layer and the dense product (declared in include/gmmfr.h):
+// C ABI of the router, the few-token MoE layer, the dense product and the grouped products (declared in include/gmmfr.h):
 // argument checks, workspace layout, launches.
 #include <algorithm>
 #include <cstdarg>
@@ -224,6 +224,42 @@ LinearLayout linear_layout(const gmmfr_linear_problem* p) {
   if (p->unaligned || odd_stride_w(p)) off = align256(off + 2 * Kp * p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1));
   L.total = off;
   return L;
+}
+
+// ---------------------------------------------------------------- products grouped by expert
+gmmfr_status validate_grouped(const gmmfr_grouped_problem* p) {
+  if (!p) return fail(GMMFR_ERR_INVALID_ARG, "problem is NULL");
+  if (p->M < 0 || p->M >= kMaxSize) return fail(GMMFR_ERR_INVALID_ARG, "M=%lld out of range [0, 2^31)", (long long)p->M);
+  if (p->N < 8 || p->K < 8 || p->N % 8 || p->K % 8 || p->N >= (int64_t(1) << 24) || p->K >= (int64_t(1) << 24) ||
+      p->N * p->K >= (int64_t(1) << 38))
+    return fail(GMMFR_ERR_INVALID_ARG, "N=%lld K=%lld are not multiples of 8 in [8, 2^24) with a product below 2^38",
+                (long long)p->N, (long long)p->K);
+  if (p->E < 1 || p->E > gmmfr::kMaxExperts) return fail(GMMFR_ERR_INVALID_ARG, "E=%lld out of range [1, 1024]", (long long)p->E);
+  if ((p->ldx && p->ldx < p->K) || (p->ldy && p->ldy < p->N) || p->ldx >= (int64_t(1) << 38) || p->ldy >= (int64_t(1) << 38))
+    return fail(GMMFR_ERR_INVALID_ARG, "a row stride is shorter than its row, or above 2^38 (ldx=%lld ldy=%lld)", (long long)p->ldx,
+                (long long)p->ldy);
+  if (p->ldx % 8) return fail(GMMFR_ERR_INVALID_ARG, "ldx=%lld is not a multiple of 8", (long long)p->ldx);
+  if (p->transposed != 0 && p->transposed != 1) return fail(GMMFR_ERR_INVALID_ARG, "transposed must be 0 or 1");
+  if (p->group_list_type != 0 && p->group_list_type != 1)
+    return fail(GMMFR_ERR_INVALID_ARG, "group_list_type=%d is not 0 (prefix sums) or 1 (counts)", p->group_list_type);
+  if (p->out_type != GMMFR_DT_BF16 && p->out_type != GMMFR_DT_F32)
+    return fail(GMMFR_ERR_INVALID_ARG, "out_type=%d is not BF16 (%d) or F32 (%d)", p->out_type, GMMFR_DT_BF16, GMMFR_DT_F32);
+  if (p->zero_rest != 0 && p->zero_rest != 1) return fail(GMMFR_ERR_INVALID_ARG, "zero_rest must be 0 or 1");
+  if (p->accumulate != 0 && p->accumulate != 1) return fail(GMMFR_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  return GMMFR_OK;
+}
+
+// [depth, rows, cols], dense, in boxes of one slice
+bool encode_slices(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const void* base, bool f32, int64_t depth, int64_t rows,
+                   int64_t cols, int box_cols, int box_rows) {
+  const int64_t size = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+  cuuint64_t strides[2] = {(cuuint64_t)(cols * size), (cuuint64_t)(rows * cols * size)};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -460,6 +496,99 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
     cudaError_t e = gmmfr::launch_linear(maps[i], parts[i], s);
     if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   }
+  return GMMFR_OK;
+}
+
+gmmfr_status gmmfr_grouped_linear_workspace_size(const gmmfr_grouped_problem* problem, size_t* bytes) {
+  if (gmmfr_status st = validate_grouped(problem)) return st;
+  if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = gmmfr::kHdrBytes;
+  return GMMFR_OK;
+}
+
+gmmfr_status gmmfr_grouped_linear(const gmmfr_grouped_problem* problem, const void* x, const void* weight,
+                                  const int64_t* group_list, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (gmmfr_status st = validate_grouped(problem)) return st;
+  const gmmfr_grouped_problem& p = *problem;
+  if (p.accumulate) return fail(GMMFR_ERR_INVALID_ARG, "accumulate is the weights' gradient's");
+  if (p.M == 0) return GMMFR_OK;
+  if (!x || !weight || !group_list || !y)
+    return fail(GMMFR_ERR_INVALID_ARG, "x, weight, group_list and y must be non-NULL when M > 0");
+  if (!aligned(x, 16) || !aligned(weight, 16)) return fail(GMMFR_ERR_INVALID_ARG, "x and weight must be 16-byte aligned");
+  const bool f32 = p.out_type == GMMFR_DT_F32;
+  if (!aligned(group_list, 8) || !aligned(y, f32 ? 4 : 2))
+    return fail(GMMFR_ERR_INVALID_ARG, "group_list or y is not aligned to its element size");
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, gmmfr::kHdrBytes)) return st;
+  gmmfr::GroupedParams g{};
+  g.group_list = group_list;
+  g.out = y;
+  g.hdr = static_cast<uint32_t*>(workspace);
+  g.M = p.M;
+  g.N = p.N;
+  g.ldo = stride_or(p.ldy, p.N);
+  g.timeout_ns = waits().limit_ns;
+  g.test_stall = waits().stall;
+  g.E = (int32_t)p.E;
+  g.group_list_type = p.group_list_type;
+  g.KB = (int32_t)cdiv(p.K, 64);
+  g.out_f32 = f32;
+  g.vec_out = aligned(y, 4) && g.ldo % 2 == 0;
+  g.zero_rest = p.zero_rest;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+  if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  gmmfr::GroupedMaps maps;
+  bool ok = p.transposed ? encode_slices(encode, &maps.w, weight, false, p.E, p.K, p.N, 64, 64)
+                         : encode_slices(encode, &maps.w, weight, false, p.E, p.N, p.K, 64, 128);
+  for (int i = 0; i < 4; ++i) ok = ok && encode_rows(encode, &maps.x[i], x, p.M, p.K, stride_or(p.ldx, p.K), 16 << i);
+  if (!ok) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld)", (long long)p.ldx);
+  cudaError_t e = gmmfr::launch_grouped(maps, g, p.transposed, gmmfr::sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
+  return GMMFR_OK;
+}
+
+gmmfr_status gmmfr_grouped_linear_grad_weight(const gmmfr_grouped_problem* problem, const void* dy, const void* x,
+                                              const int64_t* group_list, void* dweight, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  if (gmmfr_status st = validate_grouped(problem)) return st;
+  const gmmfr_grouped_problem& p = *problem;
+  const bool f32 = p.out_type == GMMFR_DT_F32;
+  if (p.zero_rest) return fail(GMMFR_ERR_INVALID_ARG, "zero_rest is the product's");
+  if (p.accumulate && !f32) return fail(GMMFR_ERR_INVALID_ARG, "accumulate takes a gradient in FP32");
+  if (p.ldy % 8) return fail(GMMFR_ERR_INVALID_ARG, "ldy=%lld is not a multiple of 8", (long long)p.ldy);
+  if (p.M == 0 && p.accumulate) return GMMFR_OK;
+  if (!dweight) return fail(GMMFR_ERR_INVALID_ARG, "dweight is NULL");
+  if (p.M > 0 && (!dy || !x || !group_list)) return fail(GMMFR_ERR_INVALID_ARG, "dy, x and group_list must be non-NULL when M > 0");
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dweight, 16))
+    return fail(GMMFR_ERR_INVALID_ARG, "dy, x and dweight must be 16-byte aligned");
+  if (!aligned(group_list, 8)) return fail(GMMFR_ERR_INVALID_ARG, "group_list is not aligned to its element size");
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, gmmfr::kHdrBytes)) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.M == 0) {
+    cudaError_t e = cudaMemsetAsync(workspace, 0, 8, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dweight, 0, (size_t)p.E * p.N * p.K * (f32 ? 4 : 2), s);
+    return e == cudaSuccess ? GMMFR_OK : cuda_fail(e, "zeros of the gradient");
+  }
+  gmmfr::GroupedGradParams g{};
+  g.group_list = group_list;
+  g.hdr = static_cast<uint32_t*>(workspace);
+  g.M = p.M;
+  g.A = p.transposed ? p.K : p.N;  // the gradient's rows, then its columns
+  g.B = p.transposed ? p.N : p.K;
+  g.timeout_ns = waits().limit_ns;
+  g.test_stall = waits().stall;
+  g.E = (int32_t)p.E;
+  g.group_list_type = p.group_list_type;
+  g.out_f32 = f32;
+  g.accumulate = p.accumulate;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+  if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  gmmfr::GroupedGradMaps maps;
+  if (!encode_rows(encode, p.transposed ? &maps.b : &maps.a, dy, p.M, p.N, stride_or(p.ldy, p.N), 64) ||
+      !encode_rows(encode, p.transposed ? &maps.a : &maps.b, x, p.M, p.K, stride_or(p.ldx, p.K), 64) ||
+      !encode_slices(encode, &maps.out, dweight, f32, p.E, g.A, g.B, f32 ? 32 : 64, 32))
+    return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld ldy=%lld)", (long long)p.ldx, (long long)p.ldy);
+  cudaError_t e = gmmfr::launch_grouped_grad(maps, g, gmmfr::sm_count(), s);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped gradient launch");
   return GMMFR_OK;
 }
 

@@ -110,4 +110,39 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStr
 cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t rows, int64_t K, int64_t Kp,
                                   int64_t ld, int sms, cudaStream_t s);
 
+// Products grouped by expert (kernels_grouped.cu)
+struct GroupedParams {
+  const int64_t* group_list;  // [E]
+  void* out;                  // [M, N]
+  uint32_t* hdr;              // error words
+  int64_t M, N, ldo;
+  int64_t timeout_ns;
+  int32_t test_stall;  // as GateParams'
+  int32_t E, group_list_type, KB;
+  int32_t out_f32;
+  int32_t vec_out;    // pairs of BF16 outputs start on 4-byte boundaries
+  int32_t zero_rest;  // 1: rows of no group are written, as zeros
+};
+struct GroupedMaps {
+  CUtensorMap w;     // [E, N, K], or [E, K, N]: boxes of 64 x 128, or two of 64 x 64
+  CUtensorMap x[4];  // [M, K], boxes of 16, 32, 64 and 128 rows
+};
+cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedParams& p, bool transposed, int sms, cudaStream_t s);
+
+// Their weights' gradient: out[e] [A, B] = sum over the rows of expert e of a^T b
+struct GroupedGradParams {
+  const int64_t* group_list;
+  uint32_t* hdr;
+  int64_t M, A, B;
+  int64_t timeout_ns;
+  int32_t test_stall;
+  int32_t E, group_list_type;
+  int32_t out_f32, accumulate;
+};
+struct GroupedGradMaps {
+  CUtensorMap a, b;  // [M, A] and [M, B], boxes of 64 columns x 64 rows
+  CUtensorMap out;   // [E, A, B], boxes of 128 bytes x 32 rows
+};
+cudaError_t launch_grouped_grad(const GroupedGradMaps& maps, const GroupedGradParams& p, int sms, cudaStream_t s);
+
 }  // namespace gmmfr
