@@ -74,6 +74,7 @@ typedef enum { GMMFR_INDEX_I64 = 0, GMMFR_INDEX_I32 = 1 } gmmfr_index_type;
 #define GMMFR_DEV_BAD_ROW_INDEX 2u  /* a routed token had row_index outside [0, batch); it was skipped */
 #define GMMFR_DEV_TIMEOUT 4u        /* a pipeline wait gave up; the output is incomplete */
 #define GMMFR_DEV_BAD_EXPERT_ID 8u  /* routing: a top-k expert id outside [0, E); that entry was routed nowhere */
+#define GMMFR_DEV_BAD_ADAPTER_ID 16u /* a row's adapter outside [-1, count); it counts as none */
 
 /*
  * Tensor views.  Every tensor argument of the operator is passed as a non-owning view of
@@ -508,6 +509,35 @@ GMMFR_API gmmfr_status gmmfr_linear_workspace_size(const gmmfr_linear_problem* p
 GMMFR_API gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight,
                                     const void* bias, const void* residual, void* out, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/*
+ * The dense product with low-rank adapters (LoRA) of many requests: row t of x has the adapter a = adapter_ids[t], or
+ * none (-1), and
+ *   y[t] = act(x[t] weight^T + bias + lora_scale[a] (x[t] A_a^T) B_a^T) + residual[t]
+ * act, weight, bias, residual and y as for gmmfr_linear.  Rows may have adapters in any order; one adapter's infinities
+ * and NaN reach its own rows only.  FP32 throughout, x A^T included; y is rounded once.
+ *   linear   the product's sizes and rule; K, ldx and ldw multiples of 8, unaligned 0
+ *   count    adapters, 1 <= count < 2^24
+ *   rank     of all of them, a multiple of 8 in [8, 256] (an adapter of lower rank has zeros in its last rows of A, or
+ *            its last columns of B)
+ */
+typedef struct {
+  gmmfr_linear_problem linear;
+  int64_t count, rank;
+} gmmfr_lora_problem;
+
+/* Workspace bytes of gmmfr_lora_linear (256-byte aligned; contents on entry do not matter).  Host only. */
+GMMFR_API gmmfr_status gmmfr_lora_linear_workspace_size(const gmmfr_lora_problem* problem, size_t* bytes);
+
+/* x and weight 16-byte aligned; lora_a [count, rank, K] and lora_b [count, N or 2N, rank] BF16, dense, 16-byte aligned;
+ * lora_scale [count] float32 or NULL (ones); adapter_ids [M] int32, checked on the device: one outside [-1, count) sets
+ * GMMFR_DEV_BAD_ADAPTER_ID and counts as none.  One launch more than gmmfr_linear.  Never syncs, never allocates;
+ * deterministic; a wait that gave up sets GMMFR_DEV_TIMEOUT in the workspace's device error word
+ * (gmmfr_check_device_errors). */
+GMMFR_API gmmfr_status gmmfr_lora_linear(const gmmfr_lora_problem* problem, const void* x, const void* weight,
+                                         const void* bias, const void* residual, const void* lora_a, const void* lora_b,
+                                         const float* lora_scale, const int32_t* adapter_ids, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
 
 /*
  * Products grouped by expert and their gradients, on weights as they lie in memory (training, where weights change

@@ -20,7 +20,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = rang
 E4M3, E5M2 = 0, 1
 INDEX_I64, INDEX_I32 = 0, 1
 DETERMINISTIC = 1
-DEV_BAD_GROUP_LIST, DEV_BAD_ROW_INDEX, DEV_TIMEOUT, DEV_BAD_EXPERT_ID = 1, 2, 4, 8
+DEV_BAD_GROUP_LIST, DEV_BAD_ROW_INDEX, DEV_TIMEOUT, DEV_BAD_EXPERT_ID, DEV_BAD_ADAPTER_ID = 1, 2, 4, 8, 16
 PROFILE_SLOTS = 5
 PROFILE_SLOT_NAMES = ("prep", "route", "gemm", "combine", "call")
 
@@ -37,6 +37,7 @@ ENTRY_POINTS = (
     "gmmfr_ffn_prepared_weights_size_mx", "gmmfr_ffn_prepare_weights_mx",
     "gmmfr_moe_layer_workspace_size", "gmmfr_moe_layer",
     "gmmfr_linear_workspace_size", "gmmfr_linear",
+    "gmmfr_lora_linear_workspace_size", "gmmfr_lora_linear",
     "gmmfr_grouped_linear_workspace_size", "gmmfr_grouped_linear", "gmmfr_grouped_linear_grad_weight",
 )
 GATE_SCORING = {"softmax": 0, "sigmoid": 1}
@@ -123,6 +124,11 @@ class LinearProblem(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32), ("unaligned", ctypes.c_int32)]
 
 
+class LoraProblem(ctypes.Structure):
+    """Mirror of gmmfr_lora_problem."""
+    _fields_ = [("linear", LinearProblem), ("count", ctypes.c_int64), ("rank", ctypes.c_int64)]
+
+
 class GroupedProblem(ctypes.Structure):
     """Mirror of gmmfr_grouped_problem."""
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("E", ctypes.c_int64),
@@ -175,7 +181,9 @@ def load(path: str = LIB_PATH):
             lib.gmmfr_moe_layer.argtypes = [LP] + [vp] * 6 + [sz, vp, sz] + [vp] * 3 + [sz, vp]
             lib.gmmfr_linear_workspace_size.argtypes = [DP, ctypes.POINTER(sz)]
             lib.gmmfr_linear.argtypes = [DP] + [vp] * 6 + [sz, vp]
-            UP = ctypes.POINTER(GroupedProblem)
+            AP, UP = ctypes.POINTER(LoraProblem), ctypes.POINTER(GroupedProblem)
+            lib.gmmfr_lora_linear_workspace_size.argtypes = [AP, ctypes.POINTER(sz)]
+            lib.gmmfr_lora_linear.argtypes = [AP] + [vp] * 10 + [sz, vp]
             lib.gmmfr_grouped_linear_workspace_size.argtypes = [UP, ctypes.POINTER(sz)]
             lib.gmmfr_grouped_linear.argtypes = [UP] + [vp] * 5 + [sz, vp]
             lib.gmmfr_grouped_linear_grad_weight.argtypes = [UP] + [vp] * 5 + [sz, vp]
@@ -356,6 +364,18 @@ def gmmfr_linear(problem: LinearProblem, x, weight, bias, residual, out, workspa
                  stream=None) -> None:
     _check(load().gmmfr_linear(ctypes.byref(problem), x, weight, bias, residual, out, workspace, workspace_bytes,
                                stream))
+
+
+def gmmfr_lora_linear_workspace_size(problem: LoraProblem) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gmmfr_lora_linear_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def gmmfr_lora_linear(problem: LoraProblem, x, weight, bias, residual, lora_a, lora_b, lora_scale, adapter_ids, out, workspace,
+                      workspace_bytes, stream=None) -> None:
+    _check(load().gmmfr_lora_linear(ctypes.byref(problem), x, weight, bias, residual, lora_a, lora_b, lora_scale, adapter_ids,
+                                    out, workspace, workspace_bytes, stream))
 
 
 def gmmfr_grouped_linear_workspace_size(problem: GroupedProblem) -> int:
@@ -908,6 +928,83 @@ class Linear(_Handle):
         cx, cr, co = self._cx, self._cr, self._co
         cx.value, cr.value, co.value = xptr, rptr, out.data_ptr()
         st = self._fn(self._ref, cx, self._cw, self._cb, cr, co, ws[0], ws[1], ws[2])
+        if st:
+            _check(st)
+        return out
+
+
+class LoraLinear(_Handle):
+    """The dense product with low-rank adapters of many requests: ``lora(x, adapter_ids, residual=None)`` ->
+    act(x @ weight.T + bias + scale[a] * (x @ lora_a[a].T) @ lora_b[a].T) + residual, a the row's entry of ``adapter_ids``
+    [M] int32, -1 for a row without an adapter.
+
+    ``weight`` and ``bias`` as :class:`Linear` takes them (K, and the rows' strides, multiples of 8); ``lora_a`` [count, rank,
+    K] and ``lora_b`` [count, N or 2N, rank] bfloat16, ``scale`` [count] float32.  They are read where they are at each
+    call, so that a server changes an adapter by writing to its place."""
+
+    def __init__(self, weight, lora_a, lora_b, scale=None, bias=None, activation: str = "none", out_dtype=None):
+        import torch
+        super().__init__(weight.device)
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
+        self._out = torch.bfloat16 if out_dtype is None else out_dtype
+        if self._out not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
+        if weight.dim() != 2:
+            _refuse("weight", weight, "[N, K]", self._index)
+        rows, K = weight.shape
+        ldw = _rows(weight, "weight", None, K, torch.bfloat16, self._index)
+        if activation == "swiglu" and rows % 2:
+            raise ValueError(f"weight: {rows} rows; swiglu takes gate and up rows, an even number")
+        if lora_a.dim() != 3:
+            _refuse("lora_a", lora_a, "[count, rank, K]", self._index)
+        count, rank = lora_a.shape[:2]
+        aptr = _dense(lora_a, "lora_a", (count, rank, K), torch.bfloat16, self._index)
+        bptr = _dense(lora_b, "lora_b", (count, rows, rank), torch.bfloat16, self._index)
+        sptr = _dense(scale, "scale", (count,), torch.float32, self._index)
+        biasptr = _dense(bias, "bias", (rows,), torch.bfloat16, self._index)
+        self._keep = (weight, lora_a, lora_b, scale, bias)
+        self._K, self._N = K, rows // 2 if activation == "swiglu" else rows
+        self._p = LoraProblem(count=count, rank=rank)
+        self._q = q = self._p.linear
+        q.N, q.K, q.ldw, q.activation = self._N, K, ldw, ACTIVATIONS[activation]
+        q.out_type = DT_F32 if self._out == torch.float32 else DT_BF16
+        self._bf16, self._i32 = torch.bfloat16, torch.int32
+        self._ref, self._fn = ctypes.byref(self._p), self._entry("gmmfr_lora_linear")
+        self._cx, self._cr, self._ci, self._co = (ctypes.c_void_p() for _ in range(4))
+        self._cw, self._cb = ctypes.c_void_p(weight.data_ptr()), ctypes.c_void_p(biasptr)
+        self._factors = ctypes.c_void_p(aptr), ctypes.c_void_p(bptr), ctypes.c_void_p(sptr)
+        gmmfr_lora_linear_workspace_size(self._p)
+        self._seen, self._need = None, 0
+
+    def __call__(self, x, adapter_ids, residual=None, out=None, stream=None):
+        q, N, dev = self._q, self._N, self._index
+        if self._current() != dev:
+            return self._there(x, adapter_ids, residual, out, stream)
+        ldx = _rows(x, "x", None, self._K, self._bf16, dev)
+        M = x.shape[0]
+        if (M, ldx) != self._seen:
+            self._seen = None  # until the size is known to be taken: the problem holds what a refused call left in it
+            q.M, q.ldx = M, ldx
+            self._need = gmmfr_lora_linear_workspace_size(self._p)
+            self._seen = (M, ldx)
+        iptr = _dense(adapter_ids, "adapter_ids", (M,), self._i32, dev)
+        rptr, q.ld_residual = None, 0
+        if residual is not None:
+            q.ld_residual = _rows(residual, "residual", M, N, self._bf16, dev)
+            rptr = residual.data_ptr()
+        if out is None:
+            out = self._new((M, N), self._out, stream)
+            q.ld_out = 0
+        else:
+            q.ld_out = _rows(out, "out", M, N, self._out, dev)
+        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
+        ws = self._spaces.get(s)
+        if ws is None or ws[3] < self._need:
+            ws = self._grow(s, self._need, stream)
+        cx, cr, ci, co = self._cx, self._cr, self._ci, self._co
+        cx.value, cr.value, ci.value, co.value = x.data_ptr(), rptr, iptr, out.data_ptr()
+        st = self._fn(self._ref, cx, self._cw, self._cb, cr, *self._factors, ci, co, ws[0], ws[1], ws[2])
         if st:
             _check(st)
         return out

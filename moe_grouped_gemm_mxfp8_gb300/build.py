@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgmmfr.so")
 SOURCES = ["api.cu", "api_ops.cu", "kernels_aux.cu", "kernels_ffn.cu", "kernels_gate.cu", "kernels_gemm.cu",
-           "kernels_grouped.cu", "kernels_layer.cu", "kernels_linear.cu", "kernels_route.cu", "noalloc.cu"]
+           "kernels_grouped.cu", "kernels_layer.cu", "kernels_linear.cu", "kernels_lora.cu", "kernels_route.cu", "noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

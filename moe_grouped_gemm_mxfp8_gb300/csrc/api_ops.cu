@@ -211,6 +211,14 @@ bool odd_stride_w(const gmmfr_linear_problem* p) {
   return p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1) > 1 && stride_or(p->ldw, p->K) % 8;
 }
 
+// gmmfr_lora_linear's besides
+struct Adapters {
+  const gmmfr_lora_problem* problem;
+  const void *a, *b;
+  const float* scale;
+  const int32_t* ids;
+};
+
 struct LinearLayout {
   size_t x, w, total;
 };
@@ -224,6 +232,123 @@ LinearLayout linear_layout(const gmmfr_linear_problem* p) {
   if (p->unaligned || odd_stride_w(p)) off = align256(off + 2 * Kp * p->N * (p->activation == GMMFR_ACT_SWIGLU ? 2 : 1));
   L.total = off;
   return L;
+}
+
+gmmfr_status validate_lora(const gmmfr_lora_problem* p) {
+  if (!p) return fail(GMMFR_ERR_INVALID_ARG, "problem is NULL");
+  if (gmmfr_status st = validate_linear(&p->linear)) return st;
+  const gmmfr_linear_problem& q = p->linear;
+  if (q.K % 8 || q.ldx % 8 || q.ldw % 8)
+    return fail(GMMFR_ERR_INVALID_ARG, "K=%lld, ldx=%lld and ldw=%lld must be multiples of 8 with adapters", (long long)q.K,
+                (long long)q.ldx, (long long)q.ldw);
+  if (q.unaligned) return fail(GMMFR_ERR_INVALID_ARG, "unaligned must be 0 with adapters");
+  if (p->count < 1 || p->count >= (int64_t(1) << 24)) return fail(GMMFR_ERR_INVALID_ARG, "count=%lld out of range [1, 2^24)", (long long)p->count);
+  if (p->rank < 8 || p->rank > 256 || p->rank % 8)
+    return fail(GMMFR_ERR_INVALID_ARG, "rank=%lld is not a multiple of 8 in [8, 256]", (long long)p->rank);
+  return GMMFR_OK;
+}
+
+// The adapters' sums behind the error words
+size_t lora_ws_bytes(const gmmfr_lora_problem* p) { return align256(gmmfr::kHdrBytes + sizeof(float) * (size_t)p->linear.M * p->rank); }
+
+// gmmfr_linear, with adapters unless null (problem and their sizes checked)
+gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight, const void* bias, const void* residual,
+                        void* out, void* workspace, size_t workspace_bytes, void* stream, const Adapters* adapters) {
+  const gmmfr_linear_problem& p = *problem;
+  if (p.M == 0 || p.N == 0) return GMMFR_OK;
+  if (!x || !weight || !out) return fail(GMMFR_ERR_INVALID_ARG, "x, weight and out must be non-NULL when M, N > 0");
+  if (!aligned(x, 2) || !aligned(weight, 2) || !aligned(bias, 2) || !aligned(residual, 2) ||
+      !aligned(out, p.out_type == GMMFR_DT_F32 ? 4 : 2))
+    return fail(GMMFR_ERR_INVALID_ARG, "an input or output is not aligned to its element size");
+  const bool gated = p.activation == GMMFR_ACT_SWIGLU;
+  const int64_t rows_w = gated ? 2 * p.N : p.N;
+  const LinearLayout L = linear_layout(problem);
+  const bool copy_x = !aligned(x, 16) || odd_stride_x(problem), copy_w = !aligned(weight, 16) || odd_stride_w(problem);
+  if (!p.unaligned && ((copy_x && !odd_stride_x(problem)) || (copy_w && !odd_stride_w(problem))))
+    return fail(GMMFR_ERR_INVALID_ARG, "x or weight is off a 16-byte boundary: set problem.unaligned (and size the workspace with it)");
+  if (adapters) {
+    if (copy_x || copy_w) return fail(GMMFR_ERR_INVALID_ARG, "x and weight must be 16-byte aligned with adapters");
+    if (!adapters->a || !adapters->b || !adapters->ids)
+      return fail(GMMFR_ERR_INVALID_ARG, "lora_a, lora_b and adapter_ids must be non-NULL when M, N > 0");
+    if (!aligned(adapters->a, 16) || !aligned(adapters->b, 16)) return fail(GMMFR_ERR_INVALID_ARG, "lora_a and lora_b must be 16-byte aligned");
+    if (!aligned(adapters->scale, 4) || !aligned(adapters->ids, 4))
+      return fail(GMMFR_ERR_INVALID_ARG, "lora_scale or adapter_ids is not aligned to its element size");
+  }
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, adapters ? lora_ws_bytes(adapters->problem) : L.total)) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = gmmfr::sm_count();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  gmmfr::LinearParams lp{};
+  lp.x = static_cast<const __nv_bfloat16*>(x);
+  lp.w = static_cast<const __nv_bfloat16*>(weight);
+  lp.bias = static_cast<const __nv_bfloat16*>(bias);
+  lp.residual = static_cast<const __nv_bfloat16*>(residual);
+  lp.out = out;
+  lp.hdr = reinterpret_cast<uint32_t*>(ws);
+  lp.M = p.M;
+  lp.N = p.N;
+  lp.K = p.K;
+  lp.ldx = stride_or(p.ldx, p.K);
+  lp.ldw = stride_or(p.ldw, p.K);
+  lp.ldr = stride_or(p.ld_residual, p.N);
+  lp.ldo = stride_or(p.ld_out, p.N);
+  lp.timeout_ns = waits().limit_ns;
+  lp.test_stall = waits().stall;
+  lp.act = p.activation;
+  lp.out_f32 = p.out_type == GMMFR_DT_F32;
+  lp.vec_out = aligned(out, 16) && lp.ldo % (lp.out_f32 ? 4 : 8) == 0 && aligned(residual, 16) && lp.ldr % 8 == 0;
+  const int64_t Kp = cdiv(p.K, 8) * 8;
+  __nv_bfloat16 *x_copy = nullptr, *w_copy = nullptr;
+  if (copy_x) {
+    lp.x = x_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
+    lp.ldx = Kp;
+  }
+  if (copy_w) {
+    lp.w = w_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.w);
+    lp.ldw = Kp;
+  }
+  gmmfr::LoraParams sums{};
+  if (adapters) {
+    lp.lora_ids = adapters->ids;
+    lp.lora_b = static_cast<const __nv_bfloat16*>(adapters->b);
+    lp.lora_s = reinterpret_cast<float*>(ws + gmmfr::kHdrBytes);
+    lp.lora_count = (int32_t)adapters->problem->count;
+    lp.lora_rank = (int32_t)adapters->problem->rank;
+    lp.lora_rows = rows_w;
+    sums = {lp.x, static_cast<const __nv_bfloat16*>(adapters->a), adapters->scale, adapters->ids, lp.lora_s, p.M, p.K, lp.ldx,
+            lp.lora_count, lp.lora_rank, 0};
+  }
+  gmmfr::LinearParams parts[2] = {lp, lp};
+  gmmfr::LinearMaps maps[2];
+  gmmfr::plan_linear(parts[0], parts[1], sms);
+  for (int i = 0; i < 2; ++i) {  // what can be refused, before anything is launched
+    const gmmfr::LinearParams& q = parts[i];
+    if (q.M == 0 || q.form == gmmfr::kLinearDirect) continue;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const bool stream_form = q.form == gmmfr::kLinearStream;
+    if (!encode_rows(encode, &maps[i].x, q.x, q.M, q.K, q.ldx, stream_form ? q.bn : 128) ||
+        !encode_rows(encode, &maps[i].w, q.w, rows_w, q.K, q.ldw, stream_form ? (gated ? 64 : 128) : q.bn / 2))
+      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld ldw=%lld)", (long long)q.ldx, (long long)q.ldw);
+  }
+  if (x_copy) {
+    cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(x), x_copy, p.M, p.K, Kp, stride_or(p.ldx, p.K), sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "x copy launch");
+  }
+  if (w_copy) {
+    cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(weight), w_copy, rows_w, p.K, Kp, stride_or(p.ldw, p.K), sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
+  }
+  if (adapters) {
+    cudaError_t e = gmmfr::launch_lora_sums(sums, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "adapters' sums launch");
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (parts[i].M == 0) continue;
+    cudaError_t e = adapters ? gmmfr::launch_lora_linear(maps[i], parts[i], s) : gmmfr::launch_linear(maps[i], parts[i], s);
+    if (e != cudaSuccess) return cuda_fail(e, "linear launch");
+  }
+  return GMMFR_OK;
 }
 
 // ---------------------------------------------------------------- products grouped by expert
@@ -425,78 +550,22 @@ gmmfr_status gmmfr_linear_workspace_size(const gmmfr_linear_problem* problem, si
 gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight, const void* bias,
                           const void* residual, void* out, void* workspace, size_t workspace_bytes, void* stream) {
   if (gmmfr_status st = validate_linear(problem)) return st;
-  const gmmfr_linear_problem& p = *problem;
-  if (p.M == 0 || p.N == 0) return GMMFR_OK;
-  if (!x || !weight || !out) return fail(GMMFR_ERR_INVALID_ARG, "x, weight and out must be non-NULL when M, N > 0");
-  if (!aligned(x, 2) || !aligned(weight, 2) || !aligned(bias, 2) || !aligned(residual, 2) ||
-      !aligned(out, p.out_type == GMMFR_DT_F32 ? 4 : 2))
-    return fail(GMMFR_ERR_INVALID_ARG, "an input or output is not aligned to its element size");
-  const bool gated = p.activation == GMMFR_ACT_SWIGLU;
-  const int64_t rows_w = gated ? 2 * p.N : p.N;
-  const LinearLayout L = linear_layout(problem);
-  const bool copy_x = !aligned(x, 16) || odd_stride_x(problem), copy_w = !aligned(weight, 16) || odd_stride_w(problem);
-  if (!p.unaligned && ((copy_x && !odd_stride_x(problem)) || (copy_w && !odd_stride_w(problem))))
-    return fail(GMMFR_ERR_INVALID_ARG, "x or weight is off a 16-byte boundary: set problem.unaligned (and size the workspace with it)");
-  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, L.total)) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = gmmfr::sm_count();
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  gmmfr::LinearParams lp{};
-  lp.x = static_cast<const __nv_bfloat16*>(x);
-  lp.w = static_cast<const __nv_bfloat16*>(weight);
-  lp.bias = static_cast<const __nv_bfloat16*>(bias);
-  lp.residual = static_cast<const __nv_bfloat16*>(residual);
-  lp.out = out;
-  lp.hdr = reinterpret_cast<uint32_t*>(ws);
-  lp.M = p.M;
-  lp.N = p.N;
-  lp.K = p.K;
-  lp.ldx = stride_or(p.ldx, p.K);
-  lp.ldw = stride_or(p.ldw, p.K);
-  lp.ldr = stride_or(p.ld_residual, p.N);
-  lp.ldo = stride_or(p.ld_out, p.N);
-  lp.timeout_ns = waits().limit_ns;
-  lp.test_stall = waits().stall;
-  lp.act = p.activation;
-  lp.out_f32 = p.out_type == GMMFR_DT_F32;
-  lp.vec_out = aligned(out, 16) && lp.ldo % (lp.out_f32 ? 4 : 8) == 0 && aligned(residual, 16) && lp.ldr % 8 == 0;
-  const int64_t Kp = cdiv(p.K, 8) * 8;
-  __nv_bfloat16 *x_copy = nullptr, *w_copy = nullptr;
-  if (copy_x) {
-    lp.x = x_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
-    lp.ldx = Kp;
-  }
-  if (copy_w) {
-    lp.w = w_copy = reinterpret_cast<__nv_bfloat16*>(ws + L.w);
-    lp.ldw = Kp;
-  }
-  gmmfr::LinearParams parts[2] = {lp, lp};
-  gmmfr::LinearMaps maps[2];
-  gmmfr::plan_linear(parts[0], parts[1], sms);
-  for (int i = 0; i < 2; ++i) {  // what can be refused, before anything is launched
-    const gmmfr::LinearParams& q = parts[i];
-    if (q.M == 0 || q.form == gmmfr::kLinearDirect) continue;
-    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
-    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const bool stream_form = q.form == gmmfr::kLinearStream;
-    if (!encode_rows(encode, &maps[i].x, q.x, q.M, q.K, q.ldx, stream_form ? q.bn : 128) ||
-        !encode_rows(encode, &maps[i].w, q.w, rows_w, q.K, q.ldw, stream_form ? (gated ? 64 : 128) : q.bn / 2))
-      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld ldw=%lld)", (long long)q.ldx, (long long)q.ldw);
-  }
-  if (x_copy) {
-    cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(x), x_copy, p.M, p.K, Kp, stride_or(p.ldx, p.K), sms, s);
-    if (e != cudaSuccess) return cuda_fail(e, "x copy launch");
-  }
-  if (w_copy) {
-    cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(weight), w_copy, rows_w, p.K, Kp, stride_or(p.ldw, p.K), sms, s);
-    if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
-  }
-  for (int i = 0; i < 2; ++i) {
-    if (parts[i].M == 0) continue;
-    cudaError_t e = gmmfr::launch_linear(maps[i], parts[i], s);
-    if (e != cudaSuccess) return cuda_fail(e, "linear launch");
-  }
+  return run_linear(problem, x, weight, bias, residual, out, workspace, workspace_bytes, stream, nullptr);
+}
+
+gmmfr_status gmmfr_lora_linear_workspace_size(const gmmfr_lora_problem* problem, size_t* bytes) {
+  if (gmmfr_status st = validate_lora(problem)) return st;
+  if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = lora_ws_bytes(problem);
   return GMMFR_OK;
+}
+
+gmmfr_status gmmfr_lora_linear(const gmmfr_lora_problem* problem, const void* x, const void* weight, const void* bias,
+                               const void* residual, const void* lora_a, const void* lora_b, const float* lora_scale,
+                               const int32_t* adapter_ids, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (gmmfr_status st = validate_lora(problem)) return st;
+  const Adapters adapters{problem, lora_a, lora_b, lora_scale, adapter_ids};
+  return run_linear(&problem->linear, x, weight, bias, residual, out, workspace, workspace_bytes, stream, &adapters);
 }
 
 gmmfr_status gmmfr_grouped_linear_workspace_size(const gmmfr_grouped_problem* problem, size_t* bytes) {

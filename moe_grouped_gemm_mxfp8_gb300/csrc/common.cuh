@@ -33,6 +33,7 @@ constexpr uint32_t kErrBadGroupList = 1u;
 constexpr uint32_t kErrBadRowIndex = 2u;
 constexpr uint32_t kErrTimeout = 4u;
 constexpr uint32_t kErrBadExpertId = 8u;
+constexpr uint32_t kErrBadAdapterId = 16u;
 
 struct PrepParams {
   const uint8_t* x2;

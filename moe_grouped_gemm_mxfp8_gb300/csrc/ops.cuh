@@ -80,7 +80,7 @@ struct LayerParams {
 cudaError_t launch_layer(const LayerParams& p, int sms, cudaStream_t s);
 int64_t layer_image_bytes(bool mx, int64_t npad);
 
-// The dense product's forms (kernels_linear.cu), and the most rows of x for the first two.
+// The dense product's forms (linear_forms.cuh), and the most rows of x for the first two.
 enum { kLinearDirect = 0, kLinearStream = 1, kLinearPair = 2 };
 constexpr int kLinearDirectRows = 32;
 constexpr int kLinearStreamRows = 128;
@@ -100,6 +100,12 @@ struct LinearParams {
   int32_t KB, tiles_m, tiles_n, n_stages, kps, split, group_m, grid;
   int32_t beside;             // 1: started while the launch before it runs, which it has to outlast
   int32_t slot_base, slots;   // its error words, and how many the call has
+  // adapters
+  const int32_t* lora_ids;       // [M]: each row's adapter, -1 none
+  const __nv_bfloat16* lora_b;   // second factors [count, rows, rank]
+  float* lora_s;                 // [M, rank]: each row's sums of its adapter's first factor, scaled
+  int32_t lora_count, lora_rank;
+  int64_t lora_rows;
 };
 struct LinearMaps {
   CUtensorMap x, w;
@@ -107,6 +113,18 @@ struct LinearMaps {
 // Chooses p's form.  tail.M > 0: the last rows, taken out of p, are a second launch that runs beside p's.
 void plan_linear(LinearParams& p, LinearParams& tail, int sms);
 cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
+// The same with adapters, after their first factors' sums.
+struct LoraParams {
+  const __nv_bfloat16 *x, *a;  // [M, K], row stride ldx; first factors [count, rank, K]
+  const float* scale;          // [count] or null
+  const int32_t* ids;          // [M]
+  float* s;                    // [M, rank]
+  int64_t M, K, ldx;
+  int32_t count, rank;
+  int32_t split;               // launch_lora_sums' choice: CTAs of a cluster
+};
+cudaError_t launch_lora_sums(LoraParams p, int sms, cudaStream_t s);
+cudaError_t launch_lora_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
 cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t rows, int64_t K, int64_t Kp,
                                   int64_t ld, int sms, cudaStream_t s);
 
