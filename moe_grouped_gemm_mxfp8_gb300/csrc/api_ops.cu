@@ -65,6 +65,19 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, con
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [depth, rows, cols], dense, in boxes of one slice
+bool encode_slices(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const void* base, bool f32, int64_t depth, int64_t rows,
+                   int64_t cols, int box_cols, int box_rows) {
+  const int64_t size = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+  cuuint64_t strides[2] = {(cuuint64_t)(cols * size), (cuuint64_t)(rows * cols * size)};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- gate
 gmmfr_status validate_gate(const gmmfr_gate_problem* p) {
   if (!p) return fail(GMMFR_ERR_INVALID_ARG, "problem is NULL");
@@ -248,8 +261,25 @@ gmmfr_status validate_lora(const gmmfr_lora_problem* p) {
   return GMMFR_OK;
 }
 
-// The adapters' sums behind the error words
-size_t lora_ws_bytes(const gmmfr_lora_problem* p) { return align256(gmmfr::kHdrBytes + sizeof(float) * (size_t)p->linear.M * p->rank); }
+// Behind the error words: the adapters' sums, and for each 256 rows a list and what its scans found
+struct LoraLayout {
+  int64_t blocks, rows;
+  int32_t scans;
+  size_t sums, lists, flags, total;
+};
+LoraLayout lora_layout(const gmmfr_lora_problem* p) {
+  LoraLayout L{};
+  L.blocks = cdiv(p->linear.M, 256);
+  L.rows = p->linear.N * (p->linear.activation == GMMFR_ACT_SWIGLU ? 2 : 1);
+  // CTAs: 32 KB for each if all rows of a list had adapters of their own, some hundred in all
+  const int64_t most = std::min({p->linear.M, p->count, int64_t(256)}) * L.rows * p->rank * 2;
+  L.scans = (int32_t)std::clamp<int64_t>(most / 32768, 1, std::max<int64_t>(4, 512 / std::max<int64_t>(L.blocks, 1)));
+  L.sums = gmmfr::kHdrBytes;
+  L.lists = align256(L.sums + sizeof(float) * (size_t)p->linear.M * p->rank);
+  L.flags = align256(L.lists + sizeof(int32_t) * gmmfr::kLoraListInts * (size_t)L.blocks);
+  L.total = align256(L.flags + sizeof(uint32_t) * (size_t)L.scans * L.blocks);
+  return L;
+}
 
 // gmmfr_linear, with adapters unless null (problem and their sizes checked)
 gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, const void* weight, const void* bias, const void* residual,
@@ -274,7 +304,7 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     if (!aligned(adapters->scale, 4) || !aligned(adapters->ids, 4))
       return fail(GMMFR_ERR_INVALID_ARG, "lora_scale or adapter_ids is not aligned to its element size");
   }
-  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, adapters ? lora_ws_bytes(adapters->problem) : L.total)) return st;
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, adapters ? lora_layout(adapters->problem).total : L.total)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = gmmfr::sm_count();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -311,16 +341,34 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
   if (adapters) {
     lp.lora_ids = adapters->ids;
     lp.lora_b = static_cast<const __nv_bfloat16*>(adapters->b);
-    lp.lora_s = reinterpret_cast<float*>(ws + gmmfr::kHdrBytes);
+    const LoraLayout A = lora_layout(adapters->problem);
+    lp.lora_s = reinterpret_cast<float*>(ws + A.sums);
     lp.lora_count = (int32_t)adapters->problem->count;
     lp.lora_rank = (int32_t)adapters->problem->rank;
     lp.lora_rows = rows_w;
-    sums = {lp.x, static_cast<const __nv_bfloat16*>(adapters->a), adapters->scale, adapters->ids, lp.lora_s, p.M, p.K, lp.ldx,
-            lp.lora_count, lp.lora_rank, 0};
+    lp.lora_lists = reinterpret_cast<int32_t*>(ws + A.lists);
+    lp.lora_flags = reinterpret_cast<uint32_t*>(ws + A.flags);
+    lp.lora_scans = A.scans;
+    sums.x = lp.x;
+    sums.a = static_cast<const __nv_bfloat16*>(adapters->a);
+    sums.scale = adapters->scale;
+    sums.ids = adapters->ids;
+    sums.s = lp.lora_s;
+    sums.M = p.M;
+    sums.K = p.K;
+    sums.ldx = lp.ldx;
+    sums.count = lp.lora_count;
+    sums.rank = lp.lora_rank;
+    sums.b = lp.lora_b;
+    sums.rows = rows_w;
+    sums.lists = reinterpret_cast<int32_t*>(ws + A.lists);
+    sums.flags = reinterpret_cast<uint32_t*>(ws + A.flags);
   }
   gmmfr::LinearParams parts[2] = {lp, lp};
   gmmfr::LinearMaps maps[2];
   gmmfr::plan_linear(parts[0], parts[1], sms);
+  parts[0].lora_early = parts[1].M == 0;  // what runs beside starts with it, and does not wait
+  sums.scans = parts[0].form == gmmfr::kLinearDirect ? 0 : lp.lora_scans;
   for (int i = 0; i < 2; ++i) {  // what can be refused, before anything is launched
     const gmmfr::LinearParams& q = parts[i];
     if (q.M == 0 || q.form == gmmfr::kLinearDirect) continue;
@@ -330,6 +378,9 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     if (!encode_rows(encode, &maps[i].x, q.x, q.M, q.K, q.ldx, stream_form ? q.bn : 128) ||
         !encode_rows(encode, &maps[i].w, q.w, rows_w, q.K, q.ldw, stream_form ? (gated ? 64 : 128) : q.bn / 2))
       return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld ldw=%lld)", (long long)q.ldx, (long long)q.ldw);
+    if (adapters && !encode_slices(encode, &maps[i].b, q.lora_b, false, q.lora_count, q.lora_rows, q.lora_rank, 64,
+                                   stream_form ? (gated ? 64 : 128) : q.bn / 2))
+      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (adapters)");
   }
   if (x_copy) {
     cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(x), x_copy, p.M, p.K, Kp, stride_or(p.ldx, p.K), sms, s);
@@ -372,19 +423,6 @@ gmmfr_status validate_grouped(const gmmfr_grouped_problem* p) {
   if (p->zero_rest != 0 && p->zero_rest != 1) return fail(GMMFR_ERR_INVALID_ARG, "zero_rest must be 0 or 1");
   if (p->accumulate != 0 && p->accumulate != 1) return fail(GMMFR_ERR_INVALID_ARG, "accumulate must be 0 or 1");
   return GMMFR_OK;
-}
-
-// [depth, rows, cols], dense, in boxes of one slice
-bool encode_slices(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const void* base, bool f32, int64_t depth, int64_t rows,
-                   int64_t cols, int box_cols, int box_rows) {
-  const int64_t size = f32 ? 4 : 2;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
-  cuuint64_t strides[2] = {(cuuint64_t)(cols * size), (cuuint64_t)(rows * cols * size)};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -556,7 +594,7 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
 gmmfr_status gmmfr_lora_linear_workspace_size(const gmmfr_lora_problem* problem, size_t* bytes) {
   if (gmmfr_status st = validate_lora(problem)) return st;
   if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = lora_ws_bytes(problem);
+  *bytes = lora_layout(problem).total;
   return GMMFR_OK;
 }
 

@@ -165,6 +165,8 @@ void plan_linear(LinearParams& p, LinearParams& tail, int sms) {
     if (tail.lora_ids) {
       tail.lora_ids += at;
       tail.lora_s += at * tail.lora_rank;
+      tail.lora_lists += at / 256 * kLoraListInts;
+      tail.lora_flags += at / 256 * tail.lora_scans;
     }
     tail.beside = 1;
   }

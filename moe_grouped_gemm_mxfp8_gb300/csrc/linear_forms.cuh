@@ -19,6 +19,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "epilogue.cuh"
 #include "ops.cuh"
@@ -55,6 +56,10 @@ constexpr int kStreamKps = 2;  // K blocks per stage: 0.33 us per stage where a 
 constexpr int kStreamArena = 220 * 1024;  // the ring, and the partial sums unless they take its place
 constexpr int kStreamSmem = kStreamArena + kStreamBars * 8 + 32 + 1024;
 static_assert(kStreamSmem <= 232448, "shared memory budget");
+
+// ---- adapters
+constexpr int kLoraWarp = kThreads / 32;  // two warps more
+constexpr int kLoraThreads = kThreads + 64;
 
 }  // namespace lin
 
@@ -171,21 +176,41 @@ __device__ __forceinline__ void add_bias32(float bias, float (&v)[32], float* ro
   __syncwarp();
 }
 
+// kLora: the activation is a choice at run time (a third of the kernels; the plain product's are compiled for each)
+template <bool kBf16, int kN>
+__device__ __forceinline__ void activate_all(int act, float (&v)[kN]) {
+  auto all = [&](auto a) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = activate<kBf16>(decltype(a)::value, v[j]);
+  };
+  switch (act) {
+    case GMMFR_ACT_RELU: return all(std::integral_constant<int, GMMFR_ACT_RELU>{});
+    case GMMFR_ACT_GELU: return all(std::integral_constant<int, GMMFR_ACT_GELU>{});
+    case GMMFR_ACT_GELU_TANH: return all(std::integral_constant<int, GMMFR_ACT_GELU_TANH>{});
+    case GMMFR_ACT_SILU: return all(std::integral_constant<int, GMMFR_ACT_SILU>{});
+    default: return;
+  }
+}
+
 // What the adapter of row m adds to columns n.. (rows n.. of the second factors) of y before the activation: the FP32
 // products of the row's first-factor sums, scaled already, with `cols` rows of the adapter's second factor.
-template <int kCols>
+// kNotFinite: of those of its elements alone that are infinite or NaN.
+template <int kCols, bool kNotFinite = false>
 __device__ __forceinline__ void add_adapter(const LinearParams& p, int adapter, int64_t m, int64_t n, int cols, float (&f)[kCols]) {
   if ((uint32_t)adapter >= (uint32_t)p.lora_count) return;
   const float* s = p.lora_s + m * p.lora_rank;
   const __nv_bfloat16* b = p.lora_b + ((int64_t)adapter * p.lora_rows + n) * p.lora_rank;
+  auto add = [](float& f, float s, float b) {
+    if (!kNotFinite || !isfinite(b)) f += s * b;
+  };
   for (int j = 0; j < p.lora_rank; j += 8) {
     const float4 lo = *reinterpret_cast<const float4*>(s + j), hi = *reinterpret_cast<const float4*>(s + j + 4);
 #pragma unroll
     for (int k = 0; k < kCols; ++k) {
       if (k < cols) {
         const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)k * p.lora_rank + j));
-        f[k] += lo.x * bf16_lo(w.x) + lo.y * bf16_hi(w.x) + lo.z * bf16_lo(w.y) + lo.w * bf16_hi(w.y) + hi.x * bf16_lo(w.z) +
-                hi.y * bf16_hi(w.z) + hi.z * bf16_lo(w.w) + hi.w * bf16_hi(w.w);
+        add(f[k], lo.x, bf16_lo(w.x)), add(f[k], lo.y, bf16_hi(w.x)), add(f[k], lo.z, bf16_lo(w.y)), add(f[k], lo.w, bf16_hi(w.y));
+        add(f[k], hi.x, bf16_lo(w.z)), add(f[k], hi.y, bf16_hi(w.z)), add(f[k], hi.z, bf16_lo(w.w)), add(f[k], hi.w, bf16_hi(w.w));
       }
     }
   }
@@ -196,6 +221,157 @@ __device__ __forceinline__ int adapter_of(const LinearParams& p, int64_t m, uint
   const int a = p.lora_ids[m];
   if (a < -1 || a >= p.lora_count) atomicOr(err, kErrBadAdapterId);
   return a;
+}
+
+// ---------------------------------------------------------------- adapters in the stream and pair form
+// The second factors join a tile's sum as further K blocks: for each adapter that any of the tile's rows has, and each 32 of
+// its ranks, a block whose W rows are the second factor's (by TMA) and whose x rows are the rows' sums, zeros in the rows of
+// other adapters.  Two warps of their own write those x rows and hand the stage over.  A sum enters as two BF16 numbers, the
+// first truncated, so that it is off by 2^-17 at most; they take the halves of a 128-byte row, both against the same 32
+// ranks.  The lists of the adapters of 256 rows come with the sums.
+// A zero does not keep an infinity or NaN of another adapter's factor out of a row.  The lists say whether their factors have
+// any: the warps then put zeros in their place where a factor has landed, and from then on the CTA's epilogues add,
+// row by row, what those elements give the rows whose adapter has them.
+struct AdapterShared {
+  uint64_t loaded[lin::kPairMaxStages];  // a stage's second factors have landed in this CTA
+  uint64_t built[lin::kPairMaxStages];   // in the CTA that issues the products: a stage is ready
+  int32_t not_finite;                    // a factor of this cluster's tiles was not finite
+};
+
+__device__ __forceinline__ void init_adapters(AdapterShared& a, int n_stages, int built_by) {
+  for (int s = 0; s < n_stages; ++s) {
+    ptx::mbar_init(ptx::smem_u32(&a.loaded[s]), 1);
+    ptx::mbar_init(ptx::smem_u32(&a.built[s]), 2 * built_by);
+  }
+  a.not_finite = 0;
+}
+
+// A list in a warp's registers: entry 32 k + lane in e[k].
+struct AdapterList {
+  int n, e[8];
+  __device__ __forceinline__ void load(const LinearParams& p, int64_t block) {
+    const int32_t* list = p.lora_lists + block * kLoraListInts;
+    n = list[0];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = 32 * k + (int)(threadIdx.x & 31) < n ? list[4 + 32 * k + (threadIdx.x & 31)] : 0;
+  }
+  __device__ __forceinline__ int at(int d) const {
+    int v = e[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (d >> 5 == k) v = e[k];
+    return __shfl_sync(0xffffffffu, v, d & 31);
+  }
+};
+
+// Ranks 32 c .. of a row's sums as pairs of BF16 numbers: the leading bits, and what they leave; zeros past the rank.
+__device__ __forceinline__ void split_sums(const float* s, int left, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 v = 4 * j < left ? *reinterpret_cast<const float4*>(s + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+    float r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      h[k] = __float_as_uint(f[k]) & 0xffff0000u;
+      r[k] = isfinite(f[k]) ? f[k] - __uint_as_float(h[k]) : 0.f;
+    }
+    hi[2 * j] = h[0] >> 16 | h[1];
+    hi[2 * j + 1] = h[2] >> 16 | h[3];
+    lo[2 * j] = pack_bf16(r[0], r[1]);
+    lo[2 * j + 1] = pack_bf16(r[2], r[3]);
+  }
+}
+
+// Zeros in place of what is not finite in the first 16 steps elements of rows r0 .. r1 - 1, of 128 bytes each (128-byte
+// swizzle).
+__device__ __noinline__ void drop_not_finite(uint8_t* at, int r0, int r1, int steps) {
+  for (int r = r0 + (int)(threadIdx.x & 31); r < r1; r += 32)
+    for (int c = 0; c < 2 * steps; ++c) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(at + r * 128 + ((c ^ (r & 7)) << 4));
+      for (int k = 0; k < 4; ++k) {
+        if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
+        if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu;
+      }
+    }
+}
+
+// A CTA's adapter warps (`half` 0 and 1) through a tile's blocks u0 .. u1 - 1, kKps to a stage, from `stage` on (a stage whose
+// factors have landed is free).  x_at, w_at: where a block's rows of x and of W lie in its stage; x_rows (128 at most) of
+// them are written, which are p's from row0 on; `to`: the CTA that issues the products, or -1.
+template <int kKps>
+__device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterShared& a, uint8_t* smem, int stage_bytes, int block_bytes,
+                                               int n_stages, int x_at, int x_rows, int w_at, int w_rows, int64_t block, int64_t row0,
+                                               int half, const AdapterList& list, int u0, int u1, int to, int& stage,
+                                               uint32_t& loaded_bits, const Ctl& ctl) {
+  if (u0 >= u1) return true;
+  const int lane = threadIdx.x & 31, ranks = p.lora_rank;
+  uint32_t flag = 0;
+  for (int g = lane; g < p.lora_scans; g += 32) flag |= p.lora_flags[block * p.lora_scans + g];
+  const bool found = __any_sync(0xffffffffu, flag);
+  int own[2];  // the adapters of this lane's rows
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t m = row0 + (2 * half + i) * 32 + lane;
+    own[i] = m < p.M ? p.lora_ids[m] : -1;
+    if ((uint32_t)own[i] >= (uint32_t)p.lora_count) own[i] = -1;
+  }
+  uint32_t hi[2][16], lo[2][16];
+  int c = u0 / list.n, d = u0 - c * list.n, c_held = -1;
+  for (int u = u0; u < u1; u += kKps) {
+    uint8_t* sb = smem + stage * stage_bytes;
+#pragma unroll
+    for (int h = 0; h < kKps; ++h) {
+      if (u + h >= u1) break;
+      const int steps = ranks - 32 * c > 16 ? 2 : 1;
+      if (c != c_held) {
+        c_held = c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          split_sums(p.lora_s + (row0 + (2 * half + i) * 32 + lane) * ranks + 32 * c, own[i] >= 0 ? ranks - 32 * c : 0, hi[i], lo[i]);
+      }
+      const int adapter = list.at(d);
+      if (h == 0) {
+        if (!warp_wait_quick(ptx::smem_u32(&a.loaded[stage]), loaded_bits >> stage & 1, ctl)) return false;
+        loaded_bits ^= 1u << stage;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 32 * (2 * half + i) + lane;
+        if (row >= x_rows) continue;
+        uint8_t* at = sb + h * block_bytes + x_at + row * 128;
+        const uint32_t keep = own[i] == adapter ? 0xffffffffu : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= 2 * steps) break;
+          *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) =
+              make_uint4(hi[i][4 * k] & keep, hi[i][4 * k + 1] & keep, hi[i][4 * k + 2] & keep, hi[i][4 * k + 3] & keep);
+          *reinterpret_cast<uint4*>(at + (((4 + k) ^ (row & 7)) << 4)) =
+              make_uint4(lo[i][4 * k] & keep, lo[i][4 * k + 1] & keep, lo[i][4 * k + 2] & keep, lo[i][4 * k + 3] & keep);
+        }
+      }
+      if (found) drop_not_finite(sb + h * block_bytes + w_at, half * w_rows / 2, (half + 1) * w_rows / 2, steps);
+      if (++d == list.n) {
+        d = 0;
+        ++c;
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    if (found) {
+      const uint32_t at = ptx::smem_u32(&a.not_finite);
+      if (lane < p.split) ptx::st_cluster_u32(p.split > 1 ? ptx::map_to_rank(at, lane) : at, 1u);
+      __threadfence();
+    }
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t bar = ptx::smem_u32(&a.built[stage]);
+      if (to >= 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, to));
+      else ptx::mbar_arrive(bar);
+    }
+    if (++stage == n_stages) stage = 0;
+  }
+  return true;
 }
 
 }  // namespace
@@ -356,7 +532,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
 // Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
 // tiles in flight share rows of x and of W in L2.
 template <int kAct, int kKps, bool kF32, bool kLora>
-__global__ void __launch_bounds__(lin::kPairThreads, 1)
+__global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   extern __shared__ uint8_t smem_raw[];
@@ -377,6 +553,8 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
   const int block_bytes = lin::kTileBytes + BN * 64, stage_bytes = kKps * block_bytes, n_stages = p.n_stages;
   const int KB = (p.KB + kKps - 1) / kKps;
   const int per = kF32 ? lin::kChunk<kGated> / kKps : KB;  // stages to an accumulator
+  [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kPairTurnOff + 8 * 32 * 33 * 4);
+  [[maybe_unused]] const int rank_chunks = (p.lora_rank + 31) / 32;  // kLora: blocks of an adapter
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
@@ -387,6 +565,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
       ptx::mbar_init(ptx::smem_u32(&acce[b]), 16);
     }
+    if constexpr (kLora) init_adapters(ad, n_stages, 2);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0;
     *s_err = 0;
@@ -406,7 +585,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
   const uint32_t smem_base = ptx::smem_u32(smem);
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
   const int tiles = p.tiles_m * p.tiles_n;
-  ptx::griddep_wait();
+  if (!kLora || !p.lora_early) ptx::griddep_wait();  // lora_early: who reads the sums or lists waits before it does
   ptx::griddep_launch_dependents();
 
   auto tile_at = [&](int t, int& mt, int& nt) {
@@ -447,6 +626,43 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
           sb = smem_base;
         }
       }
+      if constexpr (kLora) {
+        if (!ok) break;
+        if (t == first && p.lora_early) ptx::griddep_wait();
+        AdapterList list;
+        list.load(p, mt);
+        const int units = list.n * rank_chunks;
+        for (int u = 0, c = 0, d = 0; u < units; u += kKps) {
+          if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t lb = ptx::smem_u32(&ad.loaded[stage]);
+          int adapter[kKps], rank0[kKps];
+#pragma unroll
+          for (int i = 0; i < kKps; ++i) {
+            rank0[i] = 32 * c;
+            adapter[i] = list.at(d);
+            if (++d == list.n) {
+              d = 0;
+              ++c;
+            }
+          }
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(lb, min(kKps, units - u) * BN * 64);
+#pragma unroll
+            for (int i = 0; i < kKps; ++i)
+              if (u + i < units)
+                ptx::tma_load_3d(sb + i * block_bytes + lin::kTileBytes, &maps.b, rank0[i], yn, adapter[i], lb, pol);
+          }
+          sb += stage_bytes;
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+            sb = smem_base;
+          }
+        }
+      }
     }
     // the last stages: released once their products are done, so that no load is in flight at exit
     for (int s = 0; ok && s < n_stages; ++s) {
@@ -456,7 +672,9 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
         phase ^= 1;
       }
     }
-    if (!ok && rank == 0) {  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
+    if (kLora && !ok) {
+      let_loads_land();
+    } else if (!ok && rank == 0) {  // aborted: let what is in flight land (both CTAs' loads count on rank 0's barriers)
       for (int s = 0; s < n_stages; ++s)
         if (!wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1)) break;  // rank 1 gave up before its load
     } else if (!ok) {
@@ -475,6 +693,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       int stage = 0;
       uint32_t phase = 0, lo = lo0;
       int acc_i = 0;
+      [[maybe_unused]] uint32_t full_bits = 0, built_bits = 0;  // kLora: a barrier's phase by its own uses
       bool ok = true;
       for (int t = first, left = KB; ok && t < tiles; t += left == KB ? pairs : 0) {  // left: stages left of the tile
         const int buf = acc_i & 1, n = kF32 ? min(per, left) : KB;
@@ -483,10 +702,11 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
         const uint32_t d = tmem_base + buf * 256;
         uint32_t accumulate = 0;
         for (int kb = 0; kb < n; ++kb) {
-          if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
+          if (!warp_wait_quick(full0 + 8 * stage, kLora ? full_bits >> stage & 1 : phase, ctl)) {
             ok = false;
             break;
           }
+          if (kLora) full_bits ^= 1u << stage;
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
 #pragma unroll
@@ -496,7 +716,7 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
                 ptx::tc_mma_f16_pair_lo(d, lo + i * lo_block + 2 * q, lo + i * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi,
                                         idesc, i + q > 0 ? 1u : accumulate);
             ptx::tc_commit_pair(empty0 + 8 * stage);
-            if (kb == n - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+            if (kb == n - 1 && !(kLora && n == left)) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
           }
           accumulate = 1;
           lo += lo_step;
@@ -506,6 +726,38 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
             lo = lo0;
           }
         }
+        if constexpr (kLora) {
+          if (ok && n == left) {  // the tile's last accumulator takes the adapters
+            if (t == first && p.lora_early) ptx::griddep_wait();
+            int mt, nt;
+            tile_at(t, mt, nt);
+            const int count = p.lora_lists[(int64_t)mt * kLoraListInts], units = count * rank_chunks;
+            for (int u = 0; u < units; u += kKps) {
+              if (!(ok = __all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&ad.built[stage]), built_bits >> stage & 1, ctl)))) break;
+              built_bits ^= 1u << stage;
+              ptx::tc_fence_after();
+              if (ptx::elect_one()) {
+                for (int i = 0; i < kKps && u + i < units; ++i) {
+                  const int steps = u + i >= count * (rank_chunks - 1) ? (p.lora_rank - 32 * rank_chunks + 47) / 16 : 2;
+                  const uint32_t xa = lo + i * lo_block, wb = xa + (lin::kTileBytes >> 4);
+                  for (int q = 0; q < steps; ++q) {
+                    ptx::tc_mma_f16_pair_lo(d, xa + 2 * q, wb + 2 * q, desc_hi, idesc, 1u);
+                    ptx::tc_mma_f16_pair_lo(d, xa + 4 + 2 * q, wb + 2 * q, desc_hi, idesc, 1u);
+                  }
+                }
+                ptx::tc_commit_pair(empty0 + 8 * stage);
+              }
+              lo += lo_step;
+              if (++stage == n_stages) {
+                stage = 0;
+                phase ^= 1;
+                lo = lo0;
+              }
+            }
+            if (!ok) break;
+            if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+          }
+        }
         ++acc_i;
         if (kF32) left = left > n ? left - n : KB;
       }
@@ -513,6 +765,23 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       wait_bar_drain(ptx::smem_u32(drain), 0);
     }
     __syncwarp();
+  } else if (kLora && warp >= lin::kLoraWarp) {
+    if constexpr (kLora) {
+      const int half = warp - lin::kLoraWarp;
+      int stage = 0;
+      uint32_t loaded_bits = 0;
+      if (p.lora_early) ptx::griddep_wait();
+      for (int t = first; t < tiles; t += pairs) {
+        int mt, nt;
+        tile_at(t, mt, nt);
+        AdapterList list;
+        list.load(p, mt);
+        stage = (stage + KB) % n_stages;
+        if (!build_adapters<kKps>(p, ad, smem, stage_bytes, block_bytes, n_stages, 0, 128, lin::kTileBytes, BN / 2, mt,
+                                  (int64_t)mt * 256 + 128 * rank, half, list, 0, list.n * rank_chunks, 0, stage, loaded_bits, ctl))
+          break;
+      }
+    }
   } else {
     // two warps per TMEM lane quadrant, taking its 32-column chunks in turn
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -553,11 +822,12 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
       // chunk i's values v (gated: and up values u), biased, activated, with the residual, to memory
       auto finish = [&](int i, float (&v)[32], float (&u)[32]) {
         if constexpr (kLora) {
+          if (nt == 0 && i == 0 && half == 0 && m0 + lane < p.M) adapter_of(p, m0 + lane, s_err);  // reported once
           const int64_t n = n0 + 32 * half + 64 * i;
-          if (m0 + lane < p.M && n < p.N) {
-            const int a = adapter_of(p, m0 + lane, s_err), left = (int)min(p.N - n, (int64_t)32);
-            add_adapter(p, a, m0 + lane, n, left, v);
-            if constexpr (kGated) add_adapter(p, a, m0 + lane, p.N + n, left, u);
+          if (*(volatile int32_t*)&ad.not_finite && m0 + lane < p.M && n < p.N) {
+            const int a = p.lora_ids[m0 + lane], left = (int)min(p.N - n, (int64_t)32);
+            add_adapter<32, true>(p, a, m0 + lane, n, left, v);
+            if constexpr (kGated) add_adapter<32, true>(p, a, m0 + lane, p.N + n, left, u);
           }
           __syncwarp();
         }
@@ -567,8 +837,12 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = silu<!kF32>(v[j]) * u[j];
         } else {
+          if constexpr (kLora) {
+            activate_all<!kF32>(p.act, v);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = activate<!kF32>(kAct, v[j]);
+            for (int j = 0; j < 32; ++j) v[j] = activate<!kF32>(kAct, v[j]);
+          }
         }
         store_tile32<kF32>(p, m0, n0 + 32 * half + 64 * i, v, turn);
       };
@@ -647,11 +921,11 @@ __global__ void __launch_bounds__(lin::kPairThreads, 1)
 // Cluster c takes the tiles c, c + clusters, ...; its CTA of rank r the K blocks [KB r / S, KB (r + 1) / S).
 // A tile is 128 rows of W; with the gated activation 64 gate rows and the 64 up rows of the same columns.
 template <int kAct, bool kF32, bool kLora>
-__global__ void __launch_bounds__(lin::kThreads, 1)
+__global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kThreads, 1)
     linear_stream_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   constexpr int kCols = kGated ? 64 : 128;  // columns of y per tile
-  constexpr int kEpi = lin::kThreads - 64, kKps = lin::kStreamKps;
+  constexpr int kEpi = lin::kThreads - 64, kKps = lin::kStreamKps;  // kEpi: the epilogue's threads
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::kStreamArena);
@@ -673,6 +947,8 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   const int clusters = gridDim.x / S, first = blockIdx.x / S, tiles = p.tiles_n;
   // [T][128]: in the ring's place when no tile follows, whose loads would write there
   float* part = reinterpret_cast<float*>(smem + (tiles <= clusters ? 0 : n_stages * stage_bytes));
+  [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kStreamArena + lin::kStreamBars * 8 + 32);
+  [[maybe_unused]] const int rank_chunks = (p.lora_rank + 31) / 32;  // kLora: blocks of an adapter
   // one accumulator, or two in turn for the chunks of FP32 results
   const uint32_t acc_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128), tmem_cols = kF32 ? 2 * acc_cols : acc_cols;
   auto acc_of = [&](uint32_t i) { return kF32 ? i & 1 : 0; };
@@ -687,6 +963,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
       ptx::mbar_init(ptx::smem_u32(&acce[b]), 8);
     }
+    if constexpr (kLora) init_adapters(ad, n_stages, 1);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     ptx::mbar_init(ptx::smem_u32(pready), S);
     ptx::mbar_init(ptx::smem_u32(pfree), S);
@@ -711,7 +988,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
   const int per = kF32 ? lin::kChunk<kGated> / kKps : kb1 - kb0;  // stages to an accumulator
   // Beside the pair form: this kernel starts when every CTA of that one has seen its predecessors end, and may not end
   // before it does.
-  if (!kLora && !p.beside) ptx::griddep_wait();  // kLora: as in the direct form, the epilogue waits
+  if (!kLora && !p.beside) ptx::griddep_wait();  // kLora: as in the direct form, who reads the sums or lists waits
   ptx::griddep_launch_dependents();
 
   if (warp == 0) {
@@ -746,6 +1023,46 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
           sb = smem_base;
         }
       }
+      if constexpr (kLora) {  // one list serves all tiles
+        if (!ok) break;
+        if (t == first && !p.beside) ptx::griddep_wait();
+        AdapterList list;
+        list.load(p, 0);
+        const int n = list.n, u0 = n * rank_chunks * (int)rank / S, u1 = n * rank_chunks * ((int)rank + 1) / S;
+        for (int u = u0, c = u0 < u1 ? u0 / n : 0, d = u0 - c * n; u < u1; u += kKps) {
+          if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t lb = ptx::smem_u32(&ad.loaded[stage]);
+          int adapter[kKps], rank0[kKps];
+#pragma unroll
+          for (int h = 0; h < kKps; ++h) {
+            rank0[h] = 32 * c;
+            adapter[h] = list.at(d);
+            if (++d == n) {
+              d = 0;
+              ++c;
+            }
+          }
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(lb, min(kKps, u1 - u) * lin::kTileBytes);
+#pragma unroll
+            for (int h = 0; h < kKps; ++h)
+              if (u + h < u1) {
+                const uint32_t to = sb + h * block_bytes;
+                ptx::tma_load_3d(to, &maps.b, rank0[h], y, adapter[h], lb, pol_w);
+                if constexpr (kGated) ptx::tma_load_3d(to + 64 * 128, &maps.b, rank0[h], y_up, adapter[h], lb, pol_w);
+              }
+          }
+          sb += stage_bytes;
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+            sb = smem_base;
+          }
+        }
+      }
     }
     for (int s = 0; ok && s < n_stages; ++s) {  // no load is in flight at exit
       ok = warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
@@ -754,7 +1071,8 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
         phase ^= 1;
       }
     }
-    if (!ok)  // aborted: let what is in flight land
+    if (kLora && !ok) let_loads_land();
+    else if (!ok)  // aborted: let what is in flight land
       for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
     __syncwarp();
   } else if (warp == 1) {
@@ -765,6 +1083,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
     const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
     int stage = 0;
     uint32_t phase = 0, acc_i = 0, lo = lo0;
+    [[maybe_unused]] uint32_t full_bits = 0, built_bits = 0;  // kLora: a barrier's phase by its own uses
     bool ok = true;
     for (int t = first, k0 = kb0; ok && t < tiles; t += k0 == kb0 ? clusters : 0) {
       const int k1 = kF32 ? min(k0 + per, kb1) : kb1;
@@ -773,10 +1092,11 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
       const uint32_t d = tmem_base + acc_of(acc_i) * acc_cols;
       uint32_t accumulate = 0;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
+        if (!warp_wait_quick(full0 + 8 * stage, kLora ? full_bits >> stage & 1 : phase, ctl)) {
           ok = false;
           break;
         }
+        if (kLora) full_bits ^= 1u << stage;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
 #pragma unroll
@@ -786,7 +1106,7 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
               ptx::tc_mma_f16_lo(d, lo + h * lo_block + 2 * q, lo + h * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi, idesc,
                                  h + q > 0 ? 1u : accumulate);
           ptx::tc_commit(empty0 + 8 * stage);
-          if (kb == k1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
+          if (kb == k1 - 1 && !(kLora && k1 == kb1)) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
         }
         accumulate = 1;
         lo += lo_step;
@@ -796,18 +1116,63 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
           lo = lo0;
         }
       }
+      if constexpr (kLora) {
+        if (ok && k1 == kb1) {  // the tile's last accumulator takes the adapters
+          if (t == first && !p.beside) ptx::griddep_wait();
+          const int count = p.lora_lists[0], u0 = count * rank_chunks * (int)rank / S, u1 = count * rank_chunks * ((int)rank + 1) / S;
+          for (int u = u0; u < u1; u += kKps) {
+            if (!(ok = warp_wait_quick(ptx::smem_u32(&ad.built[stage]), built_bits >> stage & 1, ctl))) break;
+            built_bits ^= 1u << stage;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+              for (int h = 0; h < kKps && u + h < u1; ++h) {
+                const int steps = u + h >= count * (rank_chunks - 1) ? (p.lora_rank - 32 * rank_chunks + 47) / 16 : 2;
+                const uint32_t wa = lo + h * lo_block, xb = wa + (lin::kTileBytes >> 4);
+                for (int q = 0; q < steps; ++q) {
+                  ptx::tc_mma_f16_lo(d, wa + 2 * q, xb + 2 * q, desc_hi, idesc, 1u);
+                  ptx::tc_mma_f16_lo(d, wa + 2 * q, xb + 4 + 2 * q, desc_hi, idesc, 1u);
+                }
+              }
+              ptx::tc_commit(empty0 + 8 * stage);
+            }
+            lo += lo_step;
+            if (++stage == n_stages) {
+              stage = 0;
+              phase ^= 1;
+              lo = lo0;
+            }
+          }
+          if (!ok) break;
+          if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
+        }
+      }
       ++acc_i;
       if (kF32) k0 = k1 == kb1 ? kb0 : k1;
     }
     if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(drain));
     wait_bar_drain(ptx::smem_u32(drain), 0);
     __syncwarp();
+  } else if (kLora && warp >= lin::kLoraWarp) {
+    if constexpr (kLora) {
+      const int half = warp - lin::kLoraWarp;
+      int stage = 0;
+      uint32_t loaded_bits = 0;
+      if (!p.beside) ptx::griddep_wait();
+      AdapterList list;
+      list.load(p, 0);
+      for (int t = first; t < tiles; t += clusters) {
+        stage = (stage + kb1 - kb0) % n_stages;
+        if (!build_adapters<kKps>(p, ad, smem, stage_bytes, block_bytes, n_stages, lin::kTileBytes, npad, 0, 128, 0, 0, half, list,
+                                  list.n * rank_chunks * (int)rank / S, list.n * rank_chunks * ((int)rank + 1) / S, -1, stage, loaded_bits,
+                                  ctl))
+          break;
+      }
+    }
   } else {
     const int q = warp & 3, ep = threadIdx.x - 64;
     const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
     const int c_first = (warp - 2) / 4 * 16;  // every other 16 rows of x from there
     uint32_t ph = 0, acc_i = 0;
-    if (kLora && !p.beside) ptx::griddep_wait();
     auto wait_full = [&]() {
       const bool ok = warp_wait_quick(ptx::smem_u32(&accf[acc_of(acc_i)]), phase_of(acc_i), ctl);
       ptx::tc_fence_after();
@@ -915,14 +1280,20 @@ __global__ void __launch_bounds__(lin::kThreads, 1)
           float f[4] = {v[w].x + bias[0], v[w].y + bias[1], v[w].z + bias[2], v[w].w + bias[3]};
           float g[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
           if constexpr (kLora) {
-            const int a = adapter_of(p, tok, s_err);
-            add_adapter(p, a, tok, n, cols, f);
-            if constexpr (kGated) add_adapter(p, a, tok, p.N + n, cols, g);
+            if (t == 0 && c == 0) adapter_of(p, tok, s_err);  // reported once
+            if (*(volatile int32_t*)&ad.not_finite) {
+              add_adapter<4, true>(p, p.lora_ids[tok], tok, n, cols, f);
+              if constexpr (kGated) add_adapter<4, true>(p, p.lora_ids[tok], tok, p.N + n, cols, g);
+            }
           }
+          if constexpr (kLora && !kGated) {
+            activate_all<false>(p.act, f);
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (kGated) f[k] = silu(f[k]) * (g[k] + bias_up[k]);
-            else f[k] = activate(kAct, f[k]);
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (kGated) f[k] = silu(f[k]) * (g[k] + bias_up[k]);
+              else f[k] = activate(kAct, f[k]);
+            }
           }
           if (p.vec_out && cols == 4) {
             f[0] += bf16_lo(res[w].x);
@@ -962,23 +1333,25 @@ template <int kAct, bool kF32, bool kLora>
 static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
   auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct, kF32, kLora>
                                         : (p.kps == 1 ? linear_pair_kernel<kAct, 1, kF32, kLora> : linear_pair_kernel<kAct, 2, kF32, kLora>);
-  const int smem = p.form == kLinearStream ? lin::kStreamSmem : lin::kPairSmem;
+  constexpr int kMore = kLora ? (int)sizeof(AdapterShared) : 0;
+  static_assert(lin::kStreamSmem + kMore <= 232448 && lin::kPairSmem + kMore <= 232448, "shared memory budget");
+  const int smem = (p.form == kLinearStream ? lin::kStreamSmem : lin::kPairSmem) + kMore;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
     cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         lin::kStreamSmem);
+                                         lin::kStreamSmem + kMore);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem + kMore);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem + kMore);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)p.grid);
-  lc.blockDim = dim3(p.form == kLinearStream ? lin::kThreads : lin::kPairThreads);
+  lc.blockDim = dim3(kLora ? lin::kLoraThreads : (p.form == kLinearStream ? lin::kThreads : lin::kPairThreads));
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute attr[2];
@@ -1011,7 +1384,9 @@ static cudaError_t launch_form(const LinearMaps& maps, const LinearParams& p, cu
         {linear_direct_kernel<true, 1, kF32, kLora>, linear_direct_kernel<true, 2, kF32, kLora>, linear_direct_kernel<true, 4, kF32, kLora>}};
     return cudaLaunchKernelEx(&lc, kernels[p.act == GMMFR_ACT_SWIGLU][tiles], p);
   }
-  switch (p.act) {
+  if constexpr (kLora) {
+    return p.act == GMMFR_ACT_SWIGLU ? launch_one<GMMFR_ACT_SWIGLU, kF32, true>(maps, p, s) : launch_one<GMMFR_ACT_NONE, kF32, true>(maps, p, s);
+  } else switch (p.act) {
     case GMMFR_ACT_RELU: return launch_one<GMMFR_ACT_RELU, kF32, kLora>(maps, p, s);
     case GMMFR_ACT_GELU: return launch_one<GMMFR_ACT_GELU, kF32, kLora>(maps, p, s);
     case GMMFR_ACT_GELU_TANH: return launch_one<GMMFR_ACT_GELU_TANH, kF32, kLora>(maps, p, s);

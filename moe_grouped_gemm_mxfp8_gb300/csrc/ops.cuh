@@ -84,6 +84,7 @@ int64_t layer_image_bytes(bool mx, int64_t npad);
 enum { kLinearDirect = 0, kLinearStream = 1, kLinearPair = 2 };
 constexpr int kLinearDirectRows = 32;
 constexpr int kLinearStreamRows = 128;
+constexpr int kLoraListInts = 260;
 
 struct LinearParams {
   const __nv_bfloat16 *x, *w, *bias, *residual;  // x and w at 16-byte row pitches; nothing is read past K
@@ -106,9 +107,16 @@ struct LinearParams {
   float* lora_s;                 // [M, rank]: each row's sums of its adapter's first factor, scaled
   int32_t lora_count, lora_rank;
   int64_t lora_rows;
+  // of each 256 rows: kLoraListInts words, the number of adapters and from the fourth on each, in the order of their first
+  // rows; and lora_scans words, whether a scan of their second factors met an infinity or NaN
+  const int32_t* lora_lists;
+  const uint32_t* lora_flags;
+  int32_t lora_scans;
+  int32_t lora_early;  // pair form: it may start before the sums are there
 };
 struct LinearMaps {
   CUtensorMap x, w;
+  CUtensorMap b;  // with adapters: their second factors, boxes of 64 x as many rows as a load of w has
 };
 // Chooses p's form.  tail.M > 0: the last rows, taken out of p, are a second launch that runs beside p's.
 void plan_linear(LinearParams& p, LinearParams& tail, int sms);
@@ -121,7 +129,12 @@ struct LoraParams {
   float* s;                    // [M, rank]
   int64_t M, K, ldx;
   int32_t count, rank;
-  int32_t split;               // launch_lora_sums' choice: CTAs of a cluster
+  const __nv_bfloat16* b;      // second factors [count, rows, rank], which are scanned
+  int64_t rows;
+  int32_t* lists;              // as LinearParams'
+  uint32_t* flags;
+  int32_t scans;               // CTAs to a list; 0: no lists
+  int32_t split, depth;        // launch_lora_sums' choice: CTAs of a cluster, clusters that share a tile's adapters
 };
 cudaError_t launch_lora_sums(LoraParams p, int sms, cudaStream_t s);
 cudaError_t launch_lora_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
