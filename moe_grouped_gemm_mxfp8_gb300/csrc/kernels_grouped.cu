@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
     auto release = [&]() {
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[acc_i & 1]), 0));
+      if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&acce[acc_i & 1]), 0));
       ++acc_i;
     };
     for (int64_t u = first; u < units; u += pairs) {
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
               if (kb == n - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
             }
           } else if (lane == 0) {
-            ptx::mbar_arrive_cluster(ptx::map_to_rank(peer0 + 8 * stage, 0));
+            ptx::mbar_arrive_remote(ptx::map_to_rank(peer0 + 8 * stage, 0));
           }
           __syncwarp();
           if (++stage == grp::kGradStages) {
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
           }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acce[acc_i & 1]), 0));
+        if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&acce[acc_i & 1]), 0));
         ++acc_i;
       }
       if (!ok) break;

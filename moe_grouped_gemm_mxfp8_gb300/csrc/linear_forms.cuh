@@ -366,7 +366,7 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
     __syncwarp();
     if (lane == 0) {
       const uint32_t bar = ptx::smem_u32(&a.built[stage]);
-      if (to >= 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, to));
+      if (to >= 0) ptx::mbar_arrive_remote(ptx::map_to_rank(bar, to));
       else ptx::mbar_arrive(bar);
     }
     if (++stage == n_stages) stage = 0;
