@@ -261,23 +261,26 @@ gmmfr_status validate_lora(const gmmfr_lora_problem* p) {
   return GMMFR_OK;
 }
 
-// Behind the error words: the adapters' sums, and for each 256 rows a list and what its scans found
+// Behind the error words: the adapters' sums, for each 256 rows a list and what its scans found, the sums' own error bits
 struct LoraLayout {
-  int64_t blocks, rows;
-  int32_t scans;
-  size_t sums, lists, flags, total;
+  gmmfr::LoraParams plan;
+  size_t sums, lists, flags, errs, total;
 };
-LoraLayout lora_layout(const gmmfr_lora_problem* p) {
+LoraLayout lora_layout(const gmmfr_lora_problem* p, int sms) {
   LoraLayout L{};
-  L.blocks = cdiv(p->linear.M, 256);
-  L.rows = p->linear.N * (p->linear.activation == GMMFR_ACT_SWIGLU ? 2 : 1);
-  // CTAs: 32 KB for each if all rows of a list had adapters of their own, some hundred in all
-  const int64_t most = std::min({p->linear.M, p->count, int64_t(256)}) * L.rows * p->rank * 2;
-  L.scans = (int32_t)std::clamp<int64_t>(most / 32768, 1, std::max<int64_t>(4, 512 / std::max<int64_t>(L.blocks, 1)));
+  const int64_t M = p->linear.M, blocks = cdiv(M, 256), rows = p->linear.N * (p->linear.activation == GMMFR_ACT_SWIGLU ? 2 : 1);
+  L.plan.M = M;
+  L.plan.K = p->linear.K;
+  L.plan.count = (int32_t)p->count;
+  L.plan.rank = (int32_t)p->rank;
+  L.plan.rows = rows;
+  L.plan.scans = (int32_t)std::clamp<int64_t>(std::min(M, p->count) * rows * p->rank * 2 / 16384, 1, 1 << 20);  // 16 KB and more for a CTA
+  gmmfr::plan_lora_sums(L.plan, sms);
   L.sums = gmmfr::kHdrBytes;
-  L.lists = align256(L.sums + sizeof(float) * (size_t)p->linear.M * p->rank);
-  L.flags = align256(L.lists + sizeof(int32_t) * gmmfr::kLoraListInts * (size_t)L.blocks);
-  L.total = align256(L.flags + sizeof(uint32_t) * (size_t)L.scans * L.blocks);
+  L.lists = align256(L.sums + sizeof(float) * (size_t)L.plan.parts * M * p->rank);
+  L.flags = align256(L.lists + sizeof(int32_t) * gmmfr::kLoraListInts * (size_t)blocks);
+  L.errs = align256(L.flags + sizeof(uint32_t) * (size_t)L.plan.scans * blocks);
+  L.total = align256(L.errs + sizeof(uint32_t) * (size_t)L.plan.grid);
   return L;
 }
 
@@ -304,7 +307,7 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     if (!aligned(adapters->scale, 4) || !aligned(adapters->ids, 4))
       return fail(GMMFR_ERR_INVALID_ARG, "lora_scale or adapter_ids is not aligned to its element size");
   }
-  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, adapters ? lora_layout(adapters->problem).total : L.total)) return st;
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, adapters ? lora_layout(adapters->problem, gmmfr::sm_count()).total : L.total)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = gmmfr::sm_count();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -341,34 +344,45 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
   if (adapters) {
     lp.lora_ids = adapters->ids;
     lp.lora_b = static_cast<const __nv_bfloat16*>(adapters->b);
-    const LoraLayout A = lora_layout(adapters->problem);
-    lp.lora_s = reinterpret_cast<float*>(ws + A.sums);
-    lp.lora_count = (int32_t)adapters->problem->count;
-    lp.lora_rank = (int32_t)adapters->problem->rank;
-    lp.lora_rows = rows_w;
-    lp.lora_lists = reinterpret_cast<int32_t*>(ws + A.lists);
-    lp.lora_flags = reinterpret_cast<uint32_t*>(ws + A.flags);
-    lp.lora_scans = A.scans;
+    const LoraLayout A = lora_layout(adapters->problem, sms);
+    sums = A.plan;
+    lp.lora_s = sums.s = reinterpret_cast<float*>(ws + A.sums);
+    lp.lora_lists = sums.lists = reinterpret_cast<int32_t*>(ws + A.lists);
+    lp.lora_flags = sums.flags = reinterpret_cast<uint32_t*>(ws + A.flags);
+    lp.lora_count = sums.count;
+    lp.lora_rank = sums.rank;
+    lp.lora_rows = sums.rows;
+    lp.lora_scans = sums.scans;
     sums.x = lp.x;
+    sums.ldx = lp.ldx;
     sums.a = static_cast<const __nv_bfloat16*>(adapters->a);
+    sums.b = lp.lora_b;
     sums.scale = adapters->scale;
     sums.ids = adapters->ids;
-    sums.s = lp.lora_s;
-    sums.M = p.M;
-    sums.K = p.K;
-    sums.ldx = lp.ldx;
-    sums.count = lp.lora_count;
-    sums.rank = lp.lora_rank;
-    sums.b = lp.lora_b;
-    sums.rows = rows_w;
-    sums.lists = reinterpret_cast<int32_t*>(ws + A.lists);
-    sums.flags = reinterpret_cast<uint32_t*>(ws + A.flags);
+    lp.lora_parts = sums.parts;
+    lp.lora_part = p.M * sums.rank;
+    sums.errs = reinterpret_cast<uint32_t*>(ws + A.errs);
+    lp.lora_errs = sums.errs;
+    lp.lora_err_count = sums.grid;
+    sums.timeout_ns = lp.timeout_ns;
+    sums.test_stall = lp.test_stall;
   }
   gmmfr::LinearParams parts[2] = {lp, lp};
   gmmfr::LinearMaps maps[2];
   gmmfr::plan_linear(parts[0], parts[1], sms);
   parts[0].lora_early = parts[1].M == 0;  // what runs beside starts with it, and does not wait
-  sums.scans = parts[0].form == gmmfr::kLinearDirect ? 0 : lp.lora_scans;
+  gmmfr::LoraMaps sum_maps;
+  if (adapters && parts[0].form == gmmfr::kLinearDirect) {  // which needs no lists
+    sums.scans = 0;
+    gmmfr::plan_lora_sums(sums, sms);
+  }
+  if (adapters && p.M > gmmfr::kLoraFewRows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
+    if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    if (!encode_rows(encode, &sum_maps.x, lp.x, p.M, p.K, lp.ldx, 128) ||
+        !encode_slices(encode, &sum_maps.a, sums.a, false, sums.count, sums.rank, p.K, 64, 16))
+      return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (first factors)");
+  }
   for (int i = 0; i < 2; ++i) {  // what can be refused, before anything is launched
     const gmmfr::LinearParams& q = parts[i];
     if (q.M == 0 || q.form == gmmfr::kLinearDirect) continue;
@@ -391,7 +405,7 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
   }
   if (adapters) {
-    cudaError_t e = gmmfr::launch_lora_sums(sums, sms, s);
+    cudaError_t e = gmmfr::launch_lora_sums(sum_maps, sums, s);
     if (e != cudaSuccess) return cuda_fail(e, "adapters' sums launch");
   }
   for (int i = 0; i < 2; ++i) {
@@ -594,7 +608,7 @@ gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const void* x, co
 gmmfr_status gmmfr_lora_linear_workspace_size(const gmmfr_lora_problem* problem, size_t* bytes) {
   if (gmmfr_status st = validate_lora(problem)) return st;
   if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = lora_layout(problem).total;
+  *bytes = lora_layout(problem, gmmfr::sm_count()).total;
   return GMMFR_OK;
 }
 

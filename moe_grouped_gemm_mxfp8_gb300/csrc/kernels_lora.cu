@@ -1,20 +1,21 @@
 // The dense product with low-rank adapters of many requests (forms: linear_forms.cuh, with kLora), and the sums that it
 // starts from: s[t] = scale_a (A_a x[t]) for the adapter a of row t.
 //
-// The sums read r (16, say) rows of K for every adapter in use, and the rows of x.  Both kernels multiply by mma.sync: they wait
-// for memory, and an adapter has a few rows at a time.  A lane loads 16 bytes of a row at a time straight into operand
-// registers; the CTAs of a cluster and their warps share the K range, and their sums meet in shared memory in their order.
-//   few   up to 128 rows: a cluster for each adapter and 16 of its ranks, its rows gathered, so that every factor is read once
-//         and all of them are on their way at once
-//   many  a cluster for 64 rows of x, whose warps share the adapters of those rows when there are several
-// CTAs beside them list the adapters of each 256 rows, and scan those adapters' second factors for infinities and NaN (which
-// also brings them into L2).  The product's launch follows at once and begins with its weights; only its adapters wait.
+// The sums read r (16, say) rows of K for every adapter in use, and the rows of x.
+//   few   up to 128 rows: each adapter's rows gathered, so that every factor is read once and all of them are on their way at
+//         once.  Products by mma.sync, 16 bytes of a row at a time from global memory straight into a lane's operand
+//         registers: they wait for memory, and an adapter has a few rows.
+//   many  128 rows of x at a time, by TMA and tcgen05: the rows are one operand, 16 ranks of up to 16 of their adapters'
+//         factors the other; of what comes out a row keeps its own adapter's columns.
+// Several CTAs share a K range.  CTAs also list the adapters of each 256 rows, and scan those adapters' second
+// factors for infinities and NaN (which brings them into L2).  The product's launch follows at once and begins with its
+// weights; only its adapters wait.
 #include "linear_forms.cuh"
 
 namespace gmmfr {
 namespace lora {
-constexpr int kThreads = 256;
-constexpr int kFewRows = 128, kManyRows = 64;
+constexpr int kFewThreads = 512;
+constexpr int kTileThreads = 320, kTileStages = 10, kTileArena = 10 * (lin::kTileBytes + 2048);
 }  // namespace lora
 
 namespace {
@@ -56,10 +57,19 @@ struct SumOperands {
   }
 };
 
+// Whether one of 8 BF16 numbers is infinite or NaN
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool found = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) found |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+  return found;
+}
+
 // Whether this thread's row is the first with its adapter among `rows` rows (of which it has number tid; id -1: none)
 __device__ __forceinline__ bool first_of(const int* s_id, int tid, int id) {
   bool first = id >= 0;
-  for (int j = 0; j < tid; j += 4) {
+  for (int j = 0; j < tid && first; j += 4) {
     const int4 v = *reinterpret_cast<const int4*>(&s_id[j]);
     first &= v.x != id && (v.y != id || j + 1 >= tid) && (v.z != id || j + 2 >= tid) && (v.w != id || j + 3 >= tid);
   }
@@ -71,348 +81,379 @@ __device__ __forceinline__ int adapter_at(const LoraParams& p, int64_t m) {
   return (uint32_t)id < (uint32_t)p.count ? id : -1;
 }
 
-// Part `i` of the lists and scans: list i / scans, share i % scans of its adapters' second factors taken together.
-__device__ void list_and_scan(const LoraParams& p, int64_t i) {
-  static_assert(lora::kThreads == 256, "a thread for each of a list's rows");
+// Part `i` of the lists and scans, by kT threads (of which this one is `t`) that share barrier 1: list i / scans, share
+// i % scans of its adapters' second factors taken together.
+template <int kT>
+__device__ void list_and_scan(const LoraParams& p, int64_t i, int t) {
+  constexpr int kPer = kT < 256 ? 256 / kT : 1;  // rows of the list for each thread
   __shared__ __align__(16) int l_id[256];
   __shared__ int l_list[256];
   __shared__ uint32_t l_first[8];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int l_found;
+  const int lane = t & 31;
   const int64_t block = i / p.scans;
   const int share = (int)(i - block * p.scans);
-  const int id = adapter_at(p, block * 256 + tid);
-  l_id[tid] = id;
-  __syncthreads();
-  const bool first = first_of(l_id, tid, id);
-  const uint32_t b = __ballot_sync(0xffffffffu, first);
-  if (lane == 0) l_first[warp] = b;
-  __syncthreads();
-  int n = 0, at = __popc(b & ((1u << lane) - 1));
+  int id[kPer];
+  uint32_t firsts[kPer];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const int c = __popc(l_first[w]);
-    if (w < warp) at += c;
-    n += c;
+  for (int k = 0; k < kPer; ++k) {
+    id[k] = t < 256 ? adapter_at(p, block * 256 + k * kT + t) : -1;
+    if (t < 256) l_id[k * kT + t] = id[k];
   }
+  if (t == 0) l_found = 0;
+  ptx::bar_sync(1, kT);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    firsts[k] = __ballot_sync(0xffffffffu, first_of(l_id, k * kT + t, id[k]));  // (nothing past 256: id -1)
+    if (lane == 0 && t < 256) l_first[(k * kT + t) >> 5] = firsts[k];
+  }
+  ptx::bar_sync(1, kT);
   int32_t* list = p.lists + block * kLoraListInts;
-  if (first) {
-    l_list[at] = id;
-    if (share == 0) list[4 + at] = id;
+  int n = 0;
+  for (int w = 0; w < 8; ++w) n += __popc(l_first[w]);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    int at = __popc(firsts[k] & ((1u << lane) - 1));
+    for (int w = 0; w < min((k * kT + t) >> 5, 8); ++w) at += __popc(l_first[w]);
+    if (firsts[k] >> lane & 1) {
+      l_list[at] = id[k];
+      if (share == 0) list[4 + at] = id[k];
+    }
   }
-  if (share == 0 && tid == 0) list[0] = n;
-  __syncthreads();
+  if (share == 0 && t == 0) list[0] = n;
+  ptx::bar_sync(1, kT);
   const int64_t pieces = p.rows * p.rank / 8, from = n * pieces * share / p.scans, to = n * pieces * (share + 1) / p.scans;
   bool found = false;
   for (int64_t d = from / pieces; d * pieces < to; ++d) {
     const uint4* f = reinterpret_cast<const uint4*>(p.b) + l_list[d] * pieces;
     const int64_t end = min(to - d * pieces, pieces);
-#pragma unroll 4
-    for (int64_t k = max(from - d * pieces, (int64_t)0) + tid; k < end; k += lora::kThreads) {
-      const uint4 v = __ldg(f + k);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    int64_t k = max(from - d * pieces, (int64_t)0) + t;
+    for (; k + 7 * kT < end; k += 8 * kT) {
+      uint4 v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) found |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+      for (int u = 0; u < 8; ++u) v[u] = ptx::ld_nc_v4(f + k + u * kT);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) found |= not_finite(v[u]);
     }
+    for (; k < end; k += kT) found |= not_finite(ptx::ld_nc_v4(f + k));
   }
-  found = __syncthreads_or(found);
-  if (tid == 0) p.flags[i] = found;
+  if (found) l_found = 1;
+  ptx::bar_sync(1, kT);
+  if (t == 0) p.flags[i] = l_found;
 }
 
 }  // namespace
 
 // ============================================================================ few rows
-// Cluster (d, r): the d-th adapter in the order of the rows, ranks 16 r and up.
-__global__ void __launch_bounds__(lora::kThreads) lora_sums_few_kernel(const __grid_constant__ LoraParams p) {
-  constexpr int kU = 4;
-  __shared__ __align__(16) int s_id[lora::kFewRows];
-  __shared__ uint32_t s_first[4], s_mine[4];
-  __shared__ int s_row[lora::kFewRows];
-  __shared__ __align__(16) float part[8][8][16];
+// CTA (d, r): the d-th adapter in the order of the rows, ranks 16 r and up; where there are fewer adapters than places for
+// them, several places share an adapter's rows.  The last CTAs list and scan.
+__global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(const __grid_constant__ LoraParams p) {
+  constexpr int kU = 8, kWarps = lora::kFewThreads / 32;
+  __shared__ __align__(16) int s_id[kLoraFewRows];
+  __shared__ uint32_t s_first[4];
+  __shared__ int s_row[kLoraFewRows];
+  __shared__ __align__(16) float part[8 * kWarps][16];
+  static_assert(8 * kWarps >= kLoraFewRows, "a slot for each row");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = p.split, rc = (p.rank + 15) / 16;
-  const uint32_t crank = C > 1 ? ptx::cluster_rank() : 0u;
-  const int units = (int)min(p.M, (int64_t)p.count) * rc, unit = blockIdx.x / C, d = unit / rc, r0 = unit % rc * 16;
+  const int rc = (p.rank + 15) / 16, places = (int)min(p.M, (int64_t)p.count);
   // the launch after this one reads x and its weights without waiting for this one: it may start when all before has ended
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  if (unit >= units) {
-    const int i = blockIdx.x - units * C;
-    if (i < p.scans) list_and_scan(p, i);
+  if (blockIdx.x >= places * rc) {
+    list_and_scan<lora::kFewThreads>(p, blockIdx.x - places * rc, tid);
     return;
   }
   int id = -1;
-  if (tid < lora::kFewRows) s_id[tid] = id = adapter_at(p, tid);
+  if (tid < kLoraFewRows) s_id[tid] = id = adapter_at(p, tid);
   __syncthreads();
-  if (tid < lora::kFewRows) {
+  if (tid < kLoraFewRows) {
     const uint32_t b = __ballot_sync(0xffffffffu, first_of(s_id, tid, id));
     if (lane == 0) s_first[warp] = b;
   }
   __syncthreads();
-  // the d-th first row's adapter, and its rows
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) n += __popc(s_first[w]);
+  const int place = blockIdx.x / rc, r0 = blockIdx.x % rc * 16;
+  const int shares = n ? places / n : 0;  // of an adapter's rows
+  if (place >= n * shares) return;
+  const int share = place / n;
   int a = -1;
   {
-    int skip = d;
+    int skip = place % n;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint32_t b = s_first[w];
-      const int n = __popc(b);
-      if (a < 0 && skip < n) {
+      const int here = __popc(b);
+      if (a < 0 && skip < here) {
         for (int i = 0; i < skip; ++i) b &= b - 1;
         a = s_id[32 * w + __ffs(b) - 1];
       }
-      skip -= n;
+      skip -= here;
     }
   }
-  if (a < 0) return;  // fewer adapters: the whole cluster leaves
-  if (tid < lora::kFewRows) {
-    const uint32_t b = __ballot_sync(0xffffffffu, id == a);
-    if (lane == 0) s_mine[warp] = b;
+  int rows = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t mine = __ballot_sync(0xffffffffu, s_id[32 * w + lane] == a);
+    if (w == warp && mine >> lane & 1) s_row[rows + __popc(mine & ((1u << lane) - 1))] = tid;
+    rows += __popc(mine);
   }
   __syncthreads();
-  const int n0 = __popc(s_mine[0]), n1 = n0 + __popc(s_mine[1]), n2 = n1 + __popc(s_mine[2]), rows = n2 + __popc(s_mine[3]);
-  if (tid < lora::kFewRows && id == a)
-    s_row[(warp == 0 ? 0 : (warp == 1 ? n0 : (warp == 2 ? n1 : n2))) + __popc(s_mine[warp] & ((1u << lane) - 1))] = tid;
-  __syncthreads();
-  const float scale = p.scale ? p.scale[a] : 1.f;
+  // the warps share the tiles of 8 rows, and the K range where the tiles are fewer
+  const int all = (rows + 7) / 8, tile0 = all * share / shares, tiles = all * (share + 1) / shares - tile0;
+  int sharing = 1;
+  while (sharing < tiles) sharing *= 2;
+  const int splits = kWarps / sharing, split = warp % splits, t = warp / splits;
   const int blocks = (int)((p.K + 31) / 32);
-  const int b_begin = (int)((int64_t)blocks * crank / C) + warp, b_end = (int)((int64_t)blocks * (crank + 1) / C);
-  const __nv_bfloat16* ar = p.a + ((int64_t)a * p.rank + r0) * p.K;
-  for (int t0 = 0; t0 < rows; t0 += 8) {
-    const __nv_bfloat16* const xr[1] = {p.x + (int64_t)s_row[min(t0 + (lane >> 2), rows - 1)] * p.ldx};
+  if (t < tiles) {
+    const __nv_bfloat16* ar = p.a + ((int64_t)a * p.rank + r0) * p.K;
+    const __nv_bfloat16* const xr[1] = {p.x + (int64_t)s_row[min((tile0 + t) * 8 + (lane >> 2), rows - 1)] * p.ldx};
     float acc[1][1][4] = {};
-    for (int b0 = b_begin; b0 < b_end; b0 += 8 * kU) {
+    for (int b0 = split; b0 < blocks; b0 += splits * kU) {
       SumOperands<1, 1> o[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int64_t k = (int64_t)(b0 + 8 * u) * 32 + (lane & 3) * 8;
-        o[u].load(ar, p.rank - r0, p.K, xr, k, b0 + 8 * u < b_end && k < p.K);
+      for (int v = 0; v < kU; ++v) {
+        const int64_t k = (int64_t)(b0 + splits * v) * 32 + (lane & 3) * 8;
+        o[v].load(ar, p.rank - r0, p.K, xr, k, k < p.K);
       }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        o[u].keep(b0 + 8 * u < b_end && (int64_t)(b0 + 8 * u) * 32 + (lane & 3) * 8 < p.K);
-        o[u].multiply(acc);
+      for (int v = 0; v < kU; ++v) {
+        o[v].keep((int64_t)(b0 + splits * v) * 32 + (lane & 3) * 8 < p.K);
+        o[v].multiply(acc);
       }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) part[warp][(lane & 3) * 2 + (c & 1)][8 * (c >> 1) + (lane >> 2)] = acc[0][0][c];
-    __syncthreads();
-    // 128 sums: the warps' parts in order, then the cluster's CTAs'
-    float* sums = &part[0][0][0];
-    if (tid < 32) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float4 z = *reinterpret_cast<const float4*>(sums + w * 128 + 4 * tid);
-        v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-      }
-      *reinterpret_cast<float4*>(sums + 4 * tid) = v;
+    for (int i = 0; i < 4; ++i) part[(split * tiles + t) * 8 + (lane & 3) * 2 + (i & 1)][8 * (i >> 1) + (lane >> 2)] = acc[0][0][i];
+  }
+  __syncthreads();
+  // the splits' parts in order
+  const float scale = p.scale ? p.scale[a] : 1.f;
+  const float4* sums = reinterpret_cast<const float4*>(&part[0][0]);
+  for (int i = tid; i < tiles * 32; i += lora::kFewThreads) {
+    const int row = tile0 * 8 + i / 4, r = r0 + i % 4 * 4;
+    if (row >= rows || r >= p.rank) continue;
+    float4 v = sums[i];
+    for (int s = 1; s < splits; ++s) {
+      const float4 z = sums[s * tiles * 32 + i];
+      v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
     }
-    if (C > 1) ptx::cluster_sync();
-    else __syncthreads();
-    const int i = crank * 32 / C + tid;  // this CTA's share of the 32 x 4
-    if (tid < 32 / C && t0 + i / 4 < rows && r0 + i % 4 * 4 < p.rank) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const uint32_t at = ptx::smem_u32(sums + 4 * i);
-      for (int c = 0; c < C; ++c) {
-        const float4 z = ptx::ld_cluster_v4(C > 1 ? ptx::map_to_rank(at, c) : at);
-        v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-      }
-      *reinterpret_cast<float4*>(p.s + (int64_t)s_row[t0 + i / 4] * p.rank + r0 + i % 4 * 4) =
-          make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
-    }
-    if (C > 1) ptx::cluster_sync();
-    else __syncthreads();
+    *reinterpret_cast<float4*>(p.s + (int64_t)s_row[row] * p.rank + r) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
   }
 }
 
 // ============================================================================ many rows
-// `depth` clusters take 64 rows and share their adapters; each warp of a CTA takes kRt times 16 ranks of an adapter at a time,
-// its K range split further when the adapters are fewer than the warps.  An adapter's rows are gathered, 32 at a time.
-template <int kRt>
-__global__ void __launch_bounds__(lora::kThreads, kRt == 1 ? 2 : 1) lora_sums_many_kernel(const __grid_constant__ LoraParams p) {
-  constexpr int kTiles = 4, kRanks = 16 * kRt, kRows = lora::kManyRows;
-  __shared__ __align__(16) int s_id[kRows];
-  __shared__ uint32_t s_first[2];
-  extern __shared__ __align__(16) float part[];  // [8][kRows][kRanks]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = p.split;
-  const uint32_t crank = C > 1 ? ptx::cluster_rank() : 0u;
-  const int64_t tiles = (p.M + kRows - 1) / kRows, unit = blockIdx.x / C;
-  ptx::griddep_wait();  // as above
-  ptx::griddep_launch_dependents();
-  if (unit >= tiles * p.depth) {
-    const int64_t i = blockIdx.x - tiles * p.depth * C;
-    if (i < p.scans * ((p.M + 255) / 256)) list_and_scan(p, i);
-    return;
+// CTA (c, p, tile): the 128 rows of a tile, share c of the K range, every `passes`-th pass from p on of up to 16 units: 16 ranks of
+// an adapter.  Who reads the sums adds the shares' parts.  (Clusters that join them on the chip wait for SMs that lie
+// together: 16 us more with clusters of 8.)  Warp 0 TMA, warp 1 MMA, warps 2..9 lists and
+// scans, the first four of them the epilogue.
+__global__ void __launch_bounds__(lora::kTileThreads, 1)
+    lora_sums_many_kernel(const __grid_constant__ LoraMaps maps, const __grid_constant__ LoraParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[lora::kTileStages], empty[lora::kTileStages], accf[2], acce[2], drain;
+  __shared__ __align__(16) int s_id[128];
+  __shared__ int s_list[128];
+  __shared__ uint32_t s_first[4], tmem_slot, s_err;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp: uniform
+  const int C = p.split, share = blockIdx.x % C, pass0 = 16 * (blockIdx.x / C % p.passes), step = 16 * p.passes;
+  const int64_t row0 = (int64_t)(blockIdx.x / C / p.passes) * 128;
+  const bool works = row0 < p.M;  // the others scan
+  if (tid == 0) {
+    for (int s = 0; s < lora::kTileStages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
+      ptx::mbar_init(ptx::smem_u32(&acce[b]), 4);
+    }
+    ptx::mbar_init(ptx::smem_u32(&drain), 1);
+    abort_flag = 0;
+    s_err = 0;
+    ptx::fence_mbar_init();
   }
-  const int64_t row0 = unit % tiles * kRows;
-  const int turn = (int)(unit / tiles);
+  if (warp == 0 && lane < 2) ptx::prefetch_tensormap(lane ? &maps.a : &maps.x);
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   int id = -1;
-  if (tid < kRows) s_id[tid] = id = adapter_at(p, row0 + tid);
+  if (tid < 128) s_id[tid] = id = works ? adapter_at(p, row0 + tid) : -1;
   __syncthreads();
-  if (tid < kRows) {
+  if (tid < 128) {
     const uint32_t b = __ballot_sync(0xffffffffu, first_of(s_id, tid, id));
     if (lane == 0) s_first[warp] = b;
   }
+  ptx::tc_fence_before();
   __syncthreads();
-  uint64_t firsts = 0;  // this cluster's: every depth-th
-  {
-    uint64_t b = s_first[0] | (uint64_t)s_first[1] << 32;
-    for (int d = 0; b; ++d, b &= b - 1)
-      if (d % p.depth == turn) firsts |= b & -b;
+  ptx::tc_fence_after();
+  int n = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (tid >> 5 == w && s_first[w] >> lane & 1) s_list[n + __popc(s_first[w] & ((1u << lane) - 1))] = id;
+    n += __popc(s_first[w]);
   }
-  if (!firsts) return;  // the whole cluster leaves
-  const int adapters = __popcll(firsts);
-  const int groups = adapters <= 1 ? 1 : (adapters <= 2 ? 2 : (adapters <= 4 ? 4 : 8)), splits = 8 / groups;
-  const int group = warp / splits, split = warp - group * splits;
-  const int blocks = (int)((p.K + 31) / 32);
-  const int b_begin = (int)((int64_t)blocks * crank / C) + split, b_end = (int)((int64_t)blocks * (crank + 1) / C);
-  for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
-    uint64_t left = firsts;
-    for (int d = 0; d < adapters; ++d, left &= left - 1) {
-      if (d % groups != group) continue;
-      const int a = s_id[__ffsll(left) - 1];
-      const __nv_bfloat16* ar = p.a + ((int64_t)a * p.rank + r0) * p.K;
-      uint64_t mine = __ballot_sync(0xffffffffu, s_id[lane] == a) | (uint64_t)__ballot_sync(0xffffffffu, s_id[32 + lane] == a) << 32;
-#pragma unroll 1
-      while (mine) {
-        // up to 32 rows: lane l's are the (8 i + l / 4)-th
-        int row[kTiles];
-        const __nv_bfloat16* xr[kTiles];
-        const int n = __popcll(mine);
-        if (n == kRows || (mine << 32 == 0 && n == 32)) {  // all, or the last 32 behind them
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i) row[i] = kRows - n + 8 * i + (lane >> 2);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            int skip = min(8 * i + (lane >> 2), n - 1), at = 0;  // past the last one: it again, and not stored
-#pragma unroll
-            for (int half = 32; half >= 1; half >>= 1) {
-              const int below = __popcll(mine >> at & ((1ull << half) - 1));
-              if (skip >= below) {
-                skip -= below;
-                at += half;
-              }
-            }
-            row[i] = at;
-          }
+  __syncthreads();
+  const uint32_t tmem_base = tmem_slot, smem_base = ptx::smem_u32(smem);
+  const Ctl ctl{&abort_flag, &s_err, p.timeout_ns};
+  const int rc = (p.rank + 15) / 16, units = n * rc;  // unit u: adapter u / rc, ranks 16 (u % rc) and up
+  const int stage_bytes = lin::kTileBytes + min(units, 16) * 2048, n_stages = min(lora::kTileStages, lora::kTileArena / stage_bytes);
+  const int KB = (int)((p.K + 63) / 64), kb0 = (int)((int64_t)KB * share / C), kb1 = (int)((int64_t)KB * (share + 1) / C);
+
+  if (warp == 0) {
+    const uint64_t pol = ptx::l2_evict_last_policy();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u0 = pass0; ok && u0 < units; u0 += step) {
+      const int m = min(16, units - u0);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
+          ok = false;
+          break;
         }
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) xr[i] = p.x + (row0 + row[i]) * p.ldx;
-        float acc[kTiles][kRt][4] = {};
-        // two sets of operands: one is on its way while the other is multiplied
-        SumOperands<kTiles, kRt> even, odd;
-        auto load = [&](SumOperands<kTiles, kRt>& o, int b) {
-          const int64_t k = (int64_t)b * 32 + (lane & 3) * 8;
-          o.load(ar, p.rank - r0, p.K, xr, k, k < p.K);
-        };
-        auto multiply = [&](SumOperands<kTiles, kRt>& o, int b) {
-          o.keep((int64_t)b * 32 + (lane & 3) * 8 < p.K);
-          o.multiply(acc);
-        };
-        if (b_begin < b_end) load(even, b_begin);
-        for (int b = b_begin; b < b_end; b += 2 * splits) {
-          const bool more = b + splits < b_end;
-          if (more) load(odd, b + splits);
-          multiply(even, b);
-          if (!more) break;
-          if (b + 2 * splits < b_end) load(even, b + 2 * splits);
-          multiply(odd, b + splits);
+        if (ptx::elect_one()) {
+          const uint32_t fb = ptx::smem_u32(&full[stage]), sb = smem_base + stage * stage_bytes;
+          ptx::mbar_arrive_expect_tx(fb, lin::kTileBytes + m * 2048);
+          ptx::tma_load_2d(sb, &maps.x, kb * 64, (int)row0, fb, pol);
+          for (int u = 0; u < m; ++u)
+            ptx::tma_load_3d(sb + lin::kTileBytes + u * 2048, &maps.a, kb * 64, (u0 + u) % rc * 16, s_list[(u0 + u) / rc], fb, pol);
         }
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {  // columns 2 (lane % 4) + c of the products
-            const int to = __shfl_sync(0xffffffffu, row[i], ((lane & 3) * 2 + c) * 4);
-            if (8 * i + (lane & 3) * 2 + c < n)
-#pragma unroll
-              for (int j = 0; j < kRt; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) part[(split * kRows + to) * kRanks + 16 * j + 8 * h + (lane >> 2)] = acc[i][j][2 * h + c];
-          }
-#pragma unroll
-        for (int i = 0; i < 8 * kTiles; ++i) mine &= mine - 1;
+        __syncwarp();
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
-    __syncthreads();
-    // the splits' sums in order, then the cluster's CTAs'
-    constexpr int kFours = kRows * kRanks / 4;
-    float4* fours = reinterpret_cast<float4*>(part);
-    if (splits > 1)
-      for (int i = tid; i < kFours; i += lora::kThreads) {
-        float4 v = fours[i];
-        for (int s = 1; s < splits; ++s) {
-          const float4 z = fours[s * kFours + i];
-          v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-        }
-        fours[i] = v;
+    for (int s = 0; ok && s < n_stages; ++s) {  // no load is in flight at exit
+      ok = warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl);
+      if (++stage == n_stages) {
+        stage = 0;
+        phase ^= 1;
       }
-    if (C > 1) ptx::cluster_sync();
-    else __syncthreads();
-    for (int i = crank * lora::kThreads + tid; i < kFours; i += C * lora::kThreads) {
-      const int row = i / (kRanks / 4), r = r0 + i % (kRanks / 4) * 4, a = s_id[row];
-      if (a < 0 || r >= p.rank) continue;
-      if (adapters < 64 && p.depth > 1) {  // another cluster's
-        bool here = false;
-        for (uint64_t f = firsts; f; f &= f - 1) here |= s_id[__ffsll(f) - 1] == a;
-        if (!here) continue;
-      }
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const uint32_t at = ptx::smem_u32(&fours[i]);
-      for (int c = 0; c < C; ++c) {
-        const float4 z = ptx::ld_cluster_v4(C > 1 ? ptx::map_to_rank(at, c) : at);
-        v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
-      }
-      const float scale = p.scale ? p.scale[a] : 1.f;
-      *reinterpret_cast<float4*>(p.s + (row0 + row) * p.rank + r) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
     }
-    if (C > 1) ptx::cluster_sync();
-    else __syncthreads();
+    if (!ok)  // aborted: let what is in flight land
+      for (int s = 0; s < n_stages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint64_t da0 = ptx::smem_desc(smem_base, 16, 1024, ptx::kSwizzle128B);
+    const uint32_t desc_hi = (uint32_t)(da0 >> 32);
+    int stage = 0, acc_i = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u0 = pass0; ok && u0 < units; u0 += step, ++acc_i) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)min(16, units - u0) << 18) | ((128u >> 4) << 24);
+      const int buf = acc_i & 1;
+      if (!(ok = warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
+      ptx::tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl))) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t la = (uint32_t)da0 + stage * (stage_bytes >> 4), lb = la + (lin::kTileBytes >> 4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            ptx::tc_mma_f16_lo(tmem_base + buf * 256, la + 2 * q, lb + 2 * q, desc_hi, idesc, kb > kb0 || q > 0 ? 1u : 0u);
+          ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+          if (kb == kb1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[buf]));
+        }
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(&drain));
+    wait_bar_drain(ptx::smem_u32(&drain), 0);
+    __syncwarp();
+  } else {
+    if (blockIdx.x < p.scans * ((p.M + 255) / 256)) list_and_scan<256>(p, blockIdx.x, tid - 64);
   }
+  if (warp >= 2 && warp < 6) {
+    const int q = warp & 3, row = q * 32 + lane, mine = s_id[row];
+    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
+    const float scale = mine >= 0 && p.scale ? p.scale[mine] : 1.f;
+    float* to = p.s + (share * p.M + row0 + row) * p.rank;
+    int acc_i = 0;
+    for (int u0 = pass0; u0 < units; u0 += step, ++acc_i) {
+      const int buf = acc_i & 1;
+      if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
+      ptx::tc_fence_after();
+      for (int u = u0; u < min(u0 + 16, units); ++u) {
+        const bool own = mine == s_list[u / rc];
+        if (!__any_sync(0xffffffffu, own)) continue;
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(taddr + buf * 256 + (u - u0) * 16, v);
+        ptx::tmem_wait_ld();
+        const int r0 = u % rc * 16;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          if (own && r0 + j < p.rank)
+            *reinterpret_cast<float4*>(to + r0 + j) = make_float4(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale,
+                                                                  __uint_as_float(v[j + 2]) * scale, __uint_as_float(v[j + 3]) * scale);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, 512);
+  }
+  if (tid == 0) p.errs[blockIdx.x] = s_err;
 }
 
-cudaError_t launch_lora_sums(LoraParams p, int sms, cudaStream_t s) {
-  const bool few = p.M <= lora::kFewRows;
-  const int64_t tiles = (p.M + lora::kManyRows - 1) / lora::kManyRows;
+// ============================================================================ plan and launch
+void plan_lora_sums(LoraParams& p, int sms) {
   const int64_t ranks = (p.rank + 15) / 16;
-  int64_t units = few ? std::min<int64_t>(p.M, p.count) * ranks : tiles;
-  // few: as wide as clusters go; many: twice the SMs' number of CTAs, of at least 256 K each, and where that leaves SMs idle
-  // more clusters for the tiles that have several adapters
-  p.split = 1;
-  while (p.split < 8 && (few ? 2 * p.split * 32 <= p.K : units * p.split < 2 * sms && 2 * p.split * 256 <= p.K)) p.split *= 2;
-  p.depth = 1;
-  if (!few) {
-    while (p.depth < 8 && 2 * p.depth <= p.count && tiles * p.split * p.depth * 2 <= 4 * sms) p.depth *= 2;
-    units = tiles * p.depth;
+  p.split = p.passes = p.parts = 1;
+  if (p.M <= kLoraFewRows) {
+    const int64_t items = std::min<int64_t>(p.M, p.count) * ranks;
+    // scans on the SMs that are left (each a word that who reads the list looks at)
+    p.scans = (int32_t)std::min<int64_t>(p.scans, std::clamp<int64_t>(sms - items, 64, 128));
+    p.grid = (int32_t)(items + p.scans);
+    return;
   }
-  const int64_t scans = p.scans * ((p.M + 255) / 256);
-  const int smem = few ? 0 : 8 * lora::kManyRows * (p.rank <= 16 ? 16 : 32) * 4;
-  auto kernel = few ? lora_sums_few_kernel : (p.rank <= 16 ? lora_sums_many_kernel<1> : lora_sums_many_kernel<2>);
-  if (smem > 48 * 1024) {
+  // as many CTAs as SMs: one to a tile's passes as far as there may be some, and shares of K of two blocks and more; the others
+  // scan, as these do beside their products
+  const int64_t tiles = (p.M + 127) / 128, blocks = (p.M + 255) / 256, most = (std::min<int64_t>(128, p.count) * ranks + 15) / 16;
+  p.passes = (int32_t)std::clamp<int64_t>(sms / tiles / 2, 1, most);
+  while (p.split < 8 && tiles * p.passes * p.split * 2 <= sms && 2 * p.split * 128 <= p.K) p.split *= 2;
+  p.parts = p.split;
+  p.grid = (int32_t)std::max<int64_t>(tiles * p.passes * p.split, sms);
+  p.scans = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.grid / blocks, 128));
+}
+
+cudaError_t launch_lora_sums(const LoraMaps& maps, const LoraParams& p, cudaStream_t s) {
+  const bool few = p.M <= kLoraFewRows;
+  if (!few) {
     static std::atomic<int> configured_device{-1};
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device.load(std::memory_order_relaxed) != dev) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaError_t e = cudaFuncSetAttribute(lora_sums_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lora::kTileArena + 1024);
       if (e != cudaSuccess) return e;
       configured_device.store(dev, std::memory_order_relaxed);
     }
   }
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)((units + (scans + p.split - 1) / p.split) * p.split));
-  lc.blockDim = dim3(lora::kThreads);
-  lc.dynamicSmemBytes = smem;
+  lc.gridDim = dim3((unsigned)p.grid);
+  lc.blockDim = dim3(few ? lora::kFewThreads : lora::kTileThreads);
+  lc.dynamicSmemBytes = few ? 0 : lora::kTileArena + 1024;
   lc.stream = s;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.split;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = p.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&lc, kernel, p);
+  lc.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&lc, lora_sums_few_kernel, p) : cudaLaunchKernelEx(&lc, lora_sums_many_kernel, maps, p);
 }
 
 cudaError_t launch_lora_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {

@@ -60,6 +60,9 @@ static_assert(kStreamSmem <= 232448, "shared memory budget");
 // ---- adapters
 constexpr int kLoraWarp = kThreads / 32;  // two warps more
 constexpr int kLoraThreads = kThreads + 64;
+// The stream form leaves room on its SM for a CTA of the sums, which it starts beside: 16 K registers and 13 KB
+constexpr int kLoraStreamArena = 192 * 1024;
+constexpr int kLoraStreamBound = 512;  // threads that the registers of a thread are bounded for, to 128
 
 }  // namespace lin
 
@@ -198,13 +201,17 @@ __device__ __forceinline__ void activate_all(int act, float (&v)[kN]) {
 template <int kCols, bool kNotFinite = false>
 __device__ __forceinline__ void add_adapter(const LinearParams& p, int adapter, int64_t m, int64_t n, int cols, float (&f)[kCols]) {
   if ((uint32_t)adapter >= (uint32_t)p.lora_count) return;
-  const float* s = p.lora_s + m * p.lora_rank;
   const __nv_bfloat16* b = p.lora_b + ((int64_t)adapter * p.lora_rows + n) * p.lora_rank;
   auto add = [](float& f, float s, float b) {
     if (!kNotFinite || !isfinite(b)) f += s * b;
   };
   for (int j = 0; j < p.lora_rank; j += 8) {
-    const float4 lo = *reinterpret_cast<const float4*>(s + j), hi = *reinterpret_cast<const float4*>(s + j + 4);
+    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+    for (int c = 0; c < p.lora_parts; ++c) {
+      const float4* s = reinterpret_cast<const float4*>(p.lora_s + c * p.lora_part + m * p.lora_rank + j);
+      lo = make_float4(lo.x + s[0].x, lo.y + s[0].y, lo.z + s[0].z, lo.w + s[0].w);
+      hi = make_float4(hi.x + s[1].x, hi.y + s[1].y, hi.z + s[1].z, hi.w + s[1].w);
+    }
 #pragma unroll
     for (int k = 0; k < kCols; ++k) {
       if (k < cols) {
@@ -246,12 +253,14 @@ __device__ __forceinline__ void init_adapters(AdapterShared& a, int n_stages, in
   a.not_finite = 0;
 }
 
+__device__ __forceinline__ int adapters_of(const int32_t* list) { return (int)min((uint32_t)list[0], 256u); }
+
 // A list in a warp's registers: entry 32 k + lane in e[k].
 struct AdapterList {
   int n, e[8];
   __device__ __forceinline__ void load(const LinearParams& p, int64_t block) {
     const int32_t* list = p.lora_lists + block * kLoraListInts;
-    n = list[0];
+    n = adapters_of(list);
 #pragma unroll
     for (int k = 0; k < 8; ++k) e[k] = 32 * k + (int)(threadIdx.x & 31) < n ? list[4 + 32 * k + (threadIdx.x & 31)] : 0;
   }
@@ -265,11 +274,20 @@ struct AdapterList {
 };
 
 // Ranks 32 c .. of a row's sums as pairs of BF16 numbers: the leading bits, and what they leave; zeros past the rank.
-__device__ __forceinline__ void split_sums(const float* s, int left, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, int left, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+  float4 sum[8] = {};
+#pragma unroll 2
+  for (int c = 0; c < p.lora_parts; ++c) {
+    const float4* s = reinterpret_cast<const float4*>(p.lora_s + c * p.lora_part + m * p.lora_rank + r0);
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 4 * j < left ? s[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = make_float4(sum[j].x + v[j].x, sum[j].y + v[j].y, sum[j].z + v[j].z, sum[j].w + v[j].w);
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float4 v = 4 * j < left ? *reinterpret_cast<const float4*>(s + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float f[4] = {v.x, v.y, v.z, v.w};
+    const float f[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
     uint32_t h[4];
     float r[4];
 #pragma unroll
@@ -307,8 +325,10 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
                                                uint32_t& loaded_bits, const Ctl& ctl) {
   if (u0 >= u1) return true;
   const int lane = threadIdx.x & 31, ranks = p.lora_rank;
-  uint32_t flag = 0;
-  for (int g = lane; g < p.lora_scans; g += 32) flag |= p.lora_flags[block * p.lora_scans + g];
+  uint32_t flag = 0;  // (at most 128 scans)
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if (32 * g + lane < p.lora_scans) flag |= p.lora_flags[block * p.lora_scans + 32 * g + lane];
   const bool found = __any_sync(0xffffffffu, flag);
   int own[2];  // the adapters of this lane's rows
 #pragma unroll
@@ -329,7 +349,7 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
         c_held = c;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          split_sums(p.lora_s + (row0 + (2 * half + i) * 32 + lane) * ranks + 32 * c, own[i] >= 0 ? ranks - 32 * c : 0, hi[i], lo[i]);
+          split_sums(p, row0 + (2 * half + i) * 32 + lane, 32 * c, own[i] >= 0 ? ranks - 32 * c : 0, hi[i], lo[i]);
       }
       const int adapter = list.at(d);
       if (h == 0) {
@@ -606,6 +626,8 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
       tile_at(t, mt, nt);
       const int ym = mt * 256 + (int)rank * 128;
       const int yn = kGated ? nt * (BN / 2) + (rank ? (int)p.N : 0) : nt * BN + (int)rank * (BN / 2);
+      [[maybe_unused]] AdapterList list;
+      if (kLora && t != first) list.load(p, mt);  // of the first tile when the sums are there
       for (int kb = 0, x = 0; kb < KB; ++kb, x += kKps * lin::kBK) {
         if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
           ok = false;
@@ -628,9 +650,10 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
       }
       if constexpr (kLora) {
         if (!ok) break;
-        if (t == first && p.lora_early) ptx::griddep_wait();
-        AdapterList list;
-        list.load(p, mt);
+        if (t == first) {
+          if (p.lora_early) ptx::griddep_wait();
+          list.load(p, mt);
+        }
         const int units = list.n * rank_chunks;
         for (int u = 0, c = 0, d = 0; u < units; u += kKps) {
           if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
@@ -700,6 +723,11 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
         if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
+        [[maybe_unused]] int count = 0, mt, nt;
+        if constexpr (kLora) {
+          tile_at(t, mt, nt);
+          if (n == left && t != first) count = adapters_of(p.lora_lists + (int64_t)mt * kLoraListInts);
+        }
         uint32_t accumulate = 0;
         for (int kb = 0; kb < n; ++kb) {
           if (!warp_wait_quick(full0 + 8 * stage, kLora ? full_bits >> stage & 1 : phase, ctl)) {
@@ -728,10 +756,11 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
         }
         if constexpr (kLora) {
           if (ok && n == left) {  // the tile's last accumulator takes the adapters
-            if (t == first && p.lora_early) ptx::griddep_wait();
-            int mt, nt;
-            tile_at(t, mt, nt);
-            const int count = p.lora_lists[(int64_t)mt * kLoraListInts], units = count * rank_chunks;
+            if (t == first) {
+              if (p.lora_early) ptx::griddep_wait();
+              count = adapters_of(p.lora_lists + (int64_t)mt * kLoraListInts);
+            }
+            const int units = count * rank_chunks;
             for (int u = 0; u < units; u += kKps) {
               if (!(ok = __all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&ad.built[stage]), built_bits >> stage & 1, ctl)))) break;
               built_bits ^= 1u << stage;
@@ -771,6 +800,9 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
       int stage = 0;
       uint32_t loaded_bits = 0;
       if (p.lora_early) ptx::griddep_wait();
+      if (half == 0)
+        for (int i = blockIdx.x * 32 + lane; i < p.lora_err_count; i += gridDim.x * 32)
+          if (const uint32_t e = p.lora_errs[i]) atomicOr(s_err, e);
       for (int t = first; t < tiles; t += pairs) {
         int mt, nt;
         tile_at(t, mt, nt);
@@ -921,14 +953,15 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
 // Cluster c takes the tiles c, c + clusters, ...; its CTA of rank r the K blocks [KB r / S, KB (r + 1) / S).
 // A tile is 128 rows of W; with the gated activation 64 gate rows and the 64 up rows of the same columns.
 template <int kAct, bool kF32, bool kLora>
-__global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kThreads, 1)
+__global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads, 1)
     linear_stream_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   constexpr int kCols = kGated ? 64 : 128;  // columns of y per tile
   constexpr int kEpi = lin::kThreads - 64, kKps = lin::kStreamKps;  // kEpi: the epilogue's threads
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::kStreamArena);
+  constexpr int kArena = kLora ? lin::kLoraStreamArena : lin::kStreamArena;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kArena);
   uint64_t* empty = full + lin::kStreamMaxStages;
   uint64_t* accf = empty + lin::kStreamMaxStages;
   uint64_t* acce = accf + 2;
@@ -947,7 +980,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kThreads, 1)
   const int clusters = gridDim.x / S, first = blockIdx.x / S, tiles = p.tiles_n;
   // [T][128]: in the ring's place when no tile follows, whose loads would write there
   float* part = reinterpret_cast<float*>(smem + (tiles <= clusters ? 0 : n_stages * stage_bytes));
-  [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kStreamArena + lin::kStreamBars * 8 + 32);
+  [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + kArena + lin::kStreamBars * 8 + 32);
   [[maybe_unused]] const int rank_chunks = (p.lora_rank + 31) / 32;  // kLora: blocks of an adapter
   // one accumulator, or two in turn for the chunks of FP32 results
   const uint32_t acc_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128), tmem_cols = kF32 ? 2 * acc_cols : acc_cols;
@@ -1119,7 +1152,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kThreads, 1)
       if constexpr (kLora) {
         if (ok && k1 == kb1) {  // the tile's last accumulator takes the adapters
           if (t == first && !p.beside) ptx::griddep_wait();
-          const int count = p.lora_lists[0], u0 = count * rank_chunks * (int)rank / S, u1 = count * rank_chunks * ((int)rank + 1) / S;
+          const int count = adapters_of(p.lora_lists), u0 = count * rank_chunks * (int)rank / S, u1 = count * rank_chunks * ((int)rank + 1) / S;
           for (int u = u0; u < u1; u += kKps) {
             if (!(ok = warp_wait_quick(ptx::smem_u32(&ad.built[stage]), built_bits >> stage & 1, ctl))) break;
             built_bits ^= 1u << stage;
@@ -1333,19 +1366,19 @@ template <int kAct, bool kF32, bool kLora>
 static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
   auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct, kF32, kLora>
                                         : (p.kps == 1 ? linear_pair_kernel<kAct, 1, kF32, kLora> : linear_pair_kernel<kAct, 2, kF32, kLora>);
-  constexpr int kMore = kLora ? (int)sizeof(AdapterShared) : 0;
-  static_assert(lin::kStreamSmem + kMore <= 232448 && lin::kPairSmem + kMore <= 232448, "shared memory budget");
-  const int smem = (p.form == kLinearStream ? lin::kStreamSmem : lin::kPairSmem) + kMore;
+  constexpr int kMore = kLora ? (int)sizeof(AdapterShared) : 0, kPairBytes = lin::kPairSmem + kMore;
+  constexpr int kStreamBytes = lin::kStreamSmem - (kLora ? lin::kStreamArena - lin::kLoraStreamArena : 0) + kMore;
+  static_assert(kStreamBytes <= 232448 && kPairBytes <= 232448, "shared memory budget");
+  const int smem = p.form == kLinearStream ? kStreamBytes : kPairBytes;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         lin::kStreamSmem + kMore);
+    cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<kAct, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem + kMore);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 1, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kPairSmem + kMore);
+      e = cudaFuncSetAttribute(linear_pair_kernel<kAct, 2, kF32, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }

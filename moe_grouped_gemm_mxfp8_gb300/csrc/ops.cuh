@@ -104,7 +104,9 @@ struct LinearParams {
   // adapters
   const int32_t* lora_ids;       // [M]: each row's adapter, -1 none
   const __nv_bfloat16* lora_b;   // second factors [count, rows, rank]
-  float* lora_s;                 // [M, rank]: each row's sums of its adapter's first factor, scaled
+  float* lora_s;                 // [parts, M, rank]: each row's sums of its adapter's first factor, scaled, to be added up
+  int64_t lora_part;             // from one part to the next
+  int32_t lora_parts;
   int32_t lora_count, lora_rank;
   int64_t lora_rows;
   // of each 256 rows: kLoraListInts words, the number of adapters and from the fourth on each, in the order of their first
@@ -112,6 +114,8 @@ struct LinearParams {
   const int32_t* lora_lists;
   const uint32_t* lora_flags;
   int32_t lora_scans;
+  const uint32_t* lora_errs;  // error bits of the sums' CTAs, which the pair form passes on
+  int32_t lora_err_count;
   int32_t lora_early;  // pair form: it may start before the sums are there
 };
 struct LinearMaps {
@@ -126,7 +130,7 @@ struct LoraParams {
   const __nv_bfloat16 *x, *a;  // [M, K], row stride ldx; first factors [count, rank, K]
   const float* scale;          // [count] or null
   const int32_t* ids;          // [M]
-  float* s;                    // [M, rank]
+  float* s;                    // [parts, M, rank]
   int64_t M, K, ldx;
   int32_t count, rank;
   const __nv_bfloat16* b;      // second factors [count, rows, rank], which are scanned
@@ -134,9 +138,19 @@ struct LoraParams {
   int32_t* lists;              // as LinearParams'
   uint32_t* flags;
   int32_t scans;               // CTAs to a list; 0: no lists
-  int32_t split, depth;        // launch_lora_sums' choice: CTAs of a cluster, clusters that share a tile's adapters
+  uint32_t* errs;              // [grid], error bits of each CTA: more than kLoraFewRows rows
+  int64_t timeout_ns;
+  int32_t test_stall;
+  // plan_lora_sums' choice: shares of the K range, CTAs to a tile's passes (many rows), CTAs in all, and the parts that a
+  // sum is left in, M rows after one another; it also bounds scans
+  int32_t split, passes, grid, parts;
 };
-cudaError_t launch_lora_sums(LoraParams p, int sms, cudaStream_t s);
+struct LoraMaps {
+  CUtensorMap x, a;  // [M, K], boxes of 128 rows; first factors, boxes of 16 rows: more than kLoraFewRows rows
+};
+constexpr int kLoraFewRows = 128;
+void plan_lora_sums(LoraParams& p, int sms);
+cudaError_t launch_lora_sums(const LoraMaps& maps, const LoraParams& p, cudaStream_t s);
 cudaError_t launch_lora_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
 cudaError_t launch_linear_repitch(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t rows, int64_t K, int64_t Kp,
                                   int64_t ld, int sms, cudaStream_t s);
