@@ -357,7 +357,8 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     sums.ldx = lp.ldx;
     sums.a = static_cast<const __nv_bfloat16*>(adapters->a);
     sums.b = lp.lora_b;
-    sums.scale = adapters->scale;
+    lp.lora_a = sums.a;
+    lp.lora_scale = sums.scale = adapters->scale;
     sums.ids = adapters->ids;
     lp.lora_parts = sums.parts;
     lp.lora_part = p.M * sums.rank;
@@ -375,6 +376,10 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
   if (adapters && parts[0].form == gmmfr::kLinearDirect) {  // which needs no lists
     sums.scans = 0;
     gmmfr::plan_lora_sums(sums, sms);
+    // What each CTA reads besides its weights comes from L2.  One token, rank 16, replayed: 2048 x 2048 5.8 us, with the sums'
+    // launch 7.2; 4096 x 4096 9.0 and 7.3.  Rank 32 of 1024 x 4096: 7.3 and 7.6.
+    const int64_t units = p.M * cdiv(sums.rank, 16);
+    parts[0].lora_own = units <= 2 && units * p.K <= 2048;
   }
   if (adapters && p.M > gmmfr::kLoraFewRows) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
@@ -404,7 +409,7 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     cudaError_t e = gmmfr::launch_linear_repitch(static_cast<const __nv_bfloat16*>(weight), w_copy, rows_w, p.K, Kp, stride_or(p.ldw, p.K), sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "weight copy launch");
   }
-  if (adapters) {
+  if (adapters && !parts[0].lora_own) {
     cudaError_t e = gmmfr::launch_lora_sums(sum_maps, sums, s);
     if (e != cudaSuccess) return cuda_fail(e, "adapters' sums launch");
   }

@@ -145,8 +145,9 @@ __device__ void list_and_scan(const LoraParams& p, int64_t i, int t) {
 }  // namespace
 
 // ============================================================================ few rows
-// CTA (d, r): the d-th adapter in the order of the rows, ranks 16 r and up; where there are fewer adapters than places for
-// them, several places share an adapter's rows.  The last CTAs list and scan.
+// CTA (d, r, c): the d-th adapter in the order of the rows, ranks 16 r and up, share c of the K range (more than one where a
+// warp's loads would not all be on their way at once); where there are fewer adapters than places for them, several places
+// share an adapter's rows.  The last CTAs list and scan.
 __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(const __grid_constant__ LoraParams p) {
   constexpr int kU = 8, kWarps = lora::kFewThreads / 32;
   __shared__ __align__(16) int s_id[kLoraFewRows];
@@ -155,12 +156,12 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
   __shared__ __align__(16) float part[8 * kWarps][16];
   static_assert(8 * kWarps >= kLoraFewRows, "a slot for each row");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rc = (p.rank + 15) / 16, places = (int)min(p.M, (int64_t)p.count);
+  const int rc = (p.rank + 15) / 16, places = (int)min(p.M, (int64_t)p.count), items = places * rc * p.split;
   // the launch after this one reads x and its weights without waiting for this one: it may start when all before has ended
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  if (blockIdx.x >= places * rc) {
-    list_and_scan<lora::kFewThreads>(p, blockIdx.x - places * rc, tid);
+  if (blockIdx.x >= items) {
+    list_and_scan<lora::kFewThreads>(p, blockIdx.x - items, tid);
     return;
   }
   int id = -1;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
   int n = 0;
 #pragma unroll
   for (int w = 0; w < 4; ++w) n += __popc(s_first[w]);
-  const int place = blockIdx.x / rc, r0 = blockIdx.x % rc * 16;
+  const int c = blockIdx.x % p.split, place = blockIdx.x / p.split / rc, r0 = blockIdx.x / p.split % rc * 16;
   const int shares = n ? places / n : 0;  // of an adapter's rows
   if (place >= n * shares) return;
   const int share = place / n;
@@ -205,21 +206,21 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
   int sharing = 1;
   while (sharing < tiles) sharing *= 2;
   const int splits = kWarps / sharing, split = warp % splits, t = warp / splits;
-  const int blocks = (int)((p.K + 31) / 32);
+  const int blocks = (int)((p.K + 31) / 32), b_begin = blocks * c / p.split, b_end = blocks * (c + 1) / p.split;
   if (t < tiles) {
     const __nv_bfloat16* ar = p.a + ((int64_t)a * p.rank + r0) * p.K;
     const __nv_bfloat16* const xr[1] = {p.x + (int64_t)s_row[min((tile0 + t) * 8 + (lane >> 2), rows - 1)] * p.ldx};
     float acc[1][1][4] = {};
-    for (int b0 = split; b0 < blocks; b0 += splits * kU) {
+    for (int b0 = b_begin + split; b0 < b_end; b0 += splits * kU) {
       SumOperands<1, 1> o[kU];
 #pragma unroll
       for (int v = 0; v < kU; ++v) {
         const int64_t k = (int64_t)(b0 + splits * v) * 32 + (lane & 3) * 8;
-        o[v].load(ar, p.rank - r0, p.K, xr, k, k < p.K);
+        o[v].load(ar, p.rank - r0, p.K, xr, k, b0 + splits * v < b_end && k < p.K);
       }
 #pragma unroll
       for (int v = 0; v < kU; ++v) {
-        o[v].keep((int64_t)(b0 + splits * v) * 32 + (lane & 3) * 8 < p.K);
+        o[v].keep(b0 + splits * v < b_end && (int64_t)(b0 + splits * v) * 32 + (lane & 3) * 8 < p.K);
         o[v].multiply(acc);
       }
     }
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
       const float4 z = sums[s * tiles * 32 + i];
       v = make_float4(v.x + z.x, v.y + z.y, v.z + z.z, v.w + z.w);
     }
-    *reinterpret_cast<float4*>(p.s + (int64_t)s_row[row] * p.rank + r) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    *reinterpret_cast<float4*>(p.s + (c * p.M + s_row[row]) * p.rank + r) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
   }
 }
 
@@ -415,7 +416,9 @@ void plan_lora_sums(LoraParams& p, int sms) {
   const int64_t ranks = (p.rank + 15) / 16;
   p.split = p.passes = p.parts = 1;
   if (p.M <= kLoraFewRows) {
-    const int64_t items = std::min<int64_t>(p.M, p.count) * ranks;
+    int64_t items = std::min<int64_t>(p.M, p.count) * ranks;
+    if (p.K > 2048 && 2 * items + 64 <= sms) p.split = p.parts = 2;
+    items *= p.split;
     // scans on the SMs that are left (each a word that who reads the list looks at)
     p.scans = (int32_t)std::min<int64_t>(p.scans, std::clamp<int64_t>(sms - items, 64, 128));
     p.grid = (int32_t)(items + p.scans);

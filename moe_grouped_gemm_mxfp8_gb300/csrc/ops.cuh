@@ -116,6 +116,9 @@ struct LinearParams {
   int32_t lora_scans;
   const uint32_t* lora_errs;  // error bits of the sums' CTAs, which the pair form passes on
   int32_t lora_err_count;
+  int32_t lora_own;           // direct form: each CTA makes the sums itself, of at most two units of 16 ranks
+  const __nv_bfloat16* lora_a;  // first factors and scales, for those
+  const float* lora_scale;
   int32_t lora_early;  // pair form: it may start before the sums are there
 };
 struct LinearMaps {
