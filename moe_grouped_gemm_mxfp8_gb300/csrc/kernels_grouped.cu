@@ -44,8 +44,8 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kGradStages = 5;
 constexpr int kGradStage = 2 * kTileBytes;               // 64 rows of 128 columns of either operand
 constexpr int kGradTurnOff = kGradStages * kGradStage;   // 4 KB for each of 8 epilogue warps
-constexpr int kGradBarOff = kGradTurnOff + 8 * 4096;     // full, empty, peer, accf[2], acce[2], drain
-constexpr int kGradEndOff = kGradBarOff + (3 * kGradStages + 5) * 8;
+constexpr int kGradBarOff = kGradTurnOff + 8 * 4096;     // full, empty, landed, peer, accf[2], acce[2], drain
+constexpr int kGradEndOff = kGradBarOff + (4 * kGradStages + 5) * 8;
 constexpr int kGradScanOff = kGradEndOff + 4 * kMaxExperts;
 constexpr int kGradMiscOff = kGradScanOff + 8 * (kThreads / 32);
 constexpr int kGradSmem = kGradMiscOff + 32 + 1024;
@@ -422,16 +422,19 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
 }
 
 // ============================================================================ weights
-// Unit u is tile u % (TA TB) of expert u / (TA TB); pair c takes the units c, c + pairs, ...  Each CTA's loads count on
-// its own barrier; its warp 1 puts zeros in place of rows past the expert's last, and rank 1's tells rank 0's.
+// Unit u is tile u % (TA TB) of expert u / (TA TB); pair c takes the units c, c + pairs, ...  Both CTAs' loads count on rank
+// 0's barrier, but for an expert's last rows where their number is not a multiple of 16 (a product's K): these count on
+// each CTA's own, its warp 1 puts zeros in place of the rows that follow, and rank 1's tells rank 0's.  (With that way for
+// all rows, which takes some 500 cycles longer, 65536 rows of 64 experts, 2048 x 1024: 200 us.)
 template <bool kF32>
 __global__ void __launch_bounds__(grp::kThreads, 1)
     grouped_grad_kernel(const __grid_constant__ GroupedGradMaps maps, const __grid_constant__ GroupedGradParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + grp::kGradBarOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + grp::kGradBarOff);  // used in rank 0: both CTAs' loads
   uint64_t* empty = full + grp::kGradStages;
-  uint64_t* peer = empty + grp::kGradStages;  // used in rank 0: rank 1's stage is full
+  uint64_t* landed = empty + grp::kGradStages;  // last rows
+  uint64_t* peer = landed + grp::kGradStages;   // used in rank 0: rank 1's last rows are ready
   uint64_t* accf = peer + grp::kGradStages;
   uint64_t* acce = accf + 2;  // used in rank 0: both CTAs' epilogue warps
   uint64_t* drain = acce + 2;
@@ -448,6 +451,7 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
     for (int s = 0; s < grp::kGradStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&landed[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&peer[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -492,7 +496,8 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
 
   if (warp == 0) {
     const uint64_t pol = ptx::l2_evict_last_policy();
-    const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty);
+    const uint32_t full_own = ptx::smem_u32(full), full0 = ptx::map_to_rank(full_own, 0), landed0 = ptx::smem_u32(landed),
+                   empty0 = ptx::smem_u32(empty);
     int stage = 0;
     uint32_t phase = 0, sb = smem_base;
     bool ok = true;
@@ -507,12 +512,20 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
           break;
         }
         if (ptx::elect_one()) {
-          const uint32_t fb = full0 + 8 * stage;
-          ptx::mbar_arrive_expect_tx(fb, grp::kGradStage);
-          ptx::tma_load_2d(sb, &maps.a, xa, start + r, fb, pol);
-          ptx::tma_load_2d(sb + 8192, &maps.a, xa + 64, start + r, fb, pol);
-          ptx::tma_load_2d(sb + grp::kTileBytes, &maps.b, xb, start + r, fb, pol);
-          ptx::tma_load_2d(sb + grp::kTileBytes + 8192, &maps.b, xb + 64, start + r, fb, pol);
+          const bool last = rows - r < grp::kBK && rows % 16;
+          auto load = [&](auto copy, uint32_t bar) {
+            copy(sb, &maps.a, xa, start + r, bar, pol);
+            copy(sb + 8192, &maps.a, xa + 64, start + r, bar, pol);
+            copy(sb + grp::kTileBytes, &maps.b, xb, start + r, bar, pol);
+            copy(sb + grp::kTileBytes + 8192, &maps.b, xb + 64, start + r, bar, pol);
+          };
+          if (last) {
+            ptx::mbar_arrive_expect_tx(landed0 + 8 * stage, grp::kGradStage);
+            load([](auto... a) { ptx::tma_load_2d(a...); }, landed0 + 8 * stage);
+          } else {
+            if (rank == 0) ptx::mbar_arrive_expect_tx(full_own + 8 * stage, 2 * grp::kGradStage);
+            load([](auto... a) { ptx::tma_load_2d_pair(a...); }, full0 + 8 * stage);
+          }
         }
         sb += grp::kGradStage;
         if (++stage == grp::kGradStages) {
@@ -529,65 +542,72 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
         phase ^= 1;
       }
     }
-    if (!ok)  // aborted: let what is in flight land
-      for (int s = 0; s < grp::kGradStages; ++s) wait_bar_drain(ptx::smem_u32(&full[s]), s < stage ? phase : phase ^ 1);
+    if (!ok) let_loads_land();  // aborted
     __syncwarp();
   } else if (warp == 1) {
     // kind::f16: FP32 accumulator, A and B BF16, M = N = 256; bits 15, 16: A and B run along M and N
     constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (3u << 15) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
     const uint64_t da0 = ptx::smem_desc(smem_base, 8192, 1024, ptx::kSwizzle128B);
     const uint32_t desc_hi = (uint32_t)(da0 >> 32);
-    const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty), peer0 = ptx::smem_u32(peer);
+    const uint32_t full0 = ptx::smem_u32(full), empty0 = ptx::smem_u32(empty), landed0 = ptx::smem_u32(landed),
+                   peer0 = ptx::smem_u32(peer);
     int stage = 0, acc_i = 0;
-    uint32_t phase = 0;
+    uint32_t full_bits = 0, landed_bits = 0, peer_bits = 0;  // a barrier's phase by its own uses
     bool ok = true;
+    // an expert's last rows, when they have landed: zeros up to the next 16 in each box of 64 columns
+    auto end_rows = [&](int valid) {
+      if (!warp_wait_quick(landed0 + 8 * stage, landed_bits >> stage & 1, ctl)) return false;
+      landed_bits ^= 1u << stage;
+      uint8_t* at = smem + stage * grp::kGradStage + (lane >> 3) * 8192 + (lane & 7) * 16;
+      for (int r = valid; r & 15; ++r) *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      return true;
+    };
     for (int64_t u = first; ok && u < units; u += pairs) {
       int e, ta, tb, start;
       unit_at(u, e, ta, tb);
       const int rows = rows_of(e, start), blocks = (rows + grp::kBK - 1) / grp::kBK;
+      if (rank == 1) {
+        if (rows % 16) {
+          stage = (stage + blocks - 1) % grp::kGradStages;
+          if (!(ok = end_rows(rows - (blocks - 1) * grp::kBK))) break;
+          if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(peer0 + 8 * stage, 0));
+          stage = (stage + 1) % grp::kGradStages;
+        } else {
+          stage = (stage + blocks) % grp::kGradStages;
+        }
+        continue;
+      }
       for (int k0 = 0; ok && k0 < blocks; k0 += kPer) {
         const int n = min(kPer, blocks - k0), buf = acc_i & 1;
-        if (rank == 0) {
-          if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
+        if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) {
+          ok = false;
+          break;
         }
+        ptx::tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
         for (int kb = 0; kb < n; ++kb) {
-          if (!warp_wait_quick(full0 + 8 * stage, phase, ctl)) {
-            ok = false;
-            break;
+          const int valid = min(grp::kBK, rows - (k0 + kb) * grp::kBK);
+          if (valid & 15) {
+            ok = end_rows(valid) && __all_sync(0xffffffffu, wait_bar_cluster(peer0 + 8 * stage, peer_bits >> stage & 1, ctl));
+            peer_bits ^= 1u << stage;
+          } else {
+            ok = warp_wait_quick(full0 + 8 * stage, full_bits >> stage & 1, ctl);
+            full_bits ^= 1u << stage;
           }
-          const int valid = min(grp::kBK, rows - (k0 + kb) * grp::kBK), steps = (valid + 15) / 16;
-          if (valid & 15) {  // the rows up to the next 16: zeros in each box of 64 columns
-            uint8_t* at = smem + stage * grp::kGradStage + (lane >> 3) * 8192 + (lane & 7) * 16;
-            for (int r = valid; r < steps * 16; ++r) *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (rank == 0) {
-            if (!__all_sync(0xffffffffu, wait_bar_cluster(peer0 + 8 * stage, phase, ctl))) {
-              ok = false;
-              break;
-            }
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              const uint32_t la = (uint32_t)da0 + stage * (grp::kGradStage >> 4), lb = la + (grp::kTileBytes >> 4);
-              for (int q = 0; q < steps; ++q)
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint32_t la = (uint32_t)da0 + stage * (grp::kGradStage >> 4), lb = la + (grp::kTileBytes >> 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (16 * q < valid)
                 ptx::tc_mma_f16_pair_lo(d, la + q * (2048 >> 4), lb + q * (2048 >> 4), desc_hi, idesc, kb + q > 0 ? 1u : 0u);
-              ptx::tc_commit_pair(empty0 + 8 * stage);
-              if (kb == n - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
-            }
-          } else if (lane == 0) {
-            ptx::mbar_arrive_remote(ptx::map_to_rank(peer0 + 8 * stage, 0));
+            ptx::tc_commit_pair(empty0 + 8 * stage);
+            if (kb == n - 1) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
           }
-          __syncwarp();
-          if (++stage == grp::kGradStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          if (++stage == grp::kGradStages) stage = 0;
         }
         ++acc_i;
       }
