@@ -15,7 +15,7 @@
 namespace gmmfr {
 namespace lora {
 constexpr int kFewThreads = 512;
-constexpr int kTileThreads = 320, kTileStages = 10, kTileArena = 10 * (lin::kTileBytes + 2048);
+constexpr int kTileThreads = 448, kTileStages = 10, kTileArena = 10 * (lin::kTileBytes + 2048);
 }  // namespace lora
 
 namespace {
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
 // ============================================================================ many rows
 // CTA (c, p, tile): the 128 rows of a tile, share c of the K range, every `passes`-th pass from p on of up to 16 units: 16 ranks of
 // an adapter.  Who reads the sums adds the shares' parts.  (Clusters that join them on the chip wait for SMs that lie
-// together: 16 us more with clusters of 8.)  Warp 0 TMA, warp 1 MMA, warps 2..9 lists and
-// scans, the first four of them the epilogue.
+// together: 16 us more with clusters of 8.)  Warp 0 TMA, warp 1 MMA, warps 2..5
+// epilogue, warps 6..13 lists and scans.
 __global__ void __launch_bounds__(lora::kTileThreads, 1)
     lora_sums_many_kernel(const __grid_constant__ LoraMaps maps, const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -371,10 +371,9 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(&drain));
     wait_bar_drain(ptx::smem_u32(&drain), 0);
     __syncwarp();
+  } else if (warp >= 6) {
+    if (blockIdx.x < p.scans * ((p.M + 255) / 256)) list_and_scan<256>(p, blockIdx.x, tid - 192);
   } else {
-    if (blockIdx.x < p.scans * ((p.M + 255) / 256)) list_and_scan<256>(p, blockIdx.x, tid - 64);
-  }
-  if (warp >= 2 && warp < 6) {
     const int q = warp & 3, row = q * 32 + lane, mine = s_id[row];
     const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
     const float scale = mine >= 0 && p.scale ? p.scale[mine] : 1.f;
