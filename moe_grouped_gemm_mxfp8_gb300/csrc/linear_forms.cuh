@@ -256,51 +256,79 @@ __device__ __forceinline__ void init_adapters(AdapterShared& a, int n_stages, in
 
 __device__ __forceinline__ int adapters_of(const int32_t* list) { return (int)min((uint32_t)list[0], 256u); }
 
-// A list in a warp's registers: entry 32 k + lane in e[k].
+// A list in a warp's registers: entry 32 k + lane in e[k] (past the last: whatever lies there).
 struct AdapterList {
   int n, e[8];
   __device__ __forceinline__ void load(const LinearParams& p, int64_t block) {
     const int32_t* list = p.lora_lists + block * kLoraListInts;
     n = adapters_of(list);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = 32 * k + (int)(threadIdx.x & 31) < n ? list[4 + 32 * k + (threadIdx.x & 31)] : 0;
+    for (int k = 0; k < 8; ++k) e[k] = list[4 + 32 * k + (threadIdx.x & 31)];
   }
-  __device__ __forceinline__ int at(int d) const {
+  __device__ __forceinline__ int row_of(int k) const {
     int v = e[0];
 #pragma unroll
-    for (int k = 1; k < 8; ++k)
-      if (d >> 5 == k) v = e[k];
-    return __shfl_sync(0xffffffffu, v, d & 31);
+    for (int i = 1; i < 8; ++i)
+      if (k == i) v = e[i];
+    return v;
   }
 };
 
-// Ranks 32 c .. of a row's sums as pairs of BF16 numbers: the leading bits, and what they leave; zeros past the rank.
-__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, int left, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-  float4 sum[8] = {};
-#pragma unroll 2
-  for (int c = 0; c < p.lora_parts; ++c) {
-    const float4* s = reinterpret_cast<const float4*>(p.lora_s + c * p.lora_part + m * p.lora_rank + r0);
-    float4 v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 4 * j < left ? s[j] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = make_float4(sum[j].x + v[j].x, sum[j].y + v[j].y, sum[j].z + v[j].z, sum[j].w + v[j].w);
+// The adapters of a tile's blocks one after the other: all of a list for ranks 0 to 31, then for 32 to 63, ...
+struct AdapterBlocks {
+  const AdapterList& list;
+  int c, d, held;  // ranks 32 c and up of entry d; the 32 entries that hold it
+  __device__ __forceinline__ AdapterBlocks(const AdapterList& list, int u) : list(list) {
+    c = list.n ? u / list.n : 0;
+    d = u - c * list.n;
+    held = list.row_of(d >> 5);
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
-    uint32_t h[4];
-    float r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      h[k] = __float_as_uint(f[k]) & 0xffff0000u;
-      r[k] = isfinite(f[k]) ? f[k] - __uint_as_float(h[k]) : 0.f;
+  __device__ __forceinline__ int adapter() const { return __shfl_sync(0xffffffffu, held, d & 31); }
+  __device__ __forceinline__ void next() {
+    if (++d == list.n) {
+      d = 0;
+      ++c;
     }
-    hi[2 * j] = h[0] >> 16 | h[1];
-    hi[2 * j + 1] = h[2] >> 16 | h[3];
-    lo[2 * j] = pack_bf16(r[0], r[1]);
-    lo[2 * j + 1] = pack_bf16(r[2], r[3]);
+    if ((d & 31) == 0) held = list.row_of(d >> 5);
   }
+};
+
+// Ranks r0 .. r0 + 31 of two rows' sums (m and m + 32; past the last row: its own), as pairs of BF16 numbers: the leading bits,
+// and what they leave; zeros past the rank.
+__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, uint32_t (&hi)[2][16], uint32_t (&lo)[2][16]) {
+  const int left = p.lora_rank - r0;
+  float4 sum[2][8] = {};
+  for (int c = 0; c < p.lora_parts; ++c) {
+    float4 v[2][8];  // on their way together
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* s = p.lora_s + c * p.lora_part + min(m + 32 * i, p.M - 1) * p.lora_rank + r0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 4 * j < left ? reinterpret_cast<const float4*>(s)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        sum[i][j] = make_float4(sum[i][j].x + v[i][j].x, sum[i][j].y + v[i][j].y, sum[i][j].z + v[i][j].z, sum[i][j].w + v[i][j].w);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f[4] = {sum[i][j].x, sum[i][j].y, sum[i][j].z, sum[i][j].w};
+      uint32_t h[4];
+      float r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[k] = __float_as_uint(f[k]) & 0xffff0000u;
+        r[k] = isfinite(f[k]) ? f[k] - __uint_as_float(h[k]) : 0.f;
+      }
+      hi[i][2 * j] = h[0] >> 16 | h[1];
+      hi[i][2 * j + 1] = h[2] >> 16 | h[3];
+      lo[i][2 * j] = pack_bf16(r[0], r[1]);
+      lo[i][2 * j + 1] = pack_bf16(r[2], r[3]);
+    }
 }
 
 // Zeros in place of what is not finite in the first 16 steps elements of rows r0 .. r1 - 1, of 128 bytes each (128-byte
@@ -318,76 +346,70 @@ __device__ __noinline__ void drop_not_finite(uint8_t* at, int r0, int r1, int st
 
 // A CTA's adapter warps (`half` 0 and 1) through a tile's blocks u0 .. u1 - 1, kKps to a stage, from `stage` on (a stage whose
 // factors have landed is free).  x_at, w_at: where a block's rows of x and of W lie in its stage; x_rows (128 at most) of
-// them are written, which are p's from row0 on; `to`: the CTA that issues the products, or -1.
+// them are written, which are p's from row0 on; to_rank: the CTA that issues the products, or -1.
 template <int kKps>
 __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterShared& a, uint8_t* smem, int stage_bytes, int block_bytes,
                                                int n_stages, int x_at, int x_rows, int w_at, int w_rows, int64_t block, int64_t row0,
-                                               int half, const AdapterList& list, int u0, int u1, int to, int& stage,
+                                               int half, const AdapterList& list, int u0, int u1, int to_rank, int& stage,
                                                uint32_t& loaded_bits, const Ctl& ctl) {
   if (u0 >= u1) return true;
   const int lane = threadIdx.x & 31, ranks = p.lora_rank;
-  uint32_t flag = 0;  // (at most 128 scans)
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    if (32 * g + lane < p.lora_scans) flag |= p.lora_flags[block * p.lora_scans + 32 * g + lane];
-  const bool found = __any_sync(0xffffffffu, flag);
   int own[2];  // the adapters of this lane's rows
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t m = row0 + (2 * half + i) * 32 + lane;
     own[i] = m < p.M ? p.lora_ids[m] : -1;
-    if ((uint32_t)own[i] >= (uint32_t)p.lora_count) own[i] = -1;
   }
+  uint32_t flag = 0;  // (at most 128 scans)
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if (32 * g + lane < p.lora_scans) flag |= p.lora_flags[block * p.lora_scans + 32 * g + lane];
+  AdapterBlocks at(list, u0);
   uint32_t hi[2][16], lo[2][16];
-  int c = u0 / list.n, d = u0 - c * list.n, c_held = -1;
+  split_sums(p, row0 + 64 * half + lane, 32 * at.c, hi, lo);
+  int c_held = at.c;
+  const bool found = __any_sync(0xffffffffu, flag);
+  const uint32_t smem0 = ptx::smem_u32(smem) + x_at + (64 * half + lane) * 128, turn = lane & 7;
+  const bool write[2] = {64 * half + lane < x_rows, 64 * half + 32 + lane < x_rows};
   for (int u = u0; u < u1; u += kKps) {
-    uint8_t* sb = smem + stage * stage_bytes;
+    const uint32_t xb = smem0 + stage * stage_bytes;
 #pragma unroll
     for (int h = 0; h < kKps; ++h) {
       if (u + h >= u1) break;
-      const int steps = ranks - 32 * c > 16 ? 2 : 1;
-      if (c != c_held) {
-        c_held = c;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          split_sums(p, row0 + (2 * half + i) * 32 + lane, 32 * c, own[i] >= 0 ? ranks - 32 * c : 0, hi[i], lo[i]);
+      const int steps = ranks - 32 * at.c > 16 ? 2 : 1, adapter = at.adapter();
+      if (at.c != c_held) {
+        c_held = at.c;
+        split_sums(p, row0 + 64 * half + lane, 32 * at.c, hi, lo);
       }
-      const int adapter = list.at(d);
       if (h == 0) {
         if (!warp_wait_quick(ptx::smem_u32(&a.loaded[stage]), loaded_bits >> stage & 1, ctl)) return false;
         loaded_bits ^= 1u << stage;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = 32 * (2 * half + i) + lane;
-        if (row >= x_rows) continue;
-        uint8_t* at = sb + h * block_bytes + x_at + row * 128;
-        const uint32_t keep = own[i] == adapter ? 0xffffffffu : 0u;
+        if (!write[i]) continue;
+        const uint32_t to = xb + h * block_bytes + i * 4096, keep = own[i] == adapter ? 0xffffffffu : 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (k >= 2 * steps) break;
-          *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) =
-              make_uint4(hi[i][4 * k] & keep, hi[i][4 * k + 1] & keep, hi[i][4 * k + 2] & keep, hi[i][4 * k + 3] & keep);
-          *reinterpret_cast<uint4*>(at + (((4 + k) ^ (row & 7)) << 4)) =
-              make_uint4(lo[i][4 * k] & keep, lo[i][4 * k + 1] & keep, lo[i][4 * k + 2] & keep, lo[i][4 * k + 3] & keep);
+          ptx::st_shared_v4(to + ((k ^ turn) << 4), hi[i][4 * k] & keep, hi[i][4 * k + 1] & keep, hi[i][4 * k + 2] & keep, hi[i][4 * k + 3] & keep);
+          ptx::st_shared_v4(to + (((4 + k) ^ turn) << 4), lo[i][4 * k] & keep, lo[i][4 * k + 1] & keep, lo[i][4 * k + 2] & keep,
+                            lo[i][4 * k + 3] & keep);
         }
       }
-      if (found) drop_not_finite(sb + h * block_bytes + w_at, half * w_rows / 2, (half + 1) * w_rows / 2, steps);
-      if (++d == list.n) {
-        d = 0;
-        ++c;
-      }
+      if (found) drop_not_finite(smem + stage * stage_bytes + h * block_bytes + w_at, half * w_rows / 2, (half + 1) * w_rows / 2, steps);
+      at.next();
     }
     ptx::fence_proxy_async_smem();
     if (found) {
-      const uint32_t at = ptx::smem_u32(&a.not_finite);
-      if (lane < p.split) ptx::st_cluster_u32(p.split > 1 ? ptx::map_to_rank(at, lane) : at, 1u);
+      const uint32_t flag_at = ptx::smem_u32(&a.not_finite);
+      if (lane < p.split) ptx::st_cluster_u32(p.split > 1 ? ptx::map_to_rank(flag_at, lane) : flag_at, 1u);
       __threadfence();
     }
     __syncwarp();
     if (lane == 0) {
       const uint32_t bar = ptx::smem_u32(&a.built[stage]);
-      if (to >= 0) ptx::mbar_arrive_remote(ptx::map_to_rank(bar, to));
+      if (to_rank >= 0) ptx::mbar_arrive_remote(ptx::map_to_rank(bar, to_rank));
       else ptx::mbar_arrive(bar);
     }
     if (++stage == n_stages) stage = 0;
@@ -709,7 +731,8 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
           list.load(p, mt);
         }
         const int units = list.n * rank_chunks;
-        for (int u = 0, c = 0, d = 0; u < units; u += kKps) {
+        AdapterBlocks next(list, 0);
+        for (int u = 0; u < units; u += kKps) {
           if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
             ok = false;
             break;
@@ -718,12 +741,9 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
           int adapter[kKps], rank0[kKps];
 #pragma unroll
           for (int i = 0; i < kKps; ++i) {
-            rank0[i] = 32 * c;
-            adapter[i] = list.at(d);
-            if (++d == list.n) {
-              d = 0;
-              ++c;
-            }
+            rank0[i] = 32 * next.c;
+            adapter[i] = next.adapter();
+            next.next();
           }
           if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(lb, min(kKps, units - u) * BN * 64);
@@ -1117,7 +1137,8 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
         AdapterList list;
         list.load(p, 0);
         const int n = list.n, u0 = n * rank_chunks * (int)rank / S, u1 = n * rank_chunks * ((int)rank + 1) / S;
-        for (int u = u0, c = u0 < u1 ? u0 / n : 0, d = u0 - c * n; u < u1; u += kKps) {
+        AdapterBlocks next(list, u0);
+        for (int u = u0; u < u1; u += kKps) {
           if (!warp_wait_quick(empty0 + 8 * stage, phase ^ 1, ctl)) {
             ok = false;
             break;
@@ -1126,12 +1147,9 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
           int adapter[kKps], rank0[kKps];
 #pragma unroll
           for (int h = 0; h < kKps; ++h) {
-            rank0[h] = 32 * c;
-            adapter[h] = list.at(d);
-            if (++d == n) {
-              d = 0;
-              ++c;
-            }
+            rank0[h] = 32 * next.c;
+            adapter[h] = next.adapter();
+            next.next();
           }
           if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(lb, min(kKps, u1 - u) * lin::kTileBytes);

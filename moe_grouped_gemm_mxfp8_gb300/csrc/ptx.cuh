@@ -359,6 +359,9 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr_cluster, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_cluster), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 // A load of what nothing writes while the kernel runs, issued where it stands (the compiler moves others down to their use).
 __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
   uint4 v;
