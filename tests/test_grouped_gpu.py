@@ -300,3 +300,40 @@ def test_experts_of_a_block_forwards_and_backwards():
         slope = ((f(*plus) - f(*minus)) / (2 * h) * dy.double()).sum()
         # |error| <= |got - grad| |d|, and |d| = 1
         assert abs(float((got.double() * d).sum() - slope)) < 2 ** -6 * float(got.double().norm())
+
+
+def test_offsets_past_32_bits():
+    """y, the rows and the weights' gradient of more than 2^31 elements each (the ends of them are compared)."""
+    M, N, K = 66000, 32784, 64
+    w = _randn(1, 2, N, K, scale=K ** -0.5)
+    x = _randn(2, M, K)
+    h, g = B.GroupedLinear(w), _list([M - 300, 300], 1)
+    y = h(x, g)
+    few = B.GroupedLinear(w)(x[-300:], _list([0, 300], 1))
+    assert torch.equal(y[-300:], few)
+    dx = h.grad_input(y, g)
+    assert torch.equal(dx[-300:], h.grad_input(few, _list([0, 300], 1)))
+    del y, dx
+    torch.cuda.empty_cache()
+    E, N, K = 540, 2048, 2048
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
+    w[-1] = _randn(3, N, K)
+    sizes = [0] * (E - 1) + [50]
+    x, dy = _randn(4, 50, K), _randn(5, 50, N)
+    h, g = B.GroupedLinear(w), _list(sizes, 1)
+    one, g1 = B.GroupedLinear(w[-1:].clone()), _list([50], 1)
+    assert torch.equal(h(x, g), one(x, g1)) and torch.equal(h.grad_input(dy, g), one.grad_input(dy, g1))
+    dw = h.grad_weight(dy, x, g)
+    assert torch.equal(dw[-1], one.grad_weight(dy, x, g1)[0]) and not dw[:-1].any()
+
+
+def test_a_good_call_after_a_refused_one():
+    h, g = _handle(), _list(SOME, 1)
+    M = sum(SOME)
+    x, dy = _randn(1, M, 200), _randn(2, M, 136)
+    odd = _randn(3, M, 204)[:, :200]  # rows off 16-byte boundaries
+    want = h(x, g), h.grad_weight(dy, x, g)
+    for bad in (lambda: h(odd, g), lambda: h.grad_weight(dy, odd, g)):
+        with pytest.raises(B.GmmfrError):
+            bad()
+        assert torch.equal(h(x, g), want[0]) and torch.equal(h.grad_weight(dy, x, g), want[1])

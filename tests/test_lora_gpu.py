@@ -197,3 +197,56 @@ def test_calls_one_after_the_other_share_a_workspace():
     for x, i, y in zip(xs, ids, ys):
         assert torch.equal(h(x, i), y)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M", [3, 50, 300])
+def test_offsets_past_32_bits(M):
+    """Second factors, and first ones, of more than 2^31 elements each: the last adapter is read where it lies."""
+    N, K, r, L = 4096, 4096, 64, 8200
+    x, w = _randn(1, M, K), _randn(2, N, K, scale=K ** -0.5)
+    a1, b1 = _randn(3, 1, r, K, scale=K ** -0.5), _randn(4, 1, N, r, scale=r ** -0.5)
+    a, b = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((L, r, K), (L, N, r)))
+    a[-1], b[-1] = a1[0], b1[0]
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    ids[::2] = L - 1
+    f32 = dict(out_dtype=torch.float32)
+    want, got = B.LoraLinear(w, a1, b1, **f32)(x, torch.where(ids < 0, ids, 0)), B.LoraLinear(w, a, b, **f32)(x, ids)
+    # the number of adapters shares the sums out in another way: each is within K/8 * 2^-23 of the terms' sum, 2^-17 of the
+    # adapters' (above), of the value
+    mine = (ids >= 0)[:, None]
+    terms, more = x.abs().float() @ w.abs().float().T, (x.abs().float() @ a1[0].abs().float().T) @ b1[0].abs().float().T * mine
+    assert ((got - want).abs() <= 2 * (K / 8 * 2 ** -23 * (terms + more) + (2 ** -17 + r * 2 ** -23) * more)).all()
+    assert torch.equal(got[1::2], want[1::2]) and (got - B.Linear(w, **f32)(x))[::2].abs().max() > 0.1
+
+
+def test_a_step_of_a_block_with_adapters():
+    """Router, routed experts as grouped products, and a shared expert with adapters beside them, as one step of a served
+    model, against the formula in 64 bits."""
+    T, H, I, E, k, L, r = 70, 256, 128, 8, 2, 5, 16
+    x, wg = _randn(1, T, H), _randn(2, E, H, scale=0.2)
+    w13, w2 = _randn(3, E, 2 * I, H, scale=H ** -0.5), _randn(4, E, H, I, scale=I ** -0.5)
+    s13, s2 = _randn(5, 2 * I, H, scale=H ** -0.5), _randn(6, H, I, scale=I ** -0.5)
+    a13, b13 = _randn(7, L, r, H, scale=H ** -0.5), _randn(8, L, 2 * I, r, scale=r ** -0.5)
+    a2, b2 = _randn(9, L, r, I, scale=I ** -0.5), _randn(10, L, H, r, scale=r ** -0.5)
+    ids = _ids(T, L, "tokens")
+    experts, weights = B.MoeGate(wg, topk=k)(x)
+    routed, _ = B.route(experts, weights, x.view(torch.uint8), torch.empty((T, 2 * H // 64, 2), dtype=torch.uint8, device="cuda"), E)
+    rows, groups, perm = routed["x1"].view(torch.bfloat16), routed["group_list"], routed["perm"].long()
+    up = B.GroupedLinear(w13, out_dtype=torch.float32)(rows, groups)
+    mid = (torch.nn.functional.silu(up[:, :I]) * up[:, I:]).to(torch.bfloat16)
+    down = B.GroupedLinear(w2, out_dtype=torch.float32)(mid, groups)
+    shared = B.LoraLinear(s13, a13, b13, activation="swiglu")(x, ids)
+    out = B.LoraLinear(s2, a2, b2, out_dtype=torch.float32)(shared, ids, residual=x)
+    out = out.index_add(0, perm // k, down * weights.flatten()[perm, None])
+    ref = x.double()
+    w13d, w2d = w13.double(), w2.double()
+    for j in range(k):
+        z = torch.einsum("th,tnh->tn", x.double(), w13d[experts[:, j].long()])
+        z = torch.nn.functional.silu(z[:, :I]) * z[:, I:]
+        ref = ref + weights[:, j, None].double() * torch.einsum("ti,thi->th", z, w2d[experts[:, j].long()])
+    adapter = [torch.where((ids >= 0)[:, None, None], t.double()[ids.clamp(min=0).long()], 0.0) for t in (a13, b13, a2, b2)]
+    z = x.double() @ s13.double().T + torch.einsum("tnr,trh,th->tn", adapter[1], adapter[0], x.double())
+    z = torch.nn.functional.silu(z[:, :I]) * z[:, I:]
+    ref = ref + z @ s2.double().T + torch.einsum("tnr,tri,ti->tn", adapter[3], adapter[2], z)
+    # two roundings to BF16 on the way, of the experts' and of the shared expert's middle: 2^-9 of terms that add up at random
+    assert float((out.double() - ref).norm() / ref.norm()) < 2 ** -8
