@@ -606,10 +606,11 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
       const int a = p.lora_ids[t];
       float more[1] = {0.f}, more_up[1] = {0.f};
       const float* s = p.lora_own ? &s_sums[t * p.lora_rank] : p.lora_s + (int64_t)t * p.lora_rank;
-      add_adapter(p, a, s, p.lora_parts, p.lora_part, n, 1, more);
+      const int parts = p.lora_own ? 1 : p.lora_parts;
+      add_adapter(p, a, s, parts, p.lora_part, n, 1, more);
       v += more[0];
       if constexpr (kGated) {
-        add_adapter(p, a, s, p.lora_parts, p.lora_part, p.N + n, 1, more_up);
+        add_adapter(p, a, s, parts, p.lora_part, p.N + n, 1, more_up);
         u += more_up[0];
       }
     }
