@@ -444,6 +444,11 @@ gmmfr_status validate_grouped(const gmmfr_grouped_problem* p) {
   return GMMFR_OK;
 }
 
+// Error words; the gradient's CTAs' copies of the experts' ends
+size_t grouped_ws_bytes(const gmmfr_grouped_problem* p) {
+  return align256(gmmfr::kHdrBytes + sizeof(int32_t) * (size_t)gmmfr::grouped_grad_ctas(p->N, p->K, p->E, gmmfr::sm_count()) * p->E);
+}
+
 }  // namespace
 
 extern "C" {
@@ -628,7 +633,7 @@ gmmfr_status gmmfr_lora_linear(const gmmfr_lora_problem* problem, const void* x,
 gmmfr_status gmmfr_grouped_linear_workspace_size(const gmmfr_grouped_problem* problem, size_t* bytes) {
   if (gmmfr_status st = validate_grouped(problem)) return st;
   if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = gmmfr::kHdrBytes;
+  *bytes = grouped_ws_bytes(problem);
   return GMMFR_OK;
 }
 
@@ -687,7 +692,7 @@ gmmfr_status gmmfr_grouped_linear_grad_weight(const gmmfr_grouped_problem* probl
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dweight, 16))
     return fail(GMMFR_ERR_INVALID_ARG, "dy, x and dweight must be 16-byte aligned");
   if (!aligned(group_list, 8)) return fail(GMMFR_ERR_INVALID_ARG, "group_list is not aligned to its element size");
-  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, gmmfr::kHdrBytes)) return st;
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, grouped_ws_bytes(problem))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.M == 0) {
     cudaError_t e = cudaMemsetAsync(workspace, 0, 8, s);
@@ -697,6 +702,7 @@ gmmfr_status gmmfr_grouped_linear_grad_weight(const gmmfr_grouped_problem* probl
   gmmfr::GroupedGradParams g{};
   g.group_list = group_list;
   g.hdr = static_cast<uint32_t*>(workspace);
+  g.ends = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + gmmfr::kHdrBytes);
   g.M = p.M;
   g.A = p.transposed ? p.K : p.N;  // the gradient's rows, then its columns
   g.B = p.transposed ? p.N : p.K;

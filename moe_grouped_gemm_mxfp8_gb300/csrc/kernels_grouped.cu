@@ -41,12 +41,11 @@ constexpr int kSmem = kMiscOff + 32 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 // ---- weights
-constexpr int kGradStages = 5;
+constexpr int kGradStages = 6;
 constexpr int kGradStage = 2 * kTileBytes;               // 64 rows of 128 columns of either operand
 constexpr int kGradTurnOff = kGradStages * kGradStage;   // 4 KB for each of 8 epilogue warps
 constexpr int kGradBarOff = kGradTurnOff + 8 * 4096;     // full, empty, landed, peer, accf[2], acce[2], drain
-constexpr int kGradEndOff = kGradBarOff + (4 * kGradStages + 5) * 8;
-constexpr int kGradScanOff = kGradEndOff + 4 * kMaxExperts;
+constexpr int kGradScanOff = kGradBarOff + (4 * kGradStages + 5) * 8;
 constexpr int kGradMiscOff = kGradScanOff + 8 * (kThreads / 32);
 constexpr int kGradSmem = kGradMiscOff + 32 + 1024;
 static_assert(kGradSmem <= 232448 && kGradScanOff % 8 == 0, "shared memory budget, alignment");
@@ -63,9 +62,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// s_end[e]: where expert e's rows end (they start where the expert before ends, the first one's at 0).  A list that
+// end[e]: where expert e's rows end (they start where the expert before ends, the first one's at 0).  A list that
 // decreases, is negative or leaves [0, M] sets kErrBadGroupList and is clamped.  Every thread calls it.
-__device__ void grouped_ends(const int64_t* list, int type, int E, int64_t M, int32_t* s_end, int64_t* scratch, uint32_t* s_err) {
+__device__ void grouped_ends(const int64_t* list, int type, int E, int64_t M, int32_t* end, int64_t* scratch, uint32_t* s_err) {
   int64_t carry = 0;
   for (int base = 0; base < E; base += grp::kThreads) {
     const int e = base + (int)threadIdx.x;
@@ -82,7 +81,7 @@ __device__ void grouped_ends(const int64_t* list, int type, int E, int64_t M, in
       v = v > carry ? v : carry;
       carry = tot > carry ? tot : carry;
     }
-    if (e < E) s_end[e] = (int32_t)(v < M ? v : M);
+    if (e < E) end[e] = (int32_t)(v < M ? v : M);
   }
   if (type == 1 && threadIdx.x == 0 && carry > M) atomicOr(s_err, kErrBadGroupList);
   __syncthreads();
@@ -438,7 +437,6 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
   uint64_t* accf = peer + grp::kGradStages;
   uint64_t* acce = accf + 2;  // used in rank 0: both CTAs' epilogue warps
   uint64_t* drain = acce + 2;
-  int32_t* s_end = reinterpret_cast<int32_t*>(smem + grp::kGradEndOff);
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + grp::kGradScanOff);
   int32_t* misc = reinterpret_cast<int32_t*>(smem + grp::kGradMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&misc[0]);
@@ -471,7 +469,10 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   __syncthreads();
-  grouped_ends(p.group_list, p.group_list_type, p.E, p.M, s_end, s_scan, s_err);
+  // Where the experts' rows end, in global memory, each CTA's copy by itself: the sixth stage takes the room for 1024 of them
+  // (65536 rows of 64 experts, 2048 x 1024: 178 us with five stages, 169 with six).
+  int32_t* ends = p.ends + (int64_t)blockIdx.x * p.E;
+  grouped_ends(p.group_list, p.group_list_type, p.E, p.M, ends, s_scan, s_err);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();
@@ -490,8 +491,8 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
     tb = r - ta * TB;
   };
   auto rows_of = [&](int e, int& start) {
-    start = e ? s_end[e - 1] : 0;
-    return s_end[e] - start;
+    start = e ? ends[e - 1] : 0;
+    return ends[e] - start;
   };
 
   if (warp == 0) {
@@ -628,13 +629,27 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
       int e, ta, tb, start;
       unit_at(u, e, ta, tb);
       const int rows = rows_of(e, start), blocks = (rows + grp::kBK - 1) / grp::kBK;
-      float sum[4][32] = {};
+      float sum[4][32];
+      // One accumulator's sums are the tile's, read in whole: 413 rows to each of 24 experts of 5120 x 1288 137 -> 130 us.  With one
+      // or two blocks the writes bound it, and go better as the chunks come (16 rows to each of 256, 2048 x 1024: 180, 192).
+      const bool alone = blocks > 2 && blocks <= kPer;
+      if (!alone) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+      }
       bool ok = true;
       for (int k0 = 0; k0 < blocks; k0 += kPer) {
         ok = warp_wait_quick(ptx::smem_u32(&accf[acc_i & 1]), (acc_i >> 1) & 1, ctl);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t at = taddr + (acc_i & 1) * 256;
+        if (alone) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(at + 32 * i, reinterpret_cast<uint32_t(&)[32]>(sum[i]));
+          ptx::tmem_wait_ld();
+        } else
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -740,8 +755,12 @@ cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedParams& p, bool
   return launch_pairs<grouped_kernel<false, false>, grp::kSmem>(maps, p, units, sms, s);
 }
 
+int grouped_grad_ctas(int64_t A, int64_t B, int64_t E, int sms) {
+  return (int)(2 * std::min<int64_t>(sms / 2, E * ((A + 255) / 256) * ((B + 255) / 256)));
+}
+
 cudaError_t launch_grouped_grad(const GroupedGradMaps& maps, const GroupedGradParams& p, int sms, cudaStream_t s) {
-  const int64_t units = (int64_t)p.E * ((p.A + 255) / 256) * ((p.B + 255) / 256);
+  const int64_t units = grouped_grad_ctas(p.A, p.B, p.E, sms) / 2;
   if (p.out_f32) return launch_pairs<grouped_grad_kernel<true>, grp::kGradSmem>(maps, p, units, sms, s);
   return launch_pairs<grouped_grad_kernel<false>, grp::kGradSmem>(maps, p, units, sms, s);
 }

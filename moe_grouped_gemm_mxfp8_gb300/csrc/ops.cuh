@@ -180,6 +180,7 @@ cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedParams& p, bool
 // Their weights' gradient: out[e] [A, B] = sum over the rows of expert e of a^T b
 struct GroupedGradParams {
   const int64_t* group_list;
+  int32_t* ends;  // [grouped_grad_ctas, E]
   uint32_t* hdr;
   int64_t M, A, B;
   int64_t timeout_ns;
@@ -191,6 +192,7 @@ struct GroupedGradMaps {
   CUtensorMap a, b;  // [M, A] and [M, B], boxes of 64 columns x 64 rows
   CUtensorMap out;   // [E, A, B], boxes of 128 bytes x 32 rows
 };
+int grouped_grad_ctas(int64_t A, int64_t B, int64_t E, int sms);
 cudaError_t launch_grouped_grad(const GroupedGradMaps& maps, const GroupedGradParams& p, int sms, cudaStream_t s);
 
 }  // namespace gmmfr

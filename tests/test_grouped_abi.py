@@ -27,7 +27,7 @@ def _product(p, x=A, w=A, g=A, y=A, ws=A, n=4096):
     B.gmmfr_grouped_linear(p, x, w, g, y, ws, n)
 
 
-def _grad(p, dy=A, x=A, g=A, dw=A, ws=A, n=4096):
+def _grad(p, dy=A, x=A, g=A, dw=A, ws=A, n=1 << 20):
     B.gmmfr_grouped_linear_grad_weight(p, dy, x, g, dw, ws, n)
 
 
