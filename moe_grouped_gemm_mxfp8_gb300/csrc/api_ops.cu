@@ -274,6 +274,7 @@ LoraLayout lora_layout(const gmmfr_lora_problem* p, int sms) {
   L.plan.count = (int32_t)p->count;
   L.plan.rank = (int32_t)p->rank;
   L.plan.rows = rows;
+  L.plan.precise = p->linear.out_type == GMMFR_DT_F32;
   L.plan.scans = (int32_t)std::clamp<int64_t>(std::min(M, p->count) * rows * p->rank * 2 / 16384, 1, 1 << 20);  // 16 KB and more for a CTA
   gmmfr::plan_lora_sums(L.plan, sms);
   L.sums = gmmfr::kHdrBytes;

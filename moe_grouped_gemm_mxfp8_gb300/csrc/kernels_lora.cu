@@ -428,6 +428,8 @@ void plan_lora_sums(LoraParams& p, int sms) {
   const int64_t tiles = (p.M + 127) / 128, blocks = (p.M + 255) / 256, most = (std::min<int64_t>(128, p.count) * ranks + 15) / 16;
   p.passes = (int32_t)std::clamp<int64_t>(sms / tiles / 2, 1, most);
   while (p.split < 8 && tiles * p.passes * p.split * 2 <= sms && 2 * p.split * 128 <= p.K) p.split *= 2;
+  // FP32 results: an accumulator, whose additions truncate, takes 1024 products (of K above 16384 more)
+  if (p.precise) p.split = (int32_t)std::max<int64_t>(p.split, std::min<int64_t>((p.K + 1023) / 1024, 16));
   p.parts = p.split;
   p.grid = (int32_t)std::max<int64_t>(tiles * p.passes * p.split, sms);
   p.scans = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.grid / blocks, 128));

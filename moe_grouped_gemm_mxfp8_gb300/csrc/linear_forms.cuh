@@ -236,10 +236,19 @@ __device__ __forceinline__ int adapter_of(const LinearParams& p, int64_t m, uint
 // its ranks, a block whose W rows are the second factor's (by TMA) and whose x rows are the rows' sums, zeros in the rows of
 // other adapters.  Two warps of their own write those x rows and hand the stage over.  A sum enters as two BF16 numbers, the
 // first truncated, so that it is off by 2^-17 at most; they take the halves of a 128-byte row, both against the same 32
-// ranks.  The lists of the adapters of 256 rows come with the sums.
+// ranks.  For FP32 results it is three numbers, which leave nothing out, of 16 ranks.  The lists of the adapters of 256 rows
+// come with the sums.
 // A zero does not keep an infinity or NaN of another adapter's factor out of a row.  The lists say whether their factors have
 // any: the warps then put zeros in their place where a factor has landed, and from then on the CTA's epilogues add,
 // row by row, what those elements give the rows whose adapter has them.
+template <bool kF32>
+struct SumTerms {
+  static constexpr int kTerms = kF32 ? 3 : 2, kRanks = kF32 ? 16 : 32;  // of a block: BF16 numbers of a sum, ranks
+  static constexpr int kPieces = kRanks / 8;                            // 16-byte pieces of a row that a term takes
+  __device__ static int blocks(int rank) { return (rank + kRanks - 1) / kRanks; }
+  // products of 16 ranks in the block from r0 on
+  __device__ static int steps(int rank, int r0) { return kRanks == 32 && rank - r0 > 16 ? 2 : 1; }
+};
 struct AdapterShared {
   uint64_t loaded[lin::kPairMaxStages];  // a stage's second factors have landed in this CTA
   uint64_t built[lin::kPairMaxStages];   // in the CTA that issues the products: a stage is ready
@@ -274,10 +283,10 @@ struct AdapterList {
   }
 };
 
-// The adapters of a tile's blocks one after the other: all of a list for ranks 0 to 31, then for 32 to 63, ...
+// The adapters of a tile's blocks one after the other: all of a list for the first ranks, then for the next, ...
 struct AdapterBlocks {
   const AdapterList& list;
-  int c, d, held;  // ranks 32 c and up of entry d; the 32 entries that hold it
+  int c, d, held;  // the c-th ranks of entry d; the 32 entries that hold it
   __device__ __forceinline__ AdapterBlocks(const AdapterList& list, int u) : list(list) {
     c = list.n ? u / list.n : 0;
     d = u - c * list.n;
@@ -293,41 +302,46 @@ struct AdapterBlocks {
   }
 };
 
-// Ranks r0 .. r0 + 31 of two rows' sums (m and m + 32; past the last row: its own), as pairs of BF16 numbers: the leading bits,
-// and what they leave; zeros past the rank.
-__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, uint32_t (&hi)[2][16], uint32_t (&lo)[2][16]) {
+// The ranks from r0 on of two rows' sums (m and m + 32; past the last row: its own) as the 32-bit words of a block's row: the
+// leading bits of each, then what they leave, twice over for FP32 results; zeros past the rank.
+template <bool kF32>
+__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, uint32_t (&w)[2][32]) {
+  using Terms = SumTerms<kF32>;
+  constexpr int kFours = Terms::kRanks / 4, kWords = Terms::kRanks / 2;
   const int left = p.lora_rank - r0;
-  float4 sum[2][8] = {};
+  float4 sum[2][kFours] = {};
   for (int c = 0; c < p.lora_parts; ++c) {
-    float4 v[2][8];  // on their way together
+    float4 v[2][kFours];  // on their way together
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float* s = p.lora_s + c * p.lora_part + min(m + 32 * i, p.M - 1) * p.lora_rank + r0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 4 * j < left ? reinterpret_cast<const float4*>(s)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < kFours; ++j) v[i][j] = 4 * j < left ? reinterpret_cast<const float4*>(s)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < kFours; ++j)
         sum[i][j] = make_float4(sum[i][j].x + v[i][j].x, sum[i][j].y + v[i][j].y, sum[i][j].z + v[i][j].z, sum[i][j].w + v[i][j].w);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float f[4] = {sum[i][j].x, sum[i][j].y, sum[i][j].z, sum[i][j].w};
-      uint32_t h[4];
-      float r[4];
+    for (int j = 0; j < kFours; ++j) {
+      float f[4] = {sum[i][j].x, sum[i][j].y, sum[i][j].z, sum[i][j].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = __float_as_uint(f[k]) & 0xffff0000u;
-        r[k] = isfinite(f[k]) ? f[k] - __uint_as_float(h[k]) : 0.f;
+      for (int t = 0; t + 1 < Terms::kTerms; ++t) {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          h[k] = __float_as_uint(f[k]) & 0xffff0000u;
+          f[k] = isfinite(f[k]) ? f[k] - __uint_as_float(h[k]) : 0.f;
+        }
+        w[i][t * kWords + 2 * j] = h[0] >> 16 | h[1];
+        w[i][t * kWords + 2 * j + 1] = h[2] >> 16 | h[3];
       }
-      hi[i][2 * j] = h[0] >> 16 | h[1];
-      hi[i][2 * j + 1] = h[2] >> 16 | h[3];
-      lo[i][2 * j] = pack_bf16(r[0], r[1]);
-      lo[i][2 * j + 1] = pack_bf16(r[2], r[3]);
+      w[i][(Terms::kTerms - 1) * kWords + 2 * j] = pack_bf16(f[0], f[1]);
+      w[i][(Terms::kTerms - 1) * kWords + 2 * j + 1] = pack_bf16(f[2], f[3]);
     }
 }
 
@@ -347,7 +361,7 @@ __device__ __noinline__ void drop_not_finite(uint8_t* at, int r0, int r1, int st
 // A CTA's adapter warps (`half` 0 and 1) through a tile's blocks u0 .. u1 - 1, kKps to a stage, from `stage` on (a stage whose
 // factors have landed is free).  x_at, w_at: where a block's rows of x and of W lie in its stage; x_rows (128 at most) of
 // them are written, which are p's from row0 on; to_rank: the CTA that issues the products, or -1.
-template <int kKps>
+template <int kKps, bool kF32>
 __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterShared& a, uint8_t* smem, int stage_bytes, int block_bytes,
                                                int n_stages, int x_at, int x_rows, int w_at, int w_rows, int64_t block, int64_t row0,
                                                int half, const AdapterList& list, int u0, int u1, int to_rank, int& stage,
@@ -364,9 +378,10 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
 #pragma unroll
   for (int g = 0; g < 4; ++g)
     if (32 * g + lane < p.lora_scans) flag |= p.lora_flags[block * p.lora_scans + 32 * g + lane];
+  using Terms = SumTerms<kF32>;
   AdapterBlocks at(list, u0);
-  uint32_t hi[2][16], lo[2][16];
-  split_sums(p, row0 + 64 * half + lane, 32 * at.c, hi, lo);
+  uint32_t words[2][32];
+  split_sums<kF32>(p, row0 + 64 * half + lane, Terms::kRanks * at.c, words);
   int c_held = at.c;
   const bool found = __any_sync(0xffffffffu, flag);
   const uint32_t smem0 = ptx::smem_u32(smem) + x_at + (64 * half + lane) * 128, turn = lane & 7;
@@ -376,10 +391,10 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
 #pragma unroll
     for (int h = 0; h < kKps; ++h) {
       if (u + h >= u1) break;
-      const int steps = ranks - 32 * at.c > 16 ? 2 : 1, adapter = at.adapter();
+      const int steps = Terms::steps(ranks, Terms::kRanks * at.c), adapter = at.adapter();
       if (at.c != c_held) {
         c_held = at.c;
-        split_sums(p, row0 + 64 * half + lane, 32 * at.c, hi, lo);
+        split_sums<kF32>(p, row0 + 64 * half + lane, Terms::kRanks * at.c, words);
       }
       if (h == 0) {
         if (!warp_wait_quick(ptx::smem_u32(&a.loaded[stage]), loaded_bits >> stage & 1, ctl)) return false;
@@ -390,11 +405,14 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
         if (!write[i]) continue;
         const uint32_t to = xb + h * block_bytes + i * 4096, keep = own[i] == adapter ? 0xffffffffu : 0u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < Terms::kPieces; ++k) {
           if (k >= 2 * steps) break;
-          ptx::st_shared_v4(to + ((k ^ turn) << 4), hi[i][4 * k] & keep, hi[i][4 * k + 1] & keep, hi[i][4 * k + 2] & keep, hi[i][4 * k + 3] & keep);
-          ptx::st_shared_v4(to + (((4 + k) ^ turn) << 4), lo[i][4 * k] & keep, lo[i][4 * k + 1] & keep, lo[i][4 * k + 2] & keep,
-                            lo[i][4 * k + 3] & keep);
+#pragma unroll
+          for (int t = 0; t < Terms::kTerms; ++t) {
+            const int piece = t * Terms::kPieces + k;
+            ptx::st_shared_v4(to + ((piece ^ turn) << 4), words[i][4 * piece] & keep, words[i][4 * piece + 1] & keep,
+                              words[i][4 * piece + 2] & keep, words[i][4 * piece + 3] & keep);
+          }
         }
       }
       if (found) drop_not_finite(smem + stage * stage_bytes + h * block_bytes + w_at, half * w_rows / 2, (half + 1) * w_rows / 2, steps);
@@ -651,7 +669,8 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
   const int KB = (p.KB + kKps - 1) / kKps;
   const int per = kF32 ? lin::kChunk<kGated> / kKps : KB;  // stages to an accumulator
   [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kPairTurnOff + 8 * 32 * 33 * 4);
-  [[maybe_unused]] const int rank_chunks = (p.lora_rank + 31) / 32;  // kLora: blocks of an adapter
+  using Terms = SumTerms<kF32>;
+  [[maybe_unused]] const int rank_chunks = Terms::blocks(p.lora_rank);  // kLora: blocks of an adapter
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
@@ -742,7 +761,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
           int adapter[kKps], rank0[kKps];
 #pragma unroll
           for (int i = 0; i < kKps; ++i) {
-            rank0[i] = 32 * next.c;
+            rank0[i] = Terms::kRanks * next.c;
             adapter[i] = next.adapter();
             next.next();
           }
@@ -842,12 +861,12 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
               ptx::tc_fence_after();
               if (ptx::elect_one()) {
                 for (int i = 0; i < kKps && u + i < units; ++i) {
-                  const int steps = u + i >= count * (rank_chunks - 1) ? (p.lora_rank - 32 * rank_chunks + 47) / 16 : 2;
+                  const int steps = Terms::steps(p.lora_rank, u + i >= count * (rank_chunks - 1) ? Terms::kRanks * (rank_chunks - 1) : 0);
                   const uint32_t xa = lo + i * lo_block, wb = xa + (lin::kTileBytes >> 4);
-                  for (int q = 0; q < steps; ++q) {
-                    ptx::tc_mma_f16_pair_lo(d, xa + 2 * q, wb + 2 * q, desc_hi, idesc, 1u);
-                    ptx::tc_mma_f16_pair_lo(d, xa + 4 + 2 * q, wb + 2 * q, desc_hi, idesc, 1u);
-                  }
+                  for (int q = 0; q < steps; ++q)
+#pragma unroll
+                    for (int t = 0; t < Terms::kTerms; ++t)
+                      ptx::tc_mma_f16_pair_lo(d, xa + t * Terms::kPieces + 2 * q, wb + 2 * q, desc_hi, idesc, 1u);
                 }
                 ptx::tc_commit_pair(empty0 + 8 * stage);
               }
@@ -884,7 +903,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
         AdapterList list;
         list.load(p, mt);
         stage = (stage + KB) % n_stages;
-        if (!build_adapters<kKps>(p, ad, smem, stage_bytes, block_bytes, n_stages, 0, 128, lin::kTileBytes, BN / 2, mt,
+        if (!build_adapters<kKps, kF32>(p, ad, smem, stage_bytes, block_bytes, n_stages, 0, 128, lin::kTileBytes, BN / 2, mt,
                                   (int64_t)mt * 256 + 128 * rank, half, list, 0, list.n * rank_chunks, 0, stage, loaded_bits, ctl))
           break;
       }
@@ -1057,7 +1076,8 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
   // [T][128]: in the ring's place when no tile follows, whose loads would write there
   float* part = reinterpret_cast<float*>(smem + (tiles <= clusters ? 0 : n_stages * stage_bytes));
   [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + kArena + lin::kStreamBars * 8 + 32);
-  [[maybe_unused]] const int rank_chunks = (p.lora_rank + 31) / 32;  // kLora: blocks of an adapter
+  using Terms = SumTerms<kF32>;
+  [[maybe_unused]] const int rank_chunks = Terms::blocks(p.lora_rank);  // kLora: blocks of an adapter
   // one accumulator, or two in turn for the chunks of FP32 results
   const uint32_t acc_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128), tmem_cols = kF32 ? 2 * acc_cols : acc_cols;
   auto acc_of = [&](uint32_t i) { return kF32 ? i & 1 : 0; };
@@ -1148,7 +1168,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
           int adapter[kKps], rank0[kKps];
 #pragma unroll
           for (int h = 0; h < kKps; ++h) {
-            rank0[h] = 32 * next.c;
+            rank0[h] = Terms::kRanks * next.c;
             adapter[h] = next.adapter();
             next.next();
           }
@@ -1233,12 +1253,12 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
               for (int h = 0; h < kKps && u + h < u1; ++h) {
-                const int steps = u + h >= count * (rank_chunks - 1) ? (p.lora_rank - 32 * rank_chunks + 47) / 16 : 2;
+                const int steps = Terms::steps(p.lora_rank, u + h >= count * (rank_chunks - 1) ? Terms::kRanks * (rank_chunks - 1) : 0);
                 const uint32_t wa = lo + h * lo_block, xb = wa + (lin::kTileBytes >> 4);
-                for (int q = 0; q < steps; ++q) {
-                  ptx::tc_mma_f16_lo(d, wa + 2 * q, xb + 2 * q, desc_hi, idesc, 1u);
-                  ptx::tc_mma_f16_lo(d, wa + 2 * q, xb + 4 + 2 * q, desc_hi, idesc, 1u);
-                }
+                for (int q = 0; q < steps; ++q)
+#pragma unroll
+                  for (int t = 0; t < Terms::kTerms; ++t)
+                    ptx::tc_mma_f16_lo(d, wa + 2 * q, xb + t * Terms::kPieces + 2 * q, desc_hi, idesc, 1u);
               }
               ptx::tc_commit(empty0 + 8 * stage);
             }
@@ -1269,7 +1289,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
       list.load(p, 0);
       for (int t = first; t < tiles; t += clusters) {
         stage = (stage + kb1 - kb0) % n_stages;
-        if (!build_adapters<kKps>(p, ad, smem, stage_bytes, block_bytes, n_stages, lin::kTileBytes, npad, 0, 128, 0, 0, half, list,
+        if (!build_adapters<kKps, kF32>(p, ad, smem, stage_bytes, block_bytes, n_stages, lin::kTileBytes, npad, 0, 128, 0, 0, half, list,
                                   list.n * rank_chunks * (int)rank / S, list.n * rank_chunks * ((int)rank + 1) / S, -1, stage, loaded_bits,
                                   ctl))
           break;

@@ -141,6 +141,7 @@ struct LoraParams {
   int32_t* lists;              // as LinearParams'
   uint32_t* flags;
   int32_t scans;               // CTAs to a list; 0: no lists
+  int32_t precise;             // for FP32 results
   uint32_t* errs;              // [grid], error bits of each CTA: more than kLoraFewRows rows
   int64_t timeout_ns;
   int32_t test_stall;
