@@ -111,7 +111,10 @@ void plan_linear(LinearParams& p, LinearParams& tail, int sms) {
     // Its products come out of the registers that the loads need, so it falls behind with rows x weights per CTA: W of
     // 2048 x 2048 and 32 rows (1.0 M) 6.0 us, the stream form 6.7; 5125 x 1288 and 32 (2.0 M) 8.7 and 7.9;
     // 7168 x 4096: 8 rows (1.6 M) 12.5 and 13.8, 16 (3.1 M) 13.6 and 13.9, 32 (6.3 M) 17.7 and 14.0.
-    if (p.M == 1 || p.M * p.group_m * 16 * p.K <= 1900000) {
+    // With adapters also by what its epilogue takes from the second factors: 32 rows of 2048, rank 64 (4.2 M) 9.8 us, the
+    // stream form 12.5; 25 gated of 2 x 4160, rank 64 (13 M) 16.8 and 12.4.
+    const int64_t factors = p.lora_ids ? p.M * p.lora_rows * p.lora_rank : 0;
+    if ((p.M == 1 || p.M * p.group_m * 16 * p.K <= 1900000) && factors <= 8000000) {
       p.form = kLinearDirect;
       p.grid = (int32_t)((row_groups + p.group_m - 1) / p.group_m);
       return;

@@ -206,19 +206,32 @@ __device__ __forceinline__ void add_adapter(const LinearParams& p, int adapter, 
   auto add = [](float& f, float s, float b) {
     if (!kNotFinite || !isfinite(b)) f += s * b;
   };
-  for (int j = 0; j < p.lora_rank; j += 8) {
-    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+  if constexpr (kCols == 1 && !kNotFinite) {  // four pieces of the factor's row, and of the sums, on their way at once
     for (int c = 0; c < parts; ++c) {
-      const float4* s = reinterpret_cast<const float4*>(at + c * part + j);
-      lo = make_float4(lo.x + s[0].x, lo.y + s[0].y, lo.z + s[0].z, lo.w + s[0].w);
-      hi = make_float4(hi.x + s[1].x, hi.y + s[1].y, hi.z + s[1].z, hi.w + s[1].w);
+      const float4* s = reinterpret_cast<const float4*>(at + c * part);
+#pragma unroll 4
+      for (int j = 0; j < p.lora_rank; j += 8) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + j));
+        const float4 lo = s[j / 4], hi = s[j / 4 + 1];
+        add(f[0], lo.x, bf16_lo(w.x)), add(f[0], lo.y, bf16_hi(w.x)), add(f[0], lo.z, bf16_lo(w.y)), add(f[0], lo.w, bf16_hi(w.y));
+        add(f[0], hi.x, bf16_lo(w.z)), add(f[0], hi.y, bf16_hi(w.z)), add(f[0], hi.z, bf16_lo(w.w)), add(f[0], hi.w, bf16_hi(w.w));
+      }
     }
+  } else {
+    for (int j = 0; j < p.lora_rank; j += 8) {
+      float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+      for (int c = 0; c < parts; ++c) {
+        const float4* s = reinterpret_cast<const float4*>(at + c * part + j);
+        lo = make_float4(lo.x + s[0].x, lo.y + s[0].y, lo.z + s[0].z, lo.w + s[0].w);
+        hi = make_float4(hi.x + s[1].x, hi.y + s[1].y, hi.z + s[1].z, hi.w + s[1].w);
+      }
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) {
-      if (k < cols) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)k * p.lora_rank + j));
-        add(f[k], lo.x, bf16_lo(w.x)), add(f[k], lo.y, bf16_hi(w.x)), add(f[k], lo.z, bf16_lo(w.y)), add(f[k], lo.w, bf16_hi(w.y));
-        add(f[k], hi.x, bf16_lo(w.z)), add(f[k], hi.y, bf16_hi(w.z)), add(f[k], hi.z, bf16_lo(w.w)), add(f[k], hi.w, bf16_hi(w.w));
+      for (int k = 0; k < kCols; ++k) {
+        if (k < cols) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)k * p.lora_rank + j));
+          add(f[k], lo.x, bf16_lo(w.x)), add(f[k], lo.y, bf16_hi(w.x)), add(f[k], lo.z, bf16_lo(w.y)), add(f[k], lo.w, bf16_hi(w.y));
+          add(f[k], hi.x, bf16_lo(w.z)), add(f[k], hi.y, bf16_hi(w.z)), add(f[k], hi.z, bf16_lo(w.w)), add(f[k], hi.w, bf16_hi(w.w));
+        }
       }
     }
   }
