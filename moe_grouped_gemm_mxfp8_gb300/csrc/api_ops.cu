@@ -261,26 +261,24 @@ gmmfr_status validate_lora(const gmmfr_lora_problem* p) {
   return GMMFR_OK;
 }
 
-// Behind the error words: the adapters' sums, for each 256 rows a list and what its scans found, the sums' own error bits
+// Behind the error words: the adapters' sums, for each 256 rows a list, the sums' own error bits
 struct LoraLayout {
   gmmfr::LoraParams plan;
-  size_t sums, lists, flags, errs, total;
+  size_t sums, lists, errs, total;
 };
 LoraLayout lora_layout(const gmmfr_lora_problem* p, int sms) {
   LoraLayout L{};
-  const int64_t M = p->linear.M, blocks = cdiv(M, 256), rows = p->linear.N * (p->linear.activation == GMMFR_ACT_SWIGLU ? 2 : 1);
+  const int64_t M = p->linear.M, blocks = cdiv(M, 256);
   L.plan.M = M;
   L.plan.K = p->linear.K;
   L.plan.count = (int32_t)p->count;
   L.plan.rank = (int32_t)p->rank;
-  L.plan.rows = rows;
   L.plan.precise = p->linear.out_type == GMMFR_DT_F32;
-  L.plan.scans = (int32_t)std::clamp<int64_t>(std::min(M, p->count) * rows * p->rank * 2 / 16384, 1, 1 << 20);  // 16 KB and more for a CTA
+  L.plan.listed = 1;
   gmmfr::plan_lora_sums(L.plan, sms);
   L.sums = gmmfr::kHdrBytes;
   L.lists = align256(L.sums + sizeof(float) * (size_t)L.plan.parts * M * p->rank);
-  L.flags = align256(L.lists + sizeof(int32_t) * gmmfr::kLoraListInts * (size_t)blocks);
-  L.errs = align256(L.flags + sizeof(uint32_t) * (size_t)L.plan.scans * blocks);
+  L.errs = align256(L.lists + sizeof(int32_t) * gmmfr::kLoraListInts * (size_t)blocks);
   L.total = align256(L.errs + sizeof(uint32_t) * (size_t)L.plan.grid);
   return L;
 }
@@ -349,15 +347,12 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
     sums = A.plan;
     lp.lora_s = sums.s = reinterpret_cast<float*>(ws + A.sums);
     lp.lora_lists = sums.lists = reinterpret_cast<int32_t*>(ws + A.lists);
-    lp.lora_flags = sums.flags = reinterpret_cast<uint32_t*>(ws + A.flags);
     lp.lora_count = sums.count;
     lp.lora_rank = sums.rank;
-    lp.lora_rows = sums.rows;
-    lp.lora_scans = sums.scans;
+    lp.lora_rows = rows_w;
     sums.x = lp.x;
     sums.ldx = lp.ldx;
     sums.a = static_cast<const __nv_bfloat16*>(adapters->a);
-    sums.b = lp.lora_b;
     lp.lora_a = sums.a;
     lp.lora_scale = sums.scale = adapters->scale;
     sums.ids = adapters->ids;
@@ -375,7 +370,7 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
   parts[0].lora_early = parts[1].M == 0;  // what runs beside starts with it, and does not wait
   gmmfr::LoraMaps sum_maps;
   if (adapters && parts[0].form == gmmfr::kLinearDirect) {  // which needs no lists
-    sums.scans = 0;
+    sums.listed = 0;
     gmmfr::plan_lora_sums(sums, sms);
     // What each CTA reads besides its weights comes from L2.  One token, rank 16, replayed: 2048 x 2048 5.8 us, with the sums'
     // launch 7.2; 4096 x 4096 9.0 and 7.3.  Rank 32 of 1024 x 4096: 7.3 and 7.6.

@@ -74,7 +74,6 @@ static double plan_stream(LinearParams& p, int sms, bool beside) {
   // or its share of HBM; a wave ends with the epilogue, and with the join in a cluster.  W of 7168 x 4096, 32 rows:
   // clusters of 1, 2, 4, 8 take 14.9, 14.0, 15.1, 20.8 us; of 512 x 8192: 24.9, 15.3, 10.5, 8.3.
   const int stage = lin::kStreamKps * (lin::kTileBytes + p.bn * 128), units = (p.KB + lin::kStreamKps - 1) / lin::kStreamKps;
-  const int arena = p.lora_ids ? lin::kLoraStreamArena : lin::kStreamArena;
   double best = 1e30;
   for (int S = 1; S <= (beside ? 1 : 8) && S <= units; S *= 2) {
     const int64_t slots = stream_slots(S, sms);
@@ -85,7 +84,7 @@ static double plan_stream(LinearParams& p, int sms, bool beside) {
     if (t < best) {
       best = t;
       p.split = S;
-      p.n_stages = std::min<int>(lin::kStreamMaxStages, (arena - (waves > 1 ? (int)p.M * 512 : 0)) / stage);
+      p.n_stages = std::min<int>(lin::kStreamMaxStages, (lin::kStreamArena - (waves > 1 ? (int)p.M * 512 : 0)) / stage);
       p.grid = (int32_t)ctas;
     }
   }
@@ -170,7 +169,6 @@ void plan_linear(LinearParams& p, LinearParams& tail, int sms) {
       tail.lora_ids += at;
       tail.lora_s += at * tail.lora_rank;
       tail.lora_lists += at / 256 * kLoraListInts;
-      tail.lora_flags += at / 256 * tail.lora_scans;
     }
     tail.beside = 1;
   }

@@ -7,15 +7,15 @@
 //         registers: they wait for memory, and an adapter has a few rows.
 //   many  128 rows of x at a time, by TMA and tcgen05: the rows are one operand, 16 ranks of up to 16 of their adapters'
 //         factors the other; of what comes out a row keeps its own adapter's columns.
-// Several CTAs share a K range.  CTAs also list the adapters of each 256 rows, and scan those adapters' second
-// factors for infinities and NaN (which brings them into L2).  The product's launch follows at once and begins with its
-// weights; only its adapters wait.
+// Several CTAs share a K range.  CTAs also list the adapters of each 256 rows.  The product's launch follows
+// at once and begins with its weights; only its adapters wait.
 #include "linear_forms.cuh"
 
 namespace gmmfr {
 namespace lora {
 constexpr int kFewThreads = 512;
 constexpr int kTileThreads = 448, kTileStages = 10, kTileArena = 10 * (lin::kTileBytes + 2048);
+constexpr int kPass = 16;  // units of a pass
 }  // namespace lora
 
 namespace {
@@ -57,15 +57,6 @@ struct SumOperands {
   }
 };
 
-// Whether one of 8 BF16 numbers is infinite or NaN
-__device__ __forceinline__ bool not_finite(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool found = false;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) found |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
-  return found;
-}
-
 // Whether this thread's row is the first with its adapter among `rows` rows (of which it has number tid; id -1: none)
 __device__ __forceinline__ bool first_of(const int* s_id, int tid, int id) {
   bool first = id >= 0;
@@ -81,18 +72,13 @@ __device__ __forceinline__ int adapter_at(const LoraParams& p, int64_t m) {
   return (uint32_t)id < (uint32_t)p.count ? id : -1;
 }
 
-// Part `i` of the lists and scans, by kT threads (of which this one is `t`) that share barrier 1: list i / scans, share
-// i % scans of its adapters' second factors taken together.
+// The list of rows 256 block and up, by kT threads (of which this one is `t`) that share barrier 1.
 template <int kT>
-__device__ void list_and_scan(const LoraParams& p, int64_t i, int t) {
+__device__ void list_adapters(const LoraParams& p, int64_t block, int t) {
   constexpr int kPer = kT < 256 ? 256 / kT : 1;  // rows of the list for each thread
   __shared__ __align__(16) int l_id[256];
-  __shared__ int l_list[256];
   __shared__ uint32_t l_first[8];
-  __shared__ int l_found;
   const int lane = t & 31;
-  const int64_t block = i / p.scans;
-  const int share = (int)(i - block * p.scans);
   int id[kPer];
   uint32_t firsts[kPer];
 #pragma unroll
@@ -100,7 +86,6 @@ __device__ void list_and_scan(const LoraParams& p, int64_t i, int t) {
     id[k] = t < 256 ? adapter_at(p, block * 256 + k * kT + t) : -1;
     if (t < 256) l_id[k * kT + t] = id[k];
   }
-  if (t == 0) l_found = 0;
   ptx::bar_sync(1, kT);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -115,31 +100,9 @@ __device__ void list_and_scan(const LoraParams& p, int64_t i, int t) {
   for (int k = 0; k < kPer; ++k) {
     int at = __popc(firsts[k] & ((1u << lane) - 1));
     for (int w = 0; w < min((k * kT + t) >> 5, 8); ++w) at += __popc(l_first[w]);
-    if (firsts[k] >> lane & 1) {
-      l_list[at] = id[k];
-      if (share == 0) list[4 + at] = id[k];
-    }
+    if (firsts[k] >> lane & 1) list[4 + at] = id[k];
   }
-  if (share == 0 && t == 0) list[0] = n;
-  ptx::bar_sync(1, kT);
-  const int64_t pieces = p.rows * p.rank / 8, from = n * pieces * share / p.scans, to = n * pieces * (share + 1) / p.scans;
-  bool found = false;
-  for (int64_t d = from / pieces; d * pieces < to; ++d) {
-    const uint4* f = reinterpret_cast<const uint4*>(p.b) + l_list[d] * pieces;
-    const int64_t end = min(to - d * pieces, pieces);
-    int64_t k = max(from - d * pieces, (int64_t)0) + t;
-    for (; k + 7 * kT < end; k += 8 * kT) {
-      uint4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = ptx::ld_nc_v4(f + k + u * kT);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) found |= not_finite(v[u]);
-    }
-    for (; k < end; k += kT) found |= not_finite(ptx::ld_nc_v4(f + k));
-  }
-  if (found) l_found = 1;
-  ptx::bar_sync(1, kT);
-  if (t == 0) p.flags[i] = l_found;
+  if (t == 0) list[0] = n;
 }
 
 }  // namespace
@@ -147,7 +110,7 @@ __device__ void list_and_scan(const LoraParams& p, int64_t i, int t) {
 // ============================================================================ few rows
 // CTA (d, r, c): the d-th adapter in the order of the rows, ranks 16 r and up, share c of the K range (more than one where a
 // warp's loads would not all be on their way at once); where there are fewer adapters than places for them, several places
-// share an adapter's rows.  The last CTAs list and scan.
+// share an adapter's rows.  The last CTA lists.
 __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(const __grid_constant__ LoraParams p) {
   constexpr int kU = 8, kWarps = lora::kFewThreads / 32;
   __shared__ __align__(16) int s_id[kLoraFewRows];
@@ -161,7 +124,7 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (blockIdx.x >= items) {
-    list_and_scan<lora::kFewThreads>(p, blockIdx.x - items, tid);
+    list_adapters<lora::kFewThreads>(p, 0, tid);
     return;
   }
   int id = -1;
@@ -247,7 +210,7 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
 // CTA (c, p, tile): the 128 rows of a tile, share c of the K range, every `passes`-th pass from p on of up to 16 units: 16 ranks of
 // an adapter.  Who reads the sums adds the shares' parts.  (Clusters that join them on the chip wait for SMs that lie
 // together: 16 us more with clusters of 8.)  Warp 0 TMA, warp 1 MMA, warps 2..5
-// epilogue, warps 6..13 lists and scans.
+// epilogue, warps 6..13 lists.
 __global__ void __launch_bounds__(lora::kTileThreads, 1)
     lora_sums_many_kernel(const __grid_constant__ LoraMaps maps, const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -258,9 +221,8 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
   __shared__ uint32_t s_first[4], tmem_slot, s_err;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp: uniform
-  const int C = p.split, share = blockIdx.x % C, pass0 = 16 * (blockIdx.x / C % p.passes), step = 16 * p.passes;
+  const int C = p.split, share = blockIdx.x % C, pass0 = lora::kPass * (blockIdx.x / C % p.passes), step = lora::kPass * p.passes;
   const int64_t row0 = (int64_t)(blockIdx.x / C / p.passes) * 128;
-  const bool works = row0 < p.M;  // the others scan
   if (tid == 0) {
     for (int s = 0; s < lora::kTileStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
@@ -283,7 +245,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   int id = -1;
-  if (tid < 128) s_id[tid] = id = works ? adapter_at(p, row0 + tid) : -1;
+  if (tid < 128) s_id[tid] = id = adapter_at(p, row0 + tid);
   __syncthreads();
   if (tid < 128) {
     const uint32_t b = __ballot_sync(0xffffffffu, first_of(s_id, tid, id));
@@ -301,7 +263,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
   const uint32_t tmem_base = tmem_slot, smem_base = ptx::smem_u32(smem);
   const Ctl ctl{&abort_flag, &s_err, p.timeout_ns};
   const int rc = (p.rank + 15) / 16, units = n * rc;  // unit u: adapter u / rc, ranks 16 (u % rc) and up
-  const int stage_bytes = lin::kTileBytes + min(units, 16) * 2048, n_stages = min(lora::kTileStages, lora::kTileArena / stage_bytes);
+  const int stage_bytes = lin::kTileBytes + min(units, lora::kPass) * 2048, n_stages = min(lora::kTileStages, lora::kTileArena / stage_bytes);
   const int KB = (int)((p.K + 63) / 64), kb0 = (int)((int64_t)KB * share / C), kb1 = (int)((int64_t)KB * (share + 1) / C);
 
   if (warp == 0) {
@@ -310,7 +272,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u0 = pass0; ok && u0 < units; u0 += step) {
-      const int m = min(16, units - u0);
+      const int m = min(lora::kPass, units - u0);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
           ok = false;
@@ -347,7 +309,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u0 = pass0; ok && u0 < units; u0 += step, ++acc_i) {
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)min(16, units - u0) << 18) | ((128u >> 4) << 24);
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)min(lora::kPass, units - u0) << 18) | ((128u >> 4) << 24);
       const int buf = acc_i & 1;
       if (!(ok = warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
       ptx::tc_fence_after();
@@ -372,7 +334,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     wait_bar_drain(ptx::smem_u32(&drain), 0);
     __syncwarp();
   } else if (warp >= 6) {
-    if (blockIdx.x < p.scans * ((p.M + 255) / 256)) list_and_scan<256>(p, blockIdx.x, tid - 192);
+    if (blockIdx.x < (p.M + 255) / 256) list_adapters<256>(p, blockIdx.x, tid - 192);
   } else {
     const int q = warp & 3, row = q * 32 + lane, mine = s_id[row];
     const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -383,7 +345,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
       const int buf = acc_i & 1;
       if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
       ptx::tc_fence_after();
-      for (int u = u0; u < min(u0 + 16, units); ++u) {
+      for (int u = u0; u < min(u0 + lora::kPass, units); ++u) {
         const bool own = mine == s_list[u / rc];
         if (!__any_sync(0xffffffffu, own)) continue;
         uint32_t v[16];
@@ -418,21 +380,17 @@ void plan_lora_sums(LoraParams& p, int sms) {
     int64_t items = std::min<int64_t>(p.M, p.count) * ranks;
     if (p.K > 2048 && 2 * items + 64 <= sms) p.split = p.parts = 2;
     items *= p.split;
-    // scans on the SMs that are left (each a word that who reads the list looks at)
-    p.scans = (int32_t)std::min<int64_t>(p.scans, std::clamp<int64_t>(sms - items, 64, 128));
-    p.grid = (int32_t)(items + p.scans);
+    p.grid = (int32_t)(items + p.listed);
     return;
   }
-  // as many CTAs as SMs: one to a tile's passes as far as there may be some, and shares of K of two blocks and more; the others
-  // scan, as these do beside their products
-  const int64_t tiles = (p.M + 127) / 128, blocks = (p.M + 255) / 256, most = (std::min<int64_t>(128, p.count) * ranks + 15) / 16;
+  // as many CTAs as SMs: one to a tile's passes as far as there may be some, and shares of K of two blocks and more
+  const int64_t tiles = (p.M + 127) / 128, most = (std::min<int64_t>(128, p.count) * ranks + lora::kPass - 1) / lora::kPass;
   p.passes = (int32_t)std::clamp<int64_t>(sms / tiles / 2, 1, most);
   while (p.split < 8 && tiles * p.passes * p.split * 2 <= sms && 2 * p.split * 128 <= p.K) p.split *= 2;
   // FP32 results: an accumulator, whose additions truncate, takes 1024 products (of K above 16384 more)
   if (p.precise) p.split = (int32_t)std::max<int64_t>(p.split, std::min<int64_t>((p.K + 1023) / 1024, 16));
   p.parts = p.split;
-  p.grid = (int32_t)std::max<int64_t>(tiles * p.passes * p.split, sms);
-  p.scans = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.grid / blocks, 128));
+  p.grid = (int32_t)(tiles * p.passes * p.split);
 }
 
 cudaError_t launch_lora_sums(const LoraMaps& maps, const LoraParams& p, cudaStream_t s) {

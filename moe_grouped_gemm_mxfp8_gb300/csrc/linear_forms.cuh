@@ -58,11 +58,9 @@ constexpr int kStreamSmem = kStreamArena + kStreamBars * 8 + 32 + 1024;
 static_assert(kStreamSmem <= 232448, "shared memory budget");
 
 // ---- adapters
-constexpr int kLoraWarp = kThreads / 32;  // two warps more
-constexpr int kLoraThreads = kThreads + 64;
-// The stream form leaves room on its SM for a CTA of the sums, which it starts beside: 16 K registers and 13 KB
-constexpr int kLoraStreamArena = 192 * 1024;
-constexpr int kLoraStreamBound = 512;  // threads that the registers of a thread are bounded for, to 128
+constexpr int kLoraWarp = kThreads / 32;
+template <bool kF32>
+constexpr int kLoraWarps = kF32 ? 2 : 4;  // more: four, or two where the registers do not allow it
 
 }  // namespace lin
 
@@ -247,13 +245,13 @@ __device__ __forceinline__ int adapter_of(const LinearParams& p, int64_t m, uint
 // ---------------------------------------------------------------- adapters in the stream and pair form
 // The second factors join a tile's sum as further K blocks: for each adapter that any of the tile's rows has, and each 32 of
 // its ranks, a block whose W rows are the second factor's (by TMA) and whose x rows are the rows' sums, zeros in the rows of
-// other adapters.  Two warps of their own write those x rows and hand the stage over.  A sum enters as two BF16 numbers, the
+// other adapters.  Warps of their own write those x rows and hand the stage over.  A sum enters as two BF16 numbers, the
 // first truncated, so that it is off by 2^-17 at most; they take the halves of a 128-byte row, both against the same 32
 // ranks.  For FP32 results it is three numbers, which leave nothing out, of 16 ranks.  The lists of the adapters of 256 rows
 // come with the sums.
-// A zero does not keep an infinity or NaN of another adapter's factor out of a row.  The lists say whether their factors have
-// any: the warps then put zeros in their place where a factor has landed, and from then on the CTA's epilogues add,
-// row by row, what those elements give the rows whose adapter has them.
+// A zero does not keep an infinity or NaN of another adapter's factor out of a row.  The warps look at each factor where it has
+// landed and put zeros in the place of any; from then on the cluster's epilogues add, row by row, what those elements give the
+// rows whose adapter has them.
 template <bool kF32>
 struct SumTerms {
   static constexpr int kTerms = kF32 ? 3 : 2, kRanks = kF32 ? 16 : 32;  // of a block: BF16 numbers of a sum, ranks
@@ -268,10 +266,11 @@ struct AdapterShared {
   int32_t not_finite;                    // a factor of this cluster's tiles was not finite
 };
 
+// built_by: warps
 __device__ __forceinline__ void init_adapters(AdapterShared& a, int n_stages, int built_by) {
   for (int s = 0; s < n_stages; ++s) {
     ptx::mbar_init(ptx::smem_u32(&a.loaded[s]), 1);
-    ptx::mbar_init(ptx::smem_u32(&a.built[s]), 2 * built_by);
+    ptx::mbar_init(ptx::smem_u32(&a.built[s]), built_by);
   }
   a.not_finite = 0;
 }
@@ -315,30 +314,30 @@ struct AdapterBlocks {
   }
 };
 
-// The ranks from r0 on of two rows' sums (m and m + 32; past the last row: its own) as the 32-bit words of a block's row: the
+// The ranks from r0 on of kRows rows' sums (m, m + 32; past the last row: its own) as the 32-bit words of a block's row: the
 // leading bits of each, then what they leave, twice over for FP32 results; zeros past the rank.
-template <bool kF32>
-__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, uint32_t (&w)[2][32]) {
+template <bool kF32, int kRows>
+__device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int r0, uint32_t (&w)[kRows][32]) {
   using Terms = SumTerms<kF32>;
   constexpr int kFours = Terms::kRanks / 4, kWords = Terms::kRanks / 2;
   const int left = p.lora_rank - r0;
-  float4 sum[2][kFours] = {};
+  float4 sum[kRows][kFours] = {};
   for (int c = 0; c < p.lora_parts; ++c) {
-    float4 v[2][kFours];  // on their way together
+    float4 v[kRows][kFours];  // on their way together
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       const float* s = p.lora_s + c * p.lora_part + min(m + 32 * i, p.M - 1) * p.lora_rank + r0;
 #pragma unroll
       for (int j = 0; j < kFours; ++j) v[i][j] = 4 * j < left ? reinterpret_cast<const float4*>(s)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int j = 0; j < kFours; ++j)
         sum[i][j] = make_float4(sum[i][j].x + v[i][j].x, sum[i][j].y + v[i][j].y, sum[i][j].z + v[i][j].z, sum[i][j].w + v[i][j].w);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < kRows; ++i)
 #pragma unroll
     for (int j = 0; j < kFours; ++j) {
       float f[4] = {sum[i][j].x, sum[i][j].y, sum[i][j].z, sum[i][j].w};
@@ -371,51 +370,62 @@ __device__ __noinline__ void drop_not_finite(uint8_t* at, int r0, int r1, int st
     }
 }
 
-// A CTA's adapter warps (`half` 0 and 1) through a tile's blocks u0 .. u1 - 1, kKps to a stage, from `stage` on (a stage whose
+// A CTA's kWarps adapter warps (this one: `part`) through a tile's blocks u0 .. u1 - 1, kKps to a stage, from `stage` on (a stage whose
 // factors have landed is free).  x_at, w_at: where a block's rows of x and of W lie in its stage; x_rows (128 at most) of
 // them are written, which are p's from row0 on; to_rank: the CTA that issues the products, or -1.
-template <int kKps, bool kF32>
+template <int kKps, bool kF32, int kWarps>
 __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterShared& a, uint8_t* smem, int stage_bytes, int block_bytes,
-                                               int n_stages, int x_at, int x_rows, int w_at, int w_rows, int64_t block, int64_t row0,
-                                               int half, const AdapterList& list, int u0, int u1, int to_rank, int& stage,
+                                               int n_stages, int x_at, int x_rows, int w_at, int w_rows, int64_t row0,
+                                               int part, const AdapterList& list, int u0, int u1, int to_rank, int& stage,
                                                uint32_t& loaded_bits, const Ctl& ctl) {
   if (u0 >= u1) return true;
   const int lane = threadIdx.x & 31, ranks = p.lora_rank;
-  int own[2];  // the adapters of this lane's rows
+  constexpr int kRows = 4 / kWarps;  // a lane's
+  const int r0 = 32 * kRows * part + lane;
+  int own[kRows];  // the adapters of this lane's rows
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = row0 + (2 * half + i) * 32 + lane;
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t m = row0 + r0 + 32 * i;
     own[i] = m < p.M ? p.lora_ids[m] : -1;
   }
-  uint32_t flag = 0;  // (at most 128 scans)
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    if (32 * g + lane < p.lora_scans) flag |= p.lora_flags[block * p.lora_scans + 32 * g + lane];
   using Terms = SumTerms<kF32>;
   AdapterBlocks at(list, u0);
-  uint32_t words[2][32];
-  split_sums<kF32>(p, row0 + 64 * half + lane, Terms::kRanks * at.c, words);
+  uint32_t words[kRows][32];
+  split_sums<kF32, kRows>(p, row0 + r0, Terms::kRanks * at.c, words);
   int c_held = at.c;
-  const bool found = __any_sync(0xffffffffu, flag);
-  const uint32_t smem0 = ptx::smem_u32(smem) + x_at + (64 * half + lane) * 128, turn = lane & 7;
-  const bool write[2] = {64 * half + lane < x_rows, 64 * half + 32 + lane < x_rows};
+  const uint32_t smem0 = ptx::smem_u32(smem) + x_at + r0 * 128, turn = lane & 7;
+  const int w1 = (part + 1) * w_rows / kWarps, w0 = w1 - w_rows / kWarps + lane;  // w_rows: multiples of 16, 128 at most
   for (int u = u0; u < u1; u += kKps) {
     const uint32_t xb = smem0 + stage * stage_bytes;
+    bool found = false;  // an infinity or NaN in the stage's factors
 #pragma unroll
     for (int h = 0; h < kKps; ++h) {
       if (u + h >= u1) break;
       const int steps = Terms::steps(ranks, Terms::kRanks * at.c), adapter = at.adapter();
       if (at.c != c_held) {
         c_held = at.c;
-        split_sums<kF32>(p, row0 + 64 * half + lane, Terms::kRanks * at.c, words);
+        split_sums<kF32, kRows>(p, row0 + r0, Terms::kRanks * at.c, words);
       }
       if (h == 0) {
         if (!warp_wait_quick(ptx::smem_u32(&a.loaded[stage]), loaded_bits >> stage & 1, ctl)) return false;
         loaded_bits ^= 1u << stage;
       }
+      uint8_t* wb = smem + stage * stage_bytes + h * block_bytes + w_at;
+      uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!write[i]) continue;
+      for (int i = 0; i < kRows; ++i) {
+        const int r = w0 + 32 * i;  // a row of W
+        uint4 v[Terms::kPieces];
+#pragma unroll
+        for (int k = 0; k < Terms::kPieces; ++k)
+          v[k] = r < w1 && k < 2 * steps ? *reinterpret_cast<const uint4*>(wb + r * 128 + ((k ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < Terms::kPieces; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
+        }
+        if (r0 + 32 * i >= x_rows) continue;
         const uint32_t to = xb + h * block_bytes + i * 4096, keep = own[i] == adapter ? 0xffffffffu : 0u;
 #pragma unroll
         for (int k = 0; k < Terms::kPieces; ++k) {
@@ -428,7 +438,10 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
           }
         }
       }
-      if (found) drop_not_finite(smem + stage * stage_bytes + h * block_bytes + w_at, half * w_rows / 2, (half + 1) * w_rows / 2, steps);
+      if (__any_sync(0xffffffffu, (most & 0xffffu) >= 0x7f80u || most >> 16 >= 0x7f80u)) {
+        drop_not_finite(wb, w1 - w_rows / kWarps, w1, steps);
+        found = true;
+      }
       at.next();
     }
     ptx::fence_proxy_async_smem();
@@ -660,7 +673,7 @@ __global__ void __launch_bounds__(512, 1) linear_direct_kernel(const __grid_cons
 // Tiles of 256 x BN in groups of kGroupM row tiles, column tiles outermost within a group, so that the
 // tiles in flight share rows of x and of W in L2.
 template <int kAct, int kKps, bool kF32, bool kLora>
-__global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads, 1)
+__global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWarps<kF32> : 0), 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   extern __shared__ uint8_t smem_raw[];
@@ -694,7 +707,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
       ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
       ptx::mbar_init(ptx::smem_u32(&acce[b]), 16);
     }
-    if constexpr (kLora) init_adapters(ad, n_stages, 2);
+    if constexpr (kLora) init_adapters(ad, n_stages, 2 * lin::kLoraWarps<kF32>);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0;
     *s_err = 0;
@@ -903,11 +916,11 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
     __syncwarp();
   } else if (kLora && warp >= lin::kLoraWarp) {
     if constexpr (kLora) {
-      const int half = warp - lin::kLoraWarp;
+      const int part = warp - lin::kLoraWarp;
       int stage = 0;
       uint32_t loaded_bits = 0;
       if (p.lora_early) ptx::griddep_wait();
-      if (half == 0)
+      if (part == 0)
         for (int i = blockIdx.x * 32 + lane; i < p.lora_err_count; i += gridDim.x * 32)
           if (const uint32_t e = p.lora_errs[i]) atomicOr(s_err, e);
       for (int t = first; t < tiles; t += pairs) {
@@ -916,8 +929,8 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
         AdapterList list;
         list.load(p, mt);
         stage = (stage + KB) % n_stages;
-        if (!build_adapters<kKps, kF32>(p, ad, smem, stage_bytes, block_bytes, n_stages, 0, 128, lin::kTileBytes, BN / 2, mt,
-                                  (int64_t)mt * 256 + 128 * rank, half, list, 0, list.n * rank_chunks, 0, stage, loaded_bits, ctl))
+        if (!build_adapters<kKps, kF32, lin::kLoraWarps<kF32>>(p, ad, smem, stage_bytes, block_bytes, n_stages, 0, 128, lin::kTileBytes, BN / 2,
+                                  (int64_t)mt * 256 + 128 * rank, part, list, 0, list.n * rank_chunks, 0, stage, loaded_bits, ctl))
           break;
       }
     }
@@ -1061,15 +1074,14 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraThreads : lin::kPairThreads,
 // Cluster c takes the tiles c, c + clusters, ...; its CTA of rank r the K blocks [KB r / S, KB (r + 1) / S).
 // A tile is 128 rows of W; with the gated activation 64 gate rows and the 64 up rows of the same columns.
 template <int kAct, bool kF32, bool kLora>
-__global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads, 1)
+__global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<kF32> : 0), 1)
     linear_stream_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p) {
   constexpr bool kGated = kAct == GMMFR_ACT_SWIGLU;
   constexpr int kCols = kGated ? 64 : 128;  // columns of y per tile
   constexpr int kEpi = lin::kThreads - 64, kKps = lin::kStreamKps;  // kEpi: the epilogue's threads
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kArena = kLora ? lin::kLoraStreamArena : lin::kStreamArena;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kArena);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lin::kStreamArena);
   uint64_t* empty = full + lin::kStreamMaxStages;
   uint64_t* accf = empty + lin::kStreamMaxStages;
   uint64_t* acce = accf + 2;
@@ -1088,7 +1100,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
   const int clusters = gridDim.x / S, first = blockIdx.x / S, tiles = p.tiles_n;
   // [T][128]: in the ring's place when no tile follows, whose loads would write there
   float* part = reinterpret_cast<float*>(smem + (tiles <= clusters ? 0 : n_stages * stage_bytes));
-  [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + kArena + lin::kStreamBars * 8 + 32);
+  [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kStreamArena + lin::kStreamBars * 8 + 32);
   using Terms = SumTerms<kF32>;
   [[maybe_unused]] const int rank_chunks = Terms::blocks(p.lora_rank);  // kLora: blocks of an adapter
   // one accumulator, or two in turn for the chunks of FP32 results
@@ -1105,7 +1117,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
       ptx::mbar_init(ptx::smem_u32(&accf[b]), 1 + p.test_stall);
       ptx::mbar_init(ptx::smem_u32(&acce[b]), 8);
     }
-    if constexpr (kLora) init_adapters(ad, n_stages, 1);
+    if constexpr (kLora) init_adapters(ad, n_stages, lin::kLoraWarps<kF32>);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     ptx::mbar_init(ptx::smem_u32(pready), S);
     ptx::mbar_init(ptx::smem_u32(pfree), S);
@@ -1294,7 +1306,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
     __syncwarp();
   } else if (kLora && warp >= lin::kLoraWarp) {
     if constexpr (kLora) {
-      const int half = warp - lin::kLoraWarp;
+      const int part = warp - lin::kLoraWarp;
       int stage = 0;
       uint32_t loaded_bits = 0;
       if (!p.beside) ptx::griddep_wait();
@@ -1302,7 +1314,7 @@ __global__ void __launch_bounds__(kLora ? lin::kLoraStreamBound : lin::kThreads,
       list.load(p, 0);
       for (int t = first; t < tiles; t += clusters) {
         stage = (stage + kb1 - kb0) % n_stages;
-        if (!build_adapters<kKps, kF32>(p, ad, smem, stage_bytes, block_bytes, n_stages, lin::kTileBytes, npad, 0, 128, 0, 0, half, list,
+        if (!build_adapters<kKps, kF32, lin::kLoraWarps<kF32>>(p, ad, smem, stage_bytes, block_bytes, n_stages, lin::kTileBytes, npad, 0, 128, 0, part, list,
                                   list.n * rank_chunks * (int)rank / S, list.n * rank_chunks * ((int)rank + 1) / S, -1, stage, loaded_bits,
                                   ctl))
           break;
@@ -1475,7 +1487,7 @@ static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cud
   auto kernel = p.form == kLinearStream ? linear_stream_kernel<kAct, kF32, kLora>
                                         : (p.kps == 1 ? linear_pair_kernel<kAct, 1, kF32, kLora> : linear_pair_kernel<kAct, 2, kF32, kLora>);
   constexpr int kMore = kLora ? (int)sizeof(AdapterShared) : 0, kPairBytes = lin::kPairSmem + kMore;
-  constexpr int kStreamBytes = lin::kStreamSmem - (kLora ? lin::kStreamArena - lin::kLoraStreamArena : 0) + kMore;
+  constexpr int kStreamBytes = lin::kStreamSmem + kMore;
   static_assert(kStreamBytes <= 232448 && kPairBytes <= 232448, "shared memory budget");
   const int smem = p.form == kLinearStream ? kStreamBytes : kPairBytes;
   static int configured_device = -1;
@@ -1492,7 +1504,7 @@ static cudaError_t launch_one(const LinearMaps& maps, const LinearParams& p, cud
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)p.grid);
-  lc.blockDim = dim3(kLora ? lin::kLoraThreads : (p.form == kLinearStream ? lin::kThreads : lin::kPairThreads));
+  lc.blockDim = dim3((p.form == kLinearStream ? lin::kThreads : lin::kPairThreads) + (kLora ? 32 * lin::kLoraWarps<kF32> : 0));
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute attr[2];

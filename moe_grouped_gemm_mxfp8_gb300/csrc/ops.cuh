@@ -110,10 +110,8 @@ struct LinearParams {
   int32_t lora_count, lora_rank;
   int64_t lora_rows;
   // of each 256 rows: kLoraListInts words, the number of adapters and from the fourth on each, in the order of their first
-  // rows; and lora_scans words, whether a scan of their second factors met an infinity or NaN
+  // rows
   const int32_t* lora_lists;
-  const uint32_t* lora_flags;
-  int32_t lora_scans;
   const uint32_t* lora_errs;  // error bits of the sums' CTAs, which the pair form passes on
   int32_t lora_err_count;
   int32_t lora_own;           // direct form: each CTA makes the sums itself, of at most two units of 16 ranks
@@ -136,17 +134,14 @@ struct LoraParams {
   float* s;                    // [parts, M, rank]
   int64_t M, K, ldx;
   int32_t count, rank;
-  const __nv_bfloat16* b;      // second factors [count, rows, rank], which are scanned
-  int64_t rows;
   int32_t* lists;              // as LinearParams'
-  uint32_t* flags;
-  int32_t scans;               // CTAs to a list; 0: no lists
+  int32_t listed;              // whether lists are wanted
   int32_t precise;             // for FP32 results
   uint32_t* errs;              // [grid], error bits of each CTA: more than kLoraFewRows rows
   int64_t timeout_ns;
   int32_t test_stall;
   // plan_lora_sums' choice: shares of the K range, CTAs to a tile's passes (many rows), CTAs in all, and the parts that a
-  // sum is left in, M rows after one another; it also bounds scans
+  // sum is left in, M rows after one another
   int32_t split, passes, grid, parts;
 };
 struct LoraMaps {
