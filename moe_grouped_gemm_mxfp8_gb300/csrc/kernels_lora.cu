@@ -5,7 +5,7 @@
 //   few   up to 128 rows: each adapter's rows gathered, so that every factor is read once and all of them are on their way at
 //         once.  Products by mma.sync, 16 bytes of a row at a time from global memory straight into a lane's operand
 //         registers: they wait for memory, and an adapter has a few rows.
-//   many  128 rows of x at a time, by TMA and tcgen05: the rows are one operand, 16 ranks of up to 16 of their adapters'
+//   many  128 rows of x at a time, by TMA and tcgen05: the rows are one operand, 16 ranks of up to 8 of their adapters'
 //         factors the other; of what comes out a row keeps its own adapter's columns.
 // Several CTAs share a K range.  CTAs also list the adapters of each 256 rows.  The product's launch follows
 // at once and begins with its weights; only its adapters wait.
@@ -15,7 +15,7 @@ namespace gmmfr {
 namespace lora {
 constexpr int kFewThreads = 512;
 constexpr int kTileThreads = 448, kTileStages = 10, kTileArena = 10 * (lin::kTileBytes + 2048);
-constexpr int kPass = 16;  // units of a pass
+constexpr int kPass = 8;  // units of a pass
 }  // namespace lora
 
 namespace {
@@ -207,10 +207,13 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
 }
 
 // ============================================================================ many rows
-// CTA (c, p, tile): the 128 rows of a tile, share c of the K range, every `passes`-th pass from p on of up to 16 units: 16 ranks of
-// an adapter.  Who reads the sums adds the shares' parts.  (Clusters that join them on the chip wait for SMs that lie
-// together: 16 us more with clusters of 8.)  Warp 0 TMA, warp 1 MMA, warps 2..5
-// epilogue, warps 6..13 lists.
+// A tile is 128 rows; its items are passes over up to 8 units (16 ranks of an adapter) in shares of K, which its CTAs take in
+// turn: how many adapters a tile has is known here only.  Who reads the sums adds the shares' parts.  (Clusters that join them
+// on the chip wait for SMs that lie together: 16 us more with clusters of 8.)  With passes given out by what all adapters
+// would need, 2048 rows of 4096 x 4096 and one, 16, 32 of 64 adapters took 51.6, 88.9, 101 us with the product; so 47.9, 67.0,
+// 89.1.  Passes of 16: 47.9, 73.3, 87.1; 300 rows of 16 adapters of rank 64: 50.6, of 8: 43.7.  Up to 8 shares: 27.9 for one of
+// them, 4: 22.8 (their reader adds the parts).
+// Warp 0 TMA, warp 1 MMA, warps 2..5 epilogue, warps 6..13 lists.
 __global__ void __launch_bounds__(lora::kTileThreads, 1)
     lora_sums_many_kernel(const __grid_constant__ LoraMaps maps, const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -221,8 +224,8 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
   __shared__ uint32_t s_first[4], tmem_slot, s_err;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp: uniform
-  const int C = p.split, share = blockIdx.x % C, pass0 = lora::kPass * (blockIdx.x / C % p.passes), step = lora::kPass * p.passes;
-  const int64_t row0 = (int64_t)(blockIdx.x / C / p.passes) * 128;
+  const int C = p.split, first = blockIdx.x % p.tile_ctas;
+  const int64_t row0 = (int64_t)(blockIdx.x / p.tile_ctas) * 128;
   if (tid == 0) {
     for (int s = 0; s < lora::kTileStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
@@ -264,14 +267,22 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
   const Ctl ctl{&abort_flag, &s_err, p.timeout_ns};
   const int rc = (p.rank + 15) / 16, units = n * rc;  // unit u: adapter u / rc, ranks 16 (u % rc) and up
   const int stage_bytes = lin::kTileBytes + min(units, lora::kPass) * 2048, n_stages = min(lora::kTileStages, lora::kTileArena / stage_bytes);
-  const int KB = (int)((p.K + 63) / 64), kb0 = (int)((int64_t)KB * share / C), kb1 = (int)((int64_t)KB * (share + 1) / C);
+  // item i: the units from kPass (i / C) on, share i % C of the K blocks
+  const int KB = (int)((p.K + 63) / 64), items = (units + lora::kPass - 1) / lora::kPass * C;
+  auto item = [&](int i, int& u0, int& kb0, int& kb1) {
+    u0 = i / C * lora::kPass;
+    kb0 = (int)((int64_t)KB * (i % C) / C);
+    kb1 = (int)((int64_t)KB * (i % C + 1) / C);
+  };
 
   if (warp == 0) {
     const uint64_t pol = ptx::l2_evict_last_policy();
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u0 = pass0; ok && u0 < units; u0 += step) {
+    for (int i = first; ok && i < items; i += p.tile_ctas) {
+      int u0, kb0, kb1;
+      item(i, u0, kb0, kb1);
       const int m = min(lora::kPass, units - u0);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait_quick(ptx::smem_u32(&empty[stage]), phase ^ 1, ctl)) {
@@ -308,7 +319,9 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     int stage = 0, acc_i = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u0 = pass0; ok && u0 < units; u0 += step, ++acc_i) {
+    for (int i = first; ok && i < items; i += p.tile_ctas, ++acc_i) {
+      int u0, kb0, kb1;
+      item(i, u0, kb0, kb1);
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)min(lora::kPass, units - u0) << 18) | ((128u >> 4) << 24);
       const int buf = acc_i & 1;
       if (!(ok = warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
@@ -339,9 +352,11 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     const int q = warp & 3, row = q * 32 + lane, mine = s_id[row];
     const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
     const float scale = mine >= 0 && p.scale ? p.scale[mine] : 1.f;
-    float* to = p.s + (share * p.M + row0 + row) * p.rank;
     int acc_i = 0;
-    for (int u0 = pass0; u0 < units; u0 += step, ++acc_i) {
+    for (int i = first; i < items; i += p.tile_ctas, ++acc_i) {
+      int u0, kb0, kb1;
+      item(i, u0, kb0, kb1);
+      float* to = p.s + (i % C * p.M + row0 + row) * p.rank;
       const int buf = acc_i & 1;
       if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
       ptx::tc_fence_after();
@@ -375,7 +390,7 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
 // ============================================================================ plan and launch
 void plan_lora_sums(LoraParams& p, int sms) {
   const int64_t ranks = (p.rank + 15) / 16;
-  p.split = p.passes = p.parts = 1;
+  p.split = p.tile_ctas = p.parts = 1;
   if (p.M <= kLoraFewRows) {
     int64_t items = std::min<int64_t>(p.M, p.count) * ranks;
     if (p.K > 2048 && 2 * items + 64 <= sms) p.split = p.parts = 2;
@@ -383,14 +398,15 @@ void plan_lora_sums(LoraParams& p, int sms) {
     p.grid = (int32_t)(items + p.listed);
     return;
   }
-  // as many CTAs as SMs: one to a tile's passes as far as there may be some, and shares of K of two blocks and more
+  // as many CTAs as SMs, which share out a tile's items: passes over its adapters in shares of K, of two blocks and more
   const int64_t tiles = (p.M + 127) / 128, most = (std::min<int64_t>(128, p.count) * ranks + lora::kPass - 1) / lora::kPass;
-  p.passes = (int32_t)std::clamp<int64_t>(sms / tiles / 2, 1, most);
-  while (p.split < 8 && tiles * p.passes * p.split * 2 <= sms && 2 * p.split * 128 <= p.K) p.split *= 2;
+  const int64_t ctas = std::max<int64_t>(sms / tiles, 1);
+  while (p.split < 4 && p.split * 2 <= ctas && 2 * p.split * 128 <= p.K) p.split *= 2;
   // FP32 results: an accumulator, whose additions truncate, takes 1024 products (of K above 16384 more)
   if (p.precise) p.split = (int32_t)std::max<int64_t>(p.split, std::min<int64_t>((p.K + 1023) / 1024, 16));
   p.parts = p.split;
-  p.grid = (int32_t)(tiles * p.passes * p.split);
+  p.tile_ctas = (int32_t)std::min(ctas, most * p.split);
+  p.grid = (int32_t)(tiles * p.tile_ctas);
 }
 
 cudaError_t launch_lora_sums(const LoraMaps& maps, const LoraParams& p, cudaStream_t s) {

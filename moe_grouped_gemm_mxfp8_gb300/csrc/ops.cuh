@@ -140,9 +140,9 @@ struct LoraParams {
   uint32_t* errs;              // [grid], error bits of each CTA: more than kLoraFewRows rows
   int64_t timeout_ns;
   int32_t test_stall;
-  // plan_lora_sums' choice: shares of the K range, CTAs to a tile's passes (many rows), CTAs in all, and the parts that a
+  // plan_lora_sums' choice: shares of the K range, CTAs to a tile (many rows), CTAs in all, and the parts that a
   // sum is left in, M rows after one another
-  int32_t split, passes, grid, parts;
+  int32_t split, tile_ctas, grid, parts;
 };
 struct LoraMaps {
   CUtensorMap x, a;  // [M, K], boxes of 128 rows; first factors, boxes of 16 rows: more than kLoraFewRows rows
