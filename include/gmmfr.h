@@ -550,7 +550,7 @@ GMMFR_API gmmfr_status gmmfr_lora_linear(const gmmfr_lora_problem* problem, cons
  *   dW_e  = sum over t of dy[t,n] x[t,k]         gmmfr_grouped_linear_grad_weight; an expert without rows has zeros
  * An infinity or NaN in a row reaches that row of y (or dx) alone and the gradient of its own expert; one in a row of no
  * expert reaches nothing, one in an expert's weights its own rows.
- *   M             rows of x and y, 0 <= M < 2^31
+ *   M             rows of x and y, 0 <= M <= 2^31 - 1024
  *   N, K, E       sizes of the weights: N and K multiples of 8 in [8, 2^24), N * K < 2^38; 1 <= E <= 1024
  *   ldx, ldy      elements from one row of x, and of y or dy, to the next; 0 stands for the row's length.  Rows that are
  *                 read lie at multiples of 8

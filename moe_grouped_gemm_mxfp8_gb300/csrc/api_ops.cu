@@ -420,7 +420,8 @@ gmmfr_status run_linear(const gmmfr_linear_problem* problem, const void* x, cons
 // ---------------------------------------------------------------- products grouped by expert
 gmmfr_status validate_grouped(const gmmfr_grouped_problem* p) {
   if (!p) return fail(GMMFR_ERR_INVALID_ARG, "problem is NULL");
-  if (p->M < 0 || p->M >= kMaxSize) return fail(GMMFR_ERR_INVALID_ARG, "M=%lld out of range [0, 2^31)", (long long)p->M);
+  if (p->M < 0 || p->M > kMaxSize - 1024)  // rows are counted in 32 bits, in steps of up to 256
+    return fail(GMMFR_ERR_INVALID_ARG, "M=%lld out of range [0, 2^31 - 1024]", (long long)p->M);
   if (p->N < 8 || p->K < 8 || p->N % 8 || p->K % 8 || p->N >= (int64_t(1) << 24) || p->K >= (int64_t(1) << 24) ||
       p->N * p->K >= (int64_t(1) << 38))
     return fail(GMMFR_ERR_INVALID_ARG, "N=%lld K=%lld are not multiples of 8 in [8, 2^24) with a product below 2^38",

@@ -44,6 +44,13 @@ BAD = [
 ]
 
 
+def test_row_numbers_stay_within_32_bits():
+    assert B.gmmfr_grouped_linear_workspace_size(_problem(M=(1 << 31) - 1024)) > 0
+    for call in (B.gmmfr_grouped_linear_workspace_size, _product, _grad):
+        with pytest.raises(B.GmmfrError, match="M=2147482625"):
+            call(_problem(M=(1 << 31) - 1023))
+
+
 @pytest.mark.parametrize("kw,msg", BAD, ids=[m + str(i) for i, (_, m) in enumerate(BAD)])
 def test_refused_problems(kw, msg):
     for call in (B.gmmfr_grouped_linear_workspace_size, _product, _grad):
