@@ -572,7 +572,8 @@ typedef struct {
   int32_t accumulate;
 } gmmfr_grouped_problem;
 
-/* Workspace bytes of both calls (256-byte aligned; contents on entry do not matter).  Host only. */
+/* Workspace bytes of both calls (256-byte aligned; contents on entry do not matter); more for more rows where the weights are
+ * few, whose gradient's rows then go in shares.  Host only. */
 GMMFR_API gmmfr_status gmmfr_grouped_linear_workspace_size(const gmmfr_grouped_problem* problem, size_t* bytes);
 
 /* x [M, K] BF16 and weight BF16, dense, both 16-byte aligned; group_list [E] int64, checked on the device: sizes that are

@@ -1047,8 +1047,9 @@ class GroupedLinear(_Handle):
         self._fn, self._fn_grad = self._entry("gmmfr_grouped_linear"), self._entry("gmmfr_grouped_linear_grad_weight")
         self._cx, self._cy, self._cg, self._co = (ctypes.c_void_p() for _ in range(4))
         self._cw = ctypes.c_void_p(self._wptr)
-        for p in (self._forward, self._input, self._weight):
-            self._need = gmmfr_grouped_linear_workspace_size(p)
+        self._need = gmmfr_grouped_linear_workspace_size(self._weight)
+        self._weight.M = 1 << 30  # of few tiles the gradient takes more with many rows
+        self._shared = gmmfr_grouped_linear_workspace_size(self._weight) > self._need
 
     def _space(self, stream):
         s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
@@ -1105,6 +1106,8 @@ class GroupedLinear(_Handle):
             out = self._new(self._shape, self._grad, stream)
         else:
             _dense(out, "out", self._shape, self._grad, dev)
+        if self._shared:
+            self._need = max(self._need, gmmfr_grouped_linear_workspace_size(p))
         ws = self._space(stream)
         cx, cy, cg, co = self._cx, self._cy, self._cg, self._co
         cx.value, cy.value, cg.value, co.value = x.data_ptr(), dy.data_ptr(), gptr, out.data_ptr()

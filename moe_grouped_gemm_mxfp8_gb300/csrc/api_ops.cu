@@ -441,9 +441,18 @@ gmmfr_status validate_grouped(const gmmfr_grouped_problem* p) {
   return GMMFR_OK;
 }
 
-// Error words; the gradient's CTAs' copies of the experts' ends
-size_t grouped_ws_bytes(const gmmfr_grouped_problem* p) {
-  return align256(gmmfr::kHdrBytes + sizeof(int32_t) * (size_t)gmmfr::grouped_grad_ctas(p->N, p->K, p->E, gmmfr::sm_count()) * p->E);
+// Error words; the gradient's CTAs' copies of the experts' ends; sums of shares of their rows, if there are more than one
+struct GroupedLayout {
+  int shares;
+  size_t parts, total;
+};
+GroupedLayout grouped_layout(const gmmfr_grouped_problem* p) {
+  const int sms = gmmfr::sm_count();
+  GroupedLayout L;
+  L.shares = p->M ? gmmfr::grouped_grad_shares(p->M, p->N, p->K, p->E, sms) : 1;
+  L.parts = align256(gmmfr::kHdrBytes + sizeof(int32_t) * (size_t)gmmfr::grouped_grad_ctas(p->N, p->K, p->E * L.shares, sms) * p->E);
+  L.total = L.parts + (L.shares > 1 ? align256(sizeof(float) * (size_t)L.shares * p->E * p->N * p->K) : 0);
+  return L;
 }
 
 }  // namespace
@@ -630,7 +639,7 @@ gmmfr_status gmmfr_lora_linear(const gmmfr_lora_problem* problem, const void* x,
 gmmfr_status gmmfr_grouped_linear_workspace_size(const gmmfr_grouped_problem* problem, size_t* bytes) {
   if (gmmfr_status st = validate_grouped(problem)) return st;
   if (!bytes) return fail(GMMFR_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = grouped_ws_bytes(problem);
+  *bytes = grouped_layout(problem).total;
   return GMMFR_OK;
 }
 
@@ -689,7 +698,8 @@ gmmfr_status gmmfr_grouped_linear_grad_weight(const gmmfr_grouped_problem* probl
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dweight, 16))
     return fail(GMMFR_ERR_INVALID_ARG, "dy, x and dweight must be 16-byte aligned");
   if (!aligned(group_list, 8)) return fail(GMMFR_ERR_INVALID_ARG, "group_list is not aligned to its element size");
-  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, grouped_ws_bytes(problem))) return st;
+  const GroupedLayout L = grouped_layout(problem);
+  if (gmmfr_status st = check_workspace(workspace, workspace_bytes, L.total)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.M == 0) {
     cudaError_t e = cudaMemsetAsync(workspace, 0, 8, s);
@@ -709,12 +719,17 @@ gmmfr_status gmmfr_grouped_linear_grad_weight(const gmmfr_grouped_problem* probl
   g.group_list_type = p.group_list_type;
   g.out_f32 = f32;
   g.accumulate = p.accumulate;
+  g.shares = L.shares;
+  g.out = dweight;
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.parts);
+  g.parts = parts;
   PFN_cuTensorMapEncodeTiled_v12000 encode = gmmfr::tensor_map_encoder();
   if (!encode) return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   gmmfr::GroupedGradMaps maps;
   if (!encode_rows(encode, p.transposed ? &maps.b : &maps.a, dy, p.M, p.N, stride_or(p.ldy, p.N), 64) ||
       !encode_rows(encode, p.transposed ? &maps.a : &maps.b, x, p.M, p.K, stride_or(p.ldx, p.K), 64) ||
-      !encode_slices(encode, &maps.out, dweight, f32, p.E, g.A, g.B, f32 ? 32 : 64, 32))
+      !(L.shares > 1 ? encode_slices(encode, &maps.out, parts, true, p.E * L.shares, g.A, g.B, 32, 32)
+                     : encode_slices(encode, &maps.out, dweight, f32, p.E, g.A, g.B, f32 ? 32 : 64, 32)))
     return fail(GMMFR_ERR_CUDA, "cuTensorMapEncodeTiled failed (ldx=%lld ldy=%lld)", (long long)p.ldx, (long long)p.ldy);
   cudaError_t e = gmmfr::launch_grouped_grad(maps, g, gmmfr::sm_count(), s);
   if (e != cudaSuccess) return cuda_fail(e, "grouped gradient launch");

@@ -24,6 +24,7 @@
 namespace gmmfr {
 namespace grp {
 
+constexpr int kAddThreads = 256;
 constexpr int kThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
 constexpr int kBK = 64;        // K (or rows) per stage
 constexpr int kTileBytes = 128 * 128;
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
 }
 
 // ============================================================================ weights
-// Unit u is tile u % (TA TB) of expert u / (TA TB); pair c takes the units c, c + pairs, ...  Both CTAs' loads count on rank
+// Unit u is tile u % (TA TB) of slice u / (TA TB): share s of expert e's rows is slice s E + e.  Pair c takes the units c, c + pairs, ...  Both CTAs' loads count on rank
 // 0's barrier, but for an expert's last rows where their number is not a multiple of 16 (a product's K): these count on
 // each CTA's own, its warp 1 puts zeros in place of the rows that follow, and rank 1's tells rank 0's.  (With that way for
 // all rows, which takes some 500 cycles longer, 65536 rows of 64 experts, 2048 x 1024: 200 us.)
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
   const Ctl ctl{abort_flag, s_err, p.timeout_ns};
   const uint32_t smem_base = ptx::smem_u32(smem);
   const int TA = (int)((p.A + 255) / 256), TB = (int)((p.B + 255) / 256), TT = TA * TB;
-  const int64_t units = (int64_t)p.E * TT;
+  const int64_t units = (int64_t)p.E * p.shares * TT;
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
   constexpr int kPer = kF32 ? grp::kChunk : grp::kGradChunk;  // blocks to an accumulator
   auto unit_at = [&](int64_t u, int& e, int& ta, int& tb) {
@@ -490,9 +491,15 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
     ta = r / TB;
     tb = r - ta * TB;
   };
-  auto rows_of = [&](int e, int& start) {
+  auto rows_of = [&](int slice, int& start) {
+    const int share = p.shares > 1 ? slice / p.E : 0, e = slice - share * p.E;
     start = e ? ends[e - 1] : 0;
-    return ends[e] - start;
+    const int rows = ends[e] - start;
+    if (p.shares == 1) return rows;
+    const int64_t blocks = (rows + grp::kBK - 1) / grp::kBK;
+    const int r0 = (int)(blocks * share / p.shares * grp::kBK);
+    start += r0;
+    return (int)min((int64_t)rows, blocks * (share + 1) / p.shares * grp::kBK) - r0;
   };
 
   if (warp == 0) {
@@ -717,6 +724,39 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
   }
 }
 
+// The shares' sums of the weights' gradient, added in their order
+__global__ void __launch_bounds__(grp::kAddThreads) add_shares_kernel(const __grid_constant__ GroupedGradParams p) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int64_t pieces = p.E * p.A * p.B / 8;  // of 8 numbers: rows are multiples of 8
+  for (int64_t i = (int64_t)blockIdx.x * grp::kAddThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * grp::kAddThreads) {
+    const float4* at = reinterpret_cast<const float4*>(p.parts) + 2 * i;
+    float4 v[2] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.shares; ++s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 w = at[2 * pieces * s + h];
+        v[h] = make_float4(v[h].x + w.x, v[h].y + w.y, v[h].z + w.z, v[h].w + w.w);
+      }
+    }
+    if (p.out_f32) {
+      float4* to = static_cast<float4*>(p.out) + 2 * i;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (p.accumulate) {
+          const float4 w = to[h];
+          v[h] = make_float4(w.x + v[h].x, w.y + v[h].y, w.z + v[h].z, w.w + v[h].w);
+        }
+        to[h] = v[h];
+      }
+    } else {
+      static_cast<uint4*>(p.out)[i] = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[0].z, v[0].w), pack_bf16(v[1].x, v[1].y),
+                                                 pack_bf16(v[1].z, v[1].w));
+    }
+  }
+}
+
 // ============================================================================ launch
 template <auto kKernel, int kSmem, typename Maps, typename Params>
 static cudaError_t launch_pairs(const Maps& maps, const Params& p, int64_t units, int sms, cudaStream_t s) {
@@ -755,12 +795,38 @@ cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedParams& p, bool
   return launch_pairs<grouped_kernel<false, false>, grp::kSmem>(maps, p, units, sms, s);
 }
 
-int grouped_grad_ctas(int64_t A, int64_t B, int64_t E, int sms) {
-  return (int)(2 * std::min<int64_t>(sms / 2, E * ((A + 255) / 256) * ((B + 255) / 256)));
+// Where the experts' tiles leave half of the pairs idle or more, shares of their rows take these, of 512 on average if there are
+// three of them.  One expert of 136 x 200 and 16384 rows 94 us, in shares 15.4; of 392 x 648 and 22395 rows 127, 26.4; eight of
+// 512 x 512 and 65536 rows 40.7, 35.7, with all rows in one 274, 148.  The second launch and the parts' way cost 1 to 2 us: 1024
+// rows of 256 x 256 9.6, in two shares 10.6; 2048 rows 13.7, in four 10.6.  Shares of 256: 18.8 for the first.
+int grouped_grad_shares(int64_t M, int64_t A, int64_t B, int64_t E, int sms) {
+  const int64_t tiles = E * ((A + 255) / 256) * ((B + 255) / 256), wanted = M / E / 512;
+  return wanted < 3 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(sms / 2 / tiles, wanted));
+}
+
+int grouped_grad_ctas(int64_t A, int64_t B, int64_t slices, int sms) {
+  return (int)(2 * std::min<int64_t>(sms / 2, slices * ((A + 255) / 256) * ((B + 255) / 256)));
 }
 
 cudaError_t launch_grouped_grad(const GroupedGradMaps& maps, const GroupedGradParams& p, int sms, cudaStream_t s) {
-  const int64_t units = grouped_grad_ctas(p.A, p.B, p.E, sms) / 2;
+  const int64_t units = grouped_grad_ctas(p.A, p.B, (int64_t)p.E * p.shares, sms) / 2;
+  if (p.shares > 1) {
+    GroupedGradParams q = p;
+    q.accumulate = 0;
+    cudaError_t e = launch_pairs<grouped_grad_kernel<true>, grp::kGradSmem>(maps, q, units, sms, s);
+    if (e != cudaSuccess) return e;
+    const int64_t pieces = p.E * p.A * p.B / 8;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)std::min<int64_t>((pieces + grp::kAddThreads - 1) / grp::kAddThreads, 4 * sms));
+    lc.blockDim = dim3(grp::kAddThreads);
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, add_shares_kernel, p);
+  }
   if (p.out_f32) return launch_pairs<grouped_grad_kernel<true>, grp::kGradSmem>(maps, p, units, sms, s);
   return launch_pairs<grouped_grad_kernel<false>, grp::kGradSmem>(maps, p, units, sms, s);
 }

@@ -183,12 +183,17 @@ struct GroupedGradParams {
   int32_t test_stall;
   int32_t E, group_list_type;
   int32_t out_f32, accumulate;
+  // more than one: each expert's rows in so many shares, whose sums a second launch adds up into out
+  int32_t shares;
+  const float* parts;  // [shares, E, A, B]
+  void* out;
 };
 struct GroupedGradMaps {
   CUtensorMap a, b;  // [M, A] and [M, B], boxes of 64 columns x 64 rows
-  CUtensorMap out;   // [E, A, B], boxes of 128 bytes x 32 rows
+  CUtensorMap out;   // [E, A, B], boxes of 128 bytes x 32 rows; parts as [shares E, A, B]
 };
-int grouped_grad_ctas(int64_t A, int64_t B, int64_t E, int sms);
+int grouped_grad_shares(int64_t M, int64_t A, int64_t B, int64_t E, int sms);
+int grouped_grad_ctas(int64_t A, int64_t B, int64_t slices, int sms);
 cudaError_t launch_grouped_grad(const GroupedGradMaps& maps, const GroupedGradParams& p, int sms, cudaStream_t s);
 
 }  // namespace gmmfr

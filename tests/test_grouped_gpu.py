@@ -106,6 +106,40 @@ def test_weights_gradient(sizes, rest, N, K, transposed, out):
     _close(dw.mT if transposed else dw, ref, absb, max(sizes), "dw")
 
 
+# few tiles and many rows: the rows in shares, of which the last end in odd numbers or are empty
+LONG = [([16384], 0, 136, 200), ([2100, 0, 3333], 40, 96, 136), ([4099, 3000], 0, 520, 264), ([0, 0, 20001], 0, 40, 72),
+        ([1027], 500, 256, 256), ([3, 6200], 1, 8, 8)]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("transposed", [False, True], ids=["NK", "KN"])
+@pytest.mark.parametrize("sizes,rest,N,K", LONG, ids=[f"E{len(s)}_M{sum(s) + r}_N{n}_K{k}" for s, r, n, k in LONG])
+def test_weights_gradient_of_few_tiles(sizes, rest, N, K, transposed, out):
+    E, M = len(sizes), sum(sizes) + rest
+    x, dy, w = _randn(1, M, K), _randn(2, M, N), _randn(3, E, N, K)
+    if rest:
+        x[-rest:] = float("nan")
+        dy[-rest:] = float("inf")
+    h, g = B.GroupedLinear(w.mT.contiguous() if transposed else w, transposed=transposed, grad_dtype=out), _list(sizes, 1)
+    dw = h.grad_weight(dy, x, g)
+    assert _bits(h) == 0
+    ref, absb = O.grouped_linear_grad_weight(_f64(dy)[:M - rest], _f64(x)[:M - rest], sizes)
+    _close(dw.mT if transposed else dw, ref, absb, max(sizes), "dw")
+    graph, again = torch.cuda.CUDAGraph(), torch.empty_like(dw)
+    with torch.cuda.graph(graph):
+        h.grad_weight(dy, x, g, out=again)
+    small = h.grad_weight(dy[:64], x[:64], _list([64] + [0] * (E - 1), 1))  # one share, in the same workspace
+    graph.replay()
+    assert torch.equal(again, dw)
+    ref, absb = O.grouped_linear_grad_weight(_f64(dy[:64]), _f64(x[:64]), [64] + [0] * (E - 1))
+    _close(small.mT if transposed else small, ref, absb, 64, "dw of 64 rows")
+    if out == torch.float32:
+        base = torch.randn(dw.shape, generator=torch.Generator().manual_seed(5)).cuda()
+        acc = base.clone()
+        h.grad_weight(dy, x, g, out=acc, accumulate=True)
+        assert torch.equal(acc, base + dw)  # one addition of the same sum
+
+
 def _handle(E=5, N=136, K=200, seed=7, **kw):
     return B.GroupedLinear(_randn(seed, E, N, K, scale=K ** -0.5), **kw)
 
