@@ -411,34 +411,36 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
         loaded_bits ^= 1u << stage;
       }
       uint8_t* wb = smem + stage * stage_bytes + h * block_bytes + w_at;
-      uint32_t most = 0;
+      __nv_bfloat162 most = __float2bfloat162_rn(0.f);  // the largest, NaN before infinity
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const int r = w0 + 32 * i;  // a row of W
+        const int r = w0 + 32 * i;  // a row of W, on its way while rows of x are written
         uint4 v[Terms::kPieces];
 #pragma unroll
         for (int k = 0; k < Terms::kPieces; ++k)
           v[k] = r < w1 && k < 2 * steps ? *reinterpret_cast<const uint4*>(wb + r * 128 + ((k ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        if (r0 + 32 * i < x_rows) {
+          const uint32_t to = xb + h * block_bytes + i * 4096, keep = own[i] == adapter ? 0xffffffffu : 0u;
+#pragma unroll
+          for (int k = 0; k < Terms::kPieces; ++k) {
+            if (k >= 2 * steps) break;
+#pragma unroll
+            for (int t = 0; t < Terms::kTerms; ++t) {
+              const int piece = t * Terms::kPieces + k;
+              ptx::st_shared_v4(to + ((piece ^ turn) << 4), words[i][4 * piece] & keep, words[i][4 * piece + 1] & keep,
+                                words[i][4 * piece + 2] & keep, words[i][4 * piece + 3] & keep);
+            }
+          }
+        }
 #pragma unroll
         for (int k = 0; k < Terms::kPieces; ++k) {
           const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
-        }
-        if (r0 + 32 * i >= x_rows) continue;
-        const uint32_t to = xb + h * block_bytes + i * 4096, keep = own[i] == adapter ? 0xffffffffu : 0u;
-#pragma unroll
-        for (int k = 0; k < Terms::kPieces; ++k) {
-          if (k >= 2 * steps) break;
-#pragma unroll
-          for (int t = 0; t < Terms::kTerms; ++t) {
-            const int piece = t * Terms::kPieces + k;
-            ptx::st_shared_v4(to + ((piece ^ turn) << 4), words[i][4 * piece] & keep, words[i][4 * piece + 1] & keep,
-                              words[i][4 * piece + 2] & keep, words[i][4 * piece + 3] & keep);
-          }
+          for (int j = 0; j < 4; ++j) most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
         }
       }
-      if (__any_sync(0xffffffffu, (most & 0xffffu) >= 0x7f80u || most >> 16 >= 0x7f80u)) {
+      const uint32_t bits = *reinterpret_cast<const uint32_t*>(&most);
+      if (__any_sync(0xffffffffu, (bits & 0x7f80u) == 0x7f80u || (bits & 0x7f800000u) == 0x7f800000u)) {
         drop_not_finite(wb, w1 - w_rows / kWarps, w1, steps);
         found = true;
       }
