@@ -137,6 +137,34 @@ def test_what_is_not_finite_reaches_its_own_rows(M):
     assert torch.equal(y[at][:, rest], want[at][:, rest])
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("M,N,K,r", [(40, 1032, 2048, 24), (128, 300, 4096, 64), (130, 264, 136, 8), (513, 1096, 1288, 40)])
+def test_one_number_of_a_factor_that_is_not_finite(M, N, K, r, act, out):
+    # wherever it lies, all else is as with a zero in its place, and its own sum with the rows' other products
+    L, rows = 9, 2 * N if act == "swiglu" else N
+    x, w = _randn(1, M, K), _randn(2, rows, K, scale=K ** -0.5)
+    a, b = _randn(4, L, r, K, scale=K ** -0.5), _randn(5, L, rows, r, scale=r ** -0.5)
+    ids = _ids(M, L, "tokens")
+    for adapter, row, j, bad in [(0, 0, 0, "nan"), (8, rows - 1, r - 1, "inf"), (4, 33, r // 2, "-inf"), (7, rows // 2 + 70, 7, "nan")]:
+        b0, b1 = b.clone(), b.clone()
+        b0[adapter, row, j], b1[adapter, row, j] = 0, float(bad)
+        zero, y = (B.LoraLinear(w, a, f, activation=act, out_dtype=out)(x, ids) for f in (b0, b1))
+        its = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+        its[ids == adapter, row % N] = True
+        assert its.any() and torch.equal(y[~its], zero[~its])
+        if act == "none":
+            assert not y[its].isfinite().any()
+
+
+def test_strided_weight():
+    M, N, K = 300, 136, 200
+    x, w, ids = _randn(1, M, K), _randn(2, N, 264), _ids(M, 5, "tokens")
+    a, b = _randn(4, 5, 16, K, scale=K ** -0.5), _randn(5, 5, N, 16)
+    for m in (1, 20, 100, M):
+        assert torch.equal(B.LoraLinear(w[:, :K], a, b)(x[:m], ids[:m]), B.LoraLinear(w[:, :K].contiguous(), a, b)(x[:m], ids[:m]))
+
+
 @pytest.mark.parametrize("M", [4, 100, 400])
 def test_an_adapter_that_there_is_not_counts_as_none_and_is_reported(M):
     N, K, L, r = 72, 136, 3, 8
