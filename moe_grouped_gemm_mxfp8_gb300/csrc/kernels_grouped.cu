@@ -20,6 +20,7 @@
 #include "ops.cuh"
 #include "pipeline.cuh"
 #include "ptx.cuh"
+#include "row_tiles.h"
 
 namespace gmmfr {
 namespace grp {
@@ -88,7 +89,7 @@ __device__ void grouped_ends(const int64_t* list, int type, int E, int64_t M, in
   __syncthreads();
 }
 
-// The tiles of rows: expert e has n_e = ceil(rows / bn) of them, each ceil(rows / n_e) rows rounded up to 32.
+// The tiles of rows: expert e has ceil(rows / bn) of them, shared out by row_tile.
 struct RowTiles {
   const int32_t *end, *gbase;
   int E, bn;
@@ -104,9 +105,8 @@ struct RowTiles {
       e = lo;
     }
     const int start = e ? end[e - 1] : 0, rows = end[e] - start, n = gbase[e + 1] - gbase[e];
-    const int w = ((rows + n - 1) / n + 31) / 32 * 32;
-    t0 = start + (g - gbase[e]) * w;
-    T = min(w, end[e] - t0);
+    row_tile(rows, n, g - gbase[e], t0, T);
+    t0 += start;
   }
 };
 
