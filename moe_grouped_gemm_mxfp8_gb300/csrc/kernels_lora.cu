@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
   if (t < tiles) {
     const __nv_bfloat16* ar = p.a + ((int64_t)a * p.rank + r0) * p.K;
     const __nv_bfloat16* const xr[1] = {p.x + (int64_t)s_row[min((tile0 + t) * 8 + (lane >> 2), rows - 1)] * p.ldx};
-    float acc[1][1][4] = {};
+    float acc[1][1][4] = {}, sum[4] = {};
     for (int b0 = b_begin + split; b0 < b_end; b0 += splits * kU) {
       SumOperands<1, 1> o[kU];
 #pragma unroll
@@ -186,9 +186,17 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
         o[v].keep(b0 + splits * v < b_end && (int64_t)(b0 + splits * v) * 32 + (lane & 3) * 8 < p.K);
         o[v].multiply(acc);
       }
+      if (p.precise) {  // the tensor core adds 256 products, truncating; those sums are added to nearest
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i] += acc[0][0][i];
+          acc[0][0][i] = 0.f;
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[(split * tiles + t) * 8 + (lane & 3) * 2 + (i & 1)][8 * (i >> 1) + (lane >> 2)] = acc[0][0][i];
+    for (int i = 0; i < 4; ++i)
+      part[(split * tiles + t) * 8 + (lane & 3) * 2 + (i & 1)][8 * (i >> 1) + (lane >> 2)] = p.precise ? sum[i] : acc[0][0][i];
   }
   __syncthreads();
   // the splits' parts in order
