@@ -16,6 +16,7 @@ namespace lora {
 constexpr int kFewThreads = 512;
 constexpr int kTileThreads = 448, kTileStages = 10, kTileArena = 10 * (lin::kTileBytes + 2048);
 constexpr int kPass = 8;  // units of a pass
+constexpr int kChunk = 16;  // FP32 results: blocks of 64 to an accumulator, as the dense product's
 }  // namespace lora
 
 namespace {
@@ -282,6 +283,8 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     kb0 = (int)((int64_t)KB * (i % C) / C);
     kb1 = (int)((int64_t)KB * (i % C + 1) / C);
   };
+  // FP32 results: blocks to an accumulator; who reads it adds those of a longer share up, to nearest
+  const int per = p.precise ? lora::kChunk : KB;
 
   if (warp == 0) {
     const uint64_t pol = ptx::l2_evict_last_policy();
@@ -327,27 +330,29 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     int stage = 0, acc_i = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int i = first; ok && i < items; i += p.tile_ctas, ++acc_i) {
+    for (int i = first; ok && i < items; i += p.tile_ctas) {
       int u0, kb0, kb1;
       item(i, u0, kb0, kb1);
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)min(lora::kPass, units - u0) << 18) | ((128u >> 4) << 24);
-      const int buf = acc_i & 1;
-      if (!(ok = warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
-      ptx::tc_fence_after();
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl))) break;
+      for (int c0 = kb0; ok && c0 < kb1; c0 += per, ++acc_i) {
+        const int buf = acc_i & 1, c1 = min(c0 + per, kb1);
+        if (!(ok = warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
         ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint32_t la = (uint32_t)da0 + stage * (stage_bytes >> 4), lb = la + (lin::kTileBytes >> 4);
+        for (int kb = c0; kb < c1; ++kb) {
+          if (!(ok = warp_wait_quick(ptx::smem_u32(&full[stage]), phase, ctl))) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint32_t la = (uint32_t)da0 + stage * (stage_bytes >> 4), lb = la + (lin::kTileBytes >> 4);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            ptx::tc_mma_f16_lo(tmem_base + buf * 256, la + 2 * q, lb + 2 * q, desc_hi, idesc, kb > kb0 || q > 0 ? 1u : 0u);
-          ptx::tc_commit(ptx::smem_u32(&empty[stage]));
-          if (kb == kb1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[buf]));
-        }
-        if (++stage == n_stages) {
-          stage = 0;
-          phase ^= 1;
+            for (int q = 0; q < 4; ++q)
+              ptx::tc_mma_f16_lo(tmem_base + buf * 256, la + 2 * q, lb + 2 * q, desc_hi, idesc, kb > c0 || q > 0 ? 1u : 0u);
+            ptx::tc_commit(ptx::smem_u32(&empty[stage]));
+            if (kb == c1 - 1) ptx::tc_commit(ptx::smem_u32(&accf[buf]));
+          }
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
     }
@@ -361,29 +366,39 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
     const float scale = mine >= 0 && p.scale ? p.scale[mine] : 1.f;
     int acc_i = 0;
-    for (int i = first; i < items; i += p.tile_ctas, ++acc_i) {
+    bool ok = true;
+    for (int i = first; ok && i < items; i += p.tile_ctas) {
       int u0, kb0, kb1;
       item(i, u0, kb0, kb1);
       float* to = p.s + (i % C * p.M + row0 + row) * p.rank;
-      const int buf = acc_i & 1;
-      if (!warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl)) break;
-      ptx::tc_fence_after();
-      for (int u = u0; u < min(u0 + lora::kPass, units); ++u) {
-        const bool own = mine == s_list[u / rc];
-        if (!__any_sync(0xffffffffu, own)) continue;
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(taddr + buf * 256 + (u - u0) * 16, v);
-        ptx::tmem_wait_ld();
-        const int r0 = u % rc * 16;
+      for (int c0 = kb0; c0 < kb1; c0 += per, ++acc_i) {
+        const int buf = acc_i & 1;
+        if (!(ok = warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl))) break;
+        ptx::tc_fence_after();
+        for (int u = u0; u < min(u0 + lora::kPass, units); ++u) {
+          const bool own = mine == s_list[u / rc];
+          if (!__any_sync(0xffffffffu, own)) continue;
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + buf * 256 + (u - u0) * 16, v);
+          ptx::tmem_wait_ld();
+          const int r0 = u % rc * 16;
 #pragma unroll
-        for (int j = 0; j < 16; j += 4)
-          if (own && r0 + j < p.rank)
-            *reinterpret_cast<float4*>(to + r0 + j) = make_float4(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale,
-                                                                  __uint_as_float(v[j + 2]) * scale, __uint_as_float(v[j + 3]) * scale);
+          for (int j = 0; j < 16; j += 4)
+            if (own && r0 + j < p.rank) {
+              float4 s = make_float4(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale, __uint_as_float(v[j + 2]) * scale,
+                                     __uint_as_float(v[j + 3]) * scale);
+              float4* at = reinterpret_cast<float4*>(to + r0 + j);
+              if (c0 > kb0) {  // this thread wrote it
+                const float4 w = *at;
+                s = make_float4(w.x + s.x, w.y + s.y, w.z + s.z, w.w + s.w);
+              }
+              *at = s;
+            }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
     }
   }
   ptx::tc_fence_before();
@@ -410,7 +425,8 @@ void plan_lora_sums(LoraParams& p, int sms) {
   const int64_t tiles = (p.M + 127) / 128, most = (std::min<int64_t>(128, p.count) * ranks + lora::kPass - 1) / lora::kPass;
   const int64_t ctas = std::max<int64_t>(sms / tiles, 1);
   while (p.split < 4 && p.split * 2 <= ctas && 2 * p.split * 128 <= p.K) p.split *= 2;
-  // FP32 results: an accumulator, whose additions truncate, takes 1024 products (of K above 16384 more)
+  // FP32 results: shares of 1024 products, which is what an accumulator, whose additions truncate, takes (of K above 16384 longer
+  // ones, of several accumulators)
   if (p.precise) p.split = (int32_t)std::max<int64_t>(p.split, std::min<int64_t>((p.K + 1023) / 1024, 16));
   p.parts = p.split;
   p.tile_ctas = (int32_t)std::min(ctas, most * p.split);

@@ -57,6 +57,12 @@ def test_sums_of_many_rows(M, K, L):
     assert (y - want).norm() <= BOUND * want.norm()
 
 
+@pytest.mark.parametrize("M,K,L", [(129, 16384, 1), (300, 20000, 3), (200, 40000, 1), (513, 40000, 70), (130, 200000, 2)])
+def test_sums_of_many_rows_past_16384(M, K, L):
+    y, want = _sums(M, K, L, scale=torch.linspace(0.5, 1.7, L, device="cuda"))
+    assert (y - want).norm() <= BOUND * want.norm()
+
+
 def test_bf16_results_are_one_rounding_away():
     for M, K in ((128, 40000), (300, 40000)):
         g = torch.Generator(device="cuda").manual_seed(M)
