@@ -250,8 +250,10 @@ __device__ __forceinline__ int adapter_of(const LinearParams& p, int64_t m, uint
 // ranks.  For FP32 results it is three numbers, which leave nothing out, of 16 ranks.  The lists of the adapters of 256 rows
 // come with the sums.
 // A zero does not keep an infinity or NaN of another adapter's factor out of a row.  The warps look at each factor where it has
-// landed and put zeros in the place of any; from then on the cluster's epilogues add, row by row, what those elements give the
-// rows whose adapter has them.
+// landed and put the smallest normal number, of the same sign, in the place of any; from then on the cluster's epilogues add, row by
+// row, what those elements give the rows whose adapter has them.  (A zero in their place would do for a finite sum, but make NaN of
+// an infinite one, whose product with an infinity is an infinity.  What the small number adds to a finite sum is lost in what the
+// element itself adds.)
 template <bool kF32>
 struct SumTerms {
   static constexpr int kTerms = kF32 ? 3 : 2, kRanks = kF32 ? 16 : 32;  // of a block: BF16 numbers of a sum, ranks
@@ -357,15 +359,15 @@ __device__ __forceinline__ void split_sums(const LinearParams& p, int64_t m, int
     }
 }
 
-// Zeros in place of what is not finite in the first 16 steps elements of rows r0 .. r1 - 1, of 128 bytes each (128-byte
-// swizzle).
-__device__ __noinline__ void drop_not_finite(uint8_t* at, int r0, int r1, int steps) {
+// 2^-126, of the same sign, in place of what is not finite in the first 16 steps elements of rows r0 .. r1 - 1, of 128 bytes each
+// (128-byte swizzle).
+__device__ __noinline__ void replace_not_finite(uint8_t* at, int r0, int r1, int steps) {
   for (int r = r0 + (int)(threadIdx.x & 31); r < r1; r += 32)
     for (int c = 0; c < 2 * steps; ++c) {
       uint32_t* w = reinterpret_cast<uint32_t*>(at + r * 128 + ((c ^ (r & 7)) << 4));
       for (int k = 0; k < 4; ++k) {
-        if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-        if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu;
+        if ((w[k] & 0x7f80u) == 0x7f80u) w[k] = (w[k] & 0xffff8000u) | 0x80u;
+        if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] = (w[k] & 0x8000ffffu) | 0x800000u;
       }
     }
 }
@@ -441,7 +443,7 @@ __device__ __forceinline__ bool build_adapters(const LinearParams& p, AdapterSha
       }
       const uint32_t bits = *reinterpret_cast<const uint32_t*>(&most);
       if (__any_sync(0xffffffffu, (bits & 0x7f80u) == 0x7f80u || (bits & 0x7f800000u) == 0x7f800000u)) {
-        drop_not_finite(wb, w1 - w_rows / kWarps, w1, steps);
+        replace_not_finite(wb, w1 - w_rows / kWarps, w1, steps);
         found = true;
       }
       at.next();
