@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(lora::kFewThreads, 1) lora_sums_few_kernel(con
 // 89.1.  Passes of 16: 47.9, 73.3, 87.1; 300 rows of 16 adapters of rank 64: 50.6, of 8: 43.7.  Up to 8 shares: 27.9 for one of
 // them, 4: 22.8 (their reader adds the parts).
 // Warp 0 TMA, warp 1 MMA, warps 2..5 epilogue, warps 6..13 lists.
+template <bool kPrecise>
 __global__ void __launch_bounds__(lora::kTileThreads, 1)
     lora_sums_many_kernel(const __grid_constant__ LoraMaps maps, const __grid_constant__ LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
     kb0 = (int)((int64_t)KB * (i % C) / C);
     kb1 = (int)((int64_t)KB * (i % C + 1) / C);
   };
-  // FP32 results: blocks to an accumulator; who reads it adds those of a longer share up, to nearest
-  const int per = p.precise ? lora::kChunk : KB;
+  // where the accumulator of blocks kb and up ends; FP32 results: who reads them adds those of a longer share up, to nearest
+  auto end_of = [&](int kb, int kb1) { return kPrecise ? min(kb + lora::kChunk, kb1) : kb1; };
 
   if (warp == 0) {
     const uint64_t pol = ptx::l2_evict_last_policy();
@@ -334,8 +335,9 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
       int u0, kb0, kb1;
       item(i, u0, kb0, kb1);
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)min(lora::kPass, units - u0) << 18) | ((128u >> 4) << 24);
-      for (int c0 = kb0; ok && c0 < kb1; c0 += per, ++acc_i) {
-        const int buf = acc_i & 1, c1 = min(c0 + per, kb1);
+      for (int c0 = kb0, c1; ok && c0 < kb1; c0 = c1, ++acc_i) {
+        const int buf = acc_i & 1;
+        c1 = end_of(c0, kb1);
         if (!(ok = warp_wait_quick(ptx::smem_u32(&acce[buf]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
         ptx::tc_fence_after();
         for (int kb = c0; kb < c1; ++kb) {
@@ -371,30 +373,35 @@ __global__ void __launch_bounds__(lora::kTileThreads, 1)
       int u0, kb0, kb1;
       item(i, u0, kb0, kb1);
       float* to = p.s + (i % C * p.M + row0 + row) * p.rank;
-      for (int c0 = kb0; c0 < kb1; c0 += per, ++acc_i) {
+      for (int c0 = kb0; c0 < kb1; c0 = end_of(c0, kb1), ++acc_i) {
         const int buf = acc_i & 1;
         if (!(ok = warp_wait_quick(ptx::smem_u32(&accf[buf]), (acc_i >> 1) & 1, ctl))) break;
         ptx::tc_fence_after();
-        for (int u = u0; u < min(u0 + lora::kPass, units); ++u) {
-          const bool own = mine == s_list[u / rc];
-          if (!__any_sync(0xffffffffu, own)) continue;
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + buf * 256 + (u - u0) * 16, v);
-          ptx::tmem_wait_ld();
-          const int r0 = u % rc * 16;
+        // (the addition in a copy of its own, not beside the plain store: 777 rows of 32 adapters 48.0 -> 46.6 us)
+        auto store = [&](auto more) {
+          for (int u = u0; u < min(u0 + lora::kPass, units); ++u) {
+            const bool own = mine == s_list[u / rc];
+            if (!__any_sync(0xffffffffu, own)) continue;
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(taddr + buf * 256 + (u - u0) * 16, v);
+            ptx::tmem_wait_ld();
+            const int r0 = u % rc * 16;
 #pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            if (own && r0 + j < p.rank) {
-              float4 s = make_float4(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale, __uint_as_float(v[j + 2]) * scale,
-                                     __uint_as_float(v[j + 3]) * scale);
-              float4* at = reinterpret_cast<float4*>(to + r0 + j);
-              if (c0 > kb0) {  // this thread wrote it
-                const float4 w = *at;
-                s = make_float4(w.x + s.x, w.y + s.y, w.z + s.z, w.w + s.w);
+            for (int j = 0; j < 16; j += 4)
+              if (own && r0 + j < p.rank) {
+                float4 s = make_float4(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale,
+                                       __uint_as_float(v[j + 2]) * scale, __uint_as_float(v[j + 3]) * scale);
+                float4* at = reinterpret_cast<float4*>(to + r0 + j);
+                if constexpr (decltype(more)::value) {  // to what this thread wrote there
+                  const float4 w = *at;
+                  s = make_float4(w.x + s.x, w.y + s.y, w.z + s.z, w.w + s.w);
+                }
+                *at = s;
               }
-              *at = s;
-            }
-        }
+          }
+        };
+        if (!kPrecise || c0 == kb0) store(std::false_type{});
+        else store(std::true_type{});
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&acce[buf]));
@@ -435,13 +442,16 @@ void plan_lora_sums(LoraParams& p, int sms) {
 
 cudaError_t launch_lora_sums(const LoraMaps& maps, const LoraParams& p, cudaStream_t s) {
   const bool few = p.M <= kLoraFewRows;
+  const auto many = p.precise ? lora_sums_many_kernel<true> : lora_sums_many_kernel<false>;
   if (!few) {
     static std::atomic<int> configured_device{-1};
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device.load(std::memory_order_relaxed) != dev) {
-      cudaError_t e = cudaFuncSetAttribute(lora_sums_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lora::kTileArena + 1024);
-      if (e != cudaSuccess) return e;
+      for (auto kernel : {lora_sums_many_kernel<true>, lora_sums_many_kernel<false>}) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lora::kTileArena + 1024);
+        if (e != cudaSuccess) return e;
+      }
       configured_device.store(dev, std::memory_order_relaxed);
     }
   }
@@ -455,7 +465,7 @@ cudaError_t launch_lora_sums(const LoraMaps& maps, const LoraParams& p, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&lc, lora_sums_few_kernel, p) : cudaLaunchKernelEx(&lc, lora_sums_many_kernel, maps, p);
+  return few ? cudaLaunchKernelEx(&lc, lora_sums_few_kernel, p) : cudaLaunchKernelEx(&lc, many, maps, p);
 }
 
 cudaError_t launch_lora_linear(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
