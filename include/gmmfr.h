@@ -516,7 +516,8 @@ GMMFR_API gmmfr_status gmmfr_linear(const gmmfr_linear_problem* problem, const v
  *   y[t] = act(x[t] weight^T + bias + lora_scale[a] (x[t] A_a^T) B_a^T) + residual[t]
  * act, weight, bias, residual and y as for gmmfr_linear.  Rows may have adapters in any order; one adapter's infinities
  * and NaN reach its own rows only.  FP32 sums, x A^T included; y is rounded once.  BF16 results above some rows and
- * weights take each x A^T to 17 bits; FP32 results take all of it, in sums as gmmfr_linear's.
+ * weights take each x A^T to 17 bits; FP32 results take all of it, and x A^T and what the adapter adds are in sums of at most 1024
+ * products as gmmfr_linear's (up to rank 16 the adapter's joins the last of those).
  *   linear   the product's sizes and rule; K, ldx and ldw multiples of 8, unaligned 0
  *   count    adapters, 1 <= count < 2^24
  *   rank     of all of them, a multiple of 8 in [8, 256] (an adapter of lower rank has zeros in its last rows of A, or

@@ -259,6 +259,10 @@ struct SumTerms {
   static constexpr int kTerms = kF32 ? 3 : 2, kRanks = kF32 ? 16 : 32;  // of a block: BF16 numbers of a sum, ranks
   static constexpr int kPieces = kRanks / 8;                            // 16-byte pieces of a row that a term takes
   __device__ static int blocks(int rank) { return (rank + kRanks - 1) / kRanks; }
+  // FP32 results: what the adapters add has an accumulator of its own.  Each of its 3 rank / 16 truncating additions is of a running
+  // sum that holds the dense one already: 300 rows, K = 256, rank 256, of one sign: 5.5e-6 off in one accumulator, 1.4e-6
+  // in two.  Up to rank 16 (3 additions) they share the last: 8192 rows of 7168 x 4096 353 us, apart 364.
+  __device__ static bool apart(int rank) { return kF32 && rank > 16; }
   // products of 16 ranks in the block from r0 on
   __device__ static int steps(int rank, int r0) { return kRanks == 32 && rank - r0 > 16 ? 2 : 1; }
 };
@@ -701,6 +705,7 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
   [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kPairTurnOff + 8 * 32 * 33 * 4);
   using Terms = SumTerms<kF32>;
   [[maybe_unused]] const int rank_chunks = Terms::blocks(p.lora_rank);  // kLora: blocks of an adapter
+  [[maybe_unused]] const bool apart = Terms::apart(p.lora_rank);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
@@ -868,7 +873,7 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
                 ptx::tc_mma_f16_pair_lo(d, lo + i * lo_block + 2 * q, lo + i * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi,
                                         idesc, i + q > 0 ? 1u : accumulate);
             ptx::tc_commit_pair(empty0 + 8 * stage);
-            if (kb == n - 1 && !(kLora && n == left)) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+            if (kb == n - 1 && (!(kLora && n == left) || apart)) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
           }
           accumulate = 1;
           lo += lo_step;
@@ -879,12 +884,20 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
           }
         }
         if constexpr (kLora) {
-          if (ok && n == left) {  // the tile's last accumulator takes the adapters
+          if (ok && n == left) {  // the tile's last accumulator takes the adapters, or the next one
             if (t == first) {
               if (p.lora_early) ptx::griddep_wait();
               count = adapters_of(p.lora_lists + (int64_t)mt * kLoraListInts);
             }
             const int units = count * rank_chunks;
+            uint32_t to = d;
+            if (apart && units > 0) {
+              ++acc_i;
+              if (!__all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&acce[acc_i & 1]), ((acc_i >> 1) & 1) ^ 1, ctl))) break;
+              ptx::tc_fence_after();
+              to = tmem_base + (acc_i & 1) * 256;
+              accumulate = 0;
+            }
             for (int u = 0; u < units; u += kKps) {
               if (!(ok = __all_sync(0xffffffffu, wait_bar_cluster(ptx::smem_u32(&ad.built[stage]), built_bits >> stage & 1, ctl)))) break;
               built_bits ^= 1u << stage;
@@ -896,10 +909,11 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
                   for (int q = 0; q < steps; ++q)
 #pragma unroll
                     for (int t = 0; t < Terms::kTerms; ++t)
-                      ptx::tc_mma_f16_pair_lo(d, xa + t * Terms::kPieces + 2 * q, wb + 2 * q, desc_hi, idesc, 1u);
+                      ptx::tc_mma_f16_pair_lo(to, xa + t * Terms::kPieces + 2 * q, wb + 2 * q, desc_hi, idesc, kF32 && i + q + t == 0 ? accumulate : 1u);
                 }
                 ptx::tc_commit_pair(empty0 + 8 * stage);
               }
+              accumulate = 1;
               lo += lo_step;
               if (++stage == n_stages) {
                 stage = 0;
@@ -908,7 +922,7 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
               }
             }
             if (!ok) break;
-            if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(&accf[buf]));
+            if ((!apart || units > 0) && ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(&accf[acc_i & 1]));
           }
         }
         ++acc_i;
@@ -1028,7 +1042,7 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
       } else {
         float sum[4][32] = {};  // gated: two chunks of gate values, then their up values
         bool ok = true;
-        for (int kb = 0; kb < KB; kb += per) {
+        for (int kb = 0, end = KB; kb < end; kb += per) {
           ok = wait_full();
           if (!ok) break;
           const uint32_t at = taddr + (acc_i & 1) * 256;
@@ -1047,6 +1061,12 @@ __global__ void __launch_bounds__(lin::kPairThreads + (kLora ? 32 * lin::kLoraWa
             }
           }
           release();
+          if constexpr (kLora) {
+            if (apart && end == KB && kb + per >= KB) {  // the adapters' own
+              if (t == first && p.lora_early) ptx::griddep_wait();
+              if (adapters_of(p.lora_lists + (int64_t)mt * kLoraListInts)) end = kb + per + 1;
+            }
+          }
         }
         if (!ok) break;
 #pragma unroll
@@ -1107,6 +1127,7 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
   [[maybe_unused]] AdapterShared& ad = *reinterpret_cast<AdapterShared*>(smem + lin::kStreamArena + lin::kStreamBars * 8 + 32);
   using Terms = SumTerms<kF32>;
   [[maybe_unused]] const int rank_chunks = Terms::blocks(p.lora_rank);  // kLora: blocks of an adapter
+  [[maybe_unused]] const bool apart = Terms::apart(p.lora_rank);
   // one accumulator, or two in turn for the chunks of FP32 results
   const uint32_t acc_cols = npad <= 32 ? 32 : (npad <= 64 ? 64 : 128), tmem_cols = kF32 ? 2 * acc_cols : acc_cols;
   auto acc_of = [&](uint32_t i) { return kF32 ? i & 1 : 0; };
@@ -1262,7 +1283,7 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
               ptx::tc_mma_f16_lo(d, lo + h * lo_block + 2 * q, lo + h * lo_block + (lin::kTileBytes >> 4) + 2 * q, desc_hi, idesc,
                                  h + q > 0 ? 1u : accumulate);
           ptx::tc_commit(empty0 + 8 * stage);
-          if (kb == k1 - 1 && !(kLora && k1 == kb1)) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
+          if (kb == k1 - 1 && (!(kLora && k1 == kb1) || apart)) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
         }
         accumulate = 1;
         lo += lo_step;
@@ -1273,9 +1294,17 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
         }
       }
       if constexpr (kLora) {
-        if (ok && k1 == kb1) {  // the tile's last accumulator takes the adapters
+        if (ok && k1 == kb1) {  // the tile's last accumulator takes the adapters, or the next one
           if (t == first && !p.beside) ptx::griddep_wait();
           const int count = adapters_of(p.lora_lists), u0 = count * rank_chunks * (int)rank / S, u1 = count * rank_chunks * ((int)rank + 1) / S;
+          uint32_t to = d;
+          if (apart && u0 < u1) {
+            ++acc_i;
+            if (!warp_wait_quick(ptx::smem_u32(&acce[acc_of(acc_i)]), phase_of(acc_i) ^ 1, ctl)) break;
+            ptx::tc_fence_after();
+            to = tmem_base + acc_of(acc_i) * acc_cols;
+            accumulate = 0;
+          }
           for (int u = u0; u < u1; u += kKps) {
             if (!(ok = warp_wait_quick(ptx::smem_u32(&ad.built[stage]), built_bits >> stage & 1, ctl))) break;
             built_bits ^= 1u << stage;
@@ -1287,10 +1316,11 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
                 for (int q = 0; q < steps; ++q)
 #pragma unroll
                   for (int t = 0; t < Terms::kTerms; ++t)
-                    ptx::tc_mma_f16_lo(d, wa + 2 * q, xb + t * Terms::kPieces + 2 * q, desc_hi, idesc, 1u);
+                    ptx::tc_mma_f16_lo(to, wa + 2 * q, xb + t * Terms::kPieces + 2 * q, desc_hi, idesc, kF32 && h + q + t == 0 ? accumulate : 1u);
               }
               ptx::tc_commit(empty0 + 8 * stage);
             }
+            accumulate = 1;
             lo += lo_step;
             if (++stage == n_stages) {
               stage = 0;
@@ -1299,7 +1329,7 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
             }
           }
           if (!ok) break;
-          if (ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
+          if ((!apart || u0 < u1) && ptx::elect_one()) ptx::tc_commit(ptx::smem_u32(&accf[acc_of(acc_i)]));
         }
       }
       ++acc_i;
@@ -1344,7 +1374,7 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
       [[maybe_unused]] float sum[4][16] = {};
       bool ok = true;
       if constexpr (kF32) {
-        for (int kb = kb0; ok && kb < kb1; kb += per) {
+        for (int kb = kb0, end = kb1; ok && kb < end; kb += per) {
           ok = wait_full();
           if (!ok) break;
 #pragma unroll
@@ -1358,6 +1388,13 @@ __global__ void __launch_bounds__(lin::kThreads + (kLora ? 32 * lin::kLoraWarps<
             }
           }
           release();
+          if constexpr (kLora) {
+            if (apart && end == kb1 && kb + per >= kb1) {  // the adapters' own
+              if (t == first && !p.beside) ptx::griddep_wait();
+              const int blocks = adapters_of(p.lora_lists) * rank_chunks;
+              if (blocks * (int)rank / S < blocks * ((int)rank + 1) / S) end = kb + per + 1;
+            }
+          }
         }
       } else {
         ok = wait_full();
