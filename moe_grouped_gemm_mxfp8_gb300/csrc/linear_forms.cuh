@@ -205,15 +205,21 @@ __device__ __forceinline__ void add_adapter(const LinearParams& p, int adapter, 
     if (!kNotFinite || !isfinite(b)) f += s * b;
   };
   if constexpr (kCols == 1 && !kNotFinite) {  // four pieces of the factor's row, and of the sums, on their way at once
-    for (int c = 0; c < parts; ++c) {
-      const float4* s = reinterpret_cast<const float4*>(at + c * part);
+    // A sum's parts (two at most, of up to 32 rows) before its products: an infinite part beside a finite one of the other sign, and
+    // an infinite factor, come to an infinity, not to NaN.
+    const float4* s = reinterpret_cast<const float4*>(at);
+    const float4* more = reinterpret_cast<const float4*>(at + part);
 #pragma unroll 4
-      for (int j = 0; j < p.lora_rank; j += 8) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + j));
-        const float4 lo = s[j / 4], hi = s[j / 4 + 1];
-        add(f[0], lo.x, bf16_lo(w.x)), add(f[0], lo.y, bf16_hi(w.x)), add(f[0], lo.z, bf16_lo(w.y)), add(f[0], lo.w, bf16_hi(w.y));
-        add(f[0], hi.x, bf16_lo(w.z)), add(f[0], hi.y, bf16_hi(w.z)), add(f[0], hi.z, bf16_lo(w.w)), add(f[0], hi.w, bf16_hi(w.w));
+    for (int j = 0; j < p.lora_rank; j += 8) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + j));
+      float4 lo = s[j / 4], hi = s[j / 4 + 1];
+      if (parts > 1) {
+        const float4 l = more[j / 4], h = more[j / 4 + 1];
+        lo = make_float4(lo.x + l.x, lo.y + l.y, lo.z + l.z, lo.w + l.w);
+        hi = make_float4(hi.x + h.x, hi.y + h.y, hi.z + h.z, hi.w + h.w);
       }
+      add(f[0], lo.x, bf16_lo(w.x)), add(f[0], lo.y, bf16_hi(w.x)), add(f[0], lo.z, bf16_lo(w.y)), add(f[0], lo.w, bf16_hi(w.y));
+      add(f[0], hi.x, bf16_lo(w.z)), add(f[0], hi.y, bf16_hi(w.z)), add(f[0], hi.z, bf16_lo(w.w)), add(f[0], hi.w, bf16_hi(w.w));
     }
   } else {
     for (int j = 0; j < p.lora_rank; j += 8) {

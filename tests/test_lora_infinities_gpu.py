@@ -44,3 +44,24 @@ def test_both_factors_infinite_at_one_rank(M, r, out):
     assert torch.equal(_kind(y), _kind(want))
     mine = ids == 1
     assert y[mine][:, 5].isinf().all() and (y[mine][:, 5] == -y[mine][:, 263]).all()
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 20, 32, 100, 300])
+@pytest.mark.parametrize("K,at", [(2056, 5), (2552, 2551), (4096, 3000)])
+def test_sums_in_parts_of_which_one_is_infinite(K, at, M, out):
+    """K in shares, whose parts of a sum are added by who reads them: before the products with the second factor, since
+    -1 * inf + inf * inf is NaN where (-1 + inf) * inf is not."""
+    N, L, r, inf = 72, 2, 8, float("inf")
+    g = torch.Generator().manual_seed(K + M)
+    x, w, a, b = ((torch.randn(s, generator=g) * f).to(torch.bfloat16).cuda()
+                  for s, f in (((M, K), 1), ((N, K), K ** -0.5), ((L, r, K), K ** -0.5), ((L, N, r), r ** -0.5)))
+    x[:, at] = x[:, at].abs() + 0.5
+    ids = (torch.arange(M) % 3 - 1).to(torch.int32).cuda()
+    ids[0] = 1
+    a[1, 3, at], b[1, 4, 3], b[1, 71, 3], b[1, 30, 3] = inf, inf, -inf, 0.0
+    y = B.LoraLinear(w, a, b, out_dtype=out)(x, ids)
+    mine = ids == 1
+    assert (y[mine][:, 4] == inf).all() and (y[mine][:, 71] == -inf).all() and y[mine][:, 30].isnan().all()
+    rest = [n for n in range(N) if n not in (4, 30, 71)]
+    assert (y[mine][:, rest] == b[1, rest, 3].float().sign()[None] * inf).all() and y[~mine].isfinite().all()
