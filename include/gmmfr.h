@@ -533,7 +533,7 @@ GMMFR_API gmmfr_status gmmfr_lora_linear_workspace_size(const gmmfr_lora_problem
 
 /* x and weight 16-byte aligned; lora_a [count, rank, K] and lora_b [count, N or 2N, rank] BF16, dense, 16-byte aligned;
  * lora_scale [count] float32 or NULL (ones); adapter_ids [M] int32, checked on the device: one outside [-1, count) sets
- * GMMFR_DEV_BAD_ADAPTER_ID and counts as none.  One launch more than gmmfr_linear.  Never syncs, never allocates;
+ * GMMFR_DEV_BAD_ADAPTER_ID and counts as none.  One launch more than gmmfr_linear, or none.  Never syncs, never allocates;
  * deterministic; a wait that gave up sets GMMFR_DEV_TIMEOUT in the workspace's device error word
  * (gmmfr_check_device_errors). */
 GMMFR_API gmmfr_status gmmfr_lora_linear(const gmmfr_lora_problem* problem, const void* x, const void* weight,

@@ -422,10 +422,11 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
 }
 
 // ============================================================================ weights
-// Unit u is tile u % (TA TB) of slice u / (TA TB): share s of expert e's rows is slice s E + e.  Pair c takes the units c, c + pairs, ...  Both CTAs' loads count on rank
-// 0's barrier, but for an expert's last rows where their number is not a multiple of 16 (a product's K): these count on
-// each CTA's own, its warp 1 puts zeros in place of the rows that follow, and rank 1's tells rank 0's.  (With that way for
-// all rows, which takes some 500 cycles longer, 65536 rows of 64 experts, 2048 x 1024: 200 us.)
+// Unit u is tile u % (TA TB) of slice u / (TA TB): share s of expert e's rows is slice s E + e.  Pair c takes the units c,
+// c + pairs, ...  Both CTAs' loads count on rank 0's barrier, but for an expert's last rows where their number is not a
+// multiple of 16 (a product's K): these count on each CTA's own, its warp 1 puts zeros in place of the rows that follow, and
+// rank 1's tells rank 0's.  (With that way for all rows, which takes some 500 cycles longer, 65536 rows of 64 experts,
+// 2048 x 1024: 200 us.)
 template <bool kF32>
 __global__ void __launch_bounds__(grp::kThreads, 1)
     grouped_grad_kernel(const __grid_constant__ GroupedGradMaps maps, const __grid_constant__ GroupedGradParams p) {
@@ -656,17 +657,18 @@ __global__ void __launch_bounds__(grp::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(at + 32 * i, reinterpret_cast<uint32_t(&)[32]>(sum[i]));
           ptx::tmem_wait_ld();
-        } else
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int h = 0; h < 32; h += 16) {  // 32 at a time would not fit in registers beside the sums
-            uint32_t r[16];
-            ptx::tmem_ld_32x32b_x16(at + 32 * i + h, r);
-            ptx::tmem_wait_ld();
+            for (int h = 0; h < 32; h += 16) {  // 32 at a time would not fit in registers beside the sums
+              uint32_t r[16];
+              ptx::tmem_ld_32x32b_x16(at + 32 * i + h, r);
+              ptx::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[i][h + j] += __uint_as_float(r[j]);
-          }
+              for (int j = 0; j < 16; ++j) sum[i][h + j] += __uint_as_float(r[j]);
+            }
+        }
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&acce[acc_i & 1]), 0));
